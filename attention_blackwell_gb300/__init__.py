@@ -7,12 +7,13 @@ other implementation: if ``lib/libfa.so`` is missing, every call raises.
 
 Build the library with ``python -m attention_blackwell_gb300.build``.
 """
+import contextlib
 import ctypes
 import os
 
 import torch
 
-__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
+__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "page_plan", "page_pool", "kv_store", "prefix_fwd", "prefix_workspace", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "lib", "libfa.so")
@@ -69,6 +70,14 @@ def lib():
         L.fa_bwd.argtypes = [vp] * 9 + [i, i, i, i, i, f, i, vp, i, i, vp, sz, vp]
         L.fa_get_device_status.restype = i
         L.fa_get_device_status.argtypes = [vp, vp]
+        L.fa_page_plan.restype = i
+        L.fa_page_plan.argtypes = [vp, vp, i, i, vp, i, vp, i, vp, vp, vp, vp, vp, i, vp]
+        L.fa_kv_store.restype = i
+        L.fa_kv_store.argtypes = [vp, vp, i64, i64, vp, i, i, i, vp, vp, i, i, vp]
+        L.fa_prefix_workspace_size.restype = sz
+        L.fa_prefix_workspace_size.argtypes = [i] * 6
+        L.fa_prefix_fwd.restype = i
+        L.fa_prefix_fwd.argtypes = [vp, i64, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, i, vp, vp, i, vp, i, vp, sz, vp]
         L.fa_exp2_emu.restype = i
         L.fa_exp2_emu.argtypes = [vp, vp, i64, vp]
         L.fa_selftest_timeout.restype = i
@@ -242,6 +251,200 @@ def bwd(q, k, v, o, lse, do, causal=False, alpha=None, cu_seqlens=None, max_seql
                              workspace.numel(), _stream(stream))
     _check(rc, "fa_bwd")
     return dq, dk, dv
+
+
+@contextlib.contextmanager
+def _on(stream, tensors):
+    """Device and stream of a serving call: its tensors' device, the given
+    stream or that device's current one, and on it whatever the call
+    allocates.  Tensors that the caching allocator holds for another stream
+    are marked as used on this one."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    if stream is None and dev.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream()
+        return
+    with torch.cuda.device(dev):
+        s = stream if stream is not None else torch.cuda.current_stream()
+        if s.device != dev:
+            raise ValueError("the stream must be on the tensors' device")
+        if s == torch.cuda.current_stream():
+            yield s
+            return
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+        with torch.cuda.stream(s):
+            yield s
+
+
+def _rows(t, name, dim):
+    """A bf16 tensor whose last dim - 1 axes are dense; its first may have a
+    stride of its own (rows cut from a wider projection)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if t.dim() != dim:
+        raise ValueError("%s must have %d dimensions" % (name, dim))
+    if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+        raise ValueError("%s must be contiguous within a token" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[-1] * t.shape[-2]
+
+
+def _pages(k_pages, v_pages):
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, n, torch.bfloat16)
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d]")
+    return k_pages.shape
+
+
+def page_pool(num_pages, device=None):
+    """(ring, pool) of a cache whose num_pages pages are all free: int32
+    [num_pages] and int64 [3], as page_plan takes them."""
+    dev = device or "cuda"
+    return (torch.arange(num_pages, dtype=torch.int32, device=dev),
+            torch.tensor([0, num_pages, 0], dtype=torch.int64, device=dev))
+
+
+def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=None, cu_new=None, kv_lens=None,
+              slots=None, pool_out=None, stream=None):
+    """Pages and slots for a step's new tokens.  Returns (cu_new, kv_lens,
+    slots, pool_out); block_table and ring are updated in place.
+
+    ctx_lens, new_lens int32 [B] (new_lens < 0: the request leaves),
+    block_table int32 [B, W], ring int32 [num_pages], pool int64 [3] = head,
+    tail, missing (see page_pool).  -> cu_new int32 [B+1], kv_lens int32 [B],
+    slots int32 [num_slots] (-1: none), pool_out int64 [3], another tensor than
+    pool.  num_slots is needed when slots is not given.
+    """
+    for t, n, dt in ((ctx_lens, "ctx_lens", torch.int32), (new_lens, "new_lens", torch.int32),
+                     (block_table, "block_table", torch.int32), (ring, "ring", torch.int32), (pool, "pool", torch.int64)):
+        _need(t, n, dt)
+    B = ctx_lens.numel()
+    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("ctx_lens, new_lens and block_table must have one entry or row a request")
+    if pool.numel() != 3:
+        raise ValueError("pool must have 3 elements")
+    if slots is None and num_slots is None:
+        raise ValueError("page_plan needs num_slots or slots")
+    with _on(stream, (ctx_lens, new_lens, block_table, ring, pool, cu_new, kv_lens, slots, pool_out)) as s:
+        dev = ctx_lens.device
+        if cu_new is None:
+            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        if kv_lens is None:
+            kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty(num_slots, dtype=torch.int32, device=dev)
+        if pool_out is None:
+            pool_out = torch.empty(3, dtype=torch.int64, device=dev)
+        for t, n, dt, size in ((cu_new, "cu_new", torch.int32, B + 1), (kv_lens, "kv_lens", torch.int32, B),
+                               (slots, "slots", torch.int32, slots.numel()), (pool_out, "pool_out", torch.int64, 3)):
+            _need(t, n, dt)
+            if t.numel() != size:
+                raise ValueError("%s must have %d elements" % (n, size))
+        rc = lib().fa_page_plan(_ptr(ctx_lens), _ptr(new_lens), B, int(page_size), _ptr(block_table),
+                                block_table.shape[1], _ptr(ring), ring.numel(), _ptr(pool), _ptr(pool_out),
+                                _ptr(cu_new), _ptr(kv_lens), _ptr(slots), slots.numel(), _stream(s))
+    _check(rc, "fa_page_plan")
+    return cu_new, kv_lens, slots, pool_out
+
+
+def kv_store(k, v, slots, k_pages, v_pages, stream=None):
+    """Write rows of k and v ([T, Hkv, d] bf16, tokens may be strided) into the
+    cache at slots (int32 [T]; negative: skipped).  Returns (k_pages, v_pages)."""
+    P, Hkv, page, d = _pages(k_pages, v_pages)
+    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
+    _need(slots, "slots", torch.int32)
+    T = k.shape[0]
+    if tuple(k.shape) != (T, Hkv, d) or k.shape != v.shape:
+        raise ValueError("k and v must be [T, Hkv, d] with the pages' Hkv and d")
+    if slots.numel() != T:
+        raise ValueError("slots must have one element a token")
+    if T == 0:
+        return k_pages, v_pages
+    with _on(stream, (k, v, slots, k_pages, v_pages)) as s:
+        rc = lib().fa_kv_store(_ptr(k), _ptr(v), ks, vs, _ptr(slots), T, Hkv, d, _ptr(k_pages), _ptr(v_pages), P, page,
+                               _stream(s))
+    _check(rc, "fa_kv_store")
+    return k_pages, v_pages
+
+
+def prefix_workspace(B, Hq, Hkv, T, max_seqlen=1, d=HEAD_DIM, device=None):
+    """A uint8 CUDA tensor large enough for prefix_fwd of T rows of B requests
+    with at most max_seqlen rows each."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = lib().fa_prefix_workspace_size(int(T), int(B), int(Hq), int(Hkv), int(d), int(max_seqlen))
+        if n == 0:
+            raise ValueError("invalid sizes for the prefix workspace")
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_seqlen=None, prefix_table=None,
+               prefix_len=0, alpha=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of new tokens over a prefix that all requests share and each
+    request's own paged keys.  Returns (o, lse).
+
+    q [T, Hq, d] bf16 (tokens may be strided), k_pages / v_pages [num_pages,
+    Hkv, page_size, d], block_table int32 [B, W], kv_lens int32 [B] (new tokens
+    included), prefix_table int32 pages of the prefix's prefix_len tokens ->
+    o [T, Hq, d], lse float32 [Hq, T].  Without cu_seqlens (int32 [B+1]) every
+    request has one row; with it max_seqlen bounds a request's rows.
+    """
+    P, Hkv, page, d = _pages(k_pages, v_pages)
+    qs = _rows(q, "q", 3)
+    for t, n in ((block_table, "block_table"), (kv_lens, "kv_lens")):
+        _need(t, n, torch.int32)
+    T, Hq = q.shape[0], q.shape[1]
+    B = kv_lens.numel()
+    if q.shape[2] != d:
+        raise ValueError("q and the pages must have one head dim")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, W] with kv_lens' B")
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.numel() != B + 1:
+            raise ValueError("cu_seqlens must have B + 1 elements")
+        if max_seqlen is None:
+            raise ValueError("cu_seqlens needs max_seqlen")
+    elif T != B:
+        raise ValueError("without cu_seqlens q must have one row a request")
+    else:
+        max_seqlen = 1
+    prefix_len = int(prefix_len)
+    if prefix_len > 0:
+        if prefix_table is None:
+            raise ValueError("prefix_len needs prefix_table")
+        _need(prefix_table, "prefix_table", torch.int32)
+        if prefix_table.numel() * page < prefix_len:
+            raise ValueError("prefix_table is too short for prefix_len")
+    else:
+        prefix_table = None
+    if alpha is None:
+        alpha = 1.0 / (d ** 0.5)
+    with _on(stream, (q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, prefix_table, out, lse, workspace)) as s:
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        _need(out, "out", torch.bfloat16)
+        _need(lse, "lse", torch.float32)
+        if tuple(out.shape) != (T, Hq, d) or tuple(lse.shape) != (Hq, T):
+            raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
+        if T == 0:
+            return out, lse
+        if workspace is None:
+            workspace = prefix_workspace(B, Hq, Hkv, T, max_seqlen, d, device=q.device)
+        rc = lib().fa_prefix_fwd(_ptr(q), qs, _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), T, B, Hq, Hkv, d,
+                                 float(alpha), P, page, _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
+                                 _ptr(cu_seqlens), int(max_seqlen), _ptr(prefix_table), prefix_len, _ptr(workspace),
+                                 workspace.numel(), _stream(s))
+    _check(rc, "fa_prefix_fwd")
+    return out, lse
 
 
 def set_debug_counters(visits=None, inner=None, rescales=None):

@@ -181,6 +181,9 @@ cudaError_t launch_selftest_timeout(DevStatus* status, cudaStream_t stream);
 // boxes, tk and tv with 64-row boxes.
 cudaError_t launch_fwd256(const FwdLaunch& L, cudaStream_t stream);
 
+// log2 of a cache page size the library takes (16, 32, 64, 128, 256), else -1.
+int page_log2(int page_size);
+
 // The library's device status word on the current device.
 DevStatus* device_status_ptr();
 

@@ -299,6 +299,126 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
                    const int *cu_seqlens, int max_seqlen, int deterministic, cudaStream_t stream);
 
 /*
+ * Serving: a paged key/value cache and attention over it
+ * ------------------------------------------------------
+ * One step of a serving loop is fa_page_plan (pages and slots for the step's
+ * new tokens), fa_kv_store (their keys and values into the cache) and
+ * fa_prefix_fwd (attention of the new tokens).  fa_fwd serves prompts that
+ * have nothing in the cache.
+ * - The cache: k_pages and v_pages are bf16 [num_pages, Hkv, page_size, d];
+ *   page_size is 16, 32, 64, 128 or 256 tokens.  Slot s is row s % page_size
+ *   of page s / page_size, of every head.
+ * - A block table [B, table_width] (int32) lists each request's pages in the
+ *   order of its tokens.  An entry outside [0, num_pages) is "no page":
+ *   nothing is read or written there, and the keys it would hold are absent.
+ * - At most 1024 requests a call.  All lengths are read on the device, so a
+ *   captured graph serves later steps with other lengths.
+ */
+
+/*
+ * Block tables and slot maps of one step, from request lengths on the device.
+ *
+ *   have_b = ceil(c_b / page_size),  need_b = ceil((c_b + n_b) / page_size)
+ *
+ * ctx_lens [B]: c_b, request b's tokens in the cache (below 0 counts as 0,
+ * above the row's capacity table_width * page_size as that); new_lens [B]:
+ * n_b, tokens it adds in this step, or any negative number when it leaves.
+ * block_table [B, table_width], in and out: the first have_b entries of row b
+ * are read; entries have_b .. need_b - 1 are written; others are left alone.
+ * Free pages wait in a queue: ring [num_pages] with the counters
+ * pool = {head, tail, -}; position i (head <= i < tail) is ring[i %
+ * num_pages].  New pages come off its head, requests in order and each
+ * request's in order; pages of requests that leave go behind its tail in the
+ * same order (their entries as they stand, table rows untouched), and can be
+ * handed out from the next call on.  pool_out [3] receives the new {head,
+ * tail, missing}: missing counts the pages that the queue (or the row's
+ * width) could not give.  Their table entries are -1 (past the width: none),
+ * their tokens' slots -1; the caller looks at missing before the step counts
+ * as done.  Pages coming back beyond num_pages in the queue are dropped.
+ * cu_new [B+1]: prefix sums of the n_b that are >= 0 (the cu_seqlens of the
+ * step's packed rows); kv_lens [B]: c_b + n_b (at most the row's capacity), 0
+ * for a request that leaves; slots [num_slots]: the slot of packed row t, -1
+ * where it has no page and for rows t >= cu_new[B]; rows t >= num_slots get
+ * none.
+ * A call writes nothing that it reads, so the same call again gives the same.
+ * One launch, no workspace.  pool and pool_out must be different arrays; no
+ * array may overlap another.
+ * Errors: FA_ERR_INVALID (null pointer, B, table_width or num_pages < 1,
+ * num_slots < 0, pool == pool_out), FA_ERR_UNSUPPORTED (B > 1024, page_size,
+ * B * table_width, table_width * page_size or num_pages * page_size above
+ * 2^31 - 1), FA_ERR_ALIGN (an array not aligned to its element),
+ * FA_ERR_LAUNCH.
+ */
+int fa_page_plan(const int *ctx_lens, const int *new_lens, int B, int page_size, int *block_table, int table_width,
+                 int *ring, int num_pages, const int64_t *pool, int64_t *pool_out, int *cu_new, int *kv_lens,
+                 int *slots, int num_slots, cudaStream_t stream);
+
+/*
+ * Writes a step's keys and values into the cache: row t of k and v ([T, Hkv,
+ * d] bf16; k_stride and v_stride elements between tokens, at least Hkv * d and
+ * multiples of 8, so both may be cut from one projection's output) goes to
+ * slot slots[t].  Slots outside [0, num_pages * page_size) are skipped, every
+ * other slot is left as it was.  The slots of one call must be distinct: where
+ * two rows share one, the slot holds parts of either.
+ * d is 64, 128 or 256.  T == 0 is a no-op.
+ * Errors: FA_ERR_INVALID (null pointer, T < 0, Hkv, d or num_pages < 1, stride below Hkv
+ * * d), FA_ERR_UNSUPPORTED (d, page_size, num_pages * page_size above 2^31 -
+ * 1), FA_ERR_ALIGN (k, v or a page array not 16-byte aligned, a stride not a
+ * multiple of 8), FA_ERR_LAUNCH.
+ */
+int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride, const int *slots, int T, int Hkv,
+                int d, void *k_pages, void *v_pages, int num_pages, int page_size, cudaStream_t stream);
+
+/*
+ * Attention of a step's tokens for a batch whose requests share a prefix:
+ * query i (of n_b) of request b sees all prefix_len keys of the prefix and
+ * keys j <= s_b - n_b + i of its own s_b (its last n_b keys are the new
+ * tokens'; with s_b < n_b the first queries see none of them):
+ *
+ *   x_j = alpha q . k_j,  O = softmax(x) V,  LSE = ln sum_j exp(x_j)
+ *
+ * The prefix's part is computed once for the rows of all requests (each key
+ * and value of it is read once for up to 256 of them), every request's own
+ * part from its pages; the two are joined by their maxima and sums.
+ * q: bf16 [T, Hq, d], q_stride elements between tokens (>= Hq * d, a multiple
+ * of 8); o: bf16 [T, Hq, d]; lse: float32 [Hq, T].
+ * cu_seqlens [B+1] (device) delimits the requests' rows as in fa_fwd, each of
+ * at most max_seqlen rows; NULL: one row a request, T == B.  Rows outside
+ * every request are not written.  A request with more rows than max_seqlen
+ * makes the call compute nothing and report FA_ERR_INVALID through
+ * fa_get_device_status.
+ * block_table [B, table_width] and kv_lens [B] (s_b, taken as at least 0 and
+ * at most table_width * page_size): the requests' own keys; prefix_table: the
+ * prefix's pages (ceil(prefix_len / page_size) entries), NULL when prefix_len
+ * is 0.  Keys of absent pages (see above) are not seen.  A row that sees no
+ * key at all gives O = 0 and LSE = -inf.  What the cache holds behind the
+ * lengths does not matter, NaN and infinities included.
+ * workspace: at least fa_prefix_workspace_size(...) bytes, 256-byte aligned,
+ * no initialisation needed; calls that share one must not overlap on the GPU.
+ * T == 0 is a no-op.
+ * Errors: FA_ERR_INVALID (null pointer, T < 0, B, Hq, Hkv, num_pages or
+ * table_width < 1, Hq % Hkv, prefix_len < 0, alpha not finite and > 0,
+ * max_seqlen < 1, q_stride below Hq * d, T != B without cu_seqlens),
+ * FA_ERR_UNSUPPORTED (d not 64, 128 or 256; Hq / Hkv > 128; B > 1024;
+ * page_size; Hq * T, B * table_width, table_width * page_size, prefix_len +
+ * page_size or num_pages * Hkv * page_size above 2^31 - 1), FA_ERR_ALIGN,
+ * FA_ERR_WORKSPACE, FA_ERR_LAUNCH.
+ */
+int fa_prefix_fwd(const void *q, int64_t q_stride, const void *k_pages, const void *v_pages, void *o, float *lse,
+                  int T, int B, int Hq, int Hkv, int d, float alpha, int num_pages, int page_size,
+                  const int *block_table, int table_width, const int *kv_lens, const int *cu_seqlens, int max_seqlen,
+                  const int *prefix_table, int prefix_len, void *workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/*
+ * Bytes of device workspace fa_prefix_fwd needs for T rows of B requests of at
+ * most max_seqlen rows each (the current device's SM count enters: call it
+ * with the device current); 0 for invalid sizes.  Enough for every call with
+ * at most these T and B, and this max_seqlen or one below it.
+ */
+size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen);
+
+/*
  * Reads (and clears) the library's device status word on the current
  * device after synchronising `stream`: FA_OK, or FA_ERR_TIMEOUT when a
  * kernel's bounded wait gave up (the kernel then skipped its remaining work,
