@@ -181,6 +181,15 @@ cudaError_t launch_selftest_timeout(DevStatus* status, cudaStream_t stream);
 // boxes, tk and tv with 64-row boxes.
 cudaError_t launch_fwd256(const FwdLaunch& L, cudaStream_t stream);
 
+// Tensor maps (fa_api.cu).  Query rows of a packed [T, H, d] tensor whose tokens
+// are `stride` elements apart: 3-D {d, H, T}, box {64, heads, tokens}, 128-B
+// swizzle; rows past T read as zero.  Cache pages as [rows, d]: box {64, rows}.
+int make_map_rows(CUtensorMap* map, const void* ptr, int d, int H, long long T, long long stride, int heads, int tokens);
+int make_map_pages(CUtensorMap* map, const void* ptr, int d, long long rows, int box_rows);
+
+// Upper bound on the SM count, for sizes asked for without a device.
+constexpr int kMaxSMs = 192;
+
 // log2 of a cache page size the library takes (16, 32, 64, 128, 256), else -1.
 int page_log2(int page_size);
 
