@@ -9,27 +9,33 @@
 //   item     one row block of one key/value head against one list of pages:
 //            the prefix's (rows of any requests) or a request's (its rows);
 //   unit     one tile of kN keys of one item;
-//   CTA      a contiguous range of the flat list of units, so the tiles, not
+//   worker   a contiguous range of the flat list of units, so the tiles, not
 //            the requests, are shared out evenly whatever the lengths are; an
-//            item cut by a range's end is a segment in each of its CTAs;
+//            item cut by a range's end is a segment in each of its workers;
 //   segment  leaves its rows' (m, l, O) (maximum, sum, unnormalised output) in
-//            the workspace; segment ids are item + CTA, unique because every
+//            the workspace; segment ids are item + worker, unique because every
 //            step along the list raises one of the two.
 //
 // A second kernel joins each output row's segments: with M = max m_s,
 // O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s in fp32, in the list's order, so
 // the result does not depend on timing.
 //
-// Within a CTA (d = 64 and 128; two softmax warpgroups, loader and UMMA issuer):
-//   rows > 128    two row tiles share every K/V tile (the ping-pong of
-//                 fa_fwd.cu): the shape for the prefix of a large batch and for
-//                 prompts, where the tensor core sets the pace;
-//   rows <= 128   one row tile; the warpgroups take alternate K/V tiles with
-//                 accumulators of their own, joined in the epilogue: the shape
-//                 for single tokens, where the copies set the pace and two
-//                 tiles in flight hide a tile's S -> P -> O latency.
-// d = 256: one row tile, one warpgroup, S double-buffered, 64-key tiles (its
+// Some CTAs work on the prefix, the others on the requests, in proportion to
+// the cost of both.  Within a CTA (d = 64 and 128):
+//   rows > 128    the CTA is one worker: two row tiles share every K/V tile (the
+//                 ping-pong of fa_fwd.cu): the shape for the prefix of a large
+//                 batch and for prompts, where the tensor core sets the pace;
+//   rows <= 128   two workers, one for each softmax warpgroup, that share the
+//                 loader, the ring of K/V tiles and the issuer, which serves
+//                 them by turns;
+//   rows <= 32    one worker, no tcgen05 (few_rows below): single tokens, where
+//                 the copies set the pace.
+// d = 256: one worker a CTA, one row tile, S double-buffered, 64-key tiles (its
 // accumulator takes half of tensor memory).
+//
+// Warps: softmax (4 or 8), loader, issuer, and one or two that walk the list
+// ahead of the others and leave each tile's description, page numbers
+// included, in shared memory, so that no role waits for a table entry.
 //
 // Keys behind the end of a list and keys of absent pages are masked by
 // selection, and their V rows are zeroed in shared memory before the product
@@ -55,11 +61,15 @@ template <int D> struct Pf {
     static constexpr uint32_t kTile = kBoxes * kKVBox;
     static constexpr uint32_t kQBox = 16384u;                    // 128 rows x 128 B
     static constexpr uint32_t kQTile = kBoxes * kQBox;
-    static constexpr int kQSlots = kStreams;
-    static constexpr int kRing = D == 64 ? 8 : 4;                // 128 KB of K/V tiles
-    static constexpr uint32_t kTiles = kQSlots * kQTile + kRing * kTile;
-    static constexpr int kThreads = kStreams * 128 + 128;
-    static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;
+    static constexpr int kLook = 3 - kStreams;                   // tiles of one worker with S in flight
+    static constexpr int kRing = D == 64 ? 8 : 4;                // 128 KB of K/V tiles (even: few rows take K and V by pairs)
+    static constexpr uint32_t kTiles = kStreams * kQTile + kRing * kTile;
+    static constexpr int kThreads = 384;
+    // Few rows: two Q slots of 32 rows and the buffer for the join in place of
+    // the row tiles of Q.
+    static constexpr uint32_t kFewQ = 2 * 32 * D * 2;
+    static constexpr int kMergeFloats = (kStreams * kQTile - kFewQ) / 4;
+    static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
 
 // What both kernels need to know of the list of units.
@@ -71,7 +81,7 @@ struct PfTables {
 };
 
 struct PfHeader {
-    long long per_p, per_s;   // units a CTA: of the prefix, of the requests
+    long long per_p, per_s;   // units a worker: of the prefix, of the requests
     int n_p;                  // CTAs on the prefix; the rest are on the requests
     int bad;                  // a request has more rows than max_seqlen
     int pad[10];
@@ -90,11 +100,15 @@ struct PfArgs {
     int tq, tb;               // tokens a row tile, a row block
     int rows_p, rows_s;       // rows a segment keeps
     int tiles_p, blocks_p;    // prefix: tiles an item, row blocks
-    int weight_p, weight_s;   // relative cost of a unit
+    int mode_p, mode_s;       // kFew, kOne or kTwo (see above)
+    int qstep_p, qstep_s;     // rows between Q slots: a block's rows, in whole swizzle atoms
     float scale_log2;
 };
 
-enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kPfO, kPfExchange, kPfFree, kPfPV };
+constexpr int kFew = 0, kOne = 1, kTwo = 2;   // row tiles: 16 or 32 rows, 128, 2 x 128
+constexpr int kFewRows = 32;
+
+enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kPfO, kPfPV, kPfDesc, kPfDescEmpty, kPfMerge };
 
 // ------------------------------------------------------------------ the list
 
@@ -104,6 +118,17 @@ struct Item {
     int seg;
 };
 
+// What the roles need to know of one tile.
+struct Desc {
+    int page[8];            // its parts' pages, -1: none
+    int live;               // one bit a part that has a page
+    int flags;              // kMore (not the list's end), kFirst, kLast of its item's tiles here
+    int j, nkeys, lim0, hk, tok0, ntok, seg, pre;
+};
+constexpr int kMore = 1, kFirst = 2, kLast = 4;
+constexpr int kDesc = 8;    // tiles the walkers run ahead by
+constexpr int kQMax = 8;    // Q slots
+
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Item k of a request's row blocks: from both ends by turns, so that under the
@@ -111,11 +136,12 @@ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int block_of(int k, int n) { return (k & 1) ? n - 1 - (k >> 1) : k >> 1; }
 __device__ __forceinline__ int index_of(int rb, int n) { return rb < (n + 1) / 2 ? 2 * rb : 2 * (n - 1 - rb) + 1; }
 
-// A CTA's walk over its range of units.
-template <int kN>
+// A worker's walk over its range of units.
+template <int D>
 struct Walk {
+    static constexpr int kN = Pf<D>::kN;
     long long u, end;
-    int b, hk, k, cta;
+    int b, hk, k, worker;
     bool pre;
 
     __device__ __forceinline__ static int units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
@@ -124,16 +150,18 @@ struct Walk {
         return n > 0 && t.len[b] > 0 ? cdiv(t.len[b], kN) + kOverheadUnits : 0;
     }
 
-    __device__ __forceinline__ void start(const PfArgs& a, const PfTables& t, const PfHeader& h) {
+    // Worker `x` of this CTA.
+    __device__ __forceinline__ void start(const PfArgs& a, const PfTables& t, const PfHeader& h, int x) {
         const int c = blockIdx.x;
         b = hk = k = 0;
         pre = c < h.n_p;
-        cta = pre ? c : c - h.n_p;
+        const int width = (pre ? a.mode_p : a.mode_s) == kOne ? Pf<D>::kStreams : 1;
+        worker = (pre ? c : c - h.n_p) * width + x;
         const long long per = pre ? h.per_p : h.per_s;
         const long long all = pre ? (long long)a.Hkv * a.blocks_p * a.tiles_p : t.pref[a.B];
-        u = cta * per;
+        u = worker * per;
         end = u + per < all ? u + per : all;
-        if (h.bad || u >= end) {
+        if (h.bad || x >= width || u >= end) {
             u = end = 0;
             return;
         }
@@ -165,7 +193,7 @@ struct Walk {
                 it.nkeys = a.prefix_len;
                 it.lim0 = INT_MAX / 2;
                 it.tab = a.prefix_table;
-                it.seg = i + cta;
+                it.seg = i + worker;
                 it.pre = 1;
                 return true;
             }
@@ -183,7 +211,7 @@ struct Walk {
             it.nkeys = s;
             it.lim0 = s - n + i0 + 1;
             it.tab = a.table + (long long)b * a.W;
-            it.seg = t.items[b] + i + cta;
+            it.seg = t.items[b] + i + worker;
             it.pre = 0;
             it.j0 = first;
             const int seen = it.lim0 + it.ntok - 1;        // keys the block's last row sees
@@ -220,11 +248,15 @@ __device__ __forceinline__ V block_scan(V v, V* s_warp, int tid, int nthreads, O
 }
 
 struct PfShared {
-    uint64_t q_full[2], q_empty[2], full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_done, x_ready, x_free, drain;
+    Desc desc[2][kDesc];
+    uint64_t d_full[2][kDesc], d_empty[2][kDesc];
+    uint64_t q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_done[2], drain;
+    // Few rows: the eight warps hand back tiles, Q, descriptions and the join's buffer.
+    uint64_t empty8[8], q_empty8[2], d_empty8[kDesc], m_full, m_free;
+    float2 ml[8][kFewRows];
     long long scan64[12];
     int scan32[12];
     float scanf[12];
-    float2 ml[2][2][128];   // by turns: the next item's exchange may begin before the slower group has read this one's
     PfHeader hdr;
     uint32_t tmem_base;
     int abort_flag;
@@ -233,7 +265,7 @@ struct PfShared {
 // The tables of the list, by every thread of the block: offsets by the
 // library's one rule (a running maximum), units and items before each request,
 // and how many CTAs work on the prefix.
-template <int kN>
+template <int D>
 __device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t, PfShared& sh, int tid, int nthreads) {
     const int per = (a.B + 1 + nthreads - 1) / nthreads, i0 = tid * per;
     int run = 0;
@@ -265,7 +297,7 @@ __device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t,
     float cost = 0.f;
     for (int i = i0; i < min(i0 + per, a.B); ++i) {
         int n, nb;
-        const int u = Walk<kN>::units(a, t, i, n, nb);
+        const int u = Walk<D>::units(a, t, i, n, nb);
         if (n > a.max_seqlen) sh.hdr.bad = 1;
         mine += (long long)u * nb * a.Hkv;
         my_items += nb * a.Hkv;
@@ -281,7 +313,7 @@ __device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t,
     if (tid == 0) { t.pref[0] = 0; t.items[0] = 0; }
     for (int i = i0; i < min(i0 + per, a.B); ++i) {
         int n, nb;
-        const int u = Walk<kN>::units(a, t, i, n, nb);
+        const int u = Walk<D>::units(a, t, i, n, nb);
         at += (long long)u * nb * a.Hkv;
         at_items += nb * a.Hkv;
         t.pref[i + 1] = at;
@@ -290,13 +322,14 @@ __device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t,
     if (tid == nthreads - 1) {
         const int grid = gridDim.x;
         const long long units_p = (long long)a.Hkv * a.blocks_p * a.tiles_p, units_s = upto64;
-        const float cp = (float)units_p * a.weight_p, cs = upto_cost * a.weight_s;
+        // Two row tiles take twice the tensor time of one.
+        const float cp = (float)units_p * (a.mode_p == kTwo ? 2 : 1), cs = upto_cost * (a.mode_s == kTwo ? 2 : 1);
         int np = units_p == 0 ? 0 : (units_s == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
         if (units_p > 0 && units_s > 0) np = grid == 1 ? 1 : max(1, min(grid - 1, np));
-        const int ns = max(1, grid - np);
+        const int wp = np * (a.mode_p == kOne ? Pf<D>::kStreams : 1), ws = max(1, grid - np) * (a.mode_s == kOne ? Pf<D>::kStreams : 1);
         sh.hdr.n_p = np;
-        sh.hdr.per_p = np ? (units_p + np - 1) / np : 1;
-        sh.hdr.per_s = units_s ? (units_s + ns - 1) / ns : 1;
+        sh.hdr.per_p = wp ? (units_p + wp - 1) / wp : 1;
+        sh.hdr.per_s = units_s ? (units_s + ws - 1) / ws : 1;
     }
     __syncthreads();
     if (blockIdx.x == 0) {
@@ -311,16 +344,6 @@ __device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t,
             if (sh.hdr.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 101; a.status->block = 0; }
         }
     }
-}
-
-// Page of the i-th part of tile j (parts are whole pages, or a tile's share of
-// a larger page): its id and first row, or -1 where there is none.
-template <int kN>
-__device__ __forceinline__ int part_page(const PfArgs& a, const Item& it, int j, int i, int part_log2) {
-    const int key = j * kN + (i << part_log2);
-    if (j >= it.j1 || key >= it.nkeys) return -1;
-    const int p = it.tab[key >> a.ps_log2];
-    return p >= 0 && p < a.P ? p : -1;
 }
 
 // ------------------------------------------------------------------ products
@@ -348,6 +371,254 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
     });
 }
 
+// ------------------------------------------------------------------ few rows
+//
+// Blocks of at most 32 rows (single tokens, small drafts).  A 128-row product
+// would be idle padding for most of its time and its softmax would run on one
+// warp in four; the copies set the pace here, so the eight warps take 16 keys
+// of a tile each (mma.sync m16n8k16, scores and weights stay in registers) with
+// maxima, sums and accumulators of their own, joined through shared memory at
+// the item's end.  kMT 16-row tiles a warp; at d = 256 (64-key tiles) four warps
+// take the keys and the second four the second 16 rows.
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int kMT>
+__device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t sQ, uint32_t sRing, float* merge, const WaitCtx& wc,
+                                         bool pre, int warp, int lane, int part_log2) {
+    using G = Pf<D>;
+    constexpr int kN = G::kN, kRing = G::kRing;
+    constexpr int kKeyGroups = kN / 16, kOwners = kKeyGroups;        // warps that add to one row
+    constexpr bool kKeepQ = D * kMT <= 128;                          // Q's fragments in registers
+    constexpr int kKSteps = D / 16, kNT = D / 8;
+    const int kg = warp % kKeyGroups, row0 = (warp / kKeyGroups) * 16;
+    const int g = lane >> 2, t2 = (lane & 3) * 2;
+    // ldmatrix row addresses: this lane's row of the four 8 x 8 matrices, and
+    // which 16-byte chunk of each 32-byte step it is; chunks are swizzled by
+    // row % 8 within a 128-byte row.
+    const int mi = lane >> 3, mr = lane & 7;
+    const uint32_t k_row = (kg * 16 + (mi >> 1) * 8 + mr) * 128u, v_row = (kg * 16 + (mi & 1) * 8 + mr) * 128u;
+    const uint32_t q_row = (row0 + (mi & 1) * 8 + mr) * 128u;
+    const float scale = a.scale_log2;
+    uint32_t n_item = 0, n_merge = 0;
+    uint32_t qf[kKeepQ ? kMT : 1][kKeepQ ? kKSteps : 1][4];
+    float o[kMT][kNT][4], m[kMT][2], l[kMT][2];
+    int lim[kMT][2], nkeys = 0, lim_min = 0, lim_max = 0, rows = 0, seg = 0;
+    uint32_t q_base = sQ;
+    bool idle = false;
+    auto q_frag = [&](uint32_t (&f)[4], int ks, int mt) {
+        ldsm4(f, q_base + (ks >> 2) * 4096u + mt * 2048u + q_row + (((((ks & 3) << 1) + (mi >> 1)) ^ mr) << 4));
+    };
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    for (uint32_t n = 0;; ++n) {
+        if (!mbar_wait_w(&sh.d_full[0][n % kDesc], (n / kDesc) & 1, wc, kPfDesc)) return false;
+        const Desc& d = sh.desc[0][n % kDesc];
+        const int flags = d.flags, k0 = d.j * kN + kg * 16;
+        const bool page = (d.live >> ((kg * 16) >> part_log2)) & 1;
+        if (!(flags & kMore)) return true;
+        if (flags & kFirst) {
+            nkeys = d.nkeys;
+            rows = d.ntok * a.G;
+            seg = d.seg;
+            lim_min = pre ? nkeys : min(nkeys, d.lim0);
+            lim_max = pre ? nkeys : min(nkeys, d.lim0 + d.ntok - 1);
+            idle = row0 >= rows;
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = row0 + mt * 16 + h * 8 + g;
+                    lim[mt][h] = r >= rows ? 0 : (pre ? nkeys : min(nkeys, d.lim0 + r / a.G));
+                    m[mt][h] = -INFINITY;
+                    l[mt][h] = 0.f;
+                }
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int i = 0; i < kNT; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
+            if (!mbar_wait_w(&sh.q_full[n_item & 1], (n_item >> 1) & 1, wc, kPfQFull)) return false;
+            q_base = sQ + (n_item & 1) * (32u * D * 2u);
+            if constexpr (kKeepQ) {
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int ks = 0; ks < kKSteps; ++ks) q_frag(qf[mt][ks], ks, mt);
+                arrive(&sh.q_empty8[n_item & 1]);
+            }
+        }
+        const uint32_t ik = 2 * n, iv = 2 * n + 1, slot_k = ik % kRing, slot_v = iv % kRing;
+        const bool work = page && !idle && k0 < lim_max;
+        uint32_t p[kMT][4];
+        if (!mbar_wait_w(&sh.full[slot_k], (ik / kRing) & 1, wc, kPfRingFull)) return false;
+        if (work) {
+            float s[kMT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+            const uint32_t base = sRing + slot_k * G::kTile + k_row;
+#pragma unroll
+            for (int ks = 0; ks < kKSteps; ++ks) {
+                uint32_t b[4];
+                ldsm4(b, base + (ks >> 2) * G::kKVBox + (((((ks & 3) << 1) + (mi & 1)) ^ mr) << 4));
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+                    uint32_t f[4];
+                    if constexpr (!kKeepQ) q_frag(f, ks, mt);
+                    mma16816(s[mt][0], kKeepQ ? qf[kKeepQ ? mt : 0][kKeepQ ? ks : 0] : f, b[0], b[1]);
+                    mma16816(s[mt][1], kKeepQ ? qf[kKeepQ ? mt : 0][kKeepQ ? ks : 0] : f, b[2], b[3]);
+                }
+            }
+            if (k0 + 16 > lim_min) {
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (k0 + i * 8 + t2 + (e & 1) >= lim[mt][e >> 1]) s[mt][i][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+                float fac[2], use[2];
+                bool jump = false;
+                float mn[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    mn[h] = fmaxf(m[mt][h], x * scale);
+                    // Rows without a query (lim 0) never jump.
+                    jump |= lim[mt][h] > 0 && ((m[mt][h] == -INFINITY) ? (mn[h] != -INFINITY) : (mn[h] - m[mt][h] > kTau));
+                }
+                if (__any_sync(0xffffffffu, jump)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        fac[h] = m[mt][h] == -INFINITY ? 0.f : ex2_mufu(m[mt][h] - mn[h]);
+                        l[mt][h] *= fac[h];
+                        m[mt][h] = mn[h];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kNT; ++i) {
+                        o[mt][i][0] *= fac[0];
+                        o[mt][i][1] *= fac[0];
+                        o[mt][i][2] *= fac[1];
+                        o[mt][i][3] *= fac[1];
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) use[h] = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float p0 = ex2_mufu(fmaf(s[mt][i][2 * h], scale, -use[h]));
+                        const float p1 = ex2_mufu(fmaf(s[mt][i][2 * h + 1], scale, -use[h]));
+                        l[mt][h] += p0 + p1;
+                        p[mt][2 * i + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
+                    }
+            }
+        }
+        arrive(&sh.empty8[slot_k]);
+        if (!mbar_wait_w(&sh.full[slot_v], (iv / kRing) & 1, wc, kPfRingFull)) return false;
+        if (work) {
+            const uint32_t base = sRing + slot_v * G::kTile + v_row;
+            // Keys behind the list's end: whatever their rows hold, they count as 0.
+            auto half = [&](int key) {
+                return (key < nkeys ? 0xffffu : 0u) | (key + 1 < nkeys ? 0xffff0000u : 0u);
+            };
+            const bool tail = k0 + 16 > nkeys;
+            const uint32_t w0 = tail ? half(k0 + t2) : ~0u, w1 = tail ? half(k0 + 8 + t2) : ~0u;
+#pragma unroll
+            for (int i = 0; i < kNT; i += 2) {
+                uint32_t b[4];
+                ldsm4t(b, base + (i >> 3) * G::kKVBox + ((((i & 7) + (mi >> 1)) ^ mr) << 4));
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+                    mma16816(o[mt][i], p[mt], b[0] & w0, b[1] & w1);
+                    mma16816(o[mt][i + 1], p[mt], b[2] & w0, b[3] & w1);
+                }
+            }
+        }
+        arrive(&sh.empty8[slot_v]);
+        arrive(&sh.d_empty8[n % kDesc]);
+        if (!(flags & kLast)) continue;
+        // ------------------------------------------------------------ the item's end
+        if constexpr (!kKeepQ) arrive(&sh.q_empty8[n_item & 1]);
+        ++n_item;
+        // Rows in shared memory, C columns of D at a time; 8 floats of padding
+        // keep the eight rows of a store in different banks.
+        const int rp = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+        int C = D;
+        while (kOwners * rp * (C + 8) > G::kMergeFloats) C >>= 1;
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
+                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
+            }
+        const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s);
+        float* out = (pre ? a.o_p : a.o_s) + at * D;
+        for (int c0 = 0; c0 < D; c0 += C, ++n_merge) {
+            if (!mbar_wait_w(&sh.m_free, (n_merge & 1) ^ 1, wc, kPfMerge)) return false;
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = row0 + mt * 16 + h * 8 + g;
+                    if (r < rows) {
+                        if (t2 == 0) sh.ml[kg][r] = make_float2(m[mt][h], l[mt][h]);
+                        float* to = merge + (kg * rp + r) * (C + 8) - c0 + t2;
+#pragma unroll
+                        for (int i = 0; i < kNT; ++i)
+                            if (i * 8 >= c0 && i * 8 < c0 + C)
+                                *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
+                    }
+                }
+            arrive(&sh.m_full);
+            if (!mbar_wait_w(&sh.m_full, n_merge & 1, wc, kPfMerge)) return false;
+            const int quads = C / 4;
+            for (int i = warp * 32 + lane; i < rows * quads; i += 256) {
+                const int r = i / quads, c = (i - r * quads) * 4;
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int w = 0; w < kOwners; ++w) M = fmaxf(M, sh.ml[w][r].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kOwners; ++w) {
+                    const float2 ml = sh.ml[w][r];
+                    const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M);
+                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * rp + r) * (C + 8) + c);
+                    L = fmaf(f, ml.y, L);
+                    v.x = fmaf(f, x.x, v.x);
+                    v.y = fmaf(f, x.y, v.y);
+                    v.z = fmaf(f, x.z, v.z);
+                    v.w = fmaf(f, x.w, v.w);
+                }
+                *reinterpret_cast<float4*>(out + (long long)r * D + c0 + c) = v;
+                if (c0 + c == 0) (pre ? a.ml_p : a.ml_s)[at + r] = make_float2(M, L);
+            }
+            arrive(&sh.m_free);
+        }
+    }
+}
+
 // -------------------------------------------------------------------- kernel
 
 template <int D>
@@ -356,13 +627,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PfArgs a) {
     using G = Pf<D>;
     constexpr int kN = G::kN, kStreams = G::kStreams, kRing = G::kRing, kBoxes = G::kBoxes;
-    constexpr int kSoftWarps = 4 * kStreams, kThreads = G::kThreads;
+    constexpr int kSoftWarps = 8, kThreads = G::kThreads;
     extern __shared__ uint8_t dsmem[];
     __shared__ PfShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t base = (smem_u32(dsmem) + 1023u) & ~1023u;
     uint8_t* gbase = dsmem + (base - smem_u32(dsmem));
-    const uint32_t sQ = base, sRing = base + G::kQSlots * G::kQTile;
+    const uint32_t sQ = base, sRing = base + G::kStreams * G::kQTile;
     PfTables t;
     t.pref = reinterpret_cast<long long*>(gbase + G::kTiles);
     t.items = reinterpret_cast<int*>(t.pref + a.B + 1);
@@ -371,17 +642,21 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.q_full[i], 1);
-            mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_ready[i], 4);
             mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.o_done[i], 1);
+            for (int k = 0; k < kDesc; ++k) { mbar_init(&sh.d_full[i][k], 1); mbar_init(&sh.d_empty[i][k], 1); }
         }
+        for (int i = 0; i < kQMax; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_empty[i], 1); }
         for (int i = 0; i < kRing; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
-        mbar_init(&sh.o_done, 1);
-        mbar_init(&sh.x_ready, kSoftWarps);
-        mbar_init(&sh.x_free, kSoftWarps);
         mbar_init(&sh.drain, 1);
+        for (int i = 0; i < 8; ++i) mbar_init(&sh.empty8[i], 8);
+        for (int i = 0; i < kDesc; ++i) mbar_init(&sh.d_empty8[i], 8);
+        mbar_init(&sh.q_empty8[0], 8);
+        mbar_init(&sh.q_empty8[1], 8);
+        mbar_init(&sh.m_full, 8);
+        mbar_init(&sh.m_free, 8);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
@@ -395,7 +670,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
     }
-    build_tables<kN>(a, t, sh, tid, kThreads);
+    build_tables<D>(a, t, sh, tid, kThreads);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -404,89 +679,117 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     const uint32_t tmem = sh.tmem_base;
     // Parts of a tile: whole pages, or one part where a page is larger.
     const int part_log2 = min(a.ps_log2, kN == 64 ? 6 : 7), parts = kN >> part_log2;
-    Walk<kN> walk;
-    walk.start(a, t, sh.hdr);
-    Item it;
+    const bool pre = (int)blockIdx.x < sh.hdr.n_p;
+    const int mode = pre ? a.mode_p : a.mode_s;
+    const bool two = kStreams == 2 && mode == kTwo, few = mode == kFew;
+    const int workers = two || few ? 1 : kStreams;
+    // Q slots: two row tiles, one slot of both; else as many in a worker's row
+    // tile as its rows (in whole swizzle atoms) leave room for.  The products
+    // read 128 rows from a slot on; the rows past its own give scores that
+    // nobody looks at.
+    const int qstep = pre ? a.qstep_p : a.qstep_s;
+    const uint32_t qn = two ? 1 : few ? 2 : min(kQMax / kStreams, 128 / qstep);
+    auto q_slot = [&](int x, uint32_t item) { return two ? 0u : x * qn + item % qn; };
+    auto q_addr = [&](int x, uint32_t item) {
+        return few ? sQ + (item & 1) * (G::kFewQ / 2) : sQ + x * G::kQTile + (two ? 0u : (item % qn) * qstep * 128u);
+    };
+    auto desc_wait = [&](int x, uint32_t n) { return mbar_wait_w(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
 
     if (warp >= kSoftWarps) {
-        if constexpr (kStreams == 2) regs_dec<72>();
+        regs_dec<72>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------------------ loader
+            // The issuer's order: every worker's first K (kLook of them), then by
+            // turns a worker's V of the oldest tile and K of the next one.
             // Lane i * kBoxes + c copies box c of part i (at most 16 lanes).
-            uint32_t n_ring = 0, qc[2] = {0, 0}, qsel = 0;
+            uint32_t n_ring = 0, n_item[2] = {0, 0}, n_k[2] = {0, 0}, n_v[2] = {0, 0};
+            bool ended[2] = {false, false};
+            int pg[2][2] = {}, row[2][2] = {};               // of tiles whose V is still to come
             const int part = lane / kBoxes, col = lane % kBoxes;
-            const bool mine = part < parts;
             const uint32_t part_bytes = 128u << part_log2;
             bool ok = true;
-            auto page = [&](int j) { return mine ? part_page<kN>(a, it, j, part, part_log2) : -1; };
-            auto load = [&](const CUtensorMap* map, int j, int pg) -> bool {
+            auto load = [&](const CUtensorMap* map, int p, int r) -> bool {
                 const uint32_t slot = n_ring % kRing;
-                if (!mbar_wait_w(&sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
-                const uint32_t live = __ballot_sync(0xffffffffu, pg >= 0);
+                if (!mbar_wait_w(few ? &sh.empty8[slot] : &sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
+                const uint32_t live = __ballot_sync(0xffffffffu, p >= 0);
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], __popc(live) * part_bytes);
                 __syncwarp();
-                if (pg >= 0) {
-                    const int row = ((pg * a.Hkv + it.hk) << a.ps_log2) + ((j * kN + (part << part_log2)) & ((1 << a.ps_log2) - 1));
-                    tma_load_2d(sRing + slot * G::kTile + col * G::kKVBox + part * part_bytes, map, &sh.full[slot], col * 64, row);
-                }
+                if (p >= 0)
+                    tma_load_2d(sRing + slot * G::kTile + col * G::kKVBox + part * part_bytes, map, &sh.full[slot], col * 64, r);
                 ++n_ring;
                 return true;
             };
-            while (ok && walk.next(a, t, it)) {
-                const bool two = it.ntok > a.tq;
-                const int ahead = two ? 1 : 2;
-                int p0 = page(it.j0), p1 = page(it.j0 + 1), p2 = page(it.j0 + 2);
-                if (!(ok = load(&tk, it.j0, p0))) break;
-                // Q: one box column a lane.
-                for (int x = 0; x < (two ? 2 : 1) && ok; ++x) {
-                    const uint32_t qs = two ? (uint32_t)x : qsel;
-                    if (!(ok = mbar_wait_w(&sh.q_empty[qs], (qc[qs] & 1) ^ 1, wc, kPfQEmpty))) break;
-                    const uint32_t box = 128u * a.G * (it.pre ? a.tq : min(a.tq, a.max_seqlen));
-                    if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[qs], kBoxes * box);
-                    __syncwarp();
-                    if (lane < kBoxes)
-                        tma_load_3d(sQ + qs * G::kQTile + lane * G::kQBox, it.pre ? &tq_p : &tq_s, &sh.q_full[qs], lane * 64,
-                                    it.hk * a.G, it.tok0 + x * a.tq);
-                    ++qc[qs];
+            auto load_k = [&](int x) -> bool {
+                if (!desc_wait(x, n_k[x])) return false;
+                const Desc& d = sh.desc[x][n_k[x] % kDesc];
+                const int flags = d.flags;
+                if (!(flags & kMore)) {
+                    ended[x] = true;
+                    return true;
                 }
-                if (!two) qsel ^= G::kQSlots - 1;
-                if (!ok) break;
-                if (ahead == 2 && it.j0 + 1 < it.j1 && !(ok = load(&tk, it.j0 + 1, p1))) break;
-                for (int j = it.j0; j < it.j1; ++j) {
-                    const int p3 = page(j + 3);
-                    if (!(ok = load(&tv, j, p0))) break;
-                    if (j + ahead < it.j1 && !(ok = load(&tk, j + ahead, two ? p1 : p2))) break;
-                    p0 = p1;
-                    p1 = p2;
-                    p2 = p3;
+                pg[x][1] = pg[x][0];
+                row[x][1] = row[x][0];
+                pg[x][0] = part < parts ? d.page[part] : -1;
+                row[x][0] = ((pg[x][0] * a.Hkv + d.hk) << a.ps_log2) + ((d.j * kN + (part << part_log2)) & ((1 << a.ps_log2) - 1));
+                if (!load(&tk, pg[x][0], row[x][0])) return false;
+                if (flags & kFirst) {
+                    const uint32_t i = n_item[x], s = q_slot(x, i);
+                    if (!mbar_wait_w(few ? &sh.q_empty8[s] : &sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
+                    const int boxes = two ? 2 * kBoxes : kBoxes;
+                    if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[s], boxes * 128u * a.G * min(a.tq, pre ? a.T : a.max_seqlen));
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const int tile = lane / kBoxes, c = lane % kBoxes;
+                        tma_load_3d(q_addr(two ? tile : x, i) + c * (few ? 4096u : G::kQBox), pre ? &tq_p : &tq_s, &sh.q_full[s], c * 64, d.hk * a.G,
+                                    d.tok0 + tile * a.tq);
+                    }
+                    ++n_item[x];
+                }
+                ++n_k[x];
+                return true;
+            };
+            const int look = few ? 1 : G::kLook;   // few rows: K and V of a tile, then the next one's
+            for (int i = 0; i < look && ok; ++i)
+#pragma unroll
+                for (int x = 0; x < kStreams; ++x)
+                    if (ok && x < workers && !ended[x]) ok = load_k(x);
+            bool any = true;
+            while (ok && any) {
+                any = false;
+#pragma unroll
+                for (int x = 0; x < kStreams; ++x) {
+                    if (!ok || n_v[x] == n_k[x]) continue;
+                    any = true;
+                    const bool older = n_k[x] - n_v[x] == 2;
+                    if (!(ok = load(&tv, older ? pg[x][1] : pg[x][0], older ? row[x][1] : row[x][0]))) break;
+                    ++n_v[x];
+                    if (!ended[x]) ok = load_k(x);
                 }
             }
             // Every copy lands before teardown.
             const uint64_t t0 = globaltimer_ns();
             for (uint32_t i = n_ring > kRing ? n_ring - kRing : 0; i < n_ring; ++i)
                 while (!mbar_try_wait(smem_u32(&sh.full[i % kRing]), (i / kRing) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-            for (int x = 0; x < G::kQSlots; ++x)
-                if (qc[x] > 0)
-                    while (!mbar_try_wait(smem_u32(&sh.q_full[x]), (qc[x] - 1) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+            for (int x = 0; x < workers; ++x)
+                for (uint32_t i = n_item[x] > qn ? n_item[x] - qn : 0; i < n_item[x]; ++i)
+                    while (!mbar_try_wait(smem_u32(&sh.q_full[q_slot(x, i)]), (i / qn) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
-        } else if (warp == kSoftWarps + 1) {
+        } else if (warp == kSoftWarps + 1 && !few) {
             // ------------------------------------------------------- UMMA issuer
-            uint32_t n_ring = 0, qc[2] = {0, 0}, pc[2] = {0, 0}, qsel = 0, done = 0;
+            uint32_t n_ring = 0;
             bool ok = true;
             auto col_s = [&](int x) { return tmem + G::kColS + x * G::kColSStep; };
-            // Waits for the next tile of the ring; its address.
+            // Waits for the next tile of the ring; its slot.
             auto take = [&](uint32_t& slot) -> bool {
                 slot = n_ring % kRing;
                 if (!mbar_wait_w(&sh.full[slot], (n_ring / kRing) & 1, wc, kPfRingFull)) return false;
                 ++n_ring;
                 return true;
             };
-            // Zeroes the V rows of tile j that hold no visible key of the list
-            // (live: its parts that have a page).
-            auto clean = [&](uint32_t slot, int j, uint32_t live) {
-                const int rows = it.nkeys - j * kN;     // of the tile's kN
-                const uint32_t all = (1u << parts) - 1u;
-                if (rows >= kN && live == all) return;
+            // Zeroes the V rows of a tile that hold no key of the list.
+            auto clean = [&](uint32_t slot, const Desc& d) {
+                const int rows = d.nkeys - d.j * kN, live = d.live;
+                if (rows >= kN && live == (1 << parts) - 1) return;
                 for (int i = 0; i < parts; ++i) {
                     const int r0 = i << part_log2, r1 = r0 + (1 << part_log2);
                     const int from = (live >> i) & 1 ? max(r0, min(r1, rows)) : r0;
@@ -498,260 +801,312 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
             };
-            auto live_of = [&](int j) {
-                return __ballot_sync(0xffffffffu, lane < parts && part_page<kN>(a, it, j, lane, part_log2) >= 0);
+            auto free_desc = [&](int x, uint32_t n) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.d_empty[x][n % kDesc]);
             };
-            while (ok && walk.next(a, t, it)) {
-                const bool two = it.ntok > a.tq;
-                const int n = it.j1 - it.j0;
-                uint32_t ks, vs;
-                uint32_t live = live_of(it.j0);
-                if (two) {
-                    if constexpr (kStreams == 2) {
-                        if (!(ok = mbar_wait_w(&sh.q_full[0], qc[0] & 1, wc, kPfQFull))) break;
-                        if (!(ok = mbar_wait_w(&sh.q_full[1], qc[1] & 1, wc, kPfQFull))) break;
-                        ++qc[0];
-                        ++qc[1];
-                        if (!(ok = take(ks))) break;
-                        tc_fence_after();
-                        for (int x = 0; x < 2; ++x) {
-                            pf_issue_qk<D>(col_s(x), sQ + x * G::kQTile, sRing + ks * G::kTile);
-                            umma_commit_w(&sh.s_full[x]);
+            if (two) {
+                if constexpr (kStreams == 2) {
+                    uint32_t ks, vs, items = 0;
+                    auto qk = [&](int x, int flags) {
+                        pf_issue_qk<D>(col_s(x), sQ + x * G::kQTile, sRing + ks * G::kTile);
+                        umma_commit_w(&sh.s_full[x]);
+                        if (x == 1) {
+                            umma_commit_w(&sh.empty[ks]);
+                            if (flags & kLast) umma_commit_w(&sh.q_empty[0]);
                         }
-                        umma_commit_w(&sh.empty[ks]);
-                        if (n == 1) { umma_commit_w(&sh.q_empty[0]); umma_commit_w(&sh.q_empty[1]); }
-                        for (int g = 0; g < n; ++g) {
-                            const bool more = g + 1 < n;
-                            if (!(ok = take(vs))) break;
-                            if (more && !(ok = take(ks))) break;
-                            clean(vs, it.j0 + g, live);
-                            live = live_of(it.j0 + g + 1);
-                            if (g == 0 && done > 0 && !(ok = mbar_wait_w(&sh.x_free, (done - 1) & 1, wc, kPfFree))) break;
-                            for (int x = 0; x < 2; ++x) {
-                                if (!(ok = mbar_wait_w(&sh.p_ready[x], pc[x] & 1, wc, kPfP))) break;
-                                ++pc[x];
-                                tc_fence_after();
-                                pf_issue_pv<D>(tmem + x * G::kColO1, col_s(x), sRing + vs * G::kTile, g > 0);
-                                if (x == 1) umma_commit_w(&sh.empty[vs]);
-                                if (more) {
-                                    pf_issue_qk<D>(col_s(x), sQ + x * G::kQTile, sRing + ks * G::kTile);
-                                    umma_commit_w(&sh.s_full[x]);
-                                    if (g + 2 == n) umma_commit_w(&sh.q_empty[x]);
-                                    if (x == 1) umma_commit_w(&sh.empty[ks]);
-                                }
-                            }
-                            if (!ok) break;
-                        }
-                    }
-                } else {
-                    const uint32_t qs = qsel;
-                    qsel ^= G::kQSlots - 1;
-                    if (!(ok = mbar_wait_w(&sh.q_full[qs], qc[qs] & 1, wc, kPfQFull))) break;
-                    ++qc[qs];
-                    auto qk = [&](int g) {
-                        pf_issue_qk<D>(col_s(g & 1), sQ + qs * G::kQTile, sRing + ks * G::kTile);
-                        umma_commit_w(&sh.s_full[g & 1]);
-                        umma_commit_w(&sh.empty[ks]);
-                        if (g == n - 1) umma_commit_w(&sh.q_empty[qs]);
                     };
-                    for (int g = 0; g < 2 && g < n; ++g) {
-                        if (!(ok = take(ks))) break;
-                        tc_fence_after();
-                        qk(g);
+                    auto new_item = [&]() -> bool { return mbar_wait_w(&sh.q_full[0], items++ & 1, wc, kPfQFull); };
+                    int flags = 0;
+                    if ((ok = desc_wait(0, 0))) flags = sh.desc[0][0].flags;
+                    if (ok && (flags & kMore) && (ok = take(ks)) && (ok = new_item())) {
+                        qk(0, flags);
+                        qk(1, flags);
                     }
-                    for (int g = 0; g < n && ok; ++g) {
-                        const int x = g & 1;
+                    for (uint32_t n = 0; ok && (flags & kMore); ++n) {
+                        const Desc& d = sh.desc[0][n % kDesc];
+                        if (!(ok = desc_wait(0, n + 1))) break;
+                        const int ahead = sh.desc[0][(n + 1) % kDesc].flags;
                         if (!(ok = take(vs))) break;
-                        clean(vs, it.j0 + g, live);
-                        live = live_of(it.j0 + g + 1);
-                        if (g == 0 && done > 0 && !(ok = mbar_wait_w(&sh.x_free, (done - 1) & 1, wc, kPfFree))) break;
-                        if (!(ok = mbar_wait_w(&sh.p_ready[x], pc[x] & 1, wc, kPfP))) break;
-                        ++pc[x];
-                        tc_fence_after();
-                        pf_issue_pv<D>(tmem + (kStreams == 2 ? x * G::kColO1 : 0), col_s(x), sRing + vs * G::kTile, g >= kStreams);
-                        umma_commit_w(&sh.empty[vs]);
-                        if (kStreams == 1) umma_commit_w(&sh.pv_done[x]);
-                        if (g + 2 < n) {
-                            if (!(ok = take(ks))) break;
-                            qk(g + 2);
+                        if ((ahead & kMore) && !(ok = take(ks))) break;
+                        clean(vs, d);
+                        for (int x = 0; x < 2; ++x) {
+                            if (!(ok = mbar_wait_w(&sh.p_ready[x], n & 1, wc, kPfP))) break;
+                            tc_fence_after();
+                            pf_issue_pv<D>(tmem + x * G::kColO1, col_s(x), sRing + vs * G::kTile, !(flags & kFirst));
+                            if (x == 1) umma_commit_w(&sh.empty[vs]);
+                            if (flags & kLast) umma_commit_w(&sh.o_done[x]);
+                            else qk(x, ahead);
                         }
+                        if (!ok) break;
+                        if ((flags & kLast) && (ahead & kMore)) {
+                            if (!(ok = new_item())) break;
+                            qk(0, ahead);
+                            qk(1, ahead);
+                        }
+                        free_desc(0, n);
+                        flags = ahead;
                     }
                 }
-                if (!ok) break;
-                umma_commit_w(&sh.o_done);
-                ++done;
+            } else {
+                uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_item[2] = {0, 0};
+                bool ended[2] = {false, false};
+                // S of worker x's next tile.
+                auto issue_s = [&](int x) -> bool {
+                    if (!desc_wait(x, n_s[x])) return false;
+                    const int flags = sh.desc[x][n_s[x] % kDesc].flags;
+                    if (!(flags & kMore)) {
+                        ended[x] = true;
+                        return true;
+                    }
+                    uint32_t ks;
+                    if (!take(ks)) return false;
+                    if (flags & kFirst) {
+                        const uint32_t i = n_item[x]++;
+                        if (!mbar_wait_w(&sh.q_full[q_slot(x, i)], (i / qn) & 1, wc, kPfQFull)) return false;
+                    }
+                    const int buf = kStreams == 2 ? x : n_s[x] & 1;
+                    pf_issue_qk<D>(col_s(buf), q_addr(x, n_item[x] - 1), sRing + ks * G::kTile);
+                    umma_commit_w(&sh.s_full[buf]);
+                    umma_commit_w(&sh.empty[ks]);
+                    if (flags & kLast) umma_commit_w(&sh.q_empty[q_slot(x, n_item[x] - 1)]);
+                    ++n_s[x];
+                    return true;
+                };
+                for (int i = 0; i < G::kLook && ok; ++i)
+#pragma unroll
+                    for (int x = 0; x < kStreams; ++x)
+                        if (ok && !ended[x]) ok = issue_s(x);
+                bool any = true;
+                while (ok && any) {
+                    any = false;
+#pragma unroll
+                    for (int x = 0; x < kStreams; ++x) {
+                        if (!ok || n_p[x] == n_s[x]) continue;
+                        any = true;
+                        const uint32_t n = n_p[x];
+                        const Desc& d = sh.desc[x][n % kDesc];
+                        const int flags = d.flags, buf = kStreams == 2 ? x : n & 1;
+                        uint32_t vs;
+                        if (!(ok = take(vs))) break;
+                        clean(vs, d);
+                        if (!(ok = mbar_wait_w(&sh.p_ready[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfP))) break;
+                        tc_fence_after();
+                        pf_issue_pv<D>(tmem + x * G::kColO1, col_s(buf), sRing + vs * G::kTile, !(flags & kFirst));
+                        umma_commit_w(&sh.empty[vs]);
+                        if (kStreams == 1) umma_commit_w(&sh.pv_done[buf]);
+                        if (flags & kLast) umma_commit_w(&sh.o_done[x]);
+                        free_desc(x, n);
+                        ++n_p[x];
+                        if (!ended[x]) ok = issue_s(x);
+                    }
+                }
             }
             // All products complete before tensor memory is freed.
             umma_commit_w(&sh.drain);
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
+        } else if (warp >= kSoftWarps + 2 && warp - (kSoftWarps + 2) < workers) {
+            // ------------------------------------------------------ list walkers
+            // Pages of four tiles at a time, a lane each; the next four's loads
+            // (the next item's, past an item's end) run while these are handed on.
+            const int x = warp - (kSoftWarps + 2), q = lane >> 3, part = lane & 7;
+            Walk<D> walk;
+            walk.start(a, t, sh.hdr, x);
+            Item it, ahead;
+            auto pages = [&](const Item& i, int j) {
+                const int tile = j + q, key = tile * kN + (part << part_log2);
+                if (part >= parts || tile >= i.j1 || key >= i.nkeys) return -1;
+                const int p = i.tab[key >> a.ps_log2];
+                return p >= 0 && p < a.P ? p : -1;
+            };
+            uint32_t n = 0;
+            bool ok = true, more = walk.next(a, t, it);
+            int j = more ? it.j0 : 0, val = more ? pages(it, j) : -1;
+            while (ok) {
+                int j_next = j + 4, val_next = -1;
+                bool more_next = more;
+                ahead = it;
+                if (more) {
+                    if (j_next >= it.j1) {
+                        more_next = walk.next(a, t, ahead);
+                        j_next = more_next ? ahead.j0 : 0;
+                    }
+                    if (more_next) val_next = pages(ahead, j_next);
+                }
+                const int last = more ? min(j + 4, it.j1) : j + 1;
+                for (int jj = j; jj < last && ok; ++jj, ++n) {
+                    if (!(ok = mbar_wait_w(few ? &sh.d_empty8[n % kDesc] : &sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
+                    Desc& d = sh.desc[x][n % kDesc];
+                    const uint32_t live = __ballot_sync(0xffffffffu, val >= 0);
+                    if (q == jj - j) d.page[part] = val;
+                    if (lane == 0) {
+                        d.live = (live >> (8 * (jj - j))) & 0xff;
+                        d.flags = more ? kMore | (jj == it.j0 ? kFirst : 0) | (jj == it.j1 - 1 ? kLast : 0) : 0;
+                        d.j = jj;
+                        d.nkeys = it.nkeys;
+                        d.lim0 = it.lim0;
+                        d.hk = it.hk;
+                        d.tok0 = it.tok0;
+                        d.ntok = it.ntok;
+                        d.seg = it.seg;
+                        d.pre = it.pre;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.d_full[x][n % kDesc]);
+                }
+                if (!more) break;
+                it = ahead;
+                more = more_next;
+                j = j_next;
+                val = val_next;
+            }
+            __syncwarp();
         }
+    } else if (few) {
+        regs_inc<216>();
+        float* merge = reinterpret_cast<float*>(gbase + G::kFewQ);
+        if (D == 256 || (pre ? a.qstep_p : a.qstep_s) <= 16)
+            few_rows<D, 1>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
+        else if constexpr (D != 256)
+            few_rows<D, 2>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
     } else {
-        if constexpr (kStreams == 2) regs_inc<216>();
+        regs_inc<216>();
         // ------------------------------------------------------------- softmax
-        const int wg = warp >> 2;
+        const int wg = warp >> 2, x = two ? 0 : wg;           // worker
         const int r = (warp & 3) * 32 + lane;                 // row of the tile == TMEM lane
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int r_tok = r / a.G;                            // token of the tile
+        const uint32_t tO = lanes + wg * G::kColO1;
+        const int tok = r / a.G + (two ? wg * a.tq : 0);      // token of the block
         const float scale = a.scale_log2;
-        uint32_t sc[2] = {0, 0}, done = 0, xc = 0;
-        bool ok = true;
-        auto page_bits = [&](int j) {
-            return __ballot_sync(0xffffffffu, lane < parts && part_page<kN>(a, it, j, lane, part_log2) >= 0);
-        };
-        while (ok && walk.next(a, t, it)) {
-            const bool two = it.ntok > a.tq;
-            const int tok = r_tok + (two ? wg * a.tq : 0);     // token of the block
-            const bool valid = r < a.tq * a.G && tok < it.ntok;
-            const bool live_warp = __any_sync(0xffffffffu, valid);
-            const int lim_row = it.pre ? it.nkeys : min(it.nkeys, it.lim0 + tok);
-            const int step = two || kStreams == 1 ? 1 : 2;
-            float m_ref = -INFINITY, l = 0.f;
-            bool first = true;
-            int j = it.j0 + (step == 2 ? wg : 0);
-            uint32_t bits = j < it.j1 ? page_bits(j) : 0;
-            for (; j < it.j1; j += step) {
-                const int x = kStreams == 2 ? wg : (j - it.j0) & 1;
-                const uint32_t tS = lanes + G::kColS + x * G::kColSStep;
-                const uint32_t cur = bits;
-                if (j + step < it.j1) bits = page_bits(j + step);
-                if (!(ok = mbar_wait_w(&sh.s_full[x], sc[x] & 1, wc, kPfS))) break;
-                ++sc[x];
-                tc_fence_after();
-                if (live_warp) {
-                    float s[kN];
-                    {
-                        uint32_t* su = reinterpret_cast<uint32_t*>(s);
-#pragma unroll
-                        for (int c = 0; c < kN; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(su + c));
-                        tmem_wait_ld();
-                    }
-                    const int k0 = j * kN;
-                    if (__any_sync(0xffffffffu, k0 + kN > lim_row)) {
-                        const int lim = lim_row - k0;
-#pragma unroll
-                        for (int c = 0; c < kN; ++c)
-                            if (c >= lim) s[c] = -INFINITY;
-                    }
-                    if (cur != (1u << parts) - 1u) {
-#pragma unroll
-                        for (int c = 0; c < kN; ++c)
-                            if (!((cur >> (c >> part_log2)) & 1u)) s[c] = -INFINITY;
-                    }
-                    float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]), mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
-#pragma unroll
-                    for (int c = 8; c < kN; c += 8) {
-                        mx0 = fmax3(mx0, s[c], s[c + 1]);
-                        mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
-                        mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
-                        mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
-                    }
-                    const float m_new = fmaxf(m_ref, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale);
-                    // Rows that hold no query must not decide: what they hold is left over.
-                    const bool jump = valid && ((m_ref == -INFINITY) ? (m_new != -INFINITY) : (m_new - m_ref > kTau));
-                    if (__any_sync(0xffffffffu, jump)) {
-                        const float fac = (m_ref == -INFINITY) ? 0.f : ex2_mufu(m_ref - m_new);
-                        l *= fac;
-                        if (!first) {
-                            // Two streams: S of this tile was issued after the
-                            // stream's last P V.  One stream: the P V of the
-                            // tile before may still run; its barrier (of two,
-                            // by turns) cannot be a phase further.
-                            const uint32_t tO = lanes + (kStreams == 2 ? wg * G::kColO1 : 0);
-                            if (kStreams == 1) {
-                                if (!(ok = mbar_wait_w(&sh.pv_done[x ^ 1], (sc[x ^ 1] - 1) & 1, wc, kPfPV))) break;
-                                tc_fence_after();
-                            }
-#pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 32) {
-                                uint32_t o[32];
-                                tmem_ld32(tO + c0, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
-                                tmem_st32(tO + c0, o);
-                            }
-                        }
-                        m_ref = m_new;
-                    }
-                    const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-                    const uint64_t sc2 = f2_pack(scale, scale), nm2 = f2_pack(-m_use, -m_use);
-                    uint64_t la = f2_pack(0.f, 0.f), lb = la;
-#pragma unroll
-                    for (int st = 0; st < kN / 32; ++st) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int c = st * 32 + 2 * i;
-                            float x0, x1;
-                            f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nm2), x0, x1);
-                            const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
-                            if (i & 1) lb = f2_add(lb, f2_pack(p0, p1));
-                            else la = f2_add(la, f2_pack(p0, p1));
-                            pk[i] = pack_bf16x2(p0, p1);   // 16-bit weights feed the tensor core; l keeps 32 bits
-                        }
-                        tmem_st16(tS + st * 16, pk);
-                    }
-                    float a0, a1, b0, b1;
-                    f2_unpack(la, a0, a1);
-                    f2_unpack(lb, b0, b1);
-                    l += (a0 + a1) + (b0 + b1);
-                    tmem_wait_st();
-                }
-                first = false;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_ready[x]);
+        uint32_t items = 0;
+        bool ok = true, valid = false, live_warp = false;
+        int lim_row = 0, seg = 0;
+        float m_ref = -INFINITY, l = 0.f;
+        for (uint32_t n = 0; x < workers; ++n) {   // d = 256: one worker, the second four warps have none
+            if (!(ok = desc_wait(x, n))) break;
+            const Desc& d = sh.desc[x][n % kDesc];
+            const int flags = d.flags, live = d.live, k0 = d.j * kN;
+            if (!(flags & kMore)) break;
+            if (flags & kFirst) {
+                valid = r < a.tq * a.G && tok < d.ntok;
+                live_warp = __any_sync(0xffffffffu, valid);
+                lim_row = pre ? d.nkeys : min(d.nkeys, d.lim0 + tok);
+                seg = d.seg;
+                m_ref = -INFINITY;
+                l = 0.f;
             }
-            if (!ok) break;
-            // -------------------------------------------------------- epilogue
-            // The rows' (m, l, O) into the segment's place.
-            const int row = two ? wg * a.tq * a.G + r : r;
-            const long long at = (long long)it.seg * (it.pre ? a.rows_p : a.rows_s) + row;
-            float* orow = (it.pre ? a.o_p : a.o_s) + at * D;
-            float2* ml = (it.pre ? a.ml_p : a.ml_s) + at;
-            const bool join = kStreams == 2 && !two;
-            float f_own = 1.f, f_other = 0.f, m = m_ref, l_all = l;
-            bool other = false;
-            if (join) {
-                // One row tile, two streams: weights of both accumulators.
-                sh.ml[xc & 1][wg][r] = make_float2(m_ref, l);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.x_ready);
-                if (!(ok = mbar_wait_w(&sh.x_ready, xc & 1, wc, kPfExchange))) break;
-                const float2 o2 = sh.ml[xc & 1][wg ^ 1][r];
-                ++xc;
-                m = fmaxf(m_ref, o2.x);
-                f_own = m_ref == -INFINITY ? 0.f : ex2_mufu(m_ref - m);
-                f_other = o2.x == -INFINITY ? 0.f : ex2_mufu(o2.x - m);
-                l_all = l * f_own + o2.y * f_other;
-                other = it.j1 - it.j0 > 1;     // the second stream had a tile
-            }
-            if (!(ok = mbar_wait_w(&sh.o_done, done & 1, wc, kPfO))) break;
-            ++done;
+            const int buf = kStreams == 2 ? wg : n & 1;
+            const uint32_t tS = lanes + G::kColS + buf * G::kColSStep;
+            if (!(ok = mbar_wait_w(&sh.s_full[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfS))) break;
             tc_fence_after();
             if (live_warp) {
-                const int c_lo = join ? wg * (D / 2) : 0, c_hi = join ? c_lo + D / 2 : D;
-                const uint32_t t_own = lanes + (kStreams == 2 ? (join ? 0 : wg * G::kColO1) : 0);
-                const float f0 = join ? (wg == 0 ? f_own : f_other) : 1.f, f1 = wg == 0 ? f_other : f_own;
-#pragma unroll 1
-                for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(t_own + c0, o);
-                    tmem_wait_ld();
-                    if (join) {
+                float s[kN];
+                {
+                    uint32_t* su = reinterpret_cast<uint32_t*>(s);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f0);
-                        if (other) {
-                            uint32_t o1[32];
-                            tmem_ld32(lanes + G::kColO1 + c0, o1);
+                    for (int c = 0; c < kN; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(su + c));
+                    tmem_wait_ld();
+                }
+                if (__any_sync(0xffffffffu, k0 + kN > lim_row)) {
+                    const int lim = lim_row - k0;
+#pragma unroll
+                    for (int c = 0; c < kN; ++c)
+                        if (c >= lim) s[c] = -INFINITY;
+                }
+                if (live != (1 << parts) - 1) {
+                    // Keys of absent pages, 32 at a time (a part is a multiple of 16).
+#pragma unroll
+                    for (int c0 = 0; c0 < kN; c0 += 32) {
+                        uint32_t w = 0;
+                        for (int h = 0; h < 2; ++h)
+                            if ((live >> ((c0 + 16 * h) >> part_log2)) & 1) w |= 0xffffu << (16 * h);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!((w >> c) & 1u)) s[c0 + c] = -INFINITY;
+                    }
+                }
+                // Row maximum in four chains of three-input maxima, the
+                // exponents two at a time, the row sum in two packed sums (as in
+                // the forward kernels).
+                float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]), mx2 = fmaxf(s[4], s[5]), mx3 = fmaxf(s[6], s[7]);
+#pragma unroll
+                for (int c = 8; c < kN; c += 8) {
+                    mx0 = fmax3(mx0, s[c], s[c + 1]);
+                    mx1 = fmax3(mx1, s[c + 2], s[c + 3]);
+                    mx2 = fmax3(mx2, s[c + 4], s[c + 5]);
+                    mx3 = fmax3(mx3, s[c + 6], s[c + 7]);
+                }
+                const float m_new = fmaxf(m_ref, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale);
+                // Rows that hold no query must not decide: what they hold is left over.
+                const bool jump = valid && ((m_ref == -INFINITY) ? (m_new != -INFINITY) : (m_new - m_ref > kTau));
+                if (__any_sync(0xffffffffu, jump)) {
+                    const float fac = (m_ref == -INFINITY) ? 0.f : ex2_mufu(m_ref - m_new);
+                    l *= fac;
+                    if (!(flags & kFirst)) {
+                        // Single-buffered S: it was issued after the worker's last
+                        // P V.  Double-buffered: the P V of the tile before may
+                        // still run; its barrier (of two, by turns) has completed
+                        // every earlier phase, since this S was issued after the
+                        // P V of two tiles before, and cannot be a phase further.
+                        if (kStreams == 1) {
+                            if (!(ok = mbar_wait_w(&sh.pv_done[buf ^ 1], ((n - 1) >> 1) & 1, wc, kPfPV))) break;
+                            tc_fence_after();
+                        }
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + c0, o);
                             tmem_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                o[i] = __float_as_uint(fmaf(__uint_as_float(o1[i]), f1, __uint_as_float(o[i])));
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac);
+                            tmem_st32(tO + c0, o);
                         }
                     }
+                    m_ref = m_new;
+                }
+                const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
+                const uint64_t sc2 = f2_pack(scale, scale), nm2 = f2_pack(-m_use, -m_use);
+                uint64_t la = f2_pack(0.f, 0.f), lb = la;
+#pragma unroll
+                for (int st = 0; st < kN / 32; ++st) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int c = st * 32 + 2 * i;
+                        float x0, x1;
+                        f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, nm2), x0, x1);
+                        const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
+                        if (i & 1) lb = f2_add(lb, f2_pack(p0, p1));
+                        else la = f2_add(la, f2_pack(p0, p1));
+                        pk[i] = pack_bf16x2(p0, p1);   // 16-bit weights feed the tensor core; l keeps 32 bits
+                    }
+                    tmem_st16(tS + st * 16, pk);
+                }
+                float a0, a1, b0, b1;
+                f2_unpack(la, a0, a1);
+                f2_unpack(lb, b0, b1);
+                l += (a0 + a1) + (b0 + b1);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_ready[buf]);
+            if (!(flags & kLast)) continue;
+            // Epilogue: the rows' (m, l, O) into the segment's place.  The next
+            // item's first P V overwrites O only after this warp's next P.
+            if (!(ok = mbar_wait_w(&sh.o_done[wg], items & 1, wc, kPfO))) break;
+            ++items;
+            tc_fence_after();
+            if (live_warp) {
+                const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s) + (two ? wg * a.tq * a.G + r : r);
+                float* orow = (pre ? a.o_p : a.o_s) + at * D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c0, o);
+                    tmem_wait_ld();
                     if (valid) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -761,11 +1116,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                                            "r"(o[8 * q + 7]) : "memory");
                     }
                 }
-                if (valid && (!join || wg == 0)) *ml = make_float2(m, l_all);
+                if (valid) (pre ? a.ml_p : a.ml_s)[at] = make_float2(m_ref, l);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.x_free);
         }
     }
 
@@ -888,7 +1240,7 @@ struct PfLayout {
 };
 
 // Workspace: header, tables, the segments' rows.  Prefix segments: one an item
-// and CTA boundary; the requests': sum of ceil(n_b / tb) <= T / tb + B items a
+// and worker; the requests': sum of ceil(n_b / tb) <= T / tb + B items a
 // key/value head.
 PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms) {
     PfLayout w;
@@ -896,8 +1248,8 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
     w.tb = d == 256 ? w.tq : 2 * w.tq;
     w.rows_p = (T < w.tb ? T : w.tb) * G;
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
-    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + sms;
-    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + sms;
+    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + 2 * sms;
+    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + 2 * sms;
     w.pref = align256(sizeof(PfHeader));
     w.items = align256(w.pref + (size_t)(B + 1) * 8);
     w.cu = align256(w.items + (size_t)(B + 1) * 4);
@@ -1006,13 +1358,16 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.rows_s = w.rows_s;
     a.tiles_p = (prefix_len + kN - 1) / kN;
     a.blocks_p = (T + w.tb - 1) / w.tb;
-    a.weight_p = w.rows_p > 128 ? 2 : 1;
-    a.weight_s = w.rows_s > 128 ? 2 : 1;
+    a.mode_p = T * (long long)G <= kFewRows ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
+    a.mode_s = max_seqlen * (long long)G <= kFewRows ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
+    const int box_p = T < w.tq ? T : w.tq, box_s = max_seqlen < w.tq ? max_seqlen : w.tq;
+    a.qstep_p = (box_p * G + 7) & ~7;
+    a.qstep_s = (box_s * G + 7) & ~7;
     a.scale_log2 = alpha * 1.4426950408889634f;
 
     CUtensorMap tq_p, tq_s, tk, tv;
-    int rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, w.tq);
-    if (rc == FA_OK) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, max_seqlen < w.tq ? max_seqlen : w.tq);
+    int rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
+    if (rc == FA_OK) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
     const long long slots = (long long)num_pages * Hkv * page_size;
     const int part = page_size < kN ? page_size : kN;
     if (rc == FA_OK) rc = make_map_pages(&tk, k_pages, d, slots, part);
