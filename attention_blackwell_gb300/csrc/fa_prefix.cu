@@ -74,17 +74,17 @@ template <int D> struct Pf {
 
 // What both kernels need to know of the list of units.
 struct PfTables {
-    long long* pref;     // [B+1] units of requests before b (all key/value heads)
+    int* pref;           // [B+1] units of requests before b (all key/value heads)
     int* items;          // [B+1] items of requests before b
     int* cu;             // [B+1] sanitised offsets
     int* len;            // [B] own keys
 };
 
 struct PfHeader {
-    long long per_p, per_s;   // units a worker: of the prefix, of the requests
+    int per_p, per_s;         // units a worker: of the prefix, of the requests
     int n_p;                  // CTAs on the prefix; the rest are on the requests
     int bad;                  // a request has more rows than max_seqlen
-    int pad[10];
+    int pad[12];
 };
 
 struct PfArgs {
@@ -114,7 +114,7 @@ enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kP
 
 struct Item {
     const int* tab;
-    int pre, hk, tok0, ntok, j0, j1, nkeys, lim0;
+    int hk, tok0, ntok, j0, j1, nkeys, lim0;
     int seg;
 };
 
@@ -123,7 +123,7 @@ struct Desc {
     int page[8];            // its parts' pages, -1: none
     int live;               // one bit a part that has a page
     int flags;              // kMore (not the list's end), kFirst, kLast of its item's tiles here
-    int j, nkeys, lim0, hk, tok0, ntok, seg, pre;
+    int j, nkeys, lim0, hk, tok0, ntok, seg;
 };
 constexpr int kMore = 1, kFirst = 2, kLast = 4;
 constexpr int kDesc = 8;    // tiles the walkers run ahead by
@@ -136,19 +136,22 @@ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int block_of(int k, int n) { return (k & 1) ? n - 1 - (k >> 1) : k >> 1; }
 __device__ __forceinline__ int index_of(int rb, int n) { return rb < (n + 1) / 2 ? 2 * rb : 2 * (n - 1 - rb) + 1; }
 
-// A worker's walk over its range of units.
+// Units an item of request b has (0: no rows or no keys), its rows and row blocks.
+template <int D>
+__device__ __forceinline__ int item_units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
+    n = t.cu[b + 1] - t.cu[b];
+    nb = cdiv(n, a.tb);
+    return n > 0 && t.len[b] > 0 ? cdiv(t.len[b], Pf<D>::kN) + kOverheadUnits : 0;
+}
+
+// A worker's walk over its range of units.  Everything fits 32 bits: the host
+// refuses longer lists.
 template <int D>
 struct Walk {
     static constexpr int kN = Pf<D>::kN;
-    long long u, end;
+    int u, end;
     int b, hk, k, worker;
     bool pre;
-
-    __device__ __forceinline__ static int units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
-        n = t.cu[b + 1] - t.cu[b];
-        nb = cdiv(n, a.tb);
-        return n > 0 && t.len[b] > 0 ? cdiv(t.len[b], kN) + kOverheadUnits : 0;
-    }
 
     // Worker `x` of this CTA.
     __device__ __forceinline__ void start(const PfArgs& a, const PfTables& t, const PfHeader& h, int x) {
@@ -157,10 +160,10 @@ struct Walk {
         pre = c < h.n_p;
         const int width = (pre ? a.mode_p : a.mode_s) == kOne ? Pf<D>::kStreams : 1;
         worker = (pre ? c : c - h.n_p) * width + x;
-        const long long per = pre ? h.per_p : h.per_s;
-        const long long all = pre ? (long long)a.Hkv * a.blocks_p * a.tiles_p : t.pref[a.B];
-        u = worker * per;
-        end = u + per < all ? u + per : all;
+        const int per = pre ? h.per_p : h.per_s, all = pre ? a.Hkv * a.blocks_p * a.tiles_p : t.pref[a.B];
+        // worker * per passes the list's end by at most a CTA count times per.
+        u = worker >= (all + per - 1) / per ? all : worker * per;
+        end = min(all - u, per) + u;
         if (h.bad || x >= width || u >= end) {
             u = end = 0;
             return;
@@ -173,19 +176,17 @@ struct Walk {
         }
         b = lo;
         int n, nb;
-        const int per_item = units(a, t, b, n, nb);
-        const int i = (int)((u - t.pref[b]) / per_item);
-        hk = i / nb;
+        const int per_item = item_units<D>(a, t, b, n, nb), i = (u - t.pref[b]) / per_item;
+        hk = nb == 1 ? i : i / nb;
         k = i - hk * nb;
     }
 
     __device__ __forceinline__ bool next(const PfArgs& a, const PfTables& t, Item& it) {
         while (u < end) {
             if (pre) {
-                const int i = (int)(u / a.tiles_p);
-                it.j0 = (int)(u - (long long)i * a.tiles_p);
-                const long long left = end - u;
-                it.j1 = left < a.tiles_p - it.j0 ? it.j0 + (int)left : a.tiles_p;
+                const int i = u / a.tiles_p;
+                it.j0 = u - i * a.tiles_p;
+                it.j1 = min(a.tiles_p, it.j0 + end - u);
                 u += it.j1 - it.j0;
                 it.hk = i / a.blocks_p;
                 it.tok0 = (i - it.hk * a.blocks_p) * a.tb;
@@ -194,15 +195,12 @@ struct Walk {
                 it.lim0 = INT_MAX / 2;
                 it.tab = a.prefix_table;
                 it.seg = i + worker;
-                it.pre = 1;
                 return true;
             }
             int n, nb;
-            const int per_item = units(a, t, b, n, nb), s = t.len[b];
+            const int per_item = item_units<D>(a, t, b, n, nb), s = t.len[b];
             const int i = hk * nb + k;
-            const int first = (int)(u - (t.pref[b] + (long long)i * per_item));
-            const long long left = end - u;
-            const int last = left < per_item - first ? first + (int)left : per_item;
+            const int first = u - (t.pref[b] + i * per_item), last = min(per_item, first + end - u);
             u += last - first;
             const int i0 = block_of(k, nb) * a.tb;
             it.hk = hk;
@@ -212,7 +210,6 @@ struct Walk {
             it.lim0 = s - n + i0 + 1;
             it.tab = a.table + (long long)b * a.W;
             it.seg = t.items[b] + i + worker;
-            it.pre = 0;
             it.j0 = first;
             const int seen = it.lim0 + it.ntok - 1;        // keys the block's last row sees
             it.j1 = min(last, seen > 0 ? cdiv(seen, kN) : 0);
@@ -231,119 +228,137 @@ struct Walk {
     }
 };
 
-// Inclusive scan of one value a thread over the block (nthreads a multiple of 32).
-template <typename V, typename Op>
-__device__ __forceinline__ V block_scan(V v, V* s_warp, int tid, int nthreads, Op op) {
-    const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const V x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v = op(x, v);
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) v = op(s_warp[w], v);
-    return v;
-}
-
+// Barriers, by their arrival counts.
 struct PfShared {
     Desc desc[2][kDesc];
-    uint64_t d_full[2][kDesc], d_empty[2][kDesc];
-    uint64_t q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], p_ready[2], pv_done[2], o_done[2], drain;
-    // Few rows: the eight warps hand back tiles, Q, descriptions and the join's buffer.
+    // One arrival a phase.
+    uint64_t d_full[2][kDesc], d_empty[2][kDesc], q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], pv_done[2], o_done[2], drain;
+    // Four: the warps of a softmax warpgroup.
+    uint64_t p_ready[2];
+    // Eight: few rows; the warps hand back tiles, Q, descriptions and the join's buffer.
     uint64_t empty8[8], q_empty8[2], d_empty8[kDesc], m_full, m_free;
     float2 ml[8][kFewRows];
-    long long scan64[12];
-    int scan32[12];
-    float scanf[12];
-    PfHeader hdr;
+    int4 scan[12];
     uint32_t tmem_base;
-    int abort_flag;
+    int abort_flag, bad;
 };
 
-// The tables of the list, by every thread of the block: offsets by the
-// library's one rule (a running maximum), units and items before each request,
-// and how many CTAs work on the prefix.
+// The tables of the list, by every thread of the block: the offsets by the
+// library's one rule, units and items before each request, and how many CTAs
+// work on the prefix.  Three block barriers when the offsets are well formed
+// and B <= 384: a single-token call's latency begins here.
 template <int D>
-__device__ __forceinline__ void build_tables(const PfArgs& a, const PfTables& t, PfShared& sh, int tid, int nthreads) {
-    const int per = (a.B + 1 + nthreads - 1) / nthreads, i0 = tid * per;
-    int run = 0;
-    auto offset = [&](int i) {
-        const int c = a.cu ? a.cu[i] : i;
-        return c < 0 ? 0 : (c > a.T ? a.T : c);
-    };
-    for (int i = i0; i < min(i0 + per, a.B + 1); ++i) run = max(run, offset(i));
-    // Exclusive running maximum up to this thread's entries.
-    const int upto = block_scan(run, sh.scan32, tid, nthreads, [](int x, int y) { return max(x, y); });
-    int before = __shfl_up_sync(0xffffffffu, upto, 1);
-    if ((tid & 31) == 0) {
-        before = 0;
-        for (int w = 0; w < (tid >> 5); ++w) before = max(before, sh.scan32[w]);
-    }
-    for (int i = i0; i < min(i0 + per, a.B + 1); ++i) {
-        before = max(before, offset(i));
-        t.cu[i] = before;
+__device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables& t, PfShared& sh, int tid) {
+    constexpr int kThreads = Pf<D>::kThreads, kWarps = kThreads / 32;
+    const int lane = tid & 31, warp = tid >> 5;
+    const long long cap = (long long)a.W << a.ps_log2;
+    bool fine = true;
+    for (int i = tid; i <= a.B; i += kThreads) {
+        const int c = a.cu ? a.cu[i] : i, before = a.cu && i > 0 ? a.cu[i - 1] : 0;
+        fine = fine && c >= before && c >= 0 && c <= a.T;
+        t.cu[i] = c;
         if (i < a.B) {
-            const long long cap = (long long)a.W << a.ps_log2;
             const int s = a.kv_lens[i];
             t.len[i] = s < 0 ? 0 : (s > cap ? (int)cap : s);
         }
     }
-    if (tid == 0) sh.hdr.bad = 0;
-    __syncthreads();
-    long long mine = 0;
-    int my_items = 0;
+    if (tid == 0) sh.bad = 0;
+    if (!__syncthreads_and(fine)) {
+        // Clamped to [0, T] and raised to the one before: a running maximum.
+        if (warp == 0) {
+            int run = 0;
+            for (int base = 0; base <= a.B; base += 32) {
+                int c = base + lane <= a.B ? t.cu[base + lane] : 0;
+                c = c < 0 ? 0 : (c > a.T ? a.T : c);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, c, o);
+                    if (lane >= o) c = max(c, x);
+                }
+                c = max(c, run);
+                if (base + lane <= a.B) t.cu[base + lane] = c;
+                run = __shfl_sync(0xffffffffu, c, 31);
+            }
+        }
+        __syncthreads();
+    }
+    int units = 0, items = 0;      // of the requests before this round's
     float cost = 0.f;
-    for (int i = i0; i < min(i0 + per, a.B); ++i) {
-        int n, nb;
-        const int u = Walk<D>::units(a, t, i, n, nb);
-        if (n > a.max_seqlen) sh.hdr.bad = 1;
-        mine += (long long)u * nb * a.Hkv;
-        my_items += nb * a.Hkv;
-        // What the causal mask leaves of a row block's tiles, on average.
-        const float left = fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)));
-        cost += (float)u * nb * a.Hkv * left;
+    for (int base = 0; base < a.B; base += kThreads) {
+        const int i = base + tid;
+        int u = 0, it = 0;
+        float c = 0.f;
+        if (i < a.B) {
+            int n, nb;
+            const int per = item_units<D>(a, t, i, n, nb);
+            if (n > a.max_seqlen) sh.bad = 1;
+            it = nb * a.Hkv;
+            u = per * it;
+            // What the causal mask leaves of a row block's tiles, on average.
+            c = (float)u * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)));
+        }
+        const int u_own = u, it_own = it;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, it, o);
+            if (lane >= o) {
+                u += x;
+                it += y;
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        if (base) __syncthreads();
+        if (lane == 31) sh.scan[warp] = make_int4(u, it, __float_as_int(c), 0);
+        __syncthreads();
+        int u_all = 0, it_all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int4 x = sh.scan[w];
+            if (w == warp) {
+                u += units + u_all;
+                it += items + it_all;
+            }
+            u_all += x.x;
+            it_all += x.y;
+            cost += __int_as_float(x.z);
+        }
+        if (i < a.B) {
+            t.pref[i] = u - u_own;
+            t.items[i] = it - it_own;
+        }
+        units += u_all;
+        items += it_all;
     }
-    const long long upto64 = block_scan(mine, sh.scan64, tid, nthreads, [](long long x, long long y) { return x + y; });
-    const int upto_items = block_scan(my_items, sh.scan32, tid, nthreads, [](int x, int y) { return x + y; });
-    const float upto_cost = block_scan(cost, sh.scanf, tid, nthreads, [](float x, float y) { return x + y; });
-    long long at = upto64 - mine;
-    int at_items = upto_items - my_items;
-    if (tid == 0) { t.pref[0] = 0; t.items[0] = 0; }
-    for (int i = i0; i < min(i0 + per, a.B); ++i) {
-        int n, nb;
-        const int u = Walk<D>::units(a, t, i, n, nb);
-        at += (long long)u * nb * a.Hkv;
-        at_items += nb * a.Hkv;
-        t.pref[i + 1] = at;
-        t.items[i + 1] = at_items;
-    }
-    if (tid == nthreads - 1) {
-        const int grid = gridDim.x;
-        const long long units_p = (long long)a.Hkv * a.blocks_p * a.tiles_p, units_s = upto64;
-        // Two row tiles take twice the tensor time of one.
-        const float cp = (float)units_p * (a.mode_p == kTwo ? 2 : 1), cs = upto_cost * (a.mode_s == kTwo ? 2 : 1);
-        int np = units_p == 0 ? 0 : (units_s == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
-        if (units_p > 0 && units_s > 0) np = grid == 1 ? 1 : max(1, min(grid - 1, np));
-        const int wp = np * (a.mode_p == kOne ? Pf<D>::kStreams : 1), ws = max(1, grid - np) * (a.mode_s == kOne ? Pf<D>::kStreams : 1);
-        sh.hdr.n_p = np;
-        sh.hdr.per_p = wp ? (units_p + wp - 1) / wp : 1;
-        sh.hdr.per_s = units_s ? (units_s + ws - 1) / ws : 1;
+    if (tid == 0) {
+        t.pref[a.B] = units;
+        t.items[a.B] = items;
     }
     __syncthreads();
+    PfHeader h;
+    const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
+    // Two row tiles take twice the tensor time of one.
+    const float cp = (float)units_p * (a.mode_p == kTwo ? 2 : 1), cs = cost * (a.mode_s == kTwo ? 2 : 1);
+    int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
+    if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
+    const int wp = np * (a.mode_p == kOne ? Pf<D>::kStreams : 1), ws = max(1, grid - np) * (a.mode_s == kOne ? Pf<D>::kStreams : 1);
+    h.n_p = np;
+    h.per_p = wp ? (units_p + wp - 1) / wp : 1;
+    h.per_s = units ? (units + ws - 1) / ws : 1;
+    h.bad = sh.bad;
     if (blockIdx.x == 0) {
-        for (int i = tid; i <= a.B; i += nthreads) {
+        for (int i = tid; i <= a.B; i += kThreads) {
             a.ws.pref[i] = t.pref[i];
             a.ws.items[i] = t.items[i];
             a.ws.cu[i] = t.cu[i];
             if (i < a.B) a.ws.len[i] = t.len[i];
         }
         if (tid == 0) {
-            *a.hdr = sh.hdr;
-            if (sh.hdr.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 101; a.status->block = 0; }
+            *a.hdr = h;
+            if (h.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 101; a.status->block = 0; }
         }
     }
+    return h;
 }
 
 // ------------------------------------------------------------------ products
@@ -378,8 +393,9 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 // warp in four; the copies set the pace here, so the eight warps take 16 keys
 // of a tile each (mma.sync m16n8k16, scores and weights stay in registers) with
 // maxima, sums and accumulators of their own, joined through shared memory at
-// the item's end.  kMT 16-row tiles a warp; at d = 256 (64-key tiles) four warps
-// take the keys and the second four the second 16 rows.
+// the item's end.  With more than 16 rows, and at d = 256 (64-key tiles), four
+// warps share the keys (kKT = 32 or 16 each) and the second four take the second
+// 16 rows.
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -394,13 +410,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int kMT>
+template <int D, int kKT>
 __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t sQ, uint32_t sRing, float* merge, const WaitCtx& wc,
                                          bool pre, int warp, int lane, int part_log2) {
     using G = Pf<D>;
     constexpr int kN = G::kN, kRing = G::kRing;
-    constexpr int kKeyGroups = kN / 16, kOwners = kKeyGroups;        // warps that add to one row
-    constexpr bool kKeepQ = D * kMT <= 128;                          // Q's fragments in registers
+    constexpr int kKeys = 16 * kKT, kKeyGroups = kN / kKeys;         // keys a warp, warps that add to one row
+    constexpr bool kKeepQ = D <= 128;                                // Q's fragments in registers
     constexpr int kKSteps = D / 16, kNT = D / 8;
     const int kg = warp % kKeyGroups, row0 = (warp / kKeyGroups) * 16;
     const int g = lane >> 2, t2 = (lane & 3) * 2;
@@ -408,17 +424,17 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
     // which 16-byte chunk of each 32-byte step it is; chunks are swizzled by
     // row % 8 within a 128-byte row.
     const int mi = lane >> 3, mr = lane & 7;
-    const uint32_t k_row = (kg * 16 + (mi >> 1) * 8 + mr) * 128u, v_row = (kg * 16 + (mi & 1) * 8 + mr) * 128u;
+    const uint32_t k_row = (kg * kKeys + (mi >> 1) * 8 + mr) * 128u, v_row = (kg * kKeys + (mi & 1) * 8 + mr) * 128u;
     const uint32_t q_row = (row0 + (mi & 1) * 8 + mr) * 128u;
     const float scale = a.scale_log2;
     uint32_t n_item = 0, n_merge = 0;
-    uint32_t qf[kKeepQ ? kMT : 1][kKeepQ ? kKSteps : 1][4];
-    float o[kMT][kNT][4], m[kMT][2], l[kMT][2];
-    int lim[kMT][2], nkeys = 0, lim_min = 0, lim_max = 0, rows = 0, seg = 0;
+    uint32_t qf[kKeepQ ? kKSteps : 1][4];
+    float o[kNT][4], m[2], l[2];
+    int lim[2], nkeys = 0, lim_min = 0, lim_max = 0, rows = 0, seg = 0;
     uint32_t q_base = sQ;
     bool idle = false;
-    auto q_frag = [&](uint32_t (&f)[4], int ks, int mt) {
-        ldsm4(f, q_base + (ks >> 2) * 4096u + mt * 2048u + q_row + (((((ks & 3) << 1) + (mi >> 1)) ^ mr) << 4));
+    auto q_frag = [&](uint32_t (&f)[4], int ks) {
+        ldsm4(f, q_base + (ks >> 2) * 4096u + q_row + (((((ks & 3) << 1) + (mi >> 1)) ^ mr) << 4));
     };
     auto arrive = [&](uint64_t* bar) {
         __syncwarp();
@@ -427,8 +443,10 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
     for (uint32_t n = 0;; ++n) {
         if (!mbar_wait_w(&sh.d_full[0][n % kDesc], (n / kDesc) & 1, wc, kPfDesc)) return false;
         const Desc& d = sh.desc[0][n % kDesc];
-        const int flags = d.flags, k0 = d.j * kN + kg * 16;
-        const bool page = (d.live >> ((kg * 16) >> part_log2)) & 1;
+        const int flags = d.flags, k0 = d.j * kN + kg * kKeys;
+        int live = 0;                                   // one bit a 16-key part that has a page
+#pragma unroll
+        for (int kt = 0; kt < kKT; ++kt) live |= ((d.live >> ((kg * kKeys + 16 * kt) >> part_log2)) & 1) << kt;
         if (!(flags & kMore)) return true;
         if (flags & kFirst) {
             nkeys = d.nkeys;
@@ -438,120 +456,110 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
             lim_max = pre ? nkeys : min(nkeys, d.lim0 + d.ntok - 1);
             idle = row0 >= rows;
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                const int r = row0 + h * 8 + g;
+                lim[h] = r >= rows ? 0 : (pre ? nkeys : min(nkeys, d.lim0 + r / a.G));
+                m[h] = -INFINITY;
+                l[h] = 0.f;
+            }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row0 + mt * 16 + h * 8 + g;
-                    lim[mt][h] = r >= rows ? 0 : (pre ? nkeys : min(nkeys, d.lim0 + r / a.G));
-                    m[mt][h] = -INFINITY;
-                    l[mt][h] = 0.f;
-                }
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.f;
+            for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             if (!mbar_wait_w(&sh.q_full[n_item & 1], (n_item >> 1) & 1, wc, kPfQFull)) return false;
             q_base = sQ + (n_item & 1) * (32u * D * 2u);
             if constexpr (kKeepQ) {
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int ks = 0; ks < kKSteps; ++ks) q_frag(qf[mt][ks], ks, mt);
+                for (int ks = 0; ks < kKSteps; ++ks) q_frag(qf[ks], ks);
                 arrive(&sh.q_empty8[n_item & 1]);
             }
         }
         const uint32_t ik = 2 * n, iv = 2 * n + 1, slot_k = ik % kRing, slot_v = iv % kRing;
-        const bool work = page && !idle && k0 < lim_max;
-        uint32_t p[kMT][4];
+        const bool work = live && !idle && k0 < lim_max;
+        uint32_t p[kKT][4];
         if (!mbar_wait_w(&sh.full[slot_k], (ik / kRing) & 1, wc, kPfRingFull)) return false;
         if (work) {
-            float s[kMT][2][4];
+            float s[2 * kKT][4];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) s[mt][i][0] = s[mt][i][1] = s[mt][i][2] = s[mt][i][3] = 0.f;
+            for (int i = 0; i < 2 * kKT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
             const uint32_t base = sRing + slot_k * G::kTile + k_row;
 #pragma unroll
             for (int ks = 0; ks < kKSteps; ++ks) {
-                uint32_t b[4];
-                ldsm4(b, base + (ks >> 2) * G::kKVBox + (((((ks & 3) << 1) + (mi & 1)) ^ mr) << 4));
+                uint32_t f[4];
+                if constexpr (!kKeepQ) q_frag(f, ks);
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                    uint32_t f[4];
-                    if constexpr (!kKeepQ) q_frag(f, ks, mt);
-                    mma16816(s[mt][0], kKeepQ ? qf[kKeepQ ? mt : 0][kKeepQ ? ks : 0] : f, b[0], b[1]);
-                    mma16816(s[mt][1], kKeepQ ? qf[kKeepQ ? mt : 0][kKeepQ ? ks : 0] : f, b[2], b[3]);
+                for (int kt = 0; kt < kKT; ++kt) {
+                    uint32_t b[4];
+                    ldsm4(b, base + kt * 2048u + (ks >> 2) * G::kKVBox + (((((ks & 3) << 1) + (mi & 1)) ^ mr) << 4));
+                    mma16816(s[2 * kt], kKeepQ ? qf[kKeepQ ? ks : 0] : f, b[0], b[1]);
+                    mma16816(s[2 * kt + 1], kKeepQ ? qf[kKeepQ ? ks : 0] : f, b[2], b[3]);
                 }
             }
-            if (k0 + 16 > lim_min) {
+            if (k0 + kKeys > lim_min || live != (1 << kKT) - 1) {
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
+                for (int i = 0; i < 2 * kKT; ++i)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (k0 + i * 8 + t2 + (e & 1) >= lim[mt][e >> 1]) s[mt][i][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e)
+                        if (!((live >> (i >> 1)) & 1) || k0 + i * 8 + t2 + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
             }
+            float mn[2];
+            bool jump = false;
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-                float fac[2], use[2];
-                bool jump = false;
-                float mn[2];
+            for (int h = 0; h < 2; ++h) {
+                float x = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+                for (int i = 1; i < 2 * kKT; ++i) x = fmax3(x, s[i][2 * h], s[i][2 * h + 1]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                mn[h] = fmaxf(m[h], x * scale);
+                // Rows without a query (lim 0) never jump.
+                jump |= lim[h] > 0 && ((m[h] == -INFINITY) ? (mn[h] != -INFINITY) : (mn[h] - m[h] > kTau));
+            }
+            if (__any_sync(0xffffffffu, jump)) {
+                float fac[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float x = fmaxf(fmaxf(s[mt][0][2 * h], s[mt][0][2 * h + 1]), fmaxf(s[mt][1][2 * h], s[mt][1][2 * h + 1]));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    mn[h] = fmaxf(m[mt][h], x * scale);
-                    // Rows without a query (lim 0) never jump.
-                    jump |= lim[mt][h] > 0 && ((m[mt][h] == -INFINITY) ? (mn[h] != -INFINITY) : (mn[h] - m[mt][h] > kTau));
-                }
-                if (__any_sync(0xffffffffu, jump)) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        fac[h] = m[mt][h] == -INFINITY ? 0.f : ex2_mufu(m[mt][h] - mn[h]);
-                        l[mt][h] *= fac[h];
-                        m[mt][h] = mn[h];
-                    }
-#pragma unroll
-                    for (int i = 0; i < kNT; ++i) {
-                        o[mt][i][0] *= fac[0];
-                        o[mt][i][1] *= fac[0];
-                        o[mt][i][2] *= fac[1];
-                        o[mt][i][3] *= fac[1];
-                    }
+                    fac[h] = m[h] == -INFINITY ? 0.f : ex2_mufu(m[h] - mn[h]);
+                    l[h] *= fac[h];
+                    m[h] = mn[h];
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) use[h] = m[mt][h] == -INFINITY ? 0.f : m[mt][h];
+                for (int i = 0; i < kNT; ++i) {
+                    o[i][0] *= fac[0];
+                    o[i][1] *= fac[0];
+                    o[i][2] *= fac[1];
+                    o[i][3] *= fac[1];
+                }
+            }
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+            for (int h = 0; h < 2; ++h) {
+                const float use = m[h] == -INFINITY ? 0.f : m[h];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float p0 = ex2_mufu(fmaf(s[mt][i][2 * h], scale, -use[h]));
-                        const float p1 = ex2_mufu(fmaf(s[mt][i][2 * h + 1], scale, -use[h]));
-                        l[mt][h] += p0 + p1;
-                        p[mt][2 * i + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
-                    }
+                for (int i = 0; i < 2 * kKT; ++i) {
+                    const float p0 = ex2_mufu(fmaf(s[i][2 * h], scale, -use)), p1 = ex2_mufu(fmaf(s[i][2 * h + 1], scale, -use));
+                    l[h] += p0 + p1;
+                    p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
+                }
             }
         }
         arrive(&sh.empty8[slot_k]);
         if (!mbar_wait_w(&sh.full[slot_v], (iv / kRing) & 1, wc, kPfRingFull)) return false;
         if (work) {
             const uint32_t base = sRing + slot_v * G::kTile + v_row;
-            // Keys behind the list's end: whatever their rows hold, they count as 0.
+            // Keys behind the list's end and of absent pages count as 0, whatever
+            // their rows hold.
             auto half = [&](int key) {
                 return (key < nkeys ? 0xffffu : 0u) | (key + 1 < nkeys ? 0xffff0000u : 0u);
             };
-            const bool tail = k0 + 16 > nkeys;
-            const uint32_t w0 = tail ? half(k0 + t2) : ~0u, w1 = tail ? half(k0 + 8 + t2) : ~0u;
+            const bool whole = k0 + kKeys <= nkeys && live == (1 << kKT) - 1;
 #pragma unroll
-            for (int i = 0; i < kNT; i += 2) {
-                uint32_t b[4];
-                ldsm4t(b, base + (i >> 3) * G::kKVBox + ((((i & 7) + (mi >> 1)) ^ mr) << 4));
+            for (int kt = 0; kt < kKT; ++kt) {
+                const bool here = (live >> kt) & 1;
+                const uint32_t w0 = whole ? ~0u : here ? half(k0 + 16 * kt + t2) : 0u, w1 = whole ? ~0u : here ? half(k0 + 16 * kt + 8 + t2) : 0u;
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                    mma16816(o[mt][i], p[mt], b[0] & w0, b[1] & w1);
-                    mma16816(o[mt][i + 1], p[mt], b[2] & w0, b[3] & w1);
+                for (int i = 0; i < kNT; i += 2) {
+                    uint32_t b[4];
+                    ldsm4t(b, base + kt * 2048u + (i >> 3) * G::kKVBox + ((((i & 7) + (mi >> 1)) ^ mr) << 4));
+                    mma16816(o[i], p[kt], b[0] & w0, b[1] & w1);
+                    mma16816(o[i + 1], p[kt], b[2] & w0, b[3] & w1);
                 }
             }
         }
@@ -565,32 +573,28 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
         // keep the eight rows of a store in different banks.
         const int rp = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
         int C = D;
-        while (kOwners * rp * (C + 8) > G::kMergeFloats) C >>= 1;
+        while (kKeyGroups * rp * (C + 8) > G::kMergeFloats) C >>= 1;
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 1);
-                l[mt][h] += __shfl_xor_sync(0xffffffffu, l[mt][h], 2);
-            }
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
         const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s);
         float* out = (pre ? a.o_p : a.o_s) + at * D;
         for (int c0 = 0; c0 < D; c0 += C, ++n_merge) {
             if (!mbar_wait_w(&sh.m_free, (n_merge & 1) ^ 1, wc, kPfMerge)) return false;
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int h = 0; h < 2; ++h) {
+                const int r = row0 + h * 8 + g;
+                if (r < rows) {
+                    if (t2 == 0) sh.ml[kg][r] = make_float2(m[h], l[h]);
+                    float* to = merge + (kg * rp + r) * (C + 8) - c0 + t2;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = row0 + mt * 16 + h * 8 + g;
-                    if (r < rows) {
-                        if (t2 == 0) sh.ml[kg][r] = make_float2(m[mt][h], l[mt][h]);
-                        float* to = merge + (kg * rp + r) * (C + 8) - c0 + t2;
-#pragma unroll
-                        for (int i = 0; i < kNT; ++i)
-                            if (i * 8 >= c0 && i * 8 < c0 + C)
-                                *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[mt][i][2 * h], o[mt][i][2 * h + 1]);
-                    }
+                    for (int i = 0; i < kNT; ++i)
+                        if (i * 8 >= c0 && i * 8 < c0 + C)
+                            *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
                 }
+            }
             arrive(&sh.m_full);
             if (!mbar_wait_w(&sh.m_full, n_merge & 1, wc, kPfMerge)) return false;
             const int quads = C / 4;
@@ -598,10 +602,10 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
                 const int r = i / quads, c = (i - r * quads) * 4;
                 float M = -INFINITY, L = 0.f;
 #pragma unroll
-                for (int w = 0; w < kOwners; ++w) M = fmaxf(M, sh.ml[w][r].x);
+                for (int w = 0; w < kKeyGroups; ++w) M = fmaxf(M, sh.ml[w][r].x);
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kOwners; ++w) {
+                for (int w = 0; w < kKeyGroups; ++w) {
                     const float2 ml = sh.ml[w][r];
                     const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M);
                     const float4 x = *reinterpret_cast<const float4*>(merge + (w * rp + r) * (C + 8) + c);
@@ -627,7 +631,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PfArgs a) {
     using G = Pf<D>;
     constexpr int kN = G::kN, kStreams = G::kStreams, kRing = G::kRing, kBoxes = G::kBoxes;
-    constexpr int kSoftWarps = 8, kThreads = G::kThreads;
+    constexpr int kSoftWarps = 8;
     extern __shared__ uint8_t dsmem[];
     __shared__ PfShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -635,30 +639,21 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     uint8_t* gbase = dsmem + (base - smem_u32(dsmem));
     const uint32_t sQ = base, sRing = base + G::kStreams * G::kQTile;
     PfTables t;
-    t.pref = reinterpret_cast<long long*>(gbase + G::kTiles);
+    t.pref = reinterpret_cast<int*>(gbase + G::kTiles);
     t.items = reinterpret_cast<int*>(t.pref + a.B + 1);
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
 
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_ready[i], 4);
-            mbar_init(&sh.pv_done[i], 1);
-            mbar_init(&sh.o_done[i], 1);
-            for (int k = 0; k < kDesc; ++k) { mbar_init(&sh.d_full[i][k], 1); mbar_init(&sh.d_empty[i][k], 1); }
+    {   // One barrier a thread, in the order of PfShared.
+        constexpr int n1 = (offsetof(PfShared, p_ready) - offsetof(PfShared, d_full)) / 8;
+        constexpr int n4 = (offsetof(PfShared, empty8) - offsetof(PfShared, p_ready)) / 8;
+        constexpr int n8 = (offsetof(PfShared, ml) - offsetof(PfShared, empty8)) / 8;
+        static_assert(n1 + n4 + n8 <= G::kThreads, "one barrier a thread");
+        if (tid < n1 + n4 + n8) {
+            mbar_init(&sh.d_full[0][0] + tid, tid < n1 ? 1 : tid < n1 + n4 ? 4 : 8);
+            fence_mbar_init();
         }
-        for (int i = 0; i < kQMax; ++i) { mbar_init(&sh.q_full[i], 1); mbar_init(&sh.q_empty[i], 1); }
-        for (int i = 0; i < kRing; ++i) { mbar_init(&sh.full[i], 1); mbar_init(&sh.empty[i], 1); }
-        mbar_init(&sh.drain, 1);
-        for (int i = 0; i < 8; ++i) mbar_init(&sh.empty8[i], 8);
-        for (int i = 0; i < kDesc; ++i) mbar_init(&sh.d_empty8[i], 8);
-        mbar_init(&sh.q_empty8[0], 8);
-        mbar_init(&sh.q_empty8[1], 8);
-        mbar_init(&sh.m_full, 8);
-        mbar_init(&sh.m_free, 8);
-        sh.abort_flag = 0;
-        fence_mbar_init();
+        if (tid == 0) sh.abort_flag = 0;
     }
     if (warp == kSoftWarps && lane == 0) {
         tma_prefetch_desc(&tq_p);
@@ -666,11 +661,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
-    if (warp == 0) {
+    if (warp == kSoftWarps + 3) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
     }
-    build_tables<D>(a, t, sh, tid, kThreads);
+    const PfHeader hdr = build_tables<D>(a, t, sh, tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -679,7 +674,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     const uint32_t tmem = sh.tmem_base;
     // Parts of a tile: whole pages, or one part where a page is larger.
     const int part_log2 = min(a.ps_log2, kN == 64 ? 6 : 7), parts = kN >> part_log2;
-    const bool pre = (int)blockIdx.x < sh.hdr.n_p;
+    const bool pre = (int)blockIdx.x < hdr.n_p;
     const int mode = pre ? a.mode_p : a.mode_s;
     const bool two = kStreams == 2 && mode == kTwo, few = mode == kFew;
     const int workers = two || few ? 1 : kStreams;
@@ -696,7 +691,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     auto desc_wait = [&](int x, uint32_t n) { return mbar_wait_w(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
 
     if (warp >= kSoftWarps) {
-        regs_dec<72>();
+        regs_dec<88>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------------------ loader
             // The issuer's order: every worker's first K (kLook of them), then by
@@ -913,7 +908,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // (the next item's, past an item's end) run while these are handed on.
             const int x = warp - (kSoftWarps + 2), q = lane >> 3, part = lane & 7;
             Walk<D> walk;
-            walk.start(a, t, sh.hdr, x);
+            walk.start(a, t, hdr, x);
             Item it, ahead;
             auto pages = [&](const Item& i, int j) {
                 const int tile = j + q, key = tile * kN + (part << part_log2);
@@ -951,7 +946,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         d.tok0 = it.tok0;
                         d.ntok = it.ntok;
                         d.seg = it.seg;
-                        d.pre = it.pre;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.d_full[x][n % kDesc]);
@@ -965,14 +959,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             __syncwarp();
         }
     } else if (few) {
-        regs_inc<216>();
+        regs_inc<208>();
         float* merge = reinterpret_cast<float*>(gbase + G::kFewQ);
-        if (D == 256 || (pre ? a.qstep_p : a.qstep_s) <= 16)
+        if (D == 256 || qstep <= 16)
             few_rows<D, 1>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
         else if constexpr (D != 256)
             few_rows<D, 2>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
     } else {
-        regs_inc<216>();
+        regs_inc<208>();
         // ------------------------------------------------------------- softmax
         const int wg = warp >> 2, x = two ? 0 : wg;           // worker
         const int r = (warp & 3) * 32 + lane;                 // row of the tile == TMEM lane
@@ -1124,7 +1118,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, 512);
+    if (warp == kSoftWarps + 3) tmem_dealloc(tmem, 512);
 }
 
 // ---------------------------------------------------------------------- join
@@ -1157,8 +1151,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     long long seg_p = 0, seg_s = 0, row_p = 0, row_s = 0;
     if (a.prefix_len > 0) {
         const int blk = t / a.tb, item = hk * a.blocks_p + blk;
-        const long long u0 = (long long)item * a.tiles_p;
-        const int ca = (int)(u0 / h.per_p), cb = (int)((u0 + a.tiles_p - 1) / h.per_p);
+        const int u0 = item * a.tiles_p, ca = u0 / h.per_p, cb = (u0 + a.tiles_p - 1) / h.per_p;
         np = cb - ca + 1;
         seg_p = item + ca;
         row_p = (t - blk * a.tb) * a.G + gi;
@@ -1167,8 +1160,8 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     const int ntok = min(a.tb, n - rb * a.tb), seen = s - n + rb * a.tb + ntok;   // of the block's last row
     if (seen > 0 && s > 0) {
         const int item = hk * nb + index_of(rb, nb);
-        const long long u0 = a.ws.pref[b] + (long long)item * (cdiv(s, kN) + kOverheadUnits);
-        const int ca = (int)(u0 / h.per_s), cb = (int)((u0 + cdiv(seen, kN) - 1) / h.per_s);
+        const int u0 = a.ws.pref[b] + item * (cdiv(s, kN) + kOverheadUnits);
+        const int ca = u0 / h.per_s, cb = (u0 + cdiv(seen, kN) - 1) / h.per_s;
         ns = cb - ca + 1;
         seg_s = a.ws.items[b] + item + ca;
         row_s = (i - rb * a.tb) * a.G + gi;
@@ -1251,7 +1244,7 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
     const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + 2 * sms;
     const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + 2 * sms;
     w.pref = align256(sizeof(PfHeader));
-    w.items = align256(w.pref + (size_t)(B + 1) * 8);
+    w.items = align256(w.pref + (size_t)(B + 1) * 4);
     w.cu = align256(w.items + (size_t)(B + 1) * 4);
     w.len = align256(w.cu + (size_t)(B + 1) * 4);
     w.ml_p = align256(w.len + (size_t)B * 4);
@@ -1266,8 +1259,8 @@ template <int D>
 int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtensorMap& tk, const CUtensorMap& tv, const PfArgs& a,
                   int sms, cudaStream_t stream) {
     using G = Pf<D>;
-    const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 16 + a.B * 4;
-    static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 16 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
+    const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4;
+    static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
     auto kern = prefix_kernel<D>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
     kern<<<sms, G::kThreads, smem, stream>>>(tq_p, tq_s, tk, tv, a);
@@ -1324,6 +1317,10 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
 
     const int kN = d == 256 ? 64 : 128;
+    // The list of tiles, at its longest, stays within 32 bits.
+    const long long tiles_s = ((long long)table_width * page_size + kN - 1) / kN + kOverheadUnits, tiles_p = ((long long)prefix_len + kN - 1) / kN;
+    const long long blocks_s = (long long)Hkv * (T / w.tb + (T < B ? T : B)), blocks_p = (long long)Hkv * ((T + w.tb - 1) / w.tb);
+    if (blocks_s * tiles_s > lim - (1 << 20) || blocks_p * tiles_p > lim - (1 << 20)) return FA_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PfArgs a;
     a.table = block_table;
@@ -1332,7 +1329,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.prefix_table = prefix_table;
     a.status = status;
     a.hdr = reinterpret_cast<PfHeader*>(ws);
-    a.ws.pref = reinterpret_cast<long long*>(ws + w.pref);
+    a.ws.pref = reinterpret_cast<int*>(ws + w.pref);
     a.ws.items = reinterpret_cast<int*>(ws + w.items);
     a.ws.cu = reinterpret_cast<int*>(ws + w.cu);
     a.ws.len = reinterpret_cast<int*>(ws + w.len);
