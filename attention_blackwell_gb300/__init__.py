@@ -7,7 +7,6 @@ other implementation: if ``lib/libfa.so`` is missing, every call raises.
 
 Build the library with ``python -m attention_blackwell_gb300.build``.
 """
-import contextlib
 import ctypes
 import os
 
@@ -253,50 +252,82 @@ def bwd(q, k, v, o, lse, do, causal=False, alpha=None, cu_seqlens=None, max_seql
     return dq, dk, dv
 
 
-@contextlib.contextmanager
-def _on(stream, tensors):
+# A serving step is a few short kernels, so what a call costs on the host counts:
+# checks are single expressions that hand over to _need for the message, and
+# pointers and the stream go to ctypes as plain integers.
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _current_raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    _current_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _dense(t, name, dtype):
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, name, dtype)
+
+
+class _On:
     """Device and stream of a serving call: its tensors' device, the given
     stream or that device's current one, and on it whatever the call
     allocates.  Tensors that the caching allocator holds for another stream
     are marked as used on this one."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one device")
-    if stream is None and dev.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream()
-        return
-    with torch.cuda.device(dev):
-        s = stream if stream is not None else torch.cuda.current_stream()
-        if s.device != dev:
-            raise ValueError("the stream must be on the tensors' device")
-        if s == torch.cuda.current_stream():
-            yield s
-            return
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].get_device()
         for t in tensors:
-            if t is not None:
-                t.record_stream(s)
-        with torch.cuda.stream(s):
-            yield s
+            if t is not None and t.get_device() != dev:
+                raise ValueError("all tensors must be on one device")
+        self.guards = ()
+        if stream is None and dev == _current_device():
+            self.raw = _current_raw_stream(dev)
+            return
+        guards = [torch.cuda.device(dev)]
+        if stream is not None:
+            if stream.device.index != dev:
+                raise ValueError("the stream must be on the tensors' device")
+            if stream != torch.cuda.current_stream(dev):
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+                guards.append(torch.cuda.stream(stream))
+        self.guards = guards
+        self.raw = stream.cuda_stream if stream is not None else _current_raw_stream(dev)
+
+    def __enter__(self):
+        for g in self.guards:
+            g.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
 
 
-def _rows(t, name, dim):
-    """A bf16 tensor whose last dim - 1 axes are dense; its first may have a
-    stride of its own (rows cut from a wider projection)."""
+def _rows(t, name):
+    """Elements between the tokens of a bf16 [T, H, d] tensor that is dense
+    within a token (rows may be cut from a wider projection)."""
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != dim:
-        raise ValueError("%s must have %d dimensions" % (name, dim))
-    if t.shape[-1] > 1 and t.stride(-1) != 1 or t.shape[-2] > 1 and t.stride(-2) != t.shape[-1]:
+    if t.dim() != 3:
+        raise ValueError("%s must have 3 dimensions" % name)
+    T, H, d = t.shape
+    st, sh, sd = t.stride()
+    if d > 1 and sd != 1 or H > 1 and sh != d:
         raise ValueError("%s must be contiguous within a token" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[-1] * t.shape[-2]
+    return st if T > 1 else H * d
 
 
 def _pages(k_pages, v_pages):
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _need(t, n, torch.bfloat16)
+    _dense(k_pages, "k_pages", torch.bfloat16)
+    _dense(v_pages, "v_pages", torch.bfloat16)
     if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d]")
     return k_pages.shape
@@ -321,9 +352,12 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
     slots int32 [num_slots] (-1: none), pool_out int64 [3], another tensor than
     pool.  num_slots is needed when slots is not given.
     """
-    for t, n, dt in ((ctx_lens, "ctx_lens", torch.int32), (new_lens, "new_lens", torch.int32),
-                     (block_table, "block_table", torch.int32), (ring, "ring", torch.int32), (pool, "pool", torch.int64)):
-        _need(t, n, dt)
+    i32 = torch.int32
+    _dense(ctx_lens, "ctx_lens", i32)
+    _dense(new_lens, "new_lens", i32)
+    _dense(block_table, "block_table", i32)
+    _dense(ring, "ring", i32)
+    _dense(pool, "pool", torch.int64)
     B = ctx_lens.numel()
     if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("ctx_lens, new_lens and block_table must have one entry or row a request")
@@ -331,24 +365,25 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
         raise ValueError("pool must have 3 elements")
     if slots is None and num_slots is None:
         raise ValueError("page_plan needs num_slots or slots")
-    with _on(stream, (ctx_lens, new_lens, block_table, ring, pool, cu_new, kv_lens, slots, pool_out)) as s:
+    with _On(stream, ctx_lens, new_lens, block_table, ring, pool, cu_new, kv_lens, slots, pool_out) as raw:
         dev = ctx_lens.device
         if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=torch.int32, device=dev)
+            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
         if kv_lens is None:
-            kv_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            kv_lens = torch.empty(B, dtype=i32, device=dev)
         if slots is None:
-            slots = torch.empty(num_slots, dtype=torch.int32, device=dev)
+            slots = torch.empty(num_slots, dtype=i32, device=dev)
         if pool_out is None:
             pool_out = torch.empty(3, dtype=torch.int64, device=dev)
-        for t, n, dt, size in ((cu_new, "cu_new", torch.int32, B + 1), (kv_lens, "kv_lens", torch.int32, B),
-                               (slots, "slots", torch.int32, slots.numel()), (pool_out, "pool_out", torch.int64, 3)):
-            _need(t, n, dt)
-            if t.numel() != size:
-                raise ValueError("%s must have %d elements" % (n, size))
-        rc = lib().fa_page_plan(_ptr(ctx_lens), _ptr(new_lens), B, int(page_size), _ptr(block_table),
-                                block_table.shape[1], _ptr(ring), ring.numel(), _ptr(pool), _ptr(pool_out),
-                                _ptr(cu_new), _ptr(kv_lens), _ptr(slots), slots.numel(), _stream(s))
+        _dense(cu_new, "cu_new", i32)
+        _dense(kv_lens, "kv_lens", i32)
+        _dense(slots, "slots", i32)
+        _dense(pool_out, "pool_out", torch.int64)
+        if cu_new.numel() != B + 1 or kv_lens.numel() != B or pool_out.numel() != 3:
+            raise ValueError("cu_new, kv_lens and pool_out must have B + 1, B and 3 elements")
+        rc = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), block_table.data_ptr(),
+                                block_table.shape[1], ring.data_ptr(), ring.numel(), pool.data_ptr(), pool_out.data_ptr(),
+                                cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), slots.numel(), raw)
     _check(rc, "fa_page_plan")
     return cu_new, kv_lens, slots, pool_out
 
@@ -357,18 +392,18 @@ def kv_store(k, v, slots, k_pages, v_pages, stream=None):
     """Write rows of k and v ([T, Hkv, d] bf16, tokens may be strided) into the
     cache at slots (int32 [T]; negative: skipped).  Returns (k_pages, v_pages)."""
     P, Hkv, page, d = _pages(k_pages, v_pages)
-    ks, vs = _rows(k, "k", 3), _rows(v, "v", 3)
-    _need(slots, "slots", torch.int32)
+    ks, vs = _rows(k, "k"), _rows(v, "v")
+    _dense(slots, "slots", torch.int32)
     T = k.shape[0]
-    if tuple(k.shape) != (T, Hkv, d) or k.shape != v.shape:
+    if k.shape != (T, Hkv, d) or k.shape != v.shape:
         raise ValueError("k and v must be [T, Hkv, d] with the pages' Hkv and d")
     if slots.numel() != T:
         raise ValueError("slots must have one element a token")
     if T == 0:
         return k_pages, v_pages
-    with _on(stream, (k, v, slots, k_pages, v_pages)) as s:
-        rc = lib().fa_kv_store(_ptr(k), _ptr(v), ks, vs, _ptr(slots), T, Hkv, d, _ptr(k_pages), _ptr(v_pages), P, page,
-                               _stream(s))
+    with _On(stream, k, v, slots, k_pages, v_pages) as raw:
+        rc = lib().fa_kv_store(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
+                               v_pages.data_ptr(), P, page, raw)
     _check(rc, "fa_kv_store")
     return k_pages, v_pages
 
@@ -396,17 +431,17 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     request has one row; with it max_seqlen bounds a request's rows.
     """
     P, Hkv, page, d = _pages(k_pages, v_pages)
-    qs = _rows(q, "q", 3)
-    for t, n in ((block_table, "block_table"), (kv_lens, "kv_lens")):
-        _need(t, n, torch.int32)
-    T, Hq = q.shape[0], q.shape[1]
+    qs = _rows(q, "q")
+    _dense(block_table, "block_table", torch.int32)
+    _dense(kv_lens, "kv_lens", torch.int32)
+    T, Hq, dq = q.shape
     B = kv_lens.numel()
-    if q.shape[2] != d:
+    if dq != d:
         raise ValueError("q and the pages must have one head dim")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, W] with kv_lens' B")
     if cu_seqlens is not None:
-        _need(cu_seqlens, "cu_seqlens", torch.int32)
+        _dense(cu_seqlens, "cu_seqlens", torch.int32)
         if cu_seqlens.numel() != B + 1:
             raise ValueError("cu_seqlens must have B + 1 elements")
         if max_seqlen is None:
@@ -419,30 +454,31 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     if prefix_len > 0:
         if prefix_table is None:
             raise ValueError("prefix_len needs prefix_table")
-        _need(prefix_table, "prefix_table", torch.int32)
+        _dense(prefix_table, "prefix_table", torch.int32)
         if prefix_table.numel() * page < prefix_len:
             raise ValueError("prefix_table is too short for prefix_len")
     else:
         prefix_table = None
     if alpha is None:
         alpha = 1.0 / (d ** 0.5)
-    with _on(stream, (q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, prefix_table, out, lse, workspace)) as s:
+    with _On(stream, q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, prefix_table, out, lse, workspace) as raw:
         if out is None:
             out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
         if lse is None:
             lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        _need(out, "out", torch.bfloat16)
-        _need(lse, "lse", torch.float32)
-        if tuple(out.shape) != (T, Hq, d) or tuple(lse.shape) != (Hq, T):
+        _dense(out, "out", torch.bfloat16)
+        _dense(lse, "lse", torch.float32)
+        if out.shape != (T, Hq, d) or lse.shape != (Hq, T):
             raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
         if T == 0:
             return out, lse
         if workspace is None:
             workspace = prefix_workspace(B, Hq, Hkv, T, max_seqlen, d, device=q.device)
-        rc = lib().fa_prefix_fwd(_ptr(q), qs, _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), T, B, Hq, Hkv, d,
-                                 float(alpha), P, page, _ptr(block_table), block_table.shape[1], _ptr(kv_lens),
-                                 _ptr(cu_seqlens), int(max_seqlen), _ptr(prefix_table), prefix_len, _ptr(workspace),
-                                 workspace.numel(), _stream(s))
+        rc = lib().fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                 T, B, Hq, Hkv, d, float(alpha), P, page, block_table.data_ptr(), block_table.shape[1],
+                                 kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
+                                 int(max_seqlen), prefix_table.data_ptr() if prefix_table is not None else None,
+                                 prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
     _check(rc, "fa_prefix_fwd")
     return out, lse
 
