@@ -51,7 +51,10 @@ namespace fa {
 namespace {
 
 constexpr float kTau = 8.0f;        // rescale threshold (log2 units), as in the forward kernels
-constexpr int kOverheadUnits = 1;   // an item of a request counts its tiles and this (its Q load and epilogue)
+// An item of a request counts its tiles and this many more: its Q, its epilogue
+// and the pipeline's refill cost about two tiles in every shape (2800 cycles
+// with few rows, 5000 with one row tile at d = 256, 7000 with two).
+constexpr int kOverheadUnits = 2;
 
 template <int D> struct Pf {
     static constexpr int kStreams = D == 256 ? 1 : 2;
@@ -69,6 +72,13 @@ template <int D> struct Pf {
     // the row tiles of Q.
     static constexpr uint32_t kFewQ = 2 * 32 * D * 2;
     static constexpr int kMergeFloats = (kStreams * kQTile - kFewQ) / 4;
+    // Cycles a CTA takes for a tile, by mode (kFew, kOne, kTwo), measured in the
+    // kernel on GB300: how the CTAs are divided between the prefix and the
+    // requests' own keys.
+    __host__ __device__ static constexpr int cost(int mode) {
+        return D == 64 ? (mode == 0 ? 1100 : mode == 1 ? 2000 : 3400) : D == 128 ? (mode == 0 ? 1400 : mode == 1 ? 3200 : 3700)
+                                                                       : (mode == 0 ? 3200 : 2700);
+    }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
 
@@ -78,13 +88,15 @@ struct PfTables {
     int* items;          // [B+1] items of requests before b
     int* cu;             // [B+1] sanitised offsets
     int* len;            // [B] own keys
+    int* owner;          // [T] request of each row, -1: none (workspace only)
 };
 
 struct PfHeader {
     int per_p, per_s;         // units a worker: of the prefix, of the requests
     int n_p;                  // CTAs on the prefix; the rest are on the requests
+    int chunk, chunks;        // prefix: tiles an item (the last chunk's may have fewer), items a row block
     int bad;                  // a request has more rows than max_seqlen
-    int pad[12];
+    int pad[10];
 };
 
 struct PfArgs {
@@ -150,13 +162,15 @@ template <int D>
 struct Walk {
     static constexpr int kN = Pf<D>::kN;
     int u, end;
-    int b, hk, k, worker;
+    int b, hk, k, worker, chunk, chunks;
     bool pre;
 
     // Worker `x` of this CTA.
     __device__ __forceinline__ void start(const PfArgs& a, const PfTables& t, const PfHeader& h, int x) {
         const int c = blockIdx.x;
         b = hk = k = 0;
+        chunk = h.chunk;
+        chunks = h.chunks;
         pre = c < h.n_p;
         const int width = (pre ? a.mode_p : a.mode_s) == kOne ? Pf<D>::kStreams : 1;
         worker = (pre ? c : c - h.n_p) * width + x;
@@ -184,12 +198,19 @@ struct Walk {
     __device__ __forceinline__ bool next(const PfArgs& a, const PfTables& t, Item& it) {
         while (u < end) {
             if (pre) {
-                const int i = u / a.tiles_p;
-                it.j0 = u - i * a.tiles_p;
-                it.j1 = min(a.tiles_p, it.j0 + end - u);
+                // Key/value head, chunk of tiles, row block, tile: with chunks of
+                // a worker's share all workers are at the same offset within
+                // their chunks at a time, so the row blocks of a chunk read its
+                // pages together and L2 serves all but the first.
+                const int per_head = a.blocks_p * a.tiles_p;
+                it.hk = u / per_head;
+                const int r = u - it.hk * per_head, ch = r / (chunk * a.blocks_p);
+                const int r2 = r - ch * chunk * a.blocks_p, len = min(chunk, a.tiles_p - ch * chunk);
+                const int rb = r2 / len, off = r2 - rb * len, i = (it.hk * chunks + ch) * a.blocks_p + rb;
+                it.j0 = ch * chunk + off;
+                it.j1 = it.j0 + min(len - off, end - u);
                 u += it.j1 - it.j0;
-                it.hk = i / a.blocks_p;
-                it.tok0 = (i - it.hk * a.blocks_p) * a.tb;
+                it.tok0 = rb * a.tb;
                 it.ntok = min(a.tb, a.T - it.tok0);
                 it.nkeys = a.prefix_len;
                 it.lim0 = INT_MAX / 2;
@@ -295,7 +316,8 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
             it = nb * a.Hkv;
             u = per * it;
             // What the causal mask leaves of a row block's tiles, on average.
-            c = (float)u * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)));
+            c = ((float)(u - (u > 0 ? it * kOverheadUnits : 0)) * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)))) +
+                (u > 0 ? it * kOverheadUnits : 0);
         }
         const int u_own = u, it_own = it;
 #pragma unroll
@@ -337,14 +359,15 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     __syncthreads();
     PfHeader h;
     const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
-    // Two row tiles take twice the tensor time of one.
-    const float cp = (float)units_p * (a.mode_p == kTwo ? 2 : 1), cs = cost * (a.mode_s == kTwo ? 2 : 1);
+    const float cp = (float)units_p * Pf<D>::cost(a.mode_p), cs = cost * Pf<D>::cost(a.mode_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
     const int wp = np * (a.mode_p == kOne ? Pf<D>::kStreams : 1), ws = max(1, grid - np) * (a.mode_s == kOne ? Pf<D>::kStreams : 1);
     h.n_p = np;
     h.per_p = wp ? (units_p + wp - 1) / wp : 1;
     h.per_s = units ? (units + ws - 1) / ws : 1;
+    h.chunk = a.blocks_p > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
+    h.chunks = (a.tiles_p + h.chunk - 1) / h.chunk;
     h.bad = sh.bad;
     if (blockIdx.x == 0) {
         for (int i = tid; i <= a.B; i += kThreads) {
@@ -692,6 +715,21 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
     if (warp >= kSoftWarps) {
         regs_dec<88>();
+        if (warp == kSoftWarps + 3) {
+            // Which request each row belongs to, for the joining kernel.
+            for (int i = blockIdx.x * 32 + lane; i < a.T; i += gridDim.x * 32) {
+                int lo = -1;
+                if (i >= t.cu[0] && i < t.cu[a.B]) {
+                    lo = 0;
+                    for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
+                        const int mid = (lo + hi) >> 1;
+                        if (t.cu[mid] <= i) lo = mid; else hi = mid;
+                    }
+                }
+                a.ws.owner[i] = lo;
+            }
+            __syncwarp();
+        }
         if (warp == kSoftWarps) {
             // ------------------------------------------------------------ loader
             // The issuer's order: every worker's first K (kLook of them), then by
@@ -1123,104 +1161,147 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
 // ---------------------------------------------------------------------- join
 
-// kWarps warps a row: 1 where there are rows enough to fill the GPU, 8 (each
-// takes every eighth segment) where there are few rows of many segments.
-template <int D, int kWarps>
+// kHeads > 0: a warp takes that many heads of a row, whose loads overlap (many
+// rows); kHeads = 0: the eight warps of a block share one head's segments (few
+// rows, where a warp each would leave most SMs idle).
+template <int D, int kHeads>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
-    constexpr int kN = Pf<D>::kN, E = D / 32;
-    __shared__ float s_o[kWarps == 1 ? 1 : 8][kWarps == 1 ? 1 : D];
+    constexpr int kN = Pf<D>::kN, E = D / 32, H = kHeads ? kHeads : 1;
+    __shared__ float s_o[kHeads ? 1 : 8][kHeads ? 1 : D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = (a.Hq + H - 1) / H;
+    const long long w = kHeads ? blockIdx.x * 8LL + warp : blockIdx.x;
+    if (w >= (long long)a.T * groups) return;
+    const int t = (int)(w / groups), h0 = (int)(w - (long long)t * groups) * H;
     const PfHeader h = *a.hdr;
-    if (h.bad) return;
-    const long long w = kWarps == 1 ? blockIdx.x * 8LL + warp : blockIdx.x;
-    if (w >= (long long)a.T * a.Hq) return;
-    const int t = (int)(w / a.Hq), head = (int)(w - (long long)t * a.Hq), hk = head / a.G, gi = head - hk * a.G;
-    if (t < a.ws.cu[0] || t >= a.ws.cu[a.B]) return;
-    // The request that owns row t: two rounds of 32 candidates (B <= 1024).
-    int lo = 0, n_in = a.B;
-    while (n_in > 1) {
-        const int step = (n_in + 31) / 32, c = lo + lane * step;
-        const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n_in && a.ws.cu[c] <= t);
-        const int k = 31 - __clz(le);
-        lo += k * step;
-        n_in = min(step, n_in - k * step);
-    }
-    const int b = lo, c0 = a.ws.cu[b], n = a.ws.cu[b + 1] - c0, s = a.ws.len[b], i = t - c0;
-    // Segments: the prefix's first, then the request's, each in the list's order.
-    int np = 0, ns = 0;
-    long long seg_p = 0, seg_s = 0, row_p = 0, row_s = 0;
-    if (a.prefix_len > 0) {
-        const int blk = t / a.tb, item = hk * a.blocks_p + blk;
-        const int u0 = item * a.tiles_p, ca = u0 / h.per_p, cb = (u0 + a.tiles_p - 1) / h.per_p;
-        np = cb - ca + 1;
-        seg_p = item + ca;
-        row_p = (t - blk * a.tb) * a.G + gi;
-    }
-    const int nb = cdiv(n, a.tb), rb = i / a.tb;
-    const int ntok = min(a.tb, n - rb * a.tb), seen = s - n + rb * a.tb + ntok;   // of the block's last row
-    if (seen > 0 && s > 0) {
-        const int item = hk * nb + index_of(rb, nb);
-        const int u0 = a.ws.pref[b] + item * (cdiv(s, kN) + kOverheadUnits);
-        const int ca = u0 / h.per_s, cb = (u0 + cdiv(seen, kN) - 1) / h.per_s;
-        ns = cb - ca + 1;
-        seg_s = a.ws.items[b] + item + ca;
-        row_s = (i - rb * a.tb) * a.G + gi;
-    }
-    const int all = np + ns;
-    auto place = [&](int k) { return k < np ? (seg_p + k) * a.rows_p + row_p : (seg_s + k - np) * a.rows_s + row_s; };
-    float M = -INFINITY;
-    for (int k = lane; k < all; k += 32) M = fmaxf(M, (k < np ? a.ml_p : a.ml_s)[place(k)].x);
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.f, acc[E];
+    const int b = a.ws.owner[t];
+    if (h.bad || b < 0) return;
+    const int c0 = a.ws.cu[b], n = a.ws.cu[b + 1] - c0, s = a.ws.len[b], pref = a.ws.pref[b], items = a.ws.items[b], i = t - c0;
+    const int nb = cdiv(n, a.tb), rb = i / a.tb, blk = t / a.tb;
+    const int seen = s > 0 ? s - n + min(n, (rb + 1) * a.tb) : 0;      // keys of the block's last row
+    const int own_tiles = seen > 0 ? cdiv(seen, kN) : 0, own_units = cdiv(s, kN) + kOverheadUnits;
+    // Most segments that an item of the prefix can have, and room for all chunks'.
+    const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = a.prefix_len > 0 ? most * h.chunks : 0;
+    // Row of head h0 + x in the k-th of its segments, the prefix's first, then
+    // the request's, each in the list's order; negative: there is none.
+    int own_seg[H], own_n[H], all = 0;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int x = 0; x < H; ++x) {
+        own_seg[x] = own_n[x] = 0;
+        if (own_tiles > 0 && h0 + x < a.Hq) {
+            const int item = (h0 + x) / a.G * nb + index_of(rb, nb), u0 = pref + item * own_units;
+            const int ca = u0 / h.per_s;
+            own_n[x] = (u0 + own_tiles - 1) / h.per_s - ca + 1;
+            own_seg[x] = items + item + ca;
+        }
+        all = max(all, h0 + x < a.Hq ? slots + own_n[x] : 0);
+    }
+    auto place = [&](int x, int k) -> long long {
+        const int head = h0 + x, hk = head / a.G, gi = head - hk * a.G;
+        if (head >= a.Hq) return -1;
+        if (k < slots) {
+            const int ch = k / most, j = k - ch * most, len = min(h.chunk, a.tiles_p - ch * h.chunk);
+            const int u0 = hk * a.blocks_p * a.tiles_p + ch * h.chunk * a.blocks_p + blk * len;
+            const int ca = u0 / h.per_p, cb = (u0 + len - 1) / h.per_p;
+            if (ca + j > cb) return -1;
+            const int seg = (hk * h.chunks + ch) * a.blocks_p + blk + ca + j;
+            return (long long)seg * a.rows_p + (t - blk * a.tb) * a.G + gi;
+        }
+        if (k - slots >= own_n[x]) return -1;
+        return (long long)(own_seg[x] + k - slots) * a.rows_s + (i - rb * a.tb) * a.G + gi;
+    };
+    float M[H], L[H], acc[H][E];
+#pragma unroll
+    for (int x = 0; x < H; ++x) {
+        M[x] = -INFINITY;
+        L[x] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[x][e] = 0.f;
+    }
+    for (int k0 = 0; k0 < all; k0 += 32)
+#pragma unroll
+        for (int x = 0; x < H; ++x) {
+            const int k = k0 + lane;
+            const long long at = k < all ? place(x, k) : -1;
+            if (at >= 0) M[x] = fmaxf(M[x], (k < slots ? a.ml_p : a.ml_s)[at].x);
+        }
+#pragma unroll
+    for (int x = 0; x < H; ++x)
+        for (int o = 16; o; o >>= 1) M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], o));
     for (int k0 = 0; k0 < all; k0 += 32) {
-        float f = 0.f;
-        if (k0 + lane < all) {
-            const float2 ml = (k0 + lane < np ? a.ml_p : a.ml_s)[place(k0 + lane)];
-            f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M);
-            L += f * ml.y;
+        float f[H];
+        long long at[H];
+#pragma unroll
+        for (int x = 0; x < H; ++x) {
+            const int k = k0 + lane;
+            at[x] = k < all ? place(x, k) : -1;
+            f[x] = 0.f;
+            if (at[x] >= 0) {
+                const float2 ml = (k < slots ? a.ml_p : a.ml_s)[at[x]];
+                f[x] = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M[x]);
+                L[x] += f[x] * ml.y;
+            }
         }
         const int cnt = min(32, all - k0);
-#pragma unroll 4
-        for (int k = kWarps == 1 ? 0 : warp; k < cnt; k += kWarps) {
-            const float fk = __shfl_sync(0xffffffffu, f, k);
-            const long long at = place(k0 + k) * D + lane * E;
-            const float* src = (k0 + k < np ? a.o_p : a.o_s) + at;
-            float v[E];
-            if constexpr (E == 2) {
-                const float2 x = *reinterpret_cast<const float2*>(src);
-                v[0] = x.x; v[1] = x.y;
-            } else {
+#pragma unroll 2
+        for (int k = kHeads ? 0 : warp; k < cnt; k += kHeads ? 1 : 8) {
+            float fk[H], v[H][E];
 #pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const float4 x = *reinterpret_cast<const float4*>(src + e);
-                    v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
+            for (int x = 0; x < H; ++x) {
+                fk[x] = __shfl_sync(0xffffffffu, f[x], k);
+                const long long row = __shfl_sync(0xffffffffu, at[x], k);
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[x][e] = 0.f;
+                if (row >= 0) {
+                    const float* src = (k0 + k < slots ? a.o_p : a.o_s) + row * D + lane * E;
+                    if constexpr (E == 2) {
+                        const float2 q = *reinterpret_cast<const float2*>(src);
+                        v[x][0] = q.x;
+                        v[x][1] = q.y;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; e += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(src + e);
+                            v[x][e] = q.x;
+                            v[x][e + 1] = q.y;
+                            v[x][e + 2] = q.z;
+                            v[x][e + 3] = q.w;
+                        }
+                    }
                 }
             }
+            // A segment in which the row saw no key has weight 0 and holds
+            // whatever its idle accumulator held.
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, v[e], acc[e]);
+            for (int x = 0; x < H; ++x)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[x][e] = fk[x] > 0.f ? fmaf(fk[x], v[x][e], acc[x][e]) : acc[x][e];
         }
     }
-    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if constexpr (kWarps > 1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
-        __syncthreads();
-        if (warp) return;
+    for (int x = 0; x < H; ++x) {
+        for (int o = 16; o; o >>= 1) L[x] += __shfl_xor_sync(0xffffffffu, L[x], o);
+        if constexpr (kHeads == 0) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            for (int x = 1; x < kWarps; ++x) acc[e] += s_o[x][lane * E + e];
+            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[x][e];
+            __syncthreads();
+            if (warp) return;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                for (int y = 1; y < 8; ++y) acc[x][e] += s_o[y][lane * E + e];
+        }
+        const int head = h0 + x;
+        if (head >= a.Hq) return;
+        const float inv = L[x] > 0.f ? 1.f / L[x] : 0.f;
+        uint32_t out[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[x][e] * inv, acc[x][e + 1] * inv);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + head) * D) + lane * (E / 2);
+        if constexpr (E == 2) *dst = out[0];
+        else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+        else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+        if (lane == 0) a.lse[(long long)head * a.T + t] = L[x] > 0.f ? (M[x] + __log2f(L[x])) * 0.69314718055994531f : -INFINITY;
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t out[E / 2];
-#pragma unroll
-    for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + w * D) + lane * (E / 2);
-    if constexpr (E == 2) *dst = out[0];
-    else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    if (lane == 0) a.lse[(long long)head * a.T + t] = L > 0.f ? (M + __log2f(L)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---------------------------------------------------------------------- host
@@ -1229,25 +1310,27 @@ bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintpt
 
 struct PfLayout {
     int tq, tb, rows_p, rows_s;
-    size_t pref, items, cu, len, o_p, ml_p, o_s, ml_s, total;
+    size_t pref, items, cu, len, owner, o_p, ml_p, o_s, ml_s, total;
 };
 
-// Workspace: header, tables, the segments' rows.  Prefix segments: one an item
-// and worker; the requests': sum of ceil(n_b / tb) <= T / tb + B items a
-// key/value head.
+// Workspace: header, tables, the segments' rows.  The prefix's items are row
+// blocks times chunks of a worker's share of tiles, so at most row blocks plus
+// workers; the requests' at most T / tb + min(T, B) a key/value head.  Segments:
+// items plus workers (two a CTA at most).
 PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms) {
     PfLayout w;
     w.tq = 128 / G;
     w.tb = d == 256 ? w.tq : 2 * w.tq;
     w.rows_p = (T < w.tb ? T : w.tb) * G;
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
-    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + 2 * sms;
+    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + 4 * sms;
     const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + 2 * sms;
     w.pref = align256(sizeof(PfHeader));
     w.items = align256(w.pref + (size_t)(B + 1) * 4);
     w.cu = align256(w.items + (size_t)(B + 1) * 4);
     w.len = align256(w.cu + (size_t)(B + 1) * 4);
-    w.ml_p = align256(w.len + (size_t)B * 4);
+    w.owner = align256(w.len + (size_t)B * 4);
+    w.ml_p = align256(w.owner + (size_t)T * 4);
     w.ml_s = align256(w.ml_p + seg_p * w.rows_p * 8);
     w.o_p = align256(w.ml_s + seg_s * w.rows_s * 8);
     w.o_s = align256(w.o_p + seg_p * w.rows_p * d * 4);
@@ -1265,9 +1348,11 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
     kern<<<sms, G::kThreads, smem, stream>>>(tq_p, tq_s, tk, tv, a);
     const long long rows = (long long)a.T * a.Hq;
-    // Few rows: a block each (512 rows: 64 blocks of 8 rows would leave most SMs idle).
-    if (rows <= 16LL * sms) prefix_join_kernel<D, 8><<<(int)rows, 256, 0, stream>>>(a);
-    else prefix_join_kernel<D, 1><<<(int)((rows + 7) / 8), 256, 0, stream>>>(a);
+    // Rows (of one head): up to 16 an SM a block each; up to some waves of warps
+    // a warp each; past that four heads a warp.
+    if (rows <= 16LL * sms) prefix_join_kernel<D, 0><<<(int)rows, 256, 0, stream>>>(a);
+    else if (rows <= 256LL * sms) prefix_join_kernel<D, 1><<<(int)((rows + 7) / 8), 256, 0, stream>>>(a);
+    else prefix_join_kernel<D, 4><<<(int)(((long long)a.T * ((a.Hq + 3) / 4) + 7) / 8), 256, 0, stream>>>(a);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -1333,6 +1418,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.ws.items = reinterpret_cast<int*>(ws + w.items);
     a.ws.cu = reinterpret_cast<int*>(ws + w.cu);
     a.ws.len = reinterpret_cast<int*>(ws + w.len);
+    a.ws.owner = reinterpret_cast<int*>(ws + w.owner);
     a.o_p = reinterpret_cast<float*>(ws + w.o_p);
     a.o_s = reinterpret_cast<float*>(ws + w.o_s);
     a.ml_p = reinterpret_cast<float2*>(ws + w.ml_p);
