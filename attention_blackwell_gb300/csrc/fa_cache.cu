@@ -66,6 +66,8 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(const PlanArgs a) {
     __shared__ Scan3 s_warp[32];
     __shared__ long long s_lost[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    grid_launch_next();
+    grid_wait();
     const int W = a.W, P = a.P, sh = a.ps_log2;
     const long long cap = (long long)W << sh, up = (1 << sh) - 1;
 
@@ -184,6 +186,8 @@ struct StoreArgs {
 // One 16-byte chunk of K and of V a thread and step; a token's row is read in
 // the order of memory.
 __global__ void __launch_bounds__(256) kv_store_kernel(const StoreArgs a) {
+    grid_launch_next();
+    grid_wait();
     const long long stride = (long long)gridDim.x * blockDim.x;
     for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < a.n; i += stride) {
         const long long t = i / a.chunks;
@@ -252,8 +256,7 @@ int fa_page_plan(const int* ctx_lens, const int* new_lens, int B, int page_size,
     const long long pages = ((long long)B * table_width + 32LL * threads - 1) / (32LL * threads);
     grid = grid > pages ? grid : pages;
     grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
-    page_plan_kernel<<<(int)grid, threads, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(page_plan_kernel, (int)grid, threads, 0, stream, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 int fa_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int* slots, int T, int Hkv,
@@ -286,8 +289,7 @@ int fa_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride
     a.num_slots = (long long)num_pages * page_size;
     long long grid = (a.n + 255) / 256;
     if (grid > 8LL * sms) grid = 8LL * sms;
-    kv_store_kernel<<<(int)grid, 256, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(kv_store_kernel, (int)grid, 256, 0, stream, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

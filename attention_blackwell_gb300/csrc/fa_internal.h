@@ -187,6 +187,25 @@ cudaError_t launch_fwd256(const FwdLaunch& L, cudaStream_t stream);
 int make_map_rows(CUtensorMap* map, const void* ptr, int d, int H, long long T, long long stride, int heads, int tokens);
 int make_map_pages(CUtensorMap* map, const void* ptr, int d, long long rows, int box_rows);
 
+// Launch on `stream` as a programmatic dependent of the kernel before it there:
+// the launch and whatever the kernel does before grid_wait() overlap that
+// kernel's end.  Every kernel launched so calls grid_wait() before it reads or
+// writes memory, so its effects are ordered as without it.
+template <typename... P, typename... A>
+inline cudaError_t launch_dependent(void (*kern)(P...), int grid, int block, size_t smem, cudaStream_t stream, A&&... args) {
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)grid);
+    c.blockDim = dim3((unsigned)block);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...);
+}
+
 // Upper bound on the SM count, for sizes asked for without a device.
 constexpr int kMaxSMs = 192;
 

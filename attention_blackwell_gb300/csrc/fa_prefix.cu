@@ -688,6 +688,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
     }
+    grid_launch_next();
+    grid_wait();
     const PfHeader hdr = build_tables<D>(a, t, sh, tid);
     tc_fence_before();
     __syncthreads();
@@ -1173,6 +1175,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     const long long w = kHeads ? blockIdx.x * 8LL + warp : blockIdx.x;
     if (w >= (long long)a.T * groups) return;
     const int t = (int)(w / groups), h0 = (int)(w - (long long)t * groups) * H;
+    grid_wait();
     const PfHeader h = *a.hdr;
     const int b = a.ws.owner[t];
     if (h.bad || b < 0) return;
@@ -1346,14 +1349,15 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
     auto kern = prefix_kernel<D>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
-    kern<<<sms, G::kThreads, smem, stream>>>(tq_p, tq_s, tk, tv, a);
+    if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to 16 an SM a block each; up to some waves of warps
     // a warp each; past that four heads a warp.
-    if (rows <= 16LL * sms) prefix_join_kernel<D, 0><<<(int)rows, 256, 0, stream>>>(a);
-    else if (rows <= 256LL * sms) prefix_join_kernel<D, 1><<<(int)((rows + 7) / 8), 256, 0, stream>>>(a);
-    else prefix_join_kernel<D, 4><<<(int)(((long long)a.T * ((a.Hq + 3) / 4) + 7) / 8), 256, 0, stream>>>(a);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    cudaError_t e;
+    if (rows <= 16LL * sms) e = launch_dependent(prefix_join_kernel<D, 0>, (int)rows, 256, 0, stream, a);
+    else if (rows <= 256LL * sms) e = launch_dependent(prefix_join_kernel<D, 1>, (int)((rows + 7) / 8), 256, 0, stream, a);
+    else e = launch_dependent(prefix_join_kernel<D, 4>, (int)(((long long)a.T * ((a.Hq + 3) / 4) + 7) / 8), 256, 0, stream, a);
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // namespace

@@ -504,6 +504,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return r;
 }
 
+// Programmatic dependent launch: wait until the kernels this one depends on have
+// completed and their writes are visible; let the next kernel's launch begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------
 // Small math helpers.
 // ----------------------------------------------------------------------------
