@@ -132,6 +132,19 @@ int make_map_pages(CUtensorMap* map, const void* ptr, int d, long long rows, int
     return r == CUDA_SUCCESS ? FA_OK : FA_ERR_INVALID;
 }
 
+int make_map_steps(CUtensorMap* map, const void* ptr, int d, long long rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return FA_ERR_LAUNCH;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)d / 64};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, 128};
+    cuuint32_t box[3] = {64, 16, (cuuint32_t)d / 64};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? FA_OK : FA_ERR_INVALID;
+}
+
 DevStatus* device_status_ptr() {
     DeviceInfo* d = nullptr;
     return current_device_info(&d) == FA_OK ? d->status : nullptr;

@@ -186,6 +186,9 @@ cudaError_t launch_fwd256(const FwdLaunch& L, cudaStream_t stream);
 // swizzle; rows past T read as zero.  Cache pages as [rows, d]: box {64, rows}.
 int make_map_rows(CUtensorMap* map, const void* ptr, int d, int H, long long T, long long stride, int heads, int tokens);
 int make_map_pages(CUtensorMap* map, const void* ptr, int d, long long rows, int box_rows);
+// Cache pages as {64, rows, d / 64}: a box is 16 whole rows, in shared memory as
+// d / 64 blocks of 16 x 128 bytes.
+int make_map_steps(CUtensorMap* map, const void* ptr, int d, long long rows);
 
 // Launch on `stream` as a programmatic dependent of the kernel before it there:
 // the launch and whatever the kernel does before grid_wait() overlap that

@@ -28,8 +28,9 @@
 //   rows <= 128   two workers, one for each softmax warpgroup, that share the
 //                 loader, the ring of K/V tiles and the issuer, which serves
 //                 them by turns;
-//   rows <= 32    one worker, no tcgen05 (few_rows below): single tokens, where
-//                 the copies set the pace.
+//   rows <= 32    no tcgen05: every warp (or pair of warps) is a worker of its
+//                 own (few_rows below): single tokens, where the copies set the
+//                 pace.
 // d = 256: one worker a CTA, one row tile, S double-buffered, 64-key tiles (its
 // accumulator takes half of tensor memory).
 //
@@ -51,10 +52,9 @@ namespace fa {
 namespace {
 
 constexpr float kTau = 8.0f;        // rescale threshold (log2 units), as in the forward kernels
-// An item of a request counts its tiles and this many more: its Q, its epilogue
-// and the pipeline's refill cost about two tiles in every shape (2800 cycles
-// with few rows, 5000 with one row tile at d = 256, 7000 with two).
-constexpr int kOverheadUnits = 2;
+
+constexpr int kFew = 0, kOne = 1, kTwo = 2;   // row tiles: 16 or 32 rows, 128, 2 x 128
+constexpr int kFewRows = 32;
 
 template <int D> struct Pf {
     static constexpr int kStreams = D == 256 ? 1 : 2;
@@ -68,16 +68,14 @@ template <int D> struct Pf {
     static constexpr int kRing = D == 64 ? 8 : 4;                // 128 KB of K/V tiles (even: few rows take K and V by pairs)
     static constexpr uint32_t kTiles = kStreams * kQTile + kRing * kTile;
     static constexpr int kThreads = 384;
-    // Few rows: two Q slots of 32 rows and the buffer for the join in place of
-    // the row tiles of Q.
-    static constexpr uint32_t kFewQ = 2 * 32 * D * 2;
-    static constexpr int kMergeFloats = (kStreams * kQTile - kFewQ) / 4;
+    static constexpr int kFewParts = D == 256 ? 1 : 2;               // few rows: 16-key parts a step, slots of a step's K or V a warp
+    static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
     // Cycles a CTA takes for a tile, by mode (kFew, kOne, kTwo), measured in the
     // kernel on GB300: how the CTAs are divided between the prefix and the
     // requests' own keys.
     __host__ __device__ static constexpr int cost(int mode) {
-        return D == 64 ? (mode == 0 ? 1100 : mode == 1 ? 2000 : 3400) : D == 128 ? (mode == 0 ? 1400 : mode == 1 ? 3200 : 3700)
-                                                                       : (mode == 0 ? 3200 : 2700);
+        return D == 64 ? (mode == kFew ? 400 : mode == kOne ? 2000 : 3400) : D == 128 ? (mode == kFew ? 800 : mode == kOne ? 3200 : 3700)
+                                                                             : (mode == kFew ? 1600 : 2700);
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
@@ -101,6 +99,8 @@ struct PfHeader {
 
 struct PfArgs {
     const int *table, *kv_lens, *cu, *prefix_table;
+    const __nv_bfloat16* q;
+    long long q_stride;
     DevStatus* status;
     PfHeader* hdr;
     PfTables ws;              // written by CTA 0 for the joining kernel
@@ -113,12 +113,17 @@ struct PfArgs {
     int rows_p, rows_s;       // rows a segment keeps
     int tiles_p, blocks_p;    // prefix: tiles an item, row blocks
     int mode_p, mode_s;       // kFew, kOne or kTwo (see above)
+    int width_p, width_s;     // workers a CTA
+    int halves_p, halves_s;   // kFew: 16-row halves of a block, a warp each
+    int ulog_p, ulog_s;       // log2 of the keys a unit
+    // An item of a request counts its units and this many more: with 128-row
+    // tiles its Q, its epilogue and the pipeline's refill cost about two tiles
+    // (5000 cycles with one row tile at d = 256, 7000 with two), with few rows
+    // less than one unit of 64 keys.
+    int over_s;
     int qstep_p, qstep_s;     // rows between Q slots: a block's rows, in whole swizzle atoms
     float scale_log2;
 };
-
-constexpr int kFew = 0, kOne = 1, kTwo = 2;   // row tiles: 16 or 32 rows, 128, 2 x 128
-constexpr int kFewRows = 32;
 
 enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kPfO, kPfPV, kPfDesc, kPfDescEmpty, kPfMerge };
 
@@ -153,14 +158,13 @@ template <int D>
 __device__ __forceinline__ int item_units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
     n = t.cu[b + 1] - t.cu[b];
     nb = cdiv(n, a.tb);
-    return n > 0 && t.len[b] > 0 ? cdiv(t.len[b], Pf<D>::kN) + kOverheadUnits : 0;
+    return n > 0 && t.len[b] > 0 ? ((t.len[b] + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s : 0;
 }
 
 // A worker's walk over its range of units.  Everything fits 32 bits: the host
 // refuses longer lists.
 template <int D>
 struct Walk {
-    static constexpr int kN = Pf<D>::kN;
     int u, end;
     int b, hk, k, worker, chunk, chunks;
     bool pre;
@@ -172,7 +176,7 @@ struct Walk {
         chunk = h.chunk;
         chunks = h.chunks;
         pre = c < h.n_p;
-        const int width = (pre ? a.mode_p : a.mode_s) == kOne ? Pf<D>::kStreams : 1;
+        const int width = pre ? a.width_p : a.width_s;
         worker = (pre ? c : c - h.n_p) * width + x;
         const int per = pre ? h.per_p : h.per_s, all = pre ? a.Hkv * a.blocks_p * a.tiles_p : t.pref[a.B];
         // worker * per passes the list's end by at most a CTA count times per.
@@ -233,7 +237,7 @@ struct Walk {
             it.seg = t.items[b] + i + worker;
             it.j0 = first;
             const int seen = it.lim0 + it.ntok - 1;        // keys the block's last row sees
-            it.j1 = min(last, seen > 0 ? cdiv(seen, kN) : 0);
+            it.j1 = min(last, seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
             if (last == per_item) {
                 if (++k == nb) {
                     k = 0;
@@ -256,9 +260,10 @@ struct PfShared {
     uint64_t d_full[2][kDesc], d_empty[2][kDesc], q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], pv_done[2], o_done[2], drain;
     // Four: the warps of a softmax warpgroup.
     uint64_t p_ready[2];
-    // Eight: few rows; the warps hand back tiles, Q, descriptions and the join's buffer.
-    uint64_t empty8[8], q_empty8[2], d_empty8[kDesc], m_full, m_free;
-    float2 ml[8][kFewRows];
+    // One again: few rows, each warp's slots.
+    uint64_t few_full[8][12];
+    Item few_item[8][2];
+    int few_walk[8][12];
     int4 scan[12];
     uint32_t tmem_base;
     int abort_flag, bad;
@@ -316,8 +321,8 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
             it = nb * a.Hkv;
             u = per * it;
             // What the causal mask leaves of a row block's tiles, on average.
-            c = ((float)(u - (u > 0 ? it * kOverheadUnits : 0)) * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)))) +
-                (u > 0 ? it * kOverheadUnits : 0);
+            c = ((float)(u - (u > 0 ? it * a.over_s : 0)) * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)))) +
+                (u > 0 ? it * a.over_s : 0);
         }
         const int u_own = u, it_own = it;
 #pragma unroll
@@ -362,7 +367,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     const float cp = (float)units_p * Pf<D>::cost(a.mode_p), cs = cost * Pf<D>::cost(a.mode_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
-    const int wp = np * (a.mode_p == kOne ? Pf<D>::kStreams : 1), ws = max(1, grid - np) * (a.mode_s == kOne ? Pf<D>::kStreams : 1);
+    const int wp = np * a.width_p, ws = max(1, grid - np) * a.width_s;
     h.n_p = np;
     h.per_p = wp ? (units_p + wp - 1) / wp : 1;
     h.per_s = units ? (units + ws - 1) / ws : 1;
@@ -411,14 +416,15 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 
 // ------------------------------------------------------------------ few rows
 //
-// Blocks of at most 32 rows (single tokens, small drafts).  A 128-row product
-// would be idle padding for most of its time and its softmax would run on one
-// warp in four; the copies set the pace here, so the eight warps take 16 keys
-// of a tile each (mma.sync m16n8k16, scores and weights stay in registers) with
-// maxima, sums and accumulators of their own, joined through shared memory at
-// the item's end.  With more than 16 rows, and at d = 256 (64-key tiles), four
-// warps share the keys (kKT = 32 or 16 each) and the second four take the second
-// 16 rows.
+// Blocks of at most 32 rows (single tokens, small drafts): the copies set the
+// pace, and what a 128-row product would cost is synchronisation (S, P and O
+// pass between three roles for every tile) and a softmax that one warp in four
+// would run.  Here each of eight warps is a worker of its own, or each pair of
+// warps when there are more than 16 rows (each takes 16): it walks its range of
+// the list, copies 16 keys of K or V at a time into a ring of its own
+// (TMA; a slot is free as soon as this warp has read it, so nothing waits for
+// another warp), and keeps scores, weights and the accumulator in registers
+// (mma.sync m16n8k16).  An item's end costs a store of the rows and no barrier.
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -433,217 +439,283 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int kKT>
-__device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t sQ, uint32_t sRing, float* merge, const WaitCtx& wc,
-                                         bool pre, int warp, int lane, int part_log2) {
+template <int D>
+__device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMap* tv, const PfArgs& a, const PfTables& t,
+                                         const PfHeader& hdr, PfShared& sh, uint32_t smem, const WaitCtx& wc, bool pre, int warp, int lane) {
     using G = Pf<D>;
-    constexpr int kN = G::kN, kRing = G::kRing;
-    constexpr int kKeys = 16 * kKT, kKeyGroups = kN / kKeys;         // keys a warp, warps that add to one row
-    constexpr bool kKeepQ = D <= 128;                                // Q's fragments in registers
+    constexpr int kKT = G::kFewParts, kKeys = 16 * kKT;              // 16-key parts and keys a step
+    constexpr uint32_t kPart = D * 32u, kSlot = kPart * kKT;         // K or V of a part (D / 64 boxes of 16 x 128 B), of a step
+    constexpr uint32_t kRing = G::kFewRing;
     constexpr int kKSteps = D / 16, kNT = D / 8;
-    const int kg = warp % kKeyGroups, row0 = (warp / kKeyGroups) * 16;
+    const int halves = pre ? a.halves_p : a.halves_s, half = warp % halves, ulog = pre ? a.ulog_p : a.ulog_s;
     const int g = lane >> 2, t2 = (lane & 3) * 2;
-    // ldmatrix row addresses: this lane's row of the four 8 x 8 matrices, and
-    // which 16-byte chunk of each 32-byte step it is; chunks are swizzled by
-    // row % 8 within a 128-byte row.
+    // ldmatrix: this lane's row of the four 8 x 8 matrices and which 16-byte
+    // chunk of each 32-byte step it is; chunks are swizzled by row % 8 within a
+    // 128-byte row.
     const int mi = lane >> 3, mr = lane & 7;
-    const uint32_t k_row = (kg * kKeys + (mi >> 1) * 8 + mr) * 128u, v_row = (kg * kKeys + (mi & 1) * 8 + mr) * 128u;
-    const uint32_t q_row = (row0 + (mi & 1) * 8 + mr) * 128u;
+    const uint32_t ring = smem + warp * (kRing * kSlot);
+    const uint32_t k_row = ((mi >> 1) * 8 + mr) * 128u, v_row = ((mi & 1) * 8 + mr) * 128u;
     const float scale = a.scale_log2;
-    uint32_t n_item = 0, n_merge = 0;
-    uint32_t qf[kKeepQ ? kKSteps : 1][4];
-    float o[kNT][4], m[2], l[2];
-    int lim[2], nkeys = 0, lim_min = 0, lim_max = 0, rows = 0, seg = 0;
-    uint32_t q_base = sQ;
-    bool idle = false;
-    auto q_frag = [&](uint32_t (&f)[4], int ks) {
-        ldsm4(f, q_base + (ks >> 2) * 4096u + q_row + (((((ks & 3) << 1) + (mi >> 1)) ^ mr) << 4));
-    };
-    auto arrive = [&](uint64_t* bar) {
+    uint64_t* full = sh.few_full[warp];
+
+    // The walk and the two items that the warp knows (the one it works on and
+    // the next, by turns) stay in shared memory: registers go to Q and O.
+    Walk<D>* walk = reinterpret_cast<Walk<D>*>(sh.few_walk[warp]);
+    Item* items = sh.few_item[warp];
+    {
+        Walk<D> w;
+        w.start(a, t, hdr, warp / halves);
+        if (lane == 0) *walk = w;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
+    }
+    // 16-key parts of an item: up to its last row's last key.
+    auto parts_of = [&](const Item& it) {
+        return (min(min(it.j1 << ulog, it.nkeys), it.lim0 + it.ntok - 1) - (it.j0 << ulog) + 15) >> 4;
     };
-    for (uint32_t n = 0;; ++n) {
-        if (!mbar_wait_w(&sh.d_full[0][n % kDesc], (n / kDesc) & 1, wc, kPfDesc)) return false;
-        const Desc& d = sh.desc[0][n % kDesc];
-        const int flags = d.flags, k0 = d.j * kN + kg * kKeys;
-        int live = 0;                                   // one bit a 16-key part that has a page
-#pragma unroll
-        for (int kt = 0; kt < kKT; ++kt) live |= ((d.live >> ((kg * kKeys + 16 * kt) >> part_log2)) & 1) << kt;
-        if (!(flags & kMore)) return true;
-        if (flags & kFirst) {
-            nkeys = d.nkeys;
-            rows = d.ntok * a.G;
-            seg = d.seg;
-            lim_min = pre ? nkeys : min(nkeys, d.lim0);
-            lim_max = pre ? nkeys : min(nkeys, d.lim0 + d.ntok - 1);
-            idle = row0 >= rows;
+    // This half's next item (one without rows for it is skipped) into items[to].
+    auto next_item = [&](int to) -> bool {
+        Walk<D> w = *walk;
+        Item it;
+        bool more;
+        do more = w.next(a, t, it); while (more && half * 16 >= it.ntok * a.G);
+        __syncwarp();
+        if (lane == 0) {
+            *walk = w;
+            if (more) items[to] = it;
+        }
+        __syncwarp();
+        return more;
+    };
+    // Pages of 32 parts of an item, one a lane.
+    auto pages = [&](const Item& it, int s0) -> int {
+        if (s0 + lane >= parts_of(it)) return -1;
+        const int p = it.tab[((it.j0 << ulog) + (s0 + lane) * 16) >> a.ps_log2];
+        return p >= 0 && p < a.P ? p : -1;
+    };
+    // The copies run ahead of the work, at most into the next item.
+    int cur = 0;                                                     // items[cur], items[cur ^ 1] is the next
+    bool has_next = false, in_next = false;                          // it is known; the copies are in it
+    int copy_part = 0, copy_parts = 0, copy_pg = -1, copy_hk = 0, copy_key = 0;   // next part in their item, its parts, this lane's page, head, key
+    int win = -1, ahead = -1, first = -1;                            // pages: of their 32 parts, of the next 32, of the next item's first 32
+    uint32_t issued = 0, filled = 0, live_bits = 0;                  // slots filled, the next one; one bit a part (mod 32): its page exists
+    bool ok = true;
+    auto enter = [&](const Item& it) {                               // the copies begin an item
+        copy_part = 0;
+        copy_parts = parts_of(it);
+        copy_hk = it.hk;
+        copy_key = it.j0 << ulog;
+        win = first;
+        ahead = pages(it, 32);
+    };
+    // Fills the next slot (K, then V of a step) if there is a step left to copy.
+    // Lane i copies part i.
+    auto copy = [&]() {
+        if (!(issued & 1)) {                                         // a new step
+            if (copy_part >= copy_parts) {
+                if (in_next || !has_next) return;
+                in_next = true;
+                enter(items[cur ^ 1]);
+            } else if (copy_part > 0 && (copy_part & 31) == 0) {
+                win = ahead;
+                ahead = pages(items[in_next ? cur ^ 1 : cur], copy_part + 32);
+            }
+            copy_pg = __shfl_sync(0xffffffffu, win, (copy_part + (lane & (kKT - 1))) & 31);   // -1 past the item's end
+            const uint32_t live = __ballot_sync(0xffffffffu, copy_pg >= 0) & ((1u << kKT) - 1u), at = (issued >> 1) * kKT & 31;
+            live_bits = (live_bits & ~(((1u << kKT) - 1u) << at)) | live << at;
+        }
+        const uint32_t live = live_bits >> ((issued >> 1) * kKT & 31) & ((1u << kKT) - 1u);
+        uint64_t* bar = &full[filled];
+        __syncwarp();                                                // every lane has read what the slot held
+        if (lane == 0) {
+            if (live) mbar_arrive_expect_tx(bar, kPart * __popc(live));
+            else mbar_arrive(bar);
+        }
+        __syncwarp();
+        if (lane < kKT && copy_pg >= 0)
+            tma_load_3d(ring + filled * kSlot + lane * kPart, issued & 1 ? tv : tk, bar, 0,
+                        ((copy_pg * a.Hkv + copy_hk) << a.ps_log2) + ((copy_key + (copy_part + lane) * 16) & ((1 << a.ps_log2) - 1)), 0);
+        if (issued & 1) copy_part += kKT;
+        ++issued;
+        filled = filled + 1 == kRing ? 0 : filled + 1;
+    };
+
+    uint32_t n = 0, slot = 0, phase = 0;                             // slots read, the next one, its barrier's parity
+    auto wait = [&]() { return mbar_wait_w(&full[slot], phase, wc, kPfRingFull); };
+    auto next_slot = [&]() {
+        ++n;
+        if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    if (next_item(0)) {
+        first = pages(items[0], 0);
+        enter(items[0]);
+        if ((has_next = next_item(1))) first = pages(items[1], 0);
+        for (uint32_t i = 0; i < kRing; ++i) copy();
+        while (ok) {
+            const Item& it = items[cur];
+            const int parts = parts_of(it), nkeys = it.nkeys, key0 = it.j0 << ulog;
+            // Q as A fragments, straight from memory; rows without a query are 0.
+            uint32_t qf[kKSteps][4];
+            float o[kNT][4], m[2], l[2];
+            int lim[2];
+            const int rows = it.ntok * a.G;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int r = row0 + h * 8 + g;
-                lim[h] = r >= rows ? 0 : (pre ? nkeys : min(nkeys, d.lim0 + r / a.G));
+                const int r = half * 16 + h * 8 + g, tok = r / a.G;
+                const bool real = r < rows;
+                lim[h] = !real ? 0 : pre ? it.nkeys : min(it.nkeys, it.lim0 + tok);
                 m[h] = -INFINITY;
                 l[h] = 0.f;
+                const __nv_bfloat16* src = a.q + (long long)(it.tok0 + tok) * a.q_stride + (it.hk * a.G + r - tok * a.G) * D + t2;
+#pragma unroll
+                for (int ks = 0; ks < kKSteps; ++ks) {
+                    qf[ks][h] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+                    qf[ks][2 + h] = real ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+                }
             }
 #pragma unroll
             for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-            if (!mbar_wait_w(&sh.q_full[n_item & 1], (n_item >> 1) & 1, wc, kPfQFull)) return false;
-            q_base = sQ + (n_item & 1) * (32u * D * 2u);
-            if constexpr (kKeepQ) {
+            const int lim_min = pre ? it.nkeys : min(it.nkeys, it.lim0 + half * 16 / a.G);
+            for (int st = 0; st < parts; st += kKT) {
+                const int k0 = key0 + st * 16;
+                const uint32_t live = live_bits >> ((n >> 1) * kKT & 31) & ((1u << kKT) - 1u);
+                uint32_t p[kKT][4];
+                if (!(ok = wait())) break;
+                if (live) {
+                    float s[2 * kKT][4] = {};
+                    const uint32_t base = ring + slot * kSlot + k_row;
+                    // Four loads, then their eight products: a load's latency
+                    // (33 cycles) is paid once a batch.
+                    constexpr int kBatch = 4 / kKT;
 #pragma unroll
-                for (int ks = 0; ks < kKSteps; ++ks) q_frag(qf[ks], ks);
-                arrive(&sh.q_empty8[n_item & 1]);
-            }
-        }
-        const uint32_t ik = 2 * n, iv = 2 * n + 1, slot_k = ik % kRing, slot_v = iv % kRing;
-        const bool work = live && !idle && k0 < lim_max;
-        uint32_t p[kKT][4];
-        if (!mbar_wait_w(&sh.full[slot_k], (ik / kRing) & 1, wc, kPfRingFull)) return false;
-        if (work) {
-            float s[2 * kKT][4];
+                    for (int k4 = 0; k4 < kKSteps; k4 += kBatch) {
+                        uint32_t b[4][4];
 #pragma unroll
-            for (int i = 0; i < 2 * kKT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-            const uint32_t base = sRing + slot_k * G::kTile + k_row;
+                        for (int i = 0; i < 4; ++i) {
+                            const int ks = k4 + i / kKT, kt = i % kKT;
+                            ldsm4(b[i], base + kt * kPart + (ks >> 2) * 2048u + (((((ks & 3) << 1) + (mi & 1)) ^ mr) << 4));
+                        }
 #pragma unroll
-            for (int ks = 0; ks < kKSteps; ++ks) {
-                uint32_t f[4];
-                if constexpr (!kKeepQ) q_frag(f, ks);
+                        for (int i = 0; i < 4; ++i) {
+                            const int ks = k4 + i / kKT, kt = i % kKT;
+                            mma16816(s[2 * kt], qf[ks], b[i][0], b[i][1]);
+                            mma16816(s[2 * kt + 1], qf[ks], b[i][2], b[i][3]);
+                        }
+                    }
+                    if (k0 + kKeys > lim_min || live != (1u << kKT) - 1u) {
 #pragma unroll
-                for (int kt = 0; kt < kKT; ++kt) {
-                    uint32_t b[4];
-                    ldsm4(b, base + kt * 2048u + (ks >> 2) * G::kKVBox + (((((ks & 3) << 1) + (mi & 1)) ^ mr) << 4));
-                    mma16816(s[2 * kt], kKeepQ ? qf[kKeepQ ? ks : 0] : f, b[0], b[1]);
-                    mma16816(s[2 * kt + 1], kKeepQ ? qf[kKeepQ ? ks : 0] : f, b[2], b[3]);
+                        for (int i = 0; i < 2 * kKT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!((live >> (i >> 1)) & 1u) || k0 + i * 8 + t2 + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
+                    }
+                    float mn[2];
+                    bool jump = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
+#pragma unroll
+                        for (int i = 1; i < 2 * kKT; ++i) x = fmax3(x, s[i][2 * h], s[i][2 * h + 1]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        mn[h] = fmaxf(m[h], x * scale);
+                        jump |= (m[h] == -INFINITY) ? (mn[h] != -INFINITY) : (mn[h] - m[h] > kTau);
+                    }
+                    if (__any_sync(0xffffffffu, jump)) {
+                        float fac[2];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            fac[h] = m[h] == -INFINITY ? 0.f : ex2_mufu(m[h] - mn[h]);
+                            l[h] *= fac[h];
+                            m[h] = mn[h];
+                        }
+#pragma unroll
+                        for (int i = 0; i < kNT; ++i) {
+                            o[i][0] *= fac[0];
+                            o[i][1] *= fac[0];
+                            o[i][2] *= fac[1];
+                            o[i][3] *= fac[1];
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float use = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+                        for (int i = 0; i < 2 * kKT; ++i) {
+                            const float p0 = ex2_mufu(fmaf(s[i][2 * h], scale, -use)), p1 = ex2_mufu(fmaf(s[i][2 * h + 1], scale, -use));
+                            l[h] += p0 + p1;
+                            p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
+                        }
+                    }
                 }
-            }
-            if (k0 + kKeys > lim_min || live != (1 << kKT) - 1) {
+                next_slot();
+                copy();
+                if (!(ok = wait())) break;
+                if (live) {
+                    const uint32_t base = ring + slot * kSlot + v_row;
+                    // Keys behind the list's end and of absent pages count as 0,
+                    // whatever their rows hold.
+                    auto pair = [&](int key) { return (key < nkeys ? 0xffffu : 0u) | (key + 1 < nkeys ? 0xffff0000u : 0u); };
+                    const bool whole = k0 + kKeys <= nkeys && live == (1u << kKT) - 1u;
 #pragma unroll
-                for (int i = 0; i < 2 * kKT; ++i)
+                    for (int kt = 0; kt < kKT; ++kt) {
+                        const uint32_t here = (live >> kt) & 1u ? ~0u : 0u;
+                        const uint32_t w0 = whole ? ~0u : here & pair(k0 + kt * 16 + t2), w1 = whole ? ~0u : here & pair(k0 + kt * 16 + 8 + t2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!((live >> (i >> 1)) & 1) || k0 + i * 8 + t2 + (e & 1) >= lim[e >> 1]) s[i][e] = -INFINITY;
+                        for (int i4 = 0; i4 < kNT; i4 += 8) {
+                            uint32_t b[4][4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = i4 + 2 * e;
+                                ldsm4t(b[e], base + kt * kPart + (i >> 3) * 2048u + ((((i & 7) + (mi >> 1)) ^ mr) << 4));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int i = i4 + 2 * e;
+                                mma16816(o[i], p[kt], b[e][0] & w0, b[e][1] & w1);
+                                mma16816(o[i + 1], p[kt], b[e][2] & w0, b[e][3] & w1);
+                            }
+                        }
+                    }
+                }
+                next_slot();
+                copy();
             }
-            float mn[2];
-            bool jump = false;
+            if (!ok) break;
+            // The rows' (m, l, O) into the segment's place.
+            const long long at = (long long)it.seg * (pre ? a.rows_p : a.rows_s);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float x = fmaxf(s[0][2 * h], s[0][2 * h + 1]);
-#pragma unroll
-                for (int i = 1; i < 2 * kKT; ++i) x = fmax3(x, s[i][2 * h], s[i][2 * h + 1]);
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                mn[h] = fmaxf(m[h], x * scale);
-                // Rows without a query (lim 0) never jump.
-                jump |= lim[h] > 0 && ((m[h] == -INFINITY) ? (mn[h] != -INFINITY) : (mn[h] - m[h] > kTau));
-            }
-            if (__any_sync(0xffffffffu, jump)) {
-                float fac[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    fac[h] = m[h] == -INFINITY ? 0.f : ex2_mufu(m[h] - mn[h]);
-                    l[h] *= fac[h];
-                    m[h] = mn[h];
-                }
-#pragma unroll
-                for (int i = 0; i < kNT; ++i) {
-                    o[i][0] *= fac[0];
-                    o[i][1] *= fac[0];
-                    o[i][2] *= fac[1];
-                    o[i][3] *= fac[1];
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float use = m[h] == -INFINITY ? 0.f : m[h];
-#pragma unroll
-                for (int i = 0; i < 2 * kKT; ++i) {
-                    const float p0 = ex2_mufu(fmaf(s[i][2 * h], scale, -use)), p1 = ex2_mufu(fmaf(s[i][2 * h + 1], scale, -use));
-                    l[h] += p0 + p1;
-                    p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
-                }
-            }
-        }
-        arrive(&sh.empty8[slot_k]);
-        if (!mbar_wait_w(&sh.full[slot_v], (iv / kRing) & 1, wc, kPfRingFull)) return false;
-        if (work) {
-            const uint32_t base = sRing + slot_v * G::kTile + v_row;
-            // Keys behind the list's end and of absent pages count as 0, whatever
-            // their rows hold.
-            auto half = [&](int key) {
-                return (key < nkeys ? 0xffffu : 0u) | (key + 1 < nkeys ? 0xffff0000u : 0u);
-            };
-            const bool whole = k0 + kKeys <= nkeys && live == (1 << kKT) - 1;
-#pragma unroll
-            for (int kt = 0; kt < kKT; ++kt) {
-                const bool here = (live >> kt) & 1;
-                const uint32_t w0 = whole ? ~0u : here ? half(k0 + 16 * kt + t2) : 0u, w1 = whole ? ~0u : here ? half(k0 + 16 * kt + 8 + t2) : 0u;
-#pragma unroll
-                for (int i = 0; i < kNT; i += 2) {
-                    uint32_t b[4];
-                    ldsm4t(b, base + kt * 2048u + (i >> 3) * G::kKVBox + ((((i & 7) + (mi >> 1)) ^ mr) << 4));
-                    mma16816(o[i], p[kt], b[0] & w0, b[1] & w1);
-                    mma16816(o[i + 1], p[kt], b[2] & w0, b[3] & w1);
-                }
-            }
-        }
-        arrive(&sh.empty8[slot_v]);
-        arrive(&sh.d_empty8[n % kDesc]);
-        if (!(flags & kLast)) continue;
-        // ------------------------------------------------------------ the item's end
-        if constexpr (!kKeepQ) arrive(&sh.q_empty8[n_item & 1]);
-        ++n_item;
-        // Rows in shared memory, C columns of D at a time; 8 floats of padding
-        // keep the eight rows of a store in different banks.
-        const int rp = rows <= 4 ? 4 : rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-        int C = D;
-        while (kKeyGroups * rp * (C + 8) > G::kMergeFloats) C >>= 1;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
-        const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s);
-        float* out = (pre ? a.o_p : a.o_s) + at * D;
-        for (int c0 = 0; c0 < D; c0 += C, ++n_merge) {
-            if (!mbar_wait_w(&sh.m_free, (n_merge & 1) ^ 1, wc, kPfMerge)) return false;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int r = row0 + h * 8 + g;
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+                l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+                const int r = half * 16 + h * 8 + g;
                 if (r < rows) {
-                    if (t2 == 0) sh.ml[kg][r] = make_float2(m[h], l[h]);
-                    float* to = merge + (kg * rp + r) * (C + 8) - c0 + t2;
+                    float* out = (pre ? a.o_p : a.o_s) + (at + r) * D + t2;
 #pragma unroll
-                    for (int i = 0; i < kNT; ++i)
-                        if (i * 8 >= c0 && i * 8 < c0 + C)
-                            *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                    for (int i = 0; i < kNT; ++i) *reinterpret_cast<float2*>(out + i * 8) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                    if (t2 == 0) (pre ? a.ml_p : a.ml_s)[at + r] = make_float2(m[h], l[h]);
                 }
             }
-            arrive(&sh.m_full);
-            if (!mbar_wait_w(&sh.m_full, n_merge & 1, wc, kPfMerge)) return false;
-            const int quads = C / 4;
-            for (int i = warp * 32 + lane; i < rows * quads; i += 256) {
-                const int r = i / quads, c = (i - r * quads) * 4;
-                float M = -INFINITY, L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kKeyGroups; ++w) M = fmaxf(M, sh.ml[w][r].x);
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int w = 0; w < kKeyGroups; ++w) {
-                    const float2 ml = sh.ml[w][r];
-                    const float f = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M);
-                    const float4 x = *reinterpret_cast<const float4*>(merge + (w * rp + r) * (C + 8) + c);
-                    L = fmaf(f, ml.y, L);
-                    v.x = fmaf(f, x.x, v.x);
-                    v.y = fmaf(f, x.y, v.y);
-                    v.z = fmaf(f, x.z, v.z);
-                    v.w = fmaf(f, x.w, v.w);
-                }
-                *reinterpret_cast<float4*>(out + (long long)r * D + c0 + c) = v;
-                if (c0 + c == 0) (pre ? a.ml_p : a.ml_s)[at + r] = make_float2(M, L);
+            if (!has_next) break;
+            // The next item becomes this one.
+            cur ^= 1;
+            if (in_next) in_next = false;
+            else enter(items[cur]);
+            if ((has_next = next_item(cur ^ 1))) first = pages(items[cur ^ 1], 0);
+            while (issued - n < kRing) {
+                const uint32_t before = issued;
+                copy();
+                if (issued == before) break;
             }
-            arrive(&sh.m_free);
         }
     }
+    // Every copy lands before teardown (after a wait that gave up, too).
+    const uint64_t t0 = globaltimer_ns();
+    for (; n < issued; next_slot())
+        while (!mbar_try_wait(smem_u32(&full[slot]), phase) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+    __syncwarp();
 }
 
 // -------------------------------------------------------------------- kernel
@@ -651,7 +723,8 @@ __device__ __forceinline__ bool few_rows(const PfArgs& a, PfShared& sh, uint32_t
 template <int D>
 __global__ void __launch_bounds__(Pf<D>::kThreads, 1)
 prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ CUtensorMap tq_s,
-              const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const PfArgs a) {
+              const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+              const __grid_constant__ CUtensorMap tk_few, const __grid_constant__ CUtensorMap tv_few, const PfArgs a) {
     using G = Pf<D>;
     constexpr int kN = G::kN, kStreams = G::kStreams, kRing = G::kRing, kBoxes = G::kBoxes;
     constexpr int kSoftWarps = 8;
@@ -669,11 +742,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
     {   // One barrier a thread, in the order of PfShared.
         constexpr int n1 = (offsetof(PfShared, p_ready) - offsetof(PfShared, d_full)) / 8;
-        constexpr int n4 = (offsetof(PfShared, empty8) - offsetof(PfShared, p_ready)) / 8;
-        constexpr int n8 = (offsetof(PfShared, ml) - offsetof(PfShared, empty8)) / 8;
-        static_assert(n1 + n4 + n8 <= G::kThreads, "one barrier a thread");
-        if (tid < n1 + n4 + n8) {
-            mbar_init(&sh.d_full[0][0] + tid, tid < n1 ? 1 : tid < n1 + n4 ? 4 : 8);
+        constexpr int n4 = (offsetof(PfShared, few_full) - offsetof(PfShared, p_ready)) / 8;
+        constexpr int nf = (offsetof(PfShared, few_item) - offsetof(PfShared, few_full)) / 8;
+        static_assert(n1 + n4 + nf <= G::kThreads, "one barrier a thread");
+        static_assert(sizeof(Walk<D>) <= sizeof(PfShared::few_walk[0]) && G::kFewRing <= 12, "few rows");
+        if (tid < n1 + n4 + nf) {
+            mbar_init(&sh.d_full[0][0] + tid, tid >= n1 && tid < n1 + n4 ? 4 : 1);
             fence_mbar_init();
         }
         if (tid == 0) sh.abort_flag = 0;
@@ -702,36 +776,46 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     const bool pre = (int)blockIdx.x < hdr.n_p;
     const int mode = pre ? a.mode_p : a.mode_s;
     const bool two = kStreams == 2 && mode == kTwo, few = mode == kFew;
-    const int workers = two || few ? 1 : kStreams;
+    const int workers = two ? 1 : kStreams;
     // Q slots: two row tiles, one slot of both; else as many in a worker's row
     // tile as its rows (in whole swizzle atoms) leave room for.  The products
     // read 128 rows from a slot on; the rows past its own give scores that
     // nobody looks at.
     const int qstep = pre ? a.qstep_p : a.qstep_s;
-    const uint32_t qn = two ? 1 : few ? 2 : min(kQMax / kStreams, 128 / qstep);
+    const uint32_t qn = two ? 1 : min(kQMax / kStreams, 128 / qstep);
     auto q_slot = [&](int x, uint32_t item) { return two ? 0u : x * qn + item % qn; };
-    auto q_addr = [&](int x, uint32_t item) {
-        return few ? sQ + (item & 1) * (G::kFewQ / 2) : sQ + x * G::kQTile + (two ? 0u : (item % qn) * qstep * 128u);
-    };
+    auto q_addr = [&](int x, uint32_t item) { return sQ + x * G::kQTile + (two ? 0u : (item % qn) * qstep * 128u); };
     auto desc_wait = [&](int x, uint32_t n) { return mbar_wait_w(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
 
-    if (warp >= kSoftWarps) {
-        regs_dec<88>();
-        if (warp == kSoftWarps + 3) {
-            // Which request each row belongs to, for the joining kernel.
-            for (int i = blockIdx.x * 32 + lane; i < a.T; i += gridDim.x * 32) {
-                int lo = -1;
-                if (i >= t.cu[0] && i < t.cu[a.B]) {
-                    lo = 0;
-                    for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
-                        const int mid = (lo + hi) >> 1;
-                        if (t.cu[mid] <= i) lo = mid; else hi = mid;
-                    }
+    // Which request each row belongs to, for the joining kernel.
+    auto owners = [&]() {
+        if (warp != kSoftWarps + 3) return;
+        for (int i = blockIdx.x * 32 + lane; i < a.T; i += gridDim.x * 32) {
+            int lo = -1;
+            if (i >= t.cu[0] && i < t.cu[a.B]) {
+                lo = 0;
+                for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
+                    const int mid = (lo + hi) >> 1;
+                    if (t.cu[mid] <= i) lo = mid; else hi = mid;
                 }
-                a.ws.owner[i] = lo;
             }
-            __syncwarp();
+            a.ws.owner[i] = lo;
         }
+        __syncwarp();
+    };
+    // Registers: 384 x 168 at launch, moved to the warpgroups that compute
+    // (2 x 232 + 40 or 2 x 208 + 88 = 3 x 168).
+    if (few) {
+        if (warp >= kSoftWarps) {
+            regs_dec<40>();
+            owners();
+        } else {
+            regs_inc<232>();
+            few_rows<D>(&tk_few, &tv_few, a, t, hdr, sh, base, wc, pre, warp, lane);
+        }
+    } else if (warp >= kSoftWarps) {
+        regs_dec<88>();
+        owners();
         if (warp == kSoftWarps) {
             // ------------------------------------------------------------ loader
             // The issuer's order: every worker's first K (kLook of them), then by
@@ -745,7 +829,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             bool ok = true;
             auto load = [&](const CUtensorMap* map, int p, int r) -> bool {
                 const uint32_t slot = n_ring % kRing;
-                if (!mbar_wait_w(few ? &sh.empty8[slot] : &sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
+                if (!mbar_wait_w(&sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
                 const uint32_t live = __ballot_sync(0xffffffffu, p >= 0);
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], __popc(live) * part_bytes);
                 __syncwarp();
@@ -769,13 +853,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 if (!load(&tk, pg[x][0], row[x][0])) return false;
                 if (flags & kFirst) {
                     const uint32_t i = n_item[x], s = q_slot(x, i);
-                    if (!mbar_wait_w(few ? &sh.q_empty8[s] : &sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
+                    if (!mbar_wait_w(&sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
                     const int boxes = two ? 2 * kBoxes : kBoxes;
                     if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[s], boxes * 128u * a.G * min(a.tq, pre ? a.T : a.max_seqlen));
                     __syncwarp();
                     if (lane < boxes) {
                         const int tile = lane / kBoxes, c = lane % kBoxes;
-                        tma_load_3d(q_addr(two ? tile : x, i) + c * (few ? 4096u : G::kQBox), pre ? &tq_p : &tq_s, &sh.q_full[s], c * 64, d.hk * a.G,
+                        tma_load_3d(q_addr(two ? tile : x, i) + c * G::kQBox, pre ? &tq_p : &tq_s, &sh.q_full[s], c * 64, d.hk * a.G,
                                     d.tok0 + tile * a.tq);
                     }
                     ++n_item[x];
@@ -783,8 +867,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 ++n_k[x];
                 return true;
             };
-            const int look = few ? 1 : G::kLook;   // few rows: K and V of a tile, then the next one's
-            for (int i = 0; i < look && ok; ++i)
+            for (int i = 0; i < G::kLook && ok; ++i)
 #pragma unroll
                 for (int x = 0; x < kStreams; ++x)
                     if (ok && x < workers && !ended[x]) ok = load_k(x);
@@ -809,7 +892,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 for (uint32_t i = n_item[x] > qn ? n_item[x] - qn : 0; i < n_item[x]; ++i)
                     while (!mbar_try_wait(smem_u32(&sh.q_full[q_slot(x, i)]), (i / qn) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
-        } else if (warp == kSoftWarps + 1 && !few) {
+        } else if (warp == kSoftWarps + 1) {
             // ------------------------------------------------------- UMMA issuer
             uint32_t n_ring = 0;
             bool ok = true;
@@ -942,7 +1025,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
-        } else if (warp >= kSoftWarps + 2 && warp - (kSoftWarps + 2) < workers) {
+        } else if (warp - (kSoftWarps + 2) < workers) {
             // ------------------------------------------------------ list walkers
             // Pages of four tiles at a time, a lane each; the next four's loads
             // (the next item's, past an item's end) run while these are handed on.
@@ -972,7 +1055,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 }
                 const int last = more ? min(j + 4, it.j1) : j + 1;
                 for (int jj = j; jj < last && ok; ++jj, ++n) {
-                    if (!(ok = mbar_wait_w(few ? &sh.d_empty8[n % kDesc] : &sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
+                    if (!(ok = mbar_wait_w(&sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
                     Desc& d = sh.desc[x][n % kDesc];
                     const uint32_t live = __ballot_sync(0xffffffffu, val >= 0);
                     if (q == jj - j) d.page[part] = val;
@@ -998,13 +1081,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             }
             __syncwarp();
         }
-    } else if (few) {
-        regs_inc<208>();
-        float* merge = reinterpret_cast<float*>(gbase + G::kFewQ);
-        if (D == 256 || qstep <= 16)
-            few_rows<D, 1>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
-        else if constexpr (D != 256)
-            few_rows<D, 2>(a, sh, sQ, sRing, merge, wc, pre, warp, lane, part_log2);
     } else {
         regs_inc<208>();
         // ------------------------------------------------------------- softmax
@@ -1168,7 +1244,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 // rows, where a warp each would leave most SMs idle).
 template <int D, int kHeads>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
-    constexpr int kN = Pf<D>::kN, E = D / 32, H = kHeads ? kHeads : 1;
+    constexpr int E = D / 32, H = kHeads ? kHeads : 1;
     __shared__ float s_o[kHeads ? 1 : 8][kHeads ? 1 : D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (a.Hq + H - 1) / H;
@@ -1182,7 +1258,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     const int c0 = a.ws.cu[b], n = a.ws.cu[b + 1] - c0, s = a.ws.len[b], pref = a.ws.pref[b], items = a.ws.items[b], i = t - c0;
     const int nb = cdiv(n, a.tb), rb = i / a.tb, blk = t / a.tb;
     const int seen = s > 0 ? s - n + min(n, (rb + 1) * a.tb) : 0;      // keys of the block's last row
-    const int own_tiles = seen > 0 ? cdiv(seen, kN) : 0, own_units = cdiv(s, kN) + kOverheadUnits;
+    const int own_tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0, own_units = ((s + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s;
     // Most segments that an item of the prefix can have, and room for all chunks'.
     const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = a.prefix_len > 0 ? most * h.chunks : 0;
     // Row of head h0 + x in the k-th of its segments, the prefix's first, then
@@ -1319,15 +1395,15 @@ struct PfLayout {
 // Workspace: header, tables, the segments' rows.  The prefix's items are row
 // blocks times chunks of a worker's share of tiles, so at most row blocks plus
 // workers; the requests' at most T / tb + min(T, B) a key/value head.  Segments:
-// items plus workers (two a CTA at most).
+// items plus workers (eight a CTA with few rows, else two at most).
 PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms) {
     PfLayout w;
     w.tq = 128 / G;
     w.tb = d == 256 ? w.tq : 2 * w.tq;
     w.rows_p = (T < w.tb ? T : w.tb) * G;
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
-    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + 4 * sms;
-    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + 2 * sms;
+    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + (size_t)(T * (long long)G <= kFewRows ? 8 : 4) * sms;
+    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + (size_t)(max_seqlen * (long long)G <= kFewRows ? 8 : 2) * sms;
     w.pref = align256(sizeof(PfHeader));
     w.items = align256(w.pref + (size_t)(B + 1) * 4);
     w.cu = align256(w.items + (size_t)(B + 1) * 4);
@@ -1342,14 +1418,14 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
 }
 
 template <int D>
-int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtensorMap& tk, const CUtensorMap& tv, const PfArgs& a,
-                  int sms, cudaStream_t stream) {
+int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtensorMap& tk, const CUtensorMap& tv,
+                  const CUtensorMap& tk_few, const CUtensorMap& tv_few, const PfArgs& a, int sms, cudaStream_t stream) {
     using G = Pf<D>;
     const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4;
     static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
     auto kern = prefix_kernel<D>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
-    if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, a) != cudaSuccess) return FA_ERR_LAUNCH;
+    if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to 16 an SM a block each; up to some waves of warps
     // a warp each; past that four heads a warp.
@@ -1406,8 +1482,13 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
 
     const int kN = d == 256 ? 64 : 128;
+    const int mode_p = T * (long long)G <= kFewRows ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
+    const int mode_s = max_seqlen * (long long)G <= kFewRows ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
+    const int ulog_p = mode_p == kFew || d == 256 ? 6 : 7, ulog_s = mode_s == kFew || d == 256 ? 6 : 7;
     // The list of tiles, at its longest, stays within 32 bits.
-    const long long tiles_s = ((long long)table_width * page_size + kN - 1) / kN + kOverheadUnits, tiles_p = ((long long)prefix_len + kN - 1) / kN;
+    const int over_s = mode_s == kFew ? 1 : 2;
+    const long long tiles_s = (((long long)table_width * page_size + (1 << ulog_s) - 1) >> ulog_s) + over_s;
+    const long long tiles_p = ((long long)prefix_len + (1 << ulog_p) - 1) >> ulog_p;
     const long long blocks_s = (long long)Hkv * (T / w.tb + (T < B ? T : B)), blocks_p = (long long)Hkv * ((T + w.tb - 1) / w.tb);
     if (blocks_s * tiles_s > lim - (1 << 20) || blocks_p * tiles_p > lim - (1 << 20)) return FA_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -1416,6 +1497,8 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.kv_lens = kv_lens;
     a.cu = cu_seqlens;
     a.prefix_table = prefix_table;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_stride = q_stride;
     a.status = status;
     a.hdr = reinterpret_cast<PfHeader*>(ws);
     a.ws.pref = reinterpret_cast<int*>(ws + w.pref);
@@ -1443,26 +1526,38 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.tb = w.tb;
     a.rows_p = w.rows_p;
     a.rows_s = w.rows_s;
-    a.tiles_p = (prefix_len + kN - 1) / kN;
+    a.tiles_p = (int)tiles_p;
     a.blocks_p = (T + w.tb - 1) / w.tb;
-    a.mode_p = T * (long long)G <= kFewRows ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
-    a.mode_s = max_seqlen * (long long)G <= kFewRows ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
+    a.mode_p = mode_p;
+    a.mode_s = mode_s;
+    a.halves_p = T * (long long)G > 16 ? 2 : 1;
+    a.halves_s = max_seqlen * (long long)G > 16 ? 2 : 1;
+    a.width_p = a.mode_p == kFew ? 8 / a.halves_p : a.mode_p == kOne && d != 256 ? 2 : 1;
+    a.width_s = a.mode_s == kFew ? 8 / a.halves_s : a.mode_s == kOne && d != 256 ? 2 : 1;
+    a.ulog_p = ulog_p;
+    a.ulog_s = ulog_s;
+    a.over_s = over_s;
     const int box_p = T < w.tq ? T : w.tq, box_s = max_seqlen < w.tq ? max_seqlen : w.tq;
     a.qstep_p = (box_p * G + 7) & ~7;
     a.qstep_s = (box_s * G + 7) & ~7;
     a.scale_log2 = alpha * 1.4426950408889634f;
 
-    CUtensorMap tq_p, tq_s, tk, tv;
+    CUtensorMap tq_p, tq_s, tk, tv, tk_few, tv_few;
     int rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
     if (rc == FA_OK) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
     const long long slots = (long long)num_pages * Hkv * page_size;
     const int part = page_size < kN ? page_size : kN;
     if (rc == FA_OK) rc = make_map_pages(&tk, k_pages, d, slots, part);
     if (rc == FA_OK) rc = make_map_pages(&tv, v_pages, d, slots, part);
+    // Few rows: 16 keys a copy whatever the page size, all of d at once (a copy
+    // of 2 KB an instruction keeps an SM at 28 B a cycle, a third below what 60
+    // SMs need for HBM's rate).
+    if (rc == FA_OK) rc = make_map_steps(&tk_few, k_pages, d, slots);
+    if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
     if (rc != FA_OK) return rc;
-    if (d == 64) return launch_prefix<64>(tq_p, tq_s, tk, tv, a, sms, stream);
-    if (d == 128) return launch_prefix<128>(tq_p, tq_s, tk, tv, a, sms, stream);
-    return launch_prefix<256>(tq_p, tq_s, tk, tv, a, sms, stream);
+    if (d == 64) return launch_prefix<64>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
+    if (d == 128) return launch_prefix<128>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
+    return launch_prefix<256>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
 }
 
 }  // extern "C"
