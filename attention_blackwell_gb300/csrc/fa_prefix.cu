@@ -54,7 +54,7 @@ namespace {
 constexpr float kTau = 8.0f;        // rescale threshold (log2 units), as in the forward kernels
 
 constexpr int kFew = 0, kOne = 1, kTwo = 2;   // row tiles: 16 or 32 rows, 128, 2 x 128
-constexpr int kFewRows = 32;
+constexpr int few_limit(int d) { return d == 256 ? 16 : 32; }   // rows up to which kFew is taken
 
 template <int D> struct Pf {
     static constexpr int kStreams = D == 256 ? 1 : 2;
@@ -70,12 +70,15 @@ template <int D> struct Pf {
     static constexpr int kThreads = 384;
     static constexpr int kFewParts = D == 256 ? 1 : 2;               // few rows: 16-key parts a step, slots of a step's K or V a warp
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
-    // Cycles a CTA takes for a tile, by mode (kFew, kOne, kTwo), measured in the
-    // kernel on GB300: how the CTAs are divided between the prefix and the
-    // requests' own keys.
-    __host__ __device__ static constexpr int cost(int mode) {
-        return D == 64 ? (mode == kFew ? 400 : mode == kOne ? 2000 : 3400) : D == 128 ? (mode == kFew ? 800 : mode == kOne ? 3200 : 3700)
-                                                                             : (mode == kFew ? 1600 : 2700);
+    // Cycles a CTA takes for a unit, measured in the kernel on GB300; the CTAs
+    // are divided between the prefix and the requests' own keys by them.  kTwo
+    // alone: the prefix's tiles come from HBM for one row block only (`shared`:
+    // several row blocks read them, L2 serves the others), whose latency under
+    // the other CTAs' load then sets the pace.
+    __host__ __device__ static constexpr int cost(int mode, int halves, bool shared) {
+        return mode == kFew ? (D == 64 ? 600 : D == 128 ? 780 : 1900) * halves
+             : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2700)
+                            : (D == 64 ? (shared ? 3400 : 5500) : (shared ? 3700 : 6000));
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
@@ -364,7 +367,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     __syncthreads();
     PfHeader h;
     const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
-    const float cp = (float)units_p * Pf<D>::cost(a.mode_p), cs = cost * Pf<D>::cost(a.mode_s);
+    const float cp = (float)units_p * Pf<D>::cost(a.mode_p, a.halves_p, a.blocks_p > 1), cs = cost * Pf<D>::cost(a.mode_s, a.halves_s, true);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
     const int wp = np * a.width_p, ws = max(1, grid - np) * a.width_s;
@@ -967,19 +970,22 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                     }
                 }
             } else {
-                uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_item[2] = {0, 0};
+                uint32_t n_s[2] = {0, 0}, n_p[2] = {0, 0}, n_item[2] = {0, 0}, ks;
                 bool ended[2] = {false, false};
-                // S of worker x's next tile.
-                auto issue_s = [&](int x) -> bool {
+                // The K of worker x's next tile, if it has one (its flags, else 0).
+                int flags_s = 0;
+                auto take_k = [&](int x) -> bool {
+                    flags_s = 0;
+                    if (ended[x]) return true;
                     if (!desc_wait(x, n_s[x])) return false;
-                    const int flags = sh.desc[x][n_s[x] % kDesc].flags;
-                    if (!(flags & kMore)) {
-                        ended[x] = true;
-                        return true;
-                    }
-                    uint32_t ks;
-                    if (!take(ks)) return false;
-                    if (flags & kFirst) {
+                    flags_s = sh.desc[x][n_s[x] % kDesc].flags;
+                    ended[x] = !(flags_s & kMore);
+                    if (ended[x]) flags_s = 0;
+                    return ended[x] || take(ks);
+                };
+                // Its S.
+                auto issue_s = [&](int x) -> bool {
+                    if (flags_s & kFirst) {
                         const uint32_t i = n_item[x]++;
                         if (!mbar_wait_w(&sh.q_full[q_slot(x, i)], (i / qn) & 1, wc, kPfQFull)) return false;
                     }
@@ -987,14 +993,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                     pf_issue_qk<D>(col_s(buf), q_addr(x, n_item[x] - 1), sRing + ks * G::kTile);
                     umma_commit_w(&sh.s_full[buf]);
                     umma_commit_w(&sh.empty[ks]);
-                    if (flags & kLast) umma_commit_w(&sh.q_empty[q_slot(x, n_item[x] - 1)]);
+                    if (flags_s & kLast) umma_commit_w(&sh.q_empty[q_slot(x, n_item[x] - 1)]);
                     ++n_s[x];
                     return true;
                 };
                 for (int i = 0; i < G::kLook && ok; ++i)
 #pragma unroll
                     for (int x = 0; x < kStreams; ++x)
-                        if (ok && !ended[x]) ok = issue_s(x);
+                        if (ok && !ended[x]) ok = take_k(x) && (!flags_s || issue_s(x));
                 bool any = true;
                 while (ok && any) {
                     any = false;
@@ -1008,15 +1014,18 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         uint32_t vs;
                         if (!(ok = take(vs))) break;
                         clean(vs, d);
+                        // Both tiles are waited for before P, so that S follows P V
+                        // into the tensor core without a pause.
+                        if (!(ok = take_k(x))) break;
                         if (!(ok = mbar_wait_w(&sh.p_ready[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfP))) break;
                         tc_fence_after();
                         pf_issue_pv<D>(tmem + x * G::kColO1, col_s(buf), sRing + vs * G::kTile, !(flags & kFirst));
                         umma_commit_w(&sh.empty[vs]);
                         if (kStreams == 1) umma_commit_w(&sh.pv_done[buf]);
                         if (flags & kLast) umma_commit_w(&sh.o_done[x]);
+                        if (flags_s && !(ok = issue_s(x))) break;
                         free_desc(x, n);
                         ++n_p[x];
-                        if (!ended[x]) ok = issue_s(x);
                     }
                 }
             }
@@ -1402,8 +1411,8 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
     w.tb = d == 256 ? w.tq : 2 * w.tq;
     w.rows_p = (T < w.tb ? T : w.tb) * G;
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
-    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + (size_t)(T * (long long)G <= kFewRows ? 8 : 4) * sms;
-    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + (size_t)(max_seqlen * (long long)G <= kFewRows ? 8 : 2) * sms;
+    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + (size_t)(T * (long long)G <= few_limit(d) ? 8 : 4) * sms;
+    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + (size_t)(max_seqlen * (long long)G <= few_limit(d) ? 8 : 2) * sms;
     w.pref = align256(sizeof(PfHeader));
     w.items = align256(w.pref + (size_t)(B + 1) * 4);
     w.cu = align256(w.items + (size_t)(B + 1) * 4);
@@ -1482,8 +1491,11 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
 
     const int kN = d == 256 ? 64 : 128;
-    const int mode_p = T * (long long)G <= kFewRows ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
-    const int mode_s = max_seqlen * (long long)G <= kFewRows ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
+    // Few rows: at d = 256 up to 16 (two warps for 32 rows take 4000 cycles a unit of
+    // 64 keys, one row tile 2700), else up to 32 (1560 a unit at d = 128, one row
+    // tile 2500).
+    const int mode_p = T * (long long)G <= few_limit(d) ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
+    const int mode_s = max_seqlen * (long long)G <= few_limit(d) ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
     const int ulog_p = mode_p == kFew || d == 256 ? 6 : 7, ulog_s = mode_s == kFew || d == 256 ? 6 : 7;
     // The list of tiles, at its longest, stays within 32 bits.
     const int over_s = mode_s == kFew ? 1 : 2;
