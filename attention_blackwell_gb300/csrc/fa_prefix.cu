@@ -84,12 +84,16 @@ template <int D> struct Pf {
 };
 
 // What both kernels need to know of the list of units.
+// Of a row of q, for the joining kernel: its request's first row, rows and keys
+// (n = 0: no request), the units and items before it.
+struct PfRow {
+    int c0, n, s, pref, items, pad[3];
+};
 struct PfTables {
     int* pref;           // [B+1] units of requests before b (all key/value heads)
     int* items;          // [B+1] items of requests before b
     int* cu;             // [B+1] sanitised offsets
     int* len;            // [B] own keys
-    int* owner;          // [T] request of each row, -1: none (workspace only)
 };
 
 struct PfHeader {
@@ -106,7 +110,7 @@ struct PfArgs {
     long long q_stride;
     DevStatus* status;
     PfHeader* hdr;
-    PfTables ws;              // written by CTA 0 for the joining kernel
+    PfRow* rows;              // [T]
     float *o_p, *o_s;         // segments' rows [segment][rows][D]: prefix, requests
     float2 *ml_p, *ml_s;      // their (m, l)
     void* o;
@@ -156,13 +160,23 @@ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int block_of(int k, int n) { return (k & 1) ? n - 1 - (k >> 1) : k >> 1; }
 __device__ __forceinline__ int index_of(int rb, int n) { return rb < (n + 1) / 2 ? 2 * rb : 2 * (n - 1 - rb) + 1; }
 
-// Units an item of request b has (0: no rows or no keys), its rows and row blocks.
+// Units an item of a request with n rows and s keys has (0: no rows or no
+// keys): the tiles that its row blocks see under the causal mask, on average,
+// and what an item costs besides.  Row blocks are taken from both ends by turns
+// (block_of), so two neighbours make up two averages.
+__device__ __forceinline__ int units_of(const PfArgs& a, int n, int s) {
+    if (n <= 0 || s <= 0) return 0;
+    const int seen = min(s, max(1, s - n + (n + min(n, a.tb)) / 2));
+    return ((seen + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s;
+}
 template <int D>
 __device__ __forceinline__ int item_units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
     n = t.cu[b + 1] - t.cu[b];
     nb = cdiv(n, a.tb);
-    return n > 0 && t.len[b] > 0 ? ((t.len[b] + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s : 0;
+    return units_of(a, n, t.len[b]);
 }
+// Where unit u of an item's `units` falls among its `tiles`.
+__device__ __forceinline__ int tile_of(int u, int units, int tiles) { return (int)((long long)u * tiles / units); }
 
 // A worker's walk over its range of units.  Everything fits 32 bits: the host
 // refuses longer lists.
@@ -238,9 +252,10 @@ struct Walk {
             it.lim0 = s - n + i0 + 1;
             it.tab = a.table + (long long)b * a.W;
             it.seg = t.items[b] + i + worker;
-            it.j0 = first;
             const int seen = it.lim0 + it.ntok - 1;        // keys the block's last row sees
-            it.j1 = min(last, seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
+            const int tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0;
+            it.j0 = tile_of(first, per_item, tiles);
+            it.j1 = tile_of(last, per_item, tiles);
             if (last == per_item) {
                 if (++k == nb) {
                     k = 0;
@@ -267,7 +282,7 @@ struct PfShared {
     uint64_t few_full[8][12];
     Item few_item[8][2];
     int few_walk[8][12];
-    int4 scan[12];
+    int2 scan[12];
     uint32_t tmem_base;
     int abort_flag, bad;
 };
@@ -312,20 +327,15 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
         __syncthreads();
     }
     int units = 0, items = 0;      // of the requests before this round's
-    float cost = 0.f;
     for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + tid;
         int u = 0, it = 0;
-        float c = 0.f;
         if (i < a.B) {
             int n, nb;
             const int per = item_units<D>(a, t, i, n, nb);
             if (n > a.max_seqlen) sh.bad = 1;
             it = nb * a.Hkv;
             u = per * it;
-            // What the causal mask leaves of a row block's tiles, on average.
-            c = ((float)(u - (u > 0 ? it * a.over_s : 0)) * fminf(1.f, fmaxf(0.f, 1.f - 0.5f * n / fmaxf((float)t.len[i], 1.f)))) +
-                (u > 0 ? it * a.over_s : 0);
         }
         const int u_own = u, it_own = it;
 #pragma unroll
@@ -336,22 +346,19 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
                 it += y;
             }
         }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
         if (base) __syncthreads();
-        if (lane == 31) sh.scan[warp] = make_int4(u, it, __float_as_int(c), 0);
+        if (lane == 31) sh.scan[warp] = make_int2(u, it);
         __syncthreads();
         int u_all = 0, it_all = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const int4 x = sh.scan[w];
+            const int2 x = sh.scan[w];
             if (w == warp) {
                 u += units + u_all;
                 it += items + it_all;
             }
             u_all += x.x;
             it_all += x.y;
-            cost += __int_as_float(x.z);
         }
         if (i < a.B) {
             t.pref[i] = u - u_own;
@@ -367,7 +374,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     __syncthreads();
     PfHeader h;
     const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
-    const float cp = (float)units_p * Pf<D>::cost(a.mode_p, a.halves_p, a.blocks_p > 1), cs = cost * Pf<D>::cost(a.mode_s, a.halves_s, true);
+    const float cp = (float)units_p * Pf<D>::cost(a.mode_p, a.halves_p, a.blocks_p > 1), cs = (float)units * Pf<D>::cost(a.mode_s, a.halves_s, true);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
     const int wp = np * a.width_p, ws = max(1, grid - np) * a.width_s;
@@ -377,17 +384,9 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     h.chunk = a.blocks_p > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
     h.chunks = (a.tiles_p + h.chunk - 1) / h.chunk;
     h.bad = sh.bad;
-    if (blockIdx.x == 0) {
-        for (int i = tid; i <= a.B; i += kThreads) {
-            a.ws.pref[i] = t.pref[i];
-            a.ws.items[i] = t.items[i];
-            a.ws.cu[i] = t.cu[i];
-            if (i < a.B) a.ws.len[i] = t.len[i];
-        }
-        if (tid == 0) {
-            *a.hdr = h;
-            if (h.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 101; a.status->block = 0; }
-        }
+    if (blockIdx.x == 0 && tid == 0) {
+        *a.hdr = h;
+        if (h.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 101; a.status->block = 0; }
     }
     return h;
 }
@@ -790,19 +789,24 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     auto q_addr = [&](int x, uint32_t item) { return sQ + x * G::kQTile + (two ? 0u : (item % qn) * qstep * 128u); };
     auto desc_wait = [&](int x, uint32_t n) { return mbar_wait_w(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
 
-    // Which request each row belongs to, for the joining kernel.
+    // What the joining kernel needs to know of each row.
     auto owners = [&]() {
         if (warp != kSoftWarps + 3) return;
         for (int i = blockIdx.x * 32 + lane; i < a.T; i += gridDim.x * 32) {
-            int lo = -1;
+            PfRow row = {};
             if (i >= t.cu[0] && i < t.cu[a.B]) {
-                lo = 0;
+                int lo = 0;
                 for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
                     const int mid = (lo + hi) >> 1;
                     if (t.cu[mid] <= i) lo = mid; else hi = mid;
                 }
+                row.c0 = t.cu[lo];
+                row.n = t.cu[lo + 1] - row.c0;
+                row.s = t.len[lo];
+                row.pref = t.pref[lo];
+                row.items = t.items[lo];
             }
-            a.ws.owner[i] = lo;
+            a.rows[i] = row;
         }
         __syncwarp();
     };
@@ -1248,55 +1252,48 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
 // ---------------------------------------------------------------------- join
 
-// kHeads > 0: a warp takes that many heads of a row, whose loads overlap (many
-// rows); kHeads = 0: the eight warps of a block share one head's segments (few
-// rows, where a warp each would leave most SMs idle).
-template <int D, int kHeads>
+// A warp joins kHeads heads of one key/value head in one row of q: their
+// segments are the same, their rows in a segment neighbours, so one set of
+// places serves all and their loads overlap (many rows: 4 or 2 where they divide
+// the group).  kSplit: the eight warps of a block share one head's segments
+// (few rows, where a warp each would leave most SMs idle).
+template <int D, int kHeads, bool kSplit>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
-    constexpr int E = D / 32, H = kHeads ? kHeads : 1;
-    __shared__ float s_o[kHeads ? 1 : 8][kHeads ? 1 : D];
+    constexpr int E = D / 32, H = kHeads;
+    static_assert(!kSplit || H == 1, "one head a block");
+    __shared__ float s_o[kSplit ? 8 : 1][kSplit ? D : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = (a.Hq + H - 1) / H;
-    const long long w = kHeads ? blockIdx.x * 8LL + warp : blockIdx.x;
+    const int groups = a.Hq / H;
+    const long long w = kSplit ? blockIdx.x : blockIdx.x * 8LL + warp;
     if (w >= (long long)a.T * groups) return;
-    const int t = (int)(w / groups), h0 = (int)(w - (long long)t * groups) * H;
+    const int t = (int)(w / groups), h0 = (int)(w - (long long)t * groups) * H, hk = h0 / a.G, g0 = h0 - hk * a.G;
     grid_wait();
     const PfHeader h = *a.hdr;
-    const int b = a.ws.owner[t];
-    if (h.bad || b < 0) return;
-    const int c0 = a.ws.cu[b], n = a.ws.cu[b + 1] - c0, s = a.ws.len[b], pref = a.ws.pref[b], items = a.ws.items[b], i = t - c0;
-    const int nb = cdiv(n, a.tb), rb = i / a.tb, blk = t / a.tb;
-    const int seen = s > 0 ? s - n + min(n, (rb + 1) * a.tb) : 0;      // keys of the block's last row
-    const int own_tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0, own_units = ((s + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s;
+    const PfRow r = a.rows[t];
+    if (h.bad || r.n == 0) return;
+    const int i = t - r.c0, nb = cdiv(r.n, a.tb), rb = i / a.tb, blk = t / a.tb;
     // Most segments that an item of the prefix can have, and room for all chunks'.
     const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = a.prefix_len > 0 ? most * h.chunks : 0;
-    // Row of head h0 + x in the k-th of its segments, the prefix's first, then
-    // the request's, each in the list's order; negative: there is none.
-    int own_seg[H], own_n[H], all = 0;
-#pragma unroll
-    for (int x = 0; x < H; ++x) {
-        own_seg[x] = own_n[x] = 0;
-        if (own_tiles > 0 && h0 + x < a.Hq) {
-            const int item = (h0 + x) / a.G * nb + index_of(rb, nb), u0 = pref + item * own_units;
-            const int ca = u0 / h.per_s;
-            own_n[x] = (u0 + own_tiles - 1) / h.per_s - ca + 1;
-            own_seg[x] = items + item + ca;
-        }
-        all = max(all, h0 + x < a.Hq ? slots + own_n[x] : 0);
-    }
-    auto place = [&](int x, int k) -> long long {
-        const int head = h0 + x, hk = head / a.G, gi = head - hk * a.G;
-        if (head >= a.Hq) return -1;
+    // The request's item: its units from u0 on, the workers that they fall to.
+    const int units = units_of(a, r.n, r.s), seen = units ? r.s - r.n + min(r.n, (rb + 1) * a.tb) : 0;
+    const int tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0;
+    const int item = hk * nb + index_of(rb, nb), u0 = r.pref + item * units, c_own = u0 / h.per_s;
+    const int all = slots + (tiles > 0 ? (u0 + units - 1) / h.per_s - c_own + 1 : 0);
+    // Row (of head h0) in the k-th segment, the prefix's first, then the
+    // request's, each in the list's order; negative: there is none.
+    auto place = [&](int k) -> long long {
+        if (k >= all) return -1;
         if (k < slots) {
             const int ch = k / most, j = k - ch * most, len = min(h.chunk, a.tiles_p - ch * h.chunk);
-            const int u0 = hk * a.blocks_p * a.tiles_p + ch * h.chunk * a.blocks_p + blk * len;
-            const int ca = u0 / h.per_p, cb = (u0 + len - 1) / h.per_p;
+            const int v0 = hk * a.blocks_p * a.tiles_p + ch * h.chunk * a.blocks_p + blk * len;
+            const int ca = v0 / h.per_p, cb = (v0 + len - 1) / h.per_p;
             if (ca + j > cb) return -1;
-            const int seg = (hk * h.chunks + ch) * a.blocks_p + blk + ca + j;
-            return (long long)seg * a.rows_p + (t - blk * a.tb) * a.G + gi;
+            return (long long)((hk * h.chunks + ch) * a.blocks_p + blk + ca + j) * a.rows_p + (t - blk * a.tb) * a.G + g0;
         }
-        if (k - slots >= own_n[x]) return -1;
-        return (long long)(own_seg[x] + k - slots) * a.rows_s + (i - rb * a.tb) * a.G + gi;
+        const int c = c_own + k - slots;
+        const int from = max(0, c * h.per_s - u0), to = min(units, c * h.per_s + h.per_s - u0);
+        if (tile_of(from, units, tiles) >= tile_of(to, units, tiles)) return -1;
+        return (long long)(r.items + item + c) * a.rows_s + (i - rb * a.tb) * a.G + g0;
     };
     float M[H], L[H], acc[H][E];
 #pragma unroll
@@ -1306,89 +1303,84 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[x][e] = 0.f;
     }
-    for (int k0 = 0; k0 < all; k0 += 32)
+    // Places and (m, l) of the first 32 segments, one a lane; rarely there are more.
+    float2 ml[H];
+    long long at = -1;
+    auto load_ml = [&](int k) {
+        at = place(k);
 #pragma unroll
-        for (int x = 0; x < H; ++x) {
-            const int k = k0 + lane;
-            const long long at = k < all ? place(x, k) : -1;
-            if (at >= 0) M[x] = fmaxf(M[x], (k < slots ? a.ml_p : a.ml_s)[at].x);
-        }
+        for (int x = 0; x < H; ++x) ml[x] = at >= 0 ? (k < slots ? a.ml_p : a.ml_s)[at + x] : make_float2(-INFINITY, 0.f);
+    };
+    for (int k0 = (all - 1) / 32 * 32; k0 >= 0; k0 -= 32) {
+        load_ml(k0 + lane);
+#pragma unroll
+        for (int x = 0; x < H; ++x) M[x] = fmaxf(M[x], ml[x].x);
+    }
 #pragma unroll
     for (int x = 0; x < H; ++x)
         for (int o = 16; o; o >>= 1) M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], o));
     for (int k0 = 0; k0 < all; k0 += 32) {
+        if (k0) load_ml(k0 + lane);
         float f[H];
-        long long at[H];
 #pragma unroll
         for (int x = 0; x < H; ++x) {
-            const int k = k0 + lane;
-            at[x] = k < all ? place(x, k) : -1;
-            f[x] = 0.f;
-            if (at[x] >= 0) {
-                const float2 ml = (k < slots ? a.ml_p : a.ml_s)[at[x]];
-                f[x] = ml.x == -INFINITY ? 0.f : ex2_mufu(ml.x - M[x]);
-                L[x] += f[x] * ml.y;
-            }
+            f[x] = ml[x].x == -INFINITY ? 0.f : ex2_mufu(ml[x].x - M[x]);
+            L[x] += f[x] * ml[x].y;
         }
         const int cnt = min(32, all - k0);
-#pragma unroll 2
-        for (int k = kHeads ? 0 : warp; k < cnt; k += kHeads ? 1 : 8) {
-            float fk[H], v[H][E];
+#pragma unroll 4
+        for (int k = kSplit ? warp : 0; k < cnt; k += kSplit ? 8 : 1) {
+            const long long row = __shfl_sync(0xffffffffu, at, k);
+            if (row < 0) continue;
+            const float* src = (k0 + k < slots ? a.o_p : a.o_s) + row * D + lane * E;
 #pragma unroll
             for (int x = 0; x < H; ++x) {
-                fk[x] = __shfl_sync(0xffffffffu, f[x], k);
-                const long long row = __shfl_sync(0xffffffffu, at[x], k);
+                const float fk = __shfl_sync(0xffffffffu, f[x], k);
+                float v[E];
+                if constexpr (E == 2) {
+                    const float2 q = *reinterpret_cast<const float2*>(src + x * D);
+                    v[0] = q.x;
+                    v[1] = q.y;
+                } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[x][e] = 0.f;
-                if (row >= 0) {
-                    const float* src = (k0 + k < slots ? a.o_p : a.o_s) + row * D + lane * E;
-                    if constexpr (E == 2) {
-                        const float2 q = *reinterpret_cast<const float2*>(src);
-                        v[x][0] = q.x;
-                        v[x][1] = q.y;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < E; e += 4) {
-                            const float4 q = *reinterpret_cast<const float4*>(src + e);
-                            v[x][e] = q.x;
-                            v[x][e + 1] = q.y;
-                            v[x][e + 2] = q.z;
-                            v[x][e + 3] = q.w;
-                        }
+                    for (int e = 0; e < E; e += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(src + x * D + e);
+                        v[e] = q.x;
+                        v[e + 1] = q.y;
+                        v[e + 2] = q.z;
+                        v[e + 3] = q.w;
                     }
                 }
+                // A segment in which the row saw no key has weight 0 and holds
+                // whatever its idle accumulator held.
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[x][e] = fk > 0.f ? fmaf(fk, v[e], acc[x][e]) : acc[x][e];
             }
-            // A segment in which the row saw no key has weight 0 and holds
-            // whatever its idle accumulator held.
-#pragma unroll
-            for (int x = 0; x < H; ++x)
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[x][e] = fk[x] > 0.f ? fmaf(fk[x], v[x][e], acc[x][e]) : acc[x][e];
         }
     }
 #pragma unroll
-    for (int x = 0; x < H; ++x) {
+    for (int x = 0; x < H; ++x)
         for (int o = 16; o; o >>= 1) L[x] += __shfl_xor_sync(0xffffffffu, L[x], o);
-        if constexpr (kHeads == 0) {
+    if constexpr (kSplit) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[x][e];
-            __syncthreads();
-            if (warp) return;
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[0][e];
+        __syncthreads();
+        if (warp) return;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                for (int y = 1; y < 8; ++y) acc[x][e] += s_o[y][lane * E + e];
-        }
-        const int head = h0 + x;
-        if (head >= a.Hq) return;
+        for (int e = 0; e < E; ++e)
+            for (int y = 1; y < 8; ++y) acc[0][e] += s_o[y][lane * E + e];
+    }
+#pragma unroll
+    for (int x = 0; x < H; ++x) {
         const float inv = L[x] > 0.f ? 1.f / L[x] : 0.f;
         uint32_t out[E / 2];
 #pragma unroll
         for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[x][e] * inv, acc[x][e + 1] * inv);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + head) * D) + lane * (E / 2);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + h0 + x) * D) + lane * (E / 2);
         if constexpr (E == 2) *dst = out[0];
         else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
         else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (lane == 0) a.lse[(long long)head * a.T + t] = L[x] > 0.f ? (M[x] + __log2f(L[x])) * 0.69314718055994531f : -INFINITY;
+        if (lane == 0) a.lse[(long long)(h0 + x) * a.T + t] = L[x] > 0.f ? (M[x] + __log2f(L[x])) * 0.69314718055994531f : -INFINITY;
     }
 }
 
@@ -1398,10 +1390,10 @@ bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintpt
 
 struct PfLayout {
     int tq, tb, rows_p, rows_s;
-    size_t pref, items, cu, len, owner, o_p, ml_p, o_s, ml_s, total;
+    size_t rows, o_p, ml_p, o_s, ml_s, total;
 };
 
-// Workspace: header, tables, the segments' rows.  The prefix's items are row
+// Workspace: header, what the rows are, the segments' rows.  The prefix's items are row
 // blocks times chunks of a worker's share of tiles, so at most row blocks plus
 // workers; the requests' at most T / tb + min(T, B) a key/value head.  Segments:
 // items plus workers (eight a CTA with few rows, else two at most).
@@ -1413,12 +1405,8 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
     const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + (size_t)(T * (long long)G <= few_limit(d) ? 8 : 4) * sms;
     const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + (size_t)(max_seqlen * (long long)G <= few_limit(d) ? 8 : 2) * sms;
-    w.pref = align256(sizeof(PfHeader));
-    w.items = align256(w.pref + (size_t)(B + 1) * 4);
-    w.cu = align256(w.items + (size_t)(B + 1) * 4);
-    w.len = align256(w.cu + (size_t)(B + 1) * 4);
-    w.owner = align256(w.len + (size_t)B * 4);
-    w.ml_p = align256(w.owner + (size_t)T * 4);
+    w.rows = align256(sizeof(PfHeader));
+    w.ml_p = align256(w.rows + (size_t)T * sizeof(PfRow));
     w.ml_s = align256(w.ml_p + seg_p * w.rows_p * 8);
     w.o_p = align256(w.ml_s + seg_s * w.rows_s * 8);
     w.o_s = align256(w.o_p + seg_p * w.rows_p * d * 4);
@@ -1436,12 +1424,14 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
     if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
-    // Rows (of one head): up to 16 an SM a block each; up to some waves of warps
-    // a warp each; past that four heads a warp.
+    // Rows (of one head): up to two an SM a block each; up to 64 an SM (one or
+    // two rounds of warps) a warp each; past that four or two a warp.
+    auto warps = [&](int heads) { return (int)(((long long)a.T * (a.Hq / heads) + 7) / 8); };
     cudaError_t e;
-    if (rows <= 16LL * sms) e = launch_dependent(prefix_join_kernel<D, 0>, (int)rows, 256, 0, stream, a);
-    else if (rows <= 256LL * sms) e = launch_dependent(prefix_join_kernel<D, 1>, (int)((rows + 7) / 8), 256, 0, stream, a);
-    else e = launch_dependent(prefix_join_kernel<D, 4>, (int)(((long long)a.T * ((a.Hq + 3) / 4) + 7) / 8), 256, 0, stream, a);
+    if (rows <= 2LL * sms) e = launch_dependent(prefix_join_kernel<D, 1, true>, (int)rows, 256, 0, stream, a);
+    else if (rows <= 64LL * sms || a.G % 2) e = launch_dependent(prefix_join_kernel<D, 1, false>, warps(1), 256, 0, stream, a);
+    else if (a.G % 4) e = launch_dependent(prefix_join_kernel<D, 2, false>, warps(2), 256, 0, stream, a);
+    else e = launch_dependent(prefix_join_kernel<D, 4, false>, warps(4), 256, 0, stream, a);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -1513,11 +1503,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.q_stride = q_stride;
     a.status = status;
     a.hdr = reinterpret_cast<PfHeader*>(ws);
-    a.ws.pref = reinterpret_cast<int*>(ws + w.pref);
-    a.ws.items = reinterpret_cast<int*>(ws + w.items);
-    a.ws.cu = reinterpret_cast<int*>(ws + w.cu);
-    a.ws.len = reinterpret_cast<int*>(ws + w.len);
-    a.ws.owner = reinterpret_cast<int*>(ws + w.owner);
+    a.rows = reinterpret_cast<PfRow*>(ws + w.rows);
     a.o_p = reinterpret_cast<float*>(ws + w.o_p);
     a.o_s = reinterpret_cast<float*>(ws + w.o_s);
     a.ml_p = reinterpret_cast<float2*>(ws + w.ml_p);
