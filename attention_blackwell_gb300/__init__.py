@@ -253,8 +253,9 @@ def bwd(q, k, v, o, lse, do, causal=False, alpha=None, cu_seqlens=None, max_seql
 
 
 # A serving step is a few short kernels, so what a call costs on the host counts:
-# checks are single expressions that hand over to _need for the message, and
-# pointers and the stream go to ctypes as plain integers.
+# one expression checks all tensors of a kind and hands over to _need for the
+# message, pointers and the stream go to ctypes as plain integers, and only a
+# call for another device or stream goes through _elsewhere.
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
@@ -266,47 +267,36 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):
     _current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _dense(t, name, dtype):
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _need(t, name, dtype)
+def _elsewhere(stream, tensors, call):
+    """call() with the tensors' device current and, on it, the given stream or
+    that device's current one, which is then where call() allocates.  Tensors
+    that the caching allocator holds for another stream are marked as used on
+    this one."""
+    tensors = [t for t in tensors if t is not None]
+    dev = tensors[0].get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call()
+        if stream.device.index != dev:
+            raise ValueError("the stream must be on the tensors' device")
+        if stream != torch.cuda.current_stream():
+            for t in tensors:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return call()
 
 
-class _On:
-    """Device and stream of a serving call: its tensors' device, the given
-    stream or that device's current one, and on it whatever the call
-    allocates.  Tensors that the caching allocator holds for another stream
-    are marked as used on this one."""
+def _one_device(dev, tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].get_device()
-        for t in tensors:
-            if t is not None and t.get_device() != dev:
-                raise ValueError("all tensors must be on one device")
-        self.guards = ()
-        if stream is None and dev == _current_device():
-            self.raw = _current_raw_stream(dev)
-            return
-        guards = [torch.cuda.device(dev)]
-        if stream is not None:
-            if stream.device.index != dev:
-                raise ValueError("the stream must be on the tensors' device")
-            if stream != torch.cuda.current_stream(dev):
-                for t in tensors:
-                    if t is not None:
-                        t.record_stream(stream)
-                guards.append(torch.cuda.stream(stream))
-        self.guards = guards
-        self.raw = stream.cuda_stream if stream is not None else _current_raw_stream(dev)
 
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return self.raw
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-        return False
+def _all_int32(**tensors):
+    for n, t in tensors.items():
+        _need(t, n, torch.int32)
 
 
 def _rows(t, name):
@@ -326,8 +316,10 @@ def _rows(t, name):
 
 
 def _pages(k_pages, v_pages):
-    _dense(k_pages, "k_pages", torch.bfloat16)
-    _dense(v_pages, "v_pages", torch.bfloat16)
+    if (k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16 or not k_pages.is_cuda
+            or not k_pages.is_contiguous() or not v_pages.is_contiguous()):
+        _need(k_pages, "k_pages", torch.bfloat16)
+        _need(v_pages, "v_pages", torch.bfloat16)
     if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d]")
     return k_pages.shape
@@ -352,38 +344,43 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
     slots int32 [num_slots] (-1: none), pool_out int64 [3], another tensor than
     pool.  num_slots is needed when slots is not given.
     """
-    i32 = torch.int32
-    _dense(ctx_lens, "ctx_lens", i32)
-    _dense(new_lens, "new_lens", i32)
-    _dense(block_table, "block_table", i32)
-    _dense(ring, "ring", i32)
-    _dense(pool, "pool", torch.int64)
+    dev, i32 = ctx_lens.get_device(), torch.int32
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (ctx_lens, new_lens, block_table, ring, pool, cu_new, kv_lens, slots, pool_out),
+                          lambda: page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots, cu_new,
+                                            kv_lens, slots, pool_out))
     B = ctx_lens.numel()
+    if slots is None:
+        if num_slots is None:
+            raise ValueError("page_plan needs num_slots or slots")
+        slots = torch.empty(num_slots, dtype=i32, device=ctx_lens.device)
+    if cu_new is None:
+        cu_new = torch.empty(B + 1, dtype=i32, device=ctx_lens.device)
+    if kv_lens is None:
+        kv_lens = torch.empty(B, dtype=i32, device=ctx_lens.device)
+    if pool_out is None:
+        pool_out = torch.empty(3, dtype=torch.int64, device=ctx_lens.device)
+    if (ctx_lens.dtype is not i32 or new_lens.dtype is not i32 or block_table.dtype is not i32 or ring.dtype is not i32
+            or cu_new.dtype is not i32 or kv_lens.dtype is not i32 or slots.dtype is not i32
+            or pool.dtype is not torch.int64 or pool_out.dtype is not torch.int64
+            or not ctx_lens.is_contiguous() or not new_lens.is_contiguous() or not block_table.is_contiguous()
+            or not ring.is_contiguous() or not cu_new.is_contiguous() or not kv_lens.is_contiguous()
+            or not slots.is_contiguous() or not pool.is_contiguous() or not pool_out.is_contiguous()):
+        _all_int32(ctx_lens=ctx_lens, new_lens=new_lens, block_table=block_table, ring=ring, cu_new=cu_new,
+                   kv_lens=kv_lens, slots=slots)
+        _need(pool, "pool", torch.int64)
+        _need(pool_out, "pool_out", torch.int64)
+    if not (new_lens.get_device() == block_table.get_device() == ring.get_device() == pool.get_device()
+            == cu_new.get_device() == kv_lens.get_device() == slots.get_device() == pool_out.get_device() == dev):
+        raise ValueError("all tensors must be on one device")
     if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("ctx_lens, new_lens and block_table must have one entry or row a request")
-    if pool.numel() != 3:
-        raise ValueError("pool must have 3 elements")
-    if slots is None and num_slots is None:
-        raise ValueError("page_plan needs num_slots or slots")
-    with _On(stream, ctx_lens, new_lens, block_table, ring, pool, cu_new, kv_lens, slots, pool_out) as raw:
-        dev = ctx_lens.device
-        if cu_new is None:
-            cu_new = torch.empty(B + 1, dtype=i32, device=dev)
-        if kv_lens is None:
-            kv_lens = torch.empty(B, dtype=i32, device=dev)
-        if slots is None:
-            slots = torch.empty(num_slots, dtype=i32, device=dev)
-        if pool_out is None:
-            pool_out = torch.empty(3, dtype=torch.int64, device=dev)
-        _dense(cu_new, "cu_new", i32)
-        _dense(kv_lens, "kv_lens", i32)
-        _dense(slots, "slots", i32)
-        _dense(pool_out, "pool_out", torch.int64)
-        if cu_new.numel() != B + 1 or kv_lens.numel() != B or pool_out.numel() != 3:
-            raise ValueError("cu_new, kv_lens and pool_out must have B + 1, B and 3 elements")
-        rc = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), block_table.data_ptr(),
-                                block_table.shape[1], ring.data_ptr(), ring.numel(), pool.data_ptr(), pool_out.data_ptr(),
-                                cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), slots.numel(), raw)
+    if pool.numel() != 3 or cu_new.numel() != B + 1 or kv_lens.numel() != B or pool_out.numel() != 3:
+        raise ValueError("pool and pool_out must have 3 elements, cu_new B + 1 and kv_lens B")
+    rc = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), block_table.data_ptr(),
+                            block_table.shape[1], ring.data_ptr(), ring.numel(), pool.data_ptr(), pool_out.data_ptr(),
+                            cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), slots.numel(),
+                            _current_raw_stream(dev))
     _check(rc, "fa_page_plan")
     return cu_new, kv_lens, slots, pool_out
 
@@ -391,9 +388,15 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
 def kv_store(k, v, slots, k_pages, v_pages, stream=None):
     """Write rows of k and v ([T, Hkv, d] bf16, tokens may be strided) into the
     cache at slots (int32 [T]; negative: skipped).  Returns (k_pages, v_pages)."""
+    dev = k_pages.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (k_pages, v_pages, k, v, slots), lambda: kv_store(k, v, slots, k_pages, v_pages))
     P, Hkv, page, d = _pages(k_pages, v_pages)
     ks, vs = _rows(k, "k"), _rows(v, "v")
-    _dense(slots, "slots", torch.int32)
+    if slots.dtype is not torch.int32 or not slots.is_contiguous():
+        _need(slots, "slots", torch.int32)
+    if not (v_pages.get_device() == k.get_device() == v.get_device() == slots.get_device() == dev):
+        raise ValueError("all tensors must be on one device")
     T = k.shape[0]
     if k.shape != (T, Hkv, d) or k.shape != v.shape:
         raise ValueError("k and v must be [T, Hkv, d] with the pages' Hkv and d")
@@ -401,9 +404,8 @@ def kv_store(k, v, slots, k_pages, v_pages, stream=None):
         raise ValueError("slots must have one element a token")
     if T == 0:
         return k_pages, v_pages
-    with _On(stream, k, v, slots, k_pages, v_pages) as raw:
-        rc = lib().fa_kv_store(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
-                               v_pages.data_ptr(), P, page, raw)
+    rc = lib().fa_kv_store(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
+                           v_pages.data_ptr(), P, page, _current_raw_stream(dev))
     _check(rc, "fa_kv_store")
     return k_pages, v_pages
 
@@ -430,10 +432,16 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     o [T, Hq, d], lse float32 [Hq, T].  Without cu_seqlens (int32 [B+1]) every
     request has one row; with it max_seqlen bounds a request's rows.
     """
+    dev, i32 = q.get_device(), torch.int32
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, prefix_table, out, lse, workspace),
+                          lambda: prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, max_seqlen,
+                                             prefix_table, prefix_len, alpha, out, lse, workspace))
     P, Hkv, page, d = _pages(k_pages, v_pages)
     qs = _rows(q, "q")
-    _dense(block_table, "block_table", torch.int32)
-    _dense(kv_lens, "kv_lens", torch.int32)
+    if (block_table.dtype is not i32 or kv_lens.dtype is not i32 or not block_table.is_contiguous()
+            or not kv_lens.is_contiguous()):
+        _all_int32(block_table=block_table, kv_lens=kv_lens)
     T, Hq, dq = q.shape
     B = kv_lens.numel()
     if dq != d:
@@ -441,7 +449,8 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, W] with kv_lens' B")
     if cu_seqlens is not None:
-        _dense(cu_seqlens, "cu_seqlens", torch.int32)
+        if cu_seqlens.dtype is not i32 or not cu_seqlens.is_contiguous():
+            _all_int32(cu_seqlens=cu_seqlens)
         if cu_seqlens.numel() != B + 1:
             raise ValueError("cu_seqlens must have B + 1 elements")
         if max_seqlen is None:
@@ -454,31 +463,38 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     if prefix_len > 0:
         if prefix_table is None:
             raise ValueError("prefix_len needs prefix_table")
-        _dense(prefix_table, "prefix_table", torch.int32)
+        if prefix_table.dtype is not i32 or not prefix_table.is_contiguous():
+            _all_int32(prefix_table=prefix_table)
         if prefix_table.numel() * page < prefix_len:
             raise ValueError("prefix_table is too short for prefix_len")
     else:
         prefix_table = None
     if alpha is None:
         alpha = 1.0 / (d ** 0.5)
-    with _On(stream, q, k_pages, v_pages, block_table, kv_lens, cu_seqlens, prefix_table, out, lse, workspace) as raw:
-        if out is None:
-            out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
-        if lse is None:
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
-        _dense(out, "out", torch.bfloat16)
-        _dense(lse, "lse", torch.float32)
-        if out.shape != (T, Hq, d) or lse.shape != (Hq, T):
-            raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
-        if T == 0:
-            return out, lse
-        if workspace is None:
-            workspace = prefix_workspace(B, Hq, Hkv, T, max_seqlen, d, device=q.device)
-        rc = lib().fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                 T, B, Hq, Hkv, d, float(alpha), P, page, block_table.data_ptr(), block_table.shape[1],
-                                 kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
-                                 int(max_seqlen), prefix_table.data_ptr() if prefix_table is not None else None,
-                                 prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if (out.dtype is not torch.bfloat16 or lse.dtype is not torch.float32 or not out.is_contiguous()
+            or not lse.is_contiguous()):
+        _need(out, "out", torch.bfloat16)
+        _need(lse, "lse", torch.float32)
+    if out.shape != (T, Hq, d) or lse.shape != (Hq, T):
+        raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
+    if T == 0:
+        return out, lse
+    if workspace is None:
+        workspace = prefix_workspace(B, Hq, Hkv, T, max_seqlen, d, device=q.device)
+    if not (k_pages.get_device() == v_pages.get_device() == block_table.get_device() == kv_lens.get_device()
+            == out.get_device() == lse.get_device() == workspace.get_device() == dev):
+        raise ValueError("all tensors must be on one device")
+    _one_device(dev, (cu_seqlens, prefix_table))
+    rc = lib().fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                             T, B, Hq, Hkv, d, alpha, P, page, block_table.data_ptr(), block_table.shape[1],
+                             kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
+                             int(max_seqlen), prefix_table.data_ptr() if prefix_table is not None else None,
+                             prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                             _current_raw_stream(dev))
     _check(rc, "fa_prefix_fwd")
     return out, lse
 

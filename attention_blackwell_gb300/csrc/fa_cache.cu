@@ -125,26 +125,52 @@ __global__ void __launch_bounds__(1024) page_plan_kernel(const PlanArgs a) {
         return a.ring[at];
     };
     const int stride = gridDim.x * blockDim.x, first = blockIdx.x * blockDim.x + tid;
-    // Slots.
-    for (long long t = first; t < a.num_slots; t += stride) {
-        int slot = -1;
-        if (t < s_cu[a.B]) {
-            const int b = find_request(s_cu, a.B, (int)t);
-            const long long pos = (long long)s_ctx[b] + (t - s_cu[b]);
-            const long long col = pos >> sh;
-            if (col < W) {
-                const int hb = (int)(((long long)s_ctx[b] + up) >> sh);
-                int page;
-                if (col < hb) {
-                    page = a.table[(long long)b * W + col];
-                } else {
-                    const int idx = s_in[b] + (int)col - hb;
-                    page = idx < avail ? ring_at(idx) : -1;
+    // Slots.  A row a thread while there are threads enough (single tokens: each
+    // row is another request, and its lookups should not queue behind others');
+    // else four rows at a time: one search, then requests and pages as they come
+    // (a page is looked up once for the rows that lie in it).  Measured for 560000
+    // rows of 128 prompts: 12.5 us a row at a time, 8 by fours; for 1000 single
+    // tokens 10.4 us a row at a time, 12.9 by fours.
+    const int per = a.num_slots <= stride ? 1 : 4;
+    const bool wide = per == 4 && (reinterpret_cast<uintptr_t>(a.slots) & 15u) == 0;
+    const int rows = s_cu[a.B];
+    for (long long t0 = (long long)per * first; t0 < a.num_slots; t0 += (long long)per * stride) {
+        int out[4] = {-1, -1, -1, -1};
+        if (t0 < rows) {
+            int b = find_request(s_cu, a.B, (int)t0), page = -1;
+            long long at = -1;      // the column (of request b) that `page` is
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = (int)t0 + e;
+                if (e >= per || t >= rows) continue;
+                while (t >= s_cu[b + 1]) {
+                    ++b;
+                    at = -1;
                 }
-                if (page >= 0 && page < P) slot = (page << sh) + (int)(pos & up);
+                const long long pos = (long long)s_ctx[b] + (t - s_cu[b]), col = pos >> sh;
+                if (col >= W) continue;
+                if (col != at) {
+                    at = col;
+                    const int hb = (int)(((long long)s_ctx[b] + up) >> sh);
+                    if (col < hb) {
+                        page = a.table[(long long)b * W + col];
+                        if (page >= P) page = -1;
+                    } else {
+                        const int idx = s_in[b] + (int)col - hb;
+                        page = idx < avail ? ring_at(idx) : -1;
+                        if (page >= P) page = -1;
+                    }
+                }
+                if (page >= 0) out[e] = (page << sh) + (int)(pos & up);
             }
         }
-        a.slots[t] = slot;
+        if (wide && t0 + 4 <= a.num_slots) {
+            *reinterpret_cast<int4*>(a.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < per && t0 + e < a.num_slots) a.slots[t0 + e] = out[e];
+        }
     }
     // Pages handed out.
     for (long long i = first; i < total_in; i += stride) {
@@ -252,10 +278,14 @@ int fa_page_plan(const int* ctx_lens, const int* new_lens, int B, int page_size,
     a.num_slots = num_slots;
     a.ps_log2 = lg;
     const int threads = B <= 256 ? 256 : (B + 31) / 32 * 32;
-    long long grid = ((long long)num_slots + 4 * threads - 1) / (4 * threads);
-    const long long pages = ((long long)B * table_width + 32LL * threads - 1) / (32LL * threads);
+    // Blocks: a slot a thread, four past a block an SM, or 32 entries of the table that pages may go
+    // to or come from; at most what the SMs hold at a time, since every block
+    // scans all requests first.
+    const int each = num_slots <= sms * threads ? threads : 4 * threads;
+    long long grid = ((long long)num_slots + each - 1) / each;
+    const long long pages = ((long long)B * table_width + 32LL * threads - 1) / (32LL * threads), most = sms * (2048LL / threads);
     grid = grid > pages ? grid : pages;
-    grid = grid < 1 ? 1 : (grid > sms ? sms : grid);
+    grid = grid < 1 ? 1 : (grid > most ? most : grid);
     return launch_dependent(page_plan_kernel, (int)grid, threads, 0, stream, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

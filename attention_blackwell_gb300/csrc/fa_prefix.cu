@@ -45,6 +45,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/fa.h"
 #include "fa_internal.h"
 
@@ -754,12 +756,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         }
         if (tid == 0) sh.abort_flag = 0;
     }
-    if (warp == kSoftWarps && lane == 0) {
-        tma_prefetch_desc(&tq_p);
-        tma_prefetch_desc(&tq_s);
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
-    }
     if (warp == kSoftWarps + 3) {
         tmem_alloc(&sh.tmem_base, 512);
         tmem_relinquish();
@@ -1421,7 +1417,15 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4;
     static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
     auto kern = prefix_kernel<D>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
+    // Once a device: the most that any batch needs.
+    static std::atomic<uint64_t> prepared{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
+    if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
+        constexpr int most = 1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return FA_ERR_LAUNCH;
+        prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
     if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to two an SM a block each; up to 64 an SM (one or
@@ -1540,18 +1544,24 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.qstep_s = (box_s * G + 7) & ~7;
     a.scale_log2 = alpha * 1.4426950408889634f;
 
-    CUtensorMap tq_p, tq_s, tk, tv, tk_few, tv_few;
-    int rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
-    if (rc == FA_OK) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
+    CUtensorMap tq_p = {}, tq_s = {}, tk = {}, tv = {}, tk_few = {}, tv_few = {};
+    // Only the maps that a mode of this call uses are encoded (each costs the
+    // host a third of a microsecond).
+    const bool prefix_tiles = prefix_len > 0 && mode_p != kFew, own_tiles = mode_s != kFew;
     const long long slots = (long long)num_pages * Hkv * page_size;
     const int part = page_size < kN ? page_size : kN;
-    if (rc == FA_OK) rc = make_map_pages(&tk, k_pages, d, slots, part);
-    if (rc == FA_OK) rc = make_map_pages(&tv, v_pages, d, slots, part);
-    // Few rows: 16 keys a copy whatever the page size, all of d at once (a copy
-    // of 2 KB an instruction keeps an SM at 28 B a cycle, a third below what 60
-    // SMs need for HBM's rate).
-    if (rc == FA_OK) rc = make_map_steps(&tk_few, k_pages, d, slots);
-    if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
+    int rc = FA_OK;
+    if (prefix_tiles) rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
+    if (rc == FA_OK && own_tiles) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
+    if (rc == FA_OK && (prefix_tiles || own_tiles)) {
+        rc = make_map_pages(&tk, k_pages, d, slots, part);
+        if (rc == FA_OK) rc = make_map_pages(&tv, v_pages, d, slots, part);
+    }
+    // Few rows: 16 keys a copy whatever the page size, all of d at once.
+    if (rc == FA_OK && (!prefix_tiles || !own_tiles)) {
+        rc = make_map_steps(&tk_few, k_pages, d, slots);
+        if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
+    }
     if (rc != FA_OK) return rc;
     if (d == 64) return launch_prefix<64>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
     if (d == 128) return launch_prefix<128>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
