@@ -151,7 +151,7 @@ struct Desc {
     int flags;              // kMore (not the list's end), kFirst, kLast of its item's tiles here
     int j, nkeys, lim0, hk, tok0, ntok, seg;
 };
-constexpr int kMore = 1, kFirst = 2, kLast = 4;
+constexpr int kMore = 1, kFirst = 2, kLast = 4, kRagged = 8;   // kRagged: some of its V rows hold no key of the list
 constexpr int kDesc = 8;    // tiles the walkers run ahead by
 constexpr int kQMax = 8;    // Q slots
 
@@ -277,7 +277,7 @@ struct Walk {
 struct PfShared {
     Desc desc[2][kDesc];
     // One arrival a phase.
-    uint64_t d_full[2][kDesc], d_empty[2][kDesc], q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], pv_done[2], o_done[2], drain;
+    uint64_t d_full[2][kDesc], d_empty[2][kDesc], q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], pv_done[2], o_done[2], drain[2];
     // Four: the warps of a softmax warpgroup.
     uint64_t p_ready[2];
     // One again: few rows, each warp's slots.
@@ -895,7 +895,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 for (uint32_t i = n_item[x] > qn ? n_item[x] - qn : 0; i < n_item[x]; ++i)
                     while (!mbar_try_wait(smem_u32(&sh.q_full[q_slot(x, i)]), (i / qn) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
-        } else if (warp == kSoftWarps + 1) {
+        } else if (warp == kSoftWarps + 1 || (kStreams == 1 && warp == kSoftWarps + 3)) {
             // ------------------------------------------------------- UMMA issuer
             uint32_t n_ring = 0;
             bool ok = true;
@@ -910,7 +910,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // Zeroes the V rows of a tile that hold no key of the list.
             auto clean = [&](uint32_t slot, const Desc& d) {
                 const int rows = d.nkeys - d.j * kN, live = d.live;
-                if (rows >= kN && live == (1 << parts) - 1) return;
                 for (int i = 0; i < parts; ++i) {
                     const int r0 = i << part_log2, r1 = r0 + (1 << part_log2);
                     const int from = (live >> i) & 1 ? max(r0, min(r1, rows)) : r0;
@@ -950,7 +949,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const int ahead = sh.desc[0][(n + 1) % kDesc].flags;
                         if (!(ok = take(vs))) break;
                         if ((ahead & kMore) && !(ok = take(ks))) break;
-                        clean(vs, d);
+                        if (flags & kRagged) clean(vs, d);
                         for (int x = 0; x < 2; ++x) {
                             if (!(ok = mbar_wait_w(&sh.p_ready[x], n & 1, wc, kPfP))) break;
                             tc_fence_after();
@@ -967,6 +966,52 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         }
                         free_desc(0, n);
                         flags = ahead;
+                    }
+                }
+            } else if constexpr (kStreams == 1) {
+                // One worker, S double-buffered: S and P V have an issuer each.
+                // Issuing blocks while the tensor core is busy, and one issuer's
+                // waits would stand between the products of every tile (2540
+                // cycles a tile with one issuer, 1280 of them products).  The
+                // ring's order: K0, K1, V0, K2, V1, K3, ..., the last V behind the
+                // one before.
+                auto wait_tile = [&](uint32_t i) { return mbar_wait_w(&sh.full[i % kRing], (i / kRing) & 1, wc, kPfRingFull); };
+                if (warp == kSoftWarps + 3) {
+                    uint32_t items = 0;
+                    for (uint32_t n = 0;; ++n) {
+                        if (!(ok = desc_wait(0, n))) break;
+                        const int flags = sh.desc[0][n % kDesc].flags, buf = n & 1;
+                        if (!(flags & kMore)) break;
+                        const uint32_t i = n < 2 ? n : 2 * n - 1;
+                        if ((flags & kFirst) && !(ok = mbar_wait_w(&sh.q_full[q_slot(0, items)], (items / qn) & 1, wc, kPfQFull))) break;
+                        items += flags & kFirst ? 1 : 0;
+                        if (!(ok = wait_tile(i))) break;
+                        // S goes where P of two tiles before was read from.
+                        if (n >= 2 && !(ok = mbar_wait_w(&sh.pv_done[buf], ((n - 2) >> 1) & 1, wc, kPfPV))) break;
+                        tc_fence_after();
+                        pf_issue_qk<D>(col_s(buf), q_addr(0, items - 1), sRing + i % kRing * G::kTile);
+                        umma_commit_w(&sh.s_full[buf]);
+                        umma_commit_w(&sh.empty[i % kRing]);
+                        if (flags & kLast) umma_commit_w(&sh.q_empty[q_slot(0, items - 1)]);
+                    }
+                } else {
+                    if ((ok = desc_wait(0, 0))) {
+                        int flags = sh.desc[0][0].flags;
+                        for (uint32_t n = 0; flags & kMore; ++n) {
+                            if (!(ok = desc_wait(0, n + 1))) break;
+                            const int ahead = sh.desc[0][(n + 1) % kDesc].flags, buf = n & 1;
+                            const uint32_t i = ahead & kMore ? 2 * n + 2 : 2 * n + 1;
+                            if (!(ok = wait_tile(i))) break;
+                            if (flags & kRagged) clean(i % kRing, sh.desc[0][n % kDesc]);
+                            if (!(ok = mbar_wait_w(&sh.p_ready[buf], (n >> 1) & 1, wc, kPfP))) break;
+                            tc_fence_after();
+                            pf_issue_pv<D>(tmem, col_s(buf), sRing + i % kRing * G::kTile, !(flags & kFirst));
+                            umma_commit_w(&sh.pv_done[buf]);
+                            umma_commit_w(&sh.empty[i % kRing]);
+                            if (flags & kLast) umma_commit_w(&sh.o_done[0]);
+                            free_desc(0, n);
+                            flags = ahead;
+                        }
                     }
                 }
             } else {
@@ -989,18 +1034,16 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const uint32_t i = n_item[x]++;
                         if (!mbar_wait_w(&sh.q_full[q_slot(x, i)], (i / qn) & 1, wc, kPfQFull)) return false;
                     }
-                    const int buf = kStreams == 2 ? x : n_s[x] & 1;
-                    pf_issue_qk<D>(col_s(buf), q_addr(x, n_item[x] - 1), sRing + ks * G::kTile);
-                    umma_commit_w(&sh.s_full[buf]);
+                    pf_issue_qk<D>(col_s(x), q_addr(x, n_item[x] - 1), sRing + ks * G::kTile);
+                    umma_commit_w(&sh.s_full[x]);
                     umma_commit_w(&sh.empty[ks]);
                     if (flags_s & kLast) umma_commit_w(&sh.q_empty[q_slot(x, n_item[x] - 1)]);
                     ++n_s[x];
                     return true;
                 };
-                for (int i = 0; i < G::kLook && ok; ++i)
 #pragma unroll
-                    for (int x = 0; x < kStreams; ++x)
-                        if (ok && !ended[x]) ok = take_k(x) && (!flags_s || issue_s(x));
+                for (int x = 0; x < kStreams; ++x)
+                    if (ok && !ended[x]) ok = take_k(x) && (!flags_s || issue_s(x));
                 bool any = true;
                 while (ok && any) {
                     any = false;
@@ -1010,18 +1053,17 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         any = true;
                         const uint32_t n = n_p[x];
                         const Desc& d = sh.desc[x][n % kDesc];
-                        const int flags = d.flags, buf = kStreams == 2 ? x : n & 1;
+                        const int flags = d.flags;
                         uint32_t vs;
                         if (!(ok = take(vs))) break;
-                        clean(vs, d);
+                        if (flags & kRagged) clean(vs, d);
                         // Both tiles are waited for before P, so that S follows P V
                         // into the tensor core without a pause.
                         if (!(ok = take_k(x))) break;
-                        if (!(ok = mbar_wait_w(&sh.p_ready[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfP))) break;
+                        if (!(ok = mbar_wait_w(&sh.p_ready[x], n & 1, wc, kPfP))) break;
                         tc_fence_after();
-                        pf_issue_pv<D>(tmem + x * G::kColO1, col_s(buf), sRing + vs * G::kTile, !(flags & kFirst));
+                        pf_issue_pv<D>(tmem + x * G::kColO1, col_s(x), sRing + vs * G::kTile, !(flags & kFirst));
                         umma_commit_w(&sh.empty[vs]);
-                        if (kStreams == 1) umma_commit_w(&sh.pv_done[buf]);
                         if (flags & kLast) umma_commit_w(&sh.o_done[x]);
                         if (flags_s && !(ok = issue_s(x))) break;
                         free_desc(x, n);
@@ -1030,9 +1072,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 }
             }
             // All products complete before tensor memory is freed.
-            umma_commit_w(&sh.drain);
+            uint64_t* drain = &sh.drain[warp == kSoftWarps + 1 ? 0 : 1];
+            umma_commit_w(drain);
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+            while (!mbar_try_wait(smem_u32(drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
             __syncwarp();
         } else if (warp - (kSoftWarps + 2) < workers) {
             // ------------------------------------------------------ list walkers
@@ -1069,8 +1112,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                     const uint32_t live = __ballot_sync(0xffffffffu, val >= 0);
                     if (q == jj - j) d.page[part] = val;
                     if (lane == 0) {
-                        d.live = (live >> (8 * (jj - j))) & 0xff;
-                        d.flags = more ? kMore | (jj == it.j0 ? kFirst : 0) | (jj == it.j1 - 1 ? kLast : 0) : 0;
+                        const int bits = (live >> (8 * (jj - j))) & 0xff;
+                        d.flags = more ? kMore | (jj == it.j0 ? kFirst : 0) | (jj == it.j1 - 1 ? kLast : 0) |
+                                         ((jj + 1) * kN > it.nkeys || bits != (1 << parts) - 1 ? kRagged : 0) : 0;
+                        d.live = bits;
                         d.j = jj;
                         d.nkeys = it.nkeys;
                         d.lim0 = it.lim0;
