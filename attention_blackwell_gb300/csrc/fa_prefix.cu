@@ -72,15 +72,18 @@ template <int D> struct Pf {
     static constexpr int kThreads = 384;
     static constexpr int kFewParts = D == 256 ? 1 : 2;               // few rows: 16-key parts a step, slots of a step's K or V a warp
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
-    // Cycles a CTA takes for a unit, measured in the kernel on GB300; the CTAs
-    // are divided between the prefix and the requests' own keys by them.  kTwo
-    // alone: the prefix's tiles come from HBM for one row block only (`shared`:
-    // several row blocks read them, L2 serves the others), whose latency under
-    // the other CTAs' load then sets the pace.
-    __host__ __device__ static constexpr int cost(int mode, int halves, bool shared) {
-        return mode == kFew ? (D == 64 ? 600 : D == 128 ? 780 : 1900) * halves
-             : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2700)
-                            : (D == 64 ? (shared ? 3400 : 5500) : (shared ? 3700 : 6000));
+    // Cycles a CTA takes for a unit of the prefix and of the requests' own keys,
+    // measured in the kernel on GB300; the CTAs are divided between the two by
+    // them.  kTwo on the prefix: 3400 to 3700 when several row blocks share a
+    // tile (L2 serves all but the first), but alone each tile comes from HBM for
+    // 256 rows only, and its latency under the other CTAs' load sets the pace.
+    __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 600 : D == 128 ? 780 : 1900) * halves; }
+    __host__ __device__ static constexpr int cost_p(int mode, int halves, bool shared) {
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2700)
+             : D == 64 ? (shared ? 3400 : 6000) : (shared ? 3700 : 8000);
+    }
+    __host__ __device__ static constexpr int cost_s(int mode, int halves) {
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2350) : (D == 64 ? 3500 : 4000);
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
@@ -376,12 +379,21 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     __syncthreads();
     PfHeader h;
     const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
-    const float cp = (float)units_p * Pf<D>::cost(a.mode_p, a.halves_p, a.blocks_p > 1), cs = (float)units * Pf<D>::cost(a.mode_s, a.halves_s, true);
+    const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, a.blocks_p > 1), cs = (float)units * Pf<D>::cost_s(a.mode_s, a.halves_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
-    const int wp = np * a.width_p, ws = max(1, grid - np) * a.width_s;
-    h.n_p = np;
+    int wp = np * a.width_p;
     h.per_p = wp ? (units_p + wp - 1) / wp : 1;
+    // Chunks are a worker's share of tiles; a small rest would be a chunk of its
+    // own in every row block (62 tiles a worker of 256: 135 us for 100 rows of 32
+    // heads at d = 256, 64: 104), so it is spread over the others.
+    if (a.blocks_p > 1 && units > 0 && a.tiles_p > h.per_p && a.tiles_p % h.per_p < h.per_p / 4) {
+        const int k = a.tiles_p / h.per_p;
+        h.per_p = (a.tiles_p + k - 1) / k;
+        np = max(1, min(np, cdiv(units_p, h.per_p * a.width_p)));
+    }
+    const int ws = max(1, grid - np) * a.width_s;
+    h.n_p = np;
     h.per_s = units ? (units + ws - 1) / ws : 1;
     h.chunk = a.blocks_p > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
     h.chunks = (a.tiles_p + h.chunk - 1) / h.chunk;
