@@ -141,6 +141,30 @@ enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kP
 
 // ------------------------------------------------------------------ the list
 
+// The bounded wait of every pipeline here (2 s), by a whole warp.  It looks at
+// this CTA's flag alone, which takes the site that gave up, and the CTA reports it
+// as it ends: a failure that an earlier call left in the device's status word does
+// not stop this one.
+struct PfWait {
+    volatile int* abort_flag;   // shared
+};
+__device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, const PfWait& w, int site) {
+    const uint32_t a = smem_u32(bar);
+    bool ok = mbar_try_wait(a, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = 1; !(ok = mbar_try_wait(a, parity)); ++i) {
+            if (i & 63u) continue;
+            if (*w.abort_flag) break;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *w.abort_flag = site;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 struct Item {
     const int* tab;
     int hk, tok0, ntok, j0, j1, nkeys, lim0;
@@ -457,7 +481,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 
 template <int D>
 __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMap* tv, const PfArgs& a, const PfTables& t,
-                                         const PfHeader& hdr, PfShared& sh, uint32_t smem, const WaitCtx& wc, bool pre, int warp, int lane) {
+                                         const PfHeader& hdr, PfShared& sh, uint32_t smem, const PfWait& wc, bool pre, int warp, int lane) {
     using G = Pf<D>;
     constexpr int kKT = G::kFewParts, kKeys = 16 * kKT;              // 16-key parts and keys a step
     constexpr uint32_t kPart = D * 32u, kSlot = kPart * kKT;         // K or V of a part (D / 64 boxes of 16 x 128 B), of a step
@@ -556,7 +580,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
     };
 
     uint32_t n = 0, slot = 0, phase = 0;                             // slots read, the next one, its barrier's parity
-    auto wait = [&]() { return mbar_wait_w(&full[slot], phase, wc, kPfRingFull); };
+    auto wait = [&]() { return pf_wait(&full[slot], phase, wc, kPfRingFull); };
     auto next_slot = [&]() {
         ++n;
         if (++slot == kRing) {
@@ -779,7 +803,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
 
-    const WaitCtx wc{&sh.abort_flag, a.status};
+    const PfWait wc{&sh.abort_flag};
     const uint32_t tmem = sh.tmem_base;
     // Parts of a tile: whole pages, or one part where a page is larger.
     const int part_log2 = min(a.ps_log2, kN == 64 ? 6 : 7), parts = kN >> part_log2;
@@ -795,7 +819,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     const uint32_t qn = two ? 1 : min(kQMax / kStreams, 128 / qstep);
     auto q_slot = [&](int x, uint32_t item) { return two ? 0u : x * qn + item % qn; };
     auto q_addr = [&](int x, uint32_t item) { return sQ + x * G::kQTile + (two ? 0u : (item % qn) * qstep * 128u); };
-    auto desc_wait = [&](int x, uint32_t n) { return mbar_wait_w(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
+    auto desc_wait = [&](int x, uint32_t n) { return pf_wait(&sh.d_full[x][n % kDesc], (n / kDesc) & 1, wc, kPfDesc); };
 
     // What the joining kernel needs to know of each row.
     auto owners = [&]() {
@@ -844,7 +868,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             bool ok = true;
             auto load = [&](const CUtensorMap* map, int p, int r) -> bool {
                 const uint32_t slot = n_ring % kRing;
-                if (!mbar_wait_w(&sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
+                if (!pf_wait(&sh.empty[slot], ((n_ring / kRing) & 1) ^ 1, wc, kPfRingEmpty)) return false;
                 const uint32_t live = __ballot_sync(0xffffffffu, p >= 0);
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], __popc(live) * part_bytes);
                 __syncwarp();
@@ -868,7 +892,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 if (!load(&tk, pg[x][0], row[x][0])) return false;
                 if (flags & kFirst) {
                     const uint32_t i = n_item[x], s = q_slot(x, i);
-                    if (!mbar_wait_w(&sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
+                    if (!pf_wait(&sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
                     const int boxes = two ? 2 * kBoxes : kBoxes;
                     if (lane == 0) mbar_arrive_expect_tx(&sh.q_full[s], boxes * 128u * a.G * min(a.tq, pre ? a.T : a.max_seqlen));
                     __syncwarp();
@@ -915,7 +939,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // Waits for the next tile of the ring; its slot.
             auto take = [&](uint32_t& slot) -> bool {
                 slot = n_ring % kRing;
-                if (!mbar_wait_w(&sh.full[slot], (n_ring / kRing) & 1, wc, kPfRingFull)) return false;
+                if (!pf_wait(&sh.full[slot], (n_ring / kRing) & 1, wc, kPfRingFull)) return false;
                 ++n_ring;
                 return true;
             };
@@ -948,7 +972,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                             if (flags & kLast) umma_commit_w(&sh.q_empty[0]);
                         }
                     };
-                    auto new_item = [&]() -> bool { return mbar_wait_w(&sh.q_full[0], items++ & 1, wc, kPfQFull); };
+                    auto new_item = [&]() -> bool { return pf_wait(&sh.q_full[0], items++ & 1, wc, kPfQFull); };
                     int flags = 0;
                     if ((ok = desc_wait(0, 0))) flags = sh.desc[0][0].flags;
                     if (ok && (flags & kMore) && (ok = take(ks)) && (ok = new_item())) {
@@ -963,7 +987,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         if ((ahead & kMore) && !(ok = take(ks))) break;
                         if (flags & kRagged) clean(vs, d);
                         for (int x = 0; x < 2; ++x) {
-                            if (!(ok = mbar_wait_w(&sh.p_ready[x], n & 1, wc, kPfP))) break;
+                            if (!(ok = pf_wait(&sh.p_ready[x], n & 1, wc, kPfP))) break;
                             tc_fence_after();
                             pf_issue_pv<D>(tmem + x * G::kColO1, col_s(x), sRing + vs * G::kTile, !(flags & kFirst));
                             if (x == 1) umma_commit_w(&sh.empty[vs]);
@@ -987,7 +1011,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 // cycles a tile with one issuer, 1280 of them products).  The
                 // ring's order: K0, K1, V0, K2, V1, K3, ..., the last V behind the
                 // one before.
-                auto wait_tile = [&](uint32_t i) { return mbar_wait_w(&sh.full[i % kRing], (i / kRing) & 1, wc, kPfRingFull); };
+                auto wait_tile = [&](uint32_t i) { return pf_wait(&sh.full[i % kRing], (i / kRing) & 1, wc, kPfRingFull); };
                 if (warp == kSoftWarps + 3) {
                     uint32_t items = 0;
                     for (uint32_t n = 0;; ++n) {
@@ -995,11 +1019,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const int flags = sh.desc[0][n % kDesc].flags, buf = n & 1;
                         if (!(flags & kMore)) break;
                         const uint32_t i = n < 2 ? n : 2 * n - 1;
-                        if ((flags & kFirst) && !(ok = mbar_wait_w(&sh.q_full[q_slot(0, items)], (items / qn) & 1, wc, kPfQFull))) break;
+                        if ((flags & kFirst) && !(ok = pf_wait(&sh.q_full[q_slot(0, items)], (items / qn) & 1, wc, kPfQFull))) break;
                         items += flags & kFirst ? 1 : 0;
                         if (!(ok = wait_tile(i))) break;
                         // S goes where P of two tiles before was read from.
-                        if (n >= 2 && !(ok = mbar_wait_w(&sh.pv_done[buf], ((n - 2) >> 1) & 1, wc, kPfPV))) break;
+                        if (n >= 2 && !(ok = pf_wait(&sh.pv_done[buf], ((n - 2) >> 1) & 1, wc, kPfPV))) break;
                         tc_fence_after();
                         pf_issue_qk<D>(col_s(buf), q_addr(0, items - 1), sRing + i % kRing * G::kTile);
                         umma_commit_w(&sh.s_full[buf]);
@@ -1015,7 +1039,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                             const uint32_t i = ahead & kMore ? 2 * n + 2 : 2 * n + 1;
                             if (!(ok = wait_tile(i))) break;
                             if (flags & kRagged) clean(i % kRing, sh.desc[0][n % kDesc]);
-                            if (!(ok = mbar_wait_w(&sh.p_ready[buf], (n >> 1) & 1, wc, kPfP))) break;
+                            if (!(ok = pf_wait(&sh.p_ready[buf], (n >> 1) & 1, wc, kPfP))) break;
                             tc_fence_after();
                             pf_issue_pv<D>(tmem, col_s(buf), sRing + i % kRing * G::kTile, !(flags & kFirst));
                             umma_commit_w(&sh.pv_done[buf]);
@@ -1044,7 +1068,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 auto issue_s = [&](int x) -> bool {
                     if (flags_s & kFirst) {
                         const uint32_t i = n_item[x]++;
-                        if (!mbar_wait_w(&sh.q_full[q_slot(x, i)], (i / qn) & 1, wc, kPfQFull)) return false;
+                        if (!pf_wait(&sh.q_full[q_slot(x, i)], (i / qn) & 1, wc, kPfQFull)) return false;
                     }
                     pf_issue_qk<D>(col_s(x), q_addr(x, n_item[x] - 1), sRing + ks * G::kTile);
                     umma_commit_w(&sh.s_full[x]);
@@ -1072,7 +1096,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         // Both tiles are waited for before P, so that S follows P V
                         // into the tensor core without a pause.
                         if (!(ok = take_k(x))) break;
-                        if (!(ok = mbar_wait_w(&sh.p_ready[x], n & 1, wc, kPfP))) break;
+                        if (!(ok = pf_wait(&sh.p_ready[x], n & 1, wc, kPfP))) break;
                         tc_fence_after();
                         pf_issue_pv<D>(tmem + x * G::kColO1, col_s(x), sRing + vs * G::kTile, !(flags & kFirst));
                         umma_commit_w(&sh.empty[vs]);
@@ -1119,7 +1143,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 }
                 const int last = more ? min(j + 4, it.j1) : j + 1;
                 for (int jj = j; jj < last && ok; ++jj, ++n) {
-                    if (!(ok = mbar_wait_w(&sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
+                    if (!(ok = pf_wait(&sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
                     Desc& d = sh.desc[x][n % kDesc];
                     const uint32_t live = __ballot_sync(0xffffffffu, val >= 0);
                     if (q == jj - j) d.page[part] = val;
@@ -1175,7 +1199,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             }
             const int buf = kStreams == 2 ? wg : n & 1;
             const uint32_t tS = lanes + G::kColS + buf * G::kColSStep;
-            if (!(ok = mbar_wait_w(&sh.s_full[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfS))) break;
+            if (!(ok = pf_wait(&sh.s_full[buf], (kStreams == 2 ? n : n >> 1) & 1, wc, kPfS))) break;
             tc_fence_after();
             if (live_warp) {
                 float s[kN];
@@ -1227,7 +1251,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         // every earlier phase, since this S was issued after the
                         // P V of two tiles before, and cannot be a phase further.
                         if (kStreams == 1) {
-                            if (!(ok = mbar_wait_w(&sh.pv_done[buf ^ 1], ((n - 1) >> 1) & 1, wc, kPfPV))) break;
+                            if (!(ok = pf_wait(&sh.pv_done[buf ^ 1], ((n - 1) >> 1) & 1, wc, kPfPV))) break;
                             tc_fence_after();
                         }
 #pragma unroll 1
@@ -1272,7 +1296,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             if (!(flags & kLast)) continue;
             // Epilogue: the rows' (m, l, O) into the segment's place.  The next
             // item's first P V overwrites O only after this warp's next P.
-            if (!(ok = mbar_wait_w(&sh.o_done[wg], items & 1, wc, kPfO))) break;
+            if (!(ok = pf_wait(&sh.o_done[wg], items & 1, wc, kPfO))) break;
             ++items;
             tc_fence_after();
             if (live_warp) {
@@ -1300,6 +1324,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && sh.abort_flag != 0 && atomicCAS(&a.status->code, 0, kStatusTimeout) == 0) {
+        a.status->where = sh.abort_flag;
+        a.status->block = blockIdx.x;
+    }
     if (warp == kSoftWarps + 3) tmem_dealloc(tmem, 512);
 }
 
@@ -1548,12 +1576,12 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     const int mode_p = T * (long long)G <= few_limit(d) ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
     const int mode_s = max_seqlen * (long long)G <= few_limit(d) ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
     const int ulog_p = mode_p == kFew || d == 256 ? 6 : 7, ulog_s = mode_s == kFew || d == 256 ? 6 : 7;
-    // The list of tiles, at its longest, stays within 32 bits.
+    // The list of tiles at its longest, with room to spare in 32 bits.
     const int over_s = mode_s == kFew ? 1 : 2;
     const long long tiles_s = (((long long)table_width * page_size + (1 << ulog_s) - 1) >> ulog_s) + over_s;
     const long long tiles_p = ((long long)prefix_len + (1 << ulog_p) - 1) >> ulog_p;
     const long long blocks_s = (long long)Hkv * (T / w.tb + (T < B ? T : B)), blocks_p = (long long)Hkv * ((T + w.tb - 1) / w.tb);
-    if (blocks_s * tiles_s > lim - (1 << 20) || blocks_p * tiles_p > lim - (1 << 20)) return FA_ERR_UNSUPPORTED;
+    if (blocks_s * tiles_s > 1 << 30 || blocks_p * tiles_p > 1 << 30) return FA_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PfArgs a;
     a.table = block_table;

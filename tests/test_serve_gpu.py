@@ -550,3 +550,15 @@ def test_captured_step(fa):
         o2, l2 = step()
         assert torch.equal(got, o2) and torch.equal(gl, l2)
         assert fa.device_status() == 0
+
+
+def test_an_unread_failure_does_not_stop_later_calls(fa):
+    """A call that reported bad lengths leaves the status word set until it is
+    read; the calls after it compute what they should."""
+    b = Batch(8, 2, 128, 16, 3000, [900, 2000], [30, 2], seed=2)
+    assert fa.device_status() == 0
+    b.run(fa, max_seqlen=2)
+    o, lse = b.run(fa)
+    torch.cuda.synchronize()
+    assert fa.device_status() == -1
+    b.check(fa, o, lse)
