@@ -148,13 +148,21 @@ enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kP
 struct PfWait {
     volatile int* abort_flag;   // shared
 };
+__device__ __forceinline__ bool pf_try_wait_long(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool pf_wait(uint64_t* bar, uint32_t parity, const PfWait& w, int site) {
     const uint32_t a = smem_u32(bar);
     bool ok = mbar_try_wait(a, parity);
     if (!ok) {
         const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = 1; !(ok = mbar_try_wait(a, parity)); ++i) {
-            if (i & 63u) continue;
+        while (!(ok = pf_try_wait_long(a, parity))) {
             if (*w.abort_flag) break;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
                 *w.abort_flag = site;
