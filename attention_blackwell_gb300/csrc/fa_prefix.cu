@@ -74,16 +74,17 @@ template <int D> struct Pf {
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
     // Cycles a CTA takes for a unit of the prefix and of the requests' own keys,
     // measured in the kernel on GB300; the CTAs are divided between the two by
-    // them.  kTwo on the prefix: 3400 to 3700 when several row blocks share a
-    // tile (L2 serves all but the first), but alone each tile comes from HBM for
-    // 256 rows only, and its latency under the other CTAs' load sets the pace.
+    // them.  kTwo on the prefix: when several row blocks share a tile, L2 serves
+    // all but the first; alone, each tile comes from HBM for 256 rows only, and
+    // its latency grows with the share of the traffic (`own`, 0 to 1) that the
+    // requests' CTAs ask for at the same time.
     __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 600 : D == 128 ? 780 : 1900) * halves; }
-    __host__ __device__ static constexpr int cost_p(int mode, int halves, bool shared) {
-        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2700)
-             : D == 64 ? (shared ? 3400 : 6000) : (shared ? 3700 : 8000);
+    __device__ static float cost_p(int mode, int halves, bool shared, float own) {
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2400)
+             : D == 64 ? (shared ? 3400 : 3400 + 2600 * own) : (shared ? 3700 : 4400 + 4000 * own);
     }
-    __host__ __device__ static constexpr int cost_s(int mode, int halves) {
-        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2350) : (D == 64 ? 3500 : 4000);
+    __device__ static float cost_s(int mode, int halves) {
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2250) : (D == 64 ? 3500 : 4000);
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
@@ -411,7 +412,9 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     __syncthreads();
     PfHeader h;
     const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
-    const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, a.blocks_p > 1), cs = (float)units * Pf<D>::cost_s(a.mode_s, a.halves_s);
+    const float keys_p = (float)units_p * (1 << a.ulog_p), keys_s = (float)units * (1 << a.ulog_s);
+    const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, a.blocks_p > 1, keys_s / fmaxf(keys_p + keys_s, 1.f));
+    const float cs = (float)units * Pf<D>::cost_s(a.mode_s, a.halves_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
     int wp = np * a.width_p;
