@@ -70,6 +70,7 @@ template <int D> struct Pf {
     static constexpr int kRing = D == 64 ? 8 : 4;                // 128 KB of K/V tiles (even: few rows take K and V by pairs)
     static constexpr uint32_t kTiles = kStreams * kQTile + kRing * kTile;
     static constexpr int kThreads = 384;
+    static constexpr int kMaxSmem = 232448 - 4096;               // dynamic; the rest is PfShared
     static constexpr int kFewParts = D == 256 ? 1 : 2;               // few rows: 16-key parts a step, slots of a step's K or V a warp
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
     // Cycles a CTA takes for a unit of the prefix and of the requests' own keys,
@@ -93,21 +94,23 @@ template <int D> struct Pf {
 // Of a row of q, for the joining kernel: its request's first row, rows and keys
 // (n = 0: no request), the units and items before it.
 struct PfRow {
-    int c0, n, s, pref, items, pad[3];
+    int c0, n, s, pref, items, block, pad[2];   // block: its row block among the prefix's (index), -1: none
 };
 struct PfTables {
     int* pref;           // [B+1] units of requests before b (all key/value heads)
     int* items;          // [B+1] items of requests before b
     int* cu;             // [B+1] sanitised offsets
     int* len;            // [B] own keys
+    int* block;          // the prefix's row blocks, in units of tb rows of q (h.blocks of them; null: all)
 };
 
 struct PfHeader {
     int per_p, per_s;         // units a worker: of the prefix, of the requests
     int n_p;                  // CTAs on the prefix; the rest are on the requests
+    int blocks;               // prefix: row blocks
     int chunk, chunks;        // prefix: tiles an item (the last chunk's may have fewer), items a row block
     int bad;                  // a request has more rows than max_seqlen
-    int pad[10];
+    int pad[9];
 };
 
 struct PfArgs {
@@ -134,6 +137,11 @@ struct PfArgs {
     // (5000 cycles with one row tile at d = 256, 7000 with two), with few rows
     // less than one unit of 64 keys.
     int over_s;
+    // A request with at least merge_n rows (four row blocks: the last one's empty
+    // rows are a fifth of its work at most) hardly gains from sharing the
+    // prefix's tiles with other requests' rows: its items take the prefix's tiles before their own ones, and one that no range
+    // cuts writes the output itself (direct: this call's items can).
+    int merge_n, direct, listed;   // listed: room for the prefix's row blocks in shared memory
     int qstep_p, qstep_s;     // rows between Q slots: a block's rows, in whole swizzle atoms
     float scale_log2;
 };
@@ -178,6 +186,7 @@ struct Item {
     const int* tab;
     int hk, tok0, ntok, j0, j1, nkeys, lim0;
     int seg;
+    int pt, whole; // tiles of the prefix before its own; 1: all its tiles are here and nothing else joins them
 };
 
 // What the roles need to know of one tile.
@@ -187,7 +196,7 @@ struct Desc {
     int flags;              // kMore (not the list's end), kFirst, kLast of its item's tiles here
     int j, nkeys, lim0, hk, tok0, ntok, seg;
 };
-constexpr int kMore = 1, kFirst = 2, kLast = 4, kRagged = 8;   // kRagged: some of its V rows hold no key of the list
+constexpr int kMore = 1, kFirst = 2, kLast = 4, kRagged = 8, kWhole = 16;   // kRagged: some of its V rows hold no key of the list; kWhole: see Item
 constexpr int kDesc = 8;    // tiles the walkers run ahead by
 constexpr int kQMax = 8;    // Q slots
 
@@ -198,30 +207,37 @@ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ int block_of(int k, int n) { return (k & 1) ? n - 1 - (k >> 1) : k >> 1; }
 __device__ __forceinline__ int index_of(int rb, int n) { return rb < (n + 1) / 2 ? 2 * rb : 2 * (n - 1 - rb) + 1; }
 
+// Tiles of the prefix that the items of a request with n rows begin with.
+// M: the build of the kernel for calls that can have such requests; the other has
+// no trace of them (single tokens begin 2 to 4 us of a step's 50 earlier with it).
+template <bool M>
+__device__ __forceinline__ int prefix_tiles(const PfArgs& a, int n) { return M && n >= a.merge_n ? a.tiles_p : 0; }
 // Units an item of a request with n rows and s keys has (0: no rows or no
 // keys): the tiles that its row blocks see under the causal mask, on average,
 // and what an item costs besides.  Row blocks are taken from both ends by turns
 // (block_of), so two neighbours make up two averages.
+template <bool M>
 __device__ __forceinline__ int units_of(const PfArgs& a, int n, int s) {
-    if (n <= 0 || s <= 0) return 0;
-    const int seen = min(s, max(1, s - n + (n + min(n, a.tb)) / 2));
-    return ((seen + (1 << a.ulog_s) - 1) >> a.ulog_s) + a.over_s;
+    if (n <= 0) return 0;
+    const int seen = s > 0 ? min(s, max(1, s - n + (n + min(n, a.tb)) / 2)) : 0;
+    const int tiles = prefix_tiles<M>(a, n) + ((seen + (1 << a.ulog_s) - 1) >> a.ulog_s);
+    return tiles > 0 ? tiles + a.over_s : 0;
 }
-template <int D>
+template <int D, bool M>
 __device__ __forceinline__ int item_units(const PfArgs& a, const PfTables& t, int b, int& n, int& nb) {
     n = t.cu[b + 1] - t.cu[b];
     nb = cdiv(n, a.tb);
-    return units_of(a, n, t.len[b]);
+    return units_of<M>(a, n, t.len[b]);
 }
 // Where unit u of an item's `units` falls among its `tiles`.
 __device__ __forceinline__ int tile_of(int u, int units, int tiles) { return (int)((long long)u * tiles / units); }
 
 // A worker's walk over its range of units.  Everything fits 32 bits: the host
 // refuses longer lists.
-template <int D>
+template <int D, bool M>
 struct Walk {
     int u, end;
-    int b, hk, k, worker, chunk, chunks;
+    int b, hk, k, worker, chunk, chunks, blocks;
     bool pre;
 
     // Worker `x` of this CTA.
@@ -230,10 +246,11 @@ struct Walk {
         b = hk = k = 0;
         chunk = h.chunk;
         chunks = h.chunks;
+        blocks = h.blocks;
         pre = c < h.n_p;
         const int width = pre ? a.width_p : a.width_s;
         worker = (pre ? c : c - h.n_p) * width + x;
-        const int per = pre ? h.per_p : h.per_s, all = pre ? a.Hkv * a.blocks_p * a.tiles_p : t.pref[a.B];
+        const int per = pre ? h.per_p : h.per_s, all = pre ? a.Hkv * h.blocks * a.tiles_p : t.pref[a.B];
         // worker * per passes the list's end by at most a CTA count times per.
         u = worker >= (all + per - 1) / per ? all : worker * per;
         end = min(all - u, per) + u;
@@ -249,7 +266,7 @@ struct Walk {
         }
         b = lo;
         int n, nb;
-        const int per_item = item_units<D>(a, t, b, n, nb), i = (u - t.pref[b]) / per_item;
+        const int per_item = item_units<D, M>(a, t, b, n, nb), i = (u - t.pref[b]) / per_item;
         hk = nb == 1 ? i : i / nb;
         k = i - hk * nb;
     }
@@ -261,24 +278,25 @@ struct Walk {
                 // a worker's share all workers are at the same offset within
                 // their chunks at a time, so the row blocks of a chunk read its
                 // pages together and L2 serves all but the first.
-                const int per_head = a.blocks_p * a.tiles_p;
+                const int per_head = blocks * a.tiles_p;
                 it.hk = u / per_head;
-                const int r = u - it.hk * per_head, ch = r / (chunk * a.blocks_p);
-                const int r2 = r - ch * chunk * a.blocks_p, len = min(chunk, a.tiles_p - ch * chunk);
-                const int rb = r2 / len, off = r2 - rb * len, i = (it.hk * chunks + ch) * a.blocks_p + rb;
+                const int r = u - it.hk * per_head, ch = r / (chunk * blocks);
+                const int r2 = r - ch * chunk * blocks, len = min(chunk, a.tiles_p - ch * chunk);
+                const int rb = r2 / len, off = r2 - rb * len, i = (it.hk * chunks + ch) * blocks + rb;
                 it.j0 = ch * chunk + off;
                 it.j1 = it.j0 + min(len - off, end - u);
                 u += it.j1 - it.j0;
-                it.tok0 = rb * a.tb;
+                it.tok0 = (M && t.block ? t.block[rb] : rb) * a.tb;
                 it.ntok = min(a.tb, a.T - it.tok0);
                 it.nkeys = a.prefix_len;
                 it.lim0 = INT_MAX / 2;
                 it.tab = a.prefix_table;
                 it.seg = i + worker;
+                it.pt = it.whole = 0;
                 return true;
             }
             int n, nb;
-            const int per_item = item_units<D>(a, t, b, n, nb), s = t.len[b];
+            const int per_item = item_units<D, M>(a, t, b, n, nb), s = t.len[b];
             const int i = hk * nb + k;
             const int first = u - (t.pref[b] + i * per_item), last = min(per_item, first + end - u);
             u += last - first;
@@ -291,9 +309,11 @@ struct Walk {
             it.tab = a.table + (long long)b * a.W;
             it.seg = t.items[b] + i + worker;
             const int seen = it.lim0 + it.ntok - 1;        // keys the block's last row sees
-            const int tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0;
+            it.pt = prefix_tiles<M>(a, n);
+            const int tiles = it.pt + (seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
             it.j0 = tile_of(first, per_item, tiles);
             it.j1 = tile_of(last, per_item, tiles);
+            it.whole = M && (it.pt > 0 || a.tiles_p == 0) && it.j0 == 0 && it.j1 == tiles;
             if (last == per_item) {
                 if (++k == nb) {
                     k = 0;
@@ -320,7 +340,7 @@ struct PfShared {
     uint64_t few_full[8][12];
     Item few_item[8][2];
     int few_walk[8][12];
-    int2 scan[12];
+    int4 scan[12];
     uint32_t tmem_base;
     int abort_flag, bad;
 };
@@ -329,7 +349,7 @@ struct PfShared {
 // library's one rule, units and items before each request, and how many CTAs
 // work on the prefix.  Three block barriers when the offsets are well formed
 // and B <= 384: a single-token call's latency begins here.
-template <int D>
+template <int D, bool M>
 __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables& t, PfShared& sh, int tid) {
     constexpr int kThreads = Pf<D>::kThreads, kWarps = kThreads / 32;
     const int lane = tid & 31, warp = tid >> 5;
@@ -364,46 +384,66 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
         }
         __syncthreads();
     }
-    int units = 0, items = 0;      // of the requests before this round's
+    int units = 0, items = 0, blocks = 0;      // of the requests before this round's
     for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + tid;
-        int u = 0, it = 0;
+        int u = 0, it = 0, blk = 0, first_blk = 0;
         if (i < a.B) {
             int n, nb;
-            const int per = item_units<D>(a, t, i, n, nb);
+            const int per = item_units<D, M>(a, t, i, n, nb);
             if (n > a.max_seqlen) sh.bad = 1;
             it = nb * a.Hkv;
             u = per * it;
+            if (M && t.block && n > 0 && !prefix_tiles<M>(a, n)) {
+                // Row blocks of this request's rows that no request before it,
+                // whose rows share the prefix too, has listed.
+                first_blk = t.cu[i] / a.tb;
+                blk = (t.cu[i + 1] - 1) / a.tb - first_blk + 1;
+                for (int j = i - 1; j >= 0 && t.cu[j + 1] > first_blk * a.tb; --j) {
+                    const int m = t.cu[j + 1] - t.cu[j];
+                    if (m > 0 && !prefix_tiles<M>(a, m)) {
+                        ++first_blk;
+                        --blk;
+                        break;
+                    }
+                }
+            }
         }
-        const int u_own = u, it_own = it;
+        const int u_own = u, it_own = it, blk_own = blk;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, it, o);
+            const int x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, it, o), z = M ? __shfl_up_sync(0xffffffffu, blk, o) : 0;
             if (lane >= o) {
                 u += x;
                 it += y;
+                if (M) blk += z;
             }
         }
         if (base) __syncthreads();
-        if (lane == 31) sh.scan[warp] = make_int2(u, it);
+        if (lane == 31) sh.scan[warp] = make_int4(u, it, blk, 0);
         __syncthreads();
-        int u_all = 0, it_all = 0;
+        int u_all = 0, it_all = 0, blk_all = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const int2 x = sh.scan[w];
+            const int4 x = sh.scan[w];
             if (w == warp) {
                 u += units + u_all;
                 it += items + it_all;
+                blk += blocks + blk_all;
             }
             u_all += x.x;
             it_all += x.y;
+            blk_all += x.z;
         }
         if (i < a.B) {
             t.pref[i] = u - u_own;
             t.items[i] = it - it_own;
+            if (M)
+                for (int k = 0; k < blk_own; ++k) t.block[blk - blk_own + k] = first_blk + k;
         }
         units += u_all;
         items += it_all;
+        blocks += blk_all;
     }
     if (tid == 0) {
         t.pref[a.B] = units;
@@ -411,9 +451,10 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     }
     __syncthreads();
     PfHeader h;
-    const int grid = gridDim.x, units_p = a.Hkv * a.blocks_p * a.tiles_p;
+    h.blocks = M && t.block ? blocks : a.blocks_p;
+    const int grid = gridDim.x, units_p = a.Hkv * h.blocks * a.tiles_p;
     const float keys_p = (float)units_p * (1 << a.ulog_p), keys_s = (float)units * (1 << a.ulog_s);
-    const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, a.blocks_p > 1, keys_s / fmaxf(keys_p + keys_s, 1.f));
+    const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, h.blocks > 1, keys_s / fmaxf(keys_p + keys_s, 1.f));
     const float cs = (float)units * Pf<D>::cost_s(a.mode_s, a.halves_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
@@ -422,7 +463,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     // Chunks are a worker's share of tiles; a small rest would be a chunk of its
     // own in every row block (62 tiles a worker of 256: 135 us for 100 rows of 32
     // heads at d = 256, 64: 104), so it is spread over the others.
-    if (a.blocks_p > 1 && units > 0 && a.tiles_p > h.per_p && a.tiles_p % h.per_p < h.per_p / 4) {
+    if (h.blocks > 1 && units > 0 && a.tiles_p > h.per_p && a.tiles_p % h.per_p < h.per_p / 4) {
         const int k = a.tiles_p / h.per_p;
         h.per_p = (a.tiles_p + k - 1) / k;
         np = max(1, min(np, cdiv(units_p, h.per_p * a.width_p)));
@@ -430,7 +471,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     const int ws = max(1, grid - np) * a.width_s;
     h.n_p = np;
     h.per_s = units ? (units + ws - 1) / ws : 1;
-    h.chunk = a.blocks_p > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
+    h.chunk = h.blocks > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
     h.chunks = (a.tiles_p + h.chunk - 1) / h.chunk;
     h.bad = sh.bad;
     if (blockIdx.x == 0 && tid == 0) {
@@ -490,7 +531,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
+template <int D, bool M>
 __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMap* tv, const PfArgs& a, const PfTables& t,
                                          const PfHeader& hdr, PfShared& sh, uint32_t smem, const PfWait& wc, bool pre, int warp, int lane) {
     using G = Pf<D>;
@@ -511,10 +552,10 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
 
     // The walk and the two items that the warp knows (the one it works on and
     // the next, by turns) stay in shared memory: registers go to Q and O.
-    Walk<D>* walk = reinterpret_cast<Walk<D>*>(sh.few_walk[warp]);
+    Walk<D, M>* walk = reinterpret_cast<Walk<D, M>*>(sh.few_walk[warp]);
     Item* items = sh.few_item[warp];
     {
-        Walk<D> w;
+        Walk<D, M> w;
         w.start(a, t, hdr, warp / halves);
         if (lane == 0) *walk = w;
         __syncwarp();
@@ -525,7 +566,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
     };
     // This half's next item (one without rows for it is skipped) into items[to].
     auto next_item = [&](int to) -> bool {
-        Walk<D> w = *walk;
+        Walk<D, M> w = *walk;
         Item it;
         bool more;
         do more = w.next(a, t, it); while (more && half * 16 >= it.ntok * a.G);
@@ -771,7 +812,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
 
 // -------------------------------------------------------------------- kernel
 
-template <int D>
+template <int D, bool M>
 __global__ void __launch_bounds__(Pf<D>::kThreads, 1)
 prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ CUtensorMap tq_s,
               const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -790,13 +831,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     t.items = reinterpret_cast<int*>(t.pref + a.B + 1);
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
+    t.block = M && a.merge_n < INT_MAX ? t.len + a.B : nullptr;   
 
     {   // One barrier a thread, in the order of PfShared.
         constexpr int n1 = (offsetof(PfShared, p_ready) - offsetof(PfShared, d_full)) / 8;
         constexpr int n4 = (offsetof(PfShared, few_full) - offsetof(PfShared, p_ready)) / 8;
         constexpr int nf = (offsetof(PfShared, few_item) - offsetof(PfShared, few_full)) / 8;
         static_assert(n1 + n4 + nf <= G::kThreads, "one barrier a thread");
-        static_assert(sizeof(Walk<D>) <= sizeof(PfShared::few_walk[0]) && G::kFewRing <= 12, "few rows");
+        static_assert(sizeof(Walk<D, M>) <= sizeof(PfShared::few_walk[0]) && G::kFewRing <= 12, "few rows");
         if (tid < n1 + n4 + nf) {
             mbar_init(&sh.d_full[0][0] + tid, tid >= n1 && tid < n1 + n4 ? 4 : 1);
             fence_mbar_init();
@@ -809,7 +851,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     }
     grid_launch_next();
     grid_wait();
-    const PfHeader hdr = build_tables<D>(a, t, sh, tid);
+    const PfHeader hdr = build_tables<D, M>(a, t, sh, tid);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -848,6 +890,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 row.s = t.len[lo];
                 row.pref = t.pref[lo];
                 row.items = t.items[lo];
+                row.block = a.tiles_p == 0 || prefix_tiles<M>(a, row.n) ? -1 : i / a.tb;
+                if (M && t.block && row.block >= 0) {
+                    int at = 0;
+                    for (int hi = hdr.blocks; hi - at > 1;) {
+                        const int mid = (at + hi) >> 1;
+                        if (t.block[mid] <= row.block) at = mid; else hi = mid;
+                    }
+                    row.block = at;
+                }
             }
             a.rows[i] = row;
         }
@@ -861,7 +912,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             owners();
         } else {
             regs_inc<232>();
-            few_rows<D>(&tk_few, &tv_few, a, t, hdr, sh, base, wc, pre, warp, lane);
+            few_rows<D, M>(&tk_few, &tv_few, a, t, hdr, sh, base, wc, pre, warp, lane);
         }
     } else if (warp >= kSoftWarps) {
         regs_dec<88>();
@@ -1129,13 +1180,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // Pages of four tiles at a time, a lane each; the next four's loads
             // (the next item's, past an item's end) run while these are handed on.
             const int x = warp - (kSoftWarps + 2), q = lane >> 3, part = lane & 7;
-            Walk<D> walk;
+            Walk<D, M> walk;
             walk.start(a, t, hdr, x);
             Item it, ahead;
             auto pages = [&](const Item& i, int j) {
-                const int tile = j + q, key = tile * kN + (part << part_log2);
-                if (part >= parts || tile >= i.j1 || key >= i.nkeys) return -1;
-                const int p = i.tab[key >> a.ps_log2];
+                const int tile = j + q;
+                const bool shared = M && tile < i.pt;            // the prefix's tiles come first
+                const int key = (shared || !M ? tile : tile - i.pt) * kN + (part << part_log2);
+                if (part >= parts || tile >= i.j1 || key >= (shared ? a.prefix_len : i.nkeys)) return -1;
+                const int p = (shared ? a.prefix_table : i.tab)[key >> a.ps_log2];
                 return p >= 0 && p < a.P ? p : -1;
             };
             uint32_t n = 0;
@@ -1160,12 +1213,14 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                     if (q == jj - j) d.page[part] = val;
                     if (lane == 0) {
                         const int bits = (live >> (8 * (jj - j))) & 0xff;
-                        d.flags = more ? kMore | (jj == it.j0 ? kFirst : 0) | (jj == it.j1 - 1 ? kLast : 0) |
-                                         ((jj + 1) * kN > it.nkeys || bits != (1 << parts) - 1 ? kRagged : 0) : 0;
+                        const bool shared = M && jj < it.pt;
+                        const int jt = shared || !M ? jj : jj - it.pt, nkeys = shared ? a.prefix_len : it.nkeys;
+                        d.flags = more ? kMore | (jj == it.j0 ? kFirst : 0) | (jj == it.j1 - 1 ? kLast : 0) | (M && it.whole ? kWhole : 0) |
+                                         ((jt + 1) * kN > nkeys || bits != (1 << parts) - 1 ? kRagged : 0) : 0;
                         d.live = bits;
-                        d.j = jj;
-                        d.nkeys = it.nkeys;
-                        d.lim0 = it.lim0;
+                        d.j = jt;
+                        d.nkeys = nkeys;
+                        d.lim0 = shared ? INT_MAX / 2 : it.lim0;
                         d.hk = it.hk;
                         d.tok0 = it.tok0;
                         d.ntok = it.ntok;
@@ -1193,18 +1248,20 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         const float scale = a.scale_log2;
         uint32_t items = 0;
         bool ok = true, valid = false, live_warp = false;
-        int lim_row = 0, seg = 0;
+        int seg = 0, tok0 = 0, head0 = 0, lim_row = 0;
         float m_ref = -INFINITY, l = 0.f;
         for (uint32_t n = 0; x < workers; ++n) {   // d = 256: one worker, the second four warps have none
             if (!(ok = desc_wait(x, n))) break;
             const Desc& d = sh.desc[x][n % kDesc];
             const int flags = d.flags, live = d.live, k0 = d.j * kN;
             if (!(flags & kMore)) break;
+            if (M || (flags & kFirst)) lim_row = min(d.nkeys, d.lim0 + tok);
             if (flags & kFirst) {
                 valid = r < a.tq * a.G && tok < d.ntok;
                 live_warp = __any_sync(0xffffffffu, valid);
-                lim_row = pre ? d.nkeys : min(d.nkeys, d.lim0 + tok);
                 seg = d.seg;
+                tok0 = d.tok0;
+                head0 = d.hk * a.G;
                 m_ref = -INFINITY;
                 l = 0.f;
             }
@@ -1310,7 +1367,29 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             if (!(ok = pf_wait(&sh.o_done[wg], items & 1, wc, kPfO))) break;
             ++items;
             tc_fence_after();
-            if (live_warp) {
+            if (M && live_warp && (flags & kWhole)) {
+                // Nothing else joins: the output itself.
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const int head = head0 + r - r / a.G * a.G;
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)(tok0 + tok) * a.Hq + head) * D);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c0, o);
+                    tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float* f = reinterpret_cast<const float*>(o + 8 * q);
+                            // A row that saw no key holds whatever P 0 V gave: 0.
+                            dst[c0 / 8 + q] = l > 0.f ? make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv))
+                                                      : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                }
+                if (valid) a.lse[(long long)head * a.T + tok0 + tok] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            } else if (live_warp) {
                 const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s) + (two ? wg * a.tq * a.G + r : r);
                 float* orow = (pre ? a.o_p : a.o_s) + at * D;
 #pragma unroll 1
@@ -1363,24 +1442,32 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     const PfHeader h = *a.hdr;
     const PfRow r = a.rows[t];
     if (h.bad || r.n == 0) return;
-    const int i = t - r.c0, nb = cdiv(r.n, a.tb), rb = i / a.tb, blk = t / a.tb;
+    const int i = t - r.c0, nb = cdiv(r.n, a.tb), rb = i / a.tb, blk = r.block;
     // Most segments that an item of the prefix can have, and room for all chunks'.
-    const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = a.prefix_len > 0 ? most * h.chunks : 0;
+    const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = blk >= 0 ? most * h.chunks : 0;
     // The request's item: its units from u0 on, the workers that they fall to.
-    const int units = units_of(a, r.n, r.s), seen = units ? r.s - r.n + min(r.n, (rb + 1) * a.tb) : 0;
-    const int tiles = seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0;
+    const int units = units_of<true>(a, r.n, r.s), seen = r.s - r.n + min(r.n, (rb + 1) * a.tb);
+    const int tiles = prefix_tiles<true>(a, r.n) + (seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
     const int item = hk * nb + index_of(rb, nb), u0 = r.pref + item * units, c_own = u0 / h.per_s;
     const int all = slots + (tiles > 0 ? (u0 + units - 1) / h.per_s - c_own + 1 : 0);
     // Row (of head h0) in the k-th segment, the prefix's first, then the
     // request's, each in the list's order; negative: there is none.
+    if (a.direct && slots == 0 && tiles > 0) {
+        // Written already if one worker had all its tiles: the first that had any.
+        for (int c = c_own;; ++c) {
+            const int to = tile_of(min(units, c * h.per_s + h.per_s - u0), units, tiles);
+            if (to == tiles && tile_of(max(0, c * h.per_s - u0), units, tiles) == 0) return;
+            if (to > 0) break;
+        }
+    }
     auto place = [&](int k) -> long long {
         if (k >= all) return -1;
         if (k < slots) {
             const int ch = k / most, j = k - ch * most, len = min(h.chunk, a.tiles_p - ch * h.chunk);
-            const int v0 = hk * a.blocks_p * a.tiles_p + ch * h.chunk * a.blocks_p + blk * len;
+            const int v0 = hk * h.blocks * a.tiles_p + ch * h.chunk * h.blocks + blk * len;
             const int ca = v0 / h.per_p, cb = (v0 + len - 1) / h.per_p;
             if (ca + j > cb) return -1;
-            return (long long)((hk * h.chunks + ch) * a.blocks_p + blk + ca + j) * a.rows_p + (t - blk * a.tb) * a.G + g0;
+            return (long long)((hk * h.chunks + ch) * h.blocks + blk + ca + j) * a.rows_p + t % a.tb * a.G + g0;
         }
         const int c = c_own + k - slots;
         const int from = max(0, c * h.per_s - u0), to = min(units, c * h.per_s + h.per_s - u0);
@@ -1506,19 +1593,19 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
     return w;
 }
 
-template <int D>
+template <int D, bool M>
 int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtensorMap& tk, const CUtensorMap& tv,
                   const CUtensorMap& tk_few, const CUtensorMap& tv_few, const PfArgs& a, int sms, cudaStream_t stream) {
     using G = Pf<D>;
-    const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4;
-    static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 + sizeof(PfShared) <= 232448, "shared memory plan");
-    auto kern = prefix_kernel<D>;
+    const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4 + a.listed * 4;
+    static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 <= G::kMaxSmem && G::kMaxSmem + sizeof(PfShared) <= 232448, "shared memory plan");
+    auto kern = prefix_kernel<D, M>;
     // Once a device: the most that any batch needs.
     static std::atomic<uint64_t> prepared{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
-        constexpr int most = 1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4;
+        constexpr int most = Pf<D>::kMaxSmem;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
@@ -1590,9 +1677,9 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     // The list of tiles at its longest, with room to spare in 32 bits.
     const int over_s = mode_s == kFew ? 1 : 2;
     const long long tiles_s = (((long long)table_width * page_size + (1 << ulog_s) - 1) >> ulog_s) + over_s;
-    const long long tiles_p = ((long long)prefix_len + (1 << ulog_p) - 1) >> ulog_p;
+    const long long tiles_p = ((long long)prefix_len + (1 << ulog_p) - 1) >> ulog_p;   // both units are a tile where own items take the prefix's
     const long long blocks_s = (long long)Hkv * (T / w.tb + (T < B ? T : B)), blocks_p = (long long)Hkv * ((T + w.tb - 1) / w.tb);
-    if (blocks_s * tiles_s > 1 << 30 || blocks_p * tiles_p > 1 << 30) return FA_ERR_UNSUPPORTED;
+    if (blocks_s * (tiles_s + tiles_p) > 1 << 30 || blocks_p * tiles_p > 1 << 30) return FA_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     PfArgs a;
     a.table = block_table;
@@ -1635,6 +1722,14 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     a.ulog_p = ulog_p;
     a.ulog_s = ulog_s;
     a.over_s = over_s;
+    a.direct = mode_s == kTwo || (d == 256 && mode_s == kOne);
+    // The row blocks of requests with fewer rows: each touches five at most.
+    const long long listed = B * 5LL < (T + w.tb - 1) / w.tb ? B * 5LL : (T + w.tb - 1) / w.tb;
+    const int tiles_bytes = d == 64 ? Pf<64>::kTiles : d == 128 ? Pf<128>::kTiles : Pf<256>::kTiles;
+    const bool merge = a.direct && prefix_len > 0 && ulog_p == ulog_s &&
+                       1024 + tiles_bytes + (B + 1) * 12 + B * 4 + listed * 4 <= Pf<128>::kMaxSmem;
+    a.merge_n = merge ? 4 * w.tb : INT_MAX;
+    a.listed = merge ? (int)listed : 0;
     const int box_p = T < w.tq ? T : w.tq, box_s = max_seqlen < w.tq ? max_seqlen : w.tq;
     a.qstep_p = (box_p * G + 7) & ~7;
     a.qstep_s = (box_s * G + 7) & ~7;
@@ -1659,9 +1754,14 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
         if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
     }
     if (rc != FA_OK) return rc;
-    if (d == 64) return launch_prefix<64>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
-    if (d == 128) return launch_prefix<128>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
-    return launch_prefix<256>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
+    auto launch = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        return a.direct ? launch_prefix<D, true>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream)
+                        : launch_prefix<D, false>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
+    };
+    if (d == 64) return launch(std::integral_constant<int, 64>{});
+    if (d == 128) return launch(std::integral_constant<int, 128>{});
+    return launch(std::integral_constant<int, 256>{});
 }
 
 }  // extern "C"

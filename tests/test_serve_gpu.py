@@ -318,6 +318,25 @@ def test_long_prompts(fa, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (7, 1), (2, 2)])
+@pytest.mark.parametrize("prefix", [0, 300])
+def test_prompts_among_steps(fa, d, hq, hkv, prefix):
+    """Requests whose rows fill row blocks of their own, between ones that share
+    them: in order, side by side, the first, the last, with rows before and
+    behind all requests, with fewer keys than rows."""
+    tb = (128 // (hq // hkv)) * (1 if d == 256 else 2)
+    long = 4 * tb
+    n = [1, long, 2, 0, 3 * tb + 1, long + 7, long - 1, 5, 1, 1, long, tb, 3]
+    s = [9, long + 40, 2, 7, 4 * tb, long + 7, long + 300, 5, 0, 77, 10, 400, 3]
+    b = Batch(hq, hkv, d, 16, prefix, s, n, seed=d + hq + prefix, tail=5)
+    b.check(fa, *b.run(fa))
+    b = Batch(hq, hkv, d, 64, prefix, s[::-1], n[::-1], seed=d + hq + prefix + 1)
+    b.check(fa, *b.run(fa))
+    b = Batch(hq, hkv, d, 32, prefix, [long + 20], [long], seed=d)
+    b.check(fa, *b.run(fa))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_one_long_request_among_short_ones(fa, d):
     s = [3] * 20 + [9000] + [50] * 20
     b = Batch(8, 2, d, 16, 64, s, [1] * 41, seed=d + 5)
