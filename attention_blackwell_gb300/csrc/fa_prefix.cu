@@ -1369,7 +1369,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             tc_fence_after();
             if (M && live_warp && (flags & kWhole)) {
                 // Nothing else joins: the output itself.
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;   // a NaN stays one
                 const int head = head0 + r - r / a.G * a.G;
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)(tok0 + tok) * a.Hq + head) * D);
 #pragma unroll 1
@@ -1382,13 +1382,13 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         for (int q = 0; q < 4; ++q) {
                             const float* f = reinterpret_cast<const float*>(o + 8 * q);
                             // A row that saw no key holds whatever P 0 V gave: 0.
-                            dst[c0 / 8 + q] = l > 0.f ? make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                                                   pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv))
-                                                      : make_uint4(0u, 0u, 0u, 0u);
+                            dst[c0 / 8 + q] = l == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                                       : make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
+                                                                    pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
                         }
                     }
                 }
-                if (valid) a.lse[(long long)head * a.T + tok0 + tok] = l > 0.f ? (m_ref + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+                if (valid) a.lse[(long long)head * a.T + tok0 + tok] = l == 0.f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994531f;
             } else if (live_warp) {
                 const long long at = (long long)seg * (pre ? a.rows_p : a.rows_s) + (two ? wg * a.tq * a.G + r : r);
                 float* orow = (pre ? a.o_p : a.o_s) + at * D;
@@ -1503,7 +1503,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
         float f[H];
 #pragma unroll
         for (int x = 0; x < H; ++x) {
-            f[x] = ml[x].x == -INFINITY ? 0.f : ex2_mufu(ml[x].x - M[x]);
+            f[x] = ml[x].y == 0.f ? 0.f : ex2_mufu(ml[x].x - M[x]);   // a sum of 0: no key seen; a NaN stays one
             L[x] += f[x] * ml[x].y;
         }
         const int cnt = min(32, all - k0);
@@ -1551,7 +1551,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     }
 #pragma unroll
     for (int x = 0; x < H; ++x) {
-        const float inv = L[x] > 0.f ? 1.f / L[x] : 0.f;
+        const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
         uint32_t out[E / 2];
 #pragma unroll
         for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[x][e] * inv, acc[x][e + 1] * inv);
@@ -1559,7 +1559,7 @@ __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
         if constexpr (E == 2) *dst = out[0];
         else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
         else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (lane == 0) a.lse[(long long)(h0 + x) * a.T + t] = L[x] > 0.f ? (M[x] + __log2f(L[x])) * 0.69314718055994531f : -INFINITY;
+        if (lane == 0) a.lse[(long long)(h0 + x) * a.T + t] = L[x] == 0.f ? -INFINITY : (M[x] + __log2f(L[x])) * 0.69314718055994531f;
     }
 }
 

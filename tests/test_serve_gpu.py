@@ -376,6 +376,26 @@ def test_absent_pages(fa, d):
     assert torch.equal(o[6], torch.zeros_like(o[6])) and bool(torch.isneginf(lse[:, 6]).all())
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [[1, 1, 1], [1, 9, 3], [1, 1030, 2]], ids=["single", "drafts", "prompt"])
+def test_a_nan_stays_in_its_rows_and_shows(fa, d, n):
+    """A query with a NaN and one that sees a key with a NaN give NaN, O and LSE
+    alike; nothing else does."""
+    b = Batch(8, 2, d, 16, 200, [77, 1100, 30], n, seed=d + n[1])
+    row = b.cu[1] + n[1] // 2
+    b.q[row, 3, 5] = float("nan")
+    b.q[0, 7] = float("nan")
+    last = b.s[2] - 1                               # seen by the last request's last row only
+    b.k[b.table[2][last // 16], 1, last % 16, 0] = float("nan")
+    o, lse = b.run(fa)
+    b.check(fa, o, lse)
+    nan = torch.zeros(b.T, 8, dtype=torch.bool, device="cuda")
+    nan[row, 3] = nan[0, 7] = True
+    nan[-1, 4:] = True
+    assert torch.equal(torch.isnan(o).all(-1), nan) and torch.equal(torch.isnan(o).any(-1), nan)
+    assert torch.equal(torch.isnan(lse), nan.T)
+
+
 def test_extreme_lengths_are_clamped(fa):
     b = Batch(8, 2, 128, 16, 40, [100, 100, 64], [1, 1, 1], seed=2, poison=False)
     width = len(b.table[0])
