@@ -55,6 +55,7 @@ namespace {
 
 constexpr float kTau = 8.0f;        // rescale threshold (log2 units), as in the forward kernels
 
+constexpr int kMaxKeys = 1 << 29;   // of the prefix, of a request
 constexpr int kFew = 0, kOne = 1, kTwo = 2;   // row tiles: 16 or 32 rows, 128, 2 x 128
 constexpr int few_limit(int d) { return d == 256 ? 16 : 32; }   // rows up to which kFew is taken
 
@@ -1652,8 +1653,9 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     const int lg = page_log2(page_size);
     if ((d != 64 && d != 128 && d != 256) || lg < 0 || Hq / Hkv > 128 || B > kMaxVarlenSeqs) return FA_ERR_UNSUPPORTED;
     const long long lim = 0x7fffffffLL;
-    if ((long long)Hq * T > lim || (long long)B * table_width > lim || (long long)table_width * page_size > lim ||
-        (long long)num_pages * page_size * Hkv > lim || (long long)prefix_len + page_size > lim)
+    // Key indices, a tile and a causal limit past them included, are 32 bits wide.
+    if ((long long)Hq * T > lim || (long long)B * table_width > lim || (long long)table_width * page_size > kMaxKeys ||
+        (long long)num_pages * page_size * Hkv > lim || prefix_len > kMaxKeys)
         return FA_ERR_UNSUPPORTED;
     if (misaligned(q, 15) || misaligned(k_pages, 15) || misaligned(v_pages, 15) || misaligned(o, 15) ||
         misaligned(lse, 15) || misaligned(block_table, 3) || misaligned(kv_lens, 3) || misaligned(cu_seqlens, 3) ||

@@ -400,8 +400,9 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  * table_width < 1, Hq % Hkv, prefix_len < 0, alpha not finite and > 0,
  * max_seqlen < 1, q_stride below Hq * d, T != B without cu_seqlens),
  * FA_ERR_UNSUPPORTED (d not 64, 128 or 256; Hq / Hkv > 128; B > 1024;
- * page_size; Hq * T, B * table_width, table_width * page_size, prefix_len +
- * page_size or num_pages * Hkv * page_size above 2^31 - 1), FA_ERR_ALIGN,
+ * page_size; prefix_len or table_width * page_size above 2^29; Hq * T, B *
+ * table_width or num_pages * Hkv * page_size above 2^31 - 1; row blocks times
+ * tiles of 64 keys that the lengths allow above 2^30), FA_ERR_ALIGN,
  * FA_ERR_WORKSPACE, FA_ERR_LAUNCH.
  */
 int fa_prefix_fwd(const void *q, int64_t q_stride, const void *k_pages, const void *v_pages, void *o, float *lse,

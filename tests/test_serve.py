@@ -97,6 +97,9 @@ def test_prefix_fwd_refusals(attend):
                dict(Hq=129, Hkv=1, qs=129 * 128), dict(B=1025, T=1025), dict(T=1 << 30, cu=P, ms=8),
                dict(W=1 << 30), dict(P=1 << 30), dict(pl=(1 << 31) - 8), dict(W=1 << 28)):
         assert attend(**kw) == -2, kw
+    # Lists of more than 2^29 keys, whose indices would not fit with a tile past them.
+    for kw in (dict(pl=(1 << 29) + 1), dict(pl=(1 << 30) + 5), dict(W=(1 << 25) + 1), dict(W=1 << 26)):
+        assert attend(**kw) == -2, kw
     for n in ("q", "kp", "vp", "o", "lse"):
         assert attend(**{n: P + 8}) == -3, n
     for n in ("table", "kv", "pt", "cu"):
