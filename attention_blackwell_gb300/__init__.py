@@ -415,7 +415,7 @@ def prefix_workspace(B, Hq, Hkv, T, max_seqlen=1, d=HEAD_DIM, device=None):
     with at most max_seqlen rows each."""
     dev = torch.device(device or "cuda")
     with torch.cuda.device(dev):
-        n = lib().fa_prefix_workspace_size(int(T), int(B), int(Hq), int(Hkv), int(d), int(max_seqlen))
+        n = lib().fa_prefix_workspace_size(int(T), int(B), int(Hq), int(Hkv), int(d), min(int(max_seqlen), max(int(T), 1)))
         if n == 0:
             raise ValueError("invalid sizes for the prefix workspace")
         return torch.empty(n, dtype=torch.uint8, device=dev)
@@ -459,7 +459,7 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
         raise ValueError("without cu_seqlens q must have one row a request")
     else:
         max_seqlen = 1
-    prefix_len = int(prefix_len)
+    max_seqlen, prefix_len = min(int(max_seqlen), max(T, 1)), int(prefix_len)
     if prefix_len > 0:
         if prefix_table is None:
             raise ValueError("prefix_len needs prefix_table")
@@ -492,7 +492,7 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     rc = lib().fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
                              T, B, Hq, Hkv, d, alpha, P, page, block_table.data_ptr(), block_table.shape[1],
                              kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
-                             int(max_seqlen), prefix_table.data_ptr() if prefix_table is not None else None,
+                             max_seqlen, prefix_table.data_ptr() if prefix_table is not None else None,
                              prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                              _current_raw_stream(dev))
     _check(rc, "fa_prefix_fwd")

@@ -1576,21 +1576,27 @@ struct PfLayout {
 // Workspace: header, what the rows are, the segments' rows.  The prefix's items are row
 // blocks times chunks of a worker's share of tiles, so at most row blocks plus
 // workers; the requests' at most T / tb + min(T, B) a key/value head.  Segments:
-// items plus workers (eight a CTA with few rows, else two at most).
+// items plus workers (eight a CTA with few rows, else two at most).  Counted in
+// rows, and never fewer than for fewer rows a segment, so that a workspace for
+// the largest step serves all.
 PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms) {
     PfLayout w;
     w.tq = 128 / G;
     w.tb = d == 256 ? w.tq : 2 * w.tq;
     w.rows_p = (T < w.tb ? T : w.tb) * G;
     w.rows_s = (max_seqlen < w.tb ? max_seqlen : w.tb) * G;
-    const size_t seg_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) + (size_t)(T * (long long)G <= few_limit(d) ? 8 : 4) * sms;
-    const size_t seg_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) + (size_t)(max_seqlen * (long long)G <= few_limit(d) ? 8 : 2) * sms;
+    auto workers = [&](int rows, int width) -> size_t {      // rows of `width` a CTA, eight with few rows
+        const int few = few_limit(d);
+        return (size_t)sms * (rows <= few ? 8 * rows : 8 * few > width * rows ? 8 * few : width * rows);
+    };
+    const size_t all_p = (size_t)Hkv * ((T + w.tb - 1) / w.tb) * w.rows_p + workers(w.rows_p, 4);
+    const size_t all_s = (size_t)Hkv * (T / w.tb + (T < B ? T : B)) * w.rows_s + workers(w.rows_s, 2);
     w.rows = align256(sizeof(PfHeader));
     w.ml_p = align256(w.rows + (size_t)T * sizeof(PfRow));
-    w.ml_s = align256(w.ml_p + seg_p * w.rows_p * 8);
-    w.o_p = align256(w.ml_s + seg_s * w.rows_s * 8);
-    w.o_s = align256(w.o_p + seg_p * w.rows_p * d * 4);
-    w.total = align256(w.o_s + seg_s * w.rows_s * d * 4);
+    w.ml_s = align256(w.ml_p + all_p * 8);
+    w.o_p = align256(w.ml_s + all_s * 8);
+    w.o_s = align256(w.o_p + all_p * d * 4);
+    w.total = align256(w.o_s + all_s * d * 4);
     return w;
 }
 
@@ -1635,7 +1641,7 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
         (d != 64 && d != 128 && d != 256) || (long long)Hq * T > 0x7fffffffLL)
         return 0;
     const int sms = fa_num_sms();
-    return pf_layout(T, B, Hkv, Hq / Hkv, d, max_seqlen, sms > 0 ? sms : kMaxSMs).total;
+    return pf_layout(T, B, Hkv, Hq / Hkv, d, max_seqlen > T ? (T > 1 ? T : 1) : max_seqlen, sms > 0 ? sms : kMaxSMs).total;
 }
 
 int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const void* v_pages, void* o, float* lse,
@@ -1662,6 +1668,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
         misaligned(prefix_table, 3) || (q_stride & 7))
         return FA_ERR_ALIGN;
     if (T == 0) return FA_OK;
+    if (max_seqlen > T) max_seqlen = T;
     const int sms = fa_num_sms();
     DevStatus* status = device_status_ptr();
     if (sms < 1 || !status) return FA_ERR_LAUNCH;

@@ -115,6 +115,13 @@ def test_prefix_workspace_sizes(lib):
     f.restype, f.argtypes = SZ, [I] * 6
     assert f(4, 0, 8, 2, 128, 1) == f(4, 4, 8, 3, 128, 1) == f(4, 4, 8, 2, 96, 1) == f(4, 4, 8, 2, 128, 0) == 0
     assert f(-1, 4, 8, 2, 128, 1) == f(4, 4, 258, 2, 128, 1) == 0
+    sizes = sorted({x + y for x in (0, 1, 2, 4, 8, 16, 32, 64, 128, 256, 1024) for y in (0, 1, 5)})
+    for d in (64, 128, 256):
+        for hq, hkv in ((4, 4), (8, 2), (6, 2), (16, 1), (32, 1), (128, 1)):
+            for x, y in zip(sizes, sizes[1:]):
+                assert f(x, 8, hq, hkv, d, 8) <= f(y, 8, hq, hkv, d, 8), (d, hq, hkv, y)
+                assert f(1024, 8, hq, hkv, d, max(x, 1)) <= f(1024, 8, hq, hkv, d, y), (d, hq, hkv, y)
+                assert f(300, max(x, 1), hq, hkv, d, 2) <= f(300, y, hq, hkv, d, 2), (d, hq, hkv, y)
 
 
 

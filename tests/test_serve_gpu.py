@@ -406,6 +406,22 @@ def test_extreme_lengths_are_clamped(fa):
     assert width * 16 < 1 << 30
 
 
+def test_max_seqlen_above_all_rows(fa):
+    """No request has more rows than there are, whatever the caller allows."""
+    b = Batch(8, 2, 128, 16, 40, [100, 20], [3, 2], seed=2)
+    o, lse = b.run(fa)
+    for m in (b.T, 1 << 20, (1 << 32) + 1):
+        x, y = b.run(fa, max_seqlen=m, workspace=fa.prefix_workspace(2, 8, 2, b.T, m))
+        b.check(fa, x, y)
+
+
+def test_a_workspace_for_the_largest_step_serves_all(fa):
+    ws = fa.prefix_workspace(300, 16, 2, 600, 300, d=64)
+    for n in ([1], [4], [1, 3, 1], [5] * 20, [1] * 300, [300, 300]):
+        b = Batch(16, 2, 64, 16, 500, [200] * len(n) if len(n) < 50 else [20] * len(n), n, seed=len(n))
+        b.check(fa, *b.run(fa, workspace=ws))
+
+
 def test_rows_behind_the_last_request_stay(fa):
     b = Batch(8, 2, 128, 16, 40, [100, 20], [3, 2], seed=2, tail=7)
     o = torch.full((b.T, 8, 128), 5.0, dtype=torch.bfloat16, device="cuda")
