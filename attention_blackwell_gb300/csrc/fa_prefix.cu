@@ -1,10 +1,14 @@
 // fa_prefix.cu -- fa_prefix_fwd: attention of new tokens over a shared prefix
 // and each request's own paged keys (sm_103a, tcgen05 / TMEM / TMA).
 //
-// The prefix's K and V are read once for a block of up to 256 query rows (the
-// G query heads of a key/value head, times as many tokens of any requests as
-// fit), a request's own K and V once for the rows of its own tokens.  Both are
-// the same work on different pages, so one persistent kernel does both:
+// With x_j = alpha q . k_j over the keys that a row sees (the prefix's, then
+// its request's own up to the causal limit), any split of the keys into sets s
+// gives (m_s, l_s, O_s) = (max x, sum 2^(x - m_s), sum 2^(x - m_s) v), and
+//   O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s,  M = max m_s.
+// So the prefix's K and V are read once for a block of up to 256 query rows
+// (the G query heads of a key/value head, times as many tokens of any requests
+// as fit), a request's own once for the rows of its own tokens.  Both are the
+// same work on different pages, so one persistent kernel does both:
 //
 //   item     one row block of one key/value head against one list of pages:
 //            the prefix's (rows of any requests) or a request's (its rows);
@@ -16,9 +20,13 @@
 //            the workspace; segment ids are item + worker, unique because every
 //            step along the list raises one of the two.
 //
-// A second kernel joins each output row's segments: with M = max m_s,
-// O = sum 2^(m_s - M) O_s / sum 2^(m_s - M) l_s in fp32, in the list's order, so
-// the result does not depend on timing.
+// A second kernel joins each output row's segments in fp32, in the list's order,
+// so the result does not depend on timing.  A request with rows for four row
+// blocks or more (a long prompt) gains nothing from sharing the prefix's tiles
+// with other requests' rows: its items take the prefix's tiles and then their
+// own, and one that no range cuts writes its output itself (six prompts of up to
+// 2048 tokens over 8192 shared keys: 1226 us joined, 1113 so; from one row block
+// up, batches that mix prompts and steps are up to 30 % slower).
 //
 // Some CTAs work on the prefix, the others on the requests, in proportion to
 // the cost of both.  Within a CTA (d = 64 and 128):
@@ -32,15 +40,29 @@
 //                 own (few_rows below): single tokens, where the copies set the
 //                 pace.
 // d = 256: one worker a CTA, one row tile, S double-buffered, 64-key tiles (its
-// accumulator takes half of tensor memory).
+// accumulator takes half of tensor memory), S and P V issued by a warp each.
 //
-// Warps: softmax (4 or 8), loader, issuer, and one or two that walk the list
-// ahead of the others and leave each tile's description, page numbers
-// included, in shared memory, so that no role waits for a table entry.
+// Warps: softmax (4 or 8), loader, issuer (d = 256: two), and one or two that
+// walk the list ahead of the others and leave each tile's description, page
+// numbers included, in shared memory, so that no role waits for a table entry.
 //
 // Keys behind the end of a list and keys of absent pages are masked by
 // selection, and their V rows are zeroed in shared memory before the product
 // (0 * NaN would poison the sum), so the cache's leftovers never matter.
+//
+// What bounds it (GB300; 6.78 TB/s and 1892 TFLOP/s measured):
+//   single tokens, own keys of a few hundred, 128-key pages, 32 / 8 heads of
+//   128: the copies.  64 requests (282 MB): 65 us, 57 in the main kernel, 4.9
+//   TB/s there; its first 10000 cycles (5 us) go by before every warp's ring is
+//   full, and the rows' segments and their join take 8 us.
+//   512 requests over a long prefix (1.18 GB, 279 GFLOP): 344 us; the prefix's
+//   CTAs take 3430 cycles a unit of two row tiles by 128 keys, of which the
+//   products are 2048: S -> softmax -> P V of one tile has the other's to hide
+//   behind, no more.
+//   prompts (1.43 TFLOP): 1113 us, tensor pipe 57 % busy, the same chain.
+//   d = 256 (224 MB, 60 GFLOP): 98 us, 2300 cycles a 64-key tile, 1280 of them
+//   products.
+//   one request, one token: 17 us, 13 of them host and launch.
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
@@ -91,12 +113,12 @@ template <int D> struct Pf {
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
 };
 
-// What both kernels need to know of the list of units.
 // Of a row of q, for the joining kernel: its request's first row, rows and keys
 // (n = 0: no request), the units and items before it.
 struct PfRow {
     int c0, n, s, pref, items, block, pad[2];   // block: its row block among the prefix's (index), -1: none
 };
+// The list of units, in shared memory.
 struct PfTables {
     int* pref;           // [B+1] units of requests before b (all key/value heads)
     int* items;          // [B+1] items of requests before b
@@ -105,6 +127,7 @@ struct PfTables {
     int* block;          // the prefix's row blocks, in units of tb rows of q (h.blocks of them; null: all)
 };
 
+// How the list is divided: the same in every CTA, left for the joining kernel.
 struct PfHeader {
     int per_p, per_s;         // units a worker: of the prefix, of the requests
     int n_p;                  // CTAs on the prefix; the rest are on the requests
@@ -139,15 +162,15 @@ struct PfArgs {
     // less than one unit of 64 keys.
     int over_s;
     // A request with at least merge_n rows (four row blocks: the last one's empty
-    // rows are a fifth of its work at most) hardly gains from sharing the
-    // prefix's tiles with other requests' rows: its items take the prefix's tiles before their own ones, and one that no range
-    // cuts writes the output itself (direct: this call's items can).
+    // rows are a fifth of its work at most) takes the prefix's tiles before its own
+    // ones; an item with all of its row block's tiles writes the output itself
+    // (direct: this call's items can).
     int merge_n, direct, listed;   // listed: room for the prefix's row blocks in shared memory
     int qstep_p, qstep_s;     // rows between Q slots: a block's rows, in whole swizzle atoms
     float scale_log2;
 };
 
-enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kPfO, kPfPV, kPfDesc, kPfDescEmpty, kPfMerge };
+enum : int { kPfQEmpty = 61, kPfRingEmpty, kPfQFull, kPfRingFull, kPfP, kPfS, kPfO, kPfPV, kPfDesc, kPfDescEmpty };
 
 // ------------------------------------------------------------------ the list
 
@@ -518,6 +541,10 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 // (TMA; a slot is free as soon as this warp has read it, so nothing waits for
 // another warp), and keeps scores, weights and the accumulator in registers
 // (mma.sync m16n8k16).  An item's end costs a store of the rows and no barrier.
+// A step is 32 keys (16 at d = 256, where Q and O take the registers): 780 cycles
+// for 64 keys of a CTA's eight warps at d = 128, of which 8 K and 8 V copies at
+// the CTA's share of HBM are 700.  64 single tokens: 4.9 TB/s.  Eight warps that
+// share 128-key tiles and join in shared memory took 442 us where these take 349.
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -832,7 +859,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     t.items = reinterpret_cast<int*>(t.pref + a.B + 1);
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
-    t.block = M && a.merge_n < INT_MAX ? t.len + a.B : nullptr;   
+    t.block = M && a.merge_n < INT_MAX ? t.len + a.B : nullptr;
 
     {   // One barrier a thread, in the order of PfShared.
         constexpr int n1 = (offsetof(PfShared, p_ready) - offsetof(PfShared, d_full)) / 8;
@@ -1424,6 +1451,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 
 // ---------------------------------------------------------------------- join
 
+// Bound by latency (header, row, places, (m, l), O: five loads that depend on
+// one another, 3.4 us for one row) and, with many rows, by the segments' traffic
+// (512 rows of 32 heads: 23 us from a cold L2, a seventh of that out of it).
 // A warp joins kHeads heads of one key/value head in one row of q: their
 // segments are the same, their rows in a segment neighbours, so one set of
 // places serves all and their loads overlap (many rows: 4 or 2 where they divide

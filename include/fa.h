@@ -64,7 +64,7 @@ typedef enum {
     FA_ERR_ALIGN = -3,        /* a tensor is not 16-byte aligned            */
     FA_ERR_LAUNCH = -4,       /* CUDA reported an error at launch           */
     FA_ERR_TIMEOUT = -5,      /* a device-side wait gave up (see status)    */
-    FA_ERR_WORKSPACE = -6     /* backward workspace missing or too small    */
+    FA_ERR_WORKSPACE = -6     /* workspace missing or too small             */
 } fa_status;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -378,8 +378,12 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  *   x_j = alpha q . k_j,  O = softmax(x) V,  LSE = ln sum_j exp(x_j)
  *
  * The prefix's part is computed once for the rows of all requests (each key
- * and value of it is read once for up to 256 of them), every request's own
- * part from its pages; the two are joined by their maxima and sums.
+ * and value of it is read once for up to 256 rows of its head), every
+ * request's own part from its pages; the two are joined by their maxima and
+ * sums.  A request with four such blocks of rows of its own (128 rows each at
+ * d = 256) reads the prefix for itself.  Equal calls give equal results, bit for bit.
+ * Scores, sums and the output's accumulator are 32 bits wide, the weights bf16
+ * for the product with V.
  * q: bf16 [T, Hq, d], q_stride elements between tokens (>= Hq * d, a multiple
  * of 8); o: bf16 [T, Hq, d]; lse: float32 [Hq, T].
  * cu_seqlens [B+1] (device) delimits the requests' rows as in fa_fwd, each of
@@ -392,9 +396,15 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  * prefix's pages (ceil(prefix_len / page_size) entries), NULL when prefix_len
  * is 0.  Keys of absent pages (see above) are not seen.  A row that sees no
  * key at all gives O = 0 and LSE = -inf.  What the cache holds behind the
- * lengths does not matter, NaN and infinities included.
- * workspace: at least fa_prefix_workspace_size(...) bytes, 256-byte aligned,
- * no initialisation needed; calls that share one must not overlap on the GPU.
+ * lengths does not matter, NaN and infinities included; a NaN in a query or in
+ * a key gives NaN in the rows that see it, one in a value (or an infinity) may
+ * also reach the request's rows before it, whose weight for it is 0.
+ * o and lse must not overlap an input.  workspace: at least
+ * fa_prefix_workspace_size(...) bytes, 256-byte aligned, no initialisation
+ * needed; calls that share one must not overlap on the GPU (captured graphs
+ * that hold the same one included).  A call whose kernel gives up a wait (2 s)
+ * reports FA_ERR_TIMEOUT through fa_get_device_status; one that was not read
+ * does not stop later calls.
  * T == 0 is a no-op.
  * Errors: FA_ERR_INVALID (null pointer, T < 0, B, Hq, Hkv, num_pages or
  * table_width < 1, Hq % Hkv, prefix_len < 0, alpha not finite and > 0,
@@ -415,7 +425,8 @@ int fa_prefix_fwd(const void *q, int64_t q_stride, const void *k_pages, const vo
  * Bytes of device workspace fa_prefix_fwd needs for T rows of B requests of at
  * most max_seqlen rows each (the current device's SM count enters: call it
  * with the device current); 0 for invalid sizes.  Enough for every call with
- * at most these T and B, and this max_seqlen or one below it.
+ * at most these T and B, and this max_seqlen or one below it; max_seqlen above
+ * T counts as T.
  */
 size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen);
 
