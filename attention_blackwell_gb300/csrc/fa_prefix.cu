@@ -88,9 +88,9 @@ template <int D> struct Pf {
     static constexpr uint32_t kKVBox = kN * 128u;                // bytes of a box of a K/V tile
     static constexpr uint32_t kTile = kBoxes * kKVBox;
     static constexpr uint32_t kQBox = 16384u;                    // 128 rows x 128 B
-    static constexpr uint32_t kQTile = kBoxes * kQBox;
+    static constexpr uint32_t kQTile = D == 256 ? 0 : kBoxes * kQBox;   // d = 256: Q is in tensor memory
     static constexpr int kLook = 3 - kStreams;                   // tiles of one worker with S in flight
-    static constexpr int kRing = D == 64 ? 8 : 4;                // 128 KB of K/V tiles (even: few rows take K and V by pairs)
+    static constexpr int kRing = D == 64 ? 8 : D == 128 ? 4 : 6; // K/V tiles: 128 KB, at d = 256 192
     static constexpr uint32_t kTiles = kStreams * kQTile + kRing * kTile;
     static constexpr int kThreads = 384;
     static constexpr int kMaxSmem = 232448 - 4096;               // dynamic; the rest is PfShared
@@ -111,6 +111,7 @@ template <int D> struct Pf {
         return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2250) : (D == 64 ? 3500 : 4000);
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
+    static constexpr uint32_t kColQ = 384;   // d = 256: Q, bf16 pairs
 };
 
 // Of a row of q, for the joining kernel: its request's first row, rows and keys
@@ -359,7 +360,7 @@ struct PfShared {
     // One arrival a phase.
     uint64_t d_full[2][kDesc], d_empty[2][kDesc], q_full[kQMax], q_empty[kQMax], full[8], empty[8], s_full[2], pv_done[2], o_done[2], drain[2];
     // Four: the warps of a softmax warpgroup.
-    uint64_t p_ready[2];
+    uint64_t p_ready[2], q_ready;
     // One again: few rows, each warp's slots.
     uint64_t few_full[8][12];
     Item few_item[8][2];
@@ -507,15 +508,18 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
 
 // ------------------------------------------------------------------ products
 
+// Q from shared memory, at d = 256 from tensor memory: a 128 x 64 x 16 product with
+// both operands in shared memory is bound by its bandwidth (48 cycles, not 32).
 template <int D>
-__device__ __forceinline__ void pf_issue_qk(uint32_t d_tmem, uint32_t q_smem, uint32_t k_smem) {
+__device__ __forceinline__ void pf_issue_qk(uint32_t d_tmem, uint32_t q, uint32_t k_smem) {
     using G = Pf<D>;
     constexpr uint32_t idesc = idesc_bf16_f32(128, G::kN, 0, 0);
-    const uint64_t qd = sdesc_sw128(q_smem, 16, 1024), kd = sdesc_sw128(k_smem, 16, 1024);
+    const uint64_t qd = sdesc_sw128(q, 16, 1024), kd = sdesc_sw128(k_smem, 16, 1024);
     static_for<D / 16>([&](auto kc) {
         constexpr uint32_t k = kc;
         constexpr uint32_t ao = ((k >> 2) * G::kQBox + (k & 3) * 32) >> 4, bo = ((k >> 2) * G::kKVBox + (k & 3) * 32) >> 4;
-        umma_ss_k<ao, bo>(d_tmem, qd, kd, idesc, k > 0);
+        if constexpr (D == 256) umma_ts_k<k * 8, bo>(d_tmem, q, kd, idesc, k > 0);
+        else umma_ss_k<ao, bo>(d_tmem, qd, kd, idesc, k > 0);
     });
 }
 
@@ -980,7 +984,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 pg[x][0] = part < parts ? d.page[part] : -1;
                 row[x][0] = ((pg[x][0] * a.Hkv + d.hk) << a.ps_log2) + ((d.j * kN + (part << part_log2)) & ((1 << a.ps_log2) - 1));
                 if (!load(&tk, pg[x][0], row[x][0])) return false;
-                if (flags & kFirst) {
+                if (kStreams == 2 && (flags & kFirst)) {
                     const uint32_t i = n_item[x], s = q_slot(x, i);
                     if (!pf_wait(&sh.q_empty[s], ((i / qn) & 1) ^ 1, wc, kPfQEmpty)) return false;
                     const int boxes = two ? 2 * kBoxes : kBoxes;
@@ -1109,16 +1113,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const int flags = sh.desc[0][n % kDesc].flags, buf = n & 1;
                         if (!(flags & kMore)) break;
                         const uint32_t i = n < 2 ? n : 2 * n - 1;
-                        if ((flags & kFirst) && !(ok = pf_wait(&sh.q_full[q_slot(0, items)], (items / qn) & 1, wc, kPfQFull))) break;
-                        items += flags & kFirst ? 1 : 0;
+                        if ((flags & kFirst) && !(ok = pf_wait(&sh.q_ready, items++ & 1, wc, kPfQFull))) break;
                         if (!(ok = wait_tile(i))) break;
                         // S goes where P of two tiles before was read from.
                         if (n >= 2 && !(ok = pf_wait(&sh.pv_done[buf], ((n - 2) >> 1) & 1, wc, kPfPV))) break;
                         tc_fence_after();
-                        pf_issue_qk<D>(col_s(buf), q_addr(0, items - 1), sRing + i % kRing * G::kTile);
+                        pf_issue_qk<D>(col_s(buf), tmem + G::kColQ, sRing + i % kRing * G::kTile);
                         umma_commit_w(&sh.s_full[buf]);
                         umma_commit_w(&sh.empty[i % kRing]);
-                        if (flags & kLast) umma_commit_w(&sh.q_empty[q_slot(0, items - 1)]);
+                        if (flags & kLast) umma_commit_w(&sh.q_empty[0]);
                     }
                 } else {
                     if ((ok = desc_wait(0, 0))) {
@@ -1274,11 +1277,41 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
         const uint32_t tO = lanes + wg * G::kColO1;
         const int tok = r / a.G + (two ? wg * a.tq : 0);      // token of the block
         const float scale = a.scale_log2;
+        if (kStreams == 1 && wg == 1) {
+            // d = 256 has one worker: these warps bring every item's Q into tensor
+            // memory, a row a thread.  The loads run while the products of the item
+            // before do; the stores wait for its last S.
+            Walk<D, M> walk;
+            walk.start(a, t, hdr, 0);
+            Item it;
+            for (uint32_t i = 0; walk.next(a, t, it); ++i) {
+                uint32_t v[D / 64][32];
+                const bool real = r < a.tq * a.G && tok < it.ntok;
+                const uint4* src = reinterpret_cast<const uint4*>(a.q + (long long)(it.tok0 + tok) * a.q_stride + (it.hk * a.G + r - tok * a.G) * D);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 x = real ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+                    v[c / 8][c % 8 * 4] = x.x;
+                    v[c / 8][c % 8 * 4 + 1] = x.y;
+                    v[c / 8][c % 8 * 4 + 2] = x.z;
+                    v[c / 8][c % 8 * 4 + 3] = x.w;
+                }
+                if (i > 0 && !pf_wait(&sh.q_empty[0], (i - 1) & 1, wc, kPfQEmpty)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int b = 0; b < D / 64; ++b) tmem_st32(lanes + G::kColQ + 32 * b, v[b]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.q_ready);
+            }
+            __syncwarp();
+        }
         uint32_t items = 0;
         bool ok = true, valid = false, live_warp = false;
         int seg = 0, tok0 = 0, head0 = 0, lim_row = 0;
         float m_ref = -INFINITY, l = 0.f;
-        for (uint32_t n = 0; x < workers; ++n) {   // d = 256: one worker, the second four warps have none
+        for (uint32_t n = 0; x < workers; ++n) {
             if (!(ok = desc_wait(x, n))) break;
             const Desc& d = sh.desc[x][n % kDesc];
             const int flags = d.flags, live = d.live, k0 = d.j * kN;
@@ -1781,8 +1814,8 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     const long long slots = (long long)num_pages * Hkv * page_size;
     const int part = page_size < kN ? page_size : kN;
     int rc = FA_OK;
-    if (prefix_tiles) rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
-    if (rc == FA_OK && own_tiles) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
+    if (d != 256 && prefix_tiles) rc = make_map_rows(&tq_p, q, d, Hq, T, q_stride, G, box_p);
+    if (d != 256 && rc == FA_OK && own_tiles) rc = make_map_rows(&tq_s, q, d, Hq, T, q_stride, G, box_s);
     if (rc == FA_OK && (prefix_tiles || own_tiles)) {
         rc = make_map_pages(&tk, k_pages, d, slots, part);
         if (rc == FA_OK) rc = make_map_pages(&tv, v_pages, d, slots, part);
