@@ -1210,6 +1210,9 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // ------------------------------------------------------ list walkers
             // Pages of four tiles at a time, a lane each; the next four's loads
             // (the next item's, past an item's end) run while these are handed on.
+            // The first four are handed on before any others are looked up: every
+            // role waits for them.  Rounds: look up 0; hand on 0; look up 1; look up 2
+            // and hand on 1; look up 3 and hand on 2; ...
             const int x = warp - (kSoftWarps + 2), q = lane >> 3, part = lane & 7;
             Walk<D, M> walk;
             walk.start(a, t, hdr, x);
@@ -1223,19 +1226,26 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                 return p >= 0 && p < a.P ? p : -1;
             };
             uint32_t n = 0;
-            bool ok = true, more = walk.next(a, t, it);
-            int j = more ? it.j0 : 0, val = more ? pages(it, j) : -1;
-            while (ok) {
-                int j_next = j + 4, val_next = -1;
-                bool more_next = more;
-                ahead = it;
-                if (more) {
-                    if (j_next >= it.j1) {
-                        more_next = walk.next(a, t, ahead);
-                        j_next = more_next ? ahead.j0 : 0;
-                    }
-                    if (more_next) val_next = pages(ahead, j_next);
+            bool ok = true, more = false, more_next = true;
+            int j = 0, val = -1, j_next = 0, val_next = -1;
+            ahead.j0 = ahead.j1 = 0;
+            for (int round = 0; ok; ++round) {
+                const bool hand_on = round == 1 || round > 2;
+                if (hand_on) {
+                    it = ahead;
+                    more = more_next;
+                    j = j_next;
+                    val = val_next;
                 }
+                if (more_next && round != 1) {
+                    j_next += 4;
+                    if (j_next >= ahead.j1) {
+                        more_next = walk.next(a, t, ahead);
+                        j_next = ahead.j0;
+                    }
+                    val_next = more_next ? pages(ahead, j_next) : -1;
+                }
+                if (!hand_on) continue;
                 const int last = more ? min(j + 4, it.j1) : j + 1;
                 for (int jj = j; jj < last && ok; ++jj, ++n) {
                     if (!(ok = pf_wait(&sh.d_empty[x][n % kDesc], ((n / kDesc) & 1) ^ 1, wc, kPfDescEmpty))) break;
@@ -1261,10 +1271,6 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                     if (lane == 0) mbar_arrive(&sh.d_full[x][n % kDesc]);
                 }
                 if (!more) break;
-                it = ahead;
-                more = more_next;
-                j = j_next;
-                val = val_next;
             }
             __syncwarp();
         }
