@@ -447,19 +447,23 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
         if (base) __syncthreads();
         if (lane == 31) sh.scan[warp] = make_int4(u, it, blk, 0);
         __syncthreads();
-        int u_all = 0, it_all = 0, blk_all = 0;
+        // The warps' sums, a lane each.
+        int4 all = lane < kWarps ? sh.scan[lane] : make_int4(0, 0, 0, 0);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int4 x = sh.scan[w];
-            if (w == warp) {
-                u += units + u_all;
-                it += items + it_all;
-                blk += blocks + blk_all;
+        for (int o = 1; o < kWarps; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, all.x, o), y = __shfl_up_sync(0xffffffffu, all.y, o), z = M ? __shfl_up_sync(0xffffffffu, all.z, o) : 0;
+            if (lane >= o) {
+                all.x += x;
+                all.y += y;
+                if (M) all.z += z;
             }
-            u_all += x.x;
-            it_all += x.y;
-            blk_all += x.z;
         }
+        auto sum_of = [&](int x, int w) { return __shfl_sync(0xffffffffu, x, w); };
+        const int u_all = sum_of(all.x, kWarps - 1), it_all = sum_of(all.y, kWarps - 1), blk_all = M ? sum_of(all.z, kWarps - 1) : 0;
+        const int u_before = sum_of(all.x, max(warp - 1, 0)), it_before = sum_of(all.y, max(warp - 1, 0)), blk_before = M ? sum_of(all.z, max(warp - 1, 0)) : 0;
+        u += units + (warp ? u_before : 0);
+        it += items + (warp ? it_before : 0);
+        if (M) blk += blocks + (warp ? blk_before : 0);
         if (i < a.B) {
             t.pref[i] = u - u_own;
             t.items[i] = it - it_own;
