@@ -102,13 +102,18 @@ template <int D> struct Pf {
     // all but the first; alone, each tile comes from HBM for 256 rows only, and
     // its latency grows with the share of the traffic (`own`, 0 to 1) that the
     // requests' CTAs ask for at the same time.
-    __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 600 : D == 128 ? 780 : 1900) * halves; }
+    __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 600 : D == 128 ? 780 : 900) * halves; }
+    // Few rows at d = 256, where a warp takes 15000 cycles for a unit: worth it for
+    // items of few units (of them over_s for the item), else one row tile.  100
+    // keys a request of 8 heads: 44 us for 128 requests, one row tile 60; 2000 keys
+    // and 16 requests over a long prefix: 107, one row tile 84.
+    __host__ __device__ static constexpr bool few_items(int units, int items) { return D != 256 || units < 14LL * items; }
     __device__ static float cost_p(int mode, int halves, bool shared, float own) {
-        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2400)
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 1600)
              : D == 64 ? (shared ? 3400 : 3400 + 2600 * own) : (shared ? 3700 : 4400 + 4000 * own);
     }
     __device__ static float cost_s(int mode, int halves) {
-        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 2250) : (D == 64 ? 3500 : 4000);
+        return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 1550) : (D == 64 ? 3500 : 4000);
     }
     static constexpr uint32_t kColO1 = 128, kColS = 256, kColSStep = kN;   // O of the second worker or tile, S
     static constexpr uint32_t kColQ = 384;   // d = 256: Q, bf16 pairs
@@ -135,7 +140,8 @@ struct PfHeader {
     int blocks;               // prefix: row blocks
     int chunk, chunks;        // prefix: tiles an item (the last chunk's may have fewer), items a row block
     int bad;                  // a request has more rows than max_seqlen
-    int pad[9];
+    int mode_s;               // the requests' mode (see few_items)
+    int pad[8];
 };
 
 struct PfArgs {
@@ -257,6 +263,10 @@ __device__ __forceinline__ int item_units(const PfArgs& a, const PfTables& t, in
 // Where unit u of an item's `units` falls among its `tiles`.
 __device__ __forceinline__ int tile_of(int u, int units, int tiles) { return (int)((long long)u * tiles / units); }
 
+// Workers a CTA on the requests.
+template <int D>
+__device__ __forceinline__ int width_s(const PfArgs& a, const PfHeader& h) { return D == 256 && h.mode_s == kOne ? 1 : a.width_s; }
+
 // A worker's walk over its range of units.  Everything fits 32 bits: the host
 // refuses longer lists.
 template <int D, bool M>
@@ -273,7 +283,7 @@ struct Walk {
         chunks = h.chunks;
         blocks = h.blocks;
         pre = c < h.n_p;
-        const int width = pre ? a.width_p : a.width_s;
+        const int width = pre ? a.width_p : width_s<D>(a, h);
         worker = (pre ? c : c - h.n_p) * width + x;
         const int per = pre ? h.per_p : h.per_s, all = pre ? a.Hkv * h.blocks * a.tiles_p : t.pref[a.B];
         // worker * per passes the list's end by at most a CTA count times per.
@@ -480,11 +490,12 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
     }
     __syncthreads();
     PfHeader h;
+    h.mode_s = a.mode_s == kFew && !Pf<D>::few_items(units, items) ? kOne : a.mode_s;
     h.blocks = M && t.block ? blocks : a.blocks_p;
     const int grid = gridDim.x, units_p = a.Hkv * h.blocks * a.tiles_p;
     const float keys_p = (float)units_p * (1 << a.ulog_p), keys_s = (float)units * (1 << a.ulog_s);
     const float cp = (float)units_p * Pf<D>::cost_p(a.mode_p, a.halves_p, h.blocks > 1, keys_s / fmaxf(keys_p + keys_s, 1.f));
-    const float cs = (float)units * Pf<D>::cost_s(a.mode_s, a.halves_s);
+    const float cs = (float)units * Pf<D>::cost_s(h.mode_s, a.halves_s);
     int np = units_p == 0 ? 0 : (units == 0 ? grid : (int)(grid * (cp / (cp + cs)) + 0.5f));
     if (units_p > 0 && units > 0) np = max(1, min(grid - 1, np));
     int wp = np * a.width_p;
@@ -497,7 +508,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
         h.per_p = (a.tiles_p + k - 1) / k;
         np = max(1, min(np, cdiv(units_p, h.per_p * a.width_p)));
     }
-    const int ws = max(1, grid - np) * a.width_s;
+    const int ws = max(1, grid - np) * width_s<D>(a, h);
     h.n_p = np;
     h.per_s = units ? (units + ws - 1) / ws : 1;
     h.chunk = h.blocks > 1 ? max(1, min(h.per_p, a.tiles_p)) : max(1, a.tiles_p);
@@ -897,7 +908,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
     // Parts of a tile: whole pages, or one part where a page is larger.
     const int part_log2 = min(a.ps_log2, kN == 64 ? 6 : 7), parts = kN >> part_log2;
     const bool pre = (int)blockIdx.x < hdr.n_p;
-    const int mode = pre ? a.mode_p : a.mode_s;
+    const int mode = pre ? a.mode_p : hdr.mode_s;
     const bool two = kStreams == 2 && mode == kTwo, few = mode == kFew;
     const int workers = two ? 1 : kStreams;
     // Q slots: two row tiles, one slot of both; else as many in a worker's row
@@ -1750,14 +1761,15 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
 
     const int kN = d == 256 ? 64 : 128;
-    // Few rows: at d = 256 up to 16 (two warps for 32 rows take 4000 cycles a unit of
-    // 64 keys, one row tile 2700), else up to 32 (1560 a unit at d = 128, one row
-    // tile 2500).
-    const int mode_p = T * (long long)G <= few_limit(d) ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
+    // Few rows: at d = 256 up to 16 of a request's (see few_items; two warps for 32
+    // rows take 4000 cycles a unit of 64 keys, one row tile 1600), never the prefix's
+    // (3 rows of 4 heads, 32768 keys: 97 us, one row tile 61); else up to 32 (1560 a
+    // unit at d = 128, one row tile 2500).
+    const int mode_p = d != 256 && T * (long long)G <= few_limit(d) ? kFew : d != 256 && T > w.tq ? kTwo : kOne;
     const int mode_s = max_seqlen * (long long)G <= few_limit(d) ? kFew : d != 256 && max_seqlen > w.tq ? kTwo : kOne;
     const int ulog_p = mode_p == kFew || d == 256 ? 6 : 7, ulog_s = mode_s == kFew || d == 256 ? 6 : 7;
     // The list of tiles at its longest, with room to spare in 32 bits.
-    const int over_s = mode_s == kFew ? 1 : 2;
+    const int over_s = mode_s == kFew && d != 256 ? 1 : 2;
     const long long tiles_s = (((long long)table_width * page_size + (1 << ulog_s) - 1) >> ulog_s) + over_s;
     const long long tiles_p = ((long long)prefix_len + (1 << ulog_p) - 1) >> ulog_p;   // both units are a tile where own items take the prefix's
     const long long blocks_s = (long long)Hkv * (T / w.tb + (T < B ? T : B)), blocks_p = (long long)Hkv * ((T + w.tb - 1) / w.tb);
@@ -1820,7 +1832,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     CUtensorMap tq_p = {}, tq_s = {}, tk = {}, tv = {}, tk_few = {}, tv_few = {};
     // Only the maps that a mode of this call uses are encoded (each costs the
     // host a third of a microsecond).
-    const bool prefix_tiles = prefix_len > 0 && mode_p != kFew, own_tiles = mode_s != kFew;
+    const bool prefix_tiles = prefix_len > 0 && mode_p != kFew, own_tiles = mode_s != kFew || d == 256;
     const long long slots = (long long)num_pages * Hkv * page_size;
     const int part = page_size < kN ? page_size : kN;
     int rc = FA_OK;
@@ -1831,7 +1843,7 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
         if (rc == FA_OK) rc = make_map_pages(&tv, v_pages, d, slots, part);
     }
     // Few rows: 16 keys a copy whatever the page size, all of d at once.
-    if (rc == FA_OK && (!prefix_tiles || !own_tiles)) {
+    if (rc == FA_OK && (mode_p == kFew || mode_s == kFew)) {
         rc = make_map_steps(&tk_few, k_pages, d, slots);
         if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
     }

@@ -343,6 +343,18 @@ def test_one_long_request_among_short_ones(fa, d):
     b.check(fa, *b.run(fa))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (16, 1), (3, 3)])
+def test_single_tokens_with_long_histories(fa, d, hq, hkv):
+    """Few rows and many keys: at d = 256 the requests' lists decide the kernel's
+    shape, so also the same rows with short lists, and both after an absent page."""
+    for s in ([2000, 3001, 1500], [900, 900, 20], [100, 3, 1]):
+        b = Batch(hq, hkv, d, 32, 90, s, [1, 1, 1], seed=d + s[0])
+        b.check(fa, *b.run(fa))
+        b.table[0][1] = -1
+        b.check(fa, *b.run(fa))
+
+
 def test_many_requests(fa):
     g = np.random.default_rng(4)
     s = [int(x) for x in g.integers(0, 90, 1024)]
