@@ -231,7 +231,7 @@ constexpr int kMore = 1, kFirst = 2, kLast = 4, kRagged = 8, kWhole = 16;   // k
 constexpr int kDesc = 8;    // tiles the walkers run ahead by
 constexpr int kQMax = 8;    // Q slots
 
-__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // Item k of a request's row blocks: from both ends by turns, so that under the
 // causal mask two neighbours cost what any other two do.
@@ -558,7 +558,7 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 // warps when there are more than 16 rows (each takes 16): it walks its range of
 // the list, copies 16 keys of K or V at a time into a ring of its own
 // (TMA; a slot is free as soon as this warp has read it, so nothing waits for
-// another warp), and keeps scores, weights and the accumulator in registers
+// another warp), and keeps scores, wfours and the accumulator in registers
 // (mma.sync m16n8k16).  An item's end costs a store of the rows and no barrier.
 // A step is 32 keys (16 at d = 256, where Q and O take the registers): 780 cycles
 // for 64 keys of a CTA's eight warps at d = 128, of which 8 K and 8 V copies at
@@ -785,7 +785,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
                         for (int i = 0; i < 2 * kKT; ++i) {
                             const float p0 = ex2_mufu(fmaf(s[i][2 * h], scale, -use)), p1 = ex2_mufu(fmaf(s[i][2 * h + 1], scale, -use));
                             l[h] += p0 + p1;
-                            p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
+                            p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit wfours feed the product; l keeps 32 bits
                         }
                     }
                 }
@@ -1430,7 +1430,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
                         if (i & 1) lb = f2_add(lb, f2_pack(p0, p1));
                         else la = f2_add(la, f2_pack(p0, p1));
-                        pk[i] = pack_bf16x2(p0, p1);   // 16-bit weights feed the tensor core; l keeps 32 bits
+                        pk[i] = pack_bf16x2(p0, p1);   // 16-bit wfours feed the tensor core; l keeps 32 bits
                     }
                     tmem_st16(tS + st * 16, pk);
                 }
@@ -1512,139 +1512,186 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 // segments are the same, their rows in a segment neighbours, so one set of
 // places serves all and their loads overlap (many rows: 4 or 2 where they divide
 // the group).  kSplit: the eight warps of a block share one head's segments
-// (few rows, where a warp each would leave most SMs idle).
-template <int D, int kHeads, bool kSplit>
+// (few rows, where a warp each would leave most SMs idle).  kRows > 1: calls whose
+// items may have written their rows already.  A warp looks at so many rows, a lane
+// each, and the block's warps share what there is to join.  Six prompts of up to
+// 2048 tokens over 8192 shared keys, the whole call: 1113 us with a row a warp,
+// 1070 with four (or eight: but four prompts without a prefix 110, 101 and 118).
+template <int D, int kHeads, bool kSplit, int kRows>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     constexpr int E = D / 32, H = kHeads;
-    static_assert(!kSplit || H == 1, "one head a block");
+    static_assert((!kSplit || H == 1) && (!kSplit || kRows == 1), "one head and row a block");
     __shared__ float s_o[kSplit ? 8 : 1][kSplit ? D : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = a.Hq / H;
     const long long w = kSplit ? blockIdx.x : blockIdx.x * 8LL + warp;
-    if (w >= (long long)a.T * groups) return;
-    const int t = (int)(w / groups), h0 = (int)(w - (long long)t * groups) * H, hk = h0 / a.G, g0 = h0 - hk * a.G;
+    const int t0 = (int)(w / groups) * kRows;
+    int h0 = (int)(w % groups) * H, hk = h0 / a.G;
+    if (kRows == 1 && t0 >= a.T) return;
     grid_wait();
     const PfHeader h = *a.hdr;
-    const PfRow r = a.rows[t];
-    if (h.bad || r.n == 0) return;
-    const int i = t - r.c0, nb = cdiv(r.n, a.tb), rb = i / a.tb, blk = r.block;
-    // Most segments that an item of the prefix can have, and room for all chunks'.
-    const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2, slots = blk >= 0 ? most * h.chunks : 0;
-    // The request's item: its units from u0 on, the workers that they fall to.
-    const int units = units_of<true>(a, r.n, r.s), seen = r.s - r.n + min(r.n, (rb + 1) * a.tb);
-    const int tiles = prefix_tiles<true>(a, r.n) + (seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
-    const int item = hk * nb + index_of(rb, nb), u0 = r.pref + item * units, c_own = u0 / h.per_s;
-    const int all = slots + (tiles > 0 ? (u0 + units - 1) / h.per_s - c_own + 1 : 0);
-    // Row (of head h0) in the k-th segment, the prefix's first, then the
-    // request's, each in the list's order; negative: there is none.
-    if (a.direct && slots == 0 && tiles > 0) {
-        // Written already if one worker had all its tiles: the first that had any.
-        for (int c = c_own;; ++c) {
-            const int to = tile_of(min(units, c * h.per_s + h.per_s - u0), units, tiles);
-            if (to == tiles && tile_of(max(0, c * h.per_s - u0), units, tiles) == 0) return;
-            if (to > 0) break;
-        }
-    }
-    auto place = [&](int k) -> long long {
-        if (k >= all) return -1;
-        if (k < slots) {
-            const int ch = k / most, j = k - ch * most, len = min(h.chunk, a.tiles_p - ch * h.chunk);
-            const int v0 = hk * h.blocks * a.tiles_p + ch * h.chunk * h.blocks + blk * len;
-            const int ca = v0 / h.per_p, cb = (v0 + len - 1) / h.per_p;
-            if (ca + j > cb) return -1;
-            return (long long)((hk * h.chunks + ch) * h.blocks + blk + ca + j) * a.rows_p + t % a.tb * a.G + g0;
-        }
-        const int c = c_own + k - slots;
-        const int from = max(0, c * h.per_s - u0), to = min(units, c * h.per_s + h.per_s - u0);
-        if (tile_of(from, units, tiles) >= tile_of(to, units, tiles)) return -1;
-        return (long long)(r.items + item + c) * a.rows_s + (i - rb * a.tb) * a.G + g0;
-    };
-    float M[H], L[H], acc[H][E];
-#pragma unroll
-    for (int x = 0; x < H; ++x) {
-        M[x] = -INFINITY;
-        L[x] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[x][e] = 0.f;
-    }
-    // Places and (m, l) of the first 32 segments, one a lane; rarely there are more.
-    float2 ml[H];
-    long long at = -1;
-    auto load_ml = [&](int k) {
-        at = place(k);
-#pragma unroll
-        for (int x = 0; x < H; ++x) ml[x] = at >= 0 ? (k < slots ? a.ml_p : a.ml_s)[at + x] : make_float2(-INFINITY, 0.f);
-    };
-    for (int k0 = (all - 1) / 32 * 32; k0 >= 0; k0 -= 32) {
-        load_ml(k0 + lane);
-#pragma unroll
-        for (int x = 0; x < H; ++x) M[x] = fmaxf(M[x], ml[x].x);
-    }
-#pragma unroll
-    for (int x = 0; x < H; ++x)
-        for (int o = 16; o; o >>= 1) M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], o));
-    for (int k0 = 0; k0 < all; k0 += 32) {
-        if (k0) load_ml(k0 + lane);
-        float f[H];
-#pragma unroll
-        for (int x = 0; x < H; ++x) {
-            f[x] = ml[x].y == 0.f ? 0.f : ex2_mufu(ml[x].x - M[x]);   // a sum of 0: no key seen; a NaN stays one
-            L[x] += f[x] * ml[x].y;
-        }
-        const int cnt = min(32, all - k0);
-#pragma unroll 4
-        for (int k = kSplit ? warp : 0; k < cnt; k += kSplit ? 8 : 1) {
-            const long long row = __shfl_sync(0xffffffffu, at, k);
-            if (row < 0) continue;
-            const float* src = (k0 + k < slots ? a.o_p : a.o_s) + row * D + lane * E;
-#pragma unroll
-            for (int x = 0; x < H; ++x) {
-                const float fk = __shfl_sync(0xffffffffu, f[x], k);
-                float v[E];
-                if constexpr (E == 2) {
-                    const float2 q = *reinterpret_cast<const float2*>(src + x * D);
-                    v[0] = q.x;
-                    v[1] = q.y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; e += 4) {
-                        const float4 q = *reinterpret_cast<const float4*>(src + x * D + e);
-                        v[e] = q.x;
-                        v[e + 1] = q.y;
-                        v[e + 2] = q.z;
-                        v[e + 3] = q.w;
-                    }
-                }
-                // A segment in which the row saw no key has weight 0 and holds
-                // whatever its idle accumulator held.
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[x][e] = fk > 0.f ? fmaf(fk, v[e], acc[x][e]) : acc[x][e];
+    if (h.bad) return;
+    // Most segments that an item of the prefix can have.
+    const int most = h.chunk > h.per_p ? (h.chunk - 1) / h.per_p + 2 : 2;
+    PfRow r;
+    int i, rb, blk, slots, tiles, units, item, u0, c_own, all;   // slots: room for all chunks' segments
+    // What there is to join for row t; false: nothing, or it is written already.
+    auto look = [&](int t) -> bool {
+        r = a.rows[t];
+        if (r.n == 0) return false;
+        i = t - r.c0;
+        const int nb = cdiv(r.n, a.tb);
+        rb = i / a.tb;
+        blk = r.block;
+        slots = blk >= 0 ? most * h.chunks : 0;
+        // The request's item: its units from u0 on, the workers that they fall to.
+        units = units_of<true>(a, r.n, r.s);
+        const int seen = r.s - r.n + min(r.n, (rb + 1) * a.tb);
+        tiles = prefix_tiles<true>(a, r.n) + (seen > 0 ? (seen + (1 << a.ulog_s) - 1) >> a.ulog_s : 0);
+        item = hk * nb + index_of(rb, nb);
+        u0 = r.pref + item * units;
+        c_own = u0 / h.per_s;
+        all = slots + (tiles > 0 ? (u0 + units - 1) / h.per_s - c_own + 1 : 0);
+        if (a.direct && slots == 0 && tiles > 0) {
+            // Written already if one worker had all its tiles: the first that had any.
+            for (int c = c_own;; ++c) {
+                const int to = tile_of(min(units, c * h.per_s + h.per_s - u0), units, tiles);
+                if (to == tiles && tile_of(max(0, c * h.per_s - u0), units, tiles) == 0) return false;
+                if (to > 0) break;
             }
         }
-    }
-#pragma unroll
-    for (int x = 0; x < H; ++x)
-        for (int o = 16; o; o >>= 1) L[x] += __shfl_xor_sync(0xffffffffu, L[x], o);
-    if constexpr (kSplit) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[0][e];
+        return true;
+    };
+    __shared__ int s_count[8], s_task[kRows > 1 ? 64 : 1][2];
+    int tasks = 1;
+    if constexpr (kRows > 1) {
+        static_assert(kRows <= 8, "room for the tasks");
+        const uint32_t todo = __ballot_sync(0xffffffffu, lane < kRows && t0 + lane < a.T && look(t0 + lane));
+        if (lane == 0) s_count[warp] = __popc(todo);
         __syncthreads();
-        if (warp) return;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            for (int y = 1; y < 8; ++y) acc[0][e] += s_o[y][lane * E + e];
+        tasks = 0;
+        int at = __popc(todo & ((1u << lane) - 1u));
+        for (int y = 0; y < 8; ++y) {
+            if (y < warp) at += s_count[y];
+            tasks += s_count[y];
+        }
+        if (todo >> lane & 1) {
+            s_task[at][0] = t0 + lane;
+            s_task[at][1] = h0;
+        }
+        __syncthreads();
     }
+    for (int task = kRows > 1 ? warp : 0; task < tasks; task += 8) {
+        const int t = kRows > 1 ? s_task[task][0] : t0;
+        if (kRows > 1) {
+            h0 = s_task[task][1];
+            hk = h0 / a.G;
+        }
+        const int g0 = h0 - hk * a.G;
+        if (!look(t)) return;
+        // Row (of head h0) in the k-th segment, the prefix's first, then the
+        // request's, each in the list's order; negative: there is none.
+        auto place = [&](int k) -> long long {
+            if (k >= all) return -1;
+            if (k < slots) {
+                const int ch = k / most, j = k - ch * most, len = min(h.chunk, a.tiles_p - ch * h.chunk);
+                const int v0 = hk * h.blocks * a.tiles_p + ch * h.chunk * h.blocks + blk * len;
+                const int ca = v0 / h.per_p, cb = (v0 + len - 1) / h.per_p;
+                if (ca + j > cb) return -1;
+                return (long long)((hk * h.chunks + ch) * h.blocks + blk + ca + j) * a.rows_p + t % a.tb * a.G + g0;
+            }
+            const int c = c_own + k - slots;
+            const int from = max(0, c * h.per_s - u0), to = min(units, c * h.per_s + h.per_s - u0);
+            if (tile_of(from, units, tiles) >= tile_of(to, units, tiles)) return -1;
+            return (long long)(r.items + item + c) * a.rows_s + (i - rb * a.tb) * a.G + g0;
+        };
+        float M[H], L[H], acc[H][E];
 #pragma unroll
-    for (int x = 0; x < H; ++x) {
-        const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
-        uint32_t out[E / 2];
+        for (int x = 0; x < H; ++x) {
+            M[x] = -INFINITY;
+            L[x] = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[x][e] * inv, acc[x][e + 1] * inv);
-        uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + h0 + x) * D) + lane * (E / 2);
-        if constexpr (E == 2) *dst = out[0];
-        else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-        else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-        if (lane == 0) a.lse[(long long)(h0 + x) * a.T + t] = L[x] == 0.f ? -INFINITY : (M[x] + __log2f(L[x])) * 0.69314718055994531f;
+            for (int e = 0; e < E; ++e) acc[x][e] = 0.f;
+        }
+        // Places and (m, l) of the first 32 segments, one a lane; rarely there are more.
+        float2 ml[H];
+        long long at = -1;
+        auto load_ml = [&](int k) {
+            at = place(k);
+#pragma unroll
+            for (int x = 0; x < H; ++x) ml[x] = at >= 0 ? (k < slots ? a.ml_p : a.ml_s)[at + x] : make_float2(-INFINITY, 0.f);
+        };
+        for (int k0 = (all - 1) / 32 * 32; k0 >= 0; k0 -= 32) {
+            load_ml(k0 + lane);
+#pragma unroll
+            for (int x = 0; x < H; ++x) M[x] = fmaxf(M[x], ml[x].x);
+        }
+#pragma unroll
+        for (int x = 0; x < H; ++x)
+            for (int o = 16; o; o >>= 1) M[x] = fmaxf(M[x], __shfl_xor_sync(0xffffffffu, M[x], o));
+        for (int k0 = 0; k0 < all; k0 += 32) {
+            if (k0) load_ml(k0 + lane);
+            float f[H];
+#pragma unroll
+            for (int x = 0; x < H; ++x) {
+                f[x] = ml[x].y == 0.f ? 0.f : ex2_mufu(ml[x].x - M[x]);   // a sum of 0: no key seen; a NaN stays one
+                L[x] += f[x] * ml[x].y;
+            }
+            const int cnt = min(32, all - k0);
+#pragma unroll 4
+            for (int k = kSplit ? warp : 0; k < cnt; k += kSplit ? 8 : 1) {
+                const long long row = __shfl_sync(0xffffffffu, at, k);
+                if (row < 0) continue;
+                const float* src = (k0 + k < slots ? a.o_p : a.o_s) + row * D + lane * E;
+#pragma unroll
+                for (int x = 0; x < H; ++x) {
+                    const float fk = __shfl_sync(0xffffffffu, f[x], k);
+                    float v[E];
+                    if constexpr (E == 2) {
+                        const float2 q = *reinterpret_cast<const float2*>(src + x * D);
+                        v[0] = q.x;
+                        v[1] = q.y;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; e += 4) {
+                            const float4 q = *reinterpret_cast<const float4*>(src + x * D + e);
+                            v[e] = q.x;
+                            v[e + 1] = q.y;
+                            v[e + 2] = q.z;
+                            v[e + 3] = q.w;
+                        }
+                    }
+                    // A segment in which the row saw no key has weight 0 and holds
+                    // whatever its idle accumulator held.
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[x][e] = fk > 0.f ? fmaf(fk, v[e], acc[x][e]) : acc[x][e];
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < H; ++x)
+            for (int o = 16; o; o >>= 1) L[x] += __shfl_xor_sync(0xffffffffu, L[x], o);
+        if constexpr (kSplit) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[0][e];
+            __syncthreads();
+            if (warp) return;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                for (int y = 1; y < 8; ++y) acc[0][e] += s_o[y][lane * E + e];
+        }
+#pragma unroll
+        for (int x = 0; x < H; ++x) {
+            const float inv = L[x] == 0.f ? 0.f : 1.f / L[x];
+            uint32_t out[E / 2];
+#pragma unroll
+            for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[x][e] * inv, acc[x][e + 1] * inv);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + h0 + x) * D) + lane * (E / 2);
+            if constexpr (E == 2) *dst = out[0];
+            else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+            else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (lane == 0) a.lse[(long long)(h0 + x) * a.T + t] = L[x] == 0.f ? -INFINITY : (M[x] + __log2f(L[x])) * 0.69314718055994531f;
+        }
     }
 }
 
@@ -1704,12 +1751,18 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to two an SM a block each; up to 64 an SM (one or
     // two rounds of warps) a warp each; past that four or two a warp.
-    auto warps = [&](int heads) { return (int)(((long long)a.T * (a.Hq / heads) + 7) / 8); };
+    auto warps = [&](int heads, int each) { return (int)(((long long)cdiv(a.T, each) * (a.Hq / heads) + 7) / 8); };
     cudaError_t e;
-    if (rows <= 2LL * sms) e = launch_dependent(prefix_join_kernel<D, 1, true>, (int)rows, 256, 0, stream, a);
-    else if (rows <= 64LL * sms || a.G % 2) e = launch_dependent(prefix_join_kernel<D, 1, false>, warps(1), 256, 0, stream, a);
-    else if (a.G % 4) e = launch_dependent(prefix_join_kernel<D, 2, false>, warps(2), 256, 0, stream, a);
-    else e = launch_dependent(prefix_join_kernel<D, 4, false>, warps(4), 256, 0, stream, a);
+    // Four rows a warp where items may have written theirs (see prefix_join_kernel).
+    constexpr int kEach = M ? 4 : 1;
+    const bool fours = M && rows > 64LL * sms && (a.tiles_p == 0 || a.max_seqlen >= a.merge_n);
+    if (rows <= 2LL * sms) e = launch_dependent(prefix_join_kernel<D, 1, true, 1>, (int)rows, 256, 0, stream, a);
+    else if (rows <= 64LL * sms || (a.G % 2 && !fours)) e = launch_dependent(prefix_join_kernel<D, 1, false, 1>, warps(1, 1), 256, 0, stream, a);
+    else if (a.G % 4 && !fours) e = launch_dependent(prefix_join_kernel<D, 2, false, 1>, warps(2, 1), 256, 0, stream, a);
+    else if (!fours) e = launch_dependent(prefix_join_kernel<D, 4, false, 1>, warps(4, 1), 256, 0, stream, a);
+    else if (a.G % 2) e = launch_dependent(prefix_join_kernel<D, 1, false, kEach>, warps(1, kEach), 256, 0, stream, a);
+    else if (a.G % 4) e = launch_dependent(prefix_join_kernel<D, 2, false, kEach>, warps(2, kEach), 256, 0, stream, a);
+    else e = launch_dependent(prefix_join_kernel<D, 4, false, kEach>, warps(4, kEach), 256, 0, stream, a);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
