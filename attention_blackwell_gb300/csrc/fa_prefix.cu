@@ -40,28 +40,31 @@
 //                 own (few_rows below): single tokens, where the copies set the
 //                 pace.
 // d = 256: one worker a CTA, one row tile, S double-buffered, 64-key tiles (its
-// accumulator takes half of tensor memory), S and P V issued by a warp each.
+// accumulator takes half of tensor memory), Q in tensor memory too, S and P V
+// issued by a warp each; few rows only for requests of few keys (see few_items).
 //
-// Warps: softmax (4 or 8), loader, issuer (d = 256: two), and one or two that
-// walk the list ahead of the others and leave each tile's description, page
-// numbers included, in shared memory, so that no role waits for a table entry.
+// Warps: softmax (8; at d = 256 four of them bring Q), loader, issuer (d = 256:
+// two), and one or two that walk the list ahead of the others and leave each
+// tile's description, page numbers included, in shared memory, so that no role
+// waits for a table entry.
 //
 // Keys behind the end of a list and keys of absent pages are masked by
 // selection, and their V rows are zeroed in shared memory before the product
 // (0 * NaN would poison the sum), so the cache's leftovers never matter.
 //
-// What bounds it (GB300; 6.78 TB/s and 1892 TFLOP/s measured):
-//   single tokens, own keys of a few hundred, 128-key pages, 32 / 8 heads of
-//   128: the copies.  64 requests (282 MB): 65 us, 57 in the main kernel, 4.9
-//   TB/s there; its first 10000 cycles (5 us) go by before every warp's ring is
-//   full, and the rows' segments and their join take 8 us.
-//   512 requests over a long prefix (1.18 GB, 279 GFLOP): 344 us; the prefix's
-//   CTAs take 3430 cycles a unit of two row tiles by 128 keys, of which the
-//   products are 2048: S -> softmax -> P V of one tile has the other's to hide
-//   behind, no more.
-//   prompts (1.43 TFLOP): 1113 us, tensor pipe 57 % busy, the same chain.
-//   d = 256 (224 MB, 60 GFLOP): 98 us, 2300 cycles a 64-key tile, 1280 of them
-//   products.
+// What bounds it (GB300; 6.78 TB/s and 1892 TFLOP/s measured), 32 / 8 heads of
+// 128 unless said otherwise:
+//   64 single tokens, 8192 shared keys and a thousand own ones each (282 MB): 66
+//   us, 57 in the main kernel.  HBM: 5.9 TB/s once every warp's ring is full,
+//   which takes the first 12000 cycles (6 us: tables, walk, page numbers and first
+//   copies depend on one another, on cold code); the join 8.
+//   512 over 32768 (1.18 GB, 279 GFLOP): 345 us.  The prefix's CTAs take 3400
+//   cycles a unit of two row tiles by 128 keys, 2048 of them products: each row
+//   tile's chain S, softmax (1500), P V has one other's products to hide behind.
+//   prompts, six of up to 2048 tokens over 8192 (1.43 TFLOP): 1070 us, tensor
+//   pipe 58 % busy in the main kernel, the same chain.
+//   d = 256, one key/value head, 100 tokens over 16384 and 2000 own keys (224 MB,
+//   60 GFLOP): 81 us; 1570 cycles a 64-key tile, 1024 of them products.
 //   one request, one token: 17 us, 13 of them host and launch.
 #include <limits.h>
 #include <math.h>
