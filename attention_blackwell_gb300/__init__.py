@@ -302,13 +302,12 @@ def _all_int32(**tensors):
 def _rows(t, name):
     """Elements between the tokens of a bf16 [T, H, d] tensor that is dense
     within a token (rows may be cut from a wider projection)."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype is not torch.bfloat16:
         raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if t.dim() != 3:
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError("%s must have 3 dimensions" % name)
-    T, H, d = t.shape
+    T, H, d = shape
     st, sh, sd = t.stride()
     if d > 1 and sd != 1 or H > 1 and sh != d:
         raise ValueError("%s must be contiguous within a token" % name)
@@ -316,13 +315,14 @@ def _rows(t, name):
 
 
 def _pages(k_pages, v_pages):
-    if (k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16 or not k_pages.is_cuda
+    if (k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16
             or not k_pages.is_contiguous() or not v_pages.is_contiguous()):
         _need(k_pages, "k_pages", torch.bfloat16)
         _need(v_pages, "v_pages", torch.bfloat16)
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or shape != v_pages.shape:
         raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d]")
-    return k_pages.shape
+    return shape
 
 
 def page_pool(num_pages, device=None):
@@ -373,15 +373,17 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
     if not (new_lens.get_device() == block_table.get_device() == ring.get_device() == pool.get_device()
             == cu_new.get_device() == kv_lens.get_device() == slots.get_device() == pool_out.get_device() == dev):
         raise ValueError("all tensors must be on one device")
-    if new_lens.numel() != B or block_table.dim() != 2 or block_table.shape[0] != B:
+    table = block_table.shape
+    if new_lens.numel() != B or len(table) != 2 or table[0] != B:
         raise ValueError("ctx_lens, new_lens and block_table must have one entry or row a request")
     if pool.numel() != 3 or cu_new.numel() != B + 1 or kv_lens.numel() != B or pool_out.numel() != 3:
         raise ValueError("pool and pool_out must have 3 elements, cu_new B + 1 and kv_lens B")
-    rc = lib().fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), block_table.data_ptr(),
-                            block_table.shape[1], ring.data_ptr(), ring.numel(), pool.data_ptr(), pool_out.data_ptr(),
-                            cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), slots.numel(),
-                            _current_raw_stream(dev))
-    _check(rc, "fa_page_plan")
+    rc = (_lib or lib()).fa_page_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, int(page_size), block_table.data_ptr(),
+                                      table[1], ring.data_ptr(), ring.numel(), pool.data_ptr(), pool_out.data_ptr(),
+                                      cu_new.data_ptr(), kv_lens.data_ptr(), slots.data_ptr(), slots.numel(),
+                                      _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_page_plan")
     return cu_new, kv_lens, slots, pool_out
 
 
@@ -397,16 +399,18 @@ def kv_store(k, v, slots, k_pages, v_pages, stream=None):
         _need(slots, "slots", torch.int32)
     if not (v_pages.get_device() == k.get_device() == v.get_device() == slots.get_device() == dev):
         raise ValueError("all tensors must be on one device")
-    T = k.shape[0]
-    if k.shape != (T, Hkv, d) or k.shape != v.shape:
+    shape = k.shape
+    T = shape[0]
+    if shape[1] != Hkv or shape[2] != d or shape != v.shape:
         raise ValueError("k and v must be [T, Hkv, d] with the pages' Hkv and d")
     if slots.numel() != T:
         raise ValueError("slots must have one element a token")
     if T == 0:
         return k_pages, v_pages
-    rc = lib().fa_kv_store(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
-                           v_pages.data_ptr(), P, page, _current_raw_stream(dev))
-    _check(rc, "fa_kv_store")
+    rc = (_lib or lib()).fa_kv_store(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
+                                     v_pages.data_ptr(), P, page, _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_kv_store")
     return k_pages, v_pages
 
 
@@ -446,7 +450,8 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     B = kv_lens.numel()
     if dq != d:
         raise ValueError("q and the pages must have one head dim")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
         raise ValueError("block_table must be [B, W] with kv_lens' B")
     if cu_seqlens is not None:
         if cu_seqlens.dtype is not i32 or not cu_seqlens.is_contiguous():
@@ -489,13 +494,14 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
             == out.get_device() == lse.get_device() == workspace.get_device() == dev):
         raise ValueError("all tensors must be on one device")
     _one_device(dev, (cu_seqlens, prefix_table))
-    rc = lib().fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                             T, B, Hq, Hkv, d, alpha, P, page, block_table.data_ptr(), block_table.shape[1],
-                             kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
-                             max_seqlen, prefix_table.data_ptr() if prefix_table is not None else None,
-                             prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                             _current_raw_stream(dev))
-    _check(rc, "fa_prefix_fwd")
+    rc = (_lib or lib()).fa_prefix_fwd(q.data_ptr(), qs, k_pages.data_ptr(), v_pages.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                       T, B, Hq, Hkv, d, alpha, P, page, block_table.data_ptr(), table[1],
+                                       kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
+                                       max_seqlen, prefix_table.data_ptr() if prefix_table is not None else None,
+                                       prefix_len, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                       _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_prefix_fwd")
     return out, lse
 
 
