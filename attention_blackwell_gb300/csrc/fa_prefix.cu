@@ -1736,7 +1736,7 @@ PfLayout pf_layout(int T, int B, int Hkv, int G, int d, int max_seqlen, int sms)
 
 template <int D, bool M>
 int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtensorMap& tk, const CUtensorMap& tv,
-                  const CUtensorMap& tk_few, const CUtensorMap& tv_few, const PfArgs& a, int sms, cudaStream_t stream) {
+                  const CUtensorMap& tk_few, const CUtensorMap& tv_few, const PfArgs& a, int sms, int grid, cudaStream_t stream) {
     using G = Pf<D>;
     const uint32_t smem = 1024 + G::kTiles + (a.B + 1) * 12 + a.B * 4 + a.listed * 4;
     static_assert(1024 + G::kTiles + (kMaxVarlenSeqs + 1) * 12 + kMaxVarlenSeqs * 4 <= G::kMaxSmem && G::kMaxSmem + sizeof(PfShared) <= 232448, "shared memory plan");
@@ -1750,7 +1750,7 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    if (launch_dependent(kern, sms, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
+    if (launch_dependent(kern, grid, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to two an SM a block each; up to 64 an SM (one or
     // two rounds of warps) a warp each; past that four or two a warp.
@@ -1904,10 +1904,15 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
         if (rc == FA_OK) rc = make_map_steps(&tv_few, v_pages, d, slots);
     }
     if (rc != FA_OK) return rc;
+    // Twice the CTAs that one unit a worker takes, up to one an SM: code that runs
+    // once comes to all SMs from the same place in L2, and CTAs without work would
+    // ask for it too.
+    const long long need = (blocks_p * tiles_p + a.width_p - 1) / a.width_p + (blocks_s * tiles_s + a.width_s - 1) / a.width_s;
+    const int grid = 2 * need + 2 < sms ? (int)(2 * need + 2) : sms;
     auto launch = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
-        return a.direct ? launch_prefix<D, true>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream)
-                        : launch_prefix<D, false>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, stream);
+        return a.direct ? launch_prefix<D, true>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, grid, stream)
+                        : launch_prefix<D, false>(tq_p, tq_s, tk, tv, tk_few, tv_few, a, sms, grid, stream);
     };
     if (d == 64) return launch(std::integral_constant<int, 64>{});
     if (d == 128) return launch(std::integral_constant<int, 128>{});
