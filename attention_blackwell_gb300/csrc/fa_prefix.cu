@@ -94,10 +94,11 @@ template <int D> struct Pf {
     static constexpr uint32_t kQTile = D == 256 ? 0 : kBoxes * kQBox;   // d = 256: Q is in tensor memory
     static constexpr int kLook = 3 - kStreams;                   // tiles of one worker with S in flight
     static constexpr int kRing = D == 64 ? 8 : D == 128 ? 4 : 6; // K/V tiles: 128 KB, at d = 256 192
-    static constexpr uint32_t kTiles = kStreams * kQTile + kRing * kTile;
+    static constexpr uint32_t kTiles = 196608;                       // of them, or of the few rows' rings
     static constexpr int kThreads = 384;
     static constexpr int kMaxSmem = 232448 - 4096;               // dynamic; the rest is PfShared
-    static constexpr int kFewParts = D == 256 ? 1 : 2;               // few rows: 16-key parts a step, slots of a step's K or V a warp
+    static_assert(kStreams * kQTile + kRing * kTile <= kTiles, "Q and the ring");
+    static constexpr int kFewParts = 256 / D;               // few rows: 16-key parts a step, slots of a step's K or V a warp
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
     // Cycles a CTA takes for a unit of the prefix and of the requests' own keys,
     // measured in the kernel on GB300; the CTAs are divided between the two by
@@ -105,7 +106,7 @@ template <int D> struct Pf {
     // all but the first; alone, each tile comes from HBM for 256 rows only, and
     // its latency grows with the share of the traffic (`own`, 0 to 1) that the
     // requests' CTAs ask for at the same time.
-    __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 600 : D == 128 ? 780 : 900) * halves; }
+    __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 520 : D == 128 ? 780 : 900) * halves; }
     // Few rows at d = 256, where a warp takes 15000 cycles for a unit: worth it for
     // items of few units (of them over_s for the item), else one row tile.  100
     // keys a request of 8 heads: 44 us for 128 requests, one row tile 60; 2000 keys
@@ -563,9 +564,10 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 // (TMA; a slot is free as soon as this warp has read it, so nothing waits for
 // another warp), and keeps scores, wfours and the accumulator in registers
 // (mma.sync m16n8k16).  An item's end costs a store of the rows and no barrier.
-// A step is 32 keys (16 at d = 256, where Q and O take the registers): 780 cycles
-// for 64 keys of a CTA's eight warps at d = 128, of which 8 K and 8 V copies at
-// the CTA's share of HBM are 700.  64 single tokens: 4.9 TB/s.  Eight warps that
+// A step is 8 KB of K and of V (64 keys at d = 64, 16 at d = 256, where Q and O
+// take the registers): 780 cycles for 64 keys of a CTA's eight warps at d = 128,
+// of which the copies at the CTA's share of HBM are 700; 500 at d = 64 (with 32
+// keys a step 600: 32 requests of 32 heads 58 us, with 64 49).  64 single tokens: 4.9 TB/s.  Eight warps that
 // share 128-key tiles and join in shared memory took 442 us where these take 349.
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
