@@ -423,7 +423,7 @@ __device__ __forceinline__ PfHeader build_tables(const PfArgs& a, const PfTables
         }
         __syncthreads();
     }
-    int units = 0, items = 0, blocks = 0;      // of the requests before this round's
+    int units = 0, items = 0, blocks = 0;      // of the requests before these
     for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + tid;
         int u = 0, it = 0, blk = 0, first_blk = 0;
@@ -1231,7 +1231,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             // Pages of four tiles at a time, a lane each; the next four's loads
             // (the next item's, past an item's end) run while these are handed on.
             // The first four are handed on before any others are looked up: every
-            // role waits for them.  Rounds: look up 0; hand on 0; look up 1; look up 2
+            // role waits for them.  Turns: look up 0; hand on 0; look up 1; look up 2
             // and hand on 1; look up 3 and hand on 2; ...
             const int x = warp - (kSoftWarps + 2), q = lane >> 3, part = lane & 7;
             Walk<D, M> walk;
@@ -1249,15 +1249,15 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
             bool ok = true, more = false, more_next = true;
             int j = 0, val = -1, j_next = 0, val_next = -1;
             ahead.j0 = ahead.j1 = 0;
-            for (int round = 0; ok; ++round) {
-                const bool hand_on = round == 1 || round > 2;
+            for (int turn = 0; ok; ++turn) {
+                const bool hand_on = turn == 1 || turn > 2;
                 if (hand_on) {
                     it = ahead;
                     more = more_next;
                     j = j_next;
                     val = val_next;
                 }
-                if (more_next && round != 1) {
+                if (more_next && turn != 1) {
                     j_next += 4;
                     if (j_next >= ahead.j1) {
                         more_next = walk.next(a, t, ahead);
@@ -1755,7 +1755,7 @@ int launch_prefix(const CUtensorMap& tq_p, const CUtensorMap& tq_s, const CUtens
     if (launch_dependent(kern, grid, G::kThreads, smem, stream, tq_p, tq_s, tk, tv, tk_few, tv_few, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     // Rows (of one head): up to two an SM a block each; up to 64 an SM (one or
-    // two rounds of warps) a warp each; past that four or two a warp.
+    // two sets of warps) a warp each; past that four or two a warp.
     auto warps = [&](int heads, int each) { return (int)(((long long)cdiv(a.T, each) * (a.Hq / heads) + 7) / 8); };
     cudaError_t e;
     // Four rows a warp where items may have written theirs (see prefix_join_kernel).
