@@ -418,6 +418,23 @@ def test_extreme_lengths_are_clamped(fa):
     assert width * 16 < 1 << 30
 
 
+@pytest.mark.parametrize("n", [[1, 1], [1, 70]])
+def test_prefix_fwd_offsets_past_32_bits(fa, n):
+    """The same pages behind 4.7e9 elements of others give the same, bit for bit."""
+    b = Batch(8, 8, 256, 256, 300, [500, 80], n, seed=5)
+    o, lse = b.run(fa)
+    b.check(fa, o, lse)
+    P, small = 9000, b.k.shape[0]
+    k, v = (torch.empty(P, 8, 256, 256, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k[P - small:], v[P - small:] = b.k, b.v
+    moved = lambda row: [p + P - small if 0 <= p < small else -1 for p in row]
+    table, shared = i32([moved(r) for r in b.table]), i32(moved(b.prefix_pages))
+    x, y = fa.prefix_fwd(b.q, k, v, table, i32(b.s), cu_seqlens=i32(b.cu), max_seqlen=max(n), prefix_table=shared,
+                         prefix_len=b.prefix, alpha=b.alpha)
+    assert fa.device_status() == 0
+    assert torch.equal(o, x) and torch.equal(lse, y)
+
+
 def test_max_seqlen_above_all_rows(fa):
     """No request has more rows than there are, whatever the caller allows."""
     b = Batch(8, 2, 128, 16, 40, [100, 20], [3, 2], seed=2)
