@@ -266,7 +266,15 @@ int fa_page_plan(const int* ctx_lens, const int* new_lens, int B, int page_size,
         misaligned(pool, 7) || misaligned(pool_out, 7) || misaligned(cu_new, 3) || misaligned(kv_lens, 3) ||
         misaligned(slots, 3))
         return FA_ERR_ALIGN;
-    if (pool == pool_out) return FA_ERR_INVALID;
+    // Every block reads all lengths while others write: an output over any other
+    // array (kv_lens over ctx_lens, say) would be a race.  The first three are
+    // read only.
+    const size_t n = B;
+    const Span arrays[] = {{ctx_lens, 4 * n}, {new_lens, 4 * n}, {pool, 24}, {pool_out, 24}, {block_table, 4 * n * table_width},
+                           {ring, 4 * (size_t)num_pages}, {cu_new, 4 * (n + 1)}, {kv_lens, 4 * n}, {slots, 4 * (size_t)num_slots}};
+    for (int i = 3; i < 9; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(arrays[i], arrays[j])) return FA_ERR_INVALID;
     DevStatus* status = device_status_ptr();
     const int sms = fa_num_sms();
     if (!status || sms < 1) return FA_ERR_LAUNCH;

@@ -209,6 +209,16 @@ inline cudaError_t launch_dependent(void (*kern)(P...), int grid, int block, siz
     return cudaLaunchKernelEx(&c, kern, static_cast<P>(args)...);
 }
 
+// A range of bytes that a call reads or writes, and whether two share a byte.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
 // Upper bound on the SM count, for sizes asked for without a device.
 constexpr int kMaxSMs = 192;
 

@@ -341,10 +341,10 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
  * where it has no page and for rows t >= cu_new[B]; rows t >= num_slots get
  * none.
  * A call writes nothing that it reads, so the same call again gives the same.
- * One launch, no workspace.  pool and pool_out must be different arrays; no
- * array may overlap another.
+ * One launch, no workspace.  An array that is written must not overlap another
+ * (kv_lens is not written over ctx_lens, nor pool_out over pool).
  * Errors: FA_ERR_INVALID (null pointer, B, table_width or num_pages < 1,
- * num_slots < 0, pool == pool_out), FA_ERR_UNSUPPORTED (B > 1024, page_size,
+ * num_slots < 0, arrays that overlap), FA_ERR_UNSUPPORTED (B > 1024, page_size,
  * B * table_width, table_width * page_size or num_pages * page_size above
  * 2^31 - 1), FA_ERR_ALIGN (an array not aligned to its element),
  * FA_ERR_LAUNCH.

@@ -56,6 +56,21 @@ def test_page_plan_refusals(plan):
     assert plan(pool=P + 4) == plan(pool_out=P + 4) == -3
 
 
+def test_page_plan_refuses_arrays_that_overlap(plan):
+    """An output over any other array, whole or by one element; the sizes of
+    `plan`: B 4, W 8, P 64, 4 slots."""
+    names = "ctx new pool table ring pool_out cu kv slots".split()
+    sizes = dict(zip(names, (16, 16, 24, 128, 256, 24, 20, 16, 16)))
+    apart = {n: P + 4096 * i for i, n in enumerate(names)}
+    last = {n: apart[n] + (sizes[n] - 1) // 8 * 8 for n in names}      # its last multiple of 8 bytes
+    for i, out in enumerate(names[3:], 3):
+        for n in names[:i]:
+            assert plan(**dict(apart, **{out: apart[n]})) == -1, (out, n)
+            assert plan(**dict(apart, **{out: last[n]})) == -1, (out, n)
+            assert plan(**dict(apart, **{n: last[out]})) == -1, (out, n)
+    assert plan(**dict(apart, B=1024, kv=apart["ctx"] + 4092, table=1 << 30)) == -1     # a later request's
+
+
 @pytest.fixture(scope="module")
 def store(lib):
     names = "k v ks vs slots T Hkv d kp vp P page stream".split()
