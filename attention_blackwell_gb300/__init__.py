@@ -435,7 +435,8 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     Hkv, page_size, d], block_table int32 [B, W], kv_lens int32 [B] (new tokens
     included), prefix_table int32 pages of the prefix's prefix_len tokens ->
     o [T, Hq, d], lse float32 [Hq, T].  Without cu_seqlens (int32 [B+1]) every
-    request has one row; with it max_seqlen bounds a request's rows.
+    request has one row; with it max_seqlen bounds a request's rows.  out, lse
+    and the workspace must not overlap q, the pages or the tables.
     """
     dev, i32 = q.get_device(), torch.int32
     if stream is not None or dev < 0 or dev != _current_device():

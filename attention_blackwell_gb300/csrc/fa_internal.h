@@ -218,6 +218,13 @@ inline bool overlap(const Span& a, const Span& b) {
     const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
     return a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
 }
+// Whether `a` shares a byte with one of n rows of `bytes`, `stride` apart (a may
+// lie between two rows).
+inline bool overlap_rows(const Span& a, const void* rows, long long n, size_t bytes, size_t stride) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(rows);
+    const uintptr_t i = x < y + bytes ? 0 : (x - y - bytes) / stride + 1;   // the first row that ends behind a's begin
+    return a.bytes && (long long)i < n && y + i * stride < x + a.bytes;
+}
 
 // Upper bound on the SM count, for sizes asked for without a device.
 constexpr int kMaxSMs = 192;

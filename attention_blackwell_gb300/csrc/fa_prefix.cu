@@ -1810,6 +1810,18 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
         misaligned(prefix_table, 3) || (q_stride & 7))
         return FA_ERR_ALIGN;
     if (T == 0) return FA_OK;
+    // Rows are written while others are still read.
+    const size_t row = (size_t)Hq * d * 2, cache = (size_t)num_pages * Hkv * page_size * d * 2;
+    const Span inputs[] = {{k_pages, cache}, {v_pages, cache}, {block_table, 4 * (size_t)B * table_width}, {kv_lens, 4 * (size_t)B},
+                           {cu_seqlens, cu_seqlens ? 4 * ((size_t)B + 1) : 0},
+                           {prefix_table, prefix_len > 0 ? 4 * (((size_t)prefix_len + page_size - 1) >> lg) : 0}};
+    auto over_input = [&](const Span& out) {
+        for (const Span& in : inputs)
+            if (overlap(out, in)) return true;
+        return overlap_rows(out, q, T, row, (size_t)q_stride * 2);
+    };
+    const Span out_o = {o, T * row}, out_lse = {lse, 4 * (size_t)Hq * T};
+    if (over_input(out_o) || over_input(out_lse) || overlap(out_o, out_lse)) return FA_ERR_INVALID;
     if (max_seqlen > T) max_seqlen = T;
     const int sms = fa_num_sms();
     DevStatus* status = device_status_ptr();
@@ -1817,6 +1829,8 @@ int fa_prefix_fwd(const void* q, int64_t q_stride, const void* k_pages, const vo
     const int G = Hq / Hkv;
     const PfLayout w = pf_layout(T, B, Hkv, G, d, max_seqlen, sms);
     if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+    const Span scratch = {workspace, w.total};
+    if (over_input(scratch) || overlap(scratch, out_o) || overlap(scratch, out_lse)) return FA_ERR_INVALID;
 
     const int kN = d == 256 ? 64 : 128;
     // Few rows: at d = 256 up to 16 of a request's (see few_items; two warps for 32

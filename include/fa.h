@@ -399,7 +399,8 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  * lengths does not matter, NaN and infinities included; a NaN in a query or in
  * a key gives NaN in the rows that see it, one in a value (or an infinity) may
  * also reach the request's rows before it, whose weight for it is 0.
- * o and lse must not overlap an input.  workspace: at least
+ * o, lse and the workspace must not overlap an input or one another (o between
+ * the tokens of a strided q does not).  workspace: at least
  * fa_prefix_workspace_size(...) bytes, 256-byte aligned, no initialisation
  * needed; calls that share one must not overlap on the GPU (captured graphs
  * that hold the same one included).  A call whose kernel gives up a wait (2 s)
@@ -408,7 +409,8 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  * T == 0 is a no-op.
  * Errors: FA_ERR_INVALID (null pointer, T < 0, B, Hq, Hkv, num_pages or
  * table_width < 1, Hq % Hkv, prefix_len < 0, alpha not finite and > 0,
- * max_seqlen < 1, q_stride below Hq * d, T != B without cu_seqlens),
+ * max_seqlen < 1, q_stride below Hq * d, T != B without cu_seqlens, arrays that
+ * overlap),
  * FA_ERR_UNSUPPORTED (d not 64, 128 or 256; Hq / Hkv > 128; B > 1024;
  * page_size; prefix_len or table_width * page_size above 2^29; Hq * T, B *
  * table_width or num_pages * Hkv * page_size above 2^31 - 1; row blocks times

@@ -123,6 +123,25 @@ def test_prefix_fwd_refusals(attend):
     assert attend(T=0, cu=P) == 0
 
 
+def test_prefix_fwd_refuses_outputs_over_inputs(attend):
+    """o or lse over an input or each other, whole or by 16 bytes; the sizes of
+    `attend`: 4 rows of 2 KB (q's 4 KB apart), 64 pages of 8 KB, 4 x 8 table entries."""
+    names = "q kp vp table kv cu pt o lse".split()
+    sizes = dict(zip(names, (14336, 1 << 19, 1 << 19, 128, 16, 20, 28, 8192, 128)))
+    ok = {n: (i + 1) << 24 for i, n in enumerate(names)}
+    for out in ("o", "lse"):
+        for n in names:
+            if n == out:
+                continue
+            kw = dict(ok, qs=2048)
+            last = lambda m: ok[m] + (sizes[m] - 1) // 16 * 16
+            assert attend(**dict(kw, **{out: ok[n]})) == -1, (out, n)
+            assert attend(**dict(kw, **{out: last(n)})) == -1, (out, n)
+            assert attend(**dict(kw, **{n: last(out)})) == -1, (out, n)
+    for at in (0, 2032, 4096, 4096 * 3 + 2032):                     # lse (128 bytes) over a row of q
+        assert attend(**dict(ok, qs=2048, lse=ok["q"] + at)) == -1, at
+
+
 def test_prefix_workspace_sizes(lib):
     """0 for sizes that a call would refuse; more rows, requests or rows a
     request never need less."""

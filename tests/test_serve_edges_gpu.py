@@ -45,3 +45,33 @@ def test_page_plan_refuses_lengths_updated_in_place(fa):
             fa.page_plan(ctx, new, table, ring, pool, 16, num_slots=24, **kw)
         assert e.value.code == -1
     assert ctx.tolist() == [0] * 8 and new.tolist() == [3] * 8 and ring.tolist() == list(range(40))
+
+
+# ------------------------------------------------------------------- prefix_fwd
+
+def test_prefix_fwd_refuses_outputs_over_inputs(fa):
+    b = Batch(8, 2, 128, 16, 40, [100, 20], [3, 2], seed=2)
+    (table, lens), opt = b.tensors()
+    ws = fa.prefix_workspace(2, 8, 2, b.T, 3)
+    pages = b.k.view(-1)
+    for kw in (dict(out=b.q), dict(out=pages[1024:1024 + b.q.numel()].view_as(b.q)), dict(lse=ws[:4 * 8 * b.T].view(torch.float32).view(8, b.T)),
+               dict(workspace=b.k.view(torch.uint8).view(-1)), dict(workspace=ws, out=ws[4096:4096 + 2 * b.q.numel()].view(torch.bfloat16).view_as(b.q))):
+        with pytest.raises(fa.FAError) as e:
+            b.run(fa, **dict(dict(workspace=ws), **kw))
+        assert e.value.code in (-1, -6), kw.keys()       # -6: b.k is too small a workspace anyway
+    assert fa.device_status() == 0
+
+
+def test_prefix_fwd_writes_between_the_tokens_of_q(fa):
+    """One projection's output with room for o's single row between two tokens
+    of q is no overlap, nor are buffers side by side."""
+    b = Batch(4, 2, 64, 16, 40, [100, 20], [1, 1], seed=2)
+    n = 4 * 64
+    x = torch.zeros(2, 4 * n, dtype=torch.bfloat16, device="cuda")
+    x[:, :n] = b.q.view(2, n)
+    q, out = x[:, :n].unflatten(1, (4, 64)), x[0, n:3 * n].view(2, 4, 64)
+    lse = x[0, 3 * n:3 * n + 16].view(torch.float32).view(4, 2)
+    (table, lens), opt = b.tensors()
+    o, l = fa.prefix_fwd(q, b.k, b.v, table, lens, out=out, lse=lse, **opt)
+    b.check(fa, o, l)
+    assert torch.equal(x[:, :n], b.q.view(2, n))
