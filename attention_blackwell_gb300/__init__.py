@@ -390,7 +390,9 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
 
 def kv_store(k, v, slots, k_pages, v_pages, stream=None):
     """Write rows of k and v ([T, Hkv, d] bf16, tokens may be strided) into the
-    cache at slots (int32 [T]; negative: skipped).  Returns (k_pages, v_pages)."""
+    cache at slots (int32 [T], distinct; negative: skipped).  k_pages and v_pages
+    must not overlap (one tensor for both takes one k and v).  Returns (k_pages,
+    v_pages)."""
     dev = k_pages.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(stream, (k_pages, v_pages, k, v, slots), lambda: kv_store(k, v, slots, k_pages, v_pages))

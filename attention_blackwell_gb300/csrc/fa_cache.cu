@@ -317,6 +317,11 @@ int fa_kv_store(const void* k, const void* v, int64_t k_stride, int64_t v_stride
         misaligned(slots, 3) || (k_stride & 7) || (v_stride & 7))
         return FA_ERR_ALIGN;
     if (T == 0) return FA_OK;
+    // One array for keys and values (a cache that keeps one row for both) can only
+    // take the same rows for both; else two threads would write each slot.
+    const size_t cache = (size_t)num_pages * Hkv * page_size * d * 2;
+    if (overlap({k_pages, cache}, {v_pages, cache}) && !(k_pages == v_pages && k == v && k_stride == v_stride)) return FA_ERR_INVALID;
+    if (overlap({slots, 4 * (size_t)T}, {k_pages, cache}) || overlap({slots, 4 * (size_t)T}, {v_pages, cache})) return FA_ERR_INVALID;
     const int sms = fa_num_sms();
     if (sms < 1) return FA_ERR_LAUNCH;
     StoreArgs a;

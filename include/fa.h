@@ -359,10 +359,12 @@ int fa_page_plan(const int *ctx_lens, const int *new_lens, int B, int page_size,
  * multiples of 8, so both may be cut from one projection's output) goes to
  * slot slots[t].  Slots outside [0, num_pages * page_size) are skipped, every
  * other slot is left as it was.  The slots of one call must be distinct: where
- * two rows share one, the slot holds parts of either.
+ * two rows share one, the slot holds parts of either.  k and v may be rows of
+ * the cache itself, other ones than the call writes.  k_pages and v_pages must
+ * not overlap, but may be one array when k and v are one, too.
  * d is 64, 128 or 256.  T == 0 is a no-op.
  * Errors: FA_ERR_INVALID (null pointer, T < 0, Hkv, d or num_pages < 1, stride below Hkv
- * * d), FA_ERR_UNSUPPORTED (d, page_size, num_pages * page_size above 2^31 -
+ * * d, page arrays that overlap each other or slots), FA_ERR_UNSUPPORTED (d, page_size, num_pages * page_size above 2^31 -
  * 1), FA_ERR_ALIGN (k, v or a page array not 16-byte aligned, a stride not a
  * multiple of 8), FA_ERR_LAUNCH.
  */

@@ -92,6 +92,15 @@ def test_kv_store_refusals(store):
     assert store(T=0) == 0
 
 
+def test_kv_store_refuses_pages_that_overlap(store):
+    """64 pages of 8 heads, 16 x 128: 2 MB an array."""
+    kp, size = 1 << 24, 1 << 21
+    ok = dict(k=P, v=P + 4096, kp=kp, vp=kp + size, slots=1 << 28)
+    for kw in (dict(vp=kp), dict(vp=kp + size - 16), dict(vp=kp - size + 16), dict(vp=kp, v=P, vs=2048),
+               dict(slots=kp), dict(slots=kp - 12), dict(slots=kp + 2 * size - 4)):
+        assert store(**dict(ok, **kw)) == -1, kw
+
+
 @pytest.fixture(scope="module")
 def attend(lib):
     names = ("q qs kp vp o lse T B Hq Hkv d alpha P page table W kv cu ms pt pl ws wb stream").split()

@@ -47,6 +47,36 @@ def test_page_plan_refuses_lengths_updated_in_place(fa):
     assert ctx.tolist() == [0] * 8 and new.tolist() == [3] * 8 and ring.tolist() == list(range(40))
 
 
+# --------------------------------------------------------------------- kv_store
+
+def test_kv_store_one_cache_for_keys_and_values(fa):
+    """Keys that are values as well: one array takes the same rows twice, and
+    attention reads both from it; other rows for each are refused."""
+    P, Hkv, page, d, T = 6, 2, 16, 64, 40
+    x, pages = normal(1, T, Hkv, d), normal(2, P, Hkv, page, d)
+    slots = np.random.default_rng(3).permutation(P * page)[:T].astype(np.int32)
+    want = paged.kv_store(bits(x).cpu().numpy(), slots, bits(pages).cpu().numpy())
+    fa.kv_store(x, x, i32(slots.tolist()), pages, pages)
+    assert np.array_equal(bits(pages).cpu().numpy(), want)
+    q, table, lens = normal(4, 1, 4, d), i32([[3, 0, 5]]), i32([44])
+    a, b = fa.prefix_fwd(q, pages, pages, table, lens), fa.prefix_fwd(q, pages, pages.clone(), table, lens)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(fa.FAError) as e:
+        fa.kv_store(x, x.clone(), i32(slots.tolist()), pages, pages)
+    assert e.value.code == -1 and np.array_equal(bits(pages).cpu().numpy(), want)
+
+
+def test_kv_store_moves_rows_within_the_cache(fa):
+    """A page's rows as the source of another page's."""
+    P, page, d = 5, 32, 128
+    kp, vp = normal(1, P, 1, page, d), normal(2, P, 1, page, d)
+    want = [x.clone() for x in (kp, vp)]
+    for x in want:
+        x[4, 0, 3:] = x[1, 0, :29]
+    fa.kv_store(kp[1].view(page, 1, d)[:29], vp[1].view(page, 1, d)[:29], i32(list(range(4 * page + 3, 5 * page))), kp, vp)
+    assert torch.equal(kp, want[0]) and torch.equal(vp, want[1])
+
+
 # ------------------------------------------------------------------- prefix_fwd
 
 def test_prefix_fwd_refuses_outputs_over_inputs(fa):
