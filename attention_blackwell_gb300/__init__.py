@@ -340,7 +340,8 @@ def page_plan(ctx_lens, new_lens, block_table, ring, pool, page_size, num_slots=
 
     ctx_lens, new_lens int32 [B] (new_lens < 0: the request leaves),
     block_table int32 [B, W], ring int32 [num_pages], pool int64 [3] = head,
-    tail, missing (see page_pool).  -> cu_new int32 [B+1], kv_lens int32 [B],
+    tail, missing (see page_pool; missing: pages that could not be given, free
+    ones that are no pages included).  -> cu_new int32 [B+1], kv_lens int32 [B],
     slots int32 [num_slots] (-1: none), pool_out int64 [3].  num_slots is needed
     when slots is not given.  No tensor that is written may overlap another:
     kv_lens is another tensor than ctx_lens, pool_out than pool.

@@ -36,8 +36,10 @@ def page_plan(ctx, new, table, ring, pool, page, num_slots):
             if k >= W:
                 missing += 1
             elif used < free:
-                table[b][k] = old_ring[(head + used) % P]
+                page_k = old_ring[(head + used) % P]
                 used += 1
+                table[b][k] = page_k if 0 <= page_k < P else -1
+                missing += table[b][k] < 0
             else:
                 table[b][k] = -1
                 missing += 1

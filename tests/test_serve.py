@@ -238,3 +238,13 @@ def test_oracle_plan_conserves_pages():
         assert sorted(free + held) == list(range(P))
         real = [s for s in slots if s >= 0]
         assert len(set(real)) == len(real) == cu[-1]
+
+
+def test_oracle_plan_counts_absent_pages_that_it_hands_out():
+    """A request that leaves with an absent page puts it into the queue as it
+    stands; the request that gets it lacks a page."""
+    state = paged.page_plan([32, 0], [-1, 0], [[0, -1], [-1, -1]], [9, 9, 9], [0, 0, 0], 16, 0)
+    table, ring, pool = state[:3]
+    assert ring == [0, -1, 9] and pool == [0, 2, 0]
+    table, _, pool, cu, kv, slots = paged.page_plan([0, 0], [32, 0], table, ring, pool, 16, 32)
+    assert table[0] == [0, -1] and pool == [2, 2, 1] and slots == list(range(16)) + [-1] * 16

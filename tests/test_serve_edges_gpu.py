@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import paged
-from test_serve_gpu import fa, i32, random_state  # noqa: F401  (fa is a fixture)
+from test_serve_gpu import Batch, bits, fa, i32, normal, random_state, run_plan  # noqa: F401  (fa is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -45,6 +45,32 @@ def test_page_plan_refuses_lengths_updated_in_place(fa):
             fa.page_plan(ctx, new, table, ring, pool, 16, num_slots=24, **kw)
         assert e.value.code == -1
     assert ctx.tolist() == [0] * 8 and new.tolist() == [3] * 8 and ring.tolist() == list(range(40))
+
+
+@pytest.mark.parametrize("B,new_top", [(9, 30), (300, 40), (1000, 100)])
+def test_page_plan_absent_pages_in_the_queue(fa, B, new_top):
+    """Requests leave with absent pages in their rows; the next call hands the
+    queue's entries out, and those that are no pages count as missing."""
+    g = np.random.default_rng(B)
+    page, W, P = 16, 8, 8 * B
+    ctx, new, table, ring, pool = random_state(g, B, W, page, P, 60, 0, B // 2)
+    for b in range(B):
+        if new[b] < 0:
+            for k in range(W):
+                if g.random() < 0.3:
+                    table[b][k] = (-1, P, 1 << 30, -(1 << 31))[k % 4]
+    pool[0] = pool[1] - 2                                # the rest of the queue is lost
+    got = run_plan(fa, ctx, new, table, ring, pool, page, 0)
+    want = list(paged.page_plan(ctx, new, table, ring, pool, page, 0))
+    assert got == want
+    table, ring, pool, _, ctx, _ = got
+    new = [int(x) for x in g.integers(0, new_top, B)]
+    T = sum(new) + 3
+    got, want = run_plan(fa, ctx, new, table, ring, pool, page, T), list(paged.page_plan(ctx, new, table, ring, pool, page, T))
+    assert got == want
+    free = [ring[i % P] for i in range(pool[0], pool[1])]
+    holes = sum(not 0 <= p < P for p in free[:got[2][0] - pool[0]])
+    assert got[2][2] >= holes > 0
 
 
 # --------------------------------------------------------------------- kv_store
