@@ -62,9 +62,11 @@ __device__ __forceinline__ int find_request(const int* pref, int B, int x) {
 // for another's table entries and one launch does it all.
 //   have = ceil(c / page), need = min(ceil((c + n) / page), W),
 //   slot of position x = entry[x / page] * page + x % page.
-// Bound by latency: lengths, scan, search and page lookup depend on one another
-// (4.5 us on the GPU for 8 requests and for 1000; a call from Python is 7.2 us,
-// so that is what a step sees).  560000 rows of 128 prompts: 8 us for 2.2 MB.
+// Bound by latency: lengths, scan, search and page lookup depend on one another.
+// From cold caches 5 us on the GPU for 8 requests, 8.5 for 1000 (the scan over 32
+// warps), 7.9 for 560000 rows of 128 prompts (2.2 MB; the first block's count of
+// the pages is the last to end).  Calls from Python one behind the other 7.3 to
+// 8.8 us, replays of a graph of one call 6.2, 8.5 and 8.3.
 __global__ void __launch_bounds__(1024) page_plan_kernel(const PlanArgs a) {
     __shared__ int s_cu[kPlanMaxB + 1], s_in[kPlanMaxB + 1], s_out[kPlanMaxB + 1];
     __shared__ int s_ctx[kPlanMaxB];
@@ -235,7 +237,8 @@ struct StoreArgs {
 // the order of memory, and a head's row of a slot is a whole 128 bytes or more of
 // the cache, so both sides move in full lines.  Bound by HBM: 328 MB (40000 rows
 // of 8 heads of 128) in 47.5 us, 6.9 TB/s read and written together (a plain
-// copy: 6.8); 64 rows: 4.2 us on the GPU, launch and two dependent loads.
+// copy: 6.8).  64 rows: 4 us on the GPU, launch and three loads in a row (the slot,
+// K's chunk, and V's, which does not move above the store of K's).  41 MB: 8.2.
 __global__ void __launch_bounds__(256) kv_store_kernel(const StoreArgs a) {
     grid_launch_next();
     grid_wait();

@@ -29,7 +29,9 @@
 // up, batches that mix prompts and steps are up to 30 % slower).
 //
 // Some CTAs work on the prefix, the others on the requests, in proportion to
-// the cost of both.  Within a CTA (d = 64 and 128):
+// the cost of both.  Within a CTA (d = 64 and 128), by the rows that a block of
+// the prefix (all of the call's) or of a request (of max_seqlen tokens: one shape
+// for all requests of a call) may have:
 //   rows > 128    the CTA is one worker: two row tiles share every K/V tile (the
 //                 ping-pong of fa_fwd.cu): the shape for the prefix of a large
 //                 batch and for prompts, where the tensor core sets the pace;
@@ -58,14 +60,16 @@
 //   us, 57 in the main kernel.  HBM: 5.9 TB/s once every warp's ring is full,
 //   which takes the first 12000 cycles (6 us: tables, walk, page numbers and first
 //   copies depend on one another, on cold code); the join 8.
-//   512 over 32768 (1.18 GB, 279 GFLOP): 345 us.  The prefix's CTAs take 3400
+//   512 over 32768 (1.18 GB, 279 GFLOP): 343 to 349 us.  The prefix's CTAs take 3400
 //   cycles a unit of two row tiles by 128 keys, 2048 of them products: each row
 //   tile's chain S, softmax (1500), P V has one other's products to hide behind.
-//   prompts, six of up to 2048 tokens over 8192 (1.43 TFLOP): 1070 us, tensor
-//   pipe 58 % busy in the main kernel, the same chain.
+//   prompts, six of up to 2048 tokens over 8192 (1.43 TFLOP): 1070 to 1114 us,
+//   tensor pipe 58 % busy in the main kernel, the same chain.
 //   d = 256, one key/value head, 100 tokens over 16384 and 2000 own keys (224 MB,
 //   60 GFLOP): 81 us; 1570 cycles a 64-key tile, 1024 of them products.
-//   one request, one token: 15 us, 12 of them the call from Python.
+//   one request, one token: 15 to 17 us a call, the call from Python 13, the two
+//   kernels 12.5 and 7 from cold caches, a graph of them 18.  With a table of 8192
+//   pages, where the grid is all SMs, 2 more.
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>
@@ -101,16 +105,21 @@ template <int D> struct Pf {
     static constexpr int kFewParts = 256 / D;               // few rows: 16-key parts a step, slots of a step's K or V a warp
     static constexpr uint32_t kFewRing = kTiles / 8 / (D * 32 * kFewParts);
     // Cycles a CTA takes for a unit of the prefix and of the requests' own keys,
-    // measured in the kernel on GB300; the CTAs are divided between the two by
-    // them.  kTwo on the prefix: when several row blocks share a tile, L2 serves
-    // all but the first; alone, each tile comes from HBM for 256 rows only, and
-    // its latency grows with the share of the traffic (`own`, 0 to 1) that the
-    // requests' CTAs ask for at the same time.
+    // by which the CTAs are divided between the two: measured in the kernel on
+    // GB300, few rows with a third of the CTAs on the requests (512 single tokens
+    // over 32768 keys: 50 of 152).  Where every CTA streams keys, HBM makes it 780,
+    // 1520 and 2850 (d = 64, 128, 256; 6.6 to 7.2 TB/s read).  At d = 256, 900 is a
+    // compromise: of nine batches, 1400 makes some 26 % faster and others 26 %
+    // slower, 1875 (a warp's 15000, see few_items) 18 % and 34 %.
+    // kTwo on the prefix: when several row blocks share a tile, L2 serves all but the
+    // first; alone, each tile comes from HBM for 256 rows only, and its latency grows
+    // with the share of the traffic (`own`, 0 to 1) that the requests' CTAs ask for at
+    // the same time.
     __host__ __device__ static constexpr int few_cost(int halves) { return (D == 64 ? 520 : D == 128 ? 780 : 900) * halves; }
-    // Few rows at d = 256, where a warp takes 15000 cycles for a unit: worth it for
-    // items of few units (of them over_s for the item), else one row tile.  100
-    // keys a request of 8 heads: 44 us for 128 requests, one row tile 60; 2000 keys
-    // and 16 requests over a long prefix: 107, one row tile 84.
+    // Few rows at d = 256, where each of eight warps takes 15000 cycles for a unit of
+    // its own: worth it for items of few units (over_s of them for the item itself),
+    // else one row tile.  100 keys a request of 8 heads: 44 us for 128 requests, one
+    // row tile 60; 2000 keys and 16 requests over a long prefix: 107, one row tile 84.
     __host__ __device__ static constexpr bool few_items(int units, int items) { return D != 256 || units < 14LL * items; }
     __device__ static float cost_p(int mode, int halves, bool shared, float own) {
         return mode == kFew ? few_cost(halves) : mode == kOne ? (D == 64 ? 3800 : D == 128 ? 5000 : 1600)
@@ -562,13 +571,15 @@ __device__ __forceinline__ void pf_issue_pv(uint32_t d_tmem, uint32_t p_tmem, ui
 // warps when there are more than 16 rows (each takes 16): it walks its range of
 // the list, copies 16 keys of K or V at a time into a ring of its own
 // (TMA; a slot is free as soon as this warp has read it, so nothing waits for
-// another warp), and keeps scores, wfours and the accumulator in registers
+// another warp), and keeps scores, weights and the accumulator in registers
 // (mma.sync m16n8k16).  An item's end costs a store of the rows and no barrier.
 // A step is 8 KB of K and of V (64 keys at d = 64, 16 at d = 256, where Q and O
-// take the registers): 780 cycles for 64 keys of a CTA's eight warps at d = 128,
-// of which the copies at the CTA's share of HBM are 700; 500 at d = 64 (with 32
-// keys a step 600: 32 requests of 32 heads 58 us, with 64 49).  64 single tokens: 4.9 TB/s.  Eight warps that
-// share 128-key tiles and join in shared memory took 442 us where these take 349.
+// take the registers).  For 64 keys a CTA's eight warps take 780 to 880 cycles at d
+// = 128 while a third of the CTAs copy (37 to 42 B a cycle; an equal share of HBM
+// for all is 23), 520 at d = 64 (with 32 keys a step 600: 32 requests of 32 heads 58
+// us, with 64 49).  64 single tokens with 4000 to 16000 keys of their own and no
+// prefix: 6.8 TB/s.  Eight warps that share 128-key tiles and join in shared memory
+// took 442 us where these take 349.
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -790,7 +801,7 @@ __device__ __forceinline__ void few_rows(const CUtensorMap* tk, const CUtensorMa
                         for (int i = 0; i < 2 * kKT; ++i) {
                             const float p0 = ex2_mufu(fmaf(s[i][2 * h], scale, -use)), p1 = ex2_mufu(fmaf(s[i][2 * h + 1], scale, -use));
                             l[h] += p0 + p1;
-                            p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit wfours feed the product; l keeps 32 bits
+                            p[i >> 1][2 * (i & 1) + h] = pack_bf16x2(p0, p1);   // 16-bit weights feed the product; l keeps 32 bits
                         }
                     }
                 }
@@ -1435,7 +1446,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
                         const float p0 = ex2_mufu(x0), p1 = ex2_mufu(x1);
                         if (i & 1) lb = f2_add(lb, f2_pack(p0, p1));
                         else la = f2_add(la, f2_pack(p0, p1));
-                        pk[i] = pack_bf16x2(p0, p1);   // 16-bit wfours feed the tensor core; l keeps 32 bits
+                        pk[i] = pack_bf16x2(p0, p1);   // 16-bit weights feed the tensor core; l keeps 32 bits
                     }
                     tmem_st16(tS + st * 16, pk);
                 }
@@ -1511,7 +1522,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 // ---------------------------------------------------------------------- join
 
 // Bound by latency (header, row, places, (m, l), O: five loads that depend on
-// one another, 3.4 us for one row) and, with many rows, by the segments' traffic
+// one another, 3.4 us for one row, 7 from cold caches) and, with many rows, by the segments' traffic
 // (512 rows of 32 heads: 23 us from a cold L2, a seventh of that out of it).
 // A warp joins kHeads heads of one key/value head in one row of q: their
 // segments are the same, their rows in a segment neighbours, so one set of
@@ -1521,7 +1532,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tq_p, const __grid_constant__ 
 // items may have written their rows already.  A warp looks at so many rows, a lane
 // each, and the block's warps share what there is to join.  Six prompts of up to
 // 2048 tokens over 8192 shared keys, the whole call: 1113 us with a row a warp,
-// 1070 with four (or eight: but four prompts without a prefix 110, 101 and 118).
+// 1070 on the same box with four (or eight: but four prompts without a prefix 110, 101 and 118).
 template <int D, int kHeads, bool kSplit, int kRows>
 __global__ void __launch_bounds__(256) prefix_join_kernel(const PfArgs a) {
     constexpr int E = D / 32, H = kHeads;

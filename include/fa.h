@@ -311,8 +311,10 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
  * - A block table [B, table_width] (int32) lists each request's pages in the
  *   order of its tokens.  An entry outside [0, num_pages) is "no page":
  *   nothing is read or written there, and the keys it would hold are absent.
- * - At most 1024 requests a call.  All lengths are read on the device, so a
- *   captured graph serves later steps with other lengths.
+ * - At most 1024 requests a call.  The requests' lengths are read on the device,
+ *   so a captured graph serves later steps with other lengths.  What the host
+ *   passes stays as captured: prefix_len, max_seqlen, the numbers of rows and
+ *   requests, the table's width.
  */
 
 /*
@@ -395,7 +397,9 @@ int fa_kv_store(const void *k, const void *v, int64_t k_stride, int64_t v_stride
  * at most max_seqlen rows; NULL: one row a request, T == B.  Rows outside
  * every request are not written.  A request with more rows than max_seqlen
  * makes the call compute nothing and report FA_ERR_INVALID through
- * fa_get_device_status.
+ * fa_get_device_status.  max_seqlen decides one shape of the kernel for all
+ * requests: right for any mixture, but a chunk of 512 rows among 63 single
+ * tokens (32 / 8 heads of 128) takes 4 to 12 % longer than the two apart.
  * block_table [B, table_width] and kv_lens [B] (s_b, taken as at least 0 and
  * at most table_width * page_size): the requests' own keys; prefix_table: the
  * prefix's pages (ceil(prefix_len / page_size) entries), NULL when prefix_len
