@@ -337,9 +337,11 @@ int fa_bwd_noalloc(const void *q, const void *k, const void *v, const void *o, c
  * width) could not give, entries of the queue that are no pages among them (a
  * request that leaves with absent pages puts them there).  Their table entries
  * are -1 (past the width: none), their tokens' slots -1; the caller looks at
- * missing before the step counts as done.  (Tokens that go on in a page that
- * the request itself lacks have slots -1, too, and are not counted.)  Pages
- * coming back beyond num_pages in the queue are dropped.
+ * missing before the step counts as done.  (The same step repeated meets entries
+ * that are no pages again; they are gone once pool_out is taken over.  Tokens
+ * that go on in a page that the request itself lacks have slots -1, too, and
+ * are not counted.)  Pages coming back beyond num_pages in the queue are
+ * dropped.
  * cu_new [B+1]: prefix sums of the n_b that are >= 0 (the cu_seqlens of the
  * step's packed rows); kv_lens [B]: c_b + n_b (at most the row's capacity), 0
  * for a request that leaves; slots [num_slots]: the slot of packed row t, -1
