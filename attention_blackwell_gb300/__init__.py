@@ -12,7 +12,7 @@ import os
 
 import torch
 
-__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "page_plan", "page_pool", "kv_store", "prefix_fwd", "prefix_workspace", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
+__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "page_plan", "page_pool", "kv_store", "prefix_fwd", "prefix_workspace", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace", "rope_store", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "lib", "libfa.so")
@@ -77,6 +77,16 @@ def lib():
         L.fa_prefix_workspace_size.argtypes = [i] * 6
         L.fa_prefix_fwd.restype = i
         L.fa_prefix_fwd.argtypes = [vp, i64, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, i, vp, vp, i, vp, i, vp, sz, vp]
+        L.fa_qk_rope.restype = i
+        L.fa_qk_rope.argtypes = [vp, vp, i64, i64, vp, vp, i64, i64, i, i, i, i, vp, vp, i, i, i, vp, i, vp, vp, i, f, vp]
+        L.fa_qk_rope_bwd_workspace_size.restype = sz
+        L.fa_qk_rope_bwd_workspace_size.argtypes = [i]
+        L.fa_qk_rope_bwd.restype = i
+        L.fa_qk_rope_bwd.argtypes = ([vp, vp, i64, i64, vp, vp, i64, i64, vp, vp, vp, vp, i, i, i, i, vp, vp, i, i, i, vp, i, vp, vp, i, f,
+                                      vp, sz, vp])
+        L.fa_rope_store.restype = i
+        L.fa_rope_store.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, i, i, i, i, vp, vp, i, i, i, vp, vp, vp, i, f, vp, vp, vp, vp, vp,
+                                    i, i, vp]
         L.fa_exp2_emu.restype = i
         L.fa_exp2_emu.argtypes = [vp, vp, i64, vp]
         L.fa_selftest_timeout.restype = i
@@ -508,6 +518,239 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
     if rc:
         _check(rc, "fa_prefix_fwd")
     return out, lse
+
+
+def _tokens(t, name):
+    """(T, H, d, elements between tokens) of a bf16 [T, H, d] or [B, N, H, d]
+    tensor that is dense within a token and whose tokens are evenly apart."""
+    shape = t.shape
+    if len(shape) == 3:
+        st = _rows(t, name)
+        return shape[0], shape[1], shape[2], st
+    if len(shape) != 4:
+        raise ValueError("%s must have 3 or 4 dimensions" % name)
+    B, N, H, d = shape
+    sb, sn, sh, sd = t.stride()
+    if B > 1 and N > 1 and sb != N * sn:
+        raise ValueError("%s must have its tokens evenly apart" % name)
+    if t.dtype is not torch.bfloat16:
+        raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
+    if d > 1 and sd != 1 or H > 1 and sh != d:
+        raise ValueError("%s must be contiguous within a token" % name)
+    return B * N, H, d, sn if N > 1 else sb if B > 1 else H * d
+
+
+def _rope_tables(cos, sin, positions, T, d, q_weight, k_weight):
+    """Checks; returns (max_pos, rot, 1 for bf16 weights)."""
+    if cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or not cos.is_contiguous() or not sin.is_contiguous():
+        _need(cos, "cos", torch.float32)
+        _need(sin, "sin", torch.float32)
+    shape = cos.shape
+    if len(shape) != 2 or shape != sin.shape:
+        raise ValueError("cos and sin must be [max_pos, rot / 2]")
+    if positions is not None:
+        if positions.dtype is not torch.int32 or not positions.is_contiguous():
+            _need(positions, "positions", torch.int32)
+        if positions.numel() != T:
+            raise ValueError("positions must have one element a token")
+    bf16 = 0
+    for w in (q_weight, k_weight):
+        if w is not None:
+            if w.dtype is not torch.float32 and w.dtype is not torch.bfloat16 or not w.is_contiguous() or w.numel() != d:
+                raise ValueError("norm weights must be float32 or bfloat16 [d], contiguous")
+            bf16 = int(w.dtype is torch.bfloat16)
+    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
+        raise ValueError("norm weights must have one type")
+    return shape[0], 2 * shape[1], bf16
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, q_out=None, k_out=None,
+            stream=None):
+    """Norms of queries and keys for each head (where there are weights) and the
+    rotation by position, in one pass.  Returns (q_out, k_out).
+
+    q [.., Hq, d], k [.., Hkv, d] bf16 with leading [B, N] or [T] (tokens may be
+    strided), cos / sin float32 [max_pos, rot / 2], positions int32, one a token
+    (None: a token's index in its sequence, or in [T]; outside the tables: the
+    token is left alone), weights [d] float32 or bf16.  Pairs are (i, i + rot / 2),
+    or (2 i, 2 i + 1) when interleaved.  The outputs may be q and k themselves.
+    """
+    dev = q.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (q, k, cos, sin, positions, q_weight, k_weight, q_out, k_out),
+                          lambda: qk_rope(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out))
+    T, Hq, d, qs = _tokens(q, "q")
+    Tk, Hkv, dk, ks = _tokens(k, "k")
+    if q.shape[:-2] != k.shape[:-2] or d != dk:
+        raise ValueError("q and k must have the same tokens and head dim")
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    if q_out is None:
+        q_out, qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), Hq * d
+    else:
+        qo = _tokens(q_out, "q_out")[3]
+    if k_out is None:
+        k_out, ko = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), Hkv * d
+    else:
+        ko = _tokens(k_out, "k_out")[3]
+    if q_out.shape != q.shape or k_out.shape != k.shape:
+        raise ValueError("q_out and k_out must have q's and k's shapes")
+    _one_device(dev, (k, cos, sin, positions, q_weight, k_weight, q_out, k_out))
+    if T == 0:
+        return q_out, k_out
+    rc = (_lib or lib()).fa_qk_rope(q.data_ptr(), k.data_ptr(), qs, ks, q_out.data_ptr(), k_out.data_ptr(), qo, ko, T, Hq, Hkv, d,
+                                    cos.data_ptr(), sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, _at(positions),
+                                    q.shape[-3], _at(q_weight), _at(k_weight), bf16, eps, _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_qk_rope")
+    return q_out, k_out
+
+
+def qk_rope_bwd_workspace(d=HEAD_DIM, device=None):
+    """A uint8 CUDA tensor large enough for qk_rope_bwd with norm weights."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = lib().fa_qk_rope_bwd_workspace_size(int(d))
+        if n == 0:
+            raise ValueError("invalid head dim for the workspace")
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, dq=None,
+                dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Gradients of qk_rope.  Returns (dq, dk, dq_weight, dk_weight); the weights'
+    are float32 [d], None where there is no weight.
+
+    dq_out, dk_out: gradients of qk_rope's outputs; q, k and the rest as it took
+    them (q and k may be None without their weight).  dq and dk are contiguous and
+    may be dq_out and dk_out themselves.
+    """
+    dev = dq_out.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (dq_out, dk_out, q, k, cos, sin, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight, workspace),
+                          lambda: qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, dq, dk,
+                                              dq_weight, dk_weight, workspace))
+    T, Hq, d, gqs = _tokens(dq_out, "dq_out")
+    Tk, Hkv, d2, gks = _tokens(dk_out, "dk_out")
+    if dq_out.shape[:-2] != dk_out.shape[:-2] or d != d2:
+        raise ValueError("dq_out and dk_out must have the same tokens and head dim")
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    qs = ks = 0
+    if q_weight is not None:
+        if q is None or q.shape != dq_out.shape:
+            raise ValueError("q must have dq_out's shape")
+        qs = _tokens(q, "q")[3]
+    if k_weight is not None:
+        if k is None or k.shape != dk_out.shape:
+            raise ValueError("k must have dk_out's shape")
+        ks = _tokens(k, "k")[3]
+    if dq is None:
+        dq = torch.empty(dq_out.shape, dtype=torch.bfloat16, device=dq_out.device)
+    if dk is None:
+        dk = torch.empty(dk_out.shape, dtype=torch.bfloat16, device=dq_out.device)
+    _need(dq, "dq", torch.bfloat16)
+    _need(dk, "dk", torch.bfloat16)
+    if dq.shape != dq_out.shape or dk.shape != dk_out.shape:
+        raise ValueError("dq and dk must have dq_out's and dk_out's shapes")
+    if q_weight is not None and dq_weight is None:
+        dq_weight = torch.empty(d, dtype=torch.float32, device=dq_out.device)
+    if k_weight is not None and dk_weight is None:
+        dk_weight = torch.empty(d, dtype=torch.float32, device=dq_out.device)
+    for w, g, n in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if g is not None:
+            if w is None:
+                raise ValueError("%s without a weight" % n)
+            _need(g, n, torch.float32)
+            if g.numel() != d:
+                raise ValueError("%s must have d elements" % n)
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = qk_rope_bwd_workspace(d, device=dq_out.device)
+    _one_device(dev, (dk_out, q if qs else None, k if ks else None, cos, sin, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight,
+                      workspace))
+    rc = (_lib or lib()).fa_qk_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), gqs, gks, _at(q) if qs else None, _at(k) if ks else None, qs, ks,
+                                        dq.data_ptr(), dk.data_ptr(), _at(dq_weight), _at(dk_weight), T, Hq, Hkv, d, cos.data_ptr(),
+                                        sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, _at(positions), max(dq_out.shape[-3], 1),
+                                        _at(q_weight), _at(k_weight), bf16, eps, _at(workspace),
+                                        workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                        _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_qk_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+def _pages4(k_pages, k_scales, v_pages, v_scales):
+    """Shape [P, Hkv, page, d] of a 4-bit cache."""
+    u8 = torch.uint8
+    if (k_pages.dtype is not u8 or v_pages.dtype is not u8 or k_scales.dtype is not u8 or v_scales.dtype is not u8
+            or not k_pages.is_contiguous() or not v_pages.is_contiguous() or not k_scales.is_contiguous() or not v_scales.is_contiguous()):
+        for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages"), (k_scales, "k_scales"), (v_scales, "v_scales")):
+            _need(t, n, u8)
+    shape, scales = k_pages.shape, k_scales.shape
+    if len(shape) != 4 or shape != v_pages.shape or scales != v_scales.shape:
+        raise ValueError("k_pages and v_pages must be [num_pages, Hkv, page_size, d / 2], their scales one shape")
+    P, Hkv, page, half = shape
+    if len(scales) != 4 or scales[0] != P or scales[1] != Hkv or scales[2] != page or scales[3] * 16 != half:
+        raise ValueError("k_scales and v_scales must be [num_pages, Hkv, page_size, d / 32]")
+    return P, Hkv, page, 2 * half
+
+
+def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=None, v_scales=None, q_weight=None, k_weight=None,
+               eps=1e-6, interleaved=False, q_out=None, stream=None):
+    """A step's queries normed and rotated into q_out, its keys normed, rotated and
+    stored with its values in the cache at slots.  Returns q_out (None without q).
+
+    q [T, Hq, d] (or None), k, v [T, Hkv, d] bf16 (tokens may be strided),
+    positions and slots int32 [T] (a position outside the tables: the token is left
+    alone; a slot outside the cache: its key and value are not stored).  Pages are
+    bf16 [num_pages, Hkv, page_size, d], or with scales uint8 [.., d / 2] and
+    [.., d / 32] in 4 bits; cos, sin, weights and pairs as in qk_rope.  q_out may
+    be q itself.
+    """
+    dev = k_pages.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (k_pages, v_pages, k_scales, v_scales, q, k, v, cos, sin, positions, slots, q_weight, k_weight, q_out),
+                          lambda: rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales, v_scales, q_weight,
+                                             k_weight, eps, interleaved, q_out))
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("k_scales and v_scales come together")
+    P, Hkv, page, d = _pages(k_pages, v_pages) if k_scales is None else _pages4(k_pages, k_scales, v_pages, v_scales)
+    ks, vs = _rows(k, "k"), _rows(v, "v")
+    shape = k.shape
+    T = shape[0]
+    if shape[1] != Hkv or shape[2] != d or shape != v.shape:
+        raise ValueError("k and v must be [T, Hkv, d] with the pages' Hkv and d")
+    if slots.dtype is not torch.int32 or not slots.is_contiguous():
+        _need(slots, "slots", torch.int32)
+    if positions is None or slots.numel() != T:
+        raise ValueError("positions and slots must have one element a token")
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    Hq = qs = qo = 0
+    if q is None:
+        q_out = None
+    else:
+        qs = _rows(q, "q")
+        Hq = q.shape[1]
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must be [T, Hq, d] with k's T and d")
+        if q_out is None:
+            q_out, qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), Hq * d
+        else:
+            qo = _rows(q_out, "q_out")
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    _one_device(dev, (v_pages, k_scales, v_scales, q, k, v, cos, sin, positions, slots, q_weight, k_weight, q_out))
+    if T == 0:
+        return q_out
+    rc = (_lib or lib()).fa_rope_store(_at(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _at(q_out), qo, T, Hq, Hkv, d, cos.data_ptr(),
+                                       sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, positions.data_ptr(), _at(q_weight),
+                                       _at(k_weight), bf16, eps, slots.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                       _at(k_scales), _at(v_scales), P, page, _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_rope_store")
+    return q_out
 
 
 def set_debug_counters(visits=None, inner=None, rescales=None):

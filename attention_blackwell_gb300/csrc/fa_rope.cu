@@ -1,0 +1,712 @@
+// fa_rope.cu -- what lies between the projections and attention (sm_103a):
+// fa_qk_rope (norms per head and position rotation of Q and K), fa_qk_rope_bwd
+// (their gradients) and fa_rope_store (the same on the way into a paged cache of
+// bf16 or 4-bit rows).
+//
+//   n(x) = x r w, r = (mean x^2 + eps)^(-1/2)   over a head's d elements, or x
+//   y = R n(x): the first rot elements in pairs (i, i + rot/2) or (2i, 2i + 1),
+//       (a, b) -> (a cos - b sin, b cos + a sin), the angles of the token's position
+// and, for u = R^T dy and t = u w,
+//   dx = r (t - x r^2 mean(t x)),   dw = sum over rows of u x r.
+// All of it in 32 bits, rounded once where it is stored.
+//
+// Layout: a warp takes one token, d / 16 lanes a head's row, so that a lane's 16
+// elements are whole pairs whatever rot is: two 16-byte chunks, and the eight
+// angles that the lane needs are the same for every head.  They stay in registers
+// while the warp goes over the token's heads.
+#include <math.h>
+#include <stdint.h>
+
+#include "../../include/fa.h"
+#include "fa_internal.h"
+#include "fa_kv4.cuh"
+
+namespace fa {
+namespace {
+
+// What a call rotates and how.
+struct RopeArgs {
+    const float *cos, *sin;      // [max_pos, rot / 2]
+    const int* positions;        // [T] or null: t % seq_len
+    const void *wq, *wk;         // [d] float or bf16, null: no norm
+    int T, Hq, Hkv, max_pos, rot, inter, seq_len, w_bf16;
+    float eps;
+    int passes, parts;           // passes over a token's rows, warps that share a token
+};
+
+struct RowsArgs {
+    const __nv_bfloat16 *q, *k;
+    __nv_bfloat16 *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;
+};
+
+struct GradArgs {
+    const __nv_bfloat16 *gq, *gk, *q, *k;
+    __nv_bfloat16 *dq, *dk;
+    long long gq_stride, gk_stride, q_stride, k_stride;
+    float* partial;              // [grid][2][d]
+};
+
+struct PutArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    __nv_bfloat16* q_out;
+    long long q_stride, k_stride, v_stride, q_out_stride;
+    const int* slots;
+    uint8_t *kp, *vp, *ks, *vs;  // pages and, with 4 bits, their scales
+    int ps_log2;
+    long long num_slots;
+};
+
+// The lane's place in a row and its angles.
+template <int D> struct Lane {
+    static constexpr int kLanes = D / 16, kRows = 32 / kLanes;   // lanes a row, rows a pass
+    int a, b;            // first elements of its two chunks of eight
+    bool turns;
+    float c[8], s[8];
+    __device__ __forceinline__ void place(const RopeArgs& r, int lane) {
+        const int j = lane % kLanes, m = r.rot >> 4;
+        turns = j < m;
+        const bool split = turns && !r.inter;
+        a = (split ? j : 2 * j) * 8;
+        b = (split ? j + m : 2 * j + 1) * 8;
+    }
+    __device__ __forceinline__ void angles(const RopeArgs& r, int lane, int pos) {
+        if (!turns) return;
+        const long long at = (long long)pos * (r.rot >> 1) + lane % kLanes * 8;
+        const float4 *pc = reinterpret_cast<const float4*>(r.cos + at), *ps = reinterpret_cast<const float4*>(r.sin + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 x = pc[i], y = ps[i];
+            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
+            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+        }
+    }
+    // Every product and sum is rounded by itself, as the formula reads: a 4-bit
+    // cache's codes lie next to borders, and so a key gets the same code on every path.
+    __device__ __forceinline__ void turn(float (&v)[16], bool inter, float sign) const {
+        if (!turns) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = inter ? v[2 * i] : v[i], y = inter ? v[2 * i + 1] : v[8 + i], sn = sign * s[i];
+            const float p = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, sn)), q = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, sn));
+            if (inter) v[2 * i] = p, v[2 * i + 1] = q;
+            else v[i] = p, v[8 + i] = q;
+        }
+    }
+};
+
+__device__ __forceinline__ int position_of(const RopeArgs& r, int t) {
+    const int p = r.positions ? r.positions[t] : t % r.seq_len;
+    return p >= 0 && p < r.max_pos ? p : -1;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// Sum over the lanes of a row.
+template <int L> __device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int o = L / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+template <int D> __device__ __forceinline__ float inv_rms(const float (&v)[16], float eps) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
+    return 1.f / sqrtf(row_sum<D / 16>(sum) * (1.f / D) + eps);
+}
+
+// Both weights in shared memory as floats ([2][D]; rows of 1 for the one without a norm).
+template <int D> __device__ __forceinline__ void stage_weights(const RopeArgs& r, float* w) {
+    for (int i = threadIdx.x; i < 2 * D; i += blockDim.x) {
+        const void* src = i < D ? r.wq : r.wk;
+        const int e = i & (D - 1);
+        w[i] = !src ? 1.f : r.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(src)[e]) : static_cast<const float*>(src)[e];
+    }
+}
+template <int D> __device__ __forceinline__ void weigh(float (&v)[16], float x, const float* w, const Lane<D>& me) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = v[i] * x * w[me.a + i];
+        v[8 + i] = v[8 + i] * x * w[me.b + i];
+    }
+}
+
+// ------------------------------------------------------------------ forward
+
+// One pass: kRows rows, from the list of the token's q and k rows.  kDeep passes'
+// loads are made before the first is worked on.
+template <int D>
+__global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
+    using Me = Lane<D>;
+    constexpr int kDeep = 4;
+    __shared__ float s_w[2 * D];
+    grid_launch_next();
+    grid_wait();
+    if (r.wq || r.wk) stage_weights<D>(r, s_w);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, sub = lane / Me::kLanes, rows = r.Hq + r.Hkv;
+    const long long warp = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    const int t = (int)(warp / r.parts), part = (int)(warp % r.parts);
+    if (t >= r.T) return;
+    const int pos = position_of(r, t);
+    if (pos < 0) return;
+    Me me;
+    me.place(r, lane);
+    me.angles(r, lane, pos);
+    const int p1 = (int)((long long)(part + 1) * r.passes / r.parts);
+    for (int p = (int)((long long)part * r.passes / r.parts); p < p1; p += kDeep) {
+        uint4 in[kDeep][2];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int h = (p + i) * Me::kRows + sub;
+            if (p + i < p1 && h < rows) {
+                const __nv_bfloat16* src = h < r.Hq ? a.q + t * a.q_stride + h * D : a.k + t * a.k_stride + (h - r.Hq) * D;
+                in[i][0] = load16(src + me.a);
+                in[i][1] = load16(src + me.b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int h = (p + i) * Me::kRows + sub;
+            if (p + i >= p1) break;
+            const bool real = h < rows, isq = h < r.Hq;
+            float v[16] = {};
+            if (real) {
+                unpack8(in[i][0], v);
+                unpack8(in[i][1], v + 8);
+            }
+            if (r.wq || r.wk) {
+                const float x = inv_rms<D>(v, r.eps);
+                if (isq ? r.wq : r.wk) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
+            }
+            me.turn(v, r.inter, 1.f);
+            if (real) {
+                __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D : a.k_out + t * a.k_out_stride + (h - r.Hq) * D;
+                *reinterpret_cast<uint4*>(dst + me.a) = pack8(v);
+                *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 8);
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- gradients
+
+// One operand's rows (q or k): the warps go over the tokens; each block leaves its
+// sum of the weight's gradient in `partial`.
+template <int D>
+__device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_bfloat16* gs, long long g_stride, const __nv_bfloat16* xs,
+                                          long long x_stride, __nv_bfloat16* outs, const float* w, float (&s_dw)[8][D], float* partial) {
+    using Me = Lane<D>;
+    constexpr int kDeep = 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / Me::kLanes;
+    Me me;
+    me.place(r, lane);
+    float dw[16] = {};
+    for (long long t = blockIdx.x * 8LL + warp; t < r.T; t += gridDim.x * 8LL) {
+        const int pos = position_of(r, (int)t);
+        if (pos < 0) continue;
+        me.angles(r, lane, pos);
+        const __nv_bfloat16 *g = gs + t * g_stride, *x = xs + t * x_stride;
+        __nv_bfloat16* out = outs + t * H * D;
+        for (int h0 = sub; h0 - sub < H; h0 += kDeep * Me::kRows) {
+            uint4 in[kDeep][4];
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const int h = h0 + i * Me::kRows;
+                if (h < H) {
+                    in[i][0] = load16(g + h * D + me.a);
+                    in[i][1] = load16(g + h * D + me.b);
+                    if (w) {
+                        in[i][2] = load16(x + h * D + me.a);
+                        in[i][3] = load16(x + h * D + me.b);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const int h = h0 + i * Me::kRows;
+                if (h - sub >= H) break;
+                float u[16] = {};
+                if (h < H) {
+                    unpack8(in[i][0], u);
+                    unpack8(in[i][1], u + 8);
+                }
+                me.turn(u, r.inter, -1.f);
+                if (w) {
+                    float v[16] = {};
+                    if (h < H) {
+                        unpack8(in[i][2], v);
+                        unpack8(in[i][3], v + 8);
+                    }
+                    // With eps = 0 a missing row's r is infinite.
+                    const float rms = inv_rms<D>(v, r.eps), x1 = h < H ? rms : 0.f;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        v[e] *= x1;                                     // x r
+                        dw[e] = fmaf(u[e], v[e], dw[e]);
+                        u[e] *= w[(e < 8 ? me.a : me.b - 8) + e];
+                        sum = fmaf(u[e], v[e], sum);
+                    }
+                    sum = row_sum<D / 16>(sum) * (1.f / D);             // mean(t x) r
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = x1 * fmaf(-v[e], sum, u[e]);
+                }
+                if (h < H) {
+                    *reinterpret_cast<uint4*>(out + h * D + me.a) = pack8(u);
+                    *reinterpret_cast<uint4*>(out + h * D + me.b) = pack8(u + 8);
+                }
+            }
+        }
+    }
+    if (!w) return;
+    // The warp's rows, then the block's warps.
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+#pragma unroll
+        for (int o = 16; o >= Me::kLanes; o >>= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+        if (sub == 0) s_dw[warp][(e < 8 ? me.a : me.b - 8) + e] = dw[e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += 256) {
+        float sum = s_dw[0][i];
+#pragma unroll
+        for (int y = 1; y < 8; ++y) sum += s_dw[y][i];
+        partial[i] = sum;
+    }
+    __syncthreads();
+}
+
+// The blocks' sums are added up by a second kernel in the blocks' order, so equal
+// calls give equal results.
+template <int D>
+__global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
+    __shared__ float s_w[2 * D];
+    __shared__ float s_dw[8][D];
+    grid_launch_next();
+    grid_wait();
+    if (r.wq || r.wk) stage_weights<D>(r, s_w);
+    __syncthreads();
+    float* partial = a.partial + (long long)blockIdx.x * (2 * D);
+    grad_rows<D>(r, r.Hq, a.gq, a.gq_stride, a.q, a.q_stride, a.dq, r.wq ? s_w : nullptr, s_dw, partial);
+    grad_rows<D>(r, r.Hkv, a.gk, a.gk_stride, a.k, a.k_stride, a.dk, r.wk ? s_w + D : nullptr, s_dw, partial + D);
+}
+
+// 32 columns of the blocks' sums a block, eight rows at a time.
+__global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float* partial, int blocks, int d, float* dwq, float* dwk) {
+    __shared__ float s[8][32];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+    grid_wait();
+    float sum = 0.f;
+    for (int b = y; b < blocks; b += 8) sum += partial[(long long)b * (2 * d) + col];
+    s[y][x] = sum;
+    __syncthreads();
+    if (y) return;
+    for (int i = 1; i < 8; ++i) sum += s[i][x];
+    float* out = col < d ? dwq : dwk;
+    if (out) out[col & (d - 1)] = sum;
+}
+
+// --------------------------------------------------------------------- store
+
+// Four elements of a row, from i on, normed and turned (w null: no norm; turn
+// false: as they are).  Their partners in the other half are read again (they are in
+// L1): the lanes of a 4-bit row hold elements by groups, not by pairs.
+__device__ __forceinline__ void four_of(const RopeArgs& r, const __nv_bfloat16* row, int i, float x, const float* w, bool turn,
+                                        const float* pc, const float* ps, float (&y)[4]) {
+    auto get = [&](int at, float (&v)[4]) {
+        const uint2 u = *reinterpret_cast<const uint2*>(row + at);
+        v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
+        v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
+        if (w)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = v[e] * x * w[at + e];
+    };
+    get(i, y);
+    if (!turn || i >= r.rot) return;
+    const int half = r.rot >> 1;
+    if (r.inter) {
+        const float2 c = *reinterpret_cast<const float2*>(pc + (i >> 1)), s = *reinterpret_cast<const float2*>(ps + (i >> 1));
+        const float a0 = y[0], a1 = y[2];
+        y[0] = __fsub_rn(__fmul_rn(a0, c.x), __fmul_rn(y[1], s.x));
+        y[1] = __fadd_rn(__fmul_rn(y[1], c.x), __fmul_rn(a0, s.x));
+        y[2] = __fsub_rn(__fmul_rn(a1, c.y), __fmul_rn(y[3], s.y));
+        y[3] = __fadd_rn(__fmul_rn(y[3], c.y), __fmul_rn(a1, s.y));
+        return;
+    }
+    const bool low = i < half;
+    float z[4];
+    get(low ? i + half : i - half, z);
+    const int at = low ? i : i - half;
+    const float4 c4 = *reinterpret_cast<const float4*>(pc + at), s4 = *reinterpret_cast<const float4*>(ps + at);
+    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float own = __fmul_rn(y[e], c[e]), other = __fmul_rn(z[e], s[e]);
+        y[e] = low ? __fsub_rn(own, other) : __fadd_rn(own, other);
+    }
+}
+
+// A row of k or v as 4-bit codes, by eight lanes (see fa_kv4.cuh); `real`: the
+// lanes have a row.
+template <int D>
+__device__ __forceinline__ void put_four(const RopeArgs& r, const __nv_bfloat16* row, bool real, const float* w, bool turn, const float* pc,
+                                         const float* ps, uint8_t* codes, uint8_t* scales, int lane) {
+    constexpr int kGroups = D / 32;
+    const int l = lane & 7;
+    float x = 1.f;
+    if (__any_sync(0xffffffffu, w != nullptr)) {
+        float sum = 0.f;
+        if (real && w)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const uint2 u = *reinterpret_cast<const uint2*>(row + 32 * g + 4 * l);
+                const float a = __uint_as_float(u.x << 16), b = __uint_as_float(u.x & 0xffff0000u), c = __uint_as_float(u.y << 16),
+                            e = __uint_as_float(u.y & 0xffff0000u);
+                sum = fmaf(a, a, fmaf(b, b, fmaf(c, c, fmaf(e, e, sum))));
+            }
+        x = 1.f / sqrtf(row_sum<8>(sum) * (1.f / D) + r.eps);
+    }
+    float y[kGroups][4];
+    uint32_t most[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        if (real) four_of(r, row, 32 * g + 4 * l, x, w, turn, pc, ps, y[g]);
+        else y[g][0] = y[g][1] = y[g][2] = y[g][3] = 0.f;
+        most[g] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most[g] = max(most[g], __float_as_uint(y[g][e]) & 0x7fffffffu);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) most[g] = max(most[g], __shfl_xor_sync(0xffffffffu, most[g], o));
+    uint32_t out[kGroups / 2], sb[kGroups];
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        sb[g] = scale_byte(most[g]);
+        const float s = scale_f32(sb[g]);
+        const uint32_t c = sb[g] == 0 || sb[g] == kScaleNaN ? 0u : codes_of(y[g], s, __frcp_rn(s));
+        out[g / 2] = g & 1 ? out[g / 2] | c << 16 : c;
+    }
+    if (!real) return;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(codes) + l * (kGroups / 2);
+    if constexpr (D == 64) *dst = out[0];
+    else if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (l == 0) {
+        if constexpr (D == 64) *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(sb[0] | sb[1] << 8);
+        else
+#pragma unroll
+            for (int g = 0; g < kGroups; g += 4) reinterpret_cast<uint32_t*>(scales)[g / 4] = sb[g] | sb[g + 1] << 8 | sb[g + 2] << 16 | sb[g + 3] << 24;
+    }
+}
+
+// A token's rows: q, k and v of bf16 pages in one list of passes; with 4-bit pages
+// the q rows first, then k and v, four rows a pass.
+template <int D, bool kFour>
+__global__ void __launch_bounds__(256) rope_store_kernel(const RopeArgs r, const PutArgs a) {
+    using Me = Lane<D>;
+    constexpr int kDeep = 2;
+    __shared__ float s_w[2 * D];
+    grid_launch_next();
+    grid_wait();
+    const bool norm = r.wq || r.wk;
+    if (norm) stage_weights<D>(r, s_w);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, sub = lane / Me::kLanes;
+    const long long warp = blockIdx.x * 8LL + (threadIdx.x >> 5);
+    const int t = (int)(warp / r.parts), part = (int)(warp % r.parts);
+    if (t >= r.T) return;
+    const int pos = position_of(r, t);
+    const long long slot = a.slots[t];
+    if (pos < 0) return;
+    const bool keep = slot >= 0 && slot < a.num_slots;
+    Me me;
+    me.place(r, lane);
+    me.angles(r, lane, pos);
+    const long long page = (slot >> a.ps_log2) * r.Hkv, in_page = slot & ((1 << a.ps_log2) - 1);
+    // Row of the cache that key/value head h of this token is.
+    auto cell = [&](int h) { return ((page + h) << a.ps_log2) + in_page; };
+    const int rows = kFour ? r.Hq : r.Hq + 2 * r.Hkv, first = (rows + Me::kRows - 1) / Me::kRows;
+    const int p0 = (int)((long long)part * r.passes / r.parts), p1 = (int)((long long)(part + 1) * r.passes / r.parts);
+    for (int p = p0; p < min(p1, first); p += kDeep) {
+        uint4 in[kDeep][2];
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int h = (p + i) * Me::kRows + sub;
+            if (p + i < p1 && h < rows) {
+                const __nv_bfloat16* src = h < r.Hq            ? a.q + t * a.q_stride + h * D
+                                           : h < r.Hq + r.Hkv ? a.k + t * a.k_stride + (h - r.Hq) * D
+                                                               : a.v + t * a.v_stride + (h - r.Hq - r.Hkv) * D;
+                in[i][0] = load16(src + me.a);
+                in[i][1] = load16(src + me.b);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int h = (p + i) * Me::kRows + sub;
+            if (p + i >= p1) break;
+            const bool real = h < rows, isq = h < r.Hq, isv = h >= r.Hq + r.Hkv;
+            float v[16] = {};
+            if (real) {
+                unpack8(in[i][0], v);
+                unpack8(in[i][1], v + 8);
+            }
+            if (norm) {
+                const float x = inv_rms<D>(v, r.eps);
+                if (!isv && (isq ? r.wq : r.wk)) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
+            }
+            if (!isv) me.turn(v, r.inter, 1.f);
+            if (!real || !(isq || keep)) continue;
+            __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D
+                                     : reinterpret_cast<__nv_bfloat16*>(isv ? a.vp : a.kp) + cell(h - r.Hq - (isv ? r.Hkv : 0)) * D;
+            *reinterpret_cast<uint4*>(dst + me.a) = isv ? in[i][0] : pack8(v);
+            *reinterpret_cast<uint4*>(dst + me.b) = isv ? in[i][1] : pack8(v + 8);
+        }
+    }
+    if constexpr (kFour) {
+        if (!keep) return;
+        const float *pc = r.cos + (long long)pos * (r.rot >> 1), *ps = r.sin + (long long)pos * (r.rot >> 1);
+        for (int p = max(p0, first); p < p1; ++p) {
+            const int h = (p - first) * 4 + (lane >> 3);
+            const bool real = h < 2 * r.Hkv, isk = h < r.Hkv;
+            const int hk = !real ? 0 : isk ? h : h - r.Hkv;
+            const long long c = cell(hk);
+            put_four<D>(r, isk ? a.k + t * a.k_stride + hk * D : a.v + t * a.v_stride + hk * D, real, isk && r.wk ? s_w + D : nullptr, isk, pc, ps,
+                        (isk ? a.kp : a.vp) + c * (D / 2), (isk ? a.ks : a.vs) + c * (D / 32), lane);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+// Whether n rows of `pb` bytes, `ps` apart, share a byte with n rows of `qb`
+// bytes, `qs` apart.  Rows of different strides whose ranges meet count as sharing.
+bool rows_meet(const void* p, size_t pb, size_t ps, const void* q, size_t qb, size_t qs, long long n) {
+    if (!pb || !qb || n < 1) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+    if (!(x < y + (n - 1) * qs + qb && y < x + (n - 1) * ps + pb)) return false;
+    if (n == 1 || ps != qs) return true;
+    const size_t off = y >= x ? (y - x) % ps : (ps - (x - y) % ps) % ps;   // q's rows behind p's, within a stride
+    return off < pb || off + qb > ps;
+}
+
+// A strided operand of T tokens.
+struct Rows {
+    const void* p;
+    size_t bytes, stride;    // of a token's row, between tokens
+};
+bool meet(const Rows& a, const Rows& b, long long T) { return rows_meet(a.p, a.bytes, a.stride, b.p, b.bytes, b.stride, T); }
+// An output may be its input's own rows.
+bool same(const Rows& a, const Rows& b, long long T) { return a.p == b.p && a.bytes == b.bytes && (a.stride == b.stride || T == 1); }
+bool meet(const Span& s, const Rows& a, long long T) { return a.bytes && T > 0 && overlap_rows(s, a.p, T, a.bytes, a.stride); }
+
+// What the rotation's own arguments have to be.
+int check_rope(const float* cos, const float* sin, int max_pos, int rot, int d, const int* positions, int seq_len, const void* wq,
+               const void* wk, float eps) {
+    if (!cos || !sin || max_pos < 1 || rot < 1 || rot > d) return FA_ERR_INVALID;
+    if (!positions && seq_len < 1) return FA_ERR_INVALID;
+    if ((wq || wk) && !(eps >= 0.f && isfinite(eps))) return FA_ERR_INVALID;
+    if (rot % 16) return FA_ERR_UNSUPPORTED;
+    if (misaligned(cos, 15) || misaligned(sin, 15) || misaligned(positions, 3) || misaligned(wq, 15) || misaligned(wk, 15)) return FA_ERR_ALIGN;
+    return FA_OK;
+}
+int check_heads(int T, int Hq, int Hkv, int d) {
+    if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv < 1 || d < 1) return FA_ERR_INVALID;
+    if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+    if ((long long)Hq * d > 0x3fffffff || (long long)Hkv * d > 0x3fffffff) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// Warps that share a token, for `passes` passes over its rows: as many as fill the
+// card with sixteen warps an SM, none with less than one pass.
+int parts_for(int T, int passes, int sms) {
+    const long long want = (16LL * sms + T - 1) / T;
+    return (int)(want < 1 ? 1 : want > passes ? passes : want);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out, int64_t q_out_stride,
+               int64_t k_out_stride, int T, int Hq, int Hkv, int d, const float* cos, const float* sin, int max_pos, int rot,
+               int interleaved, const int* positions, int seq_len, const void* q_weight, const void* k_weight, int weights_bf16,
+               float eps, cudaStream_t stream) {
+    int rc = check_heads(T, Hq, Hkv, d);
+    if (rc != FA_OK) return rc;
+    if (T > 0 && ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)))) return FA_ERR_INVALID;
+    rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
+    if (rc != FA_OK) return rc;
+    const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (q_stride < nq || k_stride < nk || q_out_stride < nq || k_out_stride < nk) return FA_ERR_INVALID;
+    if (misaligned(q, 15) || misaligned(k, 15) || misaligned(q_out, 15) || misaligned(k_out, 15) || (q_stride & 7) || (k_stride & 7) ||
+        (q_out_stride & 7) || (k_out_stride & 7))
+        return FA_ERR_ALIGN;
+    if (T == 0) return FA_OK;
+    const size_t w = weights_bf16 ? 2 : 4;
+    const Rows in[] = {{q, (size_t)nq * 2, (size_t)q_stride * 2}, {k, (size_t)nk * 2, (size_t)k_stride * 2}};
+    const Rows out[] = {{q_out, (size_t)nq * 2, (size_t)q_out_stride * 2}, {k_out, (size_t)nk * 2, (size_t)k_out_stride * 2}};
+    const size_t table = (size_t)max_pos * rot * 2;
+    const Span small[] = {{cos, table}, {sin, table}, {positions, positions ? 4 * (size_t)T : 0}, {q_weight, q_weight ? w * d : 0},
+                          {k_weight, k_weight ? w * d : 0}};
+    if (meet(out[0], out[1], T)) return FA_ERR_INVALID;
+    for (int i = 0; i < 2; ++i) {
+        for (const Span& s : small)
+            if (meet(s, out[i], T)) return FA_ERR_INVALID;
+        if (meet(out[i], in[1 - i], T) || (meet(out[i], in[i], T) && !same(out[i], in[i], T))) return FA_ERR_INVALID;
+    }
+    const int sms = fa_num_sms();
+    if (sms < 1) return FA_ERR_LAUNCH;
+    const int per = 512 / d, passes = (Hq + Hkv + per - 1) / per, parts = parts_for(T, passes, sms);
+    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, seq_len, weights_bf16 != 0, eps, passes, parts};
+    const RowsArgs a = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(q_out),
+                        static_cast<__nv_bfloat16*>(k_out), q_stride, k_stride, q_out_stride, k_out_stride};
+    const long long grid = ((long long)T * parts + 7) / 8;
+    auto kern = d == 64 ? qk_rope_kernel<64> : d == 128 ? qk_rope_kernel<128> : qk_rope_kernel<256>;
+    return launch_dependent(kern, (int)grid, 256, 0, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_qk_rope_bwd_workspace_size(int d) {
+    if (d != 64 && d != 128 && d != 256) return 0;
+    const int sms = fa_num_sms();
+    return (size_t)2 * (sms > 0 ? sms : kMaxSMs) * 2 * d * 4;
+}
+
+int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride, int64_t dk_out_stride, const void* q, const void* k,
+                   int64_t q_stride, int64_t k_stride, void* dq, void* dk, float* dq_weight, float* dk_weight, int T, int Hq, int Hkv,
+                   int d, const float* cos, const float* sin, int max_pos, int rot, int interleaved, const int* positions, int seq_len,
+                   const void* q_weight, const void* k_weight, int weights_bf16, float eps, void* workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+    int rc = check_heads(T, Hq, Hkv, d);
+    if (rc != FA_OK) return rc;
+    if (T > 0 && ((Hq > 0 && (!dq_out || !dq || (q_weight && !q))) || (Hkv > 0 && (!dk_out || !dk || (k_weight && !k))))) return FA_ERR_INVALID;
+    if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr)) return FA_ERR_INVALID;
+    rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
+    if (rc != FA_OK) return rc;
+    const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (dq_out_stride < nq || dk_out_stride < nk || (q_weight && q_stride < nq) || (k_weight && k_stride < nk)) return FA_ERR_INVALID;
+    if (misaligned(dq_out, 15) || misaligned(dk_out, 15) || misaligned(dq, 15) || misaligned(dk, 15) || (q_weight && (misaligned(q, 15) || (q_stride & 7))) ||
+        (k_weight && (misaligned(k, 15) || (k_stride & 7))) || misaligned(dq_weight, 15) || misaligned(dk_weight, 15) || (dq_out_stride & 7) || (dk_out_stride & 7))
+        return FA_ERR_ALIGN;
+    const bool norm = q_weight || k_weight;
+    if (norm && (!workspace || misaligned(workspace, 255) || workspace_bytes < fa_qk_rope_bwd_workspace_size(d))) return FA_ERR_WORKSPACE;
+    const size_t w = weights_bf16 ? 2 : 4, table = (size_t)max_pos * rot * 2;
+    const Rows in[] = {{dq_out, (size_t)nq * 2, (size_t)dq_out_stride * 2},
+                       {dk_out, (size_t)nk * 2, (size_t)dk_out_stride * 2},
+                       {q, q_weight ? (size_t)nq * 2 : 0, (size_t)q_stride * 2},
+                       {k, k_weight ? (size_t)nk * 2 : 0, (size_t)k_stride * 2}};
+    const Rows out[] = {{dq, (size_t)nq * 2, (size_t)nq * 2}, {dk, (size_t)nk * 2, (size_t)nk * 2}};
+    const Span small[] = {{cos, table}, {sin, table}, {positions, positions ? 4 * (size_t)T : 0}, {q_weight, q_weight ? w * d : 0},
+                          {k_weight, k_weight ? w * d : 0}};
+    const Span sums[] = {{dq_weight, dq_weight ? 4 * (size_t)d : 0}, {dk_weight, dk_weight ? 4 * (size_t)d : 0},
+                         {workspace, norm ? fa_qk_rope_bwd_workspace_size(d) : 0}};
+    if (meet(out[0], out[1], T)) return FA_ERR_INVALID;
+    for (int i = 0; i < 2; ++i) {
+        for (const Span& s : small)
+            if (meet(s, out[i], T)) return FA_ERR_INVALID;
+        for (const Span& s : sums)
+            if (meet(s, out[i], T)) return FA_ERR_INVALID;
+        // A gradient may take the place of the rows that it is computed from, one for one.
+        for (int j = 0; j < 4; ++j)
+            if (meet(out[i], in[j], T) && !((j & 1) == i && same(out[i], in[j], T))) return FA_ERR_INVALID;
+    }
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(sums[i], sums[j])) return FA_ERR_INVALID;
+        for (const Span& s : small)
+            if (overlap(sums[i], s)) return FA_ERR_INVALID;
+        for (const Rows& x : in)
+            if (meet(sums[i], x, T)) return FA_ERR_INVALID;
+    }
+    if (T == 0 && !norm) return FA_OK;
+    const int sms = fa_num_sms();
+    if (sms < 1) return FA_ERR_LAUNCH;
+    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, seq_len, weights_bf16 != 0, eps, 0, 1};
+    const GradArgs a = {static_cast<const __nv_bfloat16*>(dq_out), static_cast<const __nv_bfloat16*>(dk_out), static_cast<const __nv_bfloat16*>(q),
+                        static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),
+                        dq_out_stride, dk_out_stride, q_stride, k_stride, static_cast<float*>(workspace)};
+    const long long want = ((long long)T + 7) / 8;
+    const int grid = (int)(want < 2LL * sms ? want : 2LL * sms);
+    if (grid > 0) {
+        auto kern = d == 64 ? qk_rope_bwd_kernel<64> : d == 128 ? qk_rope_bwd_kernel<128> : qk_rope_bwd_kernel<256>;
+        if (launch_dependent(kern, grid, 256, 0, stream, r, a) != cudaSuccess) return FA_ERR_LAUNCH;
+    }
+    if (!norm) return FA_OK;
+    return launch_dependent(qk_rope_dw_kernel, 2 * d / 32, 256, 0, stream, a.partial, grid, d, dq_weight, dk_weight) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
+                  int64_t q_out_stride, int T, int Hq, int Hkv, int d, const float* cos, const float* sin, int max_pos, int rot,
+                  int interleaved, const int* positions, const void* q_weight, const void* k_weight, int weights_bf16, float eps,
+                  const int* slots, void* k_pages, void* v_pages, void* k_scales, void* v_scales, int num_pages, int page_size,
+                  cudaStream_t stream) {
+    int rc = check_heads(T, Hq, Hkv, d);
+    if (rc != FA_OK) return rc;
+    if (!k || !v || !slots || !positions || !k_pages || !v_pages || Hkv < 1 || num_pages < 1) return FA_ERR_INVALID;
+    if ((Hq > 0 && (!q || !q_out)) || (k_scales != nullptr) != (v_scales != nullptr)) return FA_ERR_INVALID;
+    rc = check_rope(cos, sin, max_pos, rot, d, positions, 1, q_weight, k_weight, eps);
+    if (rc != FA_OK) return rc;
+    const int lg = page_log2(page_size);
+    if (lg < 0 || (long long)num_pages * page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (q_stride < nq || k_stride < nk || v_stride < nk || q_out_stride < nq) return FA_ERR_INVALID;
+    if (misaligned(q, 15) || misaligned(k, 15) || misaligned(v, 15) || misaligned(q_out, 15) || (q_stride & 7) || (k_stride & 7) ||
+        (v_stride & 7) || (q_out_stride & 7) || misaligned(k_pages, 15) || misaligned(v_pages, 15) || misaligned(k_scales, 15) ||
+        misaligned(v_scales, 15) || misaligned(slots, 3))
+        return FA_ERR_ALIGN;
+    if (T == 0) return FA_OK;
+    const bool four = k_scales != nullptr;
+    const size_t w = weights_bf16 ? 2 : 4, table = (size_t)max_pos * rot * 2, cells = (size_t)num_pages * page_size * Hkv;
+    const size_t pages = cells * (four ? d / 2 : 2 * d), scales = four ? cells * (d / 32) : 0;
+    const Rows in[] = {{q, (size_t)nq * 2, (size_t)q_stride * 2}, {k, (size_t)nk * 2, (size_t)k_stride * 2}, {v, (size_t)nk * 2, (size_t)v_stride * 2}};
+    const Rows out = {q_out, (size_t)nq * 2, (size_t)q_out_stride * 2};
+    const Span small[] = {{cos, table}, {sin, table}, {positions, 4 * (size_t)T}, {slots, 4 * (size_t)T}, {q_weight, q_weight ? w * d : 0},
+                          {k_weight, k_weight ? w * d : 0}};
+    const Span cache[] = {{k_pages, pages}, {v_pages, pages}, {k_scales, scales}, {v_scales, scales}};
+    if ((meet(out, in[0], T) && !same(out, in[0], T)) || meet(out, in[1], T) || meet(out, in[2], T)) return FA_ERR_INVALID;
+    for (const Span& s : small)
+        if (meet(s, out, T)) return FA_ERR_INVALID;
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(cache[i], cache[j])) return FA_ERR_INVALID;
+        for (const Span& s : small)
+            if (overlap(cache[i], s)) return FA_ERR_INVALID;
+        for (const Rows& x : in)
+            if (meet(cache[i], x, T)) return FA_ERR_INVALID;
+        if (meet(cache[i], out, T)) return FA_ERR_INVALID;
+    }
+    const int sms = fa_num_sms();
+    if (sms < 1) return FA_ERR_LAUNCH;
+    const int per = 512 / d;
+    const long long passes = four ? (Hq + per - 1) / per + (2LL * Hkv + 3) / 4 : (Hq + 2LL * Hkv + per - 1) / per;
+    const int parts = parts_for(T, (int)passes, sms);
+    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, 1, weights_bf16 != 0, eps, (int)passes, parts};
+    const PutArgs a = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
+                       static_cast<__nv_bfloat16*>(q_out), q_stride, k_stride, v_stride, q_out_stride, slots, static_cast<uint8_t*>(k_pages),
+                       static_cast<uint8_t*>(v_pages), static_cast<uint8_t*>(k_scales), static_cast<uint8_t*>(v_scales), lg,
+                       (long long)num_pages * page_size};
+    const long long grid = ((long long)T * parts + 7) / 8;
+    auto pick = [&](auto f) { return launch_dependent(f, (int)grid, 256, 0, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; };
+    if (four) return pick(d == 64 ? rope_store_kernel<64, true> : d == 128 ? rope_store_kernel<128, true> : rope_store_kernel<256, true>);
+    return pick(d == 64 ? rope_store_kernel<64, false> : d == 128 ? rope_store_kernel<128, false> : rope_store_kernel<256, false>);
+}
+
+}  // extern "C"

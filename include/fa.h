@@ -444,6 +444,109 @@ int fa_prefix_fwd(const void *q, int64_t q_stride, const void *k_pages, const vo
 size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen);
 
 /*
+ * Between the projections and attention
+ * -------------------------------------
+ * Norms of queries and keys for each head and the rotation by a token's position,
+ * in one pass, with their gradients, and the same on the way into the cache.
+ *
+ *   n(x) = x r w,  r = (mean x^2 + eps)^(-1/2)  over a head's d elements (no
+ *          weights: n(x) = x),
+ *   y = R n(x):  pairs (i, i + rot / 2) of the first rot elements, or (2 i, 2 i +
+ *          1) when interleaved = 1, become (a c - b s, b c + a s) with c, s = cos,
+ *          sin [position][i]; elements from rot on stay.
+ *
+ * - All sums and products are 32 bits wide; a result is rounded to bf16 once.
+ * - cos, sin: float32 [max_pos, rot / 2], 16-byte aligned.  rot is a multiple of
+ *   16 up to d.
+ * - positions: device int32 [T]; NULL (not in fa_rope_store): token t is at t %
+ *   seq_len.  A token whose position is not in [0, max_pos) is left alone:
+ *   nothing of its rows is written, and it adds nothing to a weight's gradient.
+ * - Weights: [d], float32 or (weights_bf16 = 1) bf16, each may be NULL.
+ * - *_stride: elements between tokens (at least heads * d, a multiple of 8), so
+ *   operands may be cut from one projection's output.  Tensors are 16-byte
+ *   aligned.  An output may be its own input's rows (same pointer and stride);
+ *   otherwise no output overlaps another array (rows that interleave with
+ *   another stride count as overlapping).
+ * - Heads of one of the two may be 0: its pointers and stride are then not looked
+ *   at (strides are at least 0).
+ */
+
+/*
+ * q [T, Hq, d], k [T, Hkv, d] -> q_out, k_out, normed and rotated.  One launch, no
+ * workspace.  T == 0 is a no-op.
+ * Errors: FA_ERR_INVALID (null pointer, T or heads < 0, no heads, max_pos, rot
+ * or (without positions) seq_len < 1, rot > d, a stride below heads * d, eps
+ * negative or not finite, arrays that overlap), FA_ERR_UNSUPPORTED (d not 64,
+ * 128 or 256, rot not a multiple of 16, heads * d above 2^30 - 1), FA_ERR_ALIGN,
+ * FA_ERR_LAUNCH.
+ */
+int fa_qk_rope(const void *q, const void *k, int64_t q_stride, int64_t k_stride, void *q_out, void *k_out,
+               int64_t q_out_stride, int64_t k_out_stride, int T, int Hq, int Hkv, int d, const float *cos,
+               const float *sin, int max_pos, int rot, int interleaved, const int *positions, int seq_len,
+               const void *q_weight, const void *k_weight, int weights_bf16, float eps, cudaStream_t stream);
+
+/*
+ * Gradients of fa_qk_rope: with u = R^T dy and t = u w,
+ *
+ *   dx = r (t - x r^2 mean(t x)),   dw = sum over tokens and heads of u x r,
+ *
+ * and dx = u without weights (q, k and their strides are then not looked at).
+ * dq_out, dk_out: gradients of fa_qk_rope's outputs (strided); q, k: its inputs;
+ * dq [T, Hq, d], dk [T, Hkv, d] bf16, contiguous; dq_weight, dk_weight float32
+ * [d], given exactly where there are weights; they are written, not added to (0
+ * when T == 0).  The sums over rows have a fixed order: equal calls on a device
+ * give equal results, bit for bit.
+ * workspace: at least fa_qk_rope_bwd_workspace_size(d) bytes, 256-byte aligned,
+ * no initialisation needed; needed only with weights.  Calls that share one must
+ * not overlap on the GPU (captured graphs that hold the same one included).
+ * Errors: as fa_qk_rope, plus FA_ERR_WORKSPACE.
+ */
+int fa_qk_rope_bwd(const void *dq_out, const void *dk_out, int64_t dq_out_stride, int64_t dk_out_stride,
+                   const void *q, const void *k, int64_t q_stride, int64_t k_stride, void *dq, void *dk,
+                   float *dq_weight, float *dk_weight, int T, int Hq, int Hkv, int d, const float *cos,
+                   const float *sin, int max_pos, int rot, int interleaved, const int *positions, int seq_len,
+                   const void *q_weight, const void *k_weight, int weights_bf16, float eps, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace fa_qk_rope_bwd needs on the current device; 0 for an
+ * unbuilt head dim. */
+size_t fa_qk_rope_bwd_workspace_size(int d);
+
+/*
+ * One step's queries, keys and values on their way into attention: q normed and
+ * rotated into q_out; k normed and rotated, and v as it is, into the cache at
+ * slots[t] (see fa_kv_store: slots outside the cache are skipped, the slots of one
+ * call are distinct).  k_scales and v_scales NULL: bf16 pages; else 4-bit pages
+ * (see "A cache in 4 bits"), which hold the codes of the 32-bit results.
+ * Hq may be 0 (keys and values only).  One launch, no workspace; T == 0 is a
+ * no-op.  The cache's arrays overlap no other one.
+ * Errors: as fa_qk_rope and fa_kv_store, and FA_ERR_INVALID where one of the
+ * scales is given without the other.
+ */
+int fa_rope_store(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                  void *q_out, int64_t q_out_stride, int T, int Hq, int Hkv, int d, const float *cos,
+                  const float *sin, int max_pos, int rot, int interleaved, const int *positions,
+                  const void *q_weight, const void *k_weight, int weights_bf16, float eps, const int *slots,
+                  void *k_pages, void *v_pages, void *k_scales, void *v_scales, int num_pages, int page_size,
+                  cudaStream_t stream);
+
+/*
+ * A cache in 4 bits
+ * -----------------
+ * k_pages and v_pages are bytes [num_pages, Hkv, page_size, d / 2] of e2m1 codes
+ * (sign, then 0 0.5 1 1.5 2 3 4 6), k_scales and v_scales bytes [num_pages, Hkv,
+ * page_size, d / 32]: one scale for 32 elements of a row, 4.25 bits an element.
+ * - A scale byte is bits 14 to 7 of an fp16 (e5m3, no sign): the nearest to a
+ *   sixth of the group's largest magnitude, at most 61440; a group with a NaN or
+ *   an infinity has 0xFC and reads as NaN.  Groups whose largest magnitude is
+ *   below 6 * 2^-18 read as 0, elements above 6 * 61440 as that; scales have
+ *   their full precision from 2^-14 on.
+ * - A code is the nearest to element / scale, ties to the even code.
+ * - Element i of a row is nibble ((i % 32) / 4 * (d / 32) + i / 32) * 4 + i % 4,
+ *   low nibbles first.  Every value is exact in bf16.
+ */
+
+/*
  * Reads (and clears) the library's device status word on the current
  * device after synchronising `stream`: FA_OK, or FA_ERR_TIMEOUT when a
  * kernel's bounded wait gave up (the kernel then skipped its remaining work,
