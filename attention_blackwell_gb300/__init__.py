@@ -12,7 +12,7 @@ import os
 
 import torch
 
-__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "page_plan", "page_pool", "kv_store", "prefix_fwd", "prefix_workspace", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace", "rope_store", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
+__all__ = ["fwd", "set_fwd_kernel", "fwd_pairs_resident", "set_bwd_kernel", "bwd_pairs_resident", "set_schedule_order", "bwd", "bwd_workspace", "page_plan", "page_pool", "kv_store", "prefix_fwd", "prefix_workspace", "qk_rope", "qk_rope_bwd", "qk_rope_bwd_workspace", "rope_store", "kv4_pages", "kv4_expand", "kv4_fwd", "kv4_workspace", "exp2_emu", "selftest_timeout", "set_tuning", "set_debug_counters", "device_status", "num_sms", "FAError", "library_path", "lib"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "lib", "libfa.so")
@@ -87,6 +87,12 @@ def lib():
         L.fa_rope_store.restype = i
         L.fa_rope_store.argtypes = [vp, vp, vp, i64, i64, i64, vp, i64, i, i, i, i, vp, vp, i, i, i, vp, vp, vp, i, f, vp, vp, vp, vp, vp,
                                     i, i, vp]
+        L.fa_kv4_expand.restype = i
+        L.fa_kv4_expand.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp]
+        L.fa_kv4_workspace_size.restype = sz
+        L.fa_kv4_workspace_size.argtypes = [i] * 8
+        L.fa_kv4_fwd.restype = i
+        L.fa_kv4_fwd.argtypes = [vp, i64, vp, vp, vp, vp, vp, vp, i, i, i, i, i, f, i, i, vp, i, vp, vp, i, vp, sz, vp]
         L.fa_exp2_emu.restype = i
         L.fa_exp2_emu.argtypes = [vp, vp, i64, vp]
         L.fa_selftest_timeout.restype = i
@@ -751,6 +757,124 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
     if rc:
         _check(rc, "fa_rope_store")
     return q_out
+
+
+def kv4_pages(num_pages, Hkv, page_size, d=HEAD_DIM, device=None):
+    """(k_pages, k_scales, v_pages, v_scales) of an empty 4-bit cache: uint8
+    [num_pages, Hkv, page_size, d / 2] of codes and [.., d / 32] of scales."""
+    dev = device or "cuda"
+    return tuple(torch.zeros(num_pages, Hkv, page_size, n, dtype=torch.uint8, device=dev) for n in (d // 2, d // 32) * 2)
+
+
+def kv4_expand(k_pages, k_scales, v_pages, v_scales, pages=None, k_out=None, v_out=None, stream=None):
+    """4-bit pages as bf16 pages, exactly.  Returns (k_out, v_out), bf16 [n, Hkv,
+    page_size, d]: page i is page pages[i] of the cache (int32 [n], None: all
+    pages in order; left as it was where there is no such page)."""
+    dev = k_pages.get_device()
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (k_pages, k_scales, v_pages, v_scales, pages, k_out, v_out),
+                          lambda: kv4_expand(k_pages, k_scales, v_pages, v_scales, pages, k_out, v_out))
+    P, Hkv, page, d = _pages4(k_pages, k_scales, v_pages, v_scales)
+    n = P
+    if pages is not None:
+        if pages.dtype is not torch.int32 or not pages.is_contiguous():
+            _need(pages, "pages", torch.int32)
+        n = pages.numel()
+    if k_out is None:
+        k_out = torch.empty((n, Hkv, page, d), dtype=torch.bfloat16, device=k_pages.device)
+    if v_out is None:
+        v_out = torch.empty((n, Hkv, page, d), dtype=torch.bfloat16, device=k_pages.device)
+    if _pages(k_out, v_out) != (n, Hkv, page, d):
+        raise ValueError("k_out and v_out must be [n, Hkv, page_size, d]")
+    _one_device(dev, (k_scales, v_pages, v_scales, pages, k_out, v_out))
+    if n == 0:
+        return k_out, v_out
+    rc = (_lib or lib()).fa_kv4_expand(k_pages.data_ptr(), k_scales.data_ptr(), v_pages.data_ptr(), v_scales.data_ptr(), _at(pages), n, Hkv,
+                                       d, P, page, k_out.data_ptr(), v_out.data_ptr(), _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_kv4_expand")
+    return k_out, v_out
+
+
+def kv4_workspace(B, Hq, Hkv, T, table_width, page_size, max_seqlen=1, d=HEAD_DIM, device=None):
+    """A uint8 CUDA tensor large enough for kv4_fwd of T rows of B requests with at
+    most max_seqlen rows each over block tables of table_width pages."""
+    dev = torch.device(device or "cuda")
+    with torch.cuda.device(dev):
+        n = lib().fa_kv4_workspace_size(int(T), int(B), int(Hq), int(Hkv), int(d), min(int(max_seqlen), max(int(T), 1)), int(table_width),
+                                        int(page_size))
+        if n == 0:
+            raise ValueError("invalid sizes for the workspace")
+        return torch.empty(n, dtype=torch.uint8, device=dev)
+
+
+def kv4_fwd(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_seqlens=None, max_seqlen=None, alpha=None, out=None,
+            lse=None, workspace=None, stream=None):
+    """Attention of new tokens over each request's keys in a 4-bit cache.  Returns
+    (o, lse).
+
+    q [T, Hq, d] bf16 (tokens may be strided), pages and scales as kv4_pages makes
+    them, block_table int32 [B, W], kv_lens int32 [B] (new tokens included) -> o
+    [T, Hq, d] bf16, lse float32 [Hq, T].  Without cu_seqlens (int32 [B+1]) every
+    request has one row; with it max_seqlen bounds a request's rows.  out, lse and
+    the workspace must not overlap q, the pages or the tables.
+    """
+    dev, i32 = q.get_device(), torch.int32
+    if stream is not None or dev < 0 or dev != _current_device():
+        return _elsewhere(stream, (q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_seqlens, out, lse, workspace),
+                          lambda: kv4_fwd(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_seqlens, max_seqlen, alpha,
+                                          out, lse, workspace))
+    P, Hkv, page, d = _pages4(k_pages, k_scales, v_pages, v_scales)
+    qs = _rows(q, "q")
+    if (block_table.dtype is not i32 or kv_lens.dtype is not i32 or not block_table.is_contiguous()
+            or not kv_lens.is_contiguous()):
+        _all_int32(block_table=block_table, kv_lens=kv_lens)
+    T, Hq, dq = q.shape
+    B = kv_lens.numel()
+    if dq != d:
+        raise ValueError("q and the pages must have one head dim")
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError("block_table must be [B, W] with kv_lens' B")
+    if cu_seqlens is not None:
+        if cu_seqlens.dtype is not i32 or not cu_seqlens.is_contiguous():
+            _all_int32(cu_seqlens=cu_seqlens)
+        if cu_seqlens.numel() != B + 1:
+            raise ValueError("cu_seqlens must have B + 1 elements")
+        if max_seqlen is None:
+            raise ValueError("cu_seqlens needs max_seqlen")
+    elif T != B:
+        raise ValueError("without cu_seqlens q must have one row a request")
+    else:
+        max_seqlen = 1
+    max_seqlen = min(int(max_seqlen), max(T, 1))
+    if alpha is None:
+        alpha = 1.0 / (d ** 0.5)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    if (out.dtype is not torch.bfloat16 or lse.dtype is not torch.float32 or not out.is_contiguous()
+            or not lse.is_contiguous()):
+        _need(out, "out", torch.bfloat16)
+        _need(lse, "lse", torch.float32)
+    if out.shape != (T, Hq, d) or lse.shape != (Hq, T):
+        raise ValueError("out must be [T, Hq, d] and lse [Hq, T]")
+    if T == 0:
+        return out, lse
+    if workspace is None:
+        workspace = kv4_workspace(B, Hq, Hkv, T, table[1], page, max_seqlen, d, device=q.device)
+    if not (k_pages.get_device() == k_scales.get_device() == v_pages.get_device() == v_scales.get_device() == block_table.get_device()
+            == kv_lens.get_device() == out.get_device() == lse.get_device() == workspace.get_device() == dev):
+        raise ValueError("all tensors must be on one device")
+    _one_device(dev, (cu_seqlens,))
+    rc = (_lib or lib()).fa_kv4_fwd(q.data_ptr(), qs, k_pages.data_ptr(), k_scales.data_ptr(), v_pages.data_ptr(), v_scales.data_ptr(),
+                                    out.data_ptr(), lse.data_ptr(), T, B, Hq, Hkv, d, alpha, P, page, block_table.data_ptr(), table[1],
+                                    kv_lens.data_ptr(), cu_seqlens.data_ptr() if cu_seqlens is not None else None, max_seqlen,
+                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(), _current_raw_stream(dev))
+    if rc:
+        _check(rc, "fa_kv4_fwd")
+    return out, lse
 
 
 def set_debug_counters(visits=None, inner=None, rescales=None):

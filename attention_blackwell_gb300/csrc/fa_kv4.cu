@@ -1,0 +1,1105 @@
+// fa_kv4.cu -- attention over a paged cache in 4 bits (fa_kv4_fwd) and its pages
+// as bf16 (fa_kv4_expand), sm_103a.
+//
+// Key j has codes c and, for group g of 32 elements, a scale s_jg (fa_kv4.cuh):
+//   x_j = alpha q . k_j = alpha sum_g s_jg (q_g . c_jg),
+//   O = sum_j w_j v_j / sum_j w_j,  v_jg = t_jg c'_jg,  w_j = e^(x_j - M).
+// Nothing is unpacked into memory: codes become fp16 in registers by the hardware's
+// conversion (exact) and go to the tensor core as they are.  A key's scales
+// multiply the sums of its groups' products, a value's scales its weight.
+//
+// fp16 weights.  A weight times a scale spans more than fp16 does, so weights are
+// kept relative to what matters for O: with 2^e_j the power of two over key j's
+// largest value scale,
+//   M = max (x_j + e_j),  p_j = 2^(x_j + e_j - M) in [0, 2^8],  t_jg 2^-e_j in [0, 4),
+// and what falls under fp16's 2^-24 is that much smaller than the largest term of
+// O, whatever the scales.  sum_j w_j = sum_j p_j 2^-e_j stays in 32 bits.  A query is
+// scaled by a power of two into [1, 2) at its largest element before it becomes
+// fp16, which all of bf16's 8 bits fit.  (p is rounded to 11 bits, p t again: less
+// than the 8 bits of a bf16 weight.)
+//
+// Few rows (single tokens, drafts): every warp is a worker with a range of the
+// flat list of (request, key/value head, row block, 64 keys) units, a ring of
+// 16-key parts in shared memory (four bulk copies a part) and its running (M, l, O) in
+// registers.  Keys are the products' M, rows their N: S^T = K Q^T and O^T = V^T
+// P^T, m16n8k16, so eight rows cost half of what they would as M = 16, and P goes
+// from one's accumulator to the other's operand by an 8 x 8 transposition.  An item
+// cut by a range's end leaves (M, l, O) in the workspace, and a second kernel joins
+// the segments in the list's order; one that is not cut is written at once.
+//
+// Many rows (prompts): the requests' pages are expanded to bf16 once, in the
+// workspace, and fa_prefix_fwd's tensor-memory pipeline does the rest: for a prompt
+// the products are all, and 4.25 bits read and 16 written and read an element are
+// little.
+#include <limits.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "../../include/fa.h"
+#include "fa_internal.h"
+#include "fa_kv4.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kTau = 8.0f;            // rescale threshold (log2 units)
+constexpr int kUnit = 64;               // keys a unit
+constexpr int kMaxKeys = 1 << 29;       // of a request
+constexpr int kManyRows = 128;          // rows of a request and key/value head above which pages are expanded
+constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
+
+template <int D, int NT> struct Kv {
+    static constexpr int kRows = 8 * NT;                 // rows of an item
+    static constexpr int kGroups = D / 32;
+    static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;   // an SM
+    static constexpr int kParts = NT == 1 && D <= 128 ? 2 : 1;  // 16-key parts a step
+    // A part in shared memory: K's codes, V's codes, K's scales, V's scales.
+    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales);
+    static constexpr uint32_t kRing = D == 64 ? 10 : D == 128 ? (NT == 1 ? 5 : 8) : NT == 1 ? 5 : 4;
+    static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
+    static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
+    static constexpr uint32_t kWarp = kRing * kPart + kQBytes;
+    static_assert(kPart % 16 == 0 && kWarp % 16 == 0, "copies are 16-byte aligned");
+    static constexpr int kTables = (3 * (kMaxVarlenSeqs + 1) + kMaxVarlenSeqs) * 4;
+    static_assert(kCtas * (8 * kWarp + kTables + 2048) <= 232448, "shared memory plan");
+};
+
+struct KvRow {
+    int c0, n, s, pref, items, pad[3];   // of a row's request: first row, rows (0: none), keys; units and items before it
+};
+struct KvHeader {
+    int per, bad, pad[2];                // units a worker; a request has more rows than max_seqlen
+};
+
+struct KvArgs {
+    const uint8_t *kp, *ks, *vp, *vs;
+    const __nv_bfloat16* q;
+    long long q_stride;
+    const int *table, *kv_lens, *cu;
+    __nv_bfloat16* o;
+    float* lse;
+    DevStatus* status;
+    KvHeader* hdr;
+    KvRow* rows;             // [T]
+    float2* ml;              // segments' rows: maximum, sum
+    float* seg;              // [segment][rows][D]
+    int T, B, Hq, Hkv, G, W, P, ps_log2, max_seqlen;
+    float scale_log2;
+};
+
+struct KvTables {
+    int *pref, *items, *cu, *len;        // [B+1], [B+1], [B+1], [B], in shared memory
+};
+
+// Row blocks of a request with n tokens, units of each of its items: its tiles of
+// keys and one for what an item costs besides.
+__device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (int)(((long long)n * G + rows - 1) / rows); }
+__device__ __forceinline__ int item_units(int s) { return s > 0 ? (s + kUnit - 1) / kUnit + 1 : 0; }
+
+// The keys that row block rb's last row sees.
+__device__ __forceinline__ int keys_seen(int n, int s, int G, int rb, int rows) {
+    const long long last = min((long long)(rb + 1) * rows, (long long)n * G) - 1;
+    return s - n + (int)(last / G) + 1;
+}
+
+// The parts that units [first, last) of an item stand for.
+__device__ __forceinline__ void parts_of(int first, int last, int seen, int& p0, int& p1) {
+    p0 = max(first - 1, 0) * (kUnit / 16);
+    p1 = min(max(last - 1, 0) * (kUnit / 16), seen > 0 ? (seen + 15) >> 4 : 0);
+}
+
+struct KvItem {
+    int b, hk, rb, rows;     // request, key/value head, row block, its rows
+    int c0, n, s;
+    int p0, p1, seen;        // parts [p0, p1), keys its last row sees
+    int seg;
+    bool whole;              // all its parts are here
+};
+
+// A worker's walk over its units.
+template <int ROWS>
+struct KvWalk {
+    int u, end, b, worker;
+    __device__ __forceinline__ void start(const KvArgs& a, const KvTables& t, const KvHeader& h, int w) {
+        worker = w;
+        const int all = h.bad ? 0 : t.pref[a.B];
+        const long long from = (long long)w * h.per;
+        u = from < all ? (int)from : all;
+        end = min(all - u, h.per) + u;
+        int lo = 0, hi = a.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (t.pref[mid + 1] > u) hi = mid; else lo = mid + 1;
+        }
+        b = lo;
+    }
+    __device__ __forceinline__ bool next(const KvArgs& a, const KvTables& t, KvItem& it) {
+        while (u < end) {
+            while (t.pref[b + 1] <= u) ++b;
+            const int n = t.cu[b + 1] - t.cu[b], s = t.len[b], per = item_units(s), nb = row_blocks(n, a.G, ROWS);
+            const int at = u - t.pref[b], i = at / per, first = at - i * per, last = min(per, first + end - u);
+            u += last - first;
+            const int hk = i / nb, rb = i - hk * nb, seen = keys_seen(n, s, a.G, rb, ROWS);
+            int p0, p1;
+            parts_of(first, last, seen, p0, p1);
+            if (p0 >= p1) continue;
+            it.b = b;
+            it.hk = hk;
+            it.rb = rb;
+            it.rows = (int)min((long long)ROWS, (long long)n * a.G - (long long)rb * ROWS);
+            it.c0 = t.cu[b];
+            it.n = n;
+            it.s = s;
+            it.p0 = p0;
+            it.p1 = p1;
+            it.seen = seen;
+            it.seg = t.items[b] + i + worker;      // one of the two rises with every segment
+            it.whole = p0 == 0 && p1 == (seen + 15) >> 4;
+            return true;
+        }
+        return false;
+    }
+};
+
+struct KvShared {
+    uint64_t full[8][10];
+    int2 scan[8];
+    int abort_flag, bad;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// The bounded wait (2 s), by a whole warp: it looks at this CTA's flag alone, which
+// takes the site that gave up, and the CTA reports it as it ends.
+__device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const uint32_t at = smem_u32(bar);
+    bool ok = mbar_try_wait(at, parity);
+    if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!(ok = mbar_try_wait(at, parity))) {
+            if (*abort_flag) break;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// The list's tables, by every thread of the block; offsets by the library's one rule.
+template <int D, int NT>
+__device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables& t, KvShared& sh, int tid) {
+    const int lane = tid & 31, warp = tid >> 5;
+    const long long cap = (long long)a.W << a.ps_log2;
+    bool fine = true;
+    for (int i = tid; i <= a.B; i += 256) {
+        const int c = a.cu ? a.cu[i] : i, before = a.cu && i > 0 ? a.cu[i - 1] : 0;
+        fine = fine && c >= before && c >= 0 && c <= a.T;
+        t.cu[i] = c;
+        if (i < a.B) {
+            const int s = a.kv_lens[i];
+            t.len[i] = s < 0 ? 0 : s > cap ? (int)cap : s;
+        }
+    }
+    if (tid == 0) sh.bad = 0;
+    if (!__syncthreads_and(fine)) {
+        if (tid == 0) {      // rare, and short: at most 1025 offsets
+            int run = 0;
+            for (int i = 0; i <= a.B; ++i) {
+                const int c = t.cu[i];
+                run = max(run, c < 0 ? 0 : c > a.T ? a.T : c);
+                t.cu[i] = run;
+            }
+        }
+        __syncthreads();
+    }
+    int units = 0, items = 0;
+    for (int base = 0; base < a.B; base += 256) {
+        const int i = base + tid;
+        int u = 0, it = 0;
+        if (i < a.B) {
+            const int n = t.cu[i + 1] - t.cu[i];
+            if (n > a.max_seqlen) sh.bad = 1;
+            it = row_blocks(n, a.G, Kv<D, NT>::kRows) * a.Hkv;
+            u = it * item_units(t.len[i]);
+        }
+        const int u_own = u, it_own = it;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, u, o), y = __shfl_up_sync(0xffffffffu, it, o);
+            if (lane >= o) u += x, it += y;
+        }
+        if (base) __syncthreads();
+        if (lane == 31) sh.scan[warp] = make_int2(u, it);
+        __syncthreads();
+        for (int w = 0; w < 8; ++w) {
+            const int2 x = sh.scan[w];
+            if (w < warp) u += x.x, it += x.y;
+        }
+        if (i < a.B) {
+            t.pref[i] = units + u - u_own;
+            t.items[i] = items + it - it_own;
+        }
+        for (int w = 0; w < 8; ++w) units += sh.scan[w].x, items += sh.scan[w].y;
+    }
+    if (tid == 0) {
+        t.pref[a.B] = units;
+        t.items[a.B] = items;
+    }
+    __syncthreads();
+    KvHeader h = {};
+    const int workers = gridDim.x * 8;
+    h.per = units ? (units + workers - 1) / workers : 1;
+    h.bad = sh.bad;
+    if (blockIdx.x == 0 && tid == 0) {
+        *a.hdr = h;
+        if (h.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 111; a.status->block = 0; }
+    }
+    return h;
+}
+
+// ------------------------------------------------------------------ products
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// N words from shared memory at a 4 N-byte boundary.
+template <int N> __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    else if constexpr (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i) : "memory");
+}
+
+// A key's scales, as floats.
+template <int D> __device__ __forceinline__ void key_scales(uint32_t addr, float (&s)[D / 32]) {
+    if constexpr (D == 64) {
+        uint16_t x;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
+        s[0] = scale_f32(x & 0xffu);
+        s[1] = scale_f32(x >> 8);
+    } else {
+        uint32_t w[D / 128];
+        lds(addr, w);
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) s[g] = scale_f32(w[g / 4] >> (g % 4 * 8) & 0xffu);
+    }
+}
+
+// The scales of two adjacent keys, as f16 pairs by group; a key that is not seen has 0.
+template <int D> __device__ __forceinline__ void pair_scales(uint32_t addr, bool first, bool second, uint32_t (&s)[D / 32]) {
+    uint32_t w[D / 64];
+    lds(addr, w);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const uint32_t m = D == 64 ? (first ? 0xffffu : 0u) | (second ? 0xffff0000u : 0u) : (2 * i < D / 64 ? first : second) ? ~0u : 0u;
+        w[i] &= m;
+    }
+#pragma unroll
+    for (int g = 0; g < D / 32; ++g) {
+        const uint32_t x = D == 64 ? __byte_perm(w[0], w[0], g | (2 + g) << 8)
+                                   : __byte_perm(w[g / 4], w[D / 128 + g / 4], g % 4 | (4 + g % 4) << 8);
+        s[g] = x << 7 & 0x7f807f80u;
+    }
+}
+
+// -------------------------------------------------------------------- kernel
+
+template <int D, int NT>
+__global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs a) {
+    using K = Kv<D, NT>;
+    constexpr int kG = K::kGroups, kParts = K::kParts;
+    constexpr uint32_t kRing = K::kRing;
+    extern __shared__ __align__(16) uint8_t dsmem[];
+    __shared__ KvShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    KvTables t;
+    t.pref = reinterpret_cast<int*>(dsmem + 8 * K::kWarp);
+    t.items = t.pref + a.B + 1;
+    t.cu = t.items + a.B + 1;
+    t.len = t.cu + a.B + 1;
+    if (tid < 8 * (int)kRing) {
+        mbar_init(&sh.full[tid / kRing][tid % kRing], 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) sh.abort_flag = 0;
+    grid_launch_next();
+    grid_wait();
+    const KvHeader hdr = build_tables<D, NT>(a, t, sh, tid);
+
+    // What the joining kernel needs to know of each row.
+    for (int i = blockIdx.x * 256 + tid; i < a.T; i += gridDim.x * 256) {
+        KvRow row = {};
+        if (i >= t.cu[0] && i < t.cu[a.B]) {
+            int lo = 0;
+            for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
+                const int mid = (lo + hi) >> 1;
+                if (t.cu[mid] <= i) lo = mid; else hi = mid;
+            }
+            row.c0 = t.cu[lo];
+            row.n = t.cu[lo + 1] - row.c0;
+            row.s = t.len[lo];
+            row.pref = t.pref[lo];
+            row.items = t.items[lo];
+        }
+        a.rows[i] = row;
+    }
+
+    uint64_t* full = sh.full[warp];
+    const uint32_t ring = smem_u32(dsmem) + warp * K::kWarp, q_smem = ring + kRing * K::kPart;
+    const int worker = blockIdx.x * 8 + warp;
+
+    // The copies: a walk of their own, ahead of the work by what the ring holds.
+    KvWalk<K::kRows> ahead;
+    KvItem to = {};
+    ahead.start(a, t, hdr, worker);
+    bool more = ahead.next(a, t, to);
+    int part = to.p0, win = -1, win_next = -1;       // next part; pages of its 32 parts, one a lane, and of the next 32
+    uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a slot: its page exists
+    auto pages = [&](int p) -> int {                 // of parts p .. p + 31
+        if (p + lane >= to.p1) return -1;
+        const int x = a.table[(long long)to.b * a.W + ((p + lane) * 16 >> a.ps_log2)];
+        return x >= 0 && x < a.P ? x : -1;
+    };
+    if (more) {
+        win = pages(part);
+        win_next = pages(part + 32);
+    }
+    auto copy = [&]() {
+        if (!more) return;
+        const int page = __shfl_sync(0xffffffffu, win, (part - to.p0) & 31);
+        uint64_t* bar = &full[filled];
+        __syncwarp();                                // every lane has read what the slot held
+        if (page >= 0) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, K::kPart);
+            __syncwarp();
+            if (lane < 4) {                          // K's codes, V's codes, K's scales, V's scales
+                const long long row = (((long long)page * a.Hkv + to.hk) << a.ps_log2) + (part * 16 & ((1 << a.ps_log2) - 1));
+                const uint8_t* base = lane == 0 ? a.kp : lane == 1 ? a.vp : lane == 2 ? a.ks : a.vs;
+                const uint32_t dst = ring + filled * K::kPart + (lane < 2 ? lane * K::kCodes : 2 * K::kCodes + (lane - 2) * K::kScales);
+                bulk_load(dst, base + row * (lane < 2 ? D / 2 : D / 32), lane < 2 ? K::kCodes : K::kScales, bar);
+            }
+        } else if (lane == 0) {
+            mbar_arrive(bar);
+        }
+        live = (live & ~(1u << filled)) | (page >= 0 ? 1u << filled : 0u);
+        filled = filled + 1 == kRing ? 0 : filled + 1;
+        ++issued;
+        if (++part == to.p1) {
+            more = ahead.next(a, t, to);
+            if (more) {
+                part = to.p0;
+                win = pages(part);
+                win_next = pages(part + 32);
+            }
+        } else if (((part - to.p0) & 31) == 0) {
+            win = win_next;
+            win_next = pages(part + 32);
+        }
+    };
+    for (uint32_t i = 0; i < kRing; ++i) copy();
+
+    KvWalk<K::kRows> walk;
+    KvItem it;
+    walk.start(a, t, hdr, worker);
+    uint32_t read = 0, slot = 0, phase = 0;
+    bool ok = true;
+    while (ok && walk.next(a, t, it)) {
+        // Q as B operands: lane (r, c) has row r's elements 32 g + 8 c to + 7, which
+        // are what it reads of a key.
+        uint32_t qf[K::kQRegs ? NT : 1][K::kQRegs ? kG : 1][4];
+        float f[NT][2];                              // what a row's sums are multiplied by, rows 2c and 2c + 1
+        int lim[NT][2];                              // keys they see
+        float m[NT][2], l[NT][2], o[kG][2][NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int x = nt * 8 + r;
+            const long long row = (long long)it.rb * K::kRows + x;
+            const int tok = (int)(row / a.G), h = (int)(row - (long long)tok * a.G);
+            uint4 in[kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                in[g] = make_uint4(0, 0, 0, 0);
+                if (x < it.rows)
+                    in[g] = *reinterpret_cast<const uint4*>(a.q + (long long)(it.c0 + tok) * a.q_stride + (it.hk * a.G + h) * D + 32 * g + 8 * c);
+            }
+            float most = 0.f;
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const uint32_t w[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);      // exponent field: 2^(e - 127)
+            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = a.scale_log2 * __uint_as_float((uint32_t)e << 23);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+                const uint32_t w[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
+                uint32_t q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
+                if constexpr (K::kQRegs) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[nt][g][i] = q[i];
+                } else {
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + ((nt * kG + g) * 32 + lane) * 16), "r"(q[0]),
+                                 "r"(q[1]), "r"(q[2]), "r"(q[3]) : "memory");
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                f[nt][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
+                const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
+                lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
+                m[nt][i] = -INFINITY;
+                l[nt][i] = 0.f;
+            }
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[g][0][nt][i] = o[g][1][nt][i] = 0.f;
+        }
+        const int lim_min = it.s - it.n + (int)((long long)it.rb * K::kRows / a.G) + 1;
+
+        for (int p = it.p0; p < it.p1; p += kParts) {
+            const int k0 = p * 16, parts = min(kParts, it.p1 - p);
+            uint32_t here = 0;                       // parts of this step with a page
+            float z[kParts][NT][4], back[kParts][2]; // scores + e, 2^-e
+            uint32_t vsc[kParts][2][kG];             // V's scales over 2^e: keys 2c, 2c + 1 and eight further
+#pragma unroll
+            for (int kt = 0; kt < kParts; ++kt) {
+                const uint32_t sl = slot + kt < kRing ? slot + kt : slot + kt - kRing;
+                const uint32_t at = ring + sl * K::kPart;
+                if (kt < parts) {
+                    const uint32_t ph = slot + kt < kRing ? phase : phase ^ 1;
+                    if (!(ok = kv_wait(&full[sl], ph, &sh.abort_flag))) break;
+                    here |= (live >> sl & 1u) << kt;
+                }
+                // Keys' codes: eight adjacent elements of every group, for keys r and r + 8.
+                uint32_t kw[2][kG];
+                float ksc[2][kG];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    lds(at + (r + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
+                    key_scales<D>(at + 2 * K::kCodes + (r + 8 * i) * (D / 32), ksc[i]);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = 0.f;
+#pragma unroll
+                for (int j = 0; j < kG / 2; ++j) {
+                    uint32_t x[2][2][4];             // [step of the group][key r, r + 8][group 2j: two pairs, group 2j + 1: two]
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        codes_f16(kw[i][j], x[0][i][0], x[0][i][1], x[0][i][2], x[0][i][3]);
+                        codes_f16(kw[i][kG / 2 + j], x[1][i][0], x[1][i][1], x[1][i][2], x[1][i][3]);
+                    }
+#pragma unroll
+                    for (int gg = 0; gg < 2; ++gg) {
+                        const int g = 2 * j + gg;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            uint32_t q[4];
+                            if constexpr (K::kQRegs) {
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) q[i] = qf[nt][g][i];
+                            } else {
+                                lds(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
+                            }
+                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                            mma_f16(acc, x[0][0][2 * gg], x[0][1][2 * gg], x[0][0][2 * gg + 1], x[0][1][2 * gg + 1], q[0], q[1]);
+                            mma_f16(acc, x[1][0][2 * gg], x[1][1][2 * gg], x[1][0][2 * gg + 1], x[1][1][2 * gg + 1], q[2], q[3]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(ksc[i >> 1][g], acc[i], z[kt][nt][i]);
+                        }
+                    }
+                }
+                // V's scales and their exponents.
+                const bool on = here >> kt & 1u;
+                const int key = k0 + kt * 16 + 2 * c;
+                uint32_t ex[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    pair_scales<D>(at + 2 * K::kCodes + K::kScales + (2 * c + 8 * i) * (D / 32), on && key + 8 * i < it.seen, on && key + 8 * i + 1 < it.seen, vsc[kt][i]);
+                    uint32_t e = 0x04000400u;        // 2^-14, fp16's smallest normal number, to 2^15
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) e = hmax2(e, vsc[kt][i][g]);
+                    ex[i] = hmin2(e, 0x78007800u) & 0x7c007c00u;
+                    const uint32_t down = 0x7c007c00u - ex[i];      // 2^-e, e = exponent field - 16
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) vsc[kt][i][g] = hmul2(vsc[kt][i][g], down);
+                }
+                float e[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {        // of keys r and r + 8: from lane r / 2
+                    const uint32_t x = __shfl_sync(0xffffffffu, ex[i], r >> 1) >> (10 + 16 * (r & 1)) & 31u;
+                    e[i] = __uint_as_float(0x4b000000u | x) - 8388624.f;
+                    back[kt][i] = __uint_as_float((143u - x) << 23);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], f[nt][i & 1], e[i >> 1]);
+            }
+            if (!ok) break;
+            if (k0 + kParts * 16 > lim_min || here != (1u << kParts) - 1u) {
+#pragma unroll
+                for (int kt = 0; kt < kParts; ++kt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(here >> kt & 1u) || k0 + kt * 16 + r + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
+            }
+            // The running maximum of each row; O and l follow it when it grows by more
+            // than kTau.
+            float mn[NT][2];
+            bool jump = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
+#pragma unroll
+                    for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    mn[nt][i] = fmaxf(m[nt][i], x);
+                    jump |= m[nt][i] == -INFINITY ? mn[nt][i] != -INFINITY : mn[nt][i] - m[nt][i] > kTau;
+                }
+            if (__any_sync(0xffffffffu, jump)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float fac = m[nt][i] == -INFINITY ? 0.f : ex2_mufu(m[nt][i] - mn[nt][i]);
+                        l[nt][i] *= fac;
+                        m[nt][i] = mn[nt][i];
+#pragma unroll
+                        for (int g = 0; g < kG; ++g)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                o[g][h][nt][i] *= fac;
+                                o[g][h][nt][2 + i] *= fac;
+                            }
+                    }
+            }
+#pragma unroll
+            for (int kt = 0; kt < kParts; ++kt) {
+                const uint32_t sl = slot + kt < kRing ? slot + kt : slot + kt - kRing;
+                const uint32_t at = ring + sl * K::kPart + K::kCodes;
+                uint32_t pt[NT][2];                  // weights as B operands: row r, keys 2c, 2c + 1 and eight further
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float use = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
+                        w[i] = ex2_mufu(z[kt][nt][i] - use);
+                        l[nt][i & 1] = fmaf(w[i], back[kt][i >> 1], l[nt][i & 1]);
+                    }
+                    pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
+                    pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
+                }
+                // Values' codes: four elements of every group, for the four keys.
+                uint32_t vw[2][2][kG / 2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) lds(at + (2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
+#pragma unroll
+                for (int j = 0; j < kG / 2; ++j) {
+                    uint32_t x[2][2][4];             // [keys 2c .., keys 2c + 8 ..][codes 0 and 2, 1 and 3][group 2j: two, group 2j + 1: two]
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t u0 = vw[i][0][j], u1 = vw[i][1][j];
+                        const uint32_t even = (u0 & 0x0f0f0f0fu) | (u1 << 4 & 0xf0f0f0f0u), odd = (u0 >> 4 & 0x0f0f0f0fu) | (u1 & 0xf0f0f0f0u);
+                        codes_f16(even, x[i][0][0], x[i][0][1], x[i][0][2], x[i][0][3]);
+                        codes_f16(odd, x[i][1][0], x[i][1][1], x[i][1][2], x[i][1][3]);
+                    }
+#pragma unroll
+                    for (int gg = 0; gg < 2; ++gg) {
+                        const int g = 2 * j + gg;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t b0 = hmul2(pt[nt][0], vsc[kt][0][g]), b1 = hmul2(pt[nt][1], vsc[kt][1][g]);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                mma_f16(o[g][h][nt], x[0][0][2 * gg + h], x[0][1][2 * gg + h], x[1][0][2 * gg + h], x[1][1][2 * gg + h], b0, b1);
+                        }
+                    }
+                }
+            }
+            for (int i = 0; i < parts; ++i) {
+                ++read;
+                if (++slot == kRing) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                copy();
+            }
+        }
+        if (!ok) break;
+        // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
+                l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+                const int x = nt * 8 + 2 * c + i;
+                if (x >= it.rows) continue;
+                if (it.whole) {
+                    const long long row = (long long)it.rb * K::kRows + x;
+                    const int tok = (int)(row / a.G), h = it.hk * a.G + (int)(row - (long long)tok * a.G);
+                    const float inv = l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i];
+                    const long long tt = it.c0 + tok;
+                    __nv_bfloat16* dst = a.o + (tt * a.Hq + h) * D + 4 * r;
+#pragma unroll
+                    for (int g = 0; g < kG; ++g)
+                        *reinterpret_cast<uint2*>(dst + 32 * g) = make_uint2(pack_bf16x2(o[g][0][nt][i] * inv, o[g][0][nt][2 + i] * inv),
+                                                                             pack_bf16x2(o[g][1][nt][i] * inv, o[g][1][nt][2 + i] * inv));
+                    if (r == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
+                } else {
+                    const long long row = (long long)it.seg * K::kRows + x;
+                    float* dst = a.seg + row * D + 4 * r;
+#pragma unroll
+                    for (int g = 0; g < kG; ++g)
+                        *reinterpret_cast<float4*>(dst + 32 * g) = make_float4(o[g][0][nt][i], o[g][0][nt][2 + i], o[g][1][nt][i], o[g][1][nt][2 + i]);
+                    if (r == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
+                }
+            }
+    }
+    // Every copy lands before the block ends (after a wait that gave up, too).
+    const uint64_t t0 = globaltimer_ns();
+    for (; read < issued; ++read) {
+        while (!mbar_try_wait(smem_u32(&full[slot]), phase) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+        if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    __syncwarp();
+    if (!ok && lane == 0 && atomicCAS(&a.status->code, 0, kStatusTimeout) == 0) {
+        a.status->where = 112;
+        a.status->block = blockIdx.x;
+    }
+}
+
+// Joins the segments of a row (of one head) that a range's end has cut; writes the
+// rows without a key.  A warp a row, or with few rows a block of eight.
+template <int D, bool kSplit>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_item) {
+    constexpr int E = D / 32;
+    __shared__ float s_o[kSplit ? 8 : 1][kSplit ? D : 1];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long w = kSplit ? blockIdx.x : blockIdx.x * 8LL + warp;
+    if (w >= (long long)a.T * a.Hq) return;
+    const int t = (int)(w / a.Hq), h = (int)(w - (long long)t * a.Hq), hk = h / a.G;
+    grid_wait();
+    const KvHeader hdr = *a.hdr;
+    const KvRow q = a.rows[t];
+    if (hdr.bad || q.n == 0) return;
+    const long long row = (long long)(t - q.c0) * a.G + h - hk * a.G;
+    const int rb = (int)(row / rows_item), in = (int)(row - (long long)rb * rows_item), nb = row_blocks(q.n, a.G, rows_item);
+    const int units = item_units(q.s), item = hk * nb + rb, u0 = q.pref + item * units, seen = keys_seen(q.n, q.s, a.G, rb, rows_item);
+    const int first = u0 / hdr.per, all = units > 0 && seen > 0 ? (u0 + units - 1) / hdr.per - first + 1 : 0;
+    // Row in the k-th worker's segment, -1: it has none.
+    auto place = [&](int k) -> long long {
+        if (k >= all) return -1;
+        const int from = max(0, (first + k) * hdr.per - u0), to = min(units, (first + k + 1) * hdr.per - u0);
+        int p0, p1;
+        parts_of(from, to, seen, p0, p1);
+        if (p0 >= p1) return -1;
+        return p0 == 0 && p1 == (seen + 15) >> 4 ? -2 : (long long)(q.items + item + first + k) * rows_item + in;
+    };
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float2 ml;
+    long long at;
+    auto load = [&](int k) {
+        at = place(k);
+        ml = at >= 0 ? a.ml[at] : make_float2(-INFINITY, 0.f);
+    };
+    for (int k0 = all > 0 ? (all - 1) / 32 * 32 : 0; k0 >= 0; k0 -= 32) {
+        load(k0 + lane);
+        if (__any_sync(0xffffffffu, at == -2)) return;       // written by its one worker
+        M = fmaxf(M, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int k0 = 0; k0 < all; k0 += 32) {
+        if (k0) load(k0 + lane);
+        const float f = ml.y == 0.f ? 0.f : ex2_mufu(ml.x - M);   // a sum of 0: no key seen; a NaN stays one
+        L += f * ml.y;
+        const int cnt = min(32, all - k0);
+#pragma unroll 4
+        for (int k = kSplit ? warp : 0; k < cnt; k += kSplit ? 8 : 1) {
+            const long long from = __shfl_sync(0xffffffffu, at, k);
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            if (from < 0 || fk == 0.f) continue;
+            const float* src = a.seg + from * D + lane * E;
+            float v[E];
+            if constexpr (E == 2) {
+                const float2 x = *reinterpret_cast<const float2*>(src);
+                v[0] = x.x, v[1] = x.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    const float4 x = *reinterpret_cast<const float4*>(src + e);
+                    v[e] = x.x, v[e + 1] = x.y, v[e + 2] = x.z, v[e + 3] = x.w;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, v[e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if constexpr (kSplit) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
+        __syncthreads();
+        if (warp) return;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            for (int y = 1; y < 8; ++y) acc[e] += s_o[y][lane * E + e];
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    uint32_t out[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + ((long long)t * a.Hq + h) * D) + lane * (E / 2);
+    if constexpr (E == 2) *dst = out[0];
+    else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (lane == 0) a.lse[(long long)h * a.T + t] = L == 0.f ? -INFINITY : (M + __log2f(L)) * 0.69314718055994531f;
+}
+
+// -------------------------------------------------------------------- expand
+
+struct ExpandArgs {
+    const uint8_t *kp, *ks, *vp, *vs;
+    __nv_bfloat16 *ko, *vo;
+    const int* list;         // [n] pages, null: page i
+    const int* lens;         // [n / W] (null: all): entries past a request's keys are passed over
+    int* table;              // [n] or null: takes i where page i was written, else -1
+    int n, W, Hkv, P, ps_log2;
+};
+
+// A warp takes 16 rows of one page, head and of K or V: four at a time, eight lanes
+// a row, whose four loads are made before the first is used.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_expand_kernel(const ExpandArgs a) {
+    constexpr int kG = D / 32;
+    grid_launch_next();
+    grid_wait();
+    const int lane = threadIdx.x & 31, l = lane & 7, ps = 1 << a.ps_log2;
+    const long long all = ((long long)a.n * a.Hkv) << (a.ps_log2 - 3);
+    for (long long w = blockIdx.x * 8LL + (threadIdx.x >> 5); w < all; w += gridDim.x * 8LL) {
+        const bool v = w & 1;
+        const int quarter = (int)(w >> 1) & ((ps >> 4) - 1);
+        const long long x = w >> (a.ps_log2 - 3);
+        const int i = (int)(x / a.Hkv), h = (int)(x - (long long)i * a.Hkv);
+        const bool skip = a.lens && ((long long)(i % a.W) << a.ps_log2) >= a.lens[i / a.W];
+        const int page = skip ? -1 : a.list ? a.list[i] : i;
+        const bool real = page >= 0 && page < a.P;
+        if (a.table && !v && h == 0 && quarter == 0 && lane == 0) a.table[i] = real ? i : -1;
+        if (!real) continue;
+        const long long from = (((long long)page * a.Hkv + h) << a.ps_log2) + quarter * 16 + (lane >> 3);
+        const long long to = (((long long)i * a.Hkv + h) << a.ps_log2) + quarter * 16 + (lane >> 3);
+        const uint8_t *codes = (v ? a.vp : a.kp) + from * (D / 2) + l * (D / 16), *scales = (v ? a.vs : a.ks) + from * kG;
+        __nv_bfloat16* out = (v ? a.vo : a.ko) + to * D + 4 * l;
+        uint32_t c[4][kG / 2], s[4][D == 256 ? 2 : 1];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const uint8_t *pc = codes + y * 4 * (D / 2), *pss = scales + y * 4 * kG;
+            if constexpr (D == 64) {
+                c[y][0] = *reinterpret_cast<const uint32_t*>(pc);
+                s[y][0] = *reinterpret_cast<const uint16_t*>(pss);
+            } else if constexpr (D == 128) {
+                const uint2 u = *reinterpret_cast<const uint2*>(pc);
+                c[y][0] = u.x, c[y][1] = u.y;
+                s[y][0] = *reinterpret_cast<const uint32_t*>(pss);
+            } else {
+                const uint4 u = *reinterpret_cast<const uint4*>(pc);
+                c[y][0] = u.x, c[y][1] = u.y, c[y][2] = u.z, c[y][3] = u.w;
+                const uint2 z = *reinterpret_cast<const uint2*>(pss);
+                s[y][0] = z.x, s[y][1] = z.y;
+            }
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int j = 0; j < kG / 2; ++j) {
+                uint32_t p[4];
+                codes_f16(c[y][j], p[0], p[1], p[2], p[3]);
+#pragma unroll
+                for (int gg = 0; gg < 2; ++gg) {
+                    const int g = 2 * j + gg;
+                    const float sc = scale_f32(s[y][g / 4] >> (g % 4 * 8) & 0xffu);
+                    const float2 lo = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * gg])), hi = __half22float2(*reinterpret_cast<const __half2*>(&p[2 * gg + 1]));
+                    *reinterpret_cast<uint2*>(out + (long long)y * 4 * D + 32 * g) = make_uint2(pack_bf16x2(lo.x * sc, lo.y * sc), pack_bf16x2(hi.x * sc, hi.y * sc));
+                }
+            }
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+bool misaligned(const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; }
+
+int launch_expand(const ExpandArgs& a, int d, int sms, cudaStream_t stream) {
+    const long long all = ((long long)a.n * a.Hkv) << (a.ps_log2 - 3), most = 8LL * sms;
+    const long long blocks = (all + 7) / 8;
+    auto kern = d == 64 ? kv4_expand_kernel<64> : d == 128 ? kv4_expand_kernel<128> : kv4_expand_kernel<256>;
+    return launch_dependent(kern, (int)(blocks < most ? blocks : most), 256, 0, stream, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// Rows of an item of few rows: eight a product's N.
+int item_rows(int d, long long rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
+
+// Workspace of few rows: header, what the rows are, the segments' (m, l) and O.  The
+// largest of the three item sizes, so that a workspace for long drafts serves
+// single tokens.
+struct KvLayout {
+    size_t rows, ml, seg, total;
+};
+KvLayout kv_layout(int T, int B, int Hkv, int G, int d, int sms) {
+    size_t most = 0;
+    for (int rows = 8; rows <= (d == 256 ? 16 : 32); rows *= 2) {
+        const size_t items = (size_t)Hkv * ((long long)T * G / rows + (T < B ? T : B)), workers = (size_t)sms * 8 * (rows == 8 && d <= 128 ? 2 : 1);
+        const size_t n = (items + workers) * rows;
+        most = n > most ? n : most;
+    }
+    KvLayout w;
+    w.rows = 256;
+    w.ml = align256(w.rows + (size_t)T * sizeof(KvRow));
+    w.seg = align256(w.ml + most * 8);
+    w.total = align256(w.seg + most * d * 4);
+    return w;
+}
+
+// Workspace of many rows: the expanded pages, the table that names them, and
+// fa_prefix_fwd's; 0: this call's pages are too many.
+struct ManyLayout {
+    size_t k, v, table, prefix, total;
+};
+ManyLayout many_layout(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int W, int page) {
+    ManyLayout w = {};
+    const size_t one = (size_t)B * W * page * Hkv * d * 2;
+    if (max_seqlen * (long long)(Hq / Hkv) <= kManyRows || one > kExpandMost / 2 || (long long)B * W * page * Hkv > 0x7fffffffLL) return w;
+    w.v = align256(one);
+    w.table = w.v + align256(one);
+    w.prefix = align256(w.table + 4 * (size_t)B * W);
+    w.total = w.prefix + fa_prefix_workspace_size(T, B, Hq, Hkv, d, max_seqlen);
+    return w;
+}
+
+template <int D, int NT>
+int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
+    using K = Kv<D, NT>;
+    auto kern = kv4_kernel<D, NT>;
+    const size_t smem = 8 * K::kWarp + (3 * (a.B + 1) + a.B) * 4;
+    static std::atomic<uint64_t> prepared{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
+    if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(8 * K::kWarp + K::kTables)) != cudaSuccess) return FA_ERR_LAUNCH;
+        prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
+    const long long items = (long long)a.Hkv * ((long long)a.T * a.G / K::kRows + (a.T < a.B ? a.T : a.B));
+    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + 7) / 8;
+    const int most = sms * K::kCtas, grid = 2 * need < most ? (int)(2 * need) : most;
+    if (launch_dependent(kern, grid, 256, smem, stream, a) != cudaSuccess) return FA_ERR_LAUNCH;
+    const long long rows = (long long)a.T * a.Hq;
+    cudaError_t e;
+    if (rows <= 8LL * sms) e = launch_dependent(kv4_join_kernel<D, true>, (int)rows, 256, 0, stream, a, K::kRows);
+    else e = launch_dependent(kv4_join_kernel<D, false>, (int)((rows + 7) / 8), 256, 0, stream, a, K::kRows);
+    return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int check_pages(int Hkv, int d, int num_pages, int page_size) {
+    if (Hkv < 1 || d < 1 || num_pages < 1) return FA_ERR_INVALID;
+    if ((d != 64 && d != 128 && d != 256) || page_log2(page_size) < 0) return FA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+int fa_kv4_expand(const void* k_pages, const void* k_scales, const void* v_pages, const void* v_scales, const int* pages, int n,
+                  int Hkv, int d, int num_pages, int page_size, void* k_out, void* v_out, cudaStream_t stream) {
+    if (!k_pages || !k_scales || !v_pages || !v_scales || n < 0 || (n > 0 && (!k_out || !v_out))) return FA_ERR_INVALID;
+    const int rc = check_pages(Hkv, d, num_pages, page_size);
+    if (rc != FA_OK) return rc;
+    if (!pages && n > num_pages) return FA_ERR_INVALID;
+    if ((long long)n * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    if (misaligned(k_pages, 15) || misaligned(v_pages, 15) || misaligned(k_scales, 15) || misaligned(v_scales, 15) || misaligned(k_out, 15) ||
+        misaligned(v_out, 15) || misaligned(pages, 3))
+        return FA_ERR_ALIGN;
+    if (n == 0) return FA_OK;
+    const size_t cells = (size_t)num_pages * Hkv * page_size, out = (size_t)n * Hkv * page_size * d * 2;
+    const Span in[] = {{k_pages, cells * (d / 2)}, {v_pages, cells * (d / 2)}, {k_scales, cells * (d / 32)}, {v_scales, cells * (d / 32)},
+                       {pages, pages ? 4 * (size_t)n : 0}};
+    if (overlap({k_out, out}, {v_out, out})) return FA_ERR_INVALID;
+    for (const Span& s : in)
+        if (overlap({k_out, out}, s) || overlap({v_out, out}, s)) return FA_ERR_INVALID;
+    const int sms = fa_num_sms();
+    if (sms < 1) return FA_ERR_LAUNCH;
+    const ExpandArgs a = {static_cast<const uint8_t*>(k_pages), static_cast<const uint8_t*>(k_scales), static_cast<const uint8_t*>(v_pages),
+                          static_cast<const uint8_t*>(v_scales), static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out),
+                          pages, nullptr, nullptr, n, 1, Hkv, num_pages, page_log2(page_size)};
+    return launch_expand(a, d, sms, stream);
+}
+
+size_t fa_kv4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int table_width, int page_size) {
+    if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > 128 || max_seqlen < 1 || table_width < 1 ||
+        (d != 64 && d != 128 && d != 256) || page_log2(page_size) < 0 || (long long)Hq * T > 0x7fffffffLL ||
+        (long long)B * table_width > 0x7fffffffLL || (long long)table_width * page_size > kMaxKeys)
+        return 0;
+    const int sms = fa_num_sms();
+    if (max_seqlen > T) max_seqlen = T > 1 ? T : 1;
+    const size_t few = kv_layout(T, B, Hkv, Hq / Hkv, d, sms > 0 ? sms : kMaxSMs).total;
+    const size_t many = many_layout(T, B, Hq, Hkv, d, max_seqlen, table_width, page_size).total;
+    return few > many ? few : many;
+}
+
+int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void* k_scales, const void* v_pages, const void* v_scales,
+               void* o, float* lse, int T, int B, int Hq, int Hkv, int d, float alpha, int num_pages, int page_size,
+               const int* block_table, int table_width, const int* kv_lens, const int* cu_seqlens, int max_seqlen, void* workspace,
+               size_t workspace_bytes, cudaStream_t stream) {
+    if (!q || !k_pages || !k_scales || !v_pages || !v_scales || !o || !lse || !block_table || !kv_lens) return FA_ERR_INVALID;
+    if (T < 0 || B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || num_pages < 1 || table_width < 1 || max_seqlen < 1) return FA_ERR_INVALID;
+    if (!(alpha > 0.0f) || !isfinite(alpha)) return FA_ERR_INVALID;
+    if (!cu_seqlens && T != B) return FA_ERR_INVALID;
+    if (q_stride < (long long)Hq * d) return FA_ERR_INVALID;
+    const int rc = check_pages(Hkv, d, num_pages, page_size);
+    if (rc != FA_OK) return rc;
+    if (Hq / Hkv > 128 || B > kMaxVarlenSeqs) return FA_ERR_UNSUPPORTED;
+    const long long lim = 0x7fffffffLL;
+    if ((long long)Hq * T > lim || (long long)B * table_width > lim || (long long)table_width * page_size > kMaxKeys) return FA_ERR_UNSUPPORTED;
+    if (misaligned(q, 15) || misaligned(k_pages, 15) || misaligned(v_pages, 15) || misaligned(k_scales, 15) || misaligned(v_scales, 15) ||
+        misaligned(o, 15) || misaligned(lse, 15) || misaligned(block_table, 3) || misaligned(kv_lens, 3) || misaligned(cu_seqlens, 3) || (q_stride & 7))
+        return FA_ERR_ALIGN;
+    if (T == 0) return FA_OK;
+    const int G = Hq / Hkv;
+    if (max_seqlen > T) max_seqlen = T;
+    // The list of units at its longest fits 32 bits, a worker's share past it too.
+    const long long tiles = ((long long)table_width * page_size + kUnit - 1) / kUnit + 1;
+    const long long items = (long long)Hkv * ((long long)T * G / 8 + (T < B ? T : B));
+    if (items * (tiles + 2) > 1 << 30) return FA_ERR_UNSUPPORTED;
+    const size_t row = (size_t)Hq * d * 2, cells = (size_t)num_pages * Hkv * page_size;
+    const Span inputs[] = {{k_pages, cells * (d / 2)}, {v_pages, cells * (d / 2)}, {k_scales, cells * (d / 32)}, {v_scales, cells * (d / 32)},
+                           {block_table, 4 * (size_t)B * table_width}, {kv_lens, 4 * (size_t)B}, {cu_seqlens, cu_seqlens ? 4 * ((size_t)B + 1) : 0}};
+    auto over_input = [&](const Span& out) {
+        for (const Span& in : inputs)
+            if (overlap(out, in)) return true;
+        return overlap_rows(out, q, T, row, (size_t)q_stride * 2);
+    };
+    const Span out_o = {o, T * row}, out_lse = {lse, 4 * (size_t)Hq * T};
+    if (over_input(out_o) || over_input(out_lse) || overlap(out_o, out_lse)) return FA_ERR_INVALID;
+    const int sms = fa_num_sms();
+    DevStatus* status = device_status_ptr();
+    if (sms < 1 || !status) return FA_ERR_LAUNCH;
+    const KvLayout w = kv_layout(T, B, Hkv, G, d, sms);
+    const ManyLayout many = many_layout(T, B, Hq, Hkv, d, max_seqlen, table_width, page_size);
+    if (!workspace || misaligned(workspace, 255) || workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+    const bool expand = many.total > 0 && workspace_bytes >= many.total;
+    const Span scratch = {workspace, expand ? many.total : w.total};
+    if (over_input(scratch) || overlap(scratch, out_o) || overlap(scratch, out_lse)) return FA_ERR_INVALID;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const uint8_t *kp = static_cast<const uint8_t*>(k_pages), *ks = static_cast<const uint8_t*>(k_scales),
+                  *vp = static_cast<const uint8_t*>(v_pages), *vs = static_cast<const uint8_t*>(v_scales);
+    const int lg = page_log2(page_size);
+    if (expand) {
+        int* table = reinterpret_cast<int*>(ws + many.table);
+        const ExpandArgs e = {kp, ks, vp, vs, reinterpret_cast<__nv_bfloat16*>(ws), reinterpret_cast<__nv_bfloat16*>(ws + many.v),
+                              block_table, kv_lens, table, B * table_width, table_width, Hkv, num_pages, lg};
+        const int rc2 = launch_expand(e, d, sms, stream);
+        if (rc2 != FA_OK) return rc2;
+        return fa_prefix_fwd(q, q_stride, ws, ws + many.v, o, lse, T, B, Hq, Hkv, d, alpha, B * table_width, page_size, table, table_width,
+                             kv_lens, cu_seqlens, max_seqlen, nullptr, 0, ws + many.prefix, many.total - many.prefix, stream);
+    }
+    KvArgs a;
+    a.kp = kp;
+    a.ks = ks;
+    a.vp = vp;
+    a.vs = vs;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.q_stride = q_stride;
+    a.table = block_table;
+    a.kv_lens = kv_lens;
+    a.cu = cu_seqlens;
+    a.o = static_cast<__nv_bfloat16*>(o);
+    a.lse = lse;
+    a.status = status;
+    a.hdr = reinterpret_cast<KvHeader*>(ws);
+    a.rows = reinterpret_cast<KvRow*>(ws + w.rows);
+    a.ml = reinterpret_cast<float2*>(ws + w.ml);
+    a.seg = reinterpret_cast<float*>(ws + w.seg);
+    a.T = T;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = G;
+    a.W = table_width;
+    a.P = num_pages;
+    a.ps_log2 = lg;
+    a.max_seqlen = max_seqlen;
+    a.scale_log2 = alpha * 1.4426950408889634f;
+    const int rows = item_rows(d, max_seqlen * (long long)G);
+    if (d == 64) return rows == 8 ? launch_few<64, 1>(a, sms, stream) : rows == 16 ? launch_few<64, 2>(a, sms, stream) : launch_few<64, 4>(a, sms, stream);
+    if (d == 128) return rows == 8 ? launch_few<128, 1>(a, sms, stream) : rows == 16 ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 4>(a, sms, stream);
+    return rows == 8 ? launch_few<256, 1>(a, sms, stream) : launch_few<256, 2>(a, sms, stream);
+}
+
+}  // extern "C"

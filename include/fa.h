@@ -547,6 +547,58 @@ int fa_rope_store(const void *q, const void *k, const void *v, int64_t q_stride,
  */
 
 /*
+ * 4-bit pages as bf16 pages, exactly: page pages[i] (NULL: page i; then n <=
+ * num_pages) of k_pages and v_pages becomes page i of k_out and v_out, bf16 [n,
+ * Hkv, page_size, d].  For a page that is none, page i of the outputs is left as it
+ * was.  One launch, no workspace; n == 0 is a no-op.
+ * Errors: FA_ERR_INVALID (null pointer, n < 0, Hkv, d or num_pages < 1, more pages
+ * than there are, outputs that overlap an array), FA_ERR_UNSUPPORTED (d,
+ * page_size, num_pages * page_size or n * Hkv above 2^31 - 1), FA_ERR_ALIGN,
+ * FA_ERR_LAUNCH.
+ */
+int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages, const void *v_scales,
+                  const int *pages, int n, int Hkv, int d, int num_pages, int page_size, void *k_out, void *v_out,
+                  cudaStream_t stream);
+
+/*
+ * Attention of a step's tokens over a 4-bit cache: what fa_prefix_fwd computes
+ * without a prefix (rows, tables, lengths, causal limit, absent pages, rows that
+ * see no key and rows outside every request as there), keys and values read from
+ * 4-bit pages.  Scores, sums and the output's accumulator are 32 bits wide, the
+ * weights fp16 relative to the largest weight times value scale.
+ * Up to 128 rows of a request and key/value head (max_seqlen * Hq / Hkv) are
+ * computed from the codes; above that, and while 4 * B * table_width * page_size
+ * * Hkv * d is up to 2^32, the call expands the requests' pages into the
+ * workspace once and goes on as fa_prefix_fwd.  A workspace too small for that, but
+ * not for a call with max_seqlen 1, makes the rows be computed from the codes: right,
+ * and for long prompts several times slower.  Equal calls with equal workspace
+ * sizes give equal results, bit for bit.
+ * What the cache holds behind the lengths does not matter.  A NaN in a query or
+ * in a key that a row sees gives NaN in its O and LSE; one in a value (a scale of
+ * 0xFC) may also reach the O of other rows of its request.
+ * o, lse and the workspace must not overlap an input or one another.  workspace:
+ * 256-byte aligned, no initialisation needed; calls that share one must not
+ * overlap on the GPU (captured graphs that hold the same one included).  A call
+ * whose kernel gives up a wait (2 s) reports FA_ERR_TIMEOUT through
+ * fa_get_device_status, one with a request of more rows than max_seqlen computes
+ * nothing and reports FA_ERR_INVALID there.  T == 0 is a no-op.
+ * Errors: as fa_prefix_fwd, and FA_ERR_UNSUPPORTED where key/value heads times
+ * (T * Hq / Hkv / 8 + min(T, B)) times (table_width * page_size / 64 + 3) is
+ * above 2^30.
+ */
+int fa_kv4_fwd(const void *q, int64_t q_stride, const void *k_pages, const void *k_scales, const void *v_pages,
+               const void *v_scales, void *o, float *lse, int T, int B, int Hq, int Hkv, int d, float alpha,
+               int num_pages, int page_size, const int *block_table, int table_width, const int *kv_lens,
+               const int *cu_seqlens, int max_seqlen, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Bytes of device workspace fa_kv4_fwd needs for T rows of B requests of at most
+ * max_seqlen rows each over tables of table_width pages (the current device's SM
+ * count enters); 0 for invalid sizes.
+ */
+size_t fa_kv4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int table_width, int page_size);
+
+/*
  * Reads (and clears) the library's device status word on the current
  * device after synchronising `stream`: FA_OK, or FA_ERR_TIMEOUT when a
  * kernel's bounded wait gave up (the kernel then skipped its remaining work,
