@@ -53,17 +53,21 @@ constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call t
 template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
-    static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;   // an SM
-    static constexpr int kParts = NT == 1 && D <= 128 ? 2 : 1;  // 16-key parts a step
-    // A part in shared memory: K's codes, V's codes, K's scales, V's scales.
-    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales);
-    static constexpr uint32_t kRing = D == 64 ? 10 : D == 128 ? (NT == 1 ? 5 : 8) : NT == 1 ? 5 : 4;
+    static constexpr int kWarps = NT == 1 ? (D == 64 ? 14 : D == 128 ? 15 : 8) : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
+    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
+    static constexpr int kKeys = 16 * kParts;
+    // A step's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
+    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kParts * kPart;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 3 : NT == 2 ? 5 : 8) : D == 64 ? (NT == 1 ? 3 : 8) : NT == 1 ? 5 : 4;
     static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
-    static constexpr uint32_t kWarp = kRing * kPart + kQBytes;
-    static_assert(kPart % 16 == 0 && kWarp % 16 == 0, "copies are 16-byte aligned");
+    // A step's scales as the products want them: K's as floats [key][group], V's as
+    // pairs of keys [key / 2][group], (e, 2^-e) [key].
+    static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
+    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPrep;
+    static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0, "copies are 16-byte aligned");
     static constexpr int kTables = (3 * (kMaxVarlenSeqs + 1) + kMaxVarlenSeqs) * 4;
-    static_assert(kCtas * (8 * kWarp + kTables + 2048) <= 232448, "shared memory plan");
+    static_assert(kWarps * kWarp + kTables + 1536 <= 232448, "shared memory plan");
 };
 
 struct KvRow {
@@ -164,8 +168,8 @@ struct KvWalk {
 };
 
 struct KvShared {
-    uint64_t full[8][10];
-    int2 scan[8];
+    uint64_t full[16][8];
+    int2 scan[16];
     int abort_flag, bad;
 };
 
@@ -198,7 +202,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
     const int lane = tid & 31, warp = tid >> 5;
     const long long cap = (long long)a.W << a.ps_log2;
     bool fine = true;
-    for (int i = tid; i <= a.B; i += 256) {
+    for (int i = tid; i <= a.B; i += Kv<D, NT>::kThreads) {
         const int c = a.cu ? a.cu[i] : i, before = a.cu && i > 0 ? a.cu[i - 1] : 0;
         fine = fine && c >= before && c >= 0 && c <= a.T;
         t.cu[i] = c;
@@ -220,7 +224,8 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
         __syncthreads();
     }
     int units = 0, items = 0;
-    for (int base = 0; base < a.B; base += 256) {
+    constexpr int kThreads = Kv<D, NT>::kThreads, kWarps = Kv<D, NT>::kWarps;
+    for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + tid;
         int u = 0, it = 0;
         if (i < a.B) {
@@ -238,7 +243,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
         if (base) __syncthreads();
         if (lane == 31) sh.scan[warp] = make_int2(u, it);
         __syncthreads();
-        for (int w = 0; w < 8; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const int2 x = sh.scan[w];
             if (w < warp) u += x.x, it += x.y;
         }
@@ -246,7 +251,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
             t.pref[i] = units + u - u_own;
             t.items[i] = items + it - it_own;
         }
-        for (int w = 0; w < 8; ++w) units += sh.scan[w].x, items += sh.scan[w].y;
+        for (int w = 0; w < kWarps; ++w) units += sh.scan[w].x, items += sh.scan[w].y;
     }
     if (tid == 0) {
         t.pref[a.B] = units;
@@ -254,7 +259,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
     }
     __syncthreads();
     KvHeader h = {};
-    const int workers = gridDim.x * 8;
+    const int workers = gridDim.x * kWarps;
     h.per = units ? (units + workers - 1) / workers : 1;
     h.bad = sh.bad;
     if (blockIdx.x == 0 && tid == 0) {
@@ -269,6 +274,10 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
@@ -307,42 +316,80 @@ template <int N> __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w
                          : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i) : "memory");
 }
 
-// A key's scales, as floats.
-template <int D> __device__ __forceinline__ void key_scales(uint32_t addr, float (&s)[D / 32]) {
+template <int N> __device__ __forceinline__ void sts(uint32_t addr, const uint32_t (&w)[N]) {
+    if constexpr (N == 1) asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w[0]) : "memory");
+    else if constexpr (N == 2) asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(w[0]), "r"(w[1]) : "memory");
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr + 4 * i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]) : "memory");
+}
+
+// A key's scales as f16 pairs (groups 2i and 2i + 1).
+template <int D> __device__ __forceinline__ void scale_pairs(uint32_t addr, bool real, uint32_t (&h)[D / 64]) {
+    uint32_t w[D == 256 ? 2 : 1];
     if constexpr (D == 64) {
         uint16_t x;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
-        s[0] = scale_f32(x & 0xffu);
-        s[1] = scale_f32(x >> 8);
+        w[0] = x;
     } else {
-        uint32_t w[D / 128];
         lds(addr, w);
-#pragma unroll
-        for (int g = 0; g < D / 32; ++g) s[g] = scale_f32(w[g / 4] >> (g % 4 * 8) & 0xffu);
     }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) h[i] = __byte_perm(real ? w[i / 2] : 0u, 0u, i & 1 ? 0x4342 : 0x4140) << 7;
 }
 
-// The scales of two adjacent keys, as f16 pairs by group; a key that is not seen has 0.
-template <int D> __device__ __forceinline__ void pair_scales(uint32_t addr, bool first, bool second, uint32_t (&s)[D / 32]) {
-    uint32_t w[D / 64];
-    lds(addr, w);
+// A step's scales, a key a lane: each is wanted by eight or four lanes, so the work is
+// done once (as part of every lane's it was a quarter of all instructions).  `real`:
+// this key is seen by some row; one that is not has value scales 0.
+template <int D, int NT>
+__device__ __forceinline__ void prepare_key(uint32_t ks, uint32_t vs, uint32_t prep, int key, int lane, bool real) {
+    using K = Kv<D, NT>;
+    constexpr int kG = K::kGroups;
+    uint32_t h[kG / 2], f[kG];
+    scale_pairs<D>(ks + key * kG, true, h);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-        const uint32_t m = D == 64 ? (first ? 0xffffu : 0u) | (second ? 0xffff0000u : 0u) : (2 * i < D / 64 ? first : second) ? ~0u : 0u;
-        w[i] &= m;
+    for (int i = 0; i < kG / 2; ++i) {
+        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        f[2 * i] = __float_as_uint(x.x);
+        f[2 * i + 1] = __float_as_uint(x.y);
     }
+    sts(prep + key * (4 * kG), f);
+    scale_pairs<D>(vs + key * kG, real, h);
+    // 2^e from 2^-14, fp16's smallest normal number, to 2^15; a NaN counts for nothing here.
+    uint32_t m = h[0];
 #pragma unroll
-    for (int g = 0; g < D / 32; ++g) {
-        const uint32_t x = D == 64 ? __byte_perm(w[0], w[0], g | (2 + g) << 8)
-                                   : __byte_perm(w[g / 4], w[D / 128 + g / 4], g % 4 | (4 + g % 4) << 8);
-        s[g] = x << 7 & 0x7f807f80u;
+    for (int i = 1; i < kG / 2; ++i) m = hmax2(m, h[i]);
+    m = hmax2(m, __byte_perm(m, m, 0x1032));
+    const uint32_t ex = hmin2(hmax2(m, 0x04000400u), 0x78007800u) & 0x7c007c00u, down = 0x7c007c00u - ex;    // 2^(16 - field) = 2^-e
+#pragma unroll
+    for (int i = 0; i < kG / 2; ++i) h[i] = hmul2(h[i], down);
+    const uint32_t field = ex >> 26;
+    const uint32_t eb[2] = {__float_as_uint(__uint_as_float(0x4b000000u | field) - 8388624.f), (143u - field) << 23};
+    sts(prep + K::kExp + key * 8, eb);
+    // Pairs of keys: the even key's lane takes the first half of the groups.
+    const bool odd = lane & 1;
+    if constexpr (kG == 2) {
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, h[0], 1);
+        const uint32_t out[1] = {odd ? __byte_perm(other, h[0], 0x7632) : __byte_perm(h[0], other, 0x5410)};
+        sts(prep + K::kVPairs + (key >> 1) * 8 + (odd ? 4 : 0), out);
+    } else {
+        uint32_t out[kG / 2];
+#pragma unroll
+        for (int i = 0; i < kG / 4; ++i) {
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[kG / 4 + i], 1);
+            const uint32_t x = odd ? other : h[i], y = odd ? h[kG / 4 + i] : other;
+            out[2 * i] = __byte_perm(x, y, 0x5410);
+            out[2 * i + 1] = __byte_perm(x, y, 0x7632);
+        }
+        sts(prep + K::kVPairs + (key >> 1) * (4 * kG) + (odd ? 2 * kG : 0), out);
     }
 }
 
 // -------------------------------------------------------------------- kernel
 
 template <int D, int NT>
-__global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs a) {
+__global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArgs a) {
     using K = Kv<D, NT>;
     constexpr int kG = K::kGroups, kParts = K::kParts;
     constexpr uint32_t kRing = K::kRing;
@@ -350,11 +397,11 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
     __shared__ KvShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     KvTables t;
-    t.pref = reinterpret_cast<int*>(dsmem + 8 * K::kWarp);
+    t.pref = reinterpret_cast<int*>(dsmem + K::kWarps * K::kWarp);
     t.items = t.pref + a.B + 1;
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
-    if (tid < 8 * (int)kRing) {
+    if (tid < K::kWarps * (int)kRing) {
         mbar_init(&sh.full[tid / kRing][tid % kRing], 1);
         fence_mbar_init();
     }
@@ -364,7 +411,7 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
     const KvHeader hdr = build_tables<D, NT>(a, t, sh, tid);
 
     // What the joining kernel needs to know of each row.
-    for (int i = blockIdx.x * 256 + tid; i < a.T; i += gridDim.x * 256) {
+    for (int i = blockIdx.x * K::kThreads + tid; i < a.T; i += gridDim.x * K::kThreads) {
         KvRow row = {};
         if (i >= t.cu[0] && i < t.cu[a.B]) {
             int lo = 0;
@@ -382,8 +429,8 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
     }
 
     uint64_t* full = sh.full[warp];
-    const uint32_t ring = smem_u32(dsmem) + warp * K::kWarp, q_smem = ring + kRing * K::kPart;
-    const int worker = blockIdx.x * 8 + warp;
+    const uint32_t ring = smem_u32(dsmem) + warp * K::kWarp, q_smem = ring + kRing * K::kSlot, prep = q_smem + K::kQBytes;
+    const int worker = blockIdx.x * K::kWarps + warp;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
     KvWalk<K::kRows> ahead;
@@ -391,7 +438,7 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
     ahead.start(a, t, hdr, worker);
     bool more = ahead.next(a, t, to);
     int part = to.p0, win = -1, win_next = -1;       // next part; pages of its 32 parts, one a lane, and of the next 32
-    uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a slot: its page exists
+    uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a part of a slot: its page exists
     auto pages = [&](int p) -> int {                 // of parts p .. p + 31
         if (p + lane >= to.p1) return -1;
         const int x = a.table[(long long)to.b * a.W + ((p + lane) * 16 >> a.ps_log2)];
@@ -401,27 +448,35 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
         win = pages(part);
         win_next = pages(part + 32);
     }
+    // This lane's copies: one of K's codes, V's codes, K's scales and V's scales, of
+    // one part of a step.
+    const int what = lane & 3, which = lane >> 2;
+    const uint8_t* const from = what == 0 ? a.kp : what == 1 ? a.vp : what == 2 ? a.ks : a.vs;
+    const uint32_t bytes = what < 2 ? K::kCodes : K::kScales;
+    const uint32_t into = ring + (what < 2 ? (what * kParts + which) * K::kCodes : 2 * kParts * K::kCodes + ((what - 2) * kParts + which) * K::kScales);
     auto copy = [&]() {
         if (!more) return;
-        const int page = __shfl_sync(0xffffffffu, win, (part - to.p0) & 31);
+        const int page = __shfl_sync(0xffffffffu, win, (part - to.p0 + which) & 31);      // -1 past the item's end
+        const bool real = lane < 4 * kParts && page >= 0;
+        uint32_t on = __ballot_sync(0xffffffffu, real);
+        on = kParts == 4 ? (on & 1) | (on >> 3 & 2) | (on >> 6 & 4) | (on >> 9 & 8) : kParts == 2 ? (on & 1) | (on >> 3 & 2) : on & 1;
         uint64_t* bar = &full[filled];
         __syncwarp();                                // every lane has read what the slot held
-        if (page >= 0) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, K::kPart);
-            __syncwarp();
-            if (lane < 4) {                          // K's codes, V's codes, K's scales, V's scales
-                const long long row = (((long long)page * a.Hkv + to.hk) << a.ps_log2) + (part * 16 & ((1 << a.ps_log2) - 1));
-                const uint8_t* base = lane == 0 ? a.kp : lane == 1 ? a.vp : lane == 2 ? a.ks : a.vs;
-                const uint32_t dst = ring + filled * K::kPart + (lane < 2 ? lane * K::kCodes : 2 * K::kCodes + (lane - 2) * K::kScales);
-                bulk_load(dst, base + row * (lane < 2 ? D / 2 : D / 32), lane < 2 ? K::kCodes : K::kScales, bar);
-            }
-        } else if (lane == 0) {
-            mbar_arrive(bar);
+        if (lane == 0) {
+            if (on) mbar_arrive_expect_tx(bar, K::kPart * __popc(on));
+            else mbar_arrive(bar);
         }
-        live = (live & ~(1u << filled)) | (page >= 0 ? 1u << filled : 0u);
+        __syncwarp();
+        if (real) {
+            const int key = (part + which) * 16;
+            const long long row = (((long long)page * a.Hkv + to.hk) << a.ps_log2) + (key & ((1 << a.ps_log2) - 1));
+            bulk_load(into + filled * K::kSlot, from + row * (what < 2 ? D / 2 : D / 32), bytes, bar);
+        }
+        live = (live & ~(((1u << kParts) - 1u) << (filled * kParts))) | on << (filled * kParts);
         filled = filled + 1 == kRing ? 0 : filled + 1;
         ++issued;
-        if (++part == to.p1) {
+        part += kParts;
+        if (part >= to.p1) {
             more = ahead.next(a, t, to);
             if (more) {
                 part = to.p0;
@@ -500,31 +555,27 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
         const int lim_min = it.s - it.n + (int)((long long)it.rb * K::kRows / a.G) + 1;
 
         for (int p = it.p0; p < it.p1; p += kParts) {
-            const int k0 = p * 16, parts = min(kParts, it.p1 - p);
-            uint32_t here = 0;                       // parts of this step with a page
+            const int k0 = p * 16;
+            const uint32_t at = ring + slot * K::kSlot, here = live >> (slot * kParts) & ((1u << kParts) - 1u);
+            if (!(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
+            const bool ragged = k0 + K::kKeys > lim_min || here != (1u << kParts) - 1u;
+#pragma unroll
+            for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
+                const int key = i * 32 + (lane & (K::kKeys - 1));      // sixteen keys: every key twice, with the same results
+                const bool real = !ragged || (k0 + key < it.seen && (here >> (key >> 4) & 1u));
+                prepare_key<D, NT>(at + 2 * kParts * K::kCodes, at + 2 * kParts * K::kCodes + kParts * K::kScales, prep, key, lane, real);
+            }
+            __syncwarp();
             float z[kParts][NT][4], back[kParts][2]; // scores + e, 2^-e
-            uint32_t vsc[kParts][2][kG];             // V's scales over 2^e: keys 2c, 2c + 1 and eight further
 #pragma unroll
             for (int kt = 0; kt < kParts; ++kt) {
-                const uint32_t sl = slot + kt < kRing ? slot + kt : slot + kt - kRing;
-                const uint32_t at = ring + sl * K::kPart;
-                if (kt < parts) {
-                    const uint32_t ph = slot + kt < kRing ? phase : phase ^ 1;
-                    if (!(ok = kv_wait(&full[sl], ph, &sh.abort_flag))) break;
-                    here |= (live >> sl & 1u) << kt;
-                }
                 // Keys' codes: eight adjacent elements of every group, for keys r and r + 8.
-                uint32_t kw[2][kG];
-                float ksc[2][kG];
+                uint32_t kw[2][kG], ksc[2][kG];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    lds(at + (r + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
-                    key_scales<D>(at + 2 * K::kCodes + (r + 8 * i) * (D / 32), ksc[i]);
+                    lds(at + (kt * 16 + r + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
+                    lds(prep + (kt * 16 + r + 8 * i) * (4 * kG), ksc[i]);
                 }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < kG / 2; ++j) {
                     uint32_t x[2][2][4];             // [step of the group][key r, r + 8][group 2j: two pairs, group 2j + 1: two]
@@ -545,43 +596,29 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
                             } else {
                                 lds(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
                             }
-                            float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                            mma_f16(acc, x[0][0][2 * gg], x[0][1][2 * gg], x[0][0][2 * gg + 1], x[0][1][2 * gg + 1], q[0], q[1]);
+                            float acc[4];
+                            mma_f16_0(acc, x[0][0][2 * gg], x[0][1][2 * gg], x[0][0][2 * gg + 1], x[0][1][2 * gg + 1], q[0], q[1]);
                             mma_f16(acc, x[1][0][2 * gg], x[1][1][2 * gg], x[1][0][2 * gg + 1], x[1][1][2 * gg + 1], q[2], q[3]);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(ksc[i >> 1][g], acc[i], z[kt][nt][i]);
+                            for (int i = 0; i < 4; ++i) {
+                                const float sc = __uint_as_float(ksc[i >> 1][g]);
+                                z[kt][nt][i] = g == 0 ? sc * acc[i] : fmaf(sc, acc[i], z[kt][nt][i]);
+                            }
                         }
                     }
                 }
-                // V's scales and their exponents.
-                const bool on = here >> kt & 1u;
-                const int key = k0 + kt * 16 + 2 * c;
-                uint32_t ex[2];
+                uint32_t eb[2][2];                   // of keys r and r + 8
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    pair_scales<D>(at + 2 * K::kCodes + K::kScales + (2 * c + 8 * i) * (D / 32), on && key + 8 * i < it.seen, on && key + 8 * i + 1 < it.seen, vsc[kt][i]);
-                    uint32_t e = 0x04000400u;        // 2^-14, fp16's smallest normal number, to 2^15
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) e = hmax2(e, vsc[kt][i][g]);
-                    ex[i] = hmin2(e, 0x78007800u) & 0x7c007c00u;
-                    const uint32_t down = 0x7c007c00u - ex[i];      // 2^-e, e = exponent field - 16
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) vsc[kt][i][g] = hmul2(vsc[kt][i][g], down);
-                }
-                float e[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {        // of keys r and r + 8: from lane r / 2
-                    const uint32_t x = __shfl_sync(0xffffffffu, ex[i], r >> 1) >> (10 + 16 * (r & 1)) & 31u;
-                    e[i] = __uint_as_float(0x4b000000u | x) - 8388624.f;
-                    back[kt][i] = __uint_as_float((143u - x) << 23);
+                    lds(prep + K::kExp + (kt * 16 + r + 8 * i) * 8, eb[i]);
+                    back[kt][i] = __uint_as_float(eb[i][1]);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], f[nt][i & 1], e[i >> 1]);
+                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], f[nt][i & 1], __uint_as_float(eb[i >> 1][0]));
             }
-            if (!ok) break;
-            if (k0 + kParts * 16 > lim_min || here != (1u << kParts) - 1u) {
+            if (ragged) {
 #pragma unroll
                 for (int kt = 0; kt < kParts; ++kt)
 #pragma unroll
@@ -626,8 +663,6 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
             }
 #pragma unroll
             for (int kt = 0; kt < kParts; ++kt) {
-                const uint32_t sl = slot + kt < kRing ? slot + kt : slot + kt - kRing;
-                const uint32_t at = ring + sl * K::kPart + K::kCodes;
                 uint32_t pt[NT][2];                  // weights as B operands: row r, keys 2c, 2c + 1 and eight further
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -641,12 +676,14 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
                     pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
                     pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
                 }
-                // Values' codes: four elements of every group, for the four keys.
-                uint32_t vw[2][2][kG / 2];
+                // Values' codes: four elements of every group, for the four keys, and scales.
+                uint32_t vw[2][2][kG / 2], vsc[2][kG];
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + (2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
+                    for (int y = 0; y < 2; ++y) lds(at + kParts * K::kCodes + (kt * 16 + 2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
+                    lds(prep + K::kVPairs + (kt * 8 + c + 4 * i) * (4 * kG), vsc[i]);
+                }
 #pragma unroll
                 for (int j = 0; j < kG / 2; ++j) {
                     uint32_t x[2][2][4];             // [keys 2c .., keys 2c + 8 ..][codes 0 and 2, 1 and 3][group 2j: two, group 2j + 1: two]
@@ -662,7 +699,7 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
                         const int g = 2 * j + gg;
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t b0 = hmul2(pt[nt][0], vsc[kt][0][g]), b1 = hmul2(pt[nt][1], vsc[kt][1][g]);
+                            const uint32_t b0 = hmul2(pt[nt][0], vsc[0][g]), b1 = hmul2(pt[nt][1], vsc[1][g]);
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
                                 mma_f16(o[g][h][nt], x[0][0][2 * gg + h], x[0][1][2 * gg + h], x[1][0][2 * gg + h], x[1][1][2 * gg + h], b0, b1);
@@ -670,14 +707,13 @@ __global__ void __launch_bounds__(256, Kv<D, NT>::kCtas) kv4_kernel(const KvArgs
                     }
                 }
             }
-            for (int i = 0; i < parts; ++i) {
-                ++read;
-                if (++slot == kRing) {
-                    slot = 0;
-                    phase ^= 1;
-                }
-                copy();
+            ++read;
+            if (++slot == kRing) {
+                slot = 0;
+                phase ^= 1;
             }
+            __syncwarp();
+            copy();
         }
         if (!ok) break;
         // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
@@ -910,7 +946,7 @@ struct KvLayout {
 KvLayout kv_layout(int T, int B, int Hkv, int G, int d, int sms) {
     size_t most = 0;
     for (int rows = 8; rows <= (d == 256 ? 16 : 32); rows *= 2) {
-        const size_t items = (size_t)Hkv * ((long long)T * G / rows + (T < B ? T : B)), workers = (size_t)sms * 8 * (rows == 8 && d <= 128 ? 2 : 1);
+        const size_t items = (size_t)Hkv * ((long long)T * G / rows + (T < B ? T : B)), workers = (size_t)sms * 16;
         const size_t n = (items + workers) * rows;
         most = n > most ? n : most;
     }
@@ -942,19 +978,19 @@ template <int D, int NT>
 int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
     using K = Kv<D, NT>;
     auto kern = kv4_kernel<D, NT>;
-    const size_t smem = 8 * K::kWarp + (3 * (a.B + 1) + a.B) * 4;
+    const size_t smem = K::kWarps * K::kWarp + (3 * (a.B + 1) + a.B) * 4;
     static std::atomic<uint64_t> prepared{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(8 * K::kWarp + K::kTables)) != cudaSuccess) return FA_ERR_LAUNCH;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWarps * K::kWarp + K::kTables)) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
     const long long items = (long long)a.Hkv * ((long long)a.T * a.G / K::kRows + (a.T < a.B ? a.T : a.B));
-    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + 7) / 8;
-    const int most = sms * K::kCtas, grid = 2 * need < most ? (int)(2 * need) : most;
-    if (launch_dependent(kern, grid, 256, smem, stream, a) != cudaSuccess) return FA_ERR_LAUNCH;
+    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + K::kWarps - 1) / K::kWarps;
+    const int grid = 2 * need < sms ? (int)(2 * need) : sms;
+    if (launch_dependent(kern, grid, K::kThreads, smem, stream, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     cudaError_t e;
     if (rows <= 8LL * sms) e = launch_dependent(kv4_join_kernel<D, true>, (int)rows, 256, 0, stream, a, K::kRows);
