@@ -45,20 +45,27 @@ namespace fa {
 namespace {
 
 constexpr float kTau = 8.0f;            // rescale threshold (log2 units)
+constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every finite score; a hidden key's -inf less it is -inf
 constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kManyRows = 128;          // rows of a request and key/value head above which pages are expanded
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
+// A CTA's tables of the list: in shared memory up to kTableMost requests, else in its
+// own piece of the workspace.
+constexpr int kTableMost = 128;
+__host__ __device__ constexpr uint32_t table_bytes(int B) { return (4u * B + 3) * 4; }
+
 template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
-    static constexpr int kWarps = NT == 1 ? (D == 64 ? 14 : D == 128 ? 15 : 8) : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
+    static constexpr int kWarps = NT == 1 && D <= 128 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
     static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
-    static constexpr int kKeys = 16 * kParts;
-    // A step's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
-    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 3 : NT == 2 ? 5 : 8) : D == 64 ? (NT == 1 ? 3 : 8) : NT == 1 ? 5 : 4;
+    static constexpr int kSteps = D == 128 && NT <= 2 ? 2 : D == 64 && NT == 2 ? 2 : 1;   // steps a slot of the ring
+    static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kParts;
+    // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
+    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : 4;
     static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
     // A step's scales as the products want them: K's as floats [key][group], V's as
@@ -66,8 +73,8 @@ template <int D, int NT> struct Kv {
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
     static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPrep;
     static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0, "copies are 16-byte aligned");
-    static constexpr int kTables = (3 * (kMaxVarlenSeqs + 1) + kMaxVarlenSeqs) * 4;
-    static_assert(kWarps * kWarp + kTables + 1536 <= 232448, "shared memory plan");
+    static_assert(kRing * kSlotParts <= 32 && kRing <= 8 && 4 * kSlotParts <= 32, "a bit a part, a lane a copy");
+    static_assert(kWarps * kWarp + table_bytes(kTableMost) + 1536 <= 232448, "shared memory plan");
 };
 
 struct KvRow {
@@ -86,6 +93,7 @@ struct KvArgs {
     float* lse;
     DevStatus* status;
     KvHeader* hdr;
+    int* tables;             // [CTA][4 B + 3], B > kTableMost
     KvRow* rows;             // [T]
     float2* ml;              // segments' rows: maximum, sum
     float* seg;              // [segment][rows][D]
@@ -94,7 +102,7 @@ struct KvArgs {
 };
 
 struct KvTables {
-    int *pref, *items, *cu, *len;        // [B+1], [B+1], [B+1], [B], in shared memory
+    int *pref, *items, *cu, *len;        // [B+1], [B+1], [B+1], [B]
 };
 
 // Row blocks of a request with n tokens, units of each of its items: its tiles of
@@ -391,13 +399,13 @@ __device__ __forceinline__ void prepare_key(uint32_t ks, uint32_t vs, uint32_t p
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArgs a) {
     using K = Kv<D, NT>;
-    constexpr int kG = K::kGroups, kParts = K::kParts;
+    constexpr int kG = K::kGroups, kParts = K::kParts, kSteps = K::kSteps, kSP = K::kSlotParts;
     constexpr uint32_t kRing = K::kRing;
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ KvShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
     KvTables t;
-    t.pref = reinterpret_cast<int*>(dsmem + K::kWarps * K::kWarp);
+    t.pref = a.B <= kTableMost ? reinterpret_cast<int*>(dsmem + K::kWarps * K::kWarp) : a.tables + (long long)blockIdx.x * (4 * a.B + 3);
     t.items = t.pref + a.B + 1;
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
@@ -453,13 +461,13 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     const int what = lane & 3, which = lane >> 2;
     const uint8_t* const from = what == 0 ? a.kp : what == 1 ? a.vp : what == 2 ? a.ks : a.vs;
     const uint32_t bytes = what < 2 ? K::kCodes : K::kScales;
-    const uint32_t into = ring + (what < 2 ? (what * kParts + which) * K::kCodes : 2 * kParts * K::kCodes + ((what - 2) * kParts + which) * K::kScales);
+    const uint32_t into = ring + (what < 2 ? (what * kSP + which) * K::kCodes : 2 * kSP * K::kCodes + ((what - 2) * kSP + which) * K::kScales);
     auto copy = [&]() {
         if (!more) return;
         const int page = __shfl_sync(0xffffffffu, win, (part - to.p0 + which) & 31);      // -1 past the item's end
-        const bool real = lane < 4 * kParts && page >= 0;
+        const bool real = lane < 4 * kSP && page >= 0;
         uint32_t on = __ballot_sync(0xffffffffu, real);
-        on = kParts == 4 ? (on & 1) | (on >> 3 & 2) | (on >> 6 & 4) | (on >> 9 & 8) : kParts == 2 ? (on & 1) | (on >> 3 & 2) : on & 1;
+        on = kSP == 4 ? (on & 1) | (on >> 3 & 2) | (on >> 6 & 4) | (on >> 9 & 8) : kSP == 2 ? (on & 1) | (on >> 3 & 2) : on & 1;
         uint64_t* bar = &full[filled];
         __syncwarp();                                // every lane has read what the slot held
         if (lane == 0) {
@@ -472,10 +480,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             const long long row = (((long long)page * a.Hkv + to.hk) << a.ps_log2) + (key & ((1 << a.ps_log2) - 1));
             bulk_load(into + filled * K::kSlot, from + row * (what < 2 ? D / 2 : D / 32), bytes, bar);
         }
-        live = (live & ~(((1u << kParts) - 1u) << (filled * kParts))) | on << (filled * kParts);
+        live = (live & ~(((1u << kSP) - 1u) << (filled * kSP))) | on << (filled * kSP);
         filled = filled + 1 == kRing ? 0 : filled + 1;
         ++issued;
-        part += kParts;
+        part += kSP;
         if (part >= to.p1) {
             more = ahead.next(a, t, to);
             if (more) {
@@ -544,7 +552,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 f[nt][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
                 const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
                 lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
-                m[nt][i] = -INFINITY;
+                m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
 #pragma unroll
@@ -555,15 +563,18 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         const int lim_min = it.s - it.n + (int)((long long)it.rb * K::kRows / a.G) + 1;
 
         for (int p = it.p0; p < it.p1; p += kParts) {
-            const int k0 = p * 16;
-            const uint32_t at = ring + slot * K::kSlot, here = live >> (slot * kParts) & ((1u << kParts) - 1u);
-            if (!(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
+            const int k0 = p * 16, sub = kSteps == 1 ? 0 : (p - it.p0) / kParts & (kSteps - 1);    // step of the slot
+            // The step's K codes, K scales; V's lie kSP parts behind each.
+            const uint32_t at = ring + slot * K::kSlot + sub * (kParts * K::kCodes);
+            const uint32_t scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
+            const uint32_t here = live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
+            if (sub == 0 && !(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
             const bool ragged = k0 + K::kKeys > lim_min || here != (1u << kParts) - 1u;
 #pragma unroll
             for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
                 const int key = i * 32 + (lane & (K::kKeys - 1));      // sixteen keys: every key twice, with the same results
                 const bool real = !ragged || (k0 + key < it.seen && (here >> (key >> 4) & 1u));
-                prepare_key<D, NT>(at + 2 * kParts * K::kCodes, at + 2 * kParts * K::kCodes + kParts * K::kScales, prep, key, lane, real);
+                prepare_key<D, NT>(scales, scales + kSP * K::kScales, prep, key, lane, real);
             }
             __syncwarp();
             float z[kParts][NT][4], back[kParts][2]; // scores + e, 2^-e
@@ -627,9 +638,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                         for (int i = 0; i < 4; ++i)
                             if (!(here >> kt & 1u) || k0 + kt * 16 + r + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
             }
-            // The running maximum of each row; O and l follow it when it grows by more
-            // than kTau.
-            float mn[NT][2];
+            // O and l follow a row's running maximum when it grows by more than kTau: only
+            // then do the lanes that share the row look for it together.
             bool jump = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -638,20 +648,22 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
                     for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    mn[nt][i] = fmaxf(m[nt][i], x);
-                    jump |= m[nt][i] == -INFINITY ? mn[nt][i] != -INFINITY : mn[nt][i] - m[nt][i] > kTau;
+                    jump |= x - m[nt][i] > kTau;
                 }
             if (__any_sync(0xffffffffu, jump)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float fac = m[nt][i] == -INFINITY ? 0.f : ex2_mufu(m[nt][i] - mn[nt][i]);
+                        float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
+#pragma unroll
+                        for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(m[nt][i], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)));
+                        const float fac = ex2_mufu(m[nt][i] - x);
                         l[nt][i] *= fac;
-                        m[nt][i] = mn[nt][i];
+                        m[nt][i] = x;
 #pragma unroll
                         for (int g = 0; g < kG; ++g)
 #pragma unroll
@@ -669,8 +681,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     float w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float use = m[nt][i & 1] == -INFINITY ? 0.f : m[nt][i & 1];
-                        w[i] = ex2_mufu(z[kt][nt][i] - use);
+                        w[i] = ex2_mufu(z[kt][nt][i] - m[nt][i & 1]);
                         l[nt][i & 1] = fmaf(w[i], back[kt][i >> 1], l[nt][i & 1]);
                     }
                     pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + kParts * K::kCodes + (kt * 16 + 2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
+                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
                     lds(prep + K::kVPairs + (kt * 8 + c + 4 * i) * (4 * kG), vsc[i]);
                 }
 #pragma unroll
@@ -707,13 +718,15 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     }
                 }
             }
-            ++read;
-            if (++slot == kRing) {
-                slot = 0;
-                phase ^= 1;
-            }
             __syncwarp();
-            copy();
+            if (sub == kSteps - 1 || p + kParts >= it.p1) {
+                ++read;
+                if (++slot == kRing) {
+                    slot = 0;
+                    phase ^= 1;
+                }
+                copy();
+            }
         }
         if (!ok) break;
         // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
@@ -941,7 +954,7 @@ int item_rows(int d, long long rows) { return rows <= 8 ? 8 : rows <= 16 || d ==
 // largest of the three item sizes, so that a workspace for long drafts serves
 // single tokens.
 struct KvLayout {
-    size_t rows, ml, seg, total;
+    size_t tables, rows, ml, seg, total;
 };
 KvLayout kv_layout(int T, int B, int Hkv, int G, int d, int sms) {
     size_t most = 0;
@@ -951,7 +964,8 @@ KvLayout kv_layout(int T, int B, int Hkv, int G, int d, int sms) {
         most = n > most ? n : most;
     }
     KvLayout w;
-    w.rows = 256;
+    w.tables = 256;
+    w.rows = align256(w.tables + (B > kTableMost ? (size_t)sms * table_bytes(B) : 0));
     w.ml = align256(w.rows + (size_t)T * sizeof(KvRow));
     w.seg = align256(w.ml + most * 8);
     w.total = align256(w.seg + most * d * 4);
@@ -978,12 +992,12 @@ template <int D, int NT>
 int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
     using K = Kv<D, NT>;
     auto kern = kv4_kernel<D, NT>;
-    const size_t smem = K::kWarps * K::kWarp + (3 * (a.B + 1) + a.B) * 4;
+    const size_t smem = K::kWarps * K::kWarp + (a.B <= kTableMost ? table_bytes(a.B) : 0);
     static std::atomic<uint64_t> prepared{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWarps * K::kWarp + K::kTables)) != cudaSuccess) return FA_ERR_LAUNCH;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWarps * K::kWarp + table_bytes(kTableMost))) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
@@ -1119,6 +1133,7 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     a.lse = lse;
     a.status = status;
     a.hdr = reinterpret_cast<KvHeader*>(ws);
+    a.tables = reinterpret_cast<int*>(ws + w.tables);
     a.rows = reinterpret_cast<KvRow*>(ws + w.rows);
     a.ml = reinterpret_cast<float2*>(ws + w.ml);
     a.seg = reinterpret_cast<float*>(ws + w.seg);
