@@ -81,8 +81,14 @@ struct KvRow {
     int c0, n, s, pref, items, pad[3];   // of a row's request: first row, rows (0: none), keys; units and items before it
 };
 struct KvHeader {
-    int per, bad, pad[2];                // units a worker; a request has more rows than max_seqlen
+    int per, more, bad, pad;             // units a worker, the first `more` one more; a request has more rows than max_seqlen
 };
+// A worker's first unit, and the worker of a unit.
+__device__ __forceinline__ int unit_of(const KvHeader& h, int worker) { return worker * h.per + min(worker, h.more); }
+__device__ __forceinline__ int worker_of(const KvHeader& h, int unit) {
+    const int longer = h.more * (h.per + 1);
+    return unit < longer ? unit / (h.per + 1) : h.more + (unit - longer) / h.per;
+}
 
 struct KvArgs {
     const uint8_t *kp, *ks, *vp, *vs;
@@ -136,10 +142,8 @@ struct KvWalk {
     int u, end, b, worker;
     __device__ __forceinline__ void start(const KvArgs& a, const KvTables& t, const KvHeader& h, int w) {
         worker = w;
-        const int all = h.bad ? 0 : t.pref[a.B];
-        const long long from = (long long)w * h.per;
-        u = from < all ? (int)from : all;
-        end = min(all - u, h.per) + u;
+        u = h.bad ? 0 : unit_of(h, w);
+        end = h.bad ? 0 : unit_of(h, w + 1);
         int lo = 0, hi = a.B - 1;
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -268,7 +272,8 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
     __syncthreads();
     KvHeader h = {};
     const int workers = gridDim.x * kWarps;
-    h.per = units ? (units + workers - 1) / workers : 1;
+    h.per = units / workers;
+    h.more = units - h.per * workers;
     h.bad = sh.bad;
     if (blockIdx.x == 0 && tid == 0) {
         *a.hdr = h;
@@ -280,16 +285,16 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
 // ------------------------------------------------------------------ products
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_f16_0(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -313,35 +318,36 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// N words from shared memory at a 4 N-byte boundary.
-template <int N> __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
-    if constexpr (N == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
-    else if constexpr (N == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-    else
+// N words from or to shared memory at a 4 N-byte boundary (16 bytes at most at a time).
+template <int N> __device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]) : "r"(addr + 4 * i) : "memory");
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p + 4 * i);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+        }
+    }
 }
-
-template <int N> __device__ __forceinline__ void sts(uint32_t addr, const uint32_t (&w)[N]) {
-    if constexpr (N == 1) asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(w[0]) : "memory");
-    else if constexpr (N == 2) asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(w[0]), "r"(w[1]) : "memory");
+template <int N> __device__ __forceinline__ void sts(uint8_t* p, const uint32_t (&w)[N]) {
+    if constexpr (N == 1) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else if constexpr (N == 2) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr + 4 * i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]) : "memory");
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
 }
 
 // A key's scales as f16 pairs (groups 2i and 2i + 1).
-template <int D> __device__ __forceinline__ void scale_pairs(uint32_t addr, bool real, uint32_t (&h)[D / 64]) {
+template <int D> __device__ __forceinline__ void scale_pairs(const uint8_t* p, bool real, uint32_t (&h)[D / 64]) {
     uint32_t w[D == 256 ? 2 : 1];
     if constexpr (D == 64) {
-        uint16_t x;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr) : "memory");
-        w[0] = x;
+        w[0] = *reinterpret_cast<const uint16_t*>(p);
     } else {
-        lds(addr, w);
+        lds(p, w);
     }
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) h[i] = __byte_perm(real ? w[i / 2] : 0u, 0u, i & 1 ? 0x4342 : 0x4140) << 7;
@@ -351,7 +357,7 @@ template <int D> __device__ __forceinline__ void scale_pairs(uint32_t addr, bool
 // done once (as part of every lane's it was a quarter of all instructions).  `real`:
 // this key is seen by some row; one that is not has value scales 0.
 template <int D, int NT>
-__device__ __forceinline__ void prepare_key(uint32_t ks, uint32_t vs, uint32_t prep, int key, int lane, bool real) {
+__device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs, uint8_t* prep, int key, int lane, bool real) {
     using K = Kv<D, NT>;
     constexpr int kG = K::kGroups;
     uint32_t h[kG / 2], f[kG];
@@ -437,7 +443,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     }
 
     uint64_t* full = sh.full[warp];
-    const uint32_t ring = smem_u32(dsmem) + warp * K::kWarp, q_smem = ring + kRing * K::kSlot, prep = q_smem + K::kQBytes;
+    uint8_t* const ring = dsmem + warp * K::kWarp;
+    uint8_t *const q_smem = ring + kRing * K::kSlot, *const prep = q_smem + K::kQBytes;
     const int worker = blockIdx.x * K::kWarps + warp;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     const int what = lane & 3, which = lane >> 2;
     const uint8_t* const from = what == 0 ? a.kp : what == 1 ? a.vp : what == 2 ? a.ks : a.vs;
     const uint32_t bytes = what < 2 ? K::kCodes : K::kScales;
-    const uint32_t into = ring + (what < 2 ? (what * kSP + which) * K::kCodes : 2 * kSP * K::kCodes + ((what - 2) * kSP + which) * K::kScales);
+    const uint32_t into = smem_u32(ring) + (what < 2 ? (what * kSP + which) * K::kCodes : 2 * kSP * K::kCodes + ((what - 2) * kSP + which) * K::kScales);
     auto copy = [&]() {
         if (!more) return;
         const int page = __shfl_sync(0xffffffffu, win, (part - to.p0 + which) & 31);      // -1 past the item's end
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             win_next = pages(part + 32);
         }
     };
-    for (uint32_t i = 0; i < kRing; ++i) copy();
+    copy();
 
     KvWalk<K::kRows> walk;
     KvItem it;
@@ -543,8 +550,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[nt][g][i] = q[i];
                 } else {
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_smem + ((nt * kG + g) * 32 + lane) * 16), "r"(q[0]),
-                                 "r"(q[1]), "r"(q[2]), "r"(q[3]) : "memory");
+                    sts(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
                 }
             }
 #pragma unroll
@@ -565,10 +571,16 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         for (int p = it.p0; p < it.p1; p += kParts) {
             const int k0 = p * 16, sub = kSteps == 1 ? 0 : (p - it.p0) / kParts & (kSteps - 1);    // step of the slot
             // The step's K codes, K scales; V's lie kSP parts behind each.
-            const uint32_t at = ring + slot * K::kSlot + sub * (kParts * K::kCodes);
-            const uint32_t scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
+            const uint8_t* const at = ring + slot * K::kSlot + sub * (kParts * K::kCodes);
+            const uint8_t* const scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
             const uint32_t here = live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
-            if (sub == 0 && !(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
+            if (sub == 0) {
+                if (!(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
+                // The ring is filled once the first slot is there: all at once, every
+                // warp's first slot would wait for the others' second.
+                if (read == 0)
+                    for (uint32_t i = 1; i < kRing; ++i) copy();
+            }
             const bool ragged = k0 + K::kKeys > lim_min || here != (1u << kParts) - 1u;
 #pragma unroll
             for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
@@ -793,11 +805,12 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_
     const long long row = (long long)(t - q.c0) * a.G + h - hk * a.G;
     const int rb = (int)(row / rows_item), in = (int)(row - (long long)rb * rows_item), nb = row_blocks(q.n, a.G, rows_item);
     const int units = item_units(q.s), item = hk * nb + rb, u0 = q.pref + item * units, seen = keys_seen(q.n, q.s, a.G, rb, rows_item);
-    const int first = u0 / hdr.per, all = units > 0 && seen > 0 ? (u0 + units - 1) / hdr.per - first + 1 : 0;
+    const bool some = units > 0 && seen > 0;
+    const int first = some ? worker_of(hdr, u0) : 0, all = some ? worker_of(hdr, u0 + units - 1) - first + 1 : 0;
     // Row in the k-th worker's segment, -1: it has none.
     auto place = [&](int k) -> long long {
         if (k >= all) return -1;
-        const int from = max(0, (first + k) * hdr.per - u0), to = min(units, (first + k + 1) * hdr.per - u0);
+        const int from = max(0, unit_of(hdr, first + k) - u0), to = min(units, unit_of(hdr, first + k + 1) - u0);
         int p0, p1;
         parts_of(from, to, seen, p0, p1);
         if (p0 >= p1) return -1;
