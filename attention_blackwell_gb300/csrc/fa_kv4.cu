@@ -381,11 +381,13 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
     const uint32_t field = ex >> 26;
     const uint32_t eb[2] = {__float_as_uint(__uint_as_float(0x4b000000u | field) - 8388624.f), (143u - field) << 23};
     sts(prep + K::kExp + key * 8, eb);
-    // Pairs of keys: the even key's lane takes the first half of the groups.
-    const bool odd = lane & 1;
+    // Pairs of keys, in the order of the products' key axis (1 0 in the second and
+    // third pair of eight): the even key's lane takes the first half of the groups.
+    const bool odd = lane & 1, turned = (key >> 1 ^ key >> 2) & 1;
+    const uint32_t lo = turned ? 0x1054 : 0x5410, hi = turned ? 0x3276 : 0x7632;
     if constexpr (kG == 2) {
         const uint32_t other = __shfl_xor_sync(0xffffffffu, h[0], 1);
-        const uint32_t out[1] = {odd ? __byte_perm(other, h[0], 0x7632) : __byte_perm(h[0], other, 0x5410)};
+        const uint32_t out[1] = {odd ? __byte_perm(other, h[0], hi) : __byte_perm(h[0], other, lo)};
         sts(prep + K::kVPairs + (key >> 1) * 8 + (odd ? 4 : 0), out);
     } else {
         uint32_t out[kG / 2];
@@ -393,8 +395,8 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
         for (int i = 0; i < kG / 4; ++i) {
             const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? h[i] : h[kG / 4 + i], 1);
             const uint32_t x = odd ? other : h[i], y = odd ? h[kG / 4 + i] : other;
-            out[2 * i] = __byte_perm(x, y, 0x5410);
-            out[2 * i + 1] = __byte_perm(x, y, 0x7632);
+            out[2 * i] = __byte_perm(x, y, lo);
+            out[2 * i + 1] = __byte_perm(x, y, hi);
         }
         sts(prep + K::kVPairs + (key >> 1) * (4 * kG) + (odd ? 2 * kG : 0), out);
     }
@@ -410,6 +412,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ KvShared sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r = lane >> 2, c = lane & 3;
+    // Index i of the products' key axis is key i ^ (i >> 1) of each eight: the rows that
+    // lanes read together then lie in different banks (V's loads, in order: four
+    // wavefronts for one at d = 128, two at d = 64).
+    const int kr = r ^ (r >> 1);
     KvTables t;
     t.pref = a.B <= kTableMost ? reinterpret_cast<int*>(dsmem + K::kWarps * K::kWarp) : a.tables + (long long)blockIdx.x * (4 * a.B + 3);
     t.items = t.pref + a.B + 1;
@@ -596,8 +602,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 uint32_t kw[2][kG], ksc[2][kG];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    lds(at + (kt * 16 + r + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
-                    lds(prep + (kt * 16 + r + 8 * i) * (4 * kG), ksc[i]);
+                    lds(at + (kt * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
+                    lds(prep + (kt * 16 + kr + 8 * i) * (4 * kG), ksc[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < kG / 2; ++j) {
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 uint32_t eb[2][2];                   // of keys r and r + 8
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    lds(prep + K::kExp + (kt * 16 + r + 8 * i) * 8, eb[i]);
+                    lds(prep + K::kExp + (kt * 16 + kr + 8 * i) * 8, eb[i]);
                     back[kt][i] = __uint_as_float(eb[i][1]);
                 }
 #pragma unroll
@@ -648,7 +654,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!(here >> kt & 1u) || k0 + kt * 16 + r + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
+                            if (!(here >> kt & 1u) || k0 + kt * 16 + kr + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
             }
             // O and l follow a row's running maximum when it grows by more than kTau: only
             // then do the lanes that share the row look for it together.
@@ -704,8 +710,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 2 * c + 8 * i + y) * (D / 2) + r * (D / 16), vw[i][y]);
-                    lds(prep + K::kVPairs + (kt * 8 + c + 4 * i) * (4 * kG), vsc[i]);
+                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16), vw[i][y]);
+                    lds(prep + K::kVPairs + (kt * 8 + (c ^ (c >> 1)) + 4 * i) * (4 * kG), vsc[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < kG / 2; ++j) {
