@@ -57,12 +57,17 @@ struct PutArgs {
     long long num_slots;
 };
 
+// Two floats in a register pair: products and sums of a row's elements go two an
+// instruction (as one each, qk_rope spent half as much again on arithmetic).
+using F2 = uint64_t;
+__device__ __forceinline__ F2 both(float x) { return f2_pack(x, x); }
+
 // The lane's place in a row and its angles.
 template <int D> struct Lane {
     static constexpr int kLanes = D / 16, kRows = 32 / kLanes;   // lanes a row, rows a pass
     int a, b;            // first elements of its two chunks of eight
     bool turns;
-    float c[8], s[8];
+    F2 c[4], s[4], ns[4];    // ns = -s
     __device__ __forceinline__ void place(const RopeArgs& r, int lane) {
         const int j = lane % kLanes, m = r.rot >> 4;
         turns = j < m;
@@ -70,27 +75,39 @@ template <int D> struct Lane {
         a = (split ? j : 2 * j) * 8;
         b = (split ? j + m : 2 * j + 1) * 8;
     }
-    __device__ __forceinline__ void angles(const RopeArgs& r, int lane, int pos) {
+    // sign -1: the angles' opposites.
+    __device__ __forceinline__ void angles(const RopeArgs& r, int lane, int pos, float sign) {
         if (!turns) return;
         const long long at = (long long)pos * (r.rot >> 1) + lane % kLanes * 8;
         const float4 *pc = reinterpret_cast<const float4*>(r.cos + at), *ps = reinterpret_cast<const float4*>(r.sin + at);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float4 x = pc[i], y = ps[i];
-            c[4 * i] = x.x, c[4 * i + 1] = x.y, c[4 * i + 2] = x.z, c[4 * i + 3] = x.w;
-            s[4 * i] = y.x, s[4 * i + 1] = y.y, s[4 * i + 2] = y.z, s[4 * i + 3] = y.w;
+            c[2 * i] = f2_pack(x.x, x.y), c[2 * i + 1] = f2_pack(x.z, x.w);
+            s[2 * i] = f2_pack(sign * y.x, sign * y.y), s[2 * i + 1] = f2_pack(sign * y.z, sign * y.w);
+            ns[2 * i] = f2_pack(-sign * y.x, -sign * y.y), ns[2 * i + 1] = f2_pack(-sign * y.z, -sign * y.w);
         }
     }
-    // Every product and sum is rounded by itself, as the formula reads: a 4-bit
-    // cache's codes lie next to borders, and so a key gets the same code on every path.
-    __device__ __forceinline__ void turn(float (&v)[16], bool inter, float sign) const {
+    __device__ __forceinline__ void turn(F2 (&v)[8], bool inter) const {
         if (!turns) return;
+        if (!inter) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float x = inter ? v[2 * i] : v[i], y = inter ? v[2 * i + 1] : v[8 + i], sn = sign * s[i];
-            const float p = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, sn)), q = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, sn));
-            if (inter) v[2 * i] = p, v[2 * i + 1] = q;
-            else v[i] = p, v[8 + i] = q;
+            for (int i = 0; i < 4; ++i) {
+                const F2 x = v[i], y = v[4 + i];
+                v[i] = f2_fma(y, ns[i], f2_mul(x, c[i]));
+                v[4 + i] = f2_fma(x, s[i], f2_mul(y, c[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float c0, c1, s0, s1, x0, y0, x1, y1;
+                f2_unpack(c[i], c0, c1);
+                f2_unpack(s[i], s0, s1);
+                f2_unpack(v[2 * i], x0, y0);
+                f2_unpack(v[2 * i + 1], x1, y1);
+                v[2 * i] = f2_pack(x0 * c0 - y0 * s0, y0 * c0 + x0 * s0);
+                v[2 * i + 1] = f2_pack(x1 * c1 - y1 * s1, y1 * c1 + x1 * s1);
+            }
         }
     }
 };
@@ -100,17 +117,17 @@ __device__ __forceinline__ int position_of(const RopeArgs& r, int t) {
     return p >= 0 && p < r.max_pos ? p : -1;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& u, float* v) {
+__device__ __forceinline__ void unpack8(const uint4& u, F2* v) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const float* v) {
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint32_t pack2(F2 v) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return pack_bf16x2(x, y);
 }
+__device__ __forceinline__ uint4 pack8(const F2* v) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // Sum over the lanes of a row.
@@ -119,11 +136,19 @@ template <int L> __device__ __forceinline__ float row_sum(float x) {
     for (int o = L / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-template <int D> __device__ __forceinline__ float inv_rms(const float (&v)[16], float eps) {
-    float sum = 0.f;
+__device__ __forceinline__ float sum2(F2 v) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return x + y;
+}
+template <int D> __device__ __forceinline__ float inv_rms(const F2 (&v)[8], float eps) {
+    F2 s0 = f2_mul(v[0], v[0]), s1 = f2_mul(v[1], v[1]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum = fmaf(v[i], v[i], sum);
-    return 1.f / sqrtf(row_sum<D / 16>(sum) * (1.f / D) + eps);
+    for (int i = 2; i < 8; i += 2) {
+        s0 = f2_fma(v[i], v[i], s0);
+        s1 = f2_fma(v[i + 1], v[i + 1], s1);
+    }
+    return rsqrtf(row_sum<D / 16>(sum2(f2_add(s0, s1))) * (1.f / D) + eps);
 }
 
 // Both weights in shared memory as floats ([2][D]; rows of 1 for the one without a norm).
@@ -134,12 +159,21 @@ template <int D> __device__ __forceinline__ void stage_weights(const RopeArgs& r
         w[i] = !src ? 1.f : r.w_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(src)[e]) : static_cast<const float*>(src)[e];
     }
 }
-template <int D> __device__ __forceinline__ void weigh(float (&v)[16], float x, const float* w, const Lane<D>& me) {
+// The lane's weights (w: a row of D).
+template <int D> __device__ __forceinline__ void weights_of(const float* w, const Lane<D>& me, F2 (&out)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[i] = v[i] * x * w[me.a + i];
-        v[8 + i] = v[8 + i] * x * w[me.b + i];
+    for (int i = 0; i < 2; ++i) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(w + me.a + 4 * i), y = *reinterpret_cast<const ulonglong2*>(w + me.b + 4 * i);
+        out[2 * i] = x.x, out[2 * i + 1] = x.y;
+        out[4 + 2 * i] = y.x, out[4 + 2 * i + 1] = y.y;
     }
+}
+template <int D> __device__ __forceinline__ void weigh(F2 (&v)[8], float x, const float* w, const Lane<D>& me) {
+    F2 ww[8];
+    weights_of<D>(w, me, ww);
+    const F2 xx = both(x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = f2_mul(f2_mul(v[i], xx), ww[i]);
 }
 
 // ------------------------------------------------------------------ forward
@@ -150,7 +184,7 @@ template <int D>
 __global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
     using Me = Lane<D>;
     constexpr int kDeep = 4;
-    __shared__ float s_w[2 * D];
+    __shared__ __align__(16) float s_w[2 * D];
     grid_launch_next();
     grid_wait();
     if (r.wq || r.wk) stage_weights<D>(r, s_w);
@@ -163,7 +197,7 @@ __global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs r, const Ro
     if (pos < 0) return;
     Me me;
     me.place(r, lane);
-    me.angles(r, lane, pos);
+    me.angles(r, lane, pos, 1.f);
     const int p1 = (int)((long long)(part + 1) * r.passes / r.parts);
     for (int p = (int)((long long)part * r.passes / r.parts); p < p1; p += kDeep) {
         uint4 in[kDeep][2];
@@ -181,20 +215,20 @@ __global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs r, const Ro
             const int h = (p + i) * Me::kRows + sub;
             if (p + i >= p1) break;
             const bool real = h < rows, isq = h < r.Hq;
-            float v[16] = {};
+            F2 v[8] = {};
             if (real) {
                 unpack8(in[i][0], v);
-                unpack8(in[i][1], v + 8);
+                unpack8(in[i][1], v + 4);
             }
             if (r.wq || r.wk) {
                 const float x = inv_rms<D>(v, r.eps);
                 if (isq ? r.wq : r.wk) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
             }
-            me.turn(v, r.inter, 1.f);
+            me.turn(v, r.inter);
             if (real) {
                 __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D : a.k_out + t * a.k_out_stride + (h - r.Hq) * D;
                 *reinterpret_cast<uint4*>(dst + me.a) = pack8(v);
-                *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 8);
+                *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 4);
             }
         }
     }
@@ -212,11 +246,11 @@ __device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_b
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / Me::kLanes;
     Me me;
     me.place(r, lane);
-    float dw[16] = {};
+    F2 dw[8] = {};
     for (long long t = blockIdx.x * 8LL + warp; t < r.T; t += gridDim.x * 8LL) {
         const int pos = position_of(r, (int)t);
         if (pos < 0) continue;
-        me.angles(r, lane, pos);
+        me.angles(r, lane, pos, -1.f);
         const __nv_bfloat16 *g = gs + t * g_stride, *x = xs + t * x_stride;
         __nv_bfloat16* out = outs + t * H * D;
         for (int h0 = sub; h0 - sub < H; h0 += kDeep * Me::kRows) {
@@ -237,35 +271,37 @@ __device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_b
             for (int i = 0; i < kDeep; ++i) {
                 const int h = h0 + i * Me::kRows;
                 if (h - sub >= H) break;
-                float u[16] = {};
+                F2 u[8] = {};
                 if (h < H) {
                     unpack8(in[i][0], u);
-                    unpack8(in[i][1], u + 8);
+                    unpack8(in[i][1], u + 4);
                 }
-                me.turn(u, r.inter, -1.f);
+                me.turn(u, r.inter);
                 if (w) {
-                    float v[16] = {};
+                    F2 v[8] = {};
                     if (h < H) {
                         unpack8(in[i][2], v);
-                        unpack8(in[i][3], v + 8);
+                        unpack8(in[i][3], v + 4);
                     }
                     // With eps = 0 a missing row's r is infinite.
                     const float rms = inv_rms<D>(v, r.eps), x1 = h < H ? rms : 0.f;
-                    float sum = 0.f;
+                    const F2 xx = both(x1);
+                    F2 ww[8], sum = 0;
+                    weights_of<D>(w, me, ww);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        v[e] *= x1;                                     // x r
-                        dw[e] = fmaf(u[e], v[e], dw[e]);
-                        u[e] *= w[(e < 8 ? me.a : me.b - 8) + e];
-                        sum = fmaf(u[e], v[e], sum);
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = f2_mul(v[e], xx);                        // x r
+                        dw[e] = f2_fma(u[e], v[e], dw[e]);
+                        u[e] = f2_mul(u[e], ww[e]);
+                        sum = f2_fma(u[e], v[e], sum);
                     }
-                    sum = row_sum<D / 16>(sum) * (1.f / D);             // mean(t x) r
+                    const F2 mean = both(row_sum<D / 16>(sum2(sum)) * (-1.f / D));      // -mean(t x) r
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) u[e] = x1 * fmaf(-v[e], sum, u[e]);
+                    for (int e = 0; e < 8; ++e) u[e] = f2_mul(f2_fma(v[e], mean, u[e]), xx);
                 }
                 if (h < H) {
                     *reinterpret_cast<uint4*>(out + h * D + me.a) = pack8(u);
-                    *reinterpret_cast<uint4*>(out + h * D + me.b) = pack8(u + 8);
+                    *reinterpret_cast<uint4*>(out + h * D + me.b) = pack8(u + 4);
                 }
             }
         }
@@ -274,9 +310,12 @@ __device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_b
     // The warp's rows, then the block's warps.
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
+        float x, y;
+        f2_unpack(dw[e >> 1], x, y);
+        if (e & 1) x = y;
 #pragma unroll
-        for (int o = 16; o >= Me::kLanes; o >>= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-        if (sub == 0) s_dw[warp][(e < 8 ? me.a : me.b - 8) + e] = dw[e];
+        for (int o = 16; o >= Me::kLanes; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (sub == 0) s_dw[warp][(e < 8 ? me.a : me.b - 8) + e] = x;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += 256) {
@@ -292,7 +331,7 @@ __device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_b
 // calls give equal results.
 template <int D>
 __global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
-    __shared__ float s_w[2 * D];
+    __shared__ __align__(16) float s_w[2 * D];
     __shared__ float s_dw[8][D];
     grid_launch_next();
     grid_wait();
@@ -320,98 +359,148 @@ __global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float* partial, i
 
 // --------------------------------------------------------------------- store
 
-// Four elements of a row, from i on, normed and turned (w null: no norm; turn
-// false: as they are).  Their partners in the other half are read again (they are in
-// L1): the lanes of a 4-bit row hold elements by groups, not by pairs.
-__device__ __forceinline__ void four_of(const RopeArgs& r, const __nv_bfloat16* row, int i, float x, const float* w, bool turn,
-                                        const float* pc, const float* ps, float (&y)[4]) {
-    auto get = [&](int at, float (&v)[4]) {
-        const uint2 u = *reinterpret_cast<const uint2*>(row + at);
-        v[0] = __uint_as_float(u.x << 16), v[1] = __uint_as_float(u.x & 0xffff0000u);
-        v[2] = __uint_as_float(u.y << 16), v[3] = __uint_as_float(u.y & 0xffff0000u);
-        if (w)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = v[e] * x * w[at + e];
-    };
-    get(i, y);
-    if (!turn || i >= r.rot) return;
-    const int half = r.rot >> 1;
-    if (r.inter) {
-        const float2 c = *reinterpret_cast<const float2*>(pc + (i >> 1)), s = *reinterpret_cast<const float2*>(ps + (i >> 1));
-        const float a0 = y[0], a1 = y[2];
-        y[0] = __fsub_rn(__fmul_rn(a0, c.x), __fmul_rn(y[1], s.x));
-        y[1] = __fadd_rn(__fmul_rn(y[1], c.x), __fmul_rn(a0, s.x));
-        y[2] = __fsub_rn(__fmul_rn(a1, c.y), __fmul_rn(y[3], s.y));
-        y[3] = __fadd_rn(__fmul_rn(y[3], c.y), __fmul_rn(a1, s.y));
-        return;
-    }
-    const bool low = i < half;
-    float z[4];
-    get(low ? i + half : i - half, z);
-    const int at = low ? i : i - half;
-    const float4 c4 = *reinterpret_cast<const float4*>(pc + at), s4 = *reinterpret_cast<const float4*>(ps + at);
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float own = __fmul_rn(y[e], c[e]), other = __fmul_rn(z[e], s[e]);
-        y[e] = low ? __fsub_rn(own, other) : __fadd_rn(own, other);
-    }
+__device__ __forceinline__ float max_abs(float a, float b) {     // NaN if either is; the sign means nothing
+    float m;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
 }
 
-// A row of k or v as 4-bit codes, by eight lanes (see fa_kv4.cuh); `real`: the
-// lanes have a row.
+// Eight lanes' row y (lane l: elements 32 g + 4 l to + 3) as 4-bit codes and scales
+// (see fa_kv4.cuh).  A group's scale is worked out by one lane for all eight.
 template <int D>
-__device__ __forceinline__ void put_four(const RopeArgs& r, const __nv_bfloat16* row, bool real, const float* w, bool turn, const float* pc,
-                                         const float* ps, uint8_t* codes, uint8_t* scales, int lane) {
-    constexpr int kGroups = D / 32;
+__device__ __forceinline__ void put_codes(const F2 (&y)[D / 32][2], bool real, uint8_t* codes, uint8_t* scales, int lane) {
+    constexpr int kG = D / 32;
     const int l = lane & 7;
-    float x = 1.f;
-    if (__any_sync(0xffffffffu, w != nullptr)) {
-        float sum = 0.f;
-        if (real && w)
+    uint32_t most[kG];
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                const uint2 u = *reinterpret_cast<const uint2*>(row + 32 * g + 4 * l);
-                const float a = __uint_as_float(u.x << 16), b = __uint_as_float(u.x & 0xffff0000u), c = __uint_as_float(u.y << 16),
-                            e = __uint_as_float(u.y & 0xffff0000u);
-                sum = fmaf(a, a, fmaf(b, b, fmaf(c, c, fmaf(e, e, sum))));
-            }
-        x = 1.f / sqrtf(row_sum<8>(sum) * (1.f / D) + r.eps);
-    }
-    float y[kGroups][4];
-    uint32_t most[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        if (real) four_of(r, row, 32 * g + 4 * l, x, w, turn, pc, ps, y[g]);
-        else y[g][0] = y[g][1] = y[g][2] = y[g][3] = 0.f;
-        most[g] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) most[g] = max(most[g], __float_as_uint(y[g][e]) & 0x7fffffffu);
+    for (int g = 0; g < kG; ++g) {
+        float a, b, c, d;
+        f2_unpack(y[g][0], a, b);
+        f2_unpack(y[g][1], c, d);
+        most[g] = __float_as_uint(max_abs(max_abs(a, b), max_abs(c, d))) & 0x7fffffffu;
     }
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1)
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) most[g] = max(most[g], __shfl_xor_sync(0xffffffffu, most[g], o));
-    uint32_t out[kGroups / 2], sb[kGroups];
+        for (int g = 0; g < kG; ++g) most[g] = max(most[g], __shfl_xor_sync(0xffffffffu, most[g], o));
+    uint32_t mine = most[0];
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        sb[g] = scale_byte(most[g]);
-        const float s = scale_f32(sb[g]);
-        const uint32_t c = sb[g] == 0 || sb[g] == kScaleNaN ? 0u : codes_of(y[g], s, __frcp_rn(s));
+    for (int g = 1; g < kG; ++g) mine = l % kG == g ? most[g] : mine;
+    const uint32_t byte = scale_byte(mine);
+    const bool plain = byte != 0 && byte != kScaleNaN;       // else codes of 0
+    const float s_own = plain ? scale_f32(byte) : 0.f, inv_own = plain ? __frcp_rn(s_own) : 0.f;
+    uint32_t out[kG / 2];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        const float s = __shfl_sync(0xffffffffu, s_own, (lane & 24) + g), inv = __shfl_sync(0xffffffffu, inv_own, (lane & 24) + g);
+        float v[4];
+        f2_unpack(y[g][0], v[0], v[1]);
+        f2_unpack(y[g][1], v[2], v[3]);
+        const uint32_t c = codes_of(v, s, inv);
         out[g / 2] = g & 1 ? out[g / 2] | c << 16 : c;
     }
     if (!real) return;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(codes) + l * (kGroups / 2);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(codes) + l * (kG / 2);
     if constexpr (D == 64) *dst = out[0];
     else if constexpr (D == 128) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-    if (l == 0) {
-        if constexpr (D == 64) *reinterpret_cast<uint16_t*>(scales) = (uint16_t)(sb[0] | sb[1] << 8);
-        else
+    if (l < kG) scales[l] = (uint8_t)byte;
+}
+
+__device__ __forceinline__ void four_of(const __nv_bfloat16* p, F2 (&y)[2]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    y[0] = f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+    y[1] = f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+}
+
+// A row by eight lanes, normed where there are weights.
+template <int D>
+__device__ __forceinline__ void load_four(const RopeArgs& r, const __nv_bfloat16* row, bool real, bool norm, const float* w, int l, F2 (&y)[D / 32][2], float& x) {
+    constexpr int kG = D / 32;
 #pragma unroll
-            for (int g = 0; g < kGroups; g += 4) reinterpret_cast<uint32_t*>(scales)[g / 4] = sb[g] | sb[g + 1] << 8 | sb[g + 2] << 16 | sb[g + 3] << 24;
+    for (int g = 0; g < kG; ++g) {
+        y[g][0] = y[g][1] = 0;
+        if (real) four_of(row + 32 * g + 4 * l, y[g]);
+    }
+    if (!norm) return;
+    F2 sum = 0;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) sum = f2_fma(y[g][1], y[g][1], f2_fma(y[g][0], y[g][0], sum));
+    x = rsqrtf(row_sum<8>(sum2(sum)) * (1.f / D) + r.eps);
+    if (!w) return;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(w + 32 * g + 4 * l);
+        y[g][0] = f2_mul(f2_mul(y[g][0], both(x)), ww.x);
+        y[g][1] = f2_mul(f2_mul(y[g][1], both(x)), ww.y);
     }
 }
+
+// The rotation of a row that eight lanes hold.  Every product and sum is rounded by
+// itself, as the formula reads: codes lie next to borders, and so it is plain which
+// side a key falls on.  Whole rows in halves (the common case): a pair's two
+// elements are the same lane's, d / 2 apart, and the angles stay in registers.
+template <int D> struct Four {
+    static constexpr int kG = D / 32;
+    F2 c[kG / 2][2], s[kG / 2][2];
+    const float *pc, *ps;
+    __device__ __forceinline__ void angles(const RopeArgs& r, int pos, int l, bool whole) {
+        pc = r.cos + (long long)pos * (r.rot >> 1);
+        ps = r.sin + (long long)pos * (r.rot >> 1);
+        if (!whole) return;
+#pragma unroll
+        for (int g = 0; g < kG / 2; ++g) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(pc + 32 * g + 4 * l), y = *reinterpret_cast<const ulonglong2*>(ps + 32 * g + 4 * l);
+            c[g][0] = x.x, c[g][1] = x.y;
+            s[g][0] = y.x, s[g][1] = y.y;
+        }
+    }
+    __device__ __forceinline__ void turn_whole(F2 (&y)[kG][2]) const {
+#pragma unroll
+        for (int g = 0; g < kG / 2; ++g)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const F2 a = y[g][i], b = y[g + kG / 2][i], minus = both(-1.f);
+                y[g][i] = f2_add(f2_mul(a, c[g][i]), f2_mul(f2_mul(b, s[g][i]), minus));
+                y[g + kG / 2][i] = f2_add(f2_mul(b, c[g][i]), f2_mul(a, s[g][i]));
+            }
+    }
+    // Any other rotation: partners are read again (they are in L1).
+    __device__ __forceinline__ void turn(const RopeArgs& r, const __nv_bfloat16* row, bool real, float x, const float* w, int l, F2 (&y)[kG][2]) const {
+        const int half = r.rot >> 1;
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            const int i = 32 * g + 4 * l;
+            if (i >= r.rot || !real) continue;
+            float v[4];
+            f2_unpack(y[g][0], v[0], v[1]);
+            f2_unpack(y[g][1], v[2], v[3]);
+            if (r.inter) {
+                const float2 c2 = *reinterpret_cast<const float2*>(pc + (i >> 1)), s2 = *reinterpret_cast<const float2*>(ps + (i >> 1));
+                y[g][0] = f2_pack(__fsub_rn(__fmul_rn(v[0], c2.x), __fmul_rn(v[1], s2.x)), __fadd_rn(__fmul_rn(v[1], c2.x), __fmul_rn(v[0], s2.x)));
+                y[g][1] = f2_pack(__fsub_rn(__fmul_rn(v[2], c2.y), __fmul_rn(v[3], s2.y)), __fadd_rn(__fmul_rn(v[3], c2.y), __fmul_rn(v[2], s2.y)));
+                continue;
+            }
+            const bool low = i < half;
+            const int at = low ? i : i - half, there = low ? i + half : i - half;
+            F2 z2[2];
+            four_of(row + there, z2);
+            float z[4];
+            f2_unpack(z2[0], z[0], z[1]);
+            f2_unpack(z2[1], z[2], z[3]);
+            const float4 c4 = *reinterpret_cast<const float4*>(pc + at), s4 = *reinterpret_cast<const float4*>(ps + at);
+            const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (w) z[e] = z[e] * x * w[there + e];
+                const float own = __fmul_rn(v[e], cc[e]), other = __fmul_rn(z[e], ss[e]);
+                v[e] = low ? __fsub_rn(own, other) : __fadd_rn(own, other);
+            }
+            y[g][0] = f2_pack(v[0], v[1]);
+            y[g][1] = f2_pack(v[2], v[3]);
+        }
+    }
+};
 
 // A token's rows: q, k and v of bf16 pages in one list of passes; with 4-bit pages
 // the q rows first, then k and v, four rows a pass.
@@ -419,7 +508,7 @@ template <int D, bool kFour>
 __global__ void __launch_bounds__(256) rope_store_kernel(const RopeArgs r, const PutArgs a) {
     using Me = Lane<D>;
     constexpr int kDeep = 2;
-    __shared__ float s_w[2 * D];
+    __shared__ __align__(16) float s_w[2 * D];
     grid_launch_next();
     grid_wait();
     const bool norm = r.wq || r.wk;
@@ -435,7 +524,7 @@ __global__ void __launch_bounds__(256) rope_store_kernel(const RopeArgs r, const
     const bool keep = slot >= 0 && slot < a.num_slots;
     Me me;
     me.place(r, lane);
-    me.angles(r, lane, pos);
+    me.angles(r, lane, pos, 1.f);
     const long long page = (slot >> a.ps_log2) * r.Hkv, in_page = slot & ((1 << a.ps_log2) - 1);
     // Row of the cache that key/value head h of this token is.
     auto cell = [&](int h) { return ((page + h) << a.ps_log2) + in_page; };
@@ -459,33 +548,44 @@ __global__ void __launch_bounds__(256) rope_store_kernel(const RopeArgs r, const
             const int h = (p + i) * Me::kRows + sub;
             if (p + i >= p1) break;
             const bool real = h < rows, isq = h < r.Hq, isv = h >= r.Hq + r.Hkv;
-            float v[16] = {};
+            F2 v[8] = {};
             if (real) {
                 unpack8(in[i][0], v);
-                unpack8(in[i][1], v + 8);
+                unpack8(in[i][1], v + 4);
             }
             if (norm) {
                 const float x = inv_rms<D>(v, r.eps);
                 if (!isv && (isq ? r.wq : r.wk)) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
             }
-            if (!isv) me.turn(v, r.inter, 1.f);
+            if (!isv) me.turn(v, r.inter);
             if (!real || !(isq || keep)) continue;
             __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D
                                      : reinterpret_cast<__nv_bfloat16*>(isv ? a.vp : a.kp) + cell(h - r.Hq - (isv ? r.Hkv : 0)) * D;
             *reinterpret_cast<uint4*>(dst + me.a) = isv ? in[i][0] : pack8(v);
-            *reinterpret_cast<uint4*>(dst + me.b) = isv ? in[i][1] : pack8(v + 8);
+            *reinterpret_cast<uint4*>(dst + me.b) = isv ? in[i][1] : pack8(v + 4);
         }
     }
     if constexpr (kFour) {
         if (!keep) return;
-        const float *pc = r.cos + (long long)pos * (r.rot >> 1), *ps = r.sin + (long long)pos * (r.rot >> 1);
+        const int l = lane & 7;
+        const bool whole = r.rot == D && !r.inter;
+        Four<D> turner;
+        turner.angles(r, pos, l, whole);
         for (int p = max(p0, first); p < p1; ++p) {
             const int h = (p - first) * 4 + (lane >> 3);
             const bool real = h < 2 * r.Hkv, isk = h < r.Hkv;
             const int hk = !real ? 0 : isk ? h : h - r.Hkv;
-            const long long c = cell(hk);
-            put_four<D>(r, isk ? a.k + t * a.k_stride + hk * D : a.v + t * a.v_stride + hk * D, real, isk && r.wk ? s_w + D : nullptr, isk, pc, ps,
-                        (isk ? a.kp : a.vp) + c * (D / 2), (isk ? a.ks : a.vs) + c * (D / 32), lane);
+            const long long at = cell(hk);
+            const __nv_bfloat16* row = isk ? a.k + t * a.k_stride + hk * D : a.v + t * a.v_stride + hk * D;
+            const float* w = isk && r.wk ? s_w + D : nullptr;
+            F2 y[D / 32][2];
+            float x = 1.f;
+            load_four<D>(r, row, real, r.wk != nullptr, w, l, y, x);
+            if (isk) {
+                if (whole) turner.turn_whole(y);
+                else turner.turn(r, row, real, x, w, l, y);
+            }
+            put_codes<D>(y, real, (isk ? a.kp : a.vp) + at * (D / 2), (isk ? a.ks : a.vs) + at * (D / 32), lane);
         }
     }
 }
