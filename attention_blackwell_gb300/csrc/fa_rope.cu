@@ -10,12 +10,17 @@
 //   dx = r (t - x r^2 mean(t x)),   dw = sum over rows of u x r.
 // All of it in 32 bits, rounded once where it is stored.
 //
-// Layout: a warp takes one token, d / 16 lanes a head's row, so that a lane's 16
-// elements are whole pairs whatever rot is: two 16-byte chunks, and the eight
-// angles that the lane needs are the same for every head.  They stay in registers
-// while the warp goes over the token's heads.
+// A unit is up to kChunk rows of one token's q, k or v, which are adjacent in memory,
+// with its rows of the cos and sin tables.  Every warp has a ring of units in shared
+// memory, filled by bulk copies (what is in flight costs no registers; loaded into
+// registers ahead, the same work moved 4.6 TB/s at its best), and takes every
+// W-th unit of the call.  d / 16 lanes share a row, so that a lane's 16 elements are
+// whole pairs whatever rot is: two 16-byte chunks.
 #include <math.h>
 #include <stdint.h>
+
+#include <atomic>
+#include <type_traits>
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
@@ -31,7 +36,8 @@ struct RopeArgs {
     const void *wq, *wk;         // [d] float or bf16, null: no norm
     int T, Hq, Hkv, max_pos, rot, inter, seq_len, w_bf16;
     float eps;
-    int passes, parts;           // passes over a token's rows, warps that share a token
+    int per_q, per_k, per;       // units of a token's q rows, of its k (and v) rows, of all
+    DevStatus* status;
 };
 
 struct RowsArgs {
@@ -75,11 +81,10 @@ template <int D> struct Lane {
         a = (split ? j : 2 * j) * 8;
         b = (split ? j + m : 2 * j + 1) * 8;
     }
-    // sign -1: the angles' opposites.
-    __device__ __forceinline__ void angles(const RopeArgs& r, int lane, int pos, float sign) {
+    // From the unit's rows of the tables; sign -1: the angles' opposites.
+    __device__ __forceinline__ void angles(const RopeArgs& r, const float* table, int lane, float sign) {
         if (!turns) return;
-        const long long at = (long long)pos * (r.rot >> 1) + lane % kLanes * 8;
-        const float4 *pc = reinterpret_cast<const float4*>(r.cos + at), *ps = reinterpret_cast<const float4*>(r.sin + at);
+        const float4 *pc = reinterpret_cast<const float4*>(table + lane % kLanes * 8), *ps = reinterpret_cast<const float4*>(table + (r.rot >> 1) + lane % kLanes * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float4 x = pc[i], y = ps[i];
@@ -128,7 +133,7 @@ __device__ __forceinline__ uint32_t pack2(F2 v) {
     return pack_bf16x2(x, y);
 }
 __device__ __forceinline__ uint4 pack8(const F2* v) { return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3])); }
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint4 load16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
 
 // Sum over the lanes of a row.
 template <int L> __device__ __forceinline__ float row_sum(float x) {
@@ -176,170 +181,296 @@ template <int D> __device__ __forceinline__ void weigh(F2 (&v)[8], float x, cons
     for (int i = 0; i < 8; ++i) v[i] = f2_mul(f2_mul(v[i], xx), ww[i]);
 }
 
+// ------------------------------------------------------------------ the units
+
+// What a unit is, at the head of its slot.
+struct __align__(16) Unit {
+    int t, j, pos, slot;     // token, unit of the token, position, slot of the cache
+};
+
+// A warp's ring of units: kArrays arrays of kBytes (the rows), the tables' rows.
+template <int D, int kBytes, int kArrays, int kRing> struct Feed {
+    static constexpr uint32_t kTable = 16 + kArrays * kBytes, kSlot = kTable + D * 4, kWarp = kRing * kSlot;
+    static_assert(kSlot % 16 == 0 && kRing <= 4, "copies are 16-byte aligned");
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Calls work(unit, slot) for this warp's units.  rows(t, j, array, bytes) is where
+// a unit's rows are and how many bytes of them.
+template <int D, int kBytes, int kArrays, int kRing, class Rows, class Work>
+__device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t* full, const int* slots, const Rows& rows, const Work& work) {
+    using F = Feed<D, kBytes, kArrays, kRing>;
+    const int lane = threadIdx.x & 31;
+    const long long first = blockIdx.x * 8LL + (threadIdx.x >> 5), step = gridDim.x * 8LL, all = (long long)r.T * r.per;
+    const long long n = first < all ? (all - first + step - 1) / step : 0;
+    // The units that the copies come to next, 32 at a time, one a lane, and the 32 after them.
+    auto fetch = [&](long long k) {
+        Unit u = {0, 0, -1, 0};
+        if (k + lane < n) {
+            const long long id = first + (k + lane) * step;
+            u.t = (int)(id / r.per);
+            u.j = (int)(id - (long long)u.t * r.per);
+            u.pos = position_of(r, u.t);
+            u.slot = slots ? slots[u.t] : 0;
+        }
+        return u;
+    };
+    Unit now = fetch(0), next = fetch(32);
+    long long k = 0;
+    uint32_t filled = 0, issued = 0;
+    auto copy = [&]() {
+        Unit u;
+        do {                                         // tokens off the tables are passed over
+            if (k >= n) return;
+            if (k && (k & 31) == 0) {
+                now = next;
+                next = fetch(k + 32);
+            }
+            const int i = (int)k & 31;
+            u.pos = __shfl_sync(0xffffffffu, now.pos, i);
+            u.t = __shfl_sync(0xffffffffu, now.t, i);
+            u.j = __shfl_sync(0xffffffffu, now.j, i);
+            u.slot = __shfl_sync(0xffffffffu, now.slot, i);
+            ++k;
+        } while (u.pos < 0);
+        uint8_t* to = ring + filled * F::kSlot;
+        uint64_t* bar = &full[filled];
+        uint32_t bytes = 0;
+        const uint8_t* from = nullptr;
+        if (lane < kArrays) from = rows(u.t, u.j, lane, bytes);
+        else if (lane < kArrays + 2) {
+            bytes = r.rot * 2;
+            from = reinterpret_cast<const uint8_t*>((lane == kArrays ? r.cos : r.sin) + (long long)u.pos * (r.rot >> 1));
+        }
+        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        __syncwarp();                                // every lane has read what the slot held
+        if (lane == 0) {
+            *reinterpret_cast<Unit*>(to) = u;
+            mbar_arrive_expect_tx(bar, total);
+        }
+        __syncwarp();
+        if (bytes) bulk_load(smem_u32(to) + (lane < kArrays ? 16 + lane * kBytes : F::kTable + (lane - kArrays) * r.rot * 2), from, bytes, bar);
+        filled = filled + 1 == kRing ? 0 : filled + 1;
+        ++issued;
+    };
+    for (int i = 0; i < kRing; ++i) copy();
+    uint32_t slot = 0, phase = 0;
+    for (uint32_t done = 0; done != issued; ++done) {
+        // The bounded wait (2 s); after one that gave up, the copies in flight get as long again.
+        const uint32_t bar = smem_u32(&full[slot]);
+        bool ok = mbar_try_wait(bar, phase);
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!(ok = mbar_try_wait(bar, phase)) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+        }
+        if (!__all_sync(0xffffffffu, ok)) {
+            if (lane == 0 && atomicCAS(&r.status->code, 0, kStatusTimeout) == 0) {
+                r.status->where = 121;
+                r.status->block = blockIdx.x;
+            }
+            const uint64_t t0 = globaltimer_ns();
+            for (; done != issued; ++done) {
+                while (!mbar_try_wait(smem_u32(&full[slot]), phase) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+                if (++slot == kRing) slot = 0, phase ^= 1;
+            }
+            return;
+        }
+        const uint8_t* at = ring + slot * F::kSlot;
+        work(*reinterpret_cast<const Unit*>(at), at + 16, reinterpret_cast<const float*>(at + F::kTable));
+        if (++slot == kRing) slot = 0, phase ^= 1;
+        __syncwarp();
+        copy();
+    }
+}
+
+// Which rows of a token unit j is: of q (0), k (1) or v (2), from row h0 on, n of them.
+struct Chunk {
+    int what, h0, n;
+};
+template <int kChunk> __device__ __forceinline__ Chunk chunk_of(const RopeArgs& r, int j) {
+    Chunk c;
+    c.what = j < r.per_q ? 0 : j < r.per_q + r.per_k ? 1 : 2;
+    c.h0 = (c.what == 0 ? j : c.what == 1 ? j - r.per_q : j - r.per_q - r.per_k) * kChunk;
+    c.n = min(kChunk, (c.what == 0 ? r.Hq : r.Hkv) - c.h0);
+    return c;
+}
+
+// Bytes of rows a unit, and the rows: two passes of 32 lanes; one in the backward
+// pass, whose units hold two arrays.
+constexpr int kBytes = 2048, kBytesGrad = 1024, kRing = 4;
+template <int D> constexpr int kChunk = kBytes / (2 * D);
+template <int D> constexpr int kChunkGrad = kBytesGrad / (2 * D);
+template <int D> constexpr uint32_t kSmem = 8 * Feed<D, kBytes, 1, kRing>::kWarp;
+template <int D> constexpr uint32_t kSmemGrad = 8 * Feed<D, kBytesGrad, 2, kRing>::kWarp;
+
+// The block's barriers, before the kernel it depends on is done.
+__device__ __forceinline__ void init_barriers(uint64_t (&full)[8][kRing]) {
+    if (threadIdx.x < 8 * kRing) {
+        mbar_init(&full[0][0] + threadIdx.x, 1);
+        fence_mbar_init();
+    }
+}
+
 // ------------------------------------------------------------------ forward
 
-// One pass: kRows rows, from the list of the token's q and k rows.  kDeep passes'
-// loads are made before the first is worked on.
-template <int D>
-__global__ void __launch_bounds__(256) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
+// A unit's rows of q or k, normed and turned, to out(row).
+template <int D, class Out>
+__device__ __forceinline__ void turn_rows(const RopeArgs& r, Lane<D>& me, const Chunk& c, const uint8_t* in, const float* table, const float* s_w, const Out& out) {
     using Me = Lane<D>;
-    constexpr int kDeep = 4;
+    const int lane = threadIdx.x & 31, sub = lane / Me::kLanes;
+    const bool norm = c.what ? r.wk != nullptr : r.wq != nullptr;
+    me.angles(r, table, lane, 1.f);
+#pragma unroll
+    for (int p = 0; p < kChunk<D> / Me::kRows; ++p) {
+        const int i = p * Me::kRows + sub;
+        if (p * Me::kRows >= c.n) break;
+        F2 v[8] = {};
+        if (i < c.n) {
+            unpack8(load16(in + (i * D + me.a) * 2), v);
+            unpack8(load16(in + (i * D + me.b) * 2), v + 4);
+        }
+        if (norm) weigh<D>(v, inv_rms<D>(v, r.eps), s_w + (c.what ? D : 0), me);
+        me.turn(v, r.inter);
+        if (i < c.n) {
+            __nv_bfloat16* dst = out(c.h0 + i);
+            *reinterpret_cast<uint4*>(dst + me.a) = pack8(v);
+            *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 4);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(256, 2) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
+    extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ __align__(16) float s_w[2 * D];
+    __shared__ uint64_t full[8][kRing];
+    init_barriers(full);
     grid_launch_next();
     grid_wait();
     if (r.wq || r.wk) stage_weights<D>(r, s_w);
     __syncthreads();
-    const int lane = threadIdx.x & 31, sub = lane / Me::kLanes, rows = r.Hq + r.Hkv;
-    const long long warp = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    const int t = (int)(warp / r.parts), part = (int)(warp % r.parts);
-    if (t >= r.T) return;
-    const int pos = position_of(r, t);
-    if (pos < 0) return;
-    Me me;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Lane<D> me;
     me.place(r, lane);
-    me.angles(r, lane, pos, 1.f);
-    const int p1 = (int)((long long)(part + 1) * r.passes / r.parts);
-    for (int p = (int)((long long)part * r.passes / r.parts); p < p1; p += kDeep) {
-        uint4 in[kDeep][2];
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int h = (p + i) * Me::kRows + sub;
-            if (p + i < p1 && h < rows) {
-                const __nv_bfloat16* src = h < r.Hq ? a.q + t * a.q_stride + h * D : a.k + t * a.k_stride + (h - r.Hq) * D;
-                in[i][0] = load16(src + me.a);
-                in[i][1] = load16(src + me.b);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int h = (p + i) * Me::kRows + sub;
-            if (p + i >= p1) break;
-            const bool real = h < rows, isq = h < r.Hq;
-            F2 v[8] = {};
-            if (real) {
-                unpack8(in[i][0], v);
-                unpack8(in[i][1], v + 4);
-            }
-            if (r.wq || r.wk) {
-                const float x = inv_rms<D>(v, r.eps);
-                if (isq ? r.wq : r.wk) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
-            }
-            me.turn(v, r.inter);
-            if (real) {
-                __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D : a.k_out + t * a.k_out_stride + (h - r.Hq) * D;
-                *reinterpret_cast<uint4*>(dst + me.a) = pack8(v);
-                *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 4);
-            }
-        }
-    }
+    auto rows = [&](int t, int j, int, uint32_t& bytes) {
+        const Chunk c = chunk_of<kChunk<D>>(r, j);
+        bytes = c.n * D * 2;
+        return reinterpret_cast<const uint8_t*>((c.what ? a.k + t * a.k_stride : a.q + t * a.q_stride) + c.h0 * D);
+    };
+    feed<D, kBytes, 1, kRing>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], nullptr, rows,
+                              [&](const Unit& u, const uint8_t* in, const float* table) {
+        const Chunk c = chunk_of<kChunk<D>>(r, u.j);
+        __nv_bfloat16* to = c.what ? a.k_out + u.t * a.k_out_stride : a.q_out + u.t * a.q_out_stride;
+        turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
+    });
 }
 
 // ----------------------------------------------------------------- gradients
 
-// One operand's rows (q or k): the warps go over the tokens; each block leaves its
-// sum of the weight's gradient in `partial`.
+// A pass over rows of q or k; dw: the lane's share of the weight's gradient.
 template <int D>
-__device__ __forceinline__ void grad_rows(const RopeArgs& r, int H, const __nv_bfloat16* gs, long long g_stride, const __nv_bfloat16* xs,
-                                          long long x_stride, __nv_bfloat16* outs, const float* w, float (&s_dw)[8][D], float* partial) {
+__device__ __forceinline__ void grad_row(const RopeArgs& r, const Lane<D>& me, bool real, const uint8_t* g, const uint8_t* x, const float* w, F2 (&dw)[8], __nv_bfloat16* out) {
+    F2 u[8] = {};
+    if (real) {
+        unpack8(load16(g + me.a * 2), u);
+        unpack8(load16(g + me.b * 2), u + 4);
+    }
+    me.turn(u, r.inter);
+    if (w) {
+        F2 v[8] = {};
+        if (real) {
+            unpack8(load16(x + me.a * 2), v);
+            unpack8(load16(x + me.b * 2), v + 4);
+        }
+        // With eps = 0 a missing row's r is infinite.
+        const float rms = inv_rms<D>(v, r.eps), x1 = real ? rms : 0.f;
+        const F2 xx = both(x1);
+        F2 ww[8], sum = 0;
+        weights_of<D>(w, me, ww);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            v[e] = f2_mul(v[e], xx);                        // x r
+            dw[e] = f2_fma(u[e], v[e], dw[e]);
+            u[e] = f2_mul(u[e], ww[e]);
+            sum = f2_fma(u[e], v[e], sum);
+        }
+        const F2 mean = both(row_sum<D / 16>(sum2(sum)) * (-1.f / D));      // -mean(t x) r
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = f2_mul(f2_fma(v[e], mean, u[e]), xx);
+    }
+    if (real) {
+        *reinterpret_cast<uint4*>(out + me.a) = pack8(u);
+        *reinterpret_cast<uint4*>(out + me.b) = pack8(u + 4);
+    }
+}
+
+// Each block leaves its sums of the weights' gradients, which a second kernel adds up
+// in the blocks' order, so equal calls give equal results.
+template <int D>
+__global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
     using Me = Lane<D>;
-    constexpr int kDeep = 2;
+    extern __shared__ __align__(16) uint8_t dsmem[];
+    __shared__ __align__(16) float s_w[2 * D];
+    __shared__ uint64_t full[8][kRing];
+    init_barriers(full);
+    grid_launch_next();
+    grid_wait();
+    const bool norm = r.wq || r.wk;
+    if (norm) stage_weights<D>(r, s_w);
+    __syncthreads();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / Me::kLanes;
     Me me;
     me.place(r, lane);
-    F2 dw[8] = {};
-    for (long long t = blockIdx.x * 8LL + warp; t < r.T; t += gridDim.x * 8LL) {
-        const int pos = position_of(r, (int)t);
-        if (pos < 0) continue;
-        me.angles(r, lane, pos, -1.f);
-        const __nv_bfloat16 *g = gs + t * g_stride, *x = xs + t * x_stride;
-        __nv_bfloat16* out = outs + t * H * D;
-        for (int h0 = sub; h0 - sub < H; h0 += kDeep * Me::kRows) {
-            uint4 in[kDeep][4];
-#pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
-                const int h = h0 + i * Me::kRows;
-                if (h < H) {
-                    in[i][0] = load16(g + h * D + me.a);
-                    in[i][1] = load16(g + h * D + me.b);
-                    if (w) {
-                        in[i][2] = load16(x + h * D + me.a);
-                        in[i][3] = load16(x + h * D + me.b);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
-                const int h = h0 + i * Me::kRows;
-                if (h - sub >= H) break;
-                F2 u[8] = {};
-                if (h < H) {
-                    unpack8(in[i][0], u);
-                    unpack8(in[i][1], u + 4);
-                }
-                me.turn(u, r.inter);
-                if (w) {
-                    F2 v[8] = {};
-                    if (h < H) {
-                        unpack8(in[i][2], v);
-                        unpack8(in[i][3], v + 4);
-                    }
-                    // With eps = 0 a missing row's r is infinite.
-                    const float rms = inv_rms<D>(v, r.eps), x1 = h < H ? rms : 0.f;
-                    const F2 xx = both(x1);
-                    F2 ww[8], sum = 0;
-                    weights_of<D>(w, me, ww);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] = f2_mul(v[e], xx);                        // x r
-                        dw[e] = f2_fma(u[e], v[e], dw[e]);
-                        u[e] = f2_mul(u[e], ww[e]);
-                        sum = f2_fma(u[e], v[e], sum);
-                    }
-                    const F2 mean = both(row_sum<D / 16>(sum2(sum)) * (-1.f / D));      // -mean(t x) r
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = f2_mul(f2_fma(v[e], mean, u[e]), xx);
-                }
-                if (h < H) {
-                    *reinterpret_cast<uint4*>(out + h * D + me.a) = pack8(u);
-                    *reinterpret_cast<uint4*>(out + h * D + me.b) = pack8(u + 4);
-                }
-            }
-        }
-    }
-    if (!w) return;
-    // The warp's rows, then the block's warps.
+    F2 dwq[8] = {}, dwk[8] = {};
+    auto rows = [&](int t, int j, int array, uint32_t& bytes) {
+        const Chunk c = chunk_of<kChunkGrad<D>>(r, j);
+        bytes = array && !(c.what ? r.wk : r.wq) ? 0 : c.n * D * 2;
+        const __nv_bfloat16* p = c.what ? (array ? a.k + t * a.k_stride : a.gk + t * a.gk_stride) : array ? a.q + t * a.q_stride : a.gq + t * a.gq_stride;
+        return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
+    };
+    feed<D, kBytesGrad, 2, kRing>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRing>::kWarp, full[warp], nullptr, rows,
+                                  [&](const Unit& u, const uint8_t* in, const float* table) {
+        const Chunk c = chunk_of<kChunkGrad<D>>(r, u.j);
+        me.angles(r, table, lane, -1.f);
+        const bool real = sub < c.n;
+        const uint8_t *g = in + sub * D * 2, *x = g + kBytesGrad;
+        const long long row = (long long)(c.h0 + sub) * D;
+        if (c.what == 0) grad_row<D>(r, me, real, g, x, r.wq ? s_w : nullptr, dwq, a.dq + (long long)u.t * r.Hq * D + row);
+        else grad_row<D>(r, me, real, g, x, r.wk ? s_w + D : nullptr, dwk, a.dk + (long long)u.t * r.Hkv * D + row);
+    });
+    if (!norm) return;
+    // The warp's rows, then the block's warps; the rings are done with.
+    __syncthreads();
+    float (*s_dw)[2 * D] = reinterpret_cast<float (*)[2 * D]>(dsmem);
+    static_assert(8 * 2 * D * 4 <= kSmemGrad<D>, "room for the sums");
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        float x, y;
-        f2_unpack(dw[e >> 1], x, y);
-        if (e & 1) x = y;
+        float q[2], k[2];
+        f2_unpack(dwq[e >> 1], q[0], q[1]);
+        f2_unpack(dwk[e >> 1], k[0], k[1]);
+        float x = q[e & 1], y = k[e & 1];
 #pragma unroll
-        for (int o = 16; o >= Me::kLanes; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (sub == 0) s_dw[warp][(e < 8 ? me.a : me.b - 8) + e] = x;
+        for (int o = 16; o >= Me::kLanes; o >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, o);
+            y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if (sub == 0) {
+            const int i = (e < 8 ? me.a : me.b - 8) + e;
+            s_dw[warp][i] = x;
+            s_dw[warp][D + i] = y;
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < D; i += 256) {
+    for (int i = threadIdx.x; i < 2 * D; i += 256) {
         float sum = s_dw[0][i];
 #pragma unroll
         for (int y = 1; y < 8; ++y) sum += s_dw[y][i];
-        partial[i] = sum;
+        a.partial[(long long)blockIdx.x * (2 * D) + i] = sum;
     }
-    __syncthreads();
-}
-
-// The blocks' sums are added up by a second kernel in the blocks' order, so equal
-// calls give equal results.
-template <int D>
-__global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
-    __shared__ __align__(16) float s_w[2 * D];
-    __shared__ float s_dw[8][D];
-    grid_launch_next();
-    grid_wait();
-    if (r.wq || r.wk) stage_weights<D>(r, s_w);
-    __syncthreads();
-    float* partial = a.partial + (long long)blockIdx.x * (2 * D);
-    grad_rows<D>(r, r.Hq, a.gq, a.gq_stride, a.q, a.q_stride, a.dq, r.wq ? s_w : nullptr, s_dw, partial);
-    grad_rows<D>(r, r.Hkv, a.gk, a.gk_stride, a.k, a.k_stride, a.dk, r.wk ? s_w + D : nullptr, s_dw, partial + D);
 }
 
 // 32 columns of the blocks' sums a block, eight rows at a time.
@@ -407,27 +538,22 @@ __device__ __forceinline__ void put_codes(const F2 (&y)[D / 32][2], bool real, u
     if (l < kG) scales[l] = (uint8_t)byte;
 }
 
-__device__ __forceinline__ void four_of(const __nv_bfloat16* p, F2 (&y)[2]) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ void unpack4(const uint2& u, F2 (&y)[2]) {
     y[0] = f2_pack(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
     y[1] = f2_pack(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
 // A row by eight lanes, normed where there are weights.
 template <int D>
-__device__ __forceinline__ void load_four(const RopeArgs& r, const __nv_bfloat16* row, bool real, bool norm, const float* w, int l, F2 (&y)[D / 32][2], float& x) {
+__device__ __forceinline__ void norm_four(const RopeArgs& r, const uint8_t* row, bool norm, const float* w, int l, F2 (&y)[D / 32][2], float& x) {
     constexpr int kG = D / 32;
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-        y[g][0] = y[g][1] = 0;
-        if (real) four_of(row + 32 * g + 4 * l, y[g]);
-    }
+    for (int g = 0; g < kG; ++g) unpack4(*reinterpret_cast<const uint2*>(row + (32 * g + 4 * l) * 2), y[g]);
     if (!norm) return;
     F2 sum = 0;
 #pragma unroll
     for (int g = 0; g < kG; ++g) sum = f2_fma(y[g][1], y[g][1], f2_fma(y[g][0], y[g][0], sum));
     x = rsqrtf(row_sum<8>(sum2(sum)) * (1.f / D) + r.eps);
-    if (!w) return;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
         const ulonglong2 ww = *reinterpret_cast<const ulonglong2*>(w + 32 * g + 4 * l);
@@ -443,10 +569,10 @@ __device__ __forceinline__ void load_four(const RopeArgs& r, const __nv_bfloat16
 template <int D> struct Four {
     static constexpr int kG = D / 32;
     F2 c[kG / 2][2], s[kG / 2][2];
-    const float *pc, *ps;
-    __device__ __forceinline__ void angles(const RopeArgs& r, int pos, int l, bool whole) {
-        pc = r.cos + (long long)pos * (r.rot >> 1);
-        ps = r.sin + (long long)pos * (r.rot >> 1);
+    const float *pc, *ps;    // the unit's rows of the tables
+    __device__ __forceinline__ void angles(const RopeArgs& r, const float* table, int l, bool whole) {
+        pc = table;
+        ps = table + (r.rot >> 1);
         if (!whole) return;
 #pragma unroll
         for (int g = 0; g < kG / 2; ++g) {
@@ -465,13 +591,13 @@ template <int D> struct Four {
                 y[g + kG / 2][i] = f2_add(f2_mul(b, c[g][i]), f2_mul(a, s[g][i]));
             }
     }
-    // Any other rotation: partners are read again (they are in L1).
-    __device__ __forceinline__ void turn(const RopeArgs& r, const __nv_bfloat16* row, bool real, float x, const float* w, int l, F2 (&y)[kG][2]) const {
+    // Any other rotation: partners are read again.
+    __device__ __forceinline__ void turn(const RopeArgs& r, const uint8_t* row, float x, const float* w, int l, F2 (&y)[kG][2]) const {
         const int half = r.rot >> 1;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
             const int i = 32 * g + 4 * l;
-            if (i >= r.rot || !real) continue;
+            if (i >= r.rot) continue;
             float v[4];
             f2_unpack(y[g][0], v[0], v[1]);
             f2_unpack(y[g][1], v[2], v[3]);
@@ -484,7 +610,7 @@ template <int D> struct Four {
             const bool low = i < half;
             const int at = low ? i : i - half, there = low ? i + half : i - half;
             F2 z2[2];
-            four_of(row + there, z2);
+            unpack4(*reinterpret_cast<const uint2*>(row + there * 2), z2);
             float z[4];
             f2_unpack(z2[0], z[0], z[1]);
             f2_unpack(z2[1], z[2], z[3]);
@@ -502,92 +628,72 @@ template <int D> struct Four {
     }
 };
 
-// A token's rows: q, k and v of bf16 pages in one list of passes; with 4-bit pages
-// the q rows first, then k and v, four rows a pass.
+// Rows of k or v into 4-bit pages, four rows a pass.
+template <int D>
+__device__ __forceinline__ void put_rows(const RopeArgs& r, const PutArgs& a, const Chunk& c, const uint8_t* in, const float* table, const float* s_w, long long cell) {
+    const int lane = threadIdx.x & 31, l = lane & 7;
+    const bool isk = c.what == 1, norm = isk && r.wk != nullptr, whole = r.rot == D && !r.inter;
+    const float* w = s_w + D;
+    Four<D> turner;
+    if (isk) turner.angles(r, table, l, whole);
+#pragma unroll 1
+    for (int i = lane >> 3; i - (lane >> 3) < c.n; i += 4) {
+        const bool real = i < c.n;
+        const uint8_t* row = in + (real ? i : 0) * (D * 2);
+        F2 y[D / 32][2];
+        float x = 1.f;
+        norm_four<D>(r, row, norm, w, l, y, x);
+        if (isk) {
+            if (whole) turner.turn_whole(y);
+            else turner.turn(r, row, x, norm ? w : nullptr, l, y);
+        }
+        const long long at = cell + ((long long)(c.h0 + i) << a.ps_log2);
+        put_codes<D>(y, real, (isk ? a.kp : a.vp) + at * (D / 2), (isk ? a.ks : a.vs) + at * (D / 32), lane);
+    }
+}
+
 template <int D, bool kFour>
-__global__ void __launch_bounds__(256) rope_store_kernel(const RopeArgs r, const PutArgs a) {
+__global__ void __launch_bounds__(256, 2) rope_store_kernel(const RopeArgs r, const PutArgs a) {
     using Me = Lane<D>;
-    constexpr int kDeep = 2;
+    extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ __align__(16) float s_w[2 * D];
+    __shared__ uint64_t full[8][kRing];
+    init_barriers(full);
     grid_launch_next();
     grid_wait();
-    const bool norm = r.wq || r.wk;
-    if (norm) stage_weights<D>(r, s_w);
+    if (r.wq || r.wk) stage_weights<D>(r, s_w);
     __syncthreads();
-    const int lane = threadIdx.x & 31, sub = lane / Me::kLanes;
-    const long long warp = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    const int t = (int)(warp / r.parts), part = (int)(warp % r.parts);
-    if (t >= r.T) return;
-    const int pos = position_of(r, t);
-    const long long slot = a.slots[t];
-    if (pos < 0) return;
-    const bool keep = slot >= 0 && slot < a.num_slots;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Me me;
     me.place(r, lane);
-    me.angles(r, lane, pos, 1.f);
-    const long long page = (slot >> a.ps_log2) * r.Hkv, in_page = slot & ((1 << a.ps_log2) - 1);
-    // Row of the cache that key/value head h of this token is.
-    auto cell = [&](int h) { return ((page + h) << a.ps_log2) + in_page; };
-    const int rows = kFour ? r.Hq : r.Hq + 2 * r.Hkv, first = (rows + Me::kRows - 1) / Me::kRows;
-    const int p0 = (int)((long long)part * r.passes / r.parts), p1 = (int)((long long)(part + 1) * r.passes / r.parts);
-    for (int p = p0; p < min(p1, first); p += kDeep) {
-        uint4 in[kDeep][2];
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int h = (p + i) * Me::kRows + sub;
-            if (p + i < p1 && h < rows) {
-                const __nv_bfloat16* src = h < r.Hq            ? a.q + t * a.q_stride + h * D
-                                           : h < r.Hq + r.Hkv ? a.k + t * a.k_stride + (h - r.Hq) * D
-                                                               : a.v + t * a.v_stride + (h - r.Hq - r.Hkv) * D;
-                in[i][0] = load16(src + me.a);
-                in[i][1] = load16(src + me.b);
-            }
+    auto rows = [&](int t, int j, int, uint32_t& bytes) {
+        const Chunk c = chunk_of<kChunk<D>>(r, j);
+        bytes = c.n * D * 2;
+        const __nv_bfloat16* p = c.what == 0 ? a.q + t * a.q_stride : c.what == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
+        return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
+    };
+    feed<D, kBytes, 1, kRing>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], a.slots, rows,
+                              [&](const Unit& u, const uint8_t* in, const float* table) {
+        const Chunk c = chunk_of<kChunk<D>>(r, u.j);
+        if (c.what == 0) {
+            __nv_bfloat16* to = a.q_out + u.t * a.q_out_stride;
+            turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
+            return;
         }
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int h = (p + i) * Me::kRows + sub;
-            if (p + i >= p1) break;
-            const bool real = h < rows, isq = h < r.Hq, isv = h >= r.Hq + r.Hkv;
-            F2 v[8] = {};
-            if (real) {
-                unpack8(in[i][0], v);
-                unpack8(in[i][1], v + 4);
-            }
-            if (norm) {
-                const float x = inv_rms<D>(v, r.eps);
-                if (!isv && (isq ? r.wq : r.wk)) weigh<D>(v, x, s_w + (isq ? 0 : D), me);
-            }
-            if (!isv) me.turn(v, r.inter);
-            if (!real || !(isq || keep)) continue;
-            __nv_bfloat16* dst = isq ? a.q_out + t * a.q_out_stride + h * D
-                                     : reinterpret_cast<__nv_bfloat16*>(isv ? a.vp : a.kp) + cell(h - r.Hq - (isv ? r.Hkv : 0)) * D;
-            *reinterpret_cast<uint4*>(dst + me.a) = isv ? in[i][0] : pack8(v);
-            *reinterpret_cast<uint4*>(dst + me.b) = isv ? in[i][1] : pack8(v + 4);
+        if (u.slot < 0 || u.slot >= a.num_slots) return;
+        // Row of the cache that this token's head 0 is; head h is h pages of rows behind.
+        const long long cell = (((long long)(u.slot >> a.ps_log2) * r.Hkv) << a.ps_log2) + (u.slot & ((1 << a.ps_log2) - 1));
+        if constexpr (kFour) {
+            put_rows<D>(r, a, c, in, table, s_w, cell);
+        } else if (c.what == 1) {
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(a.kp);
+            turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + (cell + ((long long)h << a.ps_log2)) * D; });
+        } else {
+            uint4* to = reinterpret_cast<uint4*>(a.vp);
+            for (int i = lane; i < c.n * (D / 8); i += 32)
+                to[(cell + ((long long)(c.h0 + i / (D / 8)) << a.ps_log2)) * (D / 8) + i % (D / 8)] = load16(in + i * 16);
         }
-    }
-    if constexpr (kFour) {
-        if (!keep) return;
-        const int l = lane & 7;
-        const bool whole = r.rot == D && !r.inter;
-        Four<D> turner;
-        turner.angles(r, pos, l, whole);
-        for (int p = max(p0, first); p < p1; ++p) {
-            const int h = (p - first) * 4 + (lane >> 3);
-            const bool real = h < 2 * r.Hkv, isk = h < r.Hkv;
-            const int hk = !real ? 0 : isk ? h : h - r.Hkv;
-            const long long at = cell(hk);
-            const __nv_bfloat16* row = isk ? a.k + t * a.k_stride + hk * D : a.v + t * a.v_stride + hk * D;
-            const float* w = isk && r.wk ? s_w + D : nullptr;
-            F2 y[D / 32][2];
-            float x = 1.f;
-            load_four<D>(r, row, real, r.wk != nullptr, w, l, y, x);
-            if (isk) {
-                if (whole) turner.turn_whole(y);
-                else turner.turn(r, row, real, x, w, l, y);
-            }
-            put_codes<D>(y, real, (isk ? a.kp : a.vp) + at * (D / 2), (isk ? a.ks : a.vs) + at * (D / 32), lane);
-        }
-    }
+    });
 }
 
 // ---------------------------------------------------------------------- host
@@ -632,11 +738,27 @@ int check_heads(int T, int Hq, int Hkv, int d) {
     return FA_OK;
 }
 
-// Warps that share a token, for `passes` passes over its rows: as many as fill the
-// card with sixteen warps an SM, none with less than one pass.
-int parts_for(int T, int passes, int sms) {
-    const long long want = (16LL * sms + T - 1) / T;
-    return (int)(want < 1 ? 1 : want > passes ? passes : want);
+// Blocks of eight warps, two an SM (their rings fill its shared memory).
+int grid_for(long long units, int sms) {
+    const long long want = (units + 7) / 8;
+    return (int)(want < 2LL * sms ? want : 2LL * sms);
+}
+// The rotation's arguments with `chunk` rows a unit, `arrays` of Hkv rows.
+RopeArgs rope_args(const float* cos, const float* sin, const int* positions, const void* wq, const void* wk, int T, int Hq, int Hkv, int max_pos, int rot,
+                   int inter, int seq_len, int w_bf16, float eps, int chunk, int arrays, DevStatus* status) {
+    const int per_q = (Hq + chunk - 1) / chunk, per_k = (Hkv + chunk - 1) / chunk;
+    return {cos, sin, positions, wq, wk, T, Hq, Hkv, max_pos, rot, inter != 0, seq_len, w_bf16 != 0, eps, per_q, per_k, per_q + arrays * per_k, status};
+}
+// Launches with `smem` bytes of dynamic shared memory, which a kernel is allowed once a device.
+template <typename A>
+int launch_rope(void (*kern)(RopeArgs, A), std::atomic<uint64_t>& prepared, int grid, uint32_t smem, cudaStream_t stream, const RopeArgs& r, const A& a) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
+    if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
+        prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    return launch_dependent(kern, grid, 256, smem, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -674,14 +796,19 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
         if (meet(out[i], in[1 - i], T) || (meet(out[i], in[i], T) && !same(out[i], in[i], T))) return FA_ERR_INVALID;
     }
     const int sms = fa_num_sms();
-    if (sms < 1) return FA_ERR_LAUNCH;
-    const int per = 512 / d, passes = (Hq + Hkv + per - 1) / per, parts = parts_for(T, passes, sms);
-    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, seq_len, weights_bf16 != 0, eps, passes, parts};
+    DevStatus* status = device_status_ptr();
+    if (sms < 1 || !status) return FA_ERR_LAUNCH;
     const RowsArgs a = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(q_out),
                         static_cast<__nv_bfloat16*>(k_out), q_stride, k_stride, q_out_stride, k_out_stride};
-    const long long grid = ((long long)T * parts + 7) / 8;
-    auto kern = d == 64 ? qk_rope_kernel<64> : d == 128 ? qk_rope_kernel<128> : qk_rope_kernel<256>;
-    return launch_dependent(kern, (int)grid, 256, 0, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    auto launch = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        static std::atomic<uint64_t> prepared{0};
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kChunk<D>, 1, status);
+        return launch_rope(qk_rope_kernel<D>, prepared, grid_for((long long)T * r.per, sms), kSmem<D>, stream, r, a);
+    };
+    if (d == 64) return launch(std::integral_constant<int, 64>{});
+    if (d == 128) return launch(std::integral_constant<int, 128>{});
+    return launch(std::integral_constant<int, 256>{});
 }
 
 size_t fa_qk_rope_bwd_workspace_size(int d) {
@@ -738,18 +865,21 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     }
     if (T == 0 && !norm) return FA_OK;
     const int sms = fa_num_sms();
-    if (sms < 1) return FA_ERR_LAUNCH;
-    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, seq_len, weights_bf16 != 0, eps, 0, 1};
+    DevStatus* status = device_status_ptr();
+    if (sms < 1 || !status) return FA_ERR_LAUNCH;
     const GradArgs a = {static_cast<const __nv_bfloat16*>(dq_out), static_cast<const __nv_bfloat16*>(dk_out), static_cast<const __nv_bfloat16*>(q),
                         static_cast<const __nv_bfloat16*>(k), static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk),
                         dq_out_stride, dk_out_stride, q_stride, k_stride, static_cast<float*>(workspace)};
-    const long long want = ((long long)T + 7) / 8;
-    const int grid = (int)(want < 2LL * sms ? want : 2LL * sms);
-    if (grid > 0) {
-        auto kern = d == 64 ? qk_rope_bwd_kernel<64> : d == 128 ? qk_rope_bwd_kernel<128> : qk_rope_bwd_kernel<256>;
-        if (launch_dependent(kern, grid, 256, 0, stream, r, a) != cudaSuccess) return FA_ERR_LAUNCH;
-    }
-    if (!norm) return FA_OK;
+    int grid = 0;
+    auto launch = [&](auto dim) -> int {
+        constexpr int D = decltype(dim)::value;
+        static std::atomic<uint64_t> prepared{0};
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kChunkGrad<D>, 1, status);
+        grid = grid_for((long long)T * r.per, sms);
+        return grid < 1 ? FA_OK : launch_rope(qk_rope_bwd_kernel<D>, prepared, grid, kSmemGrad<D>, stream, r, a);
+    };
+    rc = d == 64 ? launch(std::integral_constant<int, 64>{}) : d == 128 ? launch(std::integral_constant<int, 128>{}) : launch(std::integral_constant<int, 256>{});
+    if (rc != FA_OK || !norm) return rc;
     return launch_dependent(qk_rope_dw_kernel, 2 * d / 32, 256, 0, stream, a.partial, grid, d, dq_weight, dk_weight) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -794,19 +924,23 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
         if (meet(cache[i], out, T)) return FA_ERR_INVALID;
     }
     const int sms = fa_num_sms();
-    if (sms < 1) return FA_ERR_LAUNCH;
-    const int per = 512 / d;
-    const long long passes = four ? (Hq + per - 1) / per + (2LL * Hkv + 3) / 4 : (Hq + 2LL * Hkv + per - 1) / per;
-    const int parts = parts_for(T, (int)passes, sms);
-    const RopeArgs r = {cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved != 0, 1, weights_bf16 != 0, eps, (int)passes, parts};
+    DevStatus* status = device_status_ptr();
+    if (sms < 1 || !status) return FA_ERR_LAUNCH;
     const PutArgs a = {static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k), static_cast<const __nv_bfloat16*>(v),
                        static_cast<__nv_bfloat16*>(q_out), q_stride, k_stride, v_stride, q_out_stride, slots, static_cast<uint8_t*>(k_pages),
                        static_cast<uint8_t*>(v_pages), static_cast<uint8_t*>(k_scales), static_cast<uint8_t*>(v_scales), lg,
                        (long long)num_pages * page_size};
-    const long long grid = ((long long)T * parts + 7) / 8;
-    auto pick = [&](auto f) { return launch_dependent(f, (int)grid, 256, 0, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH; };
-    if (four) return pick(d == 64 ? rope_store_kernel<64, true> : d == 128 ? rope_store_kernel<128, true> : rope_store_kernel<256, true>);
-    return pick(d == 64 ? rope_store_kernel<64, false> : d == 128 ? rope_store_kernel<128, false> : rope_store_kernel<256, false>);
+    auto launch = [&](auto dim, auto bits4) {
+        constexpr int D = decltype(dim)::value;
+        static std::atomic<uint64_t> prepared{0};
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, 1, weights_bf16, eps, kChunk<D>, 2, status);
+        return launch_rope(rope_store_kernel<D, decltype(bits4)::value>, prepared, grid_for((long long)T * r.per, sms), kSmem<D>, stream, r, a);
+    };
+    auto pick = [&](auto bits4) {
+        return d == 64 ? launch(std::integral_constant<int, 64>{}, bits4) : d == 128 ? launch(std::integral_constant<int, 128>{}, bits4)
+                                                                                 : launch(std::integral_constant<int, 256>{}, bits4);
+    };
+    return four ? pick(std::true_type{}) : pick(std::false_type{});
 }
 
 }  // extern "C"
