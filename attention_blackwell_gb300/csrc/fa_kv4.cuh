@@ -16,6 +16,8 @@
 #include <cuda_fp16.h>
 #include <stdint.h>
 
+#include "fa_prim.cuh"
+
 namespace fa {
 
 constexpr uint32_t kScaleNaN = 0xFC, kScaleMost = 0xF7;   // 0xF7: 61440
@@ -46,18 +48,18 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t most) {
     return r < kScaleMost ? r : kScaleMost;
 }
 
-// Codes of four values for scale s with reciprocal inv: 16 bits, the first value
-// lowest; ties go to the even code, what is above 6 to 6.  The quotient x / s has
-// to be right where it lies on a tie, which bf16 values often do: t = x inv is
-// corrected by its remainder x - t s, which an FMA gives exactly, so a quotient that
-// fits 24 bits comes out as it is.
-__device__ __forceinline__ uint32_t codes_of(const float (&x)[4], float s, float inv) {
+// Codes of four values (two pairs) for scale s with reciprocal inv, both twice: 16
+// bits, the first value lowest; ties go to the even code, what is above 6 to 6.  The
+// quotient x / s has to be right where it lies on a tie, which bf16 values often do:
+// t = x inv is corrected by its remainder x - t s, which an FMA gives exactly, so a
+// quotient that fits 24 bits comes out as it is.
+__device__ __forceinline__ uint32_t codes_of(uint64_t x01, uint64_t x23, uint64_t minus_s, uint64_t inv) {
+    uint64_t t01 = f2_mul(x01, inv), t23 = f2_mul(x23, inv);
+    t01 = f2_fma(f2_fma(t01, minus_s, x01), inv, t01);
+    t23 = f2_fma(f2_fma(t23, minus_s, x23), inv, t23);
     float t[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        t[i] = __fmul_rn(x[i], inv);
-        t[i] = fmaf(fmaf(-t[i], s, x[i]), inv, t[i]);
-    }
+    f2_unpack(t01, t[0], t[1]);
+    f2_unpack(t23, t[2], t[3]);
     uint32_t out;
     asm("{\n\t.reg .b8 lo, hi, z;\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e2m1x2.f32 lo, %2, %1;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 hi, %4, %3;\n\tmov.b16 h, {lo, hi};\n\tcvt.u32.u16 %0, h;\n\t}"

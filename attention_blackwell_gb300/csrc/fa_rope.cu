@@ -10,11 +10,11 @@
 //   dx = r (t - x r^2 mean(t x)),   dw = sum over rows of u x r.
 // All of it in 32 bits, rounded once where it is stored.
 //
-// A unit is up to kChunk rows of one token's q, k or v, which are adjacent in memory,
+// A unit is up to r.chunk rows of one token's q, k or v, which are adjacent in memory,
 // with its rows of the cos and sin tables.  Every warp has a ring of units in shared
 // memory, filled by bulk copies (what is in flight costs no registers; loaded into
-// registers ahead, the same work moved 4.6 TB/s at its best), and takes every
-// W-th unit of the call.  d / 16 lanes share a row, so that a lane's 16 elements are
+// registers ahead, the same work moved 4.6 TB/s at its best), and takes a range of
+// the call's units.  d / 16 lanes share a row, so that a lane's 16 elements are
 // whole pairs whatever rot is: two 16-byte chunks.
 #include <math.h>
 #include <stdint.h>
@@ -36,7 +36,8 @@ struct RopeArgs {
     const void *wq, *wk;         // [d] float or bf16, null: no norm
     int T, Hq, Hkv, max_pos, rot, inter, seq_len, w_bf16;
     float eps;
-    int per_q, per_k, per;       // units of a token's q rows, of its k (and v) rows, of all
+    int chunk, per_q, per_k, per;    // rows a unit; units of a token's q rows, of its k (and v) rows, of all
+    int units;
     DevStatus* status;
 };
 
@@ -199,28 +200,29 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
 }
 
-// Calls work(unit, slot) for this warp's units.  rows(t, j, array, bytes) is where
-// a unit's rows are and how many bytes of them.
-template <int D, int kBytes, int kArrays, int kRing, class Rows, class Work>
+// Calls work(unit, rows, tables) for this warp's units.  rows(t, j, array, bytes) is
+// where a unit's rows are and how many bytes of them.
+template <int D, int kBytes, int kArrays, int kRing, int kWarps, class Rows, class Work>
 __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t* full, const int* slots, const Rows& rows, const Work& work) {
     using F = Feed<D, kBytes, kArrays, kRing>;
     const int lane = threadIdx.x & 31;
-    const long long first = blockIdx.x * 8LL + (threadIdx.x >> 5), step = gridDim.x * 8LL, all = (long long)r.T * r.per;
-    const long long n = first < all ? (all - first + step - 1) / step : 0;
+    // A range of the units, so that every warp gets q, k and v in the same proportion.
+    const int warps = gridDim.x * kWarps, warp = blockIdx.x * kWarps + (threadIdx.x >> 5), share = r.units / warps, more = r.units - share * warps;
+    const int first = warp * share + min(warp, more), n = share + (warp < more);
     // The units that the copies come to next, 32 at a time, one a lane, and the 32 after them.
-    auto fetch = [&](long long k) {
+    auto fetch = [&](int k) {
         Unit u = {0, 0, -1, 0};
         if (k + lane < n) {
-            const long long id = first + (k + lane) * step;
-            u.t = (int)(id / r.per);
-            u.j = (int)(id - (long long)u.t * r.per);
+            const int id = first + k + lane;
+            u.t = id / r.per;
+            u.j = id - u.t * r.per;
             u.pos = position_of(r, u.t);
             u.slot = slots ? slots[u.t] : 0;
         }
         return u;
     };
     Unit now = fetch(0), next = fetch(32);
-    long long k = 0;
+    int k = 0;
     uint32_t filled = 0, issued = 0;
     auto copy = [&]() {
         Unit u;
@@ -230,7 +232,7 @@ __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t*
                 now = next;
                 next = fetch(k + 32);
             }
-            const int i = (int)k & 31;
+            const int i = k & 31;
             u.pos = __shfl_sync(0xffffffffu, now.pos, i);
             u.t = __shfl_sync(0xffffffffu, now.t, i);
             u.j = __shfl_sync(0xffffffffu, now.j, i);
@@ -239,21 +241,19 @@ __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t*
         } while (u.pos < 0);
         uint8_t* to = ring + filled * F::kSlot;
         uint64_t* bar = &full[filled];
-        uint32_t bytes = 0;
-        const uint8_t* from = nullptr;
+        uint32_t bytes = r.rot * 2, total = 2 * bytes;
+        const uint8_t* from;
         if (lane < kArrays) from = rows(u.t, u.j, lane, bytes);
-        else if (lane < kArrays + 2) {
-            bytes = r.rot * 2;
-            from = reinterpret_cast<const uint8_t*>((lane == kArrays ? r.cos : r.sin) + (long long)u.pos * (r.rot >> 1));
-        }
-        const uint32_t total = __reduce_add_sync(0xffffffffu, bytes);
+        else from = reinterpret_cast<const uint8_t*>((lane == kArrays ? r.cos : r.sin) + (long long)u.pos * (r.rot >> 1));
+#pragma unroll
+        for (int i = 0; i < kArrays; ++i) total += __shfl_sync(0xffffffffu, bytes, i);
         __syncwarp();                                // every lane has read what the slot held
         if (lane == 0) {
             *reinterpret_cast<Unit*>(to) = u;
             mbar_arrive_expect_tx(bar, total);
         }
         __syncwarp();
-        if (bytes) bulk_load(smem_u32(to) + (lane < kArrays ? 16 + lane * kBytes : F::kTable + (lane - kArrays) * r.rot * 2), from, bytes, bar);
+        if (lane < kArrays + 2 && bytes) bulk_load(smem_u32(to) + (lane < kArrays ? 16 + lane * kBytes : F::kTable + (lane - kArrays) * r.rot * 2), from, bytes, bar);
         filled = filled + 1 == kRing ? 0 : filled + 1;
         ++issued;
     };
@@ -291,25 +291,29 @@ __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t*
 struct Chunk {
     int what, h0, n;
 };
-template <int kChunk> __device__ __forceinline__ Chunk chunk_of(const RopeArgs& r, int j) {
+__device__ __forceinline__ Chunk chunk_of(const RopeArgs& r, int j) {
     Chunk c;
     c.what = j < r.per_q ? 0 : j < r.per_q + r.per_k ? 1 : 2;
-    c.h0 = (c.what == 0 ? j : c.what == 1 ? j - r.per_q : j - r.per_q - r.per_k) * kChunk;
-    c.n = min(kChunk, (c.what == 0 ? r.Hq : r.Hkv) - c.h0);
+    c.h0 = (c.what == 0 ? j : c.what == 1 ? j - r.per_q : j - r.per_q - r.per_k) * r.chunk;
+    c.n = min(r.chunk, (c.what == 0 ? r.Hq : r.Hkv) - c.h0);
     return c;
 }
 
-// Bytes of rows a unit, and the rows: two passes of 32 lanes; one in the backward
-// pass, whose units hold two arrays.
-constexpr int kBytes = 2048, kBytesGrad = 1024, kRing = 4;
+// Bytes of rows a unit at most: four passes of 32 lanes; in the backward pass, whose
+// units hold two arrays, two.  What a unit costs besides its passes is worth one of
+// them.
+constexpr int kBytes = 4096, kBytesGrad = 4096, kRing = 3, kRingPut = 2, kRingGrad = 2;
+constexpr int kWarps = 12, kWarpsPut = 16, kWarpsGrad = 12;      // a block, one an SM
+template <int D> constexpr int kPass = 512 / D;              // rows a pass
 template <int D> constexpr int kChunk = kBytes / (2 * D);
 template <int D> constexpr int kChunkGrad = kBytesGrad / (2 * D);
-template <int D> constexpr uint32_t kSmem = 8 * Feed<D, kBytes, 1, kRing>::kWarp;
-template <int D> constexpr uint32_t kSmemGrad = 8 * Feed<D, kBytesGrad, 2, kRing>::kWarp;
+template <int D> constexpr uint32_t kSmem = kWarps * Feed<D, kBytes, 1, kRing>::kWarp;
+template <int D> constexpr uint32_t kSmemPut = kWarpsPut * Feed<D, kBytes, 1, kRingPut>::kWarp;
+template <int D> constexpr uint32_t kSmemGrad = kWarpsGrad * Feed<D, kBytesGrad, 2, kRingGrad>::kWarp;
 
 // The block's barriers, before the kernel it depends on is done.
-__device__ __forceinline__ void init_barriers(uint64_t (&full)[8][kRing]) {
-    if (threadIdx.x < 8 * kRing) {
+template <int W, int N> __device__ __forceinline__ void init_barriers(uint64_t (&full)[W][N]) {
+    if (threadIdx.x < W * N) {
         mbar_init(&full[0][0] + threadIdx.x, 1);
         fence_mbar_init();
     }
@@ -325,9 +329,9 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& r, Lane<D>& me, const 
     const bool norm = c.what ? r.wk != nullptr : r.wq != nullptr;
     me.angles(r, table, lane, 1.f);
 #pragma unroll
-    for (int p = 0; p < kChunk<D> / Me::kRows; ++p) {
-        const int i = p * Me::kRows + sub;
-        if (p * Me::kRows >= c.n) break;
+    for (int p = 0; p < kChunk<D>; p += Me::kRows) {
+        if (p >= c.n) break;
+        const int i = p + sub;
         F2 v[8] = {};
         if (i < c.n) {
             unpack8(load16(in + (i * D + me.a) * 2), v);
@@ -344,10 +348,10 @@ __device__ __forceinline__ void turn_rows(const RopeArgs& r, Lane<D>& me, const 
 }
 
 template <int D>
-__global__ void __launch_bounds__(256, 2) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) qk_rope_kernel(const RopeArgs r, const RowsArgs a) {
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ __align__(16) float s_w[2 * D];
-    __shared__ uint64_t full[8][kRing];
+    __shared__ uint64_t full[kWarps][kRing];
     init_barriers(full);
     grid_launch_next();
     grid_wait();
@@ -357,13 +361,13 @@ __global__ void __launch_bounds__(256, 2) qk_rope_kernel(const RopeArgs r, const
     Lane<D> me;
     me.place(r, lane);
     auto rows = [&](int t, int j, int, uint32_t& bytes) {
-        const Chunk c = chunk_of<kChunk<D>>(r, j);
+        const Chunk c = chunk_of(r, j);
         bytes = c.n * D * 2;
         return reinterpret_cast<const uint8_t*>((c.what ? a.k + t * a.k_stride : a.q + t * a.q_stride) + c.h0 * D);
     };
-    feed<D, kBytes, 1, kRing>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], nullptr, rows,
+    feed<D, kBytes, 1, kRing, kWarps>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], nullptr, rows,
                               [&](const Unit& u, const uint8_t* in, const float* table) {
-        const Chunk c = chunk_of<kChunk<D>>(r, u.j);
+        const Chunk c = chunk_of(r, u.j);
         __nv_bfloat16* to = c.what ? a.k_out + u.t * a.k_out_stride : a.q_out + u.t * a.q_out_stride;
         turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
     });
@@ -411,11 +415,11 @@ __device__ __forceinline__ void grad_row(const RopeArgs& r, const Lane<D>& me, b
 // Each block leaves its sums of the weights' gradients, which a second kernel adds up
 // in the blocks' order, so equal calls give equal results.
 template <int D>
-__global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
+__global__ void __launch_bounds__(32 * kWarpsGrad, 1) qk_rope_bwd_kernel(const RopeArgs r, const GradArgs a) {
     using Me = Lane<D>;
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ __align__(16) float s_w[2 * D];
-    __shared__ uint64_t full[8][kRing];
+    __shared__ uint64_t full[kWarpsGrad][kRingGrad];
     init_barriers(full);
     grid_launch_next();
     grid_wait();
@@ -427,26 +431,29 @@ __global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, c
     me.place(r, lane);
     F2 dwq[8] = {}, dwk[8] = {};
     auto rows = [&](int t, int j, int array, uint32_t& bytes) {
-        const Chunk c = chunk_of<kChunkGrad<D>>(r, j);
+        const Chunk c = chunk_of(r, j);
         bytes = array && !(c.what ? r.wk : r.wq) ? 0 : c.n * D * 2;
         const __nv_bfloat16* p = c.what ? (array ? a.k + t * a.k_stride : a.gk + t * a.gk_stride) : array ? a.q + t * a.q_stride : a.gq + t * a.gq_stride;
         return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
     };
-    feed<D, kBytesGrad, 2, kRing>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRing>::kWarp, full[warp], nullptr, rows,
+    feed<D, kBytesGrad, 2, kRingGrad, kWarpsGrad>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRingGrad>::kWarp, full[warp], nullptr, rows,
                                   [&](const Unit& u, const uint8_t* in, const float* table) {
-        const Chunk c = chunk_of<kChunkGrad<D>>(r, u.j);
+        const Chunk c = chunk_of(r, u.j);
         me.angles(r, table, lane, -1.f);
-        const bool real = sub < c.n;
-        const uint8_t *g = in + sub * D * 2, *x = g + kBytesGrad;
-        const long long row = (long long)(c.h0 + sub) * D;
-        if (c.what == 0) grad_row<D>(r, me, real, g, x, r.wq ? s_w : nullptr, dwq, a.dq + (long long)u.t * r.Hq * D + row);
-        else grad_row<D>(r, me, real, g, x, r.wk ? s_w + D : nullptr, dwk, a.dk + (long long)u.t * r.Hkv * D + row);
+        __nv_bfloat16* out = c.what ? a.dk + ((long long)u.t * r.Hkv + c.h0) * D : a.dq + ((long long)u.t * r.Hq + c.h0) * D;
+        const uint8_t* g = in + sub * D * 2;
+        if (c.what == 0)
+            for (int p = 0; p < c.n; p += Me::kRows)
+                grad_row<D>(r, me, p + sub < c.n, g + p * D * 2, g + p * D * 2 + kBytesGrad, r.wq ? s_w : nullptr, dwq, out + (p + sub) * D);
+        else
+            for (int p = 0; p < c.n; p += Me::kRows)
+                grad_row<D>(r, me, p + sub < c.n, g + p * D * 2, g + p * D * 2 + kBytesGrad, r.wk ? s_w + D : nullptr, dwk, out + (p + sub) * D);
     });
     if (!norm) return;
     // The warp's rows, then the block's warps; the rings are done with.
     __syncthreads();
     float (*s_dw)[2 * D] = reinterpret_cast<float (*)[2 * D]>(dsmem);
-    static_assert(8 * 2 * D * 4 <= kSmemGrad<D>, "room for the sums");
+    static_assert(kWarpsGrad * 2 * D * 4 <= kSmemGrad<D>, "room for the sums");
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
         float q[2], k[2];
@@ -465,10 +472,10 @@ __global__ void __launch_bounds__(256, 2) qk_rope_bwd_kernel(const RopeArgs r, c
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * D; i += 256) {
+    for (int i = threadIdx.x; i < 2 * D; i += 32 * kWarpsGrad) {
         float sum = s_dw[0][i];
 #pragma unroll
-        for (int y = 1; y < 8; ++y) sum += s_dw[y][i];
+        for (int y = 1; y < kWarpsGrad; ++y) sum += s_dw[y][i];
         a.partial[(long long)blockIdx.x * (2 * D) + i] = sum;
     }
 }
@@ -519,15 +526,12 @@ __device__ __forceinline__ void put_codes(const F2 (&y)[D / 32][2], bool real, u
     for (int g = 1; g < kG; ++g) mine = l % kG == g ? most[g] : mine;
     const uint32_t byte = scale_byte(mine);
     const bool plain = byte != 0 && byte != kScaleNaN;       // else codes of 0
-    const float s_own = plain ? scale_f32(byte) : 0.f, inv_own = plain ? __frcp_rn(s_own) : 0.f;
+    const float minus_s = plain ? -scale_f32(byte) : 0.f, inv_own = plain ? __frcp_rn(-minus_s) : 0.f;
     uint32_t out[kG / 2];
 #pragma unroll
     for (int g = 0; g < kG; ++g) {
-        const float s = __shfl_sync(0xffffffffu, s_own, (lane & 24) + g), inv = __shfl_sync(0xffffffffu, inv_own, (lane & 24) + g);
-        float v[4];
-        f2_unpack(y[g][0], v[0], v[1]);
-        f2_unpack(y[g][1], v[2], v[3]);
-        const uint32_t c = codes_of(v, s, inv);
+        const F2 s = both(__shfl_sync(0xffffffffu, minus_s, (lane & 24) + g)), inv = both(__shfl_sync(0xffffffffu, inv_own, (lane & 24) + g));
+        const uint32_t c = codes_of(y[g][0], y[g][1], s, inv);
         out[g / 2] = g & 1 ? out[g / 2] | c << 16 : c;
     }
     if (!real) return;
@@ -653,11 +657,11 @@ __device__ __forceinline__ void put_rows(const RopeArgs& r, const PutArgs& a, co
 }
 
 template <int D, bool kFour>
-__global__ void __launch_bounds__(256, 2) rope_store_kernel(const RopeArgs r, const PutArgs a) {
+__global__ void __launch_bounds__(32 * kWarpsPut, 1) rope_store_kernel(const RopeArgs r, const PutArgs a) {
     using Me = Lane<D>;
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ __align__(16) float s_w[2 * D];
-    __shared__ uint64_t full[8][kRing];
+    __shared__ uint64_t full[kWarpsPut][kRingPut];
     init_barriers(full);
     grid_launch_next();
     grid_wait();
@@ -667,14 +671,14 @@ __global__ void __launch_bounds__(256, 2) rope_store_kernel(const RopeArgs r, co
     Me me;
     me.place(r, lane);
     auto rows = [&](int t, int j, int, uint32_t& bytes) {
-        const Chunk c = chunk_of<kChunk<D>>(r, j);
+        const Chunk c = chunk_of(r, j);
         bytes = c.n * D * 2;
         const __nv_bfloat16* p = c.what == 0 ? a.q + t * a.q_stride : c.what == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
         return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
     };
-    feed<D, kBytes, 1, kRing>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], a.slots, rows,
+    feed<D, kBytes, 1, kRingPut, kWarpsPut>(r, dsmem + warp * Feed<D, kBytes, 1, kRingPut>::kWarp, full[warp], a.slots, rows,
                               [&](const Unit& u, const uint8_t* in, const float* table) {
-        const Chunk c = chunk_of<kChunk<D>>(r, u.j);
+        const Chunk c = chunk_of(r, u.j);
         if (c.what == 0) {
             __nv_bfloat16* to = a.q_out + u.t * a.q_out_stride;
             turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
@@ -735,30 +739,37 @@ int check_heads(int T, int Hq, int Hkv, int d) {
     if (T < 0 || Hq < 0 || Hkv < 0 || Hq + (long long)Hkv < 1 || d < 1) return FA_ERR_INVALID;
     if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
     if ((long long)Hq * d > 0x3fffffff || (long long)Hkv * d > 0x3fffffff) return FA_ERR_UNSUPPORTED;
+    // Units of one pass at the least: their number, and a step past it, fits 32 bits.
+    const int pass = 512 / d;
+    if (((Hq + pass - 1) / pass + 2LL * ((Hkv + pass - 1) / pass)) * T > 0x3fffffff) return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 
-// Blocks of eight warps, two an SM (their rings fill its shared memory).
-int grid_for(long long units, int sms) {
-    const long long want = (units + 7) / 8;
-    return (int)(want < 2LL * sms ? want : 2LL * sms);
-}
-// The rotation's arguments with `chunk` rows a unit, `arrays` of Hkv rows.
+// Blocks of `warps`, up to one an SM (the rings fill its shared memory).
+int grid_for(int units, int sms, int warps) { return units < warps * sms ? (units + warps - 1) / warps : sms; }
+// The rotation's arguments, with `arrays` of Hkv rows.  Rows a unit: as many as fill
+// a slot, but no more than leave every warp a unit (whole passes).
 RopeArgs rope_args(const float* cos, const float* sin, const int* positions, const void* wq, const void* wk, int T, int Hq, int Hkv, int max_pos, int rot,
-                   int inter, int seq_len, int w_bf16, float eps, int chunk, int arrays, DevStatus* status) {
-    const int per_q = (Hq + chunk - 1) / chunk, per_k = (Hkv + chunk - 1) / chunk;
-    return {cos, sin, positions, wq, wk, T, Hq, Hkv, max_pos, rot, inter != 0, seq_len, w_bf16 != 0, eps, per_q, per_k, per_q + arrays * per_k, status};
+                   int inter, int seq_len, int w_bf16, float eps, int pass, int most, int arrays, int workers, DevStatus* status) {
+    int chunk = most, per_q, per_k;
+    for (;; chunk /= 2) {
+        per_q = (Hq + chunk - 1) / chunk;
+        per_k = (Hkv + chunk - 1) / chunk;
+        if (chunk == pass || (long long)T * (per_q + arrays * per_k) >= workers) break;
+    }
+    const int per = per_q + arrays * per_k;
+    return {cos, sin, positions, wq, wk, T, Hq, Hkv, max_pos, rot, inter != 0, seq_len, w_bf16 != 0, eps, chunk, per_q, per_k, per, T * per, status};
 }
 // Launches with `smem` bytes of dynamic shared memory, which a kernel is allowed once a device.
 template <typename A>
-int launch_rope(void (*kern)(RopeArgs, A), std::atomic<uint64_t>& prepared, int grid, uint32_t smem, cudaStream_t stream, const RopeArgs& r, const A& a) {
+int launch_rope(void (*kern)(RopeArgs, A), std::atomic<uint64_t>& prepared, int grid, int threads, uint32_t smem, cudaStream_t stream, const RopeArgs& r, const A& a) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    return launch_dependent(kern, grid, 256, smem, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(kern, grid, threads, smem, stream, r, a) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -803,8 +814,8 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
     auto launch = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
         static std::atomic<uint64_t> prepared{0};
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kChunk<D>, 1, status);
-        return launch_rope(qk_rope_kernel<D>, prepared, grid_for((long long)T * r.per, sms), kSmem<D>, stream, r, a);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kPass<D>, kChunk<D>, 1, kWarps * sms, status);
+        return launch_rope(qk_rope_kernel<D>, prepared, grid_for(r.units, sms, kWarps), 32 * kWarps, kSmem<D>, stream, r, a);
     };
     if (d == 64) return launch(std::integral_constant<int, 64>{});
     if (d == 128) return launch(std::integral_constant<int, 128>{});
@@ -874,9 +885,9 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     auto launch = [&](auto dim) -> int {
         constexpr int D = decltype(dim)::value;
         static std::atomic<uint64_t> prepared{0};
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kChunkGrad<D>, 1, status);
-        grid = grid_for((long long)T * r.per, sms);
-        return grid < 1 ? FA_OK : launch_rope(qk_rope_bwd_kernel<D>, prepared, grid, kSmemGrad<D>, stream, r, a);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kPass<D>, kChunkGrad<D>, 1, kWarpsGrad * sms, status);
+        grid = grid_for(r.units, sms, kWarpsGrad);
+        return grid < 1 ? FA_OK : launch_rope(qk_rope_bwd_kernel<D>, prepared, grid, 32 * kWarpsGrad, kSmemGrad<D>, stream, r, a);
     };
     rc = d == 64 ? launch(std::integral_constant<int, 64>{}) : d == 128 ? launch(std::integral_constant<int, 128>{}) : launch(std::integral_constant<int, 256>{});
     if (rc != FA_OK || !norm) return rc;
@@ -933,8 +944,8 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
     auto launch = [&](auto dim, auto bits4) {
         constexpr int D = decltype(dim)::value;
         static std::atomic<uint64_t> prepared{0};
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, 1, weights_bf16, eps, kChunk<D>, 2, status);
-        return launch_rope(rope_store_kernel<D, decltype(bits4)::value>, prepared, grid_for((long long)T * r.per, sms), kSmem<D>, stream, r, a);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, 1, weights_bf16, eps, kPass<D>, kChunk<D>, 2, kWarpsPut * sms, status);
+        return launch_rope(rope_store_kernel<D, decltype(bits4)::value>, prepared, grid_for(r.units, sms, kWarpsPut), 32 * kWarpsPut, kSmemPut<D>, stream, r, a);
     };
     auto pick = [&](auto bits4) {
         return d == 64 ? launch(std::integral_constant<int, 64>{}, bits4) : d == 128 ? launch(std::integral_constant<int, 128>{}, bits4)

@@ -477,8 +477,10 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  * Errors: FA_ERR_INVALID (null pointer, T or heads < 0, no heads, max_pos, rot
  * or (without positions) seq_len < 1, rot > d, a stride below heads * d, eps
  * negative or not finite, arrays that overlap), FA_ERR_UNSUPPORTED (d not 64,
- * 128 or 256, rot not a multiple of 16, heads * d above 2^30 - 1), FA_ERR_ALIGN,
- * FA_ERR_LAUNCH.
+ * 128 or 256, rot not a multiple of 16, heads * d above 2^30 - 1, T times the
+ * kilobytes of a token's rows of q and of k twice, each rounded up, above 2^30 - 1),
+ * FA_ERR_ALIGN, FA_ERR_LAUNCH.  A call whose kernel gives up a wait (2 s) reports
+ * FA_ERR_TIMEOUT through fa_get_device_status.
  */
 int fa_qk_rope(const void *q, const void *k, int64_t q_stride, int64_t k_stride, void *q_out, void *k_out,
                int64_t q_out_stride, int64_t k_out_stride, int T, int Hq, int Hkv, int d, const float *cos,
