@@ -529,28 +529,31 @@ def prefix_fwd(q, k_pages, v_pages, block_table, kv_lens, cu_seqlens=None, max_s
 def _tokens(t, name):
     """(T, H, d, elements between tokens) of a bf16 [T, H, d] or [B, N, H, d]
     tensor that is dense within a token and whose tokens are evenly apart."""
-    shape = t.shape
-    if len(shape) == 3:
-        st = _rows(t, name)
-        return shape[0], shape[1], shape[2], st
-    if len(shape) != 4:
-        raise ValueError("%s must have 3 or 4 dimensions" % name)
-    B, N, H, d = shape
-    sb, sn, sh, sd = t.stride()
-    if B > 1 and N > 1 and sb != N * sn:
-        raise ValueError("%s must have its tokens evenly apart" % name)
     if t.dtype is not torch.bfloat16:
         raise ValueError("%s must be torch.bfloat16, got %s" % (name, t.dtype))
-    if d > 1 and sd != 1 or H > 1 and sh != d:
+    shape, st = t.shape, t.stride()
+    if len(shape) == 3:
+        T, H, d = shape
+        between, sh, sd = st
+    elif len(shape) == 4:
+        B, N, H, d = shape
+        sb, sn, sh, sd = st
+        if B > 1 and N > 1 and sb != N * sn:
+            raise ValueError("%s must have its tokens evenly apart" % name)
+        T, between = B * N, sn if N > 1 else sb
+    else:
+        raise ValueError("%s must have 3 or 4 dimensions" % name)
+    if sd != 1 and d > 1 or sh != d and H > 1:
         raise ValueError("%s must be contiguous within a token" % name)
-    return B * N, H, d, sn if N > 1 else sb if B > 1 else H * d
+    return T, H, d, between if T > 1 else H * d
 
 
 def _rope_tables(cos, sin, positions, T, d, q_weight, k_weight):
     """Checks; returns (max_pos, rot, 1 for bf16 weights)."""
-    if cos.dtype is not torch.float32 or sin.dtype is not torch.float32 or not cos.is_contiguous() or not sin.is_contiguous():
-        _need(cos, "cos", torch.float32)
-        _need(sin, "sin", torch.float32)
+    f32 = torch.float32
+    if cos.dtype is not f32 or sin.dtype is not f32 or not cos.is_contiguous() or not sin.is_contiguous():
+        _need(cos, "cos", f32)
+        _need(sin, "sin", f32)
     shape = cos.shape
     if len(shape) != 2 or shape != sin.shape:
         raise ValueError("cos and sin must be [max_pos, rot / 2]")
@@ -559,15 +562,15 @@ def _rope_tables(cos, sin, positions, T, d, q_weight, k_weight):
             _need(positions, "positions", torch.int32)
         if positions.numel() != T:
             raise ValueError("positions must have one element a token")
-    bf16 = 0
-    for w in (q_weight, k_weight):
-        if w is not None:
-            if w.dtype is not torch.float32 and w.dtype is not torch.bfloat16 or not w.is_contiguous() or w.numel() != d:
-                raise ValueError("norm weights must be float32 or bfloat16 [d], contiguous")
-            bf16 = int(w.dtype is torch.bfloat16)
-    if q_weight is not None and k_weight is not None and q_weight.dtype is not k_weight.dtype:
-        raise ValueError("norm weights must have one type")
-    return shape[0], 2 * shape[1], bf16
+    w, v = q_weight if q_weight is not None else k_weight, k_weight
+    if w is None:
+        return shape[0], 2 * shape[1], 0
+    kind = w.dtype
+    if v is not None and v is not w and (v.dtype is not kind or not v.is_contiguous() or v.numel() != d):
+        raise ValueError("norm weights must have one type and be [d], contiguous")
+    if kind is not f32 and kind is not torch.bfloat16 or not w.is_contiguous() or w.numel() != d:
+        raise ValueError("norm weights must be float32 or bfloat16 [d], contiguous")
+    return shape[0], 2 * shape[1], 0 if kind is f32 else 1
 
 
 def _at(t):
@@ -591,19 +594,21 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
                           lambda: qk_rope(q, k, cos, sin, positions, q_weight, k_weight, eps, interleaved, q_out, k_out))
     T, Hq, d, qs = _tokens(q, "q")
     Tk, Hkv, dk, ks = _tokens(k, "k")
-    if q.shape[:-2] != k.shape[:-2] or d != dk:
+    if T != Tk or d != dk or q.shape[:-2] != k.shape[:-2]:
         raise ValueError("q and k must have the same tokens and head dim")
     max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
     if q_out is None:
-        q_out, qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), Hq * d
+        q_out, qo = torch.empty_like(q), Hq * d     # dense: q's tokens are
     else:
         qo = _tokens(q_out, "q_out")[3]
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
     if k_out is None:
-        k_out, ko = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device), Hkv * d
+        k_out, ko = torch.empty_like(k), Hkv * d
     else:
         ko = _tokens(k_out, "k_out")[3]
-    if q_out.shape != q.shape or k_out.shape != k.shape:
-        raise ValueError("q_out and k_out must have q's and k's shapes")
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
     _one_device(dev, (k, cos, sin, positions, q_weight, k_weight, q_out, k_out))
     if T == 0:
         return q_out, k_out
@@ -742,7 +747,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
         if q.shape[0] != T or q.shape[2] != d:
             raise ValueError("q must be [T, Hq, d] with k's T and d")
         if q_out is None:
-            q_out, qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device), Hq * d
+            q_out, qo = torch.empty_like(q), Hq * d
         else:
             qo = _rows(q_out, "q_out")
             if q_out.shape != q.shape:
