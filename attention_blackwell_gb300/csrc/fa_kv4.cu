@@ -59,22 +59,32 @@ __host__ __device__ constexpr uint32_t table_bytes(int B) { return (4u * B + 3) 
 template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
+    // Warps of a worker.  32 rows of 256 would be 256 registers of O in one warp: two
+    // share them, each with half of d.
+    static constexpr int kTeam = D == 256 && NT == 4 ? 2 : 1;
     static constexpr int kWarps = NT == 1 && D <= 128 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
-    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
+    static constexpr int kWorkers = kWarps / kTeam;
+    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : kTeam;   // 16-key parts a step
+    static constexpr int kOwn = kParts / kTeam;          // of them, those whose scores a warp computes
     static constexpr int kSteps = D == 128 && NT <= 2 ? 2 : D == 64 && NT == 2 ? 2 : 1;   // steps a slot of the ring
-    static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kParts;
+    static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kOwn;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : 4;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : NT == 2 ? 4 : 3;
     static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
-    // A step's scales as the products want them: K's as floats [key][group], V's as
-    // pairs of keys [key / 2][group], (e, 2^-e) [key].
+    // The scales of the keys that a warp scores, as the products want them: K's as floats
+    // [key][group], V's as pairs of keys [key / 2][group], (e, 2^-e) [key].
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
-    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPrep;
-    static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0, "copies are 16-byte aligned");
+    // A team: the scales of two steps for each warp (one may be a step ahead of the
+    // other), the weights [part][tile of rows][lane], factors, maxima and sums of rows.
+    static constexpr uint32_t kWeights = kParts * NT * 256, kShared = kTeam > 1 ? kWeights + 5 * kRows * 4 : 0;
+    static constexpr uint32_t kPreps = kTeam > 1 ? 2 * kTeam * kPrep : kPrep;
+    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPreps + kShared;    // of a worker
+    static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0 && kPrep % 16 == 0, "copies are 16-byte aligned");
     static_assert(kRing * kSlotParts <= 32 && kRing <= 8 && 4 * kSlotParts <= 32, "a bit a part, a lane a copy");
-    static_assert(kWarps * kWarp + table_bytes(kTableMost) + 1536 <= 232448, "shared memory plan");
+    static_assert(kTeam == 1 || (kSteps == 1 && kOwn == 1 && !kQRegs), "a team's step is a part a warp");
+    static_assert(kWorkers * kWarp + table_bytes(kTableMost) + 1536 <= 232448, "shared memory plan");
 };
 
 struct KvRow {
@@ -181,6 +191,7 @@ struct KvWalk {
 
 struct KvShared {
     uint64_t full[16][8];
+    uint32_t live[8][8];                 // teams: a slot's parts that have a page
     int2 scan[16];
     int abort_flag, bad;
 };
@@ -271,7 +282,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
     }
     __syncthreads();
     KvHeader h = {};
-    const int workers = gridDim.x * kWarps;
+    const int workers = gridDim.x * Kv<D, NT>::kWorkers;
     h.per = units / workers;
     h.more = units - h.per * workers;
     h.bad = sh.bad;
@@ -404,10 +415,21 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
 
 // -------------------------------------------------------------------- kernel
 
+// Barriers of a team, with the `or` and `and` of a flag over its threads.
+__device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.sync %0, 64;" ::"r"(team + 1) : "memory"); }
+__device__ __forceinline__ bool team_or(int team, bool x) {
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(team + 1), "r"((uint32_t)x) : "memory");
+    return y != 0;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArgs a) {
     using K = Kv<D, NT>;
-    constexpr int kG = K::kGroups, kParts = K::kParts, kSteps = K::kSteps, kSP = K::kSlotParts;
+    constexpr int kG = K::kGroups, kParts = K::kParts, kOwn = K::kOwn, kSteps = K::kSteps, kSP = K::kSlotParts;
+    constexpr bool kTeam = K::kTeam > 1;
+    constexpr int kGO = kG / K::kTeam, kNL = NT / K::kTeam;      // groups of O, tiles of Q's rows that a warp brings
     constexpr uint32_t kRing = K::kRing;
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ KvShared sh;
@@ -417,11 +439,11 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     // wavefronts for one at d = 128, two at d = 64).
     const int kr = r ^ (r >> 1);
     KvTables t;
-    t.pref = a.B <= kTableMost ? reinterpret_cast<int*>(dsmem + K::kWarps * K::kWarp) : a.tables + (long long)blockIdx.x * (4 * a.B + 3);
+    t.pref = a.B <= kTableMost ? reinterpret_cast<int*>(dsmem + K::kWorkers * K::kWarp) : a.tables + (long long)blockIdx.x * (4 * a.B + 3);
     t.items = t.pref + a.B + 1;
     t.cu = t.items + a.B + 1;
     t.len = t.cu + a.B + 1;
-    if (tid < K::kWarps * (int)kRing) {
+    if (tid < K::kWorkers * (int)kRing) {
         mbar_init(&sh.full[tid / kRing][tid % kRing], 1);
         fence_mbar_init();
     }
@@ -448,16 +470,19 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         a.rows[i] = row;
     }
 
-    uint64_t* full = sh.full[warp];
-    uint8_t* const ring = dsmem + warp * K::kWarp;
-    uint8_t *const q_smem = ring + kRing * K::kSlot, *const prep = q_smem + K::kQBytes;
-    const int worker = blockIdx.x * K::kWarps + warp;
+    const int team = warp / K::kTeam, half = warp % K::kTeam;
+    uint64_t* full = sh.full[team];
+    uint8_t* const ring = dsmem + team * K::kWarp;
+    uint8_t *const q_smem = ring + kRing * K::kSlot, *const preps = q_smem + K::kQBytes, *const weights = preps + K::kPreps;
+    float* const row_f = reinterpret_cast<float*>(weights + K::kWeights);          // a team's rows: factors, maxima and sums of each warp
+    float *const row_m = row_f + K::kRows, *const row_l = row_m + 2 * K::kRows;
+    const int worker = blockIdx.x * K::kWorkers + team;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
     KvWalk<K::kRows> ahead;
     KvItem to = {};
     ahead.start(a, t, hdr, worker);
-    bool more = ahead.next(a, t, to);
+    bool more = half == 0 && ahead.next(a, t, to);       // a team's first warp copies for both
     int part = to.p0, win = -1, win_next = -1;       // next part; pages of its 32 parts, one a lane, and of the next 32
     uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a part of a slot: its page exists
     auto pages = [&](int p) -> int {                 // of parts p .. p + 31
@@ -484,6 +509,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         uint64_t* bar = &full[filled];
         __syncwarp();                                // every lane has read what the slot held
         if (lane == 0) {
+            if (kTeam) sh.live[team][filled] = on;
             if (on) mbar_arrive_expect_tx(bar, K::kPart * __popc(on));
             else mbar_arrive(bar);
         }
@@ -514,7 +540,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     KvWalk<K::kRows> walk;
     KvItem it;
     walk.start(a, t, hdr, worker);
-    uint32_t read = 0, slot = 0, phase = 0;
+    uint32_t read = 0, slot = 0, phase = 0, step = 0;
+    bool refill = false;                             // a team: the slot before this one is done with
     bool ok = true;
     while (ok && walk.next(a, t, it)) {
         // Q as B operands: lane (r, c) has row r's elements 32 g + 8 c to + 7, which
@@ -522,10 +549,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         uint32_t qf[K::kQRegs ? NT : 1][K::kQRegs ? kG : 1][4];
         float f[NT][2];                              // what a row's sums are multiplied by, rows 2c and 2c + 1
         int lim[NT][2];                              // keys they see
-        float m[NT][2], l[NT][2], o[kG][2][NT][4];
+        float m[NT][2], l[NT][2], o[kGO][2][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int x = nt * 8 + r;
+        for (int n = 0; n < kNL; ++n) {
+            const int nt = half * kNL + n, x = nt * 8 + r;
             const long long row = (long long)it.rb * K::kRows + x;
             const int tok = (int)(row / a.G), h = (int)(row - (long long)tok * a.G);
             uint4 in[kG];
@@ -554,21 +581,31 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 for (int i = 0; i < 4; ++i) q[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
                 if constexpr (K::kQRegs) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[nt][g][i] = q[i];
+                    for (int i = 0; i < 4; ++i) qf[n][g][i] = q[i];
                 } else {
                     sts(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
                 }
             }
+            if constexpr (kTeam) {
+                if (c == 0) row_f[x] = up;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
+            }
+        }
+        if (kTeam) team_sync(team);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                f[nt][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
+                if (kTeam) f[nt][i] = row_f[nt * 8 + 2 * c + i];
                 const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
                 lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
                 m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
 #pragma unroll
-            for (int g = 0; g < kG; ++g)
+            for (int g = 0; g < kGO; ++g)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[g][0][nt][i] = o[g][1][nt][i] = 0.f;
         }
@@ -579,30 +616,34 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             // The step's K codes, K scales; V's lie kSP parts behind each.
             const uint8_t* const at = ring + slot * K::kSlot + sub * (kParts * K::kCodes);
             const uint8_t* const scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
-            const uint32_t here = live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
             if (sub == 0) {
-                if (!(ok = kv_wait(&full[slot], phase, &sh.abort_flag))) break;
+                ok = kv_wait(&full[slot], phase, &sh.abort_flag);
+                if (kTeam) ok = !team_or(team, !ok);
+                if (!ok) break;
                 // The ring is filled once the first slot is there: all at once, every
                 // warp's first slot would wait for the others' second.
                 if (read == 0)
                     for (uint32_t i = 1; i < kRing; ++i) copy();
             }
-            const bool ragged = k0 + K::kKeys > lim_min || here != (1u << kParts) - 1u;
+            const uint32_t here = kTeam ? sh.live[team][slot] : live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
+            const bool ragged = k0 + kParts * 16 > lim_min || here != (1u << kParts) - 1u;
+            const int own = half * kOwn;             // the first part whose scores are this warp's
+            uint8_t* const prep = preps + (kTeam ? (step & 1) * (2 * K::kPrep) + half * K::kPrep : 0);
 #pragma unroll
             for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
                 const int key = i * 32 + (lane & (K::kKeys - 1));      // sixteen keys: every key twice, with the same results
-                const bool real = !ragged || (k0 + key < it.seen && (here >> (key >> 4) & 1u));
-                prepare_key<D, NT>(scales, scales + kSP * K::kScales, prep, key, lane, real);
+                const bool real = !ragged || (k0 + own * 16 + key < it.seen && (here >> (own + (key >> 4)) & 1u));
+                prepare_key<D, NT>(scales + own * K::kScales, scales + (kSP + own) * K::kScales, prep, key, lane, real);
             }
             __syncwarp();
-            float z[kParts][NT][4], back[kParts][2]; // scores + e, 2^-e
+            float z[kOwn][NT][4], back[kOwn][2];     // scores + e, 2^-e
 #pragma unroll
-            for (int kt = 0; kt < kParts; ++kt) {
+            for (int kt = 0; kt < kOwn; ++kt) {
                 // Keys' codes: eight adjacent elements of every group, for keys r and r + 8.
                 uint32_t kw[2][kG], ksc[2][kG];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    lds(at + (kt * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
+                    lds(at + ((own + kt) * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
                     lds(prep + (kt * 16 + kr + 8 * i) * (4 * kG), ksc[i]);
                 }
 #pragma unroll
@@ -649,12 +690,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             }
             if (ragged) {
 #pragma unroll
-                for (int kt = 0; kt < kParts; ++kt)
+                for (int kt = 0; kt < kOwn; ++kt)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!(here >> kt & 1u) || k0 + kt * 16 + kr + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
+                            if (!(here >> (own + kt) & 1u) || k0 + (own + kt) * 16 + kr + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
             }
             // O and l follow a row's running maximum when it grows by more than kTau: only
             // then do the lanes that share the row look for it together.
@@ -665,25 +706,44 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 for (int i = 0; i < 2; ++i) {
                     float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
-                    for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                    for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                     jump |= x - m[nt][i] > kTau;
                 }
-            if (__any_sync(0xffffffffu, jump)) {
+            if constexpr (kTeam) {
+                jump = team_or(team, jump);
+                // Both warps are past the step before.
+                if (refill) copy();
+            }
+            if (kTeam ? jump : __any_sync(0xffffffffu, jump)) {
+                if constexpr (kTeam) {               // each warp's maxima for the other
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                            if (r == 0) row_m[half * K::kRows + nt * 8 + 2 * c + i] = x;
+                        }
+                    team_sync(team);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
-                        for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                        for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(m[nt][i], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)));
+                        if (kTeam) x = fmaxf(x, row_m[(half ^ 1) * K::kRows + nt * 8 + 2 * c + i]);
                         const float fac = ex2_mufu(m[nt][i] - x);
                         l[nt][i] *= fac;
                         m[nt][i] = x;
 #pragma unroll
-                        for (int g = 0; g < kG; ++g)
+                        for (int g = 0; g < kGO; ++g)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 o[g][h][nt][i] *= fac;
@@ -691,9 +751,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             }
                     }
             }
-#pragma unroll
-            for (int kt = 0; kt < kParts; ++kt) {
-                uint32_t pt[NT][2];                  // weights as B operands: row r, keys 2c, 2c + 1 and eight further
+            // Weights as B operands: row r, keys 2c, 2c + 1 and eight further.
+            auto weigh = [&](int kt, uint32_t (&pt)[NT][2]) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[4];
@@ -705,16 +764,36 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
                     pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
                 }
-                // Values' codes: four elements of every group, for the four keys, and scales.
-                uint32_t vw[2][2][kG / 2], vsc[2][kG];
+            };
+            if constexpr (kTeam) {
+                uint32_t pt[NT][2];
+                weigh(0, pt);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sts(weights + ((half * NT + nt) * 32 + lane) * 8, pt[nt]);
+                team_sync(team);
+            }
+#pragma unroll
+            for (int kt = 0; kt < kParts; ++kt) {
+                uint32_t pt[NT][2];
+                const uint8_t* scaled = prep + kt * 8 * (4 * kG);       // V's scales of the part
+                if constexpr (kTeam) {
+                    scaled = preps + (step & 1) * (2 * K::kPrep) + kt * K::kPrep;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) lds(weights + ((kt * NT + nt) * 32 + lane) * 8, pt[nt]);
+                } else {
+                    weigh(kt, pt);
+                }
+                // Values' codes: four elements of every group (a team: of half of them), for
+                // the four keys, and scales.
+                uint32_t vw[2][2][kGO / 2], vsc[2][kGO];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16), vw[i][y]);
-                    lds(prep + K::kVPairs + (kt * 8 + (c ^ (c >> 1)) + 4 * i) * (4 * kG), vsc[i]);
+                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16) + half * (2 * kGO), vw[i][y]);
+                    lds(scaled + K::kVPairs + ((c ^ (c >> 1)) + 4 * i) * (4 * kG) + half * (4 * kGO), vsc[i]);
                 }
 #pragma unroll
-                for (int j = 0; j < kG / 2; ++j) {
+                for (int j = 0; j < kGO / 2; ++j) {
                     uint32_t x[2][2][4];             // [keys 2c .., keys 2c + 8 ..][codes 0 and 2, 1 and 3][group 2j: two, group 2j + 1: two]
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -743,11 +822,14 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     slot = 0;
                     phase ^= 1;
                 }
-                copy();
+                if (kTeam) refill = true;
+                else copy();
             }
+            ++step;
         }
         if (!ok) break;
         // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
+        const int e0 = half * (kGO * 32) + 4 * r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -755,26 +837,35 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+                if (kTeam && r == 0) row_l[half * K::kRows + nt * 8 + 2 * c + i] = l[nt][i];
+            }
+        if (kTeam) team_sync(team);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 const int x = nt * 8 + 2 * c + i;
+                // A team's sums in one order, so both warps divide by the same.
+                if (kTeam) l[nt][i] = row_l[x] + row_l[K::kRows + x];
                 if (x >= it.rows) continue;
                 if (it.whole) {
                     const long long row = (long long)it.rb * K::kRows + x;
                     const int tok = (int)(row / a.G), h = it.hk * a.G + (int)(row - (long long)tok * a.G);
                     const float inv = l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i];
                     const long long tt = it.c0 + tok;
-                    __nv_bfloat16* dst = a.o + (tt * a.Hq + h) * D + 4 * r;
+                    __nv_bfloat16* dst = a.o + (tt * a.Hq + h) * D + e0;
 #pragma unroll
-                    for (int g = 0; g < kG; ++g)
+                    for (int g = 0; g < kGO; ++g)
                         *reinterpret_cast<uint2*>(dst + 32 * g) = make_uint2(pack_bf16x2(o[g][0][nt][i] * inv, o[g][0][nt][2 + i] * inv),
                                                                              pack_bf16x2(o[g][1][nt][i] * inv, o[g][1][nt][2 + i] * inv));
-                    if (r == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
+                    if (r == 0 && half == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
                 } else {
                     const long long row = (long long)it.seg * K::kRows + x;
-                    float* dst = a.seg + row * D + 4 * r;
+                    float* dst = a.seg + row * D + e0;
 #pragma unroll
-                    for (int g = 0; g < kG; ++g)
+                    for (int g = 0; g < kGO; ++g)
                         *reinterpret_cast<float4*>(dst + 32 * g) = make_float4(o[g][0][nt][i], o[g][0][nt][2 + i], o[g][1][nt][i], o[g][1][nt][2 + i]);
-                    if (r == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
+                    if (r == 0 && half == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
                 }
             }
     }
@@ -967,7 +1058,7 @@ int launch_expand(const ExpandArgs& a, int d, int sms, cudaStream_t stream) {
 }
 
 // Rows of an item of few rows: eight a product's N.
-int item_rows(int d, long long rows) { return rows <= 8 ? 8 : rows <= 16 || d == 256 ? 16 : 32; }
+int item_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 // Workspace of few rows: header, what the rows are, the segments' (m, l) and O.  The
 // largest of the three item sizes, so that a workspace for long drafts serves
@@ -977,7 +1068,7 @@ struct KvLayout {
 };
 KvLayout kv_layout(int T, int B, int Hkv, int G, int d, int sms) {
     size_t most = 0;
-    for (int rows = 8; rows <= (d == 256 ? 16 : 32); rows *= 2) {
+    for (int rows = 8; rows <= 32; rows *= 2) {
         const size_t items = (size_t)Hkv * ((long long)T * G / rows + (T < B ? T : B)), workers = (size_t)sms * 16;
         const size_t n = (items + workers) * rows;
         most = n > most ? n : most;
@@ -1011,17 +1102,17 @@ template <int D, int NT>
 int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
     using K = Kv<D, NT>;
     auto kern = kv4_kernel<D, NT>;
-    const size_t smem = K::kWarps * K::kWarp + (a.B <= kTableMost ? table_bytes(a.B) : 0);
+    const size_t smem = K::kWorkers * K::kWarp + (a.B <= kTableMost ? table_bytes(a.B) : 0);
     static std::atomic<uint64_t> prepared{0};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWarps * K::kWarp + table_bytes(kTableMost))) != cudaSuccess) return FA_ERR_LAUNCH;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWorkers * K::kWarp + table_bytes(kTableMost))) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
     const long long items = (long long)a.Hkv * ((long long)a.T * a.G / K::kRows + (a.T < a.B ? a.T : a.B));
-    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + K::kWarps - 1) / K::kWarps;
+    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + K::kWorkers - 1) / K::kWorkers;
     const int grid = 2 * need < sms ? (int)(2 * need) : sms;
     if (launch_dependent(kern, grid, K::kThreads, smem, stream, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
@@ -1166,10 +1257,10 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     a.ps_log2 = lg;
     a.max_seqlen = max_seqlen;
     a.scale_log2 = alpha * 1.4426950408889634f;
-    const int rows = item_rows(d, max_seqlen * (long long)G);
+    const int rows = item_rows(max_seqlen * (long long)G);
     if (d == 64) return rows == 8 ? launch_few<64, 1>(a, sms, stream) : rows == 16 ? launch_few<64, 2>(a, sms, stream) : launch_few<64, 4>(a, sms, stream);
     if (d == 128) return rows == 8 ? launch_few<128, 1>(a, sms, stream) : rows == 16 ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 4>(a, sms, stream);
-    return rows == 8 ? launch_few<256, 1>(a, sms, stream) : launch_few<256, 2>(a, sms, stream);
+    return rows == 8 ? launch_few<256, 1>(a, sms, stream) : rows == 16 ? launch_few<256, 2>(a, sms, stream) : launch_few<256, 4>(a, sms, stream);
 }
 
 }  // extern "C"
