@@ -59,10 +59,10 @@ __host__ __device__ constexpr uint32_t table_bytes(int B) { return (4u * B + 3) 
 template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
-    // Warps of a worker.  32 rows of 256 would be 256 registers of O in one warp: two
-    // share them, each with half of d.
-    static constexpr int kTeam = D == 256 && NT == 4 ? 2 : 1;
-    static constexpr int kWarps = NT == 1 && D <= 128 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
+    // Warps of a worker.  32 rows of 256 would be 256 registers of O in one warp: four
+    // share them, each with a quarter of d.
+    static constexpr int kTeam = D == 256 && NT == 4 ? 4 : 1;
+    static constexpr int kWarps = (NT == 1 && D <= 128) || kTeam == 4 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
     static constexpr int kWorkers = kWarps / kTeam;
     static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : kTeam;   // 16-key parts a step
     static constexpr int kOwn = kParts / kTeam;          // of them, those whose scores a warp computes
@@ -70,7 +70,7 @@ template <int D, int NT> struct Kv {
     static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kOwn;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : NT == 2 ? 4 : 3;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : NT == 2 ? 4 : 2;
     static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
     // The scales of the keys that a warp scores, as the products want them: K's as floats
@@ -78,7 +78,7 @@ template <int D, int NT> struct Kv {
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
     // A team: the scales of two steps for each warp (one may be a step ahead of the
     // other), the weights [part][tile of rows][lane], factors, maxima and sums of rows.
-    static constexpr uint32_t kWeights = kParts * NT * 256, kShared = kTeam > 1 ? kWeights + 5 * kRows * 4 : 0;
+    static constexpr uint32_t kWeights = kParts * NT * 256, kShared = kTeam > 1 ? kWeights + (2 + 2 * kTeam) * kRows * 4 : 0;
     static constexpr uint32_t kPreps = kTeam > 1 ? 2 * kTeam * kPrep : kPrep;
     static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPreps + kShared;    // of a worker
     static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0 && kPrep % 16 == 0, "copies are 16-byte aligned");
@@ -415,12 +415,12 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
 
 // -------------------------------------------------------------------- kernel
 
-// Barriers of a team, with the `or` and `and` of a flag over its threads.
-__device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.sync %0, 64;" ::"r"(team + 1) : "memory"); }
-__device__ __forceinline__ bool team_or(int team, bool x) {
+// Barriers of a team of W warps, and one with the `or` of a flag over its threads.
+template <int W> __device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory"); }
+template <int W> __device__ __forceinline__ bool team_or(int team, bool x) {
     uint32_t y;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(y) : "r"(team + 1), "r"((uint32_t)x) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"(team + 1), "r"((uint32_t)x), "n"(32 * W) : "memory");
     return y != 0;
 }
 
@@ -470,19 +470,20 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         a.rows[i] = row;
     }
 
-    const int team = warp / K::kTeam, half = warp % K::kTeam;
+    const int team = warp / K::kTeam, member = warp % K::kTeam;
     uint64_t* full = sh.full[team];
     uint8_t* const ring = dsmem + team * K::kWarp;
     uint8_t *const q_smem = ring + kRing * K::kSlot, *const preps = q_smem + K::kQBytes, *const weights = preps + K::kPreps;
     float* const row_f = reinterpret_cast<float*>(weights + K::kWeights);          // a team's rows: factors, maxima and sums of each warp
-    float *const row_m = row_f + K::kRows, *const row_l = row_m + 2 * K::kRows;
+    float *const row_m = row_f + K::kRows, *const row_l = row_m + K::kTeam * K::kRows;
+    int* const row_lim = reinterpret_cast<int*>(row_l + K::kTeam * K::kRows);      // and the keys that they see
     const int worker = blockIdx.x * K::kWorkers + team;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
     KvWalk<K::kRows> ahead;
     KvItem to = {};
     ahead.start(a, t, hdr, worker);
-    bool more = half == 0 && ahead.next(a, t, to);       // a team's first warp copies for both
+    bool more = member == 0 && ahead.next(a, t, to);       // a team's first warp copies for all
     int part = to.p0, win = -1, win_next = -1;       // next part; pages of its 32 parts, one a lane, and of the next 32
     uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a part of a slot: its page exists
     auto pages = [&](int p) -> int {                 // of parts p .. p + 31
@@ -547,12 +548,14 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         // Q as B operands: lane (r, c) has row r's elements 32 g + 8 c to + 7, which
         // are what it reads of a key.
         uint32_t qf[K::kQRegs ? NT : 1][K::kQRegs ? kG : 1][4];
-        float f[NT][2];                              // what a row's sums are multiplied by, rows 2c and 2c + 1
-        int lim[NT][2];                              // keys they see
+        // What a row's sums are multiplied by, and the keys it sees, of rows 2c and 2c + 1
+        // (a team's are in shared memory).
+        float f[kTeam ? 1 : NT][2];
+        int lim[kTeam ? 1 : NT][2];
         float m[NT][2], l[NT][2], o[kGO][2][NT][4];
 #pragma unroll
         for (int n = 0; n < kNL; ++n) {
-            const int nt = half * kNL + n, x = nt * 8 + r;
+            const int nt = member * kNL + n, x = nt * 8 + r;
             const long long row = (long long)it.rb * K::kRows + x;
             const int tok = (int)(row / a.G), h = (int)(row - (long long)tok * a.G);
             uint4 in[kG];
@@ -587,20 +590,24 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 }
             }
             if constexpr (kTeam) {
-                if (c == 0) row_f[x] = up;
+                if (c == 0) {
+                    row_f[x] = up;
+                    row_lim[x] = min(it.s, it.s - it.n + tok + 1);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
             }
         }
-        if (kTeam) team_sync(team);
+        if (kTeam) team_sync<K::kTeam>(team);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (kTeam) f[nt][i] = row_f[nt * 8 + 2 * c + i];
-                const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
-                lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
+                if constexpr (!kTeam) {
+                    const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
+                    lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
+                }
                 m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             const uint8_t* const scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
             if (sub == 0) {
                 ok = kv_wait(&full[slot], phase, &sh.abort_flag);
-                if (kTeam) ok = !team_or(team, !ok);
+                if (kTeam) ok = !team_or<K::kTeam>(team, !ok);
                 if (!ok) break;
                 // The ring is filled once the first slot is there: all at once, every
                 // warp's first slot would wait for the others' second.
@@ -627,8 +634,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             }
             const uint32_t here = kTeam ? sh.live[team][slot] : live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
             const bool ragged = k0 + kParts * 16 > lim_min || here != (1u << kParts) - 1u;
-            const int own = half * kOwn;             // the first part whose scores are this warp's
-            uint8_t* const prep = preps + (kTeam ? (step & 1) * (2 * K::kPrep) + half * K::kPrep : 0);
+            const int own = member * kOwn;             // the first part whose scores are this warp's
+            uint8_t* const prep = preps + (kTeam ? ((step & 1) * K::kTeam + member) * K::kPrep : 0);
 #pragma unroll
             for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
                 const int key = i * 32 + (lane & (K::kKeys - 1));      // sixteen keys: every key twice, with the same results
@@ -684,18 +691,22 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     back[kt][i] = __uint_as_float(eb[i][1]);
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 ff = kTeam ? *reinterpret_cast<const float2*>(row_f + nt * 8 + 2 * c) : make_float2(f[kTeam ? 0 : nt][0], f[kTeam ? 0 : nt][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], f[nt][i & 1], __uint_as_float(eb[i >> 1][0]));
+                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], i & 1 ? ff.y : ff.x, __uint_as_float(eb[i >> 1][0]));
+                }
             }
             if (ragged) {
 #pragma unroll
                 for (int kt = 0; kt < kOwn; ++kt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int2 ll = kTeam ? *reinterpret_cast<const int2*>(row_lim + nt * 8 + 2 * c) : make_int2(lim[kTeam ? 0 : nt][0], lim[kTeam ? 0 : nt][1]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!(here >> (own + kt) & 1u) || k0 + (own + kt) * 16 + kr + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
+                            if (!(here >> (own + kt) & 1u) || k0 + (own + kt) * 16 + kr + (i >> 1) * 8 >= (i & 1 ? ll.y : ll.x)) z[kt][nt][i] = -INFINITY;
+                    }
             }
             // O and l follow a row's running maximum when it grows by more than kTau: only
             // then do the lanes that share the row look for it together.
@@ -710,12 +721,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     jump |= x - m[nt][i] > kTau;
                 }
             if constexpr (kTeam) {
-                jump = team_or(team, jump);
-                // Both warps are past the step before.
+                jump = team_or<K::kTeam>(team, jump);
+                // All its warps are past the step before.
                 if (refill) copy();
             }
             if (kTeam ? jump : __any_sync(0xffffffffu, jump)) {
-                if constexpr (kTeam) {               // each warp's maxima for the other
+                if constexpr (kTeam) {               // each warp's maxima for the others
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -724,9 +735,9 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            if (r == 0) row_m[half * K::kRows + nt * 8 + 2 * c + i] = x;
+                            if (r == 0) row_m[member * K::kRows + nt * 8 + 2 * c + i] = x;
                         }
-                    team_sync(team);
+                    team_sync<K::kTeam>(team);
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -738,7 +749,9 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(m[nt][i], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)));
-                        if (kTeam) x = fmaxf(x, row_m[(half ^ 1) * K::kRows + nt * 8 + 2 * c + i]);
+                        if constexpr (kTeam)
+#pragma unroll
+                            for (int w = 0; w < K::kTeam; ++w) x = fmaxf(x, row_m[w * K::kRows + nt * 8 + 2 * c + i]);
                         const float fac = ex2_mufu(m[nt][i] - x);
                         l[nt][i] *= fac;
                         m[nt][i] = x;
@@ -769,28 +782,28 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 uint32_t pt[NT][2];
                 weigh(0, pt);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sts(weights + ((half * NT + nt) * 32 + lane) * 8, pt[nt]);
-                team_sync(team);
+                for (int nt = 0; nt < NT; ++nt) sts(weights + ((member * NT + nt) * 32 + lane) * 8, pt[nt]);
+                team_sync<K::kTeam>(team);
             }
 #pragma unroll
             for (int kt = 0; kt < kParts; ++kt) {
                 uint32_t pt[NT][2];
                 const uint8_t* scaled = prep + kt * 8 * (4 * kG);       // V's scales of the part
                 if constexpr (kTeam) {
-                    scaled = preps + (step & 1) * (2 * K::kPrep) + kt * K::kPrep;
+                    scaled = preps + ((step & 1) * K::kTeam + kt) * K::kPrep;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) lds(weights + ((kt * NT + nt) * 32 + lane) * 8, pt[nt]);
                 } else {
                     weigh(kt, pt);
                 }
-                // Values' codes: four elements of every group (a team: of half of them), for
+                // Values' codes: four elements of every group (a team: of a share of them), for
                 // the four keys, and scales.
                 uint32_t vw[2][2][kGO / 2], vsc[2][kGO];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16) + half * (2 * kGO), vw[i][y]);
-                    lds(scaled + K::kVPairs + ((c ^ (c >> 1)) + 4 * i) * (4 * kG) + half * (4 * kGO), vsc[i]);
+                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16) + member * (2 * kGO), vw[i][y]);
+                    lds(scaled + K::kVPairs + ((c ^ (c >> 1)) + 4 * i) * (4 * kG) + member * (4 * kGO), vsc[i]);
                 }
 #pragma unroll
                 for (int j = 0; j < kGO / 2; ++j) {
@@ -829,7 +842,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         }
         if (!ok) break;
         // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
-        const int e0 = half * (kGO * 32) + 4 * r;
+        const int e0 = member * (kGO * 32) + 4 * r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -837,16 +850,20 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
-                if (kTeam && r == 0) row_l[half * K::kRows + nt * 8 + 2 * c + i] = l[nt][i];
+                if (kTeam && r == 0) row_l[member * K::kRows + nt * 8 + 2 * c + i] = l[nt][i];
             }
-        if (kTeam) team_sync(team);
+        if (kTeam) team_sync<K::kTeam>(team);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int x = nt * 8 + 2 * c + i;
-                // A team's sums in one order, so both warps divide by the same.
-                if (kTeam) l[nt][i] = row_l[x] + row_l[K::kRows + x];
+                // A team's sums in one order, so all its warps divide by the same.
+                if constexpr (kTeam) {
+                    l[nt][i] = row_l[x];
+#pragma unroll
+                    for (int w = 1; w < K::kTeam; ++w) l[nt][i] += row_l[w * K::kRows + x];
+                }
                 if (x >= it.rows) continue;
                 if (it.whole) {
                     const long long row = (long long)it.rb * K::kRows + x;
@@ -858,14 +875,14 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     for (int g = 0; g < kGO; ++g)
                         *reinterpret_cast<uint2*>(dst + 32 * g) = make_uint2(pack_bf16x2(o[g][0][nt][i] * inv, o[g][0][nt][2 + i] * inv),
                                                                              pack_bf16x2(o[g][1][nt][i] * inv, o[g][1][nt][2 + i] * inv));
-                    if (r == 0 && half == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
+                    if (r == 0 && member == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
                 } else {
                     const long long row = (long long)it.seg * K::kRows + x;
                     float* dst = a.seg + row * D + e0;
 #pragma unroll
                     for (int g = 0; g < kGO; ++g)
                         *reinterpret_cast<float4*>(dst + 32 * g) = make_float4(o[g][0][nt][i], o[g][0][nt][2 + i], o[g][1][nt][i], o[g][1][nt][2 + i]);
-                    if (r == 0 && half == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
+                    if (r == 0 && member == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
                 }
             }
     }
