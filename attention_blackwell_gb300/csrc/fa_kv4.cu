@@ -48,6 +48,7 @@ constexpr float kTau = 8.0f;            // rescale threshold (log2 units)
 constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every finite score; a hidden key's -inf less it is -inf
 constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
+constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
 constexpr int kManyRows = 128;          // rows of a request and key/value head above which pages are expanded
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
@@ -60,9 +61,13 @@ template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
     // Warps of a worker.  32 rows of 256 would be 256 registers of O in one warp: four
-    // share them, each with a quarter of d.
-    static constexpr int kTeam = D == 256 && NT == 4 ? 4 : 1;
-    static constexpr int kWarps = (NT == 1 && D <= 128) || kTeam == 4 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
+    // share them, each with a quarter of d, and two share what would be 128, so that
+    // twelve warps fit an SM (32 rows of 256: 182 us for
+    // 100 requests of 8200 keys by eight single warps with 16 rows each, 134 so; 16 rows
+    // of 256: 222 and 199 for 64 requests of 4096 keys and 8 heads; 32 of 128: 384 and
+    // 359 for twice the keys).
+    static constexpr int kTeam = NT * D >= 1024 ? 4 : NT * D >= 512 && NT > 1 ? 2 : 1;
+    static constexpr int kWarps = (NT == 1 && D <= 128) || kTeam > 1 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
     static constexpr int kWorkers = kWarps / kTeam;
     static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : kTeam;   // 16-key parts a step
     static constexpr int kOwn = kParts / kTeam;          // of them, those whose scores a warp computes
@@ -70,15 +75,15 @@ template <int D, int NT> struct Kv {
     static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kOwn;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : NT == 2 ? 3 : 8) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : NT == 2 ? 4 : 2;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : 2;
     static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
     // The scales of the keys that a warp scores, as the products want them: K's as floats
     // [key][group], V's as pairs of keys [key / 2][group], (e, 2^-e) [key].
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
-    // A team: the scales of two steps for each warp (one may be a step ahead of the
-    // other), the weights [part][tile of rows][lane], factors, maxima and sums of rows.
-    static constexpr uint32_t kWeights = kParts * NT * 256, kShared = kTeam > 1 ? kWeights + (2 + 2 * kTeam) * kRows * 4 : 0;
+    // A team: the scales and the weights [part][tile of rows][lane] of two steps (one
+    // warp may be a step ahead of the others), factors, maxima and sums of rows.
+    static constexpr uint32_t kWeights = 2 * kParts * NT * 256, kShared = kTeam > 1 ? kWeights + (2 + 2 * kTeam) * kRows * 4 : 0;
     static constexpr uint32_t kPreps = kTeam > 1 ? 2 * kTeam * kPrep : kPrep;
     static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPreps + kShared;    // of a worker
     static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0 && kPrep % 16 == 0, "copies are 16-byte aligned");
@@ -123,13 +128,14 @@ struct KvTables {
 
 // Row blocks of a request with n tokens, units of each of its items: its tiles of
 // keys and one for what an item costs besides.
-__device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (int)(((long long)n * G + rows - 1) / rows); }
+// (T * Hq fits 31 bits, so rows of a request do.)
+__device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (int)(((uint32_t)(n * G) + (uint32_t)rows - 1) / (uint32_t)rows); }
 __device__ __forceinline__ int item_units(int s) { return s > 0 ? (s + kUnit - 1) / kUnit + 1 : 0; }
 
 // The keys that row block rb's last row sees.
 __device__ __forceinline__ int keys_seen(int n, int s, int G, int rb, int rows) {
-    const long long last = min((long long)(rb + 1) * rows, (long long)n * G) - 1;
-    return s - n + (int)(last / G) + 1;
+    const uint32_t last = min((uint32_t)(rb + 1) * (uint32_t)rows, (uint32_t)(n * G)) - 1;
+    return s - n + (int)(last / (uint32_t)G) + 1;
 }
 
 // The parts that units [first, last) of an item stand for.
@@ -174,7 +180,7 @@ struct KvWalk {
             it.b = b;
             it.hk = hk;
             it.rb = rb;
-            it.rows = (int)min((long long)ROWS, (long long)n * a.G - (long long)rb * ROWS);
+            it.rows = min(ROWS, n * a.G - rb * ROWS);
             it.c0 = t.cu[b];
             it.n = n;
             it.s = s;
@@ -450,6 +456,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     if (tid == 0) sh.abort_flag = 0;
     grid_launch_next();
     grid_wait();
+    // Small block tables on their way to L2 while the list is made: the first lookup is
+    // on every warp's way to its first copy.
+    {
+        const long long bytes = (long long)a.B * a.W * 4, line = ((long long)blockIdx.x * K::kThreads + tid) * 128;
+        if (bytes <= kPrefetchMost && line < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(a.table) + line));
+    }
     const KvHeader hdr = build_tables<D, NT>(a, t, sh, tid);
 
     // What the joining kernel needs to know of each row.
@@ -556,8 +568,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
         for (int n = 0; n < kNL; ++n) {
             const int nt = member * kNL + n, x = nt * 8 + r;
-            const long long row = (long long)it.rb * K::kRows + x;
-            const int tok = (int)(row / a.G), h = (int)(row - (long long)tok * a.G);
+            const uint32_t row = (uint32_t)it.rb * K::kRows + x;
+            const int tok = (int)(row / (uint32_t)a.G), h = (int)row - tok * a.G;
             uint4 in[kG];
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
@@ -605,7 +617,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if constexpr (!kTeam) {
-                    const int tk = (int)(((long long)it.rb * K::kRows + nt * 8 + 2 * c + i) / a.G);
+                    const int tk = (int)(((uint32_t)it.rb * K::kRows + nt * 8 + 2 * c + i) / (uint32_t)a.G);
                     lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
                 }
                 m[nt][i] = kNone;
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[g][0][nt][i] = o[g][1][nt][i] = 0.f;
         }
-        const int lim_min = it.s - it.n + (int)((long long)it.rb * K::kRows / a.G) + 1;
+        const int lim_min = it.s - it.n + (int)((uint32_t)it.rb * K::kRows / (uint32_t)a.G) + 1;
 
         for (int p = it.p0; p < it.p1; p += kParts) {
             const int k0 = p * 16, sub = kSteps == 1 ? 0 : (p - it.p0) / kParts & (kSteps - 1);    // step of the slot
@@ -625,8 +637,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             const uint8_t* const scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
             if (sub == 0) {
                 ok = kv_wait(&full[slot], phase, &sh.abort_flag);
-                if (kTeam) ok = !team_or<K::kTeam>(team, !ok);
-                if (!ok) break;
+                if (!kTeam && !ok) break;            // a team leaves together, see below
                 // The ring is filled once the first slot is there: all at once, every
                 // warp's first slot would wait for the others' second.
                 if (read == 0)
@@ -720,12 +731,49 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                     jump |= x - m[nt][i] > kTau;
                 }
+            // Weights as B operands: row r, keys 2c, 2c + 1 and eight further.
+            auto weigh = [&](int kt, uint32_t (&pt)[NT][2]) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[i] = ex2_mufu(z[kt][nt][i] - m[nt][i & 1]);
+                        l[nt][i & 1] = fmaf(w[i], back[kt][i >> 1], l[nt][i & 1]);
+                    }
+                    pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
+                    pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
+                }
+            };
+            uint8_t* const shared_pt = weights + (step & 1) * (K::kWeights / 2);
+            auto share = [&]() {
+                uint32_t pt[NT][2];
+                weigh(0, pt);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) sts(shared_pt + ((member * NT + nt) * 32 + lane) * 8, pt[nt]);
+            };
+            // A team: one barrier a step, for the weights as if no maximum grew.  Where one
+            // did, or a wait gave up, they are thrown away.
+            bool again = false;
+            float l_before[kTeam ? NT : 1][2];
             if constexpr (kTeam) {
-                jump = team_or<K::kTeam>(team, jump);
+                jump = __any_sync(0xffffffffu, jump);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) l_before[nt][i] = l[nt][i];
+                if (!jump) share();
+                again = team_or<K::kTeam>(team, jump || !ok);
                 // All its warps are past the step before.
                 if (refill) copy();
+                if (again && (ok = !team_or<K::kTeam>(team, !ok)) == false) break;
             }
-            if (kTeam ? jump : __any_sync(0xffffffffu, jump)) {
+            if (kTeam ? again : __any_sync(0xffffffffu, jump)) {
+                if constexpr (kTeam)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) l[nt][i] = l_before[nt][i];
                 if constexpr (kTeam) {               // each warp's maxima for the others
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -764,27 +812,11 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             }
                     }
             }
-            // Weights as B operands: row r, keys 2c, 2c + 1 and eight further.
-            auto weigh = [&](int kt, uint32_t (&pt)[NT][2]) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = ex2_mufu(z[kt][nt][i] - m[nt][i & 1]);
-                        l[nt][i & 1] = fmaf(w[i], back[kt][i >> 1], l[nt][i & 1]);
-                    }
-                    pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
-                    pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
+            if constexpr (kTeam)
+                if (again) {
+                    share();
+                    team_sync<K::kTeam>(team);
                 }
-            };
-            if constexpr (kTeam) {
-                uint32_t pt[NT][2];
-                weigh(0, pt);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sts(weights + ((member * NT + nt) * 32 + lane) * 8, pt[nt]);
-                team_sync<K::kTeam>(team);
-            }
 #pragma unroll
             for (int kt = 0; kt < kParts; ++kt) {
                 uint32_t pt[NT][2];
@@ -792,7 +824,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 if constexpr (kTeam) {
                     scaled = preps + ((step & 1) * K::kTeam + kt) * K::kPrep;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) lds(weights + ((kt * NT + nt) * 32 + lane) * 8, pt[nt]);
+                    for (int nt = 0; nt < NT; ++nt) lds(shared_pt + ((kt * NT + nt) * 32 + lane) * 8, pt[nt]);
                 } else {
                     weigh(kt, pt);
                 }
@@ -866,8 +898,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 }
                 if (x >= it.rows) continue;
                 if (it.whole) {
-                    const long long row = (long long)it.rb * K::kRows + x;
-                    const int tok = (int)(row / a.G), h = it.hk * a.G + (int)(row - (long long)tok * a.G);
+                    const uint32_t row = (uint32_t)it.rb * K::kRows + x;
+                    const int tok = (int)(row / (uint32_t)a.G), h = it.hk * a.G + (int)row - tok * a.G;
                     const float inv = l[nt][i] == 0.f ? 0.f : 1.f / l[nt][i];
                     const long long tt = it.c0 + tok;
                     __nv_bfloat16* dst = a.o + (tt * a.Hq + h) * D + e0;
@@ -916,8 +948,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_
     const KvHeader hdr = *a.hdr;
     const KvRow q = a.rows[t];
     if (hdr.bad || q.n == 0) return;
-    const long long row = (long long)(t - q.c0) * a.G + h - hk * a.G;
-    const int rb = (int)(row / rows_item), in = (int)(row - (long long)rb * rows_item), nb = row_blocks(q.n, a.G, rows_item);
+    const int row = (t - q.c0) * a.G + h - hk * a.G, rb = row / rows_item, in = row - rb * rows_item, nb = row_blocks(q.n, a.G, rows_item);
     const int units = item_units(q.s), item = hk * nb + rb, u0 = q.pref + item * units, seen = keys_seen(q.n, q.s, a.G, rb, rows_item);
     const bool some = units > 0 && seen > 0;
     const int first = some ? worker_of(hdr, u0) : 0, all = some ? worker_of(hdr, u0 + units - 1) - first + 1 : 0;

@@ -243,6 +243,22 @@ def test_long_histories(fa, d, hq, hkv):
         b.check(fa, *b.run(fa))
 
 
+@pytest.mark.parametrize("d,hq,hkv,n", [(256, 32, 1, 1), (256, 16, 1, 1), (256, 24, 2, 2), (256, 8, 1, 4), (128, 32, 1, 1), (128, 8, 1, 5), (128, 20, 4, 4)])
+def test_rows_that_warps_share(fa, d, hq, hkv, n):
+    """17 to 32 rows (9 to 16 at d = 256) are worked on by two or four warps: long and
+    short lists, absent pages, scales of every size, maxima that jump."""
+    s = [3000, 17, 900, 0, 65, 2100]
+    b = Batch(hq, hkv, d, 16, s, [n] * len(s), seed=d + hq, v_scales=(0, 0xF7))
+    b.check(fa, *b.run(fa))
+    b = Batch(hq, hkv, d, 32, s, [n, 0, n, 1, 1, n], seed=d + hq + 1, std=20.0, tail=2)
+    b.table[0][1] = b.table[2][0] = -1
+    b.table[5][10:30] = [1 << 30] * 20
+    b.check(fa, *b.run(fa))
+    b.ks[b.table[0][3], :, 5, 0] = 0xFC               # a key that every row of the request sees
+    o, lse = b.run(fa)
+    assert torch.isnan(o[:n]).all() and torch.isnan(lse[:, :n]).all() and not torch.isnan(o[n:sum(b.n)]).any()
+
+
 def test_many_requests(fa):
     g = np.random.default_rng(4)
     for hi in (90, 700):
