@@ -49,7 +49,11 @@ constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every fini
 constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
-constexpr int kManyRows = 128;          // rows of a request and key/value head above which pages are expanded
+// Rows of a request and key/value head above which pages are expanded.  8 requests of
+// 8000 keys and 8 heads, from the codes and expanded: 64 rows of 128 97 and 133 us, 128
+// rows 178 and 141; d = 64, 16 heads: 126 and 152, 242 and 170; d = 256, one head, 128
+// rows 52 and 57, 256 rows 84 and 59.
+constexpr int many_rows(int d) { return d == 256 ? 128 : 64; }
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
 // A CTA's tables of the list: in shared memory up to kTableMost requests, else in its
@@ -67,7 +71,7 @@ template <int D, int NT> struct Kv {
     // of 256: 222 and 199 for 64 requests of 4096 keys and 8 heads; 32 of 128: 384 and
     // 359 for twice the keys).
     static constexpr int kTeam = NT * D >= 1024 ? 4 : NT * D >= 512 && NT > 1 ? 2 : 1;
-    static constexpr int kWarps = (NT == 1 && D <= 128) || kTeam > 1 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
+    static constexpr int kWarps = D == 64 || NT * D <= 128 || kTeam > 1 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
     static constexpr int kWorkers = kWarps / kTeam;
     static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : kTeam;   // 16-key parts a step
     static constexpr int kOwn = kParts / kTeam;          // of them, those whose scores a warp computes
@@ -75,8 +79,8 @@ template <int D, int NT> struct Kv {
     static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kOwn;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 5 : 8) : NT == 1 ? 5 : 2;
-    static constexpr bool kQRegs = NT * D <= 256;        // Q's fragments in registers
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 8) : NT == 1 ? 5 : 2;
+    static constexpr bool kQRegs = NT <= 2 && NT * D <= 256;     // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
     // The scales of the keys that a warp scores, as the products want them: K's as floats
     // [key][group], V's as pairs of keys [key / 2][group], (e, 2^-e) [key].
@@ -659,6 +663,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             for (int kt = 0; kt < kOwn; ++kt) {
                 // Keys' codes: eight adjacent elements of every group, for keys r and r + 8.
                 uint32_t kw[2][kG], ksc[2][kG];
+                uint64_t z2[NT][2];                  // rows 2c and 2c + 1 of key r, of key r + 8
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     lds(at + ((own + kt) * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
@@ -675,6 +680,9 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                     for (int gg = 0; gg < 2; ++gg) {
                         const int g = 2 * j + gg;
+                        uint64_t sc[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) sc[i] = f2_pack(__uint_as_float(ksc[i][g]), __uint_as_float(ksc[i][g]));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             uint32_t q[4];
@@ -688,10 +696,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             mma_f16_0(acc, x[0][0][2 * gg], x[0][1][2 * gg], x[0][0][2 * gg + 1], x[0][1][2 * gg + 1], q[0], q[1]);
                             mma_f16(acc, x[1][0][2 * gg], x[1][1][2 * gg], x[1][0][2 * gg + 1], x[1][1][2 * gg + 1], q[2], q[3]);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float sc = __uint_as_float(ksc[i >> 1][g]);
-                                z[kt][nt][i] = g == 0 ? sc * acc[i] : fmaf(sc, acc[i], z[kt][nt][i]);
-                            }
+                            for (int i = 0; i < 2; ++i) z2[nt][i] = g == 0 ? f2_mul(sc[i], f2_pack(acc[2 * i], acc[2 * i + 1])) : f2_fma(sc[i], f2_pack(acc[2 * i], acc[2 * i + 1]), z2[nt][i]);
                         }
                     }
                 }
@@ -705,7 +710,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 for (int nt = 0; nt < NT; ++nt) {
                     const float2 ff = kTeam ? *reinterpret_cast<const float2*>(row_f + nt * 8 + 2 * c) : make_float2(f[kTeam ? 0 : nt][0], f[kTeam ? 0 : nt][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[kt][nt][i] = fmaf(z[kt][nt][i], i & 1 ? ff.y : ff.x, __uint_as_float(eb[i >> 1][0]));
+                    for (int i = 0; i < 2; ++i) {
+                        const float e = __uint_as_float(eb[i][0]);
+                        f2_unpack(f2_fma(z2[nt][i], f2_pack(ff.x, ff.y), f2_pack(e, e)), z[kt][nt][2 * i], z[kt][nt][2 * i + 1]);
+                    }
                 }
             }
             if (ragged) {
@@ -736,11 +744,16 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float w[4];
+                    uint64_t sum = f2_pack(l[nt][0], l[nt][1]);
+                    const uint64_t minus_m = f2_pack(-m[nt][0], -m[nt][1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        w[i] = ex2_mufu(z[kt][nt][i] - m[nt][i & 1]);
-                        l[nt][i & 1] = fmaf(w[i], back[kt][i >> 1], l[nt][i & 1]);
+                    for (int i = 0; i < 2; ++i) {
+                        f2_unpack(f2_add(f2_pack(z[kt][nt][2 * i], z[kt][nt][2 * i + 1]), minus_m), w[2 * i], w[2 * i + 1]);
+                        w[2 * i] = ex2_mufu(w[2 * i]);
+                        w[2 * i + 1] = ex2_mufu(w[2 * i + 1]);
+                        sum = f2_fma(f2_pack(w[2 * i], w[2 * i + 1]), f2_pack(back[kt][i], back[kt][i]), sum);
                     }
+                    f2_unpack(sum, l[nt][0], l[nt][1]);
                     pt[nt][0] = transposed(pack_f16x2(w[0], w[1]));
                     pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
                 }
@@ -1138,7 +1151,7 @@ struct ManyLayout {
 ManyLayout many_layout(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int W, int page) {
     ManyLayout w = {};
     const size_t one = (size_t)B * W * page * Hkv * d * 2;
-    if (max_seqlen * (long long)(Hq / Hkv) <= kManyRows || one > kExpandMost / 2 || (long long)B * W * page * Hkv > 0x7fffffffLL) return w;
+    if (max_seqlen * (long long)(Hq / Hkv) <= many_rows(d) || one > kExpandMost / 2 || (long long)B * W * page * Hkv > 0x7fffffffLL) return w;
     w.v = align256(one);
     w.table = w.v + align256(one);
     w.prefix = align256(w.table + 4 * (size_t)B * W);

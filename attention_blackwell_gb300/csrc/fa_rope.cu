@@ -480,19 +480,22 @@ __global__ void __launch_bounds__(32 * kWarpsGrad, 1) qk_rope_bwd_kernel(const R
     }
 }
 
-// 32 columns of the blocks' sums a block, eight rows at a time.
-__global__ void __launch_bounds__(256) qk_rope_dw_kernel(const float* partial, int blocks, int d, float* dwq, float* dwk) {
-    __shared__ float s[8][32];
+// 32 columns of the blocks' sums a block, 32 rows at a time.
+__global__ void __launch_bounds__(1024) qk_rope_dw_kernel(const float* partial, int blocks, int d, float* dwq, float* dwk) {
+    __shared__ float s[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
     grid_wait();
     float sum = 0.f;
-    for (int b = y; b < blocks; b += 8) sum += partial[(long long)b * (2 * d) + col];
+    for (int b = y; b < blocks; b += 32) sum += partial[(long long)b * (2 * d) + col];
     s[y][x] = sum;
     __syncthreads();
-    if (y) return;
-    for (int i = 1; i < 8; ++i) sum += s[i][x];
-    float* out = col < d ? dwq : dwk;
-    if (out) out[col & (d - 1)] = sum;
+    // A column a warp, its 32 sums a lane each, in one order.
+    sum = s[x][y];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int at = blockIdx.x * 32 + y;
+    float* out = at < d ? dwq : dwk;
+    if (x == 0 && out) out[at & (d - 1)] = sum;
 }
 
 // --------------------------------------------------------------------- store
@@ -568,7 +571,8 @@ __device__ __forceinline__ void norm_four(const RopeArgs& r, const uint8_t* row,
 
 // The rotation of a row that eight lanes hold.  Every product and sum is rounded by
 // itself, as the formula reads: codes lie next to borders, and so it is plain which
-// side a key falls on.  Whole rows in halves (the common case): a pair's two
+// side a key falls on.  (One float an instruction: the compiler joins a product of
+// two with the sum that follows.)  Whole rows in halves (the common case): a pair's two
 // elements are the same lane's, d / 2 apart, and the angles stay in registers.
 template <int D> struct Four {
     static constexpr int kG = D / 32;
@@ -590,9 +594,19 @@ template <int D> struct Four {
         for (int g = 0; g < kG / 2; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const F2 a = y[g][i], b = y[g + kG / 2][i], minus = both(-1.f);
-                y[g][i] = f2_add(f2_mul(a, c[g][i]), f2_mul(f2_mul(b, s[g][i]), minus));
-                y[g + kG / 2][i] = f2_add(f2_mul(b, c[g][i]), f2_mul(a, s[g][i]));
+                float a[2], b[2], cc[2], ss[2];
+                f2_unpack(y[g][i], a[0], a[1]);
+                f2_unpack(y[g + kG / 2][i], b[0], b[1]);
+                f2_unpack(c[g][i], cc[0], cc[1]);
+                f2_unpack(s[g][i], ss[0], ss[1]);
+                float lo[2], hi[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    lo[e] = __fsub_rn(__fmul_rn(a[e], cc[e]), __fmul_rn(b[e], ss[e]));
+                    hi[e] = __fadd_rn(__fmul_rn(b[e], cc[e]), __fmul_rn(a[e], ss[e]));
+                }
+                y[g][i] = f2_pack(lo[0], lo[1]);
+                y[g + kG / 2][i] = f2_pack(hi[0], hi[1]);
             }
     }
     // Any other rotation: partners are read again.
@@ -789,6 +803,8 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
     rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
     if (rc != FA_OK) return rc;
     const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (Hq == 0) q = q_out = nullptr, q_stride = q_out_stride = 0;
+    if (Hkv == 0) k = k_out = nullptr, k_stride = k_out_stride = 0;
     if (q_stride < nq || k_stride < nk || q_out_stride < nq || k_out_stride < nk) return FA_ERR_INVALID;
     if (misaligned(q, 15) || misaligned(k, 15) || misaligned(q_out, 15) || misaligned(k_out, 15) || (q_stride & 7) || (k_stride & 7) ||
         (q_out_stride & 7) || (k_out_stride & 7))
@@ -825,7 +841,7 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
 size_t fa_qk_rope_bwd_workspace_size(int d) {
     if (d != 64 && d != 128 && d != 256) return 0;
     const int sms = fa_num_sms();
-    return (size_t)2 * (sms > 0 ? sms : kMaxSMs) * 2 * d * 4;
+    return (size_t)(sms > 0 ? sms : kMaxSMs) * 2 * d * 4;      // a block an SM
 }
 
 int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride, int64_t dk_out_stride, const void* q, const void* k,
@@ -840,6 +856,8 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
     if (rc != FA_OK) return rc;
     const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (Hq == 0) dq_out = q = dq = nullptr, dq_out_stride = q_stride = 0;
+    if (Hkv == 0) dk_out = k = dk = nullptr, dk_out_stride = k_stride = 0;
     if (dq_out_stride < nq || dk_out_stride < nk || (q_weight && q_stride < nq) || (k_weight && k_stride < nk)) return FA_ERR_INVALID;
     if (misaligned(dq_out, 15) || misaligned(dk_out, 15) || misaligned(dq, 15) || misaligned(dk, 15) || (q_weight && (misaligned(q, 15) || (q_stride & 7))) ||
         (k_weight && (misaligned(k, 15) || (k_stride & 7))) || misaligned(dq_weight, 15) || misaligned(dk_weight, 15) || (dq_out_stride & 7) || (dk_out_stride & 7))
@@ -891,7 +909,7 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     };
     rc = d == 64 ? launch(std::integral_constant<int, 64>{}) : d == 128 ? launch(std::integral_constant<int, 128>{}) : launch(std::integral_constant<int, 256>{});
     if (rc != FA_OK || !norm) return rc;
-    return launch_dependent(qk_rope_dw_kernel, 2 * d / 32, 256, 0, stream, a.partial, grid, d, dq_weight, dk_weight) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(qk_rope_dw_kernel, 2 * d / 32, 1024, 0, stream, a.partial, grid, d, dq_weight, dk_weight) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
@@ -908,6 +926,7 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
     const int lg = page_log2(page_size);
     if (lg < 0 || (long long)num_pages * page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
     const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
+    if (Hq == 0) q = q_out = nullptr, q_stride = q_out_stride = 0;
     if (q_stride < nq || k_stride < nk || v_stride < nk || q_out_stride < nq) return FA_ERR_INVALID;
     if (misaligned(q, 15) || misaligned(k, 15) || misaligned(v, 15) || misaligned(q_out, 15) || (q_stride & 7) || (k_stride & 7) ||
         (v_stride & 7) || (q_out_stride & 7) || misaligned(k_pages, 15) || misaligned(v_pages, 15) || misaligned(k_scales, 15) ||

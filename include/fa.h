@@ -467,8 +467,8 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  *   aligned.  An output may be its own input's rows (same pointer and stride);
  *   otherwise no output overlaps another array (rows that interleave with
  *   another stride count as overlapping).
- * - Heads of one of the two may be 0: its pointers and stride are then not looked
- *   at (strides are at least 0).
+ * - Heads of one of the two may be 0: its pointers and strides are then not looked
+ *   at.
  */
 
 /*
@@ -568,8 +568,8 @@ int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages
  * see no key and rows outside every request as there), keys and values read from
  * 4-bit pages.  Scores, sums and the output's accumulator are 32 bits wide, the
  * weights fp16 relative to the largest weight times value scale.
- * Up to 128 rows of a request and key/value head (max_seqlen * Hq / Hkv) are
- * computed from the codes; above that, and while 4 * B * table_width * page_size
+ * Up to 64 rows of a request and key/value head (max_seqlen * Hq / Hkv; 128 at d =
+ * 256) are computed from the codes; above that, and while 4 * B * table_width * page_size
  * * Hkv * d is up to 2^32, the call expands the requests' pages into the
  * workspace once and goes on as fa_prefix_fwd.  A workspace too small for that, but
  * not for a call with max_seqlen 1, makes the rows be computed from the codes: right,
@@ -596,7 +596,9 @@ int fa_kv4_fwd(const void *q, int64_t q_stride, const void *k_pages, const void 
 /*
  * Bytes of device workspace fa_kv4_fwd needs for T rows of B requests of at most
  * max_seqlen rows each over tables of table_width pages (the current device's SM
- * count enters); 0 for invalid sizes.
+ * count enters), expanded pages included where there is room for them; 0 for
+ * invalid sizes.  What it gives for max_seqlen 1 is enough for every call with at
+ * most these T and B, from the codes.
  */
 size_t fa_kv4_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int table_width, int page_size);
 

@@ -169,7 +169,7 @@ class Batch:
         want, wl, mass, reach, top = self.want()
         o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
         T, hq, d = o.shape
-        many = max(self.n) * hq // self.kc.shape[1] > 128
+        many = max(self.n) * hq // self.kc.shape[1] > (128 if d == 256 else 64)
         e = (2.0 ** -23 * (d + 8) * reach + 2.0 ** -21 * (1 + reach))[..., None]
         tol = ((U if many else 2.0 ** -10) + 2 * e) * mass + U * np.abs(want) + 2.0 ** -20 * top + 1e-30
         real = ~np.isnan(want)

@@ -109,6 +109,10 @@ def test_qk_rope_refusals(fwd):
         assert fwd(**{n: A + 8}) == -3, n
     assert fwd(pos=A + 2) == -3
     assert fwd(T=0) == fwd(T=0, q=None, k=None, qo=None, ko=None) == 0
+    # heads of 0: nothing of that operand is looked at (here the other one is refused)
+    assert fwd(Hq=0, q=5, qo=3, qs=-1, qos=1, k=None) == fwd(Hkv=0, k=5, ko=3, ks=-1, kos=1, q=None) == -1
+    assert fwd(Hq=0, q=5, qo=3, qs=-1, qos=1, T=0) == fwd(Hkv=0, k=5, ko=3, ks=-1, kos=1, T=0) == 0
+    assert fwd(T=1 << 30) == -2                                    # units
 
 
 def test_qk_rope_refuses_arrays_that_overlap(fwd):

@@ -388,3 +388,30 @@ def test_shapes_and_types_are_refused(fa):
         fa.rope_store(c.q, c.k, c.v, c.cos, c.sin, c.pos, c.pos, kp, vp, ks[..., :2].contiguous(), vs[..., :2].contiguous())
     with pytest.raises(ValueError):
         fa.rope_store(c.q, c.k, c.v, c.cos, c.sin, None, c.pos, kp, vp, ks, vs)
+
+
+@pytest.mark.parametrize("d,rot,inter", [(64, 64, False), (128, 128, False), (256, 256, False), (128, 32, False), (128, 64, True)])
+def test_store_four_bits_rounds_each_product(fa, d, rot, inter):
+    """Keys on ties between codes when each product of the rotation is rounded by
+    itself, and off them, towards the odd code, were a product joined with the sum
+    (whichever of the two).  v = 2^-23: 1.25 (1 + 2 v) is 2.5 v over 1.25 and rounds to
+    2 v, 1.25 (1 + 6 v) is 7.5 v over and rounds to 8 v."""
+    v = 2.0 ** -23
+    pairs = [(1.25, 1 + 2 * v, 1.0, 1 + 2 * v),       # a c - b s = 0.25 of the first elements
+             (1.0, 1.5 + 8 * v, 1.25, 1 + 6 * v),
+             (-1.0, 1 + 2 * v, 1.25, 1 + 2 * v),      # b c + a s = 0.25 of the second
+             (-1.25, 1.5 + 8 * v, 1.0, 1 + 6 * v),
+             (6.0, 1.0, 0.0, 0.0), (0.0, 1.0, 6.0, 0.0)]      # groups' scales of 1
+    x, c, s = np.zeros((1, 1, d)), np.ones((1, rot // 2)), np.zeros((1, rot // 2))
+    first, second = R.pairs(rot, inter)
+    for i, (a, ci, b, si) in enumerate(pairs):
+        x[0, 0, first[i]], x[0, 0, second[i]], c[0, i], s[0, i] = a, b, ci, si
+    t = lambda z, kind: torch.tensor(z, dtype=torch.float32, device="cuda").to(kind)
+    want, scale = R.quantise(R.rotate(x.astype(np.float32), c.astype(np.float32), s.astype(np.float32), inter, np.float32))
+    at = [first[0], first[1], second[2], second[3]]
+    assert scale[0, 0, at[0] // 32] == scale[0, 0, at[2] // 32] == 15 << 3 and not want[0, 0, at].any()
+    k, at = t(x, torch.bfloat16), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache = fa.kv4_pages(1, 1, 16, d)
+    fa.rope_store(None, k, k, t(c, torch.float32), t(s, torch.float32), at, at, cache[0], cache[2], cache[1], cache[3], interleaved=inter)
+    got = R.unpack(cache[0][0, :, 0].cpu().numpy(), cache[1][0, :, 0].cpu().numpy())
+    assert np.array_equal(got, R.unpack(R.pack(want[0]), scale[0]))
