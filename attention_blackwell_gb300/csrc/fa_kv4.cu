@@ -27,10 +27,30 @@
 // cut by a range's end leaves (M, l, O) in the workspace, and a second kernel joins
 // the segments in the list's order; one that is not cut is written at once.
 //
+// More than 16 rows (8 at d = 256): two or four warps are a worker together (kTeam).
+// Each scores its share of a step's keys against all rows, leaves the weights in
+// shared memory, and after one barrier a step multiplies all of them with its share
+// of d of the values, so a code is converted once for up to 32 rows.
+//
 // Many rows (prompts): the requests' pages are expanded to bf16 once, in the
 // workspace, and fa_prefix_fwd's tensor-memory pipeline does the rest: for a prompt
 // the products are all, and 4.25 bits read and 16 written and read an element are
 // little.
+//
+// What bounds it (GB300; 6.78 TB/s measured; times of calls back to back):
+//   64 single tokens over up to 8191 keys each, 32 / 8 heads of 128 (303 MB): 76 us.
+//   16 keys of K and V are 2176 bytes, 93 cycles of an SM's share of HBM; they take
+//   290 instructions, 158 of them on the ALU (64 conversions at half rate, 16 to pair
+//   value codes by keys, 20 for scales), 74 and 79 cycles of the four schedulers.
+//   Measured 120: neither alone is the limit (without conversions, in an
+//   experiment, 107; copies alone 93).  8 us pass before the first product: lengths,
+//   walk, page numbers and copies depend on one another.  The join takes 5.
+//   d = 64, 16 heads with 1 to 8 drafted tokens, up to 4096 keys (98 MB): 39 us, 186
+//   instructions for 1088 bytes, the same start.
+//   32 rows of 256 over up to 16384 keys (234 MB): 134 us, products 38 % of it.
+//   one token over 1017 keys: 13 us, 12 as a graph.
+//   prompts, six of up to 2048 tokens over up to 10000 keys (563 GFLOP): 520 us, 25 of
+//   them the expansion (164 MB), the rest fa_prefix_fwd's.
 #include <limits.h>
 #include <math.h>
 #include <stdint.h>

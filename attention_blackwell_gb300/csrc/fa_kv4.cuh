@@ -23,8 +23,8 @@ namespace fa {
 constexpr uint32_t kScaleNaN = 0xFC, kScaleMost = 0xF7;   // 0xF7: 61440
 
 // The four bytes of x as pairs of codes, each pair as f16x2 (low nibble in the
-// low half).  The four take 2.2 cycles an SM of the ALU's 64 lanes; picking 4-bit
-// integers apart (shift, mask, subtract) would take twice that.
+// low half): four conversions, two cycles an SM of the ALU's 64 lanes.  Picking 4-bit
+// integers apart (shift, mask, subtract) takes three times that.
 __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
     asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\tmov.b32 {t0, t1, t2, t3}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, t0;\n\tcvt.rn.f16x2.e2m1x2 %1, t1;\n\t"
