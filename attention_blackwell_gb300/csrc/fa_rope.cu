@@ -91,8 +91,8 @@ template <int D> struct Lane {
         b = (split ? j + m : 2 * j + 1) * 8;
     }
     // From the unit's rows of the tables; sign -1: the angles' opposites.
-    __device__ __forceinline__ void angles(const RopeArgs& r, const float* table, int lane, float sign) {
-        if (!turns) return;
+    template <bool kWhole> __device__ __forceinline__ void angles(const RopeArgs& r, const float* table, int lane, float sign) {
+        if (!kWhole && !turns) return;
         const float4 *pc = reinterpret_cast<const float4*>(table + lane % kLanes * 8), *ps = reinterpret_cast<const float4*>(table + (r.rot >> 1) + lane % kLanes * 8);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -102,9 +102,12 @@ template <int D> struct Lane {
             ns[2 * i] = f2_pack(-sign * y.x, -sign * y.y), ns[2 * i + 1] = f2_pack(-sign * y.z, -sign * y.w);
         }
     }
-    __device__ __forceinline__ void turn(F2 (&v)[8], bool inter) const {
-        if (!turns) return;
-        if (!inter) {
+    // kWhole: all of a row, in halves, without a branch: a store into 4-bit pages, which
+    // is bound by its instructions, gains 5 % (20011 tokens stored and expanded 96 us, 91
+    // so); qk_rope, which HBM binds, gains nothing.
+    template <bool kWhole> __device__ __forceinline__ void turn(F2 (&v)[8], bool inter) const {
+        if (!kWhole && !turns) return;
+        if (kWhole || !inter) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const F2 x = v[i], y = v[4 + i];
@@ -330,28 +333,31 @@ template <int W, int N> __device__ __forceinline__ void init_barriers(uint64_t (
 // ------------------------------------------------------------------ forward
 
 // A unit's rows of q or k, normed and turned, to out(row).
-template <int D, class Out>
+template <int D, bool kWhole, class Out>
 __device__ __forceinline__ void turn_rows(const RopeArgs& r, Lane<D>& me, const Chunk& c, const uint8_t* in, const float* table, const float* s_w, const Out& out) {
     using Me = Lane<D>;
     const int lane = threadIdx.x & 31, sub = lane / Me::kLanes;
     const bool norm = c.what ? r.wk != nullptr : r.wq != nullptr;
-    me.angles(r, table, lane, 1.f);
-#pragma unroll
-    for (int p = 0; p < kChunk<D>; p += Me::kRows) {
-        if (p >= c.n) break;
+    me.template angles<kWhole>(r, table, lane, 1.f);
+    auto pass = [&](int p, bool real) {
         const int i = p + sub;
         F2 v[8] = {};
-        if (i < c.n) {
+        if (real) {
             unpack8(load16(in + (i * D + me.a) * 2), v);
             unpack8(load16(in + (i * D + me.b) * 2), v + 4);
         }
         if (norm) weigh<D>(v, inv_rms<D>(v, r.eps), s_w + (c.what ? D : 0), me);
-        me.turn(v, r.inter);
-        if (i < c.n) {
+        me.template turn<kWhole>(v, r.inter);
+        if (real) {
             __nv_bfloat16* dst = out(c.h0 + i);
             *reinterpret_cast<uint4*>(dst + me.a) = pack8(v);
             *reinterpret_cast<uint4*>(dst + me.b) = pack8(v + 4);
         }
+    };
+#pragma unroll (kWhole ? 1 : kChunk<D> / Me::kRows)
+    for (int p = 0; p < kChunk<D>; p += Me::kRows) {
+        if (p >= c.n) break;
+        pass(p, p + sub < c.n);
     }
 }
 
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) qk_rope_kernel(const RopeArgs 
                               [&](const Unit& u, const uint8_t* in, const float* table) {
         const Chunk c = chunk_of(r, u.j);
         __nv_bfloat16* to = c.what ? a.k_out + u.t * a.k_out_stride : a.q_out + u.t * a.q_out_stride;
-        turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
+        turn_rows<D, false>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
     });
 }
 
@@ -391,7 +397,7 @@ __device__ __forceinline__ void grad_row(const RopeArgs& r, const Lane<D>& me, b
         unpack8(load16(g + me.a * 2), u);
         unpack8(load16(g + me.b * 2), u + 4);
     }
-    me.turn(u, r.inter);
+    me.template turn<false>(u, r.inter);
     if (w) {
         F2 v[8] = {};
         if (real) {
@@ -447,15 +453,15 @@ __global__ void __launch_bounds__(32 * kWarpsGrad, 1) qk_rope_bwd_kernel(const R
     feed<D, kBytesGrad, 2, kRingGrad, kWarpsGrad>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRingGrad>::kWarp, full[warp], nullptr, rows,
                                   [&](const Unit& u, const uint8_t* in, const float* table) {
         const Chunk c = chunk_of(r, u.j);
-        me.angles(r, table, lane, -1.f);
+        me.template angles<false>(r, table, lane, -1.f);
         __nv_bfloat16* out = c.what ? a.dk + ((long long)u.t * r.Hkv + c.h0) * D : a.dq + ((long long)u.t * r.Hq + c.h0) * D;
         const uint8_t* g = in + sub * D * 2;
-        if (c.what == 0)
+        auto passes = [&](const float* w, F2 (&dw)[8]) {
             for (int p = 0; p < c.n; p += Me::kRows)
-                grad_row<D>(r, me, p + sub < c.n, g + p * D * 2, g + p * D * 2 + kBytesGrad, r.wq ? s_w : nullptr, dwq, out + (p + sub) * D);
-        else
-            for (int p = 0; p < c.n; p += Me::kRows)
-                grad_row<D>(r, me, p + sub < c.n, g + p * D * 2, g + p * D * 2 + kBytesGrad, r.wk ? s_w + D : nullptr, dwk, out + (p + sub) * D);
+                grad_row<D>(r, me, p + sub < c.n, g + p * D * 2, g + p * D * 2 + kBytesGrad, w, dw, out + (p + sub) * D);
+        };
+        if (c.what == 0) passes(r.wq ? s_w : nullptr, dwq);
+        else passes(r.wk ? s_w + D : nullptr, dwk);
     });
     if (!norm) return;
     // The warp's rows, then the block's warps; the rings are done with.
@@ -655,13 +661,13 @@ template <int D> struct Four {
 };
 
 // Rows of k or v into 4-bit pages, four rows a pass.
-template <int D>
+template <int D, bool kWhole>
 __device__ __forceinline__ void put_rows(const RopeArgs& r, const PutArgs& a, const Chunk& c, const uint8_t* in, const float* table, const float* s_w, long long cell) {
     const int lane = threadIdx.x & 31, l = lane & 7;
-    const bool isk = c.what == 1, norm = isk && r.wk != nullptr, whole = r.rot == D && !r.inter;
+    const bool isk = c.what == 1, norm = isk && r.wk != nullptr;
     const float* w = s_w + D;
     Four<D> turner;
-    if (isk) turner.angles(r, table, l, whole);
+    if (isk) turner.angles(r, table, l, kWhole);
 #pragma unroll 1
     for (int i = lane >> 3; i - (lane >> 3) < c.n; i += 4) {
         const bool real = i < c.n;
@@ -670,7 +676,7 @@ __device__ __forceinline__ void put_rows(const RopeArgs& r, const PutArgs& a, co
         float x = 1.f;
         norm_four<D>(r, row, norm, w, l, y, x);
         if (isk) {
-            if (whole) turner.turn_whole(y);
+            if (kWhole) turner.turn_whole(y);
             else turner.turn(r, row, x, norm ? w : nullptr, l, y);
         }
         const long long at = cell + ((long long)(c.h0 + i) << a.ps_log2);
@@ -678,7 +684,7 @@ __device__ __forceinline__ void put_rows(const RopeArgs& r, const PutArgs& a, co
     }
 }
 
-template <int D, bool kFour>
+template <int D, bool kFour, bool kWhole>
 __global__ void __launch_bounds__(32 * kWarpsPut, 1) rope_store_kernel(const RopeArgs r, const PutArgs a) {
     using Me = Lane<D>;
     extern __shared__ __align__(16) uint8_t dsmem[];
@@ -703,17 +709,17 @@ __global__ void __launch_bounds__(32 * kWarpsPut, 1) rope_store_kernel(const Rop
         const Chunk c = chunk_of(r, u.j);
         if (c.what == 0) {
             __nv_bfloat16* to = a.q_out + u.t * a.q_out_stride;
-            turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
+            turn_rows<D, kWhole>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
             return;
         }
         if (u.slot < 0 || u.slot >= a.num_slots) return;
         // Row of the cache that this token's head 0 is; head h is h pages of rows behind.
         const long long cell = (((long long)(u.slot >> a.ps_log2) * r.Hkv) << a.ps_log2) + (u.slot & ((1 << a.ps_log2) - 1));
         if constexpr (kFour) {
-            put_rows<D>(r, a, c, in, table, s_w, cell);
+            put_rows<D, kWhole>(r, a, c, in, table, s_w, cell);
         } else if (c.what == 1) {
             __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(a.kp);
-            turn_rows<D>(r, me, c, in, table, s_w, [&](int h) { return to + (cell + ((long long)h << a.ps_log2)) * D; });
+            turn_rows<D, kWhole>(r, me, c, in, table, s_w, [&](int h) { return to + (cell + ((long long)h << a.ps_log2)) * D; });
         } else {
             uint4* to = reinterpret_cast<uint4*>(a.vp);
             for (int i = lane; i < c.n * (D / 8); i += 32)
@@ -970,9 +976,11 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
                        (long long)num_pages * page_size};
     auto launch = [&](auto dim, auto bits4) {
         constexpr int D = decltype(dim)::value;
-        static std::atomic<uint64_t> prepared{0};
+        constexpr bool kFour = decltype(bits4)::value;
+        static std::atomic<uint64_t> prepared[2];
+        const bool whole = rot == D && !interleaved;
         const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, 1, weights_bf16, eps, kPass<D>, kChunk<D>, 2, kWarpsPut * sms, status);
-        return launch_rope(rope_store_kernel<D, decltype(bits4)::value>, prepared, grid_for(r.units, sms, kWarpsPut), 32 * kWarpsPut, kSmemPut<D>, stream, r, a);
+        return launch_rope(whole ? rope_store_kernel<D, kFour, true> : rope_store_kernel<D, kFour, false>, prepared[whole], grid_for(r.units, sms, kWarpsPut), 32 * kWarpsPut, kSmemPut<D>, stream, r, a);
     };
     auto pick = [&](auto bits4) {
         return d == 64 ? launch(std::integral_constant<int, 64>{}, bits4) : d == 128 ? launch(std::integral_constant<int, 128>{}, bits4)
