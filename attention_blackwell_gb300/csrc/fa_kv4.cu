@@ -11,12 +11,12 @@
 // fp16 weights.  A weight times a scale spans more than fp16 does, so weights are
 // kept relative to what matters for O: with 2^e_j the power of two over key j's
 // largest value scale,
-//   M = max (x_j + e_j),  p_j = 2^(x_j + e_j - M) in [0, 2^8],  t_jg 2^-e_j in [0, 4),
-// and what falls under fp16's 2^-24 is that much smaller than the largest term of
-// O, whatever the scales.  sum_j w_j = sum_j p_j 2^-e_j stays in 32 bits.  A query is
-// scaled by a power of two into [1, 2) at its largest element before it becomes
-// fp16, which all of bf16's 8 bits fit.  (p is rounded to 11 bits, p t again: less
-// than the 8 bits of a bf16 weight.)
+//   M = max (x_j + e_j),  p_j = 2^(x_j + e_j - M + 5) in [0, 2^13],  t_jg 2^-e_j in [0, 4),
+// so the largest is at least 2^6, and what falls under fp16's 2^-24 is 2^30 times
+// smaller than the largest term of O, whatever the scales.  sum_j w_j = sum_j p_j 2^-e_j
+// stays in 32 bits.  A query is scaled by a power of two into [2^14, 2^15) at its largest
+// element before it becomes fp16, which all of bf16's 8 bits fit down to 2^-31 of it.
+// (p is rounded to 11 bits, p t again: less than the 8 bits of a bf16 weight.)
 //
 // Few rows (single tokens, drafts): every warp is a worker with a range of the
 // flat list of (request, key/value head, row block, 64 keys) units, a ring of
@@ -65,6 +65,8 @@ namespace fa {
 namespace {
 
 constexpr float kTau = 8.0f;            // rescale threshold (log2 units)
+constexpr float kLift = 5.0f;           // a weight at the maximum is 2^5: 2^(kTau + kLift) times a scale below 4 fits fp16
+constexpr int kQLift = 14;              // a query's largest element becomes 2^14 or more
 constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every finite score; a hidden key's -inf less it is -inf
 constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
@@ -140,7 +142,7 @@ struct KvArgs {
     KvHeader* hdr;
     int* tables;             // [CTA][4 B + 3], B > kTableMost
     KvRow* rows;             // [T]
-    float2* ml;              // segments' rows: maximum, sum
+    float2* ml;              // segments' rows: maximum less kLift, sum
     float* seg;              // [segment][rows][D]
     int T, B, Hq, Hkv, G, W, P, ps_log2, max_seqlen;
     float scale_log2;
@@ -610,8 +612,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             }
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-            const int e = min(max((int)(__float_as_uint(most) >> 23), 1), 253);      // exponent field: 2^(e - 127)
-            const float down = __uint_as_float((uint32_t)(254 - e) << 23), up = a.scale_log2 * __uint_as_float((uint32_t)e << 23);
+            const int e = min(max((int)(__float_as_uint(most) >> 23), kQLift + 1), 254);      // exponent field: 2^(e - 127)
+            const float down = __uint_as_float((uint32_t)(254 + kQLift - e) << 23), up = a.scale_log2 * __uint_as_float((uint32_t)(e - kQLift) << 23);
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
                 const uint32_t w[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
@@ -747,8 +749,8 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             if (!(here >> (own + kt) & 1u) || k0 + (own + kt) * 16 + kr + (i >> 1) * 8 >= (i & 1 ? ll.y : ll.x)) z[kt][nt][i] = -INFINITY;
                     }
             }
-            // O and l follow a row's running maximum when it grows by more than kTau: only
-            // then do the lanes that share the row look for it together.
+            // O and l follow a row's running maximum (m: kLift below it) when it grows by more
+            // than kTau: only then do the lanes that share the row look for it together.
             bool jump = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
                     for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
-                    jump |= x - m[nt][i] > kTau;
+                    jump |= x - m[nt][i] > kTau + kLift;
                 }
             // Weights as B operands: row r, keys 2c, 2c + 1 and eight further.
             auto weigh = [&](int kt, uint32_t (&pt)[NT][2]) {
@@ -829,10 +831,11 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                         for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                        x = fmaxf(m[nt][i], fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                         if constexpr (kTeam)
 #pragma unroll
                             for (int w = 0; w < K::kTeam; ++w) x = fmaxf(x, row_m[w * K::kRows + nt * 8 + 2 * c + i]);
+                        x = fmaxf(m[nt][i], x - kLift);
                         const float fac = ex2_mufu(m[nt][i] - x);
                         l[nt][i] *= fac;
                         m[nt][i] = x;

@@ -11,7 +11,7 @@ Tolerances of the attention, elementwise:
 * the output is rounded to bf16 once: U |o|;
 * a score's error is at most e = 2^-23 (d + 8) reach + 2^-21 (1 + reach), reach =
   max_j alpha sum |q k| with |q| taken as at least 2^-8 of the row's largest (a query
-  becomes fp16 relative to that: 2^-25 an element off, far below): 2 e sum_j p_j
+  becomes fp16 relative to that, far finer): 2 e sum_j p_j
   |v_j|, and e in the logarithm of the sum, plus 2^-22 |lse| + 2^-20.
 """
 import math
@@ -290,6 +290,56 @@ def test_values_of_every_size(fa, d, n):
     b.vs[:] = 0
     o, _ = b.run(fa)
     assert (o == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3, 12])
+def test_many_keys_beside_one_that_takes_the_weight(fa, d, n):
+    """A key whose value is 0 has 2^23.5 times the weight of each of the others, which
+    make up all of O.  Their weights are 2^-18.5 in fp16, a multiple of 2^-24 (off by
+    at most 2^-25), times a scale below 4 rounded again (2^-25), codes up to 6: 30 *
+    2^-25 against a largest weight times scale of 2^6 at least, 2^-26 of it a key."""
+    b = Batch(4, 2, d, 16, [3001], [n], seed=d + n)
+    b.q[:] = 1.0
+    b.ks[:], b.vs[:] = 0, 0x60
+    b.vc &= 0x77                                     # values of one sign
+    page, at = b.table[0][40], 5
+    b.kc[page, :, at], b.ks[page, :, at], b.vc[page, :, at] = 0x77, 0x70, 0
+    b.alpha = 23.5 * math.log(2.0) / (6 * d * float(R.scales(np.uint8(0x70))))
+    o, lse = b.run(fa)
+    b.check(fa, o, lse)
+    want, _, mass, _, top = b.want()
+    # The same request 900 times: more work than workers, so items are not cut small.
+    q = torch.ones(900 * n, 4, d, dtype=torch.bfloat16, device="cuda")
+    pages = [u8(x) for x in (b.kc, b.ks, b.vc, b.vs)]
+    o, _ = fa.kv4_fwd(q, *pages, i32(b.table).repeat(900, 1), i32(b.s * 900), cu_seqlens=i32(range(0, 900 * n + 1, n)), max_seqlen=n, alpha=b.alpha)
+    assert fa.device_status() == 0
+    off = np.abs(o.double().cpu().numpy().reshape(900, n, 4, d) - want)
+    assert (off <= 2.0 ** -10 * mass + U * np.abs(want) + 2.0 ** -26 * top).all(), (off / (2.0 ** -26 * top)).max()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3, 12])
+def test_small_elements_of_a_query_beside_large_ones(fa, d, n):
+    """A query whose first 32 elements are 2^22 times the others, over keys that are 0
+    there: the score's error scales with what the products are, without a floor."""
+    b = Batch(4, 2, d, 16, [500], [n], seed=d + n, std=1.0)
+    b.q[..., :32] *= 1024.0
+    b.q[..., 32:] *= 2.0 ** -12
+    b.ks[..., 0] = 0
+    b.alpha = 2.0 ** 12 / math.sqrt(d)
+    _, lse = b.run(fa)
+    assert fa.device_status() == 0
+    k = R.unpack(b.kc, b.ks)
+    at, pg = np.arange(500) % 16, np.array([b.table[0][j // 16] for j in range(500)])
+    q = b.q.double().cpu().numpy()
+    for t in range(n):
+        for h in range(4):
+            K = k[pg, h // 2, at][:500 - n + t + 1]
+            x, reach = b.alpha * (K @ q[t, h]), b.alpha * (np.abs(K) @ np.abs(q[t, h])).max()
+            want = x.max() + math.log(np.exp(x - x.max()).sum())
+            e = 2.0 ** -23 * (d + 8) * reach + 2.0 ** -21 * (1 + reach)
+            assert abs(lse[h, t].item() - want) <= e + 2.0 ** -22 * abs(want) + 2.0 ** -20, (t, h)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
