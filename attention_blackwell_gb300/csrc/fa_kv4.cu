@@ -221,11 +221,13 @@ struct KvWalk {
     }
 };
 
-struct KvShared {
+struct KvScan {
+    int2 scan[20];
+    int abort_flag, bad;
+};
+struct KvShared : KvScan {
     uint64_t full[16][8];
     uint32_t live[8][8];                 // teams: a slot's parts that have a page
-    int2 scan[16];
-    int abort_flag, bad;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -252,12 +254,12 @@ __device__ __forceinline__ bool kv_wait(uint64_t* bar, uint32_t parity, volatile
 }
 
 // The list's tables, by every thread of the block; offsets by the library's one rule.
-template <int D, int NT>
-__device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables& t, KvShared& sh, int tid) {
+template <class K>
+__device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables& t, KvScan& sh, int tid) {
     const int lane = tid & 31, warp = tid >> 5;
     const long long cap = (long long)a.W << a.ps_log2;
     bool fine = true;
-    for (int i = tid; i <= a.B; i += Kv<D, NT>::kThreads) {
+    for (int i = tid; i <= a.B; i += K::kThreads) {
         const int c = a.cu ? a.cu[i] : i, before = a.cu && i > 0 ? a.cu[i - 1] : 0;
         fine = fine && c >= before && c >= 0 && c <= a.T;
         t.cu[i] = c;
@@ -279,14 +281,14 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
         __syncthreads();
     }
     int units = 0, items = 0;
-    constexpr int kThreads = Kv<D, NT>::kThreads, kWarps = Kv<D, NT>::kWarps;
+    constexpr int kThreads = K::kThreads, kWarps = kThreads / 32;
     for (int base = 0; base < a.B; base += kThreads) {
         const int i = base + tid;
         int u = 0, it = 0;
         if (i < a.B) {
             const int n = t.cu[i + 1] - t.cu[i];
             if (n > a.max_seqlen) sh.bad = 1;
-            it = row_blocks(n, a.G, Kv<D, NT>::kRows) * a.Hkv;
+            it = row_blocks(n, a.G, K::kRows) * a.Hkv;
             u = it * item_units(t.len[i]);
         }
         const int u_own = u, it_own = it;
@@ -314,7 +316,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
     }
     __syncthreads();
     KvHeader h = {};
-    const int workers = gridDim.x * Kv<D, NT>::kWorkers;
+    const int workers = gridDim.x * K::kWorkers;
     h.per = units / workers;
     h.more = units - h.per * workers;
     h.bad = sh.bad;
@@ -323,6 +325,33 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
         if (h.bad && atomicCAS(&a.status->code, 0, -1) == 0) { a.status->where = 111; a.status->block = 0; }
     }
     return h;
+}
+
+// What the joining kernel needs to know of each row.
+template <class K> __device__ __forceinline__ void fill_rows(const KvArgs& a, const KvTables& t, int tid) {
+    for (int i = blockIdx.x * K::kThreads + tid; i < a.T; i += gridDim.x * K::kThreads) {
+        KvRow row = {};
+        if (i >= t.cu[0] && i < t.cu[a.B]) {
+            int lo = 0;
+            for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
+                const int mid = (lo + hi) >> 1;
+                if (t.cu[mid] <= i) lo = mid; else hi = mid;
+            }
+            row.c0 = t.cu[lo];
+            row.n = t.cu[lo + 1] - row.c0;
+            row.s = t.len[lo];
+            row.pref = t.pref[lo];
+            row.items = t.items[lo];
+        }
+        a.rows[i] = row;
+    }
+}
+
+// Small block tables on their way to L2 while the list is made: the first lookup is
+// on the way to every worker's first copy.
+template <class K> __device__ __forceinline__ void prefetch_tables(const KvArgs& a, int tid) {
+    const long long bytes = (long long)a.B * a.W * 4, line = ((long long)blockIdx.x * K::kThreads + tid) * 128;
+    if (bytes <= kPrefetchMost && line < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(a.table) + line));
 }
 
 // ------------------------------------------------------------------ products
@@ -482,31 +511,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     if (tid == 0) sh.abort_flag = 0;
     grid_launch_next();
     grid_wait();
-    // Small block tables on their way to L2 while the list is made: the first lookup is
-    // on every warp's way to its first copy.
-    {
-        const long long bytes = (long long)a.B * a.W * 4, line = ((long long)blockIdx.x * K::kThreads + tid) * 128;
-        if (bytes <= kPrefetchMost && line < bytes) asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t*>(a.table) + line));
-    }
-    const KvHeader hdr = build_tables<D, NT>(a, t, sh, tid);
+    prefetch_tables<K>(a, tid);
+    const KvHeader hdr = build_tables<K>(a, t, sh, tid);
 
-    // What the joining kernel needs to know of each row.
-    for (int i = blockIdx.x * K::kThreads + tid; i < a.T; i += gridDim.x * K::kThreads) {
-        KvRow row = {};
-        if (i >= t.cu[0] && i < t.cu[a.B]) {
-            int lo = 0;
-            for (int hi = a.B; hi - lo > 1;) {   // the last request that begins at or before i
-                const int mid = (lo + hi) >> 1;
-                if (t.cu[mid] <= i) lo = mid; else hi = mid;
-            }
-            row.c0 = t.cu[lo];
-            row.n = t.cu[lo + 1] - row.c0;
-            row.s = t.len[lo];
-            row.pref = t.pref[lo];
-            row.items = t.items[lo];
-        }
-        a.rows[i] = row;
-    }
+    fill_rows<K>(a, t, tid);
 
     const int team = warp / K::kTeam, member = warp % K::kTeam;
     uint64_t* full = sh.full[team];
@@ -970,6 +978,505 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     }
 }
 
+// ----------------------------------------------------------------- more rows
+
+// Items of N rows on the fifth-generation tensor cores: a CTA is a worker, 128 keys a
+// tile.  Codes become fp16 in shared memory, scaled there (K's and V's rows by their
+// scales relative to the row's largest, which a code times is exact in fp16), in the
+// order in which a row's codes lie; Q has the same order, and O's is undone where it is
+// written.  S^T = K Q^T has keys as lanes, O^T = V^T P^T elements of d.
+template <int D, int N> struct Mid {
+    static constexpr int kRows = N, kThreads = 608, kWorkers = 1, kHalves = D / 128;
+    static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
+    static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
+    static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
+    static constexpr uint32_t kV = kTile, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + 2 * kQBox, kRawV = kRawK + kRing * kSlotK;
+    // What the softmax wants of four tiles' keys; rows: less their maximum, factors, what a
+    // sum is multiplied by, keys seen, maxima or sums of four quarters.
+    static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRowM = kKeys + 4 * 128 * 4,
+                              kRowF = kRowM + N * 4, kRowUp = kRowF + N * 4, kRowLim = kRowUp + N * 4, kRowX = kRowLim + N * 4, kWarp = kRowX + 4 * N * 4;
+    static constexpr uint32_t kColumns = N * (2 + kHalves) <= 64 ? 64 : 128;
+    static_assert((N == 16 || N == 32) && (D == 128 || D == 256), "sizes built");
+    static_assert(kRawK % 1024 == 0 && kWarp % 16 == 0 && kWarp + table_bytes(kTableMost) + 1024 <= 232448, "shared memory plan");
+};
+struct MidShared : KvScan {
+    uint64_t k_raw_full[4], k_raw_empty[4], v_raw_full[4], v_raw_empty[4], k_full, v_full, q_full, s_full[2], p_full, pv_done, drain;
+    uint32_t live[4], tmem;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
+    return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// S^T = K Q^T: both K-major.
+template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, uint32_t k_smem, uint32_t q_smem) {
+    using K = Mid<D, N>;
+    constexpr uint32_t idesc = idesc_f16_f32(128, N, 0, 0);
+    const uint64_t ad = sdesc_sw128(k_smem, 16, 1024), bd = sdesc_sw128(q_smem, 16, 1024);
+    static_for<D / 16>([&](auto kc) {
+        constexpr uint32_t k = kc, ao = ((k >> 2) * K::kBox + (k & 3) * 32) >> 4, bo = ((k >> 2) * K::kQBox + (k & 3) * 32) >> 4;
+        umma_ss_k<ao, bo>(s, ad, bd, idesc, k > 0 ? 1u : 0u);
+    });
+}
+// O^T (+)= V^T P^T for 128 of d: V's rows read MN-major (two boxes of 64 elements), P
+// K-major (rows of keys, two boxes of 64 keys).
+template <int D, int N> __device__ __forceinline__ void mid_values(uint32_t o, uint32_t v_smem, uint32_t p_smem, uint32_t acc) {
+    using K = Mid<D, N>;
+    constexpr uint32_t idesc = idesc_f16_f32(128, N, 1, 0);
+    const uint64_t ad = sdesc_sw128(v_smem, K::kBox, 1024), bd = sdesc_sw128(p_smem, 16, 1024);
+    static_for<8>([&](auto kc) {
+        constexpr uint32_t k = kc, ao = (k * 2048) >> 4, bo = ((k >> 2) * K::kQBox + (k & 3) * 32) >> 4;
+        umma_ss_k<ao, bo>(o, ad, bd, idesc, (acc | k) != 0);
+    });
+}
+
+// A key's scales (f16 pairs) times 2^(26 - field), each twice; returns the exponent
+// field of the largest (1 to 30).
+template <int D> __device__ __forceinline__ uint32_t mid_scales(const uint32_t (&h)[D / 64], uint32_t (&sc)[D / 32]) {
+    uint32_t m = h[0];
+#pragma unroll
+    for (int i = 1; i < D / 64; ++i) m = hmax2(m, h[i]);
+    m = hmax2(m, __byte_perm(m, m, 0x1032));
+    const uint32_t ex = hmin2(hmax2(m, 0x04000400u), 0x78007800u) & 0x7c007c00u, down = 0x7c007c00u - ex;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        const uint32_t x = hmul2(hmul2(h[i], down), 0x64006400u);        // 2^10
+        sc[2 * i] = __byte_perm(x, x, 0x1010);
+        sc[2 * i + 1] = __byte_perm(x, x, 0x3232);
+    }
+    return ex >> 26;
+}
+// Half of a key's codes into its row of a tile.  Lanes are keys; which 16 bytes each
+// takes first depends on its key, so that neither loads nor stores meet in a bank.
+template <int D> __device__ __forceinline__ void mid_expand(const uint8_t* codes, uint8_t* tile, int key, int half, const uint32_t (&sc)[D / 32]) {
+    constexpr int kC = D / 32, kG = D / 32;      // 16-byte pieces of a row
+    const int turn = (D == 256 ? key : key >> 1) + half * (kC / 2);
+    const uint8_t* row = codes + key * (D / 2);
+    uint8_t* to = tile + key * 128;
+    uint32_t w[kC / 2][4];
+#pragma unroll
+    for (int j = 0; j < kC / 2; ++j) lds(row + ((j + turn) & (kC - 1)) * 16, w[j]);
+#pragma unroll
+    for (int j = 0; j < kC / 2; ++j) {
+        const int c = (j + turn) & (kC - 1);
+        uint8_t* box = to + (c >> 1) * (128 * 128);
+        const int first = (c & 1) * 4;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t x[4];
+            codes_f16(w[j][k], x[0], x[1], x[2], x[3]);
+            constexpr int kMask = kG - 1;
+            x[0] = hmul2(x[0], sc[2 * k & kMask]);
+            x[1] = hmul2(x[1], sc[2 * k & kMask]);
+            x[2] = hmul2(x[2], sc[(2 * k & kMask) + 1]);
+            x[3] = hmul2(x[3], sc[(2 * k & kMask) + 1]);
+            sts(box + (((first + k) ^ (key & 7)) * 16), x);
+        }
+    }
+}
+// The element that position x of a row's codes is.
+template <int D> __device__ __forceinline__ int element_at(int x) {
+    const int u = x >> 2;
+    return u % (D / 32) * 32 + u / (D / 32) * 4 + (x & 3);
+}
+// For each of N columns, op over the warp's lanes: lane l gets column l % N.
+template <int N, class Op> __device__ __forceinline__ float over_lanes(float (&v)[N], int lane, const Op& op) {
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float keep = lane & o ? v[i + o] : v[i], send = lane & o ? v[i] : v[i + o];
+            v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+#pragma unroll
+    for (int o = N; o < 32; o *= 2) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+    return v[0];
+}
+template <int N> __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_ld16(at, r);
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at));
+    tmem_wait_ld();
+}
+template <int N> __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_st16(at, r);
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                     ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Warps 0 to 7 do the softmax (a quarter of the keys, at the end of d, and half the rows
+// each), 8 to 15 expand (two threads a key), 16 and 17 copy, 18 issues products.  K of
+// a tile is expanded before V of the tile before, so scores are ahead of weights by one.
+template <int D, int N>
+__global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
+    using K = Mid<D, N>;
+    using Walk = KvWalk<N>;
+    constexpr int kG = D / 32, kC = N / 2;
+    constexpr uint32_t kRing = K::kRing;
+    extern __shared__ __align__(1024) uint8_t dsmem_tiles[];
+    __shared__ MidShared sh;
+    uint8_t* const dsmem = dsmem_tiles;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    KvTables t;
+    t.pref = a.B <= kTableMost ? reinterpret_cast<int*>(dsmem + K::kWarp) : a.tables + (long long)blockIdx.x * (4 * a.B + 3);
+    t.items = t.pref + a.B + 1;
+    t.cu = t.items + a.B + 1;
+    t.len = t.cu + a.B + 1;
+    if (tid == 0) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.k_raw_full[i], 1);
+            mbar_init(&sh.k_raw_empty[i], 8);
+            mbar_init(&sh.v_raw_full[i], 1);
+            mbar_init(&sh.v_raw_empty[i], 8);
+        }
+        mbar_init(&sh.k_full, 8);
+        mbar_init(&sh.v_full, 8);
+        mbar_init(&sh.q_full, 8);
+        mbar_init(&sh.s_full[0], 1);
+        mbar_init(&sh.s_full[1], 1);
+        mbar_init(&sh.p_full, 8);
+        mbar_init(&sh.pv_done, 1);
+        mbar_init(&sh.drain, 1);
+        fence_mbar_init();
+        sh.abort_flag = 0;
+    }
+    if (warp == 18) {
+        tmem_alloc(&sh.tmem, K::kColumns);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    grid_launch_next();
+    grid_wait();
+    prefetch_tables<K>(a, tid);
+    const KvHeader hdr = build_tables<K>(a, t, sh, tid);
+    fill_rows<K>(a, t, tid);
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem, smem = smem_u32(dsmem);
+    // Exponent fields of K's and V's largest scales, the tile's parts that are there.
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(dsmem + K::kKeys);
+    Walk walk;
+    walk.start(a, t, hdr, blockIdx.x);
+    KvItem it;
+    bool ok = true;
+    uint32_t tile = 0;                               // tiles of this CTA so far
+    if (warp < 8) {
+        const int quarter = warp & 3, c0 = (warp >> 2) * kC, key = quarter * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)quarter << 21) + c0;
+        float *const row_m = reinterpret_cast<float*>(dsmem + K::kRowM) + c0, *const row_f = reinterpret_cast<float*>(dsmem + K::kRowF) + c0,
+              *const row_up = reinterpret_cast<float*>(dsmem + K::kRowUp) + c0, *const row_x = reinterpret_cast<float*>(dsmem + K::kRowX) + c0;
+        int* const row_lim = reinterpret_cast<int*>(dsmem + K::kRowLim) + c0;
+        uint8_t* const p_key = dsmem + K::kP + (quarter >> 1) * K::kQBox + c0 * 128 + (key & 7) * 2;
+        const int p_piece = (key & 63) >> 3;
+        while (ok && walk.next(a, t, it)) {
+            // Q in the codes' order, scaled by a power of two.
+            constexpr int kW = D / 8, kPer = 32 / kW, kPasses = N / 8 / kPer;      // 16-byte pieces of a row of fp16; rows a pass
+            const int w = lane % kW, e0 = element_at<D>(8 * w);
+            uint2 in[kPasses][2];
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int x = (warp * kPasses + i) * kPer + lane / kW;
+                const uint32_t row = (uint32_t)it.rb * N + x;
+                const int tok = (int)(row / (uint32_t)a.G), h = (int)row - tok * a.G;
+                in[i][0] = in[i][1] = make_uint2(0, 0);
+                if (x < it.rows) {
+                    const __nv_bfloat16* src = a.q + (long long)(it.c0 + tok) * a.q_stride + (it.hk * a.G + h) * D + e0;
+                    in[i][0] = *reinterpret_cast<const uint2*>(src);
+                    in[i][1] = *reinterpret_cast<const uint2*>(src + 32);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int x = (warp * kPasses + i) * kPer + lane / kW;
+                const uint32_t v[4] = {in[i][0].x, in[i][0].y, in[i][1].x, in[i][1].y};
+                float most = 0.f;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) most = fmax3(most, fabsf(__uint_as_float(v[y] << 16)), fabsf(__uint_as_float(v[y] & 0xffff0000u)));
+#pragma unroll
+                for (int o = kW / 2; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+                const int e = min(max((int)(__float_as_uint(most) >> 23), kQLift + 1), 254);
+                const float down = __uint_as_float((uint32_t)(254 + kQLift - e) << 23);
+                uint32_t q[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) q[y] = pack_f16x2(__uint_as_float(v[y] << 16) * down, __uint_as_float(v[y] & 0xffff0000u) * down);
+                sts(dsmem + K::kQ + (w >> 3) * K::kQBox + x * 128 + ((w & 7) ^ (x & 7)) * 16, q);
+                if (w == 0) {
+                    row_up[x - c0] = a.scale_log2 * __uint_as_float((uint32_t)(e - kQLift) << 23);
+                    row_m[x - c0] = -kNone;
+                    row_lim[x - c0] = min(it.s, it.s - it.n + (int)(((uint32_t)it.rb * N + x) / (uint32_t)a.G) + 1);
+                }
+            }
+            fence_async_smem();
+            team_sync<8>(0);
+            if (lane == 0) mbar_arrive(&sh.q_full);
+            const int lim_min = row_lim[0];
+            uint64_t l[kC / 2];
+#pragma unroll
+            for (int i = 0; i < kC / 2; ++i) l[i] = 0;
+            for (int p = it.p0; p < it.p1; p += 8, ++tile) {
+                ok = kv_wait(&sh.s_full[tile & 1], tile >> 1 & 1, &sh.abort_flag) && ok;
+                tc_fence_after();
+                uint32_t r[kC];
+                tmem_ld<kC>(lanes + (tile & 1) * N, r);
+                // K's scale is 2^(field - 26) times what it was expanded with, V's e is field - 16.
+                const uint32_t info = keys[(tile & 3) * 128 + key], here = info >> 16;
+                const float ek = __uint_as_float((101u + (info & 255u)) << 23), ev = __uint_as_float(0x4b000000u | (info >> 8 & 255u)) - 8388624.f,
+                            back = __uint_as_float((143u - (info >> 8 & 255u)) << 23);
+                float z[kC], most = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kC; i += 2)
+                    f2_unpack(f2_fma(f2_mul(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), f2_pack(ek, ek)), *reinterpret_cast<const uint64_t*>(row_up + i), f2_pack(ev, ev)), z[i], z[i + 1]);
+                if (p * 16 + 128 > lim_min || here != 255u) {
+                    const bool gone = !(here >> (key >> 4) & 1u);
+#pragma unroll
+                    for (int i = 0; i < kC; ++i)
+                        if (gone || p * 16 + key >= row_lim[i]) z[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < kC; i += 2) {
+                    float y[2];
+                    f2_unpack(f2_add(f2_pack(z[i], z[i + 1]), *reinterpret_cast<const uint64_t*>(row_m + i)), y[0], y[1]);
+                    most = fmax3(most, y[0], y[1]);
+                }
+                // O and l follow a row's running maximum as above.
+                if (team_or<8>(0, most > kTau + kLift || !ok)) {
+                    if (ok && tile) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag);
+                    ok = !team_or<8>(0, !ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    float v[kC];
+#pragma unroll
+                    for (int i = 0; i < kC; ++i) v[i] = z[i];
+                    const float x = over_lanes<kC>(v, lane, [](float y, float u) { return fmaxf(y, u); });
+                    if (lane < kC) row_x[quarter * N + lane] = x;
+                    team_sync<8>(0);
+                    if (quarter == 0 && lane < kC) {
+                        const float m = -row_m[lane], next = fmaxf(m, fmaxf(fmaxf(row_x[lane], row_x[N + lane]), fmaxf(row_x[2 * N + lane], row_x[3 * N + lane])) - kLift);
+                        row_f[lane] = ex2_mufu(m - next);
+                        row_m[lane] = -next;
+                    }
+                    team_sync<8>(0);
+#pragma unroll
+                    for (int i = 0; i < kC; i += 2) l[i / 2] = f2_mul(l[i / 2], *reinterpret_cast<const uint64_t*>(row_f + i));
+                    if (p > it.p0) {
+#pragma unroll
+                        for (int h = 0; h < K::kHalves; ++h) {
+                            tmem_ld<kC>(lanes + N * (2 + h), r);
+#pragma unroll
+                            for (int i = 0; i < kC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * row_f[i]);
+                            tmem_st<kC>(lanes + N * (2 + h), r);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                uint32_t weights[kC / 2];
+#pragma unroll
+                for (int i = 0; i < kC; i += 2) {
+                    float y[2];
+                    f2_unpack(f2_add(f2_pack(z[i], z[i + 1]), *reinterpret_cast<const uint64_t*>(row_m + i)), y[0], y[1]);
+                    y[0] = ex2_mufu(y[0]);
+                    y[1] = ex2_mufu(y[1]);
+                    l[i / 2] = f2_fma(f2_pack(y[0], y[1]), f2_pack(back, back), l[i / 2]);
+                    weights[i / 2] = pack_f16x2(y[0], y[1]);
+                }
+                // The weights before are multiplied.
+                if (tile) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag) && ok;
+#pragma unroll
+                for (int i = 0; i < kC; ++i)
+                    *reinterpret_cast<uint16_t*>(p_key + i * 128 + ((p_piece ^ (i & 7)) << 4)) = (uint16_t)(weights[i / 2] >> (i & 1 ? 16 : 0));
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full);
+            }
+            if (ok) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag);
+            tc_fence_after();
+            float v[kC];
+#pragma unroll
+            for (int i = 0; i < kC; i += 2) f2_unpack(l[i / 2], v[i], v[i + 1]);
+            const float sum = over_lanes<kC>(v, lane, [](float x, float y) { return x + y; });
+            if (lane < kC) row_x[quarter * N + lane] = sum;
+            ok = !team_or<8>(0, !ok);
+            if (!ok) break;
+            if (quarter == 0 && lane < kC) {
+                const float total = row_x[lane] + row_x[N + lane] + row_x[2 * N + lane] + row_x[3 * N + lane], m = -row_m[lane];
+                // V's rows are 2^10 times what they stand for.
+                row_f[lane] = !it.whole ? 0.0009765625f : total == 0.f ? 0.f : 0.0009765625f / total;
+                if (c0 + lane < it.rows) {
+                    if (it.whole) {
+                        const uint32_t row = (uint32_t)it.rb * N + c0 + lane;
+                        const int tok = (int)(row / (uint32_t)a.G), h = it.hk * a.G + (int)row - tok * a.G;
+                        a.lse[(long long)h * a.T + it.c0 + tok] = total == 0.f ? -INFINITY : (m + __log2f(total)) * 0.69314718055994531f;
+                    } else {
+                        a.ml[(long long)it.seg * N + c0 + lane] = make_float2(m, total);
+                    }
+                }
+            }
+            team_sync<8>(0);
+#pragma unroll
+            for (int h = 0; h < K::kHalves; ++h) {
+                uint32_t r[kC];
+                tmem_ld<kC>(lanes + N * (2 + h), r);
+                const int e = element_at<D>(h * 128 + key);
+                if (it.whole) {
+                    const uint32_t row = (uint32_t)it.rb * N + c0;
+                    int tok = (int)(row / (uint32_t)a.G), hh = (int)row - tok * a.G;
+#pragma unroll
+                    for (int i = 0; i < kC; ++i) {
+                        if (c0 + i < it.rows)
+                            a.o[((long long)(it.c0 + tok) * a.Hq + it.hk * a.G + hh) * D + e] = __float2bfloat16(row_f[i] == 0.f ? 0.f : __uint_as_float(r[i]) * row_f[i]);
+                        if (++hh == a.G) hh = 0, ++tok;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kC; ++i)
+                        if (c0 + i < it.rows) a.seg[((long long)it.seg * N + c0 + i) * D + e] = __uint_as_float(r[i]) * row_f[i];
+                }
+            }
+            tc_fence_before();
+            team_sync<8>(0);                         // the rows' numbers are read
+        }
+    } else if (warp < 16) {
+        const int key = tid & 127, half = warp >= 12;
+        bool more = walk.next(a, t, it);
+        int p = it.p0;
+        // K of the next tile, and what is left of its V's scales.
+        auto expand_k = [&](uint32_t (&hv)[D / 64]) -> bool {
+            const uint32_t slot = tile % kRing;
+            const uint8_t *const raw = dsmem + K::kRawK + slot * K::kSlotK, *const ks = raw + 8 * K::kCodes, *const vs = ks + 8 * K::kScales;
+            if (!kv_wait(&sh.k_raw_full[slot], tile / kRing & 1, &sh.abort_flag)) return false;
+            const uint32_t here = sh.live[slot];
+            const bool real = (here >> (key >> 4) & 1u) && p * 16 + key < it.seen;
+            uint32_t hk[D / 64], sc[kG];
+            scale_pairs<D>(vs + key * kG, real, hv);
+            const uint32_t fv = mid_scales<D>(hv, sc);
+            scale_pairs<D>(ks + key * kG, true, hk);
+            const uint32_t fk = mid_scales<D>(hk, sc);
+            // The tile before is done with K's rows.
+            if (tile && !kv_wait(&sh.s_full[(tile - 1) & 1], (tile - 1) >> 1 & 1, &sh.abort_flag)) return false;
+            if (!half) keys[(tile & 3) * 128 + key] = fk | fv << 8 | here << 16;
+            mid_expand<D>(raw, dsmem, key, half, sc);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.k_full);
+                mbar_arrive(&sh.k_raw_empty[slot]);
+            }
+            ++tile;
+            p += 8;
+            if (p >= it.p1) {
+                more = walk.next(a, t, it);
+                p = it.p0;
+            }
+            return true;
+        };
+        uint32_t now[D / 64], next[D / 64] = {};
+        if (more) ok = expand_k(now);
+        for (uint32_t done = 0; ok && done < tile; ++done) {
+            if (more && !(ok = expand_k(next))) break;
+            const uint32_t slot = done % kRing;
+            uint32_t sc[kG];
+            mid_scales<D>(now, sc);
+            if (!(ok = kv_wait(&sh.v_raw_full[slot], done / kRing & 1, &sh.abort_flag))) break;
+            if (done && !(ok = kv_wait(&sh.pv_done, (done - 1) & 1, &sh.abort_flag))) break;
+            mid_expand<D>(dsmem + K::kRawV + slot * K::kSlotV, dsmem + K::kV, key, half, sc);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sh.v_full);
+                mbar_arrive(&sh.v_raw_empty[slot]);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) now[i] = next[i];
+        }
+    } else if (warp < 18) {
+        // K's codes and both scales, or V's codes: one copy for the parts of a tile that
+        // are in one page (a copy costs its warp 85 cycles).
+        const bool v = warp == 17;
+        uint64_t *const full = v ? sh.v_raw_full : sh.k_raw_full, *const empty = v ? sh.v_raw_empty : sh.k_raw_empty;
+        const int what = lane & 3, which = lane >> 2, run_log2 = a.ps_log2 - 4;
+        const bool copies = v ? what == 0 : what < 3;
+        const uint8_t* const from = v ? a.vp : what == 0 ? a.kp : what == 1 ? a.ks : a.vs;
+        const uint32_t bytes = what == 0 ? K::kCodes : K::kScales, slot_bytes = v ? K::kSlotV : K::kSlotK, part_bytes = slot_bytes / 8;
+        const uint32_t into = smem + (v ? K::kRawV : K::kRawK) + (what == 0 ? 0 : 8 * K::kCodes + (what - 1) * 8 * K::kScales) + which * bytes;
+        while (ok && walk.next(a, t, it)) {
+            auto pages = [&](int p) -> int {         // of parts p .. p + 31
+                if (p + lane >= it.p1) return -1;
+                const int x = a.table[(long long)it.b * a.W + ((p + lane) * 16 >> a.ps_log2)];
+                return x >= 0 && x < a.P ? x : -1;
+            };
+            int win = pages(it.p0), win_next = pages(it.p0 + 32);
+            for (int p = it.p0; p < it.p1; p += 8, ++tile) {
+                if (p != it.p0 && ((p - it.p0) & 31) == 0) {
+                    win = win_next;
+                    win_next = pages(p + 32);
+                }
+                const uint32_t slot = tile % kRing;
+                if (tile >= kRing && !(ok = kv_wait(&empty[slot], (tile / kRing & 1) ^ 1, &sh.abort_flag))) break;
+                const int page = __shfl_sync(0xffffffffu, win, (p - it.p0 + which) & 31);
+                const uint32_t on4 = __ballot_sync(0xffffffffu, what == 0 && page >= 0);      // bit 4 i: part i
+                if (lane == 0) {
+                    if (!v) {
+                        uint32_t on = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) on |= (on4 >> (4 * i) & 1u) << i;
+                        sh.live[slot] = on;
+                    }
+                    if (on4) mbar_arrive_expect_tx(&full[slot], part_bytes * __popc(on4));
+                    else mbar_arrive(&full[slot]);
+                }
+                __syncwarp();
+                const int in_page = (p + which) & ((1 << run_log2) - 1);
+                if (copies && page >= 0 && (which == 0 || in_page == 0)) {
+                    const int run = min(min((1 << run_log2) - in_page, 8 - which), it.p1 - p - which);
+                    const long long row = (((long long)page * a.Hkv + it.hk) << a.ps_log2) + in_page * 16;
+                    bulk_load(into + slot * slot_bytes, from + row * (what == 0 ? D / 2 : D / 32), run * bytes, &full[slot]);
+                }
+            }
+        }
+        // Every copy lands before the block ends.
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = tile < kRing ? 0 : tile - kRing; i < tile; ++i)
+            while (!mbar_try_wait(smem_u32(&full[i % kRing]), i / kRing & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+    } else {
+        uint32_t items = 0;
+        auto scores = [&](uint32_t i) -> bool {
+            if (!kv_wait(&sh.k_full, i & 1, &sh.abort_flag)) return false;
+            tc_fence_after();
+            mid_scores<D, N>(tmem + (i & 1) * N, smem, smem + K::kQ);
+            umma_commit_w(&sh.s_full[i & 1]);
+            return true;
+        };
+        while (ok && walk.next(a, t, it)) {
+            if (!(ok = kv_wait(&sh.q_full, items++ & 1, &sh.abort_flag)) || !(ok = scores(tile))) break;
+            for (int p = it.p0; p < it.p1; p += 8, ++tile) {
+                if (p + 8 < it.p1 && !(ok = scores(tile + 1))) break;
+                if (!(ok = kv_wait(&sh.v_full, tile & 1, &sh.abort_flag) && kv_wait(&sh.p_full, tile & 1, &sh.abort_flag))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < K::kHalves; ++h) mid_values<D, N>(tmem + N * (2 + h), smem + K::kV + h * 2 * K::kBox, smem + K::kP, p > it.p0);
+                umma_commit_w(&sh.pv_done);
+            }
+        }
+        if (!ok) {                                   // products in flight end before their memory is given back
+            umma_commit_w(&sh.drain);
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (tid == 0 && sh.abort_flag && atomicCAS(&a.status->code, 0, kStatusTimeout) == 0) {
+        a.status->where = 113;
+        a.status->block = blockIdx.x;
+    }
+    if (warp == 18) tmem_dealloc(tmem, K::kColumns);
+}
+
 // Joins the segments of a row (of one head) that a range's end has cut; writes the
 // rows without a key.  A warp a row, or with few rows a block of eight.
 template <int D, bool kSplit>
@@ -1182,16 +1689,13 @@ ManyLayout many_layout(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int
     return w;
 }
 
-template <int D, int NT>
-int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
-    using K = Kv<D, NT>;
-    auto kern = kv4_kernel<D, NT>;
-    const size_t smem = K::kWorkers * K::kWarp + (a.B <= kTableMost ? table_bytes(a.B) : 0);
-    static std::atomic<uint64_t> prepared{0};
+template <class K, int D>
+int launch_few(void (*kern)(KvArgs), std::atomic<uint64_t>& prepared, const KvArgs& a, int sms, cudaStream_t stream) {
+    const size_t plan = K::kWorkers * K::kWarp, smem = plan + (a.B <= kTableMost ? table_bytes(a.B) : 0);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return FA_ERR_LAUNCH;
     if (!(prepared.load(std::memory_order_relaxed) >> dev & 1)) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(K::kWorkers * K::kWarp + table_bytes(kTableMost))) != cudaSuccess) return FA_ERR_LAUNCH;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(plan + table_bytes(kTableMost))) != cudaSuccess) return FA_ERR_LAUNCH;
         prepared.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
@@ -1204,6 +1708,14 @@ int launch_few(const KvArgs& a, int sms, cudaStream_t stream) {
     if (rows <= 8LL * sms) e = launch_dependent(kv4_join_kernel<D, true>, (int)rows, 256, 0, stream, a, K::kRows);
     else e = launch_dependent(kv4_join_kernel<D, false>, (int)((rows + 7) / 8), 256, 0, stream, a, K::kRows);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+template <int D, int NT> int launch_warps(const KvArgs& a, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> prepared{0};
+    return launch_few<Kv<D, NT>, D>(kv4_kernel<D, NT>, prepared, a, sms, stream);
+}
+template <int D, int N> int launch_mid(const KvArgs& a, int sms, cudaStream_t stream) {
+    static std::atomic<uint64_t> prepared{0};
+    return launch_few<Mid<D, N>, D>(kv4_mid_kernel<D, N>, prepared, a, sms, stream);
 }
 
 int check_pages(int Hkv, int d, int num_pages, int page_size) {
@@ -1342,9 +1854,9 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     a.max_seqlen = max_seqlen;
     a.scale_log2 = alpha * 1.4426950408889634f;
     const int rows = item_rows(max_seqlen * (long long)G);
-    if (d == 64) return rows == 8 ? launch_few<64, 1>(a, sms, stream) : rows == 16 ? launch_few<64, 2>(a, sms, stream) : launch_few<64, 4>(a, sms, stream);
-    if (d == 128) return rows == 8 ? launch_few<128, 1>(a, sms, stream) : rows == 16 ? launch_few<128, 2>(a, sms, stream) : launch_few<128, 4>(a, sms, stream);
-    return rows == 8 ? launch_few<256, 1>(a, sms, stream) : rows == 16 ? launch_few<256, 2>(a, sms, stream) : launch_few<256, 4>(a, sms, stream);
+    if (d == 64) return rows == 8 ? launch_warps<64, 1>(a, sms, stream) : rows == 16 ? launch_warps<64, 2>(a, sms, stream) : launch_warps<64, 4>(a, sms, stream);
+    if (d == 128) return rows == 8 ? launch_warps<128, 1>(a, sms, stream) : rows == 16 ? launch_mid<128, 16>(a, sms, stream) : launch_mid<128, 32>(a, sms, stream);
+    return rows == 8 ? launch_warps<256, 1>(a, sms, stream) : rows == 16 ? launch_mid<256, 16>(a, sms, stream) : launch_mid<256, 32>(a, sms, stream);
 }
 
 }  // extern "C"
