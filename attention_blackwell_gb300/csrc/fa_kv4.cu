@@ -222,7 +222,7 @@ struct KvWalk {
 };
 
 struct KvScan {
-    int2 scan[20];
+    int2 scan[28];
     int abort_flag, bad;
 };
 struct KvShared : KvScan {
@@ -986,11 +986,11 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // order in which a row's codes lie; Q has the same order, and O's is undone where it is
 // written.  S^T = K Q^T has keys as lanes, O^T = V^T P^T elements of d.
 template <int D, int N> struct Mid {
-    static constexpr int kRows = N, kThreads = 608, kWorkers = 1, kHalves = D / 128;
+    static constexpr int kRows = N, kThreads = 896, kWorkers = 1, kHalves = D / 128;
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
     static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
-    static constexpr uint32_t kV = kTile, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + 2 * kQBox, kRawV = kRawK + kRing * kSlotK;
+    static constexpr uint32_t kV = kTile, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + 128 * 2 * N, kRawV = kRawK + kRing * kSlotK;
     // What the softmax wants of four tiles' keys; rows: less their maximum, factors, what a
     // sum is multiplied by, keys seen, maxima or sums of four quarters.
     static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRowM = kKeys + 4 * 128 * 4,
@@ -1017,14 +1017,15 @@ template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, u
         umma_ss_k<ao, bo>(s, ad, bd, idesc, k > 0 ? 1u : 0u);
     });
 }
-// O^T (+)= V^T P^T for 128 of d: V's rows read MN-major (two boxes of 64 elements), P
-// K-major (rows of keys, two boxes of 64 keys).
+// O^T (+)= V^T P^T for 128 of d, both MN-major: V's rows (two boxes of 64 elements), P's
+// rows of N weights a key, 2 N bytes apart and swizzled over as many.
 template <int D, int N> __device__ __forceinline__ void mid_values(uint32_t o, uint32_t v_smem, uint32_t p_smem, uint32_t acc) {
     using K = Mid<D, N>;
-    constexpr uint32_t idesc = idesc_f16_f32(128, N, 1, 0);
-    const uint64_t ad = sdesc_sw128(v_smem, K::kBox, 1024), bd = sdesc_sw128(p_smem, 16, 1024);
+    constexpr uint32_t idesc = idesc_f16_f32(128, N, 1, 1);
+    constexpr uint64_t kOther = (uint64_t)(N == 32 ? 4 ^ 2 : 6 ^ 2) << 61;      // 64- or 32-byte swizzle for 128
+    const uint64_t ad = sdesc_sw128(v_smem, K::kBox, 1024), bd = sdesc_sw128(p_smem, 16, 16 * N) ^ kOther;
     static_for<8>([&](auto kc) {
-        constexpr uint32_t k = kc, ao = (k * 2048) >> 4, bo = ((k >> 2) * K::kQBox + (k & 3) * 32) >> 4;
+        constexpr uint32_t k = kc, ao = (k * 2048) >> 4, bo = (k * 32 * N) >> 4;
         umma_ss_k<ao, bo>(o, ad, bd, idesc, (acc | k) != 0);
     });
 }
@@ -1107,10 +1108,10 @@ template <int N> __device__ __forceinline__ void tmem_st(uint32_t at, const uint
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Warps 0 to 7 do the softmax (a quarter of the keys, at the end of d, and half the rows
-// each), 8 to 15 expand (two threads a key), 16 and 17 copy, 18 issues products.  K of
-// a tile is expanded before V of the tile before, so scores are ahead of weights by one.
+// each), 8 to 15 expand K and 16 to 23 V (two threads a key), 24 and 25 copy, 26 issues
+// products: a tile's scores before the weighted values of the tile before.
 template <int D, int N>
-__global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
+__global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
     using K = Mid<D, N>;
     using Walk = KvWalk<N>;
     constexpr int kG = D / 32, kC = N / 2;
@@ -1127,7 +1128,7 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.k_raw_full[i], 1);
-            mbar_init(&sh.k_raw_empty[i], 8);
+            mbar_init(&sh.k_raw_empty[i], 16);
             mbar_init(&sh.v_raw_full[i], 1);
             mbar_init(&sh.v_raw_empty[i], 8);
         }
@@ -1142,7 +1143,7 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
         fence_mbar_init();
         sh.abort_flag = 0;
     }
-    if (warp == 18) {
+    if (warp == 26) {
         tmem_alloc(&sh.tmem, K::kColumns);
         tmem_relinquish();
     }
@@ -1162,14 +1163,17 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
     KvItem it;
     bool ok = true;
     uint32_t tile = 0;                               // tiles of this CTA so far
+    // 896 threads of 72 registers: 2 x 104, 4 x 64 and 40 by 128 threads are as many.
     if (warp < 8) {
+        regs_inc<104>();
         const int quarter = warp & 3, c0 = (warp >> 2) * kC, key = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quarter << 21) + c0;
         float *const row_m = reinterpret_cast<float*>(dsmem + K::kRowM) + c0, *const row_f = reinterpret_cast<float*>(dsmem + K::kRowF) + c0,
               *const row_up = reinterpret_cast<float*>(dsmem + K::kRowUp) + c0, *const row_x = reinterpret_cast<float*>(dsmem + K::kRowX) + c0;
         int* const row_lim = reinterpret_cast<int*>(dsmem + K::kRowLim) + c0;
-        uint8_t* const p_key = dsmem + K::kP + (quarter >> 1) * K::kQBox + c0 * 128 + (key & 7) * 2;
-        const int p_piece = (key & 63) >> 3;
+        // Its weights: 16-byte pieces, swizzled.
+        uint8_t* const p_key = dsmem + K::kP + key * (2 * N);
+        const int p_piece = N == 32 ? c0 / 8 ^ (key >> 1 & 3) : c0 / 8 ^ (key >> 2 & 1);
         while (ok && walk.next(a, t, it)) {
             // Q in the codes' order, scaled by a power of two.
             constexpr int kW = D / 8, kPer = 32 / kW, kPasses = N / 8 / kPer;      // 16-byte pieces of a row of fp16; rows a pass
@@ -1284,8 +1288,8 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
                 // The weights before are multiplied.
                 if (tile) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag) && ok;
 #pragma unroll
-                for (int i = 0; i < kC; ++i)
-                    *reinterpret_cast<uint16_t*>(p_key + i * 128 + ((p_piece ^ (i & 7)) << 4)) = (uint16_t)(weights[i / 2] >> (i & 1 ? 16 : 0));
+                for (int i = 0; i < kC / 8; ++i)
+                    *reinterpret_cast<uint4*>(p_key + ((p_piece ^ i) << 4)) = make_uint4(weights[4 * i], weights[4 * i + 1], weights[4 * i + 2], weights[4 * i + 3]);
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -1338,32 +1342,47 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
             tc_fence_before();
             team_sync<8>(0);                         // the rows' numbers are read
         }
-    } else if (warp < 16) {
+    } else if (warp < 24) {
+        regs_dec<64>();
+      if (warp < 16) {
         const int key = tid & 127, half = warp >= 12;
+        while (ok && walk.next(a, t, it)) {
+            for (int p = it.p0; p < it.p1; p += 8, ++tile) {
+                const uint32_t slot = tile % kRing;
+                const uint8_t *const raw = dsmem + K::kRawK + slot * K::kSlotK, *const ks = raw + 8 * K::kCodes, *const vs = ks + 8 * K::kScales;
+                if (!(ok = kv_wait(&sh.k_raw_full[slot], tile / kRing & 1, &sh.abort_flag))) break;
+                const uint32_t here = sh.live[slot];
+                const bool real = (here >> (key >> 4) & 1u) && p * 16 + key < it.seen;
+                uint32_t h[D / 64], sc[kG];
+                scale_pairs<D>(vs + key * kG, real, h);
+                const uint32_t fv = mid_scales<D>(h, sc);
+                scale_pairs<D>(ks + key * kG, true, h);
+                const uint32_t fk = mid_scales<D>(h, sc);
+                // The tile before is done with K's rows.
+                if (tile && !(ok = kv_wait(&sh.s_full[(tile - 1) & 1], (tile - 1) >> 1 & 1, &sh.abort_flag))) break;
+                if (!half) keys[(tile & 3) * 128 + key] = fk | fv << 8 | here << 16;
+                mid_expand<D>(raw, dsmem, key, half, sc);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sh.k_full);
+                    mbar_arrive(&sh.k_raw_empty[slot]);
+                }
+            }
+        }
+      } else {
+        const int key = tid & 127, half = warp >= 20;
         bool more = walk.next(a, t, it);
         int p = it.p0;
-        // K of the next tile, and what is left of its V's scales.
-        auto expand_k = [&](uint32_t (&hv)[D / 64]) -> bool {
+        // V's scales come with K: those of the next tile are taken first, so that its copies
+        // need not wait for this one's V.
+        auto take = [&](uint32_t (&h)[D / 64]) -> bool {
             const uint32_t slot = tile % kRing;
-            const uint8_t *const raw = dsmem + K::kRawK + slot * K::kSlotK, *const ks = raw + 8 * K::kCodes, *const vs = ks + 8 * K::kScales;
             if (!kv_wait(&sh.k_raw_full[slot], tile / kRing & 1, &sh.abort_flag)) return false;
-            const uint32_t here = sh.live[slot];
-            const bool real = (here >> (key >> 4) & 1u) && p * 16 + key < it.seen;
-            uint32_t hk[D / 64], sc[kG];
-            scale_pairs<D>(vs + key * kG, real, hv);
-            const uint32_t fv = mid_scales<D>(hv, sc);
-            scale_pairs<D>(ks + key * kG, true, hk);
-            const uint32_t fk = mid_scales<D>(hk, sc);
-            // The tile before is done with K's rows.
-            if (tile && !kv_wait(&sh.s_full[(tile - 1) & 1], (tile - 1) >> 1 & 1, &sh.abort_flag)) return false;
-            if (!half) keys[(tile & 3) * 128 + key] = fk | fv << 8 | here << 16;
-            mid_expand<D>(raw, dsmem, key, half, sc);
-            fence_async_smem();
+            const bool real = (sh.live[slot] >> (key >> 4) & 1u) && p * 16 + key < it.seen;
+            scale_pairs<D>(dsmem + K::kRawK + slot * K::kSlotK + 8 * (K::kCodes + K::kScales) + key * kG, real, h);
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&sh.k_full);
-                mbar_arrive(&sh.k_raw_empty[slot]);
-            }
+            if (lane == 0) mbar_arrive(&sh.k_raw_empty[slot]);
             ++tile;
             p += 8;
             if (p >= it.p1) {
@@ -1373,9 +1392,9 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
             return true;
         };
         uint32_t now[D / 64], next[D / 64] = {};
-        if (more) ok = expand_k(now);
+        if (more) ok = take(now);
         for (uint32_t done = 0; ok && done < tile; ++done) {
-            if (more && !(ok = expand_k(next))) break;
+            if (more && !(ok = take(next))) break;
             const uint32_t slot = done % kRing;
             uint32_t sc[kG];
             mid_scales<D>(now, sc);
@@ -1391,10 +1410,13 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) now[i] = next[i];
         }
-    } else if (warp < 18) {
+      }
+    } else {
+        regs_dec<40>();
+      if (warp < 26) {
         // K's codes and both scales, or V's codes: one copy for the parts of a tile that
         // are in one page (a copy costs its warp 85 cycles).
-        const bool v = warp == 17;
+        const bool v = warp == 25;
         uint64_t *const full = v ? sh.v_raw_full : sh.k_raw_full, *const empty = v ? sh.v_raw_empty : sh.k_raw_empty;
         const int what = lane & 3, which = lane >> 2, run_log2 = a.ps_log2 - 4;
         const bool copies = v ? what == 0 : what < 3;
@@ -1440,7 +1462,7 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t i = tile < kRing ? 0 : tile - kRing; i < tile; ++i)
             while (!mbar_try_wait(smem_u32(&full[i % kRing]), i / kRing & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-    } else {
+      } else if (warp == 26) {
         uint32_t items = 0;
         auto scores = [&](uint32_t i) -> bool {
             if (!kv_wait(&sh.k_full, i & 1, &sh.abort_flag)) return false;
@@ -1465,6 +1487,7 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
         }
+      }
     }
     __syncwarp();
     tc_fence_before();
@@ -1474,7 +1497,7 @@ __global__ void __launch_bounds__(608, 1) kv4_mid_kernel(const KvArgs a) {
         a.status->where = 113;
         a.status->block = blockIdx.x;
     }
-    if (warp == 18) tmem_dealloc(tmem, K::kColumns);
+    if (warp == 26) tmem_dealloc(tmem, K::kColumns);
 }
 
 // Joins the segments of a row (of one head) that a range's end has cut; writes the
