@@ -990,31 +990,33 @@ template <int D, int N> struct Mid {
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
     static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
-    static constexpr uint32_t kV = kTile, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + 128 * 2 * N, kRawV = kRawK + kRing * kSlotK;
+    static constexpr int kWeights = D == 256 ? 1 : 2;    // tiles of weights (of V's rows, two)
+    static constexpr uint32_t kP1 = 128 * 2 * N, kV = 0, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + kWeights * kP1, kRawV = kRawK + kRing * kSlotK;
     // What the softmax wants of four tiles' keys; rows: less their maximum, factors, what a
     // sum is multiplied by, keys seen, maxima or sums of four quarters.
     static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRowM = kKeys + 4 * 128 * 4,
                               kRowF = kRowM + N * 4, kRowUp = kRowF + N * 4, kRowLim = kRowUp + N * 4, kRowX = kRowLim + N * 4, kWarp = kRowX + 4 * N * 4;
-    static constexpr uint32_t kColumns = N * (2 + kHalves) <= 64 ? 64 : 128;
+    // Tensor memory: scores of two tiles, O, K's rows of two tiles.
+    static constexpr uint32_t kColO = 2 * N, kColK = kColO + kHalves * N, kColumns = kColK + D <= 256 ? 256 : 512;
     static_assert((N == 16 || N == 32) && (D == 128 || D == 256), "sizes built");
     static_assert(kRawK % 1024 == 0 && kWarp % 16 == 0 && kWarp + table_bytes(kTableMost) + 1024 <= 232448, "shared memory plan");
 };
 struct MidShared : KvScan {
-    uint64_t k_raw_full[4], k_raw_empty[4], v_raw_full[4], v_raw_empty[4], k_full, v_full, q_full, s_full[2], p_full, pv_done, drain;
+    uint64_t k_raw_full[4], k_raw_empty[4], v_raw_full[4], v_raw_empty[4], k_full[2], v_full[2], q_full, s_full[2], p_full[2], pv_done[2], drain;
     uint32_t live[4], tmem;
 };
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn_major, int b_mn_major) {
     return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((uint32_t)b_mn_major << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// S^T = K Q^T: both K-major.
-template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, uint32_t k_smem, uint32_t q_smem) {
+// S^T = K Q^T: K in tensor memory (eight columns a step of 16), Q K-major.
+template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, uint32_t k_tmem, uint32_t q_smem) {
     using K = Mid<D, N>;
     constexpr uint32_t idesc = idesc_f16_f32(128, N, 0, 0);
-    const uint64_t ad = sdesc_sw128(k_smem, 16, 1024), bd = sdesc_sw128(q_smem, 16, 1024);
+    const uint64_t bd = sdesc_sw128(q_smem, 16, 1024);
     static_for<D / 16>([&](auto kc) {
-        constexpr uint32_t k = kc, ao = ((k >> 2) * K::kBox + (k & 3) * 32) >> 4, bo = ((k >> 2) * K::kQBox + (k & 3) * 32) >> 4;
-        umma_ss_k<ao, bo>(s, ad, bd, idesc, k > 0 ? 1u : 0u);
+        constexpr uint32_t k = kc, bo = ((k >> 2) * K::kQBox + (k & 3) * 32) >> 4;
+        umma_ts_k<8 * k, bo>(s, k_tmem, bd, idesc, k > 0 ? 1u : 0u);
     });
 }
 // O^T (+)= V^T P^T for 128 of d, both MN-major: V's rows (two boxes of 64 elements), P's
@@ -1074,6 +1076,44 @@ template <int D> __device__ __forceinline__ void mid_expand(const uint8_t* codes
         }
     }
 }
+// Half of a key's codes into its lane of tensor memory.  A row's pieces are loaded in an
+// order that depends on the lane (two lanes of eight meet in a bank instead of eight)
+// and put back in order by selections.
+template <int D> __device__ __forceinline__ void mid_expand_lane(const uint8_t* codes, uint32_t to, int key, int half, const uint32_t (&sc)[D / 32]) {
+    constexpr int kC = D / 64, kG = D / 32;      // 16-byte pieces of half a row
+    const int turn = D == 256 ? key : key >> 1;
+    const uint8_t* row = codes + key * (D / 2) + half * (D / 4);
+    uint32_t w[kC][4];
+#pragma unroll
+    for (int j = 0; j < kC; ++j) lds(row + ((j + turn) & (kC - 1)) * 16, w[j]);
+#pragma unroll
+    for (int o = 1; o < kC; o *= 2) {            // piece c is where (c - turn) was
+        uint32_t y[kC][4];
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[c][k] = turn & o ? w[(c - o) & (kC - 1)][k] : w[c][k];
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[c][k] = y[c][k];
+    }
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        uint32_t x[16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            constexpr int kMask = kG - 1;
+            codes_f16(w[c][k], x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            x[4 * k] = hmul2(x[4 * k], sc[2 * k & kMask]);
+            x[4 * k + 1] = hmul2(x[4 * k + 1], sc[2 * k & kMask]);
+            x[4 * k + 2] = hmul2(x[4 * k + 2], sc[(2 * k & kMask) + 1]);
+            x[4 * k + 3] = hmul2(x[4 * k + 3], sc[(2 * k & kMask) + 1]);
+        }
+        tmem_st16(to + half * (D / 4) + c * 16, x);
+    }
+    tmem_wait_st();
+}
 // The element that position x of a row's codes is.
 template <int D> __device__ __forceinline__ int element_at(int x) {
     const int u = x >> 2;
@@ -1132,13 +1172,14 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             mbar_init(&sh.v_raw_full[i], 1);
             mbar_init(&sh.v_raw_empty[i], 8);
         }
-        mbar_init(&sh.k_full, 8);
-        mbar_init(&sh.v_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.k_full[i], 8);
+            mbar_init(&sh.v_full[i], 8);
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 8);
+            mbar_init(&sh.pv_done[i], 1);
+        }
         mbar_init(&sh.q_full, 8);
-        mbar_init(&sh.s_full[0], 1);
-        mbar_init(&sh.s_full[1], 1);
-        mbar_init(&sh.p_full, 8);
-        mbar_init(&sh.pv_done, 1);
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.abort_flag = 0;
@@ -1163,6 +1204,8 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
     KvItem it;
     bool ok = true;
     uint32_t tile = 0;                               // tiles of this CTA so far
+    // What is done once a tile is told by two barriers in turn.
+    auto wait2 = [&](uint64_t (&bars)[2], uint32_t x) -> bool { return kv_wait(&bars[x & 1], x >> 1 & 1, &sh.abort_flag); };
     // 896 threads of 72 registers: 2 x 104, 4 x 64 and 40 by 128 threads are as many.
     if (warp < 8) {
         regs_inc<104>();
@@ -1220,7 +1263,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
 #pragma unroll
             for (int i = 0; i < kC / 2; ++i) l[i] = 0;
             for (int p = it.p0; p < it.p1; p += 8, ++tile) {
-                ok = kv_wait(&sh.s_full[tile & 1], tile >> 1 & 1, &sh.abort_flag) && ok;
+                ok = wait2(sh.s_full, tile) && ok;
                 tc_fence_after();
                 uint32_t r[kC];
                 tmem_ld<kC>(lanes + (tile & 1) * N, r);
@@ -1246,7 +1289,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 }
                 // O and l follow a row's running maximum as above.
                 if (team_or<8>(0, most > kTau + kLift || !ok)) {
-                    if (ok && tile) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag);
+                    if (ok && tile) ok = wait2(sh.pv_done, tile - 1);
                     ok = !team_or<8>(0, !ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -1267,10 +1310,10 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     if (p > it.p0) {
 #pragma unroll
                         for (int h = 0; h < K::kHalves; ++h) {
-                            tmem_ld<kC>(lanes + N * (2 + h), r);
+                            tmem_ld<kC>(lanes + K::kColO + N * h, r);
 #pragma unroll
                             for (int i = 0; i < kC; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * row_f[i]);
-                            tmem_st<kC>(lanes + N * (2 + h), r);
+                            tmem_st<kC>(lanes + K::kColO + N * h, r);
                         }
                         tmem_wait_st();
                     }
@@ -1285,17 +1328,18 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     l[i / 2] = f2_fma(f2_pack(y[0], y[1]), f2_pack(back, back), l[i / 2]);
                     weights[i / 2] = pack_f16x2(y[0], y[1]);
                 }
-                // The weights before are multiplied.
-                if (tile) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag) && ok;
+                // The weights that were here are multiplied.
+                if (tile >= K::kWeights) ok = wait2(sh.pv_done, tile - K::kWeights) && ok;
+                uint8_t* const to = p_key + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0);
 #pragma unroll
                 for (int i = 0; i < kC / 8; ++i)
-                    *reinterpret_cast<uint4*>(p_key + ((p_piece ^ i) << 4)) = make_uint4(weights[4 * i], weights[4 * i + 1], weights[4 * i + 2], weights[4 * i + 3]);
+                    *reinterpret_cast<uint4*>(to + ((p_piece ^ i) << 4)) = make_uint4(weights[4 * i], weights[4 * i + 1], weights[4 * i + 2], weights[4 * i + 3]);
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full);
+                if (lane == 0) mbar_arrive(&sh.p_full[tile & 1]);
             }
-            if (ok) ok = kv_wait(&sh.pv_done, (tile - 1) & 1, &sh.abort_flag);
+            if (ok) ok = wait2(sh.pv_done, tile - 1);
             tc_fence_after();
             float v[kC];
 #pragma unroll
@@ -1322,7 +1366,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
 #pragma unroll
             for (int h = 0; h < K::kHalves; ++h) {
                 uint32_t r[kC];
-                tmem_ld<kC>(lanes + N * (2 + h), r);
+                tmem_ld<kC>(lanes + K::kColO + N * h, r);
                 const int e = element_at<D>(h * 128 + key);
                 if (it.whole) {
                     const uint32_t row = (uint32_t)it.rb * N + c0;
@@ -1358,14 +1402,15 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 const uint32_t fv = mid_scales<D>(h, sc);
                 scale_pairs<D>(ks + key * kG, true, h);
                 const uint32_t fk = mid_scales<D>(h, sc);
-                // The tile before is done with K's rows.
-                if (tile && !(ok = kv_wait(&sh.s_full[(tile - 1) & 1], (tile - 1) >> 1 & 1, &sh.abort_flag))) break;
+                // The tile before the last is done with its rows.
+                if (tile >= 2 && !(ok = wait2(sh.s_full, tile - 2))) break;
+                tc_fence_after();
                 if (!half) keys[(tile & 3) * 128 + key] = fk | fv << 8 | here << 16;
-                mid_expand<D>(raw, dsmem, key, half, sc);
-                fence_async_smem();
+                mid_expand_lane<D>(raw, tmem + ((uint32_t)(warp & 3) << 21) + K::kColK + (tile & 1) * (D / 2), key, half, sc);
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&sh.k_full);
+                    mbar_arrive(&sh.k_full[tile & 1]);
                     mbar_arrive(&sh.k_raw_empty[slot]);
                 }
             }
@@ -1399,12 +1444,12 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             uint32_t sc[kG];
             mid_scales<D>(now, sc);
             if (!(ok = kv_wait(&sh.v_raw_full[slot], done / kRing & 1, &sh.abort_flag))) break;
-            if (done && !(ok = kv_wait(&sh.pv_done, (done - 1) & 1, &sh.abort_flag))) break;
-            mid_expand<D>(dsmem + K::kRawV + slot * K::kSlotV, dsmem + K::kV, key, half, sc);
+            if (done >= 2 && !(ok = wait2(sh.pv_done, done - 2))) break;
+            mid_expand<D>(dsmem + K::kRawV + slot * K::kSlotV, dsmem + K::kV + (done & 1) * K::kTile, key, half, sc);
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&sh.v_full);
+                mbar_arrive(&sh.v_full[done & 1]);
                 mbar_arrive(&sh.v_raw_empty[slot]);
             }
 #pragma unroll
@@ -1465,9 +1510,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
       } else if (warp == 26) {
         uint32_t items = 0;
         auto scores = [&](uint32_t i) -> bool {
-            if (!kv_wait(&sh.k_full, i & 1, &sh.abort_flag)) return false;
+            if (!wait2(sh.k_full, i)) return false;
             tc_fence_after();
-            mid_scores<D, N>(tmem + (i & 1) * N, smem, smem + K::kQ);
+            mid_scores<D, N>(tmem + (i & 1) * N, tmem + K::kColK + (i & 1) * (D / 2), smem + K::kQ);
             umma_commit_w(&sh.s_full[i & 1]);
             return true;
         };
@@ -1475,11 +1520,11 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             if (!(ok = kv_wait(&sh.q_full, items++ & 1, &sh.abort_flag)) || !(ok = scores(tile))) break;
             for (int p = it.p0; p < it.p1; p += 8, ++tile) {
                 if (p + 8 < it.p1 && !(ok = scores(tile + 1))) break;
-                if (!(ok = kv_wait(&sh.v_full, tile & 1, &sh.abort_flag) && kv_wait(&sh.p_full, tile & 1, &sh.abort_flag))) break;
+                if (!(ok = wait2(sh.v_full, tile) && wait2(sh.p_full, tile))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < K::kHalves; ++h) mid_values<D, N>(tmem + N * (2 + h), smem + K::kV + h * 2 * K::kBox, smem + K::kP, p > it.p0);
-                umma_commit_w(&sh.pv_done);
+                for (int h = 0; h < K::kHalves; ++h) mid_values<D, N>(tmem + K::kColO + N * h, smem + K::kV + (tile & 1) * K::kTile + h * 2 * K::kBox, smem + K::kP + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0), p > it.p0);
+                umma_commit_w(&sh.pv_done[tile & 1]);
             }
         }
         if (!ok) {                                   // products in flight end before their memory is given back
