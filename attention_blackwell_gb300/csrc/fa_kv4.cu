@@ -1002,7 +1002,7 @@ template <int D, int N> struct Mid {
     static_assert(kRawK % 1024 == 0 && kWarp % 16 == 0 && kWarp + table_bytes(kTableMost) + 1024 <= 232448, "shared memory plan");
 };
 struct MidShared : KvScan {
-    uint64_t k_raw_full[4], k_raw_empty[4], v_raw_full[4], v_raw_empty[4], k_full[2], v_full[2], q_full, s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t k_raw_full[4], k_raw_empty[4], v_raw_full[4], v_raw_empty[4], k_full[2], v_full[2], q_full, s_full[2], p_full[2], pv_done[2], drain[2];
     uint32_t live[4], tmem;
 };
 
@@ -1148,8 +1148,8 @@ template <int N> __device__ __forceinline__ void tmem_st(uint32_t at, const uint
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Warps 0 to 7 do the softmax (a quarter of the keys, at the end of d, and half the rows
-// each), 8 to 15 expand K and 16 to 23 V (two threads a key), 24 and 25 copy, 26 issues
-// products: a tile's scores before the weighted values of the tile before.
+// each), 8 to 15 expand K and 16 to 23 V (two threads a key), 24 and 25 copy, 26 and 27
+// issue the two products.
 template <int D, int N>
 __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
     using K = Mid<D, N>;
@@ -1178,9 +1178,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 8);
             mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.drain[i], 1);
         }
         mbar_init(&sh.q_full, 8);
-        mbar_init(&sh.drain, 1);
         fence_mbar_init();
         sh.abort_flag = 0;
     }
@@ -1507,30 +1507,33 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
         const uint64_t t0 = globaltimer_ns();
         for (uint32_t i = tile < kRing ? 0 : tile - kRing; i < tile; ++i)
             while (!mbar_try_wait(smem_u32(&full[i % kRing]), i / kRing & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {}
-      } else if (warp == 26) {
+      } else {
+        // Scores, and weighted values, by a warp each: one that waits holds up its own only.
+        const bool values = warp == 27;
         uint32_t items = 0;
-        auto scores = [&](uint32_t i) -> bool {
-            if (!wait2(sh.k_full, i)) return false;
-            tc_fence_after();
-            mid_scores<D, N>(tmem + (i & 1) * N, tmem + K::kColK + (i & 1) * (D / 2), smem + K::kQ);
-            umma_commit_w(&sh.s_full[i & 1]);
-            return true;
-        };
         while (ok && walk.next(a, t, it)) {
-            if (!(ok = kv_wait(&sh.q_full, items++ & 1, &sh.abort_flag)) || !(ok = scores(tile))) break;
+            if (!values && !(ok = kv_wait(&sh.q_full, items++ & 1, &sh.abort_flag))) break;
             for (int p = it.p0; p < it.p1; p += 8, ++tile) {
-                if (p + 8 < it.p1 && !(ok = scores(tile + 1))) break;
-                if (!(ok = wait2(sh.v_full, tile) && wait2(sh.p_full, tile))) break;
-                tc_fence_after();
+                if (values) {
+                    if (!(ok = wait2(sh.v_full, tile) && wait2(sh.p_full, tile))) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int h = 0; h < K::kHalves; ++h) mid_values<D, N>(tmem + K::kColO + N * h, smem + K::kV + (tile & 1) * K::kTile + h * 2 * K::kBox, smem + K::kP + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0), p > it.p0);
-                umma_commit_w(&sh.pv_done[tile & 1]);
+                    for (int h = 0; h < K::kHalves; ++h)
+                        mid_values<D, N>(tmem + K::kColO + N * h, smem + K::kV + (tile & 1) * K::kTile + h * 2 * K::kBox, smem + K::kP + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0), p > it.p0);
+                    umma_commit_w(&sh.pv_done[tile & 1]);
+                } else {
+                    // The scores that were here are read.
+                    if (!(ok = wait2(sh.k_full, tile) && (tile < 2 || wait2(sh.p_full, tile - 2)))) break;
+                    tc_fence_after();
+                    mid_scores<D, N>(tmem + (tile & 1) * N, tmem + K::kColK + (tile & 1) * (D / 2), smem + K::kQ);
+                    umma_commit_w(&sh.s_full[tile & 1]);
+                }
             }
         }
         if (!ok) {                                   // products in flight end before their memory is given back
-            umma_commit_w(&sh.drain);
+            umma_commit_w(&sh.drain[values]);
             const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&sh.drain), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
+            while (!mbar_try_wait(smem_u32(&sh.drain[values]), 0) && globaltimer_ns() - t0 < kWaitLimitNs) {}
         }
       }
     }
