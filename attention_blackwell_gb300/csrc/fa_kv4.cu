@@ -27,10 +27,9 @@
 // cut by a range's end leaves (M, l, O) in the workspace, and a second kernel joins
 // the segments in the list's order; one that is not cut is written at once.
 //
-// More than 16 rows (8 at d = 256): two or four warps are a worker together (kTeam).
-// Each scores its share of a step's keys against all rows, leaves the weights in
-// shared memory, and after one barrier a step multiplies all of them with its share
-// of d of the values, so a code is converted once for up to 32 rows.
+// More than 16 rows (8 at d = 256; not at d = 64): a CTA is a worker, and the products
+// are the fifth-generation tensor cores' (see "more rows" below): a code is converted
+// once for up to 32 rows, by warps that do nothing else.
 //
 // Many rows (prompts): the requests' pages are expanded to bf16 once, in the
 // workspace, and fa_prefix_fwd's tensor-memory pipeline does the rest: for a prompt
@@ -47,7 +46,8 @@
 //   walk, page numbers and copies depend on one another.  The join takes 5.
 //   d = 64, 16 heads with 1 to 8 drafted tokens, up to 4096 keys (98 MB): 39 us, 186
 //   instructions for 1088 bytes, the same start.
-//   32 rows of 256 over up to 16384 keys (234 MB): 134 us, products 38 % of it.
+//   32 rows of 256 over up to 16384 keys (234 MB): 104 us (134 when four warps shared an
+//   item's 32 rows with m16n8k16); see "more rows".
 //   one token over 1017 keys: 13 us, 12 as a graph.
 //   prompts, six of up to 2048 tokens over up to 10000 keys (563 GFLOP): 520 us, 25 of
 //   them the expansion (164 MB), the rest fa_prefix_fwd's.
@@ -72,10 +72,10 @@ constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
 // Rows of a request and key/value head above which pages are expanded.  8 requests of
-// 8000 keys and 8 heads, from the codes and expanded: 64 rows of 128 97 and 133 us, 128
-// rows 178 and 141; d = 64, 16 heads: 126 and 152, 242 and 170; d = 256, one head, 128
-// rows 52 and 57, 256 rows 84 and 59.
-constexpr int many_rows(int d) { return d == 256 ? 128 : 64; }
+// 8000 keys and 8 heads of 128, from the codes and expanded: 64 rows 75 and 133 us, 128
+// rows 136 and 142, 192 rows 199 and 149; of 64, 16 heads: 64 rows 126 and 152, 128 rows
+// 242 and 170; of 256, one head: 256 rows 60 and 61, 512 rows 97 and 72.
+constexpr int many_rows(int d) { return d; }
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
 // A CTA's tables of the list: in shared memory up to kTableMost requests, else in its
@@ -86,35 +86,21 @@ __host__ __device__ constexpr uint32_t table_bytes(int B) { return (4u * B + 3) 
 template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT;                 // rows of an item
     static constexpr int kGroups = D / 32;
-    // Warps of a worker.  32 rows of 256 would be 256 registers of O in one warp: four
-    // share them, each with a quarter of d, and two share what would be 128, so that
-    // twelve warps fit an SM (32 rows of 256: 182 us for
-    // 100 requests of 8200 keys by eight single warps with 16 rows each, 134 so; 16 rows
-    // of 256: 222 and 199 for 64 requests of 4096 keys and 8 heads; 32 of 128: 384 and
-    // 359 for twice the keys).
-    static constexpr int kTeam = NT * D >= 1024 ? 4 : NT * D >= 512 && NT > 1 ? 2 : 1;
-    static constexpr int kWarps = D == 64 || NT * D <= 128 || kTeam > 1 ? 12 : 8, kThreads = 32 * kWarps;   // a CTA, one an SM
-    static constexpr int kWorkers = kWarps / kTeam;
-    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : kTeam;   // 16-key parts a step
-    static constexpr int kOwn = kParts / kTeam;          // of them, those whose scores a warp computes
+    static constexpr int kWorkers = D == 64 || NT * D <= 128 ? 12 : 8, kThreads = 32 * kWorkers;   // a CTA's warps, one CTA an SM
+    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
     static constexpr int kSteps = D == 128 && NT <= 2 ? 2 : D == 64 && NT == 2 ? 2 : 1;   // steps a slot of the ring
-    static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kOwn;
+    static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kParts;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 8) : NT == 1 ? 5 : 2;
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 8) : 5;
     static constexpr bool kQRegs = NT <= 2 && NT * D <= 256;     // Q's fragments in registers
     static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
-    // The scales of the keys that a warp scores, as the products want them: K's as floats
+    // A step's scales as the products want them: K's as floats
     // [key][group], V's as pairs of keys [key / 2][group], (e, 2^-e) [key].
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
-    // A team: the scales and the weights [part][tile of rows][lane] of two steps (one
-    // warp may be a step ahead of the others), factors, maxima and sums of rows.
-    static constexpr uint32_t kWeights = 2 * kParts * NT * 256, kShared = kTeam > 1 ? kWeights + (2 + 2 * kTeam) * kRows * 4 : 0;
-    static constexpr uint32_t kPreps = kTeam > 1 ? 2 * kTeam * kPrep : kPrep;
-    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPreps + kShared;    // of a worker
+    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPrep;
     static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0 && kPrep % 16 == 0, "copies are 16-byte aligned");
     static_assert(kRing * kSlotParts <= 32 && kRing <= 8 && 4 * kSlotParts <= 32, "a bit a part, a lane a copy");
-    static_assert(kTeam == 1 || (kSteps == 1 && kOwn == 1 && !kQRegs), "a team's step is a part a warp");
     static_assert(kWorkers * kWarp + table_bytes(kTableMost) + 1536 <= 232448, "shared memory plan");
 };
 
@@ -227,7 +213,6 @@ struct KvScan {
 };
 struct KvShared : KvScan {
     uint64_t full[16][8];
-    uint32_t live[8][8];                 // teams: a slot's parts that have a page
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -476,21 +461,10 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
 
 // -------------------------------------------------------------------- kernel
 
-// Barriers of a team of W warps, and one with the `or` of a flag over its threads.
-template <int W> __device__ __forceinline__ void team_sync(int team) { asm volatile("barrier.sync %0, %1;" ::"r"(team + 1), "n"(32 * W) : "memory"); }
-template <int W> __device__ __forceinline__ bool team_or(int team, bool x) {
-    uint32_t y;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.red.or.pred q, %1, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-                 : "=r"(y) : "r"(team + 1), "r"((uint32_t)x), "n"(32 * W) : "memory");
-    return y != 0;
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArgs a) {
     using K = Kv<D, NT>;
-    constexpr int kG = K::kGroups, kParts = K::kParts, kOwn = K::kOwn, kSteps = K::kSteps, kSP = K::kSlotParts;
-    constexpr bool kTeam = K::kTeam > 1;
-    constexpr int kGO = kG / K::kTeam, kNL = NT / K::kTeam;      // groups of O, tiles of Q's rows that a warp brings
+    constexpr int kG = K::kGroups, kParts = K::kParts, kSteps = K::kSteps, kSP = K::kSlotParts;
     constexpr uint32_t kRing = K::kRing;
     extern __shared__ __align__(16) uint8_t dsmem[];
     __shared__ KvShared sh;
@@ -516,20 +490,16 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 
     fill_rows<K>(a, t, tid);
 
-    const int team = warp / K::kTeam, member = warp % K::kTeam;
-    uint64_t* full = sh.full[team];
-    uint8_t* const ring = dsmem + team * K::kWarp;
-    uint8_t *const q_smem = ring + kRing * K::kSlot, *const preps = q_smem + K::kQBytes, *const weights = preps + K::kPreps;
-    float* const row_f = reinterpret_cast<float*>(weights + K::kWeights);          // a team's rows: factors, maxima and sums of each warp
-    float *const row_m = row_f + K::kRows, *const row_l = row_m + K::kTeam * K::kRows;
-    int* const row_lim = reinterpret_cast<int*>(row_l + K::kTeam * K::kRows);      // and the keys that they see
-    const int worker = blockIdx.x * K::kWorkers + team;
+    uint64_t* full = sh.full[warp];
+    uint8_t* const ring = dsmem + warp * K::kWarp;
+    uint8_t *const q_smem = ring + kRing * K::kSlot, *const prep = q_smem + K::kQBytes;
+    const int worker = blockIdx.x * K::kWorkers + warp;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
     KvWalk<K::kRows> ahead;
     KvItem to = {};
     ahead.start(a, t, hdr, worker);
-    bool more = member == 0 && ahead.next(a, t, to);       // a team's first warp copies for all
+    bool more = ahead.next(a, t, to);
     int part = to.p0, win = -1, win_next = -1;       // next part; pages of its 32 parts, one a lane, and of the next 32
     uint32_t filled = 0, issued = 0, live = 0;       // next slot, slots filled, one bit a part of a slot: its page exists
     auto pages = [&](int p) -> int {                 // of parts p .. p + 31
@@ -556,7 +526,6 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
         uint64_t* bar = &full[filled];
         __syncwarp();                                // every lane has read what the slot held
         if (lane == 0) {
-            if (kTeam) sh.live[team][filled] = on;
             if (on) mbar_arrive_expect_tx(bar, K::kPart * __popc(on));
             else mbar_arrive(bar);
         }
@@ -587,21 +556,19 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     KvWalk<K::kRows> walk;
     KvItem it;
     walk.start(a, t, hdr, worker);
-    uint32_t read = 0, slot = 0, phase = 0, step = 0;
-    bool refill = false;                             // a team: the slot before this one is done with
+    uint32_t read = 0, slot = 0, phase = 0;
     bool ok = true;
     while (ok && walk.next(a, t, it)) {
         // Q as B operands: lane (r, c) has row r's elements 32 g + 8 c to + 7, which
         // are what it reads of a key.
         uint32_t qf[K::kQRegs ? NT : 1][K::kQRegs ? kG : 1][4];
-        // What a row's sums are multiplied by, and the keys it sees, of rows 2c and 2c + 1
-        // (a team's are in shared memory).
-        float f[kTeam ? 1 : NT][2];
-        int lim[kTeam ? 1 : NT][2];
-        float m[NT][2], l[NT][2], o[kGO][2][NT][4];
+        // What a row's sums are multiplied by, and the keys it sees, of rows 2c and 2c + 1.
+        float f[NT][2];
+        int lim[NT][2];
+        float m[NT][2], l[NT][2], o[kG][2][NT][4];
 #pragma unroll
-        for (int n = 0; n < kNL; ++n) {
-            const int nt = member * kNL + n, x = nt * 8 + r;
+        for (int n = 0; n < NT; ++n) {
+            const int x = n * 8 + r;
             const uint32_t row = (uint32_t)it.rb * K::kRows + x;
             const int tok = (int)(row / (uint32_t)a.G), h = (int)row - tok * a.G;
             uint4 in[kG];
@@ -632,33 +599,24 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
                     for (int i = 0; i < 4; ++i) qf[n][g][i] = q[i];
                 } else {
-                    sts(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
+                    sts(q_smem + ((n * kG + g) * 32 + lane) * 16, q);
                 }
             }
-            if constexpr (kTeam) {
-                if (c == 0) {
-                    row_f[x] = up;
-                    row_lim[x] = min(it.s, it.s - it.n + tok + 1);
-                }
-            } else {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
-            }
+            for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
         }
-        if (kTeam) team_sync<K::kTeam>(team);
+        __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if constexpr (!kTeam) {
-                    const int tk = (int)(((uint32_t)it.rb * K::kRows + nt * 8 + 2 * c + i) / (uint32_t)a.G);
-                    lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
-                }
+                const int tk = (int)(((uint32_t)it.rb * K::kRows + nt * 8 + 2 * c + i) / (uint32_t)a.G);
+                lim[nt][i] = min(it.s, it.s - it.n + tk + 1);
                 m[nt][i] = kNone;
                 l[nt][i] = 0.f;
             }
 #pragma unroll
-            for (int g = 0; g < kGO; ++g)
+            for (int g = 0; g < kG; ++g)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[g][0][nt][i] = o[g][1][nt][i] = 0.f;
         }
@@ -671,32 +629,30 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
             const uint8_t* const scales = ring + slot * K::kSlot + 2 * kSP * K::kCodes + sub * (kParts * K::kScales);
             if (sub == 0) {
                 ok = kv_wait(&full[slot], phase, &sh.abort_flag);
-                if (!kTeam && !ok) break;            // a team leaves together, see below
+                if (!ok) break;
                 // The ring is filled once the first slot is there: all at once, every
                 // warp's first slot would wait for the others' second.
                 if (read == 0)
                     for (uint32_t i = 1; i < kRing; ++i) copy();
             }
-            const uint32_t here = kTeam ? sh.live[team][slot] : live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
+            const uint32_t here = live >> (slot * kSP + sub * kParts) & ((1u << kParts) - 1u);
             const bool ragged = k0 + kParts * 16 > lim_min || here != (1u << kParts) - 1u;
-            const int own = member * kOwn;             // the first part whose scores are this warp's
-            uint8_t* const prep = preps + (kTeam ? ((step & 1) * K::kTeam + member) * K::kPrep : 0);
 #pragma unroll
             for (int i = 0; i < (K::kKeys + 31) / 32; ++i) {
                 const int key = i * 32 + (lane & (K::kKeys - 1));      // sixteen keys: every key twice, with the same results
-                const bool real = !ragged || (k0 + own * 16 + key < it.seen && (here >> (own + (key >> 4)) & 1u));
-                prepare_key<D, NT>(scales + own * K::kScales, scales + (kSP + own) * K::kScales, prep, key, lane, real);
+                const bool real = !ragged || (k0 + key < it.seen && (here >> (key >> 4) & 1u));
+                prepare_key<D, NT>(scales, scales + kSP * K::kScales, prep, key, lane, real);
             }
             __syncwarp();
-            float z[kOwn][NT][4], back[kOwn][2];     // scores + e, 2^-e
+            float z[kParts][NT][4], back[kParts][2];     // scores + e, 2^-e
 #pragma unroll
-            for (int kt = 0; kt < kOwn; ++kt) {
+            for (int kt = 0; kt < kParts; ++kt) {
                 // Keys' codes: eight adjacent elements of every group, for keys r and r + 8.
                 uint32_t kw[2][kG], ksc[2][kG];
                 uint64_t z2[NT][2];                  // rows 2c and 2c + 1 of key r, of key r + 8
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    lds(at + ((own + kt) * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
+                    lds(at + (kt * 16 + kr + 8 * i) * (D / 2) + c * (D / 8), kw[i]);
                     lds(prep + (kt * 16 + kr + 8 * i) * (4 * kG), ksc[i]);
                 }
 #pragma unroll
@@ -738,24 +694,21 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float2 ff = kTeam ? *reinterpret_cast<const float2*>(row_f + nt * 8 + 2 * c) : make_float2(f[kTeam ? 0 : nt][0], f[kTeam ? 0 : nt][1]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float e = __uint_as_float(eb[i][0]);
-                        f2_unpack(f2_fma(z2[nt][i], f2_pack(ff.x, ff.y), f2_pack(e, e)), z[kt][nt][2 * i], z[kt][nt][2 * i + 1]);
+                        f2_unpack(f2_fma(z2[nt][i], f2_pack(f[nt][0], f[nt][1]), f2_pack(e, e)), z[kt][nt][2 * i], z[kt][nt][2 * i + 1]);
                     }
                 }
             }
             if (ragged) {
 #pragma unroll
-                for (int kt = 0; kt < kOwn; ++kt)
+                for (int kt = 0; kt < kParts; ++kt)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int2 ll = kTeam ? *reinterpret_cast<const int2*>(row_lim + nt * 8 + 2 * c) : make_int2(lim[kTeam ? 0 : nt][0], lim[kTeam ? 0 : nt][1]);
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!(here >> (own + kt) & 1u) || k0 + (own + kt) * 16 + kr + (i >> 1) * 8 >= (i & 1 ? ll.y : ll.x)) z[kt][nt][i] = -INFINITY;
-                    }
+                            if (!(here >> kt & 1u) || k0 + kt * 16 + kr + (i >> 1) * 8 >= lim[nt][i & 1]) z[kt][nt][i] = -INFINITY;
             }
             // O and l follow a row's running maximum (m: kLift below it) when it grows by more
             // than kTau: only then do the lanes that share the row look for it together.
@@ -766,7 +719,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 for (int i = 0; i < 2; ++i) {
                     float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
-                    for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                    for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                     jump |= x - m[nt][i] > kTau + kLift;
                 }
             // Weights as B operands: row r, keys 2c, 2c + 1 and eight further.
@@ -788,67 +741,23 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     pt[nt][1] = transposed(pack_f16x2(w[2], w[3]));
                 }
             };
-            uint8_t* const shared_pt = weights + (step & 1) * (K::kWeights / 2);
-            auto share = [&]() {
-                uint32_t pt[NT][2];
-                weigh(0, pt);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) sts(shared_pt + ((member * NT + nt) * 32 + lane) * 8, pt[nt]);
-            };
-            // A team: one barrier a step, for the weights as if no maximum grew.  Where one
-            // did, or a wait gave up, they are thrown away.
-            bool again = false;
-            float l_before[kTeam ? NT : 1][2];
-            if constexpr (kTeam) {
-                jump = __any_sync(0xffffffffu, jump);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) l_before[nt][i] = l[nt][i];
-                if (!jump) share();
-                again = team_or<K::kTeam>(team, jump || !ok);
-                // All its warps are past the step before.
-                if (refill) copy();
-                if (again && (ok = !team_or<K::kTeam>(team, !ok)) == false) break;
-            }
-            if (kTeam ? again : __any_sync(0xffffffffu, jump)) {
-                if constexpr (kTeam)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) l[nt][i] = l_before[nt][i];
-                if constexpr (kTeam) {               // each warp's maxima for the others
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            if (r == 0) row_m[member * K::kRows + nt * 8 + 2 * c + i] = x;
-                        }
-                    team_sync<K::kTeam>(team);
-                }
+            if (__any_sync(0xffffffffu, jump)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float x = fmaxf(z[0][nt][i], z[0][nt][2 + i]);
 #pragma unroll
-                        for (int kt = 1; kt < kOwn; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
+                        for (int kt = 1; kt < kParts; ++kt) x = fmax3(x, z[kt][nt][i], z[kt][nt][2 + i]);
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        if constexpr (kTeam)
-#pragma unroll
-                            for (int w = 0; w < K::kTeam; ++w) x = fmaxf(x, row_m[w * K::kRows + nt * 8 + 2 * c + i]);
                         x = fmaxf(m[nt][i], x - kLift);
                         const float fac = ex2_mufu(m[nt][i] - x);
                         l[nt][i] *= fac;
                         m[nt][i] = x;
 #pragma unroll
-                        for (int g = 0; g < kGO; ++g)
+                        for (int g = 0; g < kG; ++g)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 o[g][h][nt][i] *= fac;
@@ -856,33 +765,21 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                             }
                     }
             }
-            if constexpr (kTeam)
-                if (again) {
-                    share();
-                    team_sync<K::kTeam>(team);
-                }
 #pragma unroll
             for (int kt = 0; kt < kParts; ++kt) {
                 uint32_t pt[NT][2];
                 const uint8_t* scaled = prep + kt * 8 * (4 * kG);       // V's scales of the part
-                if constexpr (kTeam) {
-                    scaled = preps + ((step & 1) * K::kTeam + kt) * K::kPrep;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) lds(shared_pt + ((kt * NT + nt) * 32 + lane) * 8, pt[nt]);
-                } else {
-                    weigh(kt, pt);
-                }
-                // Values' codes: four elements of every group (a team: of a share of them), for
-                // the four keys, and scales.
-                uint32_t vw[2][2][kGO / 2], vsc[2][kGO];
+                weigh(kt, pt);
+                // Values' codes: four elements of every group for the four keys, and scales.
+                uint32_t vw[2][2][kG / 2], vsc[2][kG];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16) + member * (2 * kGO), vw[i][y]);
-                    lds(scaled + K::kVPairs + ((c ^ (c >> 1)) + 4 * i) * (4 * kG) + member * (4 * kGO), vsc[i]);
+                    for (int y = 0; y < 2; ++y) lds(at + kSP * K::kCodes + (kt * 16 + 8 * i + ((2 * c + y) ^ c)) * (D / 2) + r * (D / 16), vw[i][y]);
+                    lds(scaled + K::kVPairs + ((c ^ (c >> 1)) + 4 * i) * (4 * kG), vsc[i]);
                 }
 #pragma unroll
-                for (int j = 0; j < kGO / 2; ++j) {
+                for (int j = 0; j < kG / 2; ++j) {
                     uint32_t x[2][2][4];             // [keys 2c .., keys 2c + 8 ..][codes 0 and 2, 1 and 3][group 2j: two, group 2j + 1: two]
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -911,14 +808,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     slot = 0;
                     phase ^= 1;
                 }
-                if (kTeam) refill = true;
-                else copy();
+                copy();
             }
-            ++step;
         }
         if (!ok) break;
         // O's elements 32 g + 4 r to + 3 of rows 2c and 2c + 1.
-        const int e0 = member * (kGO * 32) + 4 * r;
+        const int e0 = 4 * r;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -926,20 +821,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
                 l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
-                if (kTeam && r == 0) row_l[member * K::kRows + nt * 8 + 2 * c + i] = l[nt][i];
             }
-        if (kTeam) team_sync<K::kTeam>(team);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int x = nt * 8 + 2 * c + i;
-                // A team's sums in one order, so all its warps divide by the same.
-                if constexpr (kTeam) {
-                    l[nt][i] = row_l[x];
-#pragma unroll
-                    for (int w = 1; w < K::kTeam; ++w) l[nt][i] += row_l[w * K::kRows + x];
-                }
                 if (x >= it.rows) continue;
                 if (it.whole) {
                     const uint32_t row = (uint32_t)it.rb * K::kRows + x;
@@ -948,17 +835,17 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                     const long long tt = it.c0 + tok;
                     __nv_bfloat16* dst = a.o + (tt * a.Hq + h) * D + e0;
 #pragma unroll
-                    for (int g = 0; g < kGO; ++g)
+                    for (int g = 0; g < kG; ++g)
                         *reinterpret_cast<uint2*>(dst + 32 * g) = make_uint2(pack_bf16x2(o[g][0][nt][i] * inv, o[g][0][nt][2 + i] * inv),
                                                                              pack_bf16x2(o[g][1][nt][i] * inv, o[g][1][nt][2 + i] * inv));
-                    if (r == 0 && member == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
+                    if (r == 0) a.lse[(long long)h * a.T + tt] = l[nt][i] == 0.f ? -INFINITY : (m[nt][i] + __log2f(l[nt][i])) * 0.69314718055994531f;
                 } else {
                     const long long row = (long long)it.seg * K::kRows + x;
                     float* dst = a.seg + row * D + e0;
 #pragma unroll
-                    for (int g = 0; g < kGO; ++g)
+                    for (int g = 0; g < kG; ++g)
                         *reinterpret_cast<float4*>(dst + 32 * g) = make_float4(o[g][0][nt][i], o[g][0][nt][2 + i], o[g][1][nt][i], o[g][1][nt][2 + i]);
-                    if (r == 0 && member == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
+                    if (r == 0) a.ml[row] = make_float2(m[nt][i], l[nt][i]);
                 }
             }
     }
@@ -981,10 +868,20 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // ----------------------------------------------------------------- more rows
 
 // Items of N rows on the fifth-generation tensor cores: a CTA is a worker, 128 keys a
-// tile.  Codes become fp16 in shared memory, scaled there (K's and V's rows by their
-// scales relative to the row's largest, which a code times is exact in fp16), in the
-// order in which a row's codes lie; Q has the same order, and O's is undone where it is
-// written.  S^T = K Q^T has keys as lanes, O^T = V^T P^T elements of d.
+// tile.  Codes become fp16 and are scaled on the way (by a row's scales relative to its
+// largest, times 2^10: with a code exact in fp16), in the order in which a row's codes
+// lie; Q has the same order, and O's is undone where it is written.  S^T = K Q^T has keys
+// as lanes and K in tensor memory (in shared memory its tile was written and read at
+// what V's takes too, and that was all the time there is: 107 us for the 104 above),
+// O^T = V^T P^T elements of d as lanes and V in shared memory, read across its rows.
+//
+// What bounds it: a product of 128 x N x 16 takes 50 (K) and 80 (V) cycles whatever N up
+// to 32 is, for reading its 128 rows: 2100 cycles for 128 keys of 256; the chain from
+// scores to weights takes 2700.  Measured 3100, where HBM takes 1490.  64 requests of 8192 keys
+// and 8 heads: 16 rows of 256 346 us, 32 rows 360, 32 rows of 128 258 (16 rows of 256
+// with m16n8k16 and two warps an item 362, 32 rows of 128 so 352; 16 rows of 128 226,
+// and 185 by single warps).  Loads that do not depend on the scores, made before the wait for them:
+// 10 % slower (registers).
 template <int D, int N> struct Mid {
     static constexpr int kRows = N, kThreads = 896, kWorkers = 1, kHalves = D / 128;
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
@@ -1147,6 +1044,15 @@ template <int N> __device__ __forceinline__ void tmem_st(uint32_t at, const uint
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// A barrier of the softmax's 256 threads, and one with the `or` of a flag over them.
+__device__ __forceinline__ void soft_sync() { asm volatile("barrier.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool soft_or(bool x) {
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(y) : "r"((uint32_t)x) : "memory");
+    return y != 0;
+}
+
 // Warps 0 to 7 do the softmax (a quarter of the keys, at the end of d, and half the rows
 // each), 8 to 15 expand K and 16 to 23 V (two threads a key), 24 and 25 copy, 26 and 27
 // issue the two products.
@@ -1256,7 +1162,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 }
             }
             fence_async_smem();
-            team_sync<8>(0);
+            soft_sync();
             if (lane == 0) mbar_arrive(&sh.q_full);
             const int lim_min = row_lim[0];
             uint64_t l[kC / 2];
@@ -1288,9 +1194,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     most = fmax3(most, y[0], y[1]);
                 }
                 // O and l follow a row's running maximum as above.
-                if (team_or<8>(0, most > kTau + kLift || !ok)) {
+                if (soft_or(most > kTau + kLift || !ok)) {
                     if (ok && tile) ok = wait2(sh.pv_done, tile - 1);
-                    ok = !team_or<8>(0, !ok);
+                    ok = !soft_or(!ok);
                     if (!ok) break;
                     tc_fence_after();
                     float v[kC];
@@ -1298,13 +1204,13 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     for (int i = 0; i < kC; ++i) v[i] = z[i];
                     const float x = over_lanes<kC>(v, lane, [](float y, float u) { return fmaxf(y, u); });
                     if (lane < kC) row_x[quarter * N + lane] = x;
-                    team_sync<8>(0);
+                    soft_sync();
                     if (quarter == 0 && lane < kC) {
                         const float m = -row_m[lane], next = fmaxf(m, fmaxf(fmaxf(row_x[lane], row_x[N + lane]), fmaxf(row_x[2 * N + lane], row_x[3 * N + lane])) - kLift);
                         row_f[lane] = ex2_mufu(m - next);
                         row_m[lane] = -next;
                     }
-                    team_sync<8>(0);
+                    soft_sync();
 #pragma unroll
                     for (int i = 0; i < kC; i += 2) l[i / 2] = f2_mul(l[i / 2], *reinterpret_cast<const uint64_t*>(row_f + i));
                     if (p > it.p0) {
@@ -1346,7 +1252,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             for (int i = 0; i < kC; i += 2) f2_unpack(l[i / 2], v[i], v[i + 1]);
             const float sum = over_lanes<kC>(v, lane, [](float x, float y) { return x + y; });
             if (lane < kC) row_x[quarter * N + lane] = sum;
-            ok = !team_or<8>(0, !ok);
+            ok = !soft_or(!ok);
             if (!ok) break;
             if (quarter == 0 && lane < kC) {
                 const float total = row_x[lane] + row_x[N + lane] + row_x[2 * N + lane] + row_x[3 * N + lane], m = -row_m[lane];
@@ -1362,7 +1268,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     }
                 }
             }
-            team_sync<8>(0);
+            soft_sync();
 #pragma unroll
             for (int h = 0; h < K::kHalves; ++h) {
                 uint32_t r[kC];
@@ -1384,7 +1290,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 }
             }
             tc_fence_before();
-            team_sync<8>(0);                         // the rows' numbers are read
+            soft_sync();                         // the rows' numbers are read
         }
     } else if (warp < 24) {
         regs_dec<64>();
@@ -1924,9 +1830,10 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     a.ps_log2 = lg;
     a.max_seqlen = max_seqlen;
     a.scale_log2 = alpha * 1.4426950408889634f;
+    // Which kernel, by rows an item: see the figures at "more rows".
     const int rows = item_rows(max_seqlen * (long long)G);
     if (d == 64) return rows == 8 ? launch_warps<64, 1>(a, sms, stream) : rows == 16 ? launch_warps<64, 2>(a, sms, stream) : launch_warps<64, 4>(a, sms, stream);
-    if (d == 128) return rows == 8 ? launch_warps<128, 1>(a, sms, stream) : rows == 16 ? launch_mid<128, 16>(a, sms, stream) : launch_mid<128, 32>(a, sms, stream);
+    if (d == 128) return rows == 8 ? launch_warps<128, 1>(a, sms, stream) : rows == 16 ? launch_warps<128, 2>(a, sms, stream) : launch_mid<128, 32>(a, sms, stream);
     return rows == 8 ? launch_warps<256, 1>(a, sms, stream) : rows == 16 ? launch_mid<256, 16>(a, sms, stream) : launch_mid<256, 32>(a, sms, stream);
 }
 

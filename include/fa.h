@@ -570,8 +570,8 @@ int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages
  * weights fp16 relative to the largest weight times value scale (one below 2^-30 of
  * it counts for nothing in O), the queries fp16 relative to a row's largest element
  * (exact down to 2^-31 of it).
- * Up to 64 rows of a request and key/value head (max_seqlen * Hq / Hkv; 128 at d =
- * 256) are computed from the codes; above that, and while 4 * B * table_width * page_size
+ * Up to d rows of a request and key/value head (max_seqlen * Hq / Hkv) are computed
+ * from the codes; above that, and while 4 * B * table_width * page_size
  * * Hkv * d is up to 2^32, the call expands the requests' pages into the
  * workspace once and goes on as fa_prefix_fwd.  A workspace too small for that, but
  * not for a call with max_seqlen 1, makes the rows be computed from the codes: right,

@@ -245,8 +245,8 @@ def test_long_histories(fa, d, hq, hkv):
 
 @pytest.mark.parametrize("d,hq,hkv,n", [(256, 32, 1, 1), (256, 16, 1, 1), (256, 24, 2, 2), (256, 8, 1, 4), (128, 32, 1, 1), (128, 8, 1, 5), (128, 20, 4, 4)])
 def test_rows_that_warps_share(fa, d, hq, hkv, n):
-    """17 to 32 rows (9 to 16 at d = 256) are worked on by two or four warps: long and
-    short lists, absent pages, scales of every size, maxima that jump."""
+    """More than 16 rows (8 at d = 256) are shared by a block's warps: long and short
+    lists, absent pages, scales of every size, maxima that jump."""
     s = [3000, 17, 900, 0, 65, 2100]
     b = Batch(hq, hkv, d, 16, s, [n] * len(s), seed=d + hq, v_scales=(0, 0xF7))
     b.check(fa, *b.run(fa))
@@ -257,6 +257,40 @@ def test_rows_that_warps_share(fa, d, hq, hkv, n):
     b.ks[b.table[0][3], :, 5, 0] = 0xFC               # a key that every row of the request sees
     o, lse = b.run(fa)
     assert torch.isnan(o[:n]).all() and torch.isnan(lse[:, :n]).all() and not torch.isnan(o[n:sum(b.n)]).any()
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("d,hq,hkv", [(256, 12, 1), (256, 32, 1), (128, 32, 1), (128, 24, 2)])
+def test_more_rows_over_pages_of_every_size(fa, page, d, hq, hkv):
+    """Tiles of 128 keys over pages of 16 to 256: ends inside a page and a tile, pages
+    missing inside a run of keys, several blocks of rows, scores that rise with the
+    key, so that maxima move again and again."""
+    s, n = [1000, 40, 129, 128, 2300, 127, 3], [1, 4, 2, 1, 3, 1, 3]
+    b = Batch(hq, hkv, d, page, s, n, seed=page + d, std=4.0)
+    for row, m in zip(b.table, s):
+        for j in range(m):
+            b.ks[row[j // page], :, j % page] = 0x58 + 0x28 * j // m
+    b.check(fa, *b.run(fa))
+    for row in (b.table[0], b.table[4]):
+        row[1:-1:3] = [(-1, 1 << 30, -7)[i % 3] for i in range(len(row[1:-1:3]))]
+    b.check(fa, *b.run(fa))
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_more_rows_of_many_requests(fa, d):
+    """More items than blocks, none and one key among them, on two streams at once."""
+    g = np.random.default_rng(d)
+    s = [int(x) for x in g.integers(0, 300, 400)]
+    n = [int(x) for x in g.integers(0, 3, 400)]
+    b, c = (Batch(20, 1, d, 16, s, n, seed=d + i) for i in range(2))
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    o, lse = b.run(fa)
+    with torch.cuda.stream(other):
+        o2, lse2 = c.run(fa)
+    torch.cuda.synchronize()
+    b.check(fa, o, lse)
+    c.check(fa, o2, lse2)
 
 
 def test_many_requests(fa):
