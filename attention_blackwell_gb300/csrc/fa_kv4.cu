@@ -889,10 +889,9 @@ template <int D, int N> struct Mid {
     static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
     static constexpr int kWeights = D == 256 ? 1 : 2;    // tiles of weights (of V's rows, two)
     static constexpr uint32_t kP1 = 128 * 2 * N, kV = 0, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + kWeights * kP1, kRawV = kRawK + kRing * kSlotK;
-    // What the softmax wants of four tiles' keys; rows: less their maximum, factors, what a
-    // sum is multiplied by, keys seen, maxima or sums of four quarters.
-    static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRowM = kKeys + 4 * 128 * 4,
-                              kRowF = kRowM + N * 4, kRowUp = kRowF + N * 4, kRowLim = kRowUp + N * 4, kRowX = kRowLim + N * 4, kWarp = kRowX + 4 * N * 4;
+    // What the softmax wants of four tiles' keys; rows of two items: less their maximum, what
+    // a sum is multiplied by, keys seen; factors, maxima or sums of four quarters.
+    static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRows2 = kKeys + 4 * 128 * 4, kRowF = kRows2 + 2 * 3 * N * 4, kRowX = kRowF + N * 4, kWarp = kRowX + 4 * N * 4;
     // Tensor memory: scores of two tiles, O, K's rows of two tiles.
     static constexpr uint32_t kColO = 2 * N, kColK = kColO + kHalves * N, kColumns = kColK + D <= 256 ? 256 : 512;
     static_assert((N == 16 || N == 32) && (D == 128 || D == 256), "sizes built");
@@ -1117,25 +1116,24 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
         regs_inc<104>();
         const int quarter = warp & 3, c0 = (warp >> 2) * kC, key = quarter * 32 + lane;
         const uint32_t lanes = tmem + ((uint32_t)quarter << 21) + c0;
-        float *const row_m = reinterpret_cast<float*>(dsmem + K::kRowM) + c0, *const row_f = reinterpret_cast<float*>(dsmem + K::kRowF) + c0,
-              *const row_up = reinterpret_cast<float*>(dsmem + K::kRowUp) + c0, *const row_x = reinterpret_cast<float*>(dsmem + K::kRowX) + c0;
-        int* const row_lim = reinterpret_cast<int*>(dsmem + K::kRowLim) + c0;
+        float *const row_f = reinterpret_cast<float*>(dsmem + K::kRowF) + c0, *const row_x = reinterpret_cast<float*>(dsmem + K::kRowX) + c0;
         // Its weights: 16-byte pieces, swizzled.
         uint8_t* const p_key = dsmem + K::kP + key * (2 * N);
         const int p_piece = N == 32 ? c0 / 8 ^ (key >> 1 & 3) : c0 / 8 ^ (key >> 2 & 1);
-        while (ok && walk.next(a, t, it)) {
-            // Q in the codes' order, scaled by a power of two.
+        // An item's Q in the codes' order, scaled by a power of two, and its rows' numbers.
+        auto stage = [&](const KvItem& item, uint32_t which) {
+            float* const rows = reinterpret_cast<float*>(dsmem + K::kRows2) + which * (3 * N);
             constexpr int kW = D / 8, kPer = 32 / kW, kPasses = N / 8 / kPer;      // 16-byte pieces of a row of fp16; rows a pass
             const int w = lane % kW, e0 = element_at<D>(8 * w);
             uint2 in[kPasses][2];
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int x = (warp * kPasses + i) * kPer + lane / kW;
-                const uint32_t row = (uint32_t)it.rb * N + x;
+                const uint32_t row = (uint32_t)item.rb * N + x;
                 const int tok = (int)(row / (uint32_t)a.G), h = (int)row - tok * a.G;
                 in[i][0] = in[i][1] = make_uint2(0, 0);
-                if (x < it.rows) {
-                    const __nv_bfloat16* src = a.q + (long long)(it.c0 + tok) * a.q_stride + (it.hk * a.G + h) * D + e0;
+                if (x < item.rows) {
+                    const __nv_bfloat16* src = a.q + (long long)(item.c0 + tok) * a.q_stride + (item.hk * a.G + h) * D + e0;
                     in[i][0] = *reinterpret_cast<const uint2*>(src);
                     in[i][1] = *reinterpret_cast<const uint2*>(src + 32);
                 }
@@ -1156,14 +1154,23 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 for (int y = 0; y < 4; ++y) q[y] = pack_f16x2(__uint_as_float(v[y] << 16) * down, __uint_as_float(v[y] & 0xffff0000u) * down);
                 sts(dsmem + K::kQ + (w >> 3) * K::kQBox + x * 128 + ((w & 7) ^ (x & 7)) * 16, q);
                 if (w == 0) {
-                    row_up[x - c0] = a.scale_log2 * __uint_as_float((uint32_t)(e - kQLift) << 23);
-                    row_m[x - c0] = -kNone;
-                    row_lim[x - c0] = min(it.s, it.s - it.n + (int)(((uint32_t)it.rb * N + x) / (uint32_t)a.G) + 1);
+                    rows[N + x] = a.scale_log2 * __uint_as_float((uint32_t)(e - kQLift) << 23);
+                    rows[x] = -kNone;
+                    reinterpret_cast<int*>(rows)[2 * N + x] = min(item.s, item.s - item.n + (int)(((uint32_t)item.rb * N + x) / (uint32_t)a.G) + 1);
                 }
             }
             fence_async_smem();
-            soft_sync();
+            __syncwarp();
             if (lane == 0) mbar_arrive(&sh.q_full);
+        };
+        KvItem coming;
+        bool more = walk.next(a, t, coming);
+        if (more) stage(coming, 0);
+        for (uint32_t which = 0; ok && more; which ^= 1) {
+            it = coming;
+            soft_sync();                             // its rows' numbers are there, those of the one before read
+            float *const row_m = reinterpret_cast<float*>(dsmem + K::kRows2) + which * (3 * N) + c0, *const row_up = row_m + N;
+            int* const row_lim = reinterpret_cast<int*>(row_up + N);
             const int lim_min = row_lim[0];
             uint64_t l[kC / 2];
 #pragma unroll
@@ -1245,7 +1252,12 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full[tile & 1]);
             }
-            if (ok) ok = wait2(sh.pv_done, tile - 1);
+            // The next item's Q, whose first scores are then there when this one is written.
+            if (ok) {
+                more = walk.next(a, t, coming);
+                if (more) stage(coming, which ^ 1);
+                ok = wait2(sh.pv_done, tile - 1);
+            }
             tc_fence_after();
             float v[kC];
 #pragma unroll
@@ -1273,24 +1285,40 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             for (int h = 0; h < K::kHalves; ++h) {
                 uint32_t r[kC];
                 tmem_ld<kC>(lanes + K::kColO + N * h, r);
-                const int e = element_at<D>(h * 128 + key);
-                if (it.whole) {
-                    const uint32_t row = (uint32_t)it.rb * N + c0;
-                    int tok = (int)(row / (uint32_t)a.G), hh = (int)row - tok * a.G;
+                // Four lanes hold four neighbours of every row: each takes one row of four.
+                const int e = element_at<D>(h * 128 + (key & ~3)), q = lane & 3;
 #pragma unroll
-                    for (int i = 0; i < kC; ++i) {
-                        if (c0 + i < it.rows)
-                            a.o[((long long)(it.c0 + tok) * a.Hq + it.hk * a.G + hh) * D + e] = __float2bfloat16(row_f[i] == 0.f ? 0.f : __uint_as_float(r[i]) * row_f[i]);
-                        if (++hh == a.G) hh = 0, ++tok;
+                for (int i = 0; i < kC; i += 4) {
+#pragma unroll
+                    for (int j = i; j < i + 4; j += 2) {
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, q & 1 ? r[j] : r[j + 1], 1);
+                        if (q & 1) r[j] = other; else r[j + 1] = other;
                     }
-                } else {
 #pragma unroll
-                    for (int i = 0; i < kC; ++i)
-                        if (c0 + i < it.rows) a.seg[((long long)it.seg * N + c0 + i) * D + e] = __uint_as_float(r[i]) * row_f[i];
+                    for (int j = i; j < i + 2; ++j) {
+                        const uint32_t other = __shfl_xor_sync(0xffffffffu, q & 2 ? r[j] : r[j + 2], 2);
+                        if (q & 2) r[j] = other; else r[j + 2] = other;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kC; i += 4) {
+                    const int x = c0 + i + q;
+                    if (x >= it.rows) break;
+                    const float f = row_f[i + q];
+                    float y[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) y[j] = f == 0.f ? 0.f : __uint_as_float(r[i + j]) * f;
+                    if (it.whole) {
+                        const uint32_t row = (uint32_t)it.rb * N + x;
+                        const int tok = (int)(row / (uint32_t)a.G), hh = (int)row - tok * a.G;
+                        *reinterpret_cast<uint2*>(a.o + ((long long)(it.c0 + tok) * a.Hq + it.hk * a.G + hh) * D + e) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+                    } else {
+                        *reinterpret_cast<float4*>(a.seg + ((long long)it.seg * N + x) * D + e) = make_float4(y[0], y[1], y[2], y[3]);
+                    }
                 }
             }
             tc_fence_before();
-            soft_sync();                         // the rows' numbers are read
+            __syncwarp();
         }
     } else if (warp < 24) {
         regs_dec<64>();
