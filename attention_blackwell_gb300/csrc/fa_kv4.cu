@@ -44,9 +44,9 @@
 //   Measured 120: neither alone is the limit (without conversions, in an
 //   experiment, 107; copies alone 93).  8 us pass before the first product: lengths,
 //   walk, page numbers and copies depend on one another.  The join takes 5.
-//   d = 64, 16 heads with 1 to 8 drafted tokens, up to 4096 keys (98 MB): 39 us, 186
+//   d = 64, 16 heads with 1 to 8 drafted tokens, up to 4096 keys (98 MB): 40 us, 186
 //   instructions for 1088 bytes, the same start.
-//   32 rows of 256 over up to 16384 keys (234 MB): 104 us (134 when four warps shared an
+//   32 rows of 256 over up to 16384 keys (234 MB): 90 us (134 when four warps shared an
 //   item's 32 rows with m16n8k16); see "more rows".
 //   one token over 1017 keys: 13 us, 12 as a graph.
 //   prompts, six of up to 2048 tokens over up to 10000 keys (563 GFLOP): 520 us, 25 of
@@ -70,6 +70,7 @@ constexpr int kQLift = 14;              // a query's largest element becomes 2^1
 constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every finite score; a hidden key's -inf less it is -inf
 constexpr int kUnit = 64;               // keys a unit
 constexpr int kMaxKeys = 1 << 29;       // of a request
+constexpr int kExtraMost = 12;          // units that an item costs besides its keys', at most
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
 // Rows of a request and key/value head above which pages are expanded.  8 requests of
 // 8000 keys and 8 heads of 128, from the codes and expanded: 64 rows 75 and 133 us, 128
@@ -84,7 +85,7 @@ constexpr int kTableMost = 128;
 __host__ __device__ constexpr uint32_t table_bytes(int B) { return (4u * B + 3) * 4; }
 
 template <int D, int NT> struct Kv {
-    static constexpr int kRows = 8 * NT;                 // rows of an item
+    static constexpr int kRows = 8 * NT, kExtra = 1;     // rows of an item
     static constexpr int kGroups = D / 32;
     static constexpr int kWorkers = D == 64 || NT * D <= 128 ? 12 : 8, kThreads = 32 * kWorkers;   // a CTA's warps, one CTA an SM
     static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
@@ -139,10 +140,10 @@ struct KvTables {
 };
 
 // Row blocks of a request with n tokens, units of each of its items: its tiles of
-// keys and one for what an item costs besides.
+// keys and `extra` for what an item costs besides.
 // (T * Hq fits 31 bits, so rows of a request do.)
 __device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (int)(((uint32_t)(n * G) + (uint32_t)rows - 1) / (uint32_t)rows); }
-__device__ __forceinline__ int item_units(int s) { return s > 0 ? (s + kUnit - 1) / kUnit + 1 : 0; }
+__device__ __forceinline__ int item_units(int s, int extra) { return s > 0 ? (s + kUnit - 1) / kUnit + extra : 0; }
 
 // The keys that row block rb's last row sees.
 __device__ __forceinline__ int keys_seen(int n, int s, int G, int rb, int rows) {
@@ -151,9 +152,9 @@ __device__ __forceinline__ int keys_seen(int n, int s, int G, int rb, int rows) 
 }
 
 // The parts that units [first, last) of an item stand for.
-__device__ __forceinline__ void parts_of(int first, int last, int seen, int& p0, int& p1) {
-    p0 = max(first - 1, 0) * (kUnit / 16);
-    p1 = min(max(last - 1, 0) * (kUnit / 16), seen > 0 ? (seen + 15) >> 4 : 0);
+__device__ __forceinline__ void parts_of(int first, int last, int seen, int extra, int& p0, int& p1) {
+    p0 = max(first - extra, 0) * (kUnit / 16);
+    p1 = min(max(last - extra, 0) * (kUnit / 16), seen > 0 ? (seen + 15) >> 4 : 0);
 }
 
 struct KvItem {
@@ -165,7 +166,7 @@ struct KvItem {
 };
 
 // A worker's walk over its units.
-template <int ROWS>
+template <int ROWS, int EXTRA>
 struct KvWalk {
     int u, end, b, worker;
     __device__ __forceinline__ void start(const KvArgs& a, const KvTables& t, const KvHeader& h, int w) {
@@ -182,12 +183,12 @@ struct KvWalk {
     __device__ __forceinline__ bool next(const KvArgs& a, const KvTables& t, KvItem& it) {
         while (u < end) {
             while (t.pref[b + 1] <= u) ++b;
-            const int n = t.cu[b + 1] - t.cu[b], s = t.len[b], per = item_units(s), nb = row_blocks(n, a.G, ROWS);
+            const int n = t.cu[b + 1] - t.cu[b], s = t.len[b], per = item_units(s, EXTRA), nb = row_blocks(n, a.G, ROWS);
             const int at = u - t.pref[b], i = at / per, first = at - i * per, last = min(per, first + end - u);
             u += last - first;
             const int hk = i / nb, rb = i - hk * nb, seen = keys_seen(n, s, a.G, rb, ROWS);
             int p0, p1;
-            parts_of(first, last, seen, p0, p1);
+            parts_of(first, last, seen, EXTRA, p0, p1);
             if (p0 >= p1) continue;
             it.b = b;
             it.hk = hk;
@@ -274,7 +275,7 @@ __device__ __forceinline__ KvHeader build_tables(const KvArgs& a, const KvTables
             const int n = t.cu[i + 1] - t.cu[i];
             if (n > a.max_seqlen) sh.bad = 1;
             it = row_blocks(n, a.G, K::kRows) * a.Hkv;
-            u = it * item_units(t.len[i]);
+            u = it * item_units(t.len[i], K::kExtra);
         }
         const int u_own = u, it_own = it;
 #pragma unroll
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     const int worker = blockIdx.x * K::kWorkers + warp;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
-    KvWalk<K::kRows> ahead;
+    KvWalk<K::kRows, K::kExtra> ahead;
     KvItem to = {};
     ahead.start(a, t, hdr, worker);
     bool more = ahead.next(a, t, to);
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     };
     copy();
 
-    KvWalk<K::kRows> walk;
+    KvWalk<K::kRows, K::kExtra> walk;
     KvItem it;
     walk.start(a, t, hdr, worker);
     uint32_t read = 0, slot = 0, phase = 0;
@@ -871,19 +872,22 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // tile.  Codes become fp16 and are scaled on the way (by a row's scales relative to its
 // largest, times 2^10: with a code exact in fp16), in the order in which a row's codes
 // lie; Q has the same order, and O's is undone where it is written.  S^T = K Q^T has keys
-// as lanes and K in tensor memory (in shared memory its tile was written and read at
-// what V's takes too, and that was all the time there is: 107 us for the 104 above),
-// O^T = V^T P^T elements of d as lanes and V in shared memory, read across its rows.
+// as lanes and K in tensor memory, O^T = V^T P^T elements of d as lanes and V in shared
+// memory, read across its rows.  (With K in shared memory too, its tile written and read
+// there took as long as V's: 107 us where this took 104.)
 //
-// What bounds it: a product of 128 x N x 16 takes 50 (K) and 80 (V) cycles whatever N up
-// to 32 is, for reading its 128 rows: 2100 cycles for 128 keys of 256; the chain from
-// scores to weights takes 2700.  Measured 3100, where HBM takes 1490.  64 requests of 8192 keys
-// and 8 heads: 16 rows of 256 346 us, 32 rows 360, 32 rows of 128 258 (16 rows of 256
-// with m16n8k16 and two warps an item 362, 32 rows of 128 so 352; 16 rows of 128 226,
-// and 185 by single warps).  Loads that do not depend on the scores, made before the wait for them:
-// 10 % slower (registers).
+// What bounds it: a product of 128 x N x 16 takes about 50 (K) and 80 (V) cycles for its
+// 128 rows, whatever N up to 32 is: 2050 cycles for 128 keys of 256, 58 % of a CTA's
+// time (32 rows over up to 16384 keys); issue slots 61 %; a chain from scores to weights
+// of 2700, tiles one after another.  HBM takes 1490.  64 requests of 8192 keys and 8
+// heads: 16 rows of 256 322 us, 32 rows 359, 32 rows of 128 258 (16 rows of 256 with
+// m16n8k16 and two warps an item 362, 32 rows of 128 so 352; 16 rows of 128 this way
+// 226, and 185 by single warps).  Row numbers loaded before the wait for the scores: 10
+// % slower (registers).
 template <int D, int N> struct Mid {
-    static constexpr int kRows = N, kThreads = 896, kWorkers = 1, kHalves = D / 128;
+    // An item's start and end take as long as 12 units (100 requests of up to 16384 keys, 32 rows of 256: with 3, 6,
+    // 8, 12 and 16 100, 96, 94, 91 and 91 us).
+    static constexpr int kRows = N, kExtra = 12, kThreads = 896, kWorkers = 1, kHalves = D / 128;
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
     static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
@@ -894,7 +898,7 @@ template <int D, int N> struct Mid {
     static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRows2 = kKeys + 4 * 128 * 4, kRowF = kRows2 + 2 * 3 * N * 4, kRowX = kRowF + N * 4, kWarp = kRowX + 4 * N * 4;
     // Tensor memory: scores of two tiles, O, K's rows of two tiles.
     static constexpr uint32_t kColO = 2 * N, kColK = kColO + kHalves * N, kColumns = kColK + D <= 256 ? 256 : 512;
-    static_assert((N == 16 || N == 32) && (D == 128 || D == 256), "sizes built");
+    static_assert((N == 16 || N == 32) && (D == 128 || D == 256) && kExtra <= kExtraMost, "sizes built");
     static_assert(kRawK % 1024 == 0 && kWarp % 16 == 0 && kWarp + table_bytes(kTableMost) + 1024 <= 232448, "shared memory plan");
 };
 struct MidShared : KvScan {
@@ -1058,7 +1062,7 @@ __device__ __forceinline__ bool soft_or(bool x) {
 template <int D, int N>
 __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
     using K = Mid<D, N>;
-    using Walk = KvWalk<N>;
+    using Walk = KvWalk<N, K::kExtra>;
     constexpr int kG = D / 32, kC = N / 2;
     constexpr uint32_t kRing = K::kRing;
     extern __shared__ __align__(1024) uint8_t dsmem_tiles[];
@@ -1484,7 +1488,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
 
 // Joins the segments of a row (of one head) that a range's end has cut; writes the
 // rows without a key.  A warp a row, or with few rows a block of eight.
-template <int D, bool kSplit>
+template <int D, bool kSplit, int kExtra>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_item) {
     constexpr int E = D / 32;
     __shared__ float s_o[kSplit ? 8 : 1][kSplit ? D : 1];
@@ -1497,7 +1501,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_
     const KvRow q = a.rows[t];
     if (hdr.bad || q.n == 0) return;
     const int row = (t - q.c0) * a.G + h - hk * a.G, rb = row / rows_item, in = row - rb * rows_item, nb = row_blocks(q.n, a.G, rows_item);
-    const int units = item_units(q.s), item = hk * nb + rb, u0 = q.pref + item * units, seen = keys_seen(q.n, q.s, a.G, rb, rows_item);
+    const int units = item_units(q.s, kExtra), item = hk * nb + rb, u0 = q.pref + item * units, seen = keys_seen(q.n, q.s, a.G, rb, rows_item);
     const bool some = units > 0 && seen > 0;
     const int first = some ? worker_of(hdr, u0) : 0, all = some ? worker_of(hdr, u0 + units - 1) - first + 1 : 0;
     // Row in the k-th worker's segment, -1: it has none.
@@ -1505,7 +1509,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const KvArgs a, int rows_
         if (k >= all) return -1;
         const int from = max(0, unit_of(hdr, first + k) - u0), to = min(units, unit_of(hdr, first + k + 1) - u0);
         int p0, p1;
-        parts_of(from, to, seen, p0, p1);
+        parts_of(from, to, seen, kExtra, p0, p1);
         if (p0 >= p1) return -1;
         return p0 == 0 && p1 == (seen + 15) >> 4 ? -2 : (long long)(q.items + item + first + k) * rows_item + in;
     };
@@ -1705,13 +1709,13 @@ int launch_few(void (*kern)(KvArgs), std::atomic<uint64_t>& prepared, const KvAr
     }
     // Twice the CTAs that one unit a worker takes, up to what the SMs hold.
     const long long items = (long long)a.Hkv * ((long long)a.T * a.G / K::kRows + (a.T < a.B ? a.T : a.B));
-    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + 1) + K::kWorkers - 1) / K::kWorkers;
+    const long long need = (items * ((((long long)a.W << a.ps_log2) + kUnit - 1) / kUnit + K::kExtra) + K::kWorkers - 1) / K::kWorkers;
     const int grid = 2 * need < sms ? (int)(2 * need) : sms;
     if (launch_dependent(kern, grid, K::kThreads, smem, stream, a) != cudaSuccess) return FA_ERR_LAUNCH;
     const long long rows = (long long)a.T * a.Hq;
     cudaError_t e;
-    if (rows <= 8LL * sms) e = launch_dependent(kv4_join_kernel<D, true>, (int)rows, 256, 0, stream, a, K::kRows);
-    else e = launch_dependent(kv4_join_kernel<D, false>, (int)((rows + 7) / 8), 256, 0, stream, a, K::kRows);
+    if (rows <= 8LL * sms) e = launch_dependent(kv4_join_kernel<D, true, K::kExtra>, (int)rows, 256, 0, stream, a, K::kRows);
+    else e = launch_dependent(kv4_join_kernel<D, false, K::kExtra>, (int)((rows + 7) / 8), 256, 0, stream, a, K::kRows);
     return e == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 template <int D, int NT> int launch_warps(const KvArgs& a, int sms, cudaStream_t stream) {
@@ -1795,9 +1799,9 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     const int G = Hq / Hkv;
     if (max_seqlen > T) max_seqlen = T;
     // The list of units at its longest fits 32 bits, a worker's share past it too.
-    const long long tiles = ((long long)table_width * page_size + kUnit - 1) / kUnit + 1;
+    const long long tiles = ((long long)table_width * page_size + kUnit - 1) / kUnit + kExtraMost;
     const long long items = (long long)Hkv * ((long long)T * G / 8 + (T < B ? T : B));
-    if (items * (tiles + 2) > 1 << 30) return FA_ERR_UNSUPPORTED;
+    if (items * (tiles + 1) > 1 << 30) return FA_ERR_UNSUPPORTED;
     const size_t row = (size_t)Hq * d * 2, cells = (size_t)num_pages * Hkv * page_size;
     const Span inputs[] = {{k_pages, cells * (d / 2)}, {v_pages, cells * (d / 2)}, {k_scales, cells * (d / 32)}, {v_scales, cells * (d / 32)},
                            {block_table, 4 * (size_t)B * table_width}, {kv_lens, 4 * (size_t)B}, {cu_seqlens, cu_seqlens ? 4 * ((size_t)B + 1) : 0}};

@@ -13,7 +13,7 @@
 // A unit is up to r.chunk rows of one token's q, k or v, which are adjacent in memory,
 // with its rows of the cos and sin tables.  Every warp has a ring of units in shared
 // memory, filled by bulk copies (what is in flight costs no registers; loaded into
-// registers ahead, the same work moved 4.6 TB/s at its best), and takes a range of
+// registers ahead, the same work moved 5.0 TB/s at its best), and takes a range of
 // the call's units.  d / 16 lanes share a row, so that a lane's 16 elements are
 // whole pairs whatever rot is: two 16-byte chunks.
 //
@@ -22,7 +22,7 @@
 // heads of 128 with norms: forward 46 us (271 MB, 5.9 TB/s), gradients 70 (405 MB; 5 of
 // them the sum over blocks).  10003 tokens of 8 + 1 heads of 256: gradients 39 (139 MB):
 // a unit of one row, k's, costs half of one of eight.  20011 tokens of 32 + 8 + 8 heads
-// into a 4-bit cache: 78 (432 MB), 2840 instructions a token, 62 % of the issue
+// into a 4-bit cache: 73 (432 MB), 2730 instructions a token, 65 % of the issue
 // slots.  64 tokens: 4 us on the GPU; the call from Python takes 13 to 18.
 #include <math.h>
 #include <stdint.h>
@@ -310,9 +310,8 @@ __device__ __forceinline__ Chunk chunk_of(const RopeArgs& r, int j) {
     return c;
 }
 
-// Bytes of rows a unit at most: four passes of 32 lanes; in the backward pass, whose
-// units hold two arrays, two.  What a unit costs besides its passes is worth one of
-// them.
+// Bytes of rows a unit at most, of each array: four passes of 32 lanes.  What a unit
+// costs besides its passes is worth one of them.
 constexpr int kBytes = 4096, kBytesGrad = 4096, kRing = 3, kRingPut = 2, kRingGrad = 2;
 constexpr int kWarps = 12, kWarpsPut = 16, kWarpsGrad = 12;      // a block, one an SM
 template <int D> constexpr int kPass = 512 / D;              // rows a pass

@@ -587,7 +587,7 @@ int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages
  * fa_get_device_status, one with a request of more rows than max_seqlen computes
  * nothing and reports FA_ERR_INVALID there.  T == 0 is a no-op.
  * Errors: as fa_prefix_fwd, and FA_ERR_UNSUPPORTED where key/value heads times
- * (T * Hq / Hkv / 8 + min(T, B)) times (table_width * page_size / 64 + 3) is
+ * (T * Hq / Hkv / 8 + min(T, B)) times (table_width * page_size / 64 + 14) is
  * above 2^30.
  */
 int fa_kv4_fwd(const void *q, int64_t q_stride, const void *k_pages, const void *k_scales, const void *v_pages,
