@@ -887,18 +887,18 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 template <int D, int N> struct Mid {
     // An item's start and end take as long as 12 units (100 requests of up to 16384 keys, 32 rows of 256: with 3, 6,
     // 8, 12 and 16 100, 96, 94, 91 and 91 us).
-    static constexpr int kRows = N, kExtra = 12, kThreads = 896, kWorkers = 1, kHalves = D / 128;
+    static constexpr int kRows = N, kExtra = 12, kThreads = 896, kWorkers = 1, kHalves = D == 256 ? 2 : 1;
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
-    static constexpr uint32_t kBox = 128 * 128, kTile = 2 * kHalves * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
+    static constexpr uint32_t kBox = 128 * 128, kTile = D / 64 * kBox, kQBox = N * 128;      // 64 elements of 128 keys, of N rows
     static constexpr int kWeights = D == 256 ? 1 : 2;    // tiles of weights (of V's rows, two)
-    static constexpr uint32_t kP1 = 128 * 2 * N, kV = 0, kQ = 2 * kTile, kP = kQ + 2 * kHalves * kQBox, kRawK = kP + kWeights * kP1, kRawV = kRawK + kRing * kSlotK;
+    static constexpr uint32_t kP1 = 128 * 2 * N, kV = 0, kQ = 2 * kTile, kP = kQ + D / 64 * kQBox, kRawK = kP + kWeights * kP1, kRawV = kRawK + kRing * kSlotK;
     // What the softmax wants of four tiles' keys; rows of two items: less their maximum, what
     // a sum is multiplied by, keys seen; factors, maxima or sums of four quarters.
     static constexpr uint32_t kKeys = kRawV + kRing * kSlotV, kRows2 = kKeys + 4 * 128 * 4, kRowF = kRows2 + 2 * 3 * N * 4, kRowX = kRowF + N * 4, kWarp = kRowX + 4 * N * 4;
     // Tensor memory: scores of two tiles, O, K's rows of two tiles.
     static constexpr uint32_t kColO = 2 * N, kColK = kColO + kHalves * N, kColumns = kColK + D <= 256 ? 256 : 512;
-    static_assert((N == 16 || N == 32) && (D == 128 || D == 256) && kExtra <= kExtraMost, "sizes built");
+    static_assert((N == 32 || (N == 16 && D == 256)) && (D == 64 || D == 128 || D == 256) && kExtra <= kExtraMost, "sizes built");
     static_assert(kRawK % 1024 == 0 && kWarp % 16 == 0 && kWarp + table_bytes(kTableMost) + 1024 <= 232448, "shared memory plan");
 };
 struct MidShared : KvScan {
@@ -923,7 +923,7 @@ template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, u
 // rows of N weights a key, 2 N bytes apart and swizzled over as many.
 template <int D, int N> __device__ __forceinline__ void mid_values(uint32_t o, uint32_t v_smem, uint32_t p_smem, uint32_t acc) {
     using K = Mid<D, N>;
-    constexpr uint32_t idesc = idesc_f16_f32(128, N, 1, 1);
+    constexpr uint32_t idesc = idesc_f16_f32(D == 64 ? 64 : 128, N, 1, 1);
     constexpr uint64_t kOther = (uint64_t)(N == 32 ? 4 ^ 2 : 6 ^ 2) << 61;      // 64- or 32-byte swizzle for 128
     const uint64_t ad = sdesc_sw128(v_smem, K::kBox, 1024), bd = sdesc_sw128(p_smem, 16, 16 * N) ^ kOther;
     static_for<8>([&](auto kc) {
@@ -952,7 +952,7 @@ template <int D> __device__ __forceinline__ uint32_t mid_scales(const uint32_t (
 // takes first depends on its key, so that neither loads nor stores meet in a bank.
 template <int D> __device__ __forceinline__ void mid_expand(const uint8_t* codes, uint8_t* tile, int key, int half, const uint32_t (&sc)[D / 32]) {
     constexpr int kC = D / 32, kG = D / 32;      // 16-byte pieces of a row
-    const int turn = (D == 256 ? key : key >> 1) + half * (kC / 2);
+    const int turn = (D == 256 ? key : D == 128 ? key >> 1 : 0) + half * (kC / 2);
     const uint8_t* row = codes + key * (D / 2);
     uint8_t* to = tile + key * 128;
     uint32_t w[kC / 2][4];
@@ -1245,8 +1245,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                     l[i / 2] = f2_fma(f2_pack(y[0], y[1]), f2_pack(back, back), l[i / 2]);
                     weights[i / 2] = pack_f16x2(y[0], y[1]);
                 }
-                // The weights that were here are multiplied.
-                if (tile >= K::kWeights) ok = wait2(sh.pv_done, tile - K::kWeights) && ok;
+                // The weights that were here are multiplied (with two tiles of them, before these
+                // scores were).
+                if (K::kWeights == 1 && tile) ok = wait2(sh.pv_done, tile - 1) && ok;
                 uint8_t* const to = p_key + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0);
 #pragma unroll
                 for (int i = 0; i < kC / 8; ++i)
@@ -1289,8 +1290,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
             for (int h = 0; h < K::kHalves; ++h) {
                 uint32_t r[kC];
                 tmem_ld<kC>(lanes + K::kColO + N * h, r);
-                // Four lanes hold four neighbours of every row: each takes one row of four.
-                const int e = element_at<D>(h * 128 + (key & ~3)), q = lane & 3;
+                // Four lanes hold four neighbours of every row: each takes one row of four.  (64
+                // elements are in the first 16 lanes of each quarter.)
+                const int e = element_at<D>((D == 64 ? quarter * 16 + (lane & 15) : h * 128 + key) & ~3), q = lane & 3;
 #pragma unroll
                 for (int i = 0; i < kC; i += 4) {
 #pragma unroll
@@ -1307,7 +1309,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
 #pragma unroll
                 for (int i = 0; i < kC; i += 4) {
                     const int x = c0 + i + q;
-                    if (x >= it.rows) break;
+                    if (x >= it.rows || (D == 64 && lane >= 16)) break;
                     const float f = row_f[i + q];
                     float y[4];
 #pragma unroll
@@ -1460,8 +1462,8 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                         mid_values<D, N>(tmem + K::kColO + N * h, smem + K::kV + (tile & 1) * K::kTile + h * 2 * K::kBox, smem + K::kP + (K::kWeights == 2 && (tile & 1) ? K::kP1 : 0), p > it.p0);
                     umma_commit_w(&sh.pv_done[tile & 1]);
                 } else {
-                    // The scores that were here are read.
-                    if (!(ok = wait2(sh.k_full, tile) && (tile < 2 || wait2(sh.p_full, tile - 2)))) break;
+                    // The scores that were here are read and their weights multiplied.
+                    if (!(ok = wait2(sh.k_full, tile) && (tile < 2 || wait2(sh.pv_done, tile - 2)))) break;
                     tc_fence_after();
                     mid_scores<D, N>(tmem + (tile & 1) * N, tmem + K::kColK + (tile & 1) * (D / 2), smem + K::kQ);
                     umma_commit_w(&sh.s_full[tile & 1]);
@@ -1864,7 +1866,7 @@ int fa_kv4_fwd(const void* q, int64_t q_stride, const void* k_pages, const void*
     a.scale_log2 = alpha * 1.4426950408889634f;
     // Which kernel, by rows an item: see the figures at "more rows".
     const int rows = item_rows(max_seqlen * (long long)G);
-    if (d == 64) return rows == 8 ? launch_warps<64, 1>(a, sms, stream) : rows == 16 ? launch_warps<64, 2>(a, sms, stream) : launch_warps<64, 4>(a, sms, stream);
+    if (d == 64) return rows == 8 ? launch_warps<64, 1>(a, sms, stream) : rows == 16 ? launch_warps<64, 2>(a, sms, stream) : launch_mid<64, 32>(a, sms, stream);
     if (d == 128) return rows == 8 ? launch_warps<128, 1>(a, sms, stream) : rows == 16 ? launch_warps<128, 2>(a, sms, stream) : launch_mid<128, 32>(a, sms, stream);
     return rows == 8 ? launch_warps<256, 1>(a, sms, stream) : rows == 16 ? launch_mid<256, 16>(a, sms, stream) : launch_mid<256, 32>(a, sms, stream);
 }
