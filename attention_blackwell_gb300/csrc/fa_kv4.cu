@@ -27,7 +27,7 @@
 // cut by a range's end leaves (M, l, O) in the workspace, and a second kernel joins
 // the segments in the list's order; one that is not cut is written at once.
 //
-// More than 16 rows (8 at d = 256; not at d = 64): a CTA is a worker, and the products
+// More than 16 rows (8 at d = 256): a CTA is a worker, and the products
 // are the fifth-generation tensor cores' (see "more rows" below): a code is converted
 // once for up to 32 rows, by warps that do nothing else.
 //
@@ -46,7 +46,7 @@
 //   walk, page numbers and copies depend on one another.  The join takes 5.
 //   d = 64, 16 heads with 1 to 8 drafted tokens, up to 4096 keys (98 MB): 40 us, 186
 //   instructions for 1088 bytes, the same start.
-//   32 rows of 256 over up to 16384 keys (234 MB): 90 us (134 when four warps shared an
+//   32 rows of 256 over up to 16384 keys (234 MB): 89 us (134 when four warps shared an
 //   item's 32 rows with m16n8k16); see "more rows".
 //   one token over 1017 keys: 13 us, 12 as a graph.
 //   prompts, six of up to 2048 tokens over up to 10000 keys (563 GFLOP): 520 us, 25 of
@@ -73,9 +73,9 @@ constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kExtraMost = 12;          // units that an item costs besides its keys', at most
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
 // Rows of a request and key/value head above which pages are expanded.  8 requests of
-// 8000 keys and 8 heads of 128, from the codes and expanded: 64 rows 75 and 133 us, 128
-// rows 136 and 142, 192 rows 199 and 149; of 64, 16 heads: 64 rows 126 and 152, 128 rows
-// 242 and 170; of 256, one head: 256 rows 60 and 61, 512 rows 97 and 72.
+// 8000 keys and 8 heads of 128, from the codes and expanded: 64 rows 73 and 133 us, 128
+// rows 130 and 142, 192 rows 199 and 149; of 64, 16 heads: 64 rows 117 and 152, 128 rows
+// 242 and 171; of 256, one head: 256 rows 57 and 61, 512 rows 97 and 72.
 constexpr int many_rows(int d) { return d; }
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
@@ -88,18 +88,17 @@ template <int D, int NT> struct Kv {
     static constexpr int kRows = 8 * NT, kExtra = 1;     // rows of an item
     static constexpr int kGroups = D / 32;
     static constexpr int kWorkers = D == 64 || NT * D <= 128 ? 12 : 8, kThreads = 32 * kWorkers;   // a CTA's warps, one CTA an SM
-    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 && NT <= 2 ? 2 : 1;   // 16-key parts a step
-    static constexpr int kSteps = D == 128 && NT <= 2 ? 2 : D == 64 && NT == 2 ? 2 : 1;   // steps a slot of the ring
+    static constexpr int kParts = D == 64 && NT == 1 ? 4 : D <= 128 ? 2 : 1;   // 16-key parts a step
+    static constexpr int kSteps = D == 128 || (D == 64 && NT == 2) ? 2 : 1;   // steps a slot of the ring
     static constexpr int kSlotParts = kParts * kSteps, kKeys = 16 * kParts;
     // A slot's keys in shared memory: K's codes, V's codes, K's scales, V's scales.
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kPart = 2 * (kCodes + kScales), kSlot = kSlotParts * kPart;
-    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 8) : 5;
-    static constexpr bool kQRegs = NT <= 2 && NT * D <= 256;     // Q's fragments in registers
-    static constexpr uint32_t kQBytes = kQRegs ? 0 : kRows * D * 2;
-    // A step's scales as the products want them: K's as floats
-    // [key][group], V's as pairs of keys [key / 2][group], (e, 2^-e) [key].
+    static constexpr uint32_t kRing = D == 128 ? (NT == 1 ? 2 : 3) : D == 64 ? (NT == 1 ? 4 : 3) : 5;
+    // A step's scales as the products want them: K's as floats [key][group], V's as pairs of
+    // keys [key / 2][group], (e, 2^-e) [key].
     static constexpr uint32_t kVPairs = kKeys * kGroups * 4, kExp = kVPairs + kKeys * kGroups * 2, kPrep = kExp + kKeys * 8;
-    static constexpr uint32_t kWarp = kRing * kSlot + kQBytes + kPrep;
+    static constexpr uint32_t kWarp = kRing * kSlot + kPrep;
+    static_assert(NT <= 2 && NT * D <= 256, "Q and O are in registers");
     static_assert(kPart % 16 == 0 && kWarp % 16 == 0 && kVPairs % 16 == 0 && kExp % 16 == 0 && kPrep % 16 == 0, "copies are 16-byte aligned");
     static_assert(kRing * kSlotParts <= 32 && kRing <= 8 && 4 * kSlotParts <= 32, "a bit a part, a lane a copy");
     static_assert(kWorkers * kWarp + table_bytes(kTableMost) + 1536 <= 232448, "shared memory plan");
@@ -493,7 +492,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 
     uint64_t* full = sh.full[warp];
     uint8_t* const ring = dsmem + warp * K::kWarp;
-    uint8_t *const q_smem = ring + kRing * K::kSlot, *const prep = q_smem + K::kQBytes;
+    uint8_t* const prep = ring + kRing * K::kSlot;
     const int worker = blockIdx.x * K::kWorkers + warp;
 
     // The copies: a walk of their own, ahead of the work by what the ring holds.
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
     while (ok && walk.next(a, t, it)) {
         // Q as B operands: lane (r, c) has row r's elements 32 g + 8 c to + 7, which
         // are what it reads of a key.
-        uint32_t qf[K::kQRegs ? NT : 1][K::kQRegs ? kG : 1][4];
+        uint32_t qf[NT][kG][4];
         // What a row's sums are multiplied by, and the keys it sees, of rows 2c and 2c + 1.
         float f[NT][2];
         int lim[NT][2];
@@ -593,20 +592,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
                 const uint32_t w[4] = {in[g].x, in[g].y, in[g].z, in[g].w};
-                uint32_t q[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q[i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
-                if constexpr (K::kQRegs) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[n][g][i] = q[i];
-                } else {
-                    sts(q_smem + ((n * kG + g) * 32 + lane) * 16, q);
-                }
+                for (int i = 0; i < 4; ++i) qf[n][g][i] = pack_f16x2(__uint_as_float(w[i] << 16) * down, __uint_as_float(w[i] & 0xffff0000u) * down);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xffffffffu, up, 8 * c + 4 * i);
         }
-        __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -672,13 +663,7 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
                         for (int i = 0; i < 2; ++i) sc[i] = f2_pack(__uint_as_float(ksc[i][g]), __uint_as_float(ksc[i][g]));
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            uint32_t q[4];
-                            if constexpr (K::kQRegs) {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) q[i] = qf[nt][g][i];
-                            } else {
-                                lds(q_smem + ((nt * kG + g) * 32 + lane) * 16, q);
-                            }
+                            const uint32_t (&q)[4] = qf[nt][g];
                             float acc[4];
                             mma_f16_0(acc, x[0][0][2 * gg], x[0][1][2 * gg], x[0][0][2 * gg + 1], x[0][1][2 * gg + 1], q[0], q[1]);
                             mma_f16(acc, x[1][0][2 * gg], x[1][1][2 * gg], x[1][0][2 * gg + 1], x[1][1][2 * gg + 1], q[2], q[3]);
@@ -879,11 +864,12 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // What bounds it: a product of 128 x N x 16 takes about 50 (K) and 80 (V) cycles for its
 // 128 rows, whatever N up to 32 is: 2050 cycles for 128 keys of 256, 58 % of a CTA's
 // time (32 rows over up to 16384 keys); issue slots 61 %; a chain from scores to weights
-// of 2700, tiles one after another.  HBM takes 1490.  64 requests of 8192 keys and 8
-// heads: 16 rows of 256 322 us, 32 rows 359, 32 rows of 128 258 (16 rows of 256 with
-// m16n8k16 and two warps an item 362, 32 rows of 128 so 352; 16 rows of 128 this way
-// 226, and 185 by single warps).  Row numbers loaded before the wait for the scores: 10
-// % slower (registers).
+// of 2700, tiles one after another.  HBM takes 1490.  At d = 128 and 64 the chain is all:
+// 2000 cycles a tile.  64 requests of 8192 keys and 8 heads: 16 rows of 256 326 us, 32
+// rows 353, 32 rows of 128 243, of 64 219; with m16n8k16 and one, two or four warps an item
+// 362 (16 of 256), 352 and 236; 16 rows of 128 this way 226, and 184 by single warps.
+// Without gain: row numbers loaded before the wait for the scores (registers), a flag and
+// weights worked out before it is looked at instead of a barrier a tile (89 us 94).
 template <int D, int N> struct Mid {
     // An item's start and end take as long as 12 units (100 requests of up to 16384 keys, 32 rows of 256: with 3, 6,
     // 8, 12 and 16 100, 96, 94, 91 and 91 us).
@@ -919,7 +905,7 @@ template <int D, int N> __device__ __forceinline__ void mid_scores(uint32_t s, u
         umma_ts_k<8 * k, bo>(s, k_tmem, bd, idesc, k > 0 ? 1u : 0u);
     });
 }
-// O^T (+)= V^T P^T for 128 of d, both MN-major: V's rows (two boxes of 64 elements), P's
+// O^T (+)= V^T P^T for 128 (64) of d, both MN-major: V's rows (boxes of 64 elements), P's
 // rows of N weights a key, 2 N bytes apart and swizzled over as many.
 template <int D, int N> __device__ __forceinline__ void mid_values(uint32_t o, uint32_t v_smem, uint32_t p_smem, uint32_t acc) {
     using K = Mid<D, N>;

@@ -243,7 +243,7 @@ def test_long_histories(fa, d, hq, hkv):
         b.check(fa, *b.run(fa))
 
 
-@pytest.mark.parametrize("d,hq,hkv,n", [(256, 32, 1, 1), (256, 16, 1, 1), (256, 24, 2, 2), (256, 8, 1, 4), (128, 32, 1, 1), (128, 8, 1, 5), (128, 20, 4, 4)])
+@pytest.mark.parametrize("d,hq,hkv,n", [(256, 32, 1, 1), (256, 16, 1, 1), (256, 24, 2, 2), (256, 8, 1, 4), (128, 32, 1, 1), (128, 8, 1, 5), (128, 20, 4, 4), (64, 32, 1, 1), (64, 8, 2, 5)])
 def test_rows_that_warps_share(fa, d, hq, hkv, n):
     """More than 16 rows (8 at d = 256) are shared by a block's warps: long and short
     lists, absent pages, scales of every size, maxima that jump."""
@@ -260,7 +260,7 @@ def test_rows_that_warps_share(fa, d, hq, hkv, n):
 
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
-@pytest.mark.parametrize("d,hq,hkv", [(256, 12, 1), (256, 32, 1), (128, 32, 1), (128, 24, 2)])
+@pytest.mark.parametrize("d,hq,hkv", [(256, 12, 1), (256, 32, 1), (128, 32, 1), (128, 24, 2), (64, 32, 1), (64, 20, 2)])
 def test_more_rows_over_pages_of_every_size(fa, page, d, hq, hkv):
     """Tiles of 128 keys over pages of 16 to 256: ends inside a page and a tile, pages
     missing inside a run of keys, several blocks of rows, scores that rise with the
@@ -276,7 +276,7 @@ def test_more_rows_over_pages_of_every_size(fa, page, d, hq, hkv):
     b.check(fa, *b.run(fa))
 
 
-@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("d", [64, 128, 256])
 def test_more_rows_of_many_requests(fa, d):
     """More items than blocks, none and one key among them, on two streams at once."""
     g = np.random.default_rng(d)
