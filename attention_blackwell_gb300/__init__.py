@@ -677,8 +677,11 @@ def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k
             _need(g, n, torch.float32)
             if g.numel() != d:
                 raise ValueError("%s must have d elements" % n)
-    if workspace is None and (q_weight is not None or k_weight is not None):
-        workspace = qk_rope_bwd_workspace(d, device=dq_out.device)
+    if workspace is None and (q_weight is not None or k_weight is not None):    # as qk_rope_bwd_workspace, the device being current
+        n = (_lib or lib()).fa_qk_rope_bwd_workspace_size(d)
+        if n == 0:
+            raise ValueError("invalid head dim for the workspace")
+        workspace = torch.empty(n, dtype=torch.uint8, device=dq_out.device)
     _one_device(dev, (dk_out, q if qs else None, k if ks else None, cos, sin, positions, q_weight, k_weight, dq, dk, dq_weight, dk_weight,
                       workspace))
     rc = (_lib or lib()).fa_qk_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), gqs, gks, _at(q) if qs else None, _at(k) if ks else None, qs, ks,
