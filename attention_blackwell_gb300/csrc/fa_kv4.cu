@@ -925,10 +925,14 @@ template <int D> __device__ __forceinline__ uint32_t mid_scales(const uint32_t (
 #pragma unroll
     for (int i = 1; i < D / 64; ++i) m = hmax2(m, h[i]);
     m = hmax2(m, __byte_perm(m, m, 0x1032));
-    const uint32_t ex = hmin2(hmax2(m, 0x04000400u), 0x78007800u) & 0x7c007c00u, down = 0x7c007c00u - ex;
+    const uint32_t ex = hmin2(hmax2(m, 0x04000400u), 0x78007800u) & 0x7c007c00u;
+    // 2^(26 - field) in one step where it is below 2^16, else after 2^(16 - field): exact
+    // (the products are multiples of 2^-21).
+    const bool one = ex >= 0x2c002c00u;
+    const uint32_t f = (one ? 0xa400a400u : 0x7c007c00u) - ex, f2 = one ? 0x3c003c00u : 0x64006400u;
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        const uint32_t x = hmul2(hmul2(h[i], down), 0x64006400u);        // 2^10
+        const uint32_t x = hmul2(hmul2(h[i], f), f2);
         sc[2 * i] = __byte_perm(x, x, 0x1010);
         sc[2 * i + 1] = __byte_perm(x, x, 0x3232);
     }

@@ -293,6 +293,22 @@ def test_more_rows_of_many_requests(fa, d):
     c.check(fa, o2, lse2)
 
 
+@pytest.mark.parametrize("d,hq", [(64, 20), (128, 32), (256, 12), (256, 32)])
+def test_more_rows_of_values_with_one_large_group(fa, d, hq):
+    """A value's first 32 elements have 2^31 times the scale of the others: with more
+    rows a code times its scale is exact, so the others are as near as if alone."""
+    b = Batch(hq, 1, d, 32, [300, 700], [1, 2], seed=d + hq)
+    b.vs[..., 0], b.vs[..., 1:] = 0xF0, 5
+    o, lse = b.run(fa)
+    b.check(fa, o, lse)
+    want, _, mass, reach, _ = b.want()
+    e = (2.0 ** -23 * (d + 8) * reach + 2.0 ** -21 * (1 + reach))[..., None]
+    # weights: 2^-11 each, and 2^-25 against a largest of 2^5
+    tol = (2.0 ** -10 + 2 * e) * mass + U * np.abs(want) + 2.0 ** -28 * 700 * 6 * float(R.scales(np.uint8(5)))
+    off = np.abs(o.double().cpu().numpy() - want)
+    assert (off[..., 32:] <= tol[..., 32:]).all(), (off / tol)[..., 32:].max()
+
+
 def test_many_requests(fa):
     g = np.random.default_rng(4)
     for hi in (90, 700):
