@@ -869,7 +869,9 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // rows 353, 32 rows of 128 243, of 64 219; with m16n8k16 and one, two or four warps an item
 // 362 (16 of 256), 352 and 236; 16 rows of 128 this way 226, and 184 by single warps.
 // Without gain: row numbers loaded before the wait for the scores (registers), a flag and
-// weights worked out before it is looked at instead of a barrier a tile (89 us 94).
+// weights worked out before it is looked at instead of a barrier a tile (89 us 94),
+// sixteen warps for the softmax and half as many that expand (32 rows of 128 250, of 64
+// 210).
 template <int D, int N> struct Mid {
     // An item's start and end take as long as 12 units (100 requests of up to 16384 keys, 32 rows of 256: with 3, 6,
     // 8, 12 and 16 100, 96, 94, 91 and 91 us).
