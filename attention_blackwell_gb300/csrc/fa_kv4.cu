@@ -9,12 +9,14 @@
 // multiply the sums of its groups' products, a value's scales its weight.
 //
 // fp16 weights.  A weight times a scale spans more than fp16 does, so weights are
-// kept relative to what matters for O: with 2^e_j the power of two over key j's
-// largest value scale,
+// kept relative to what matters for O: with key j's largest value scale in [2, 4) 2^e_j
+// (below 2^-14 e_j = -15 and it is less, but 2^(e_j - 2) at least; where all its scales
+// are 0, as those of a sink's value may be, e_j = -64),
 //   M = max (x_j + e_j),  p_j = 2^(x_j + e_j - M + 5) in [0, 2^13],  t_jg 2^-e_j in [0, 4),
-// so the largest is at least 2^6, and what falls under fp16's 2^-24 is 2^30 times
-// smaller than the largest term of O, whatever the scales.  sum_j w_j = sum_j p_j 2^-e_j
-// stays in 32 bits.  A query is scaled by a power of two into [2^14, 2^15) at its largest
+// so the largest is at least 2^6 (2^3 below 2^-14), and what falls under fp16's 2^-24 is
+// 2^30 (2^27) times smaller than the largest term of O.  A key without a value holds M
+// up only where it has 2^64 times another's weight.  sum_j w_j = sum_j p_j 2^-e_j stays
+// in 32 bits (2^13 2^64 2^29 keys at most).  A query is scaled by a power of two into [2^14, 2^15) at its largest
 // element before it becomes fp16, which all of bf16's 8 bits fit down to 2^-31 of it.
 // (p is rounded to 11 bits, p t again: less than the 8 bits of a bf16 weight.)
 //
@@ -69,6 +71,11 @@ constexpr float kLift = 5.0f;           // a weight at the maximum is 2^5: 2^(kT
 constexpr int kQLift = 14;              // a query's largest element becomes 2^14 or more
 constexpr float kNone = -3.4028234663852886e38f;   // a maximum below every finite score; a hidden key's -inf less it is -inf
 constexpr int kUnit = 64;               // keys a unit
+// A key's e for its value's scales, kept as e + 80: 16 (e = -64) where all are 0, else
+// the largest's exponent field as an fp16 (1 to 30; e = field - 16) and 64.
+constexpr uint32_t kNoValue = 16, kValue = 64;
+__device__ __forceinline__ float value_e(uint32_t x) { return __uint_as_float(0x4b000000u | x) - 8388688.f; }
+__device__ __forceinline__ float value_back(uint32_t x) { return __uint_as_float((207u - x) << 23); }    // 2^-e
 constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kExtraMost = 12;          // units that an item costs besides its keys', at most
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
@@ -435,8 +442,8 @@ __device__ __forceinline__ void prepare_key(const uint8_t* ks, const uint8_t* vs
     const uint32_t ex = hmin2(hmax2(m, 0x04000400u), 0x78007800u) & 0x7c007c00u, down = 0x7c007c00u - ex;    // 2^(16 - field) = 2^-e
 #pragma unroll
     for (int i = 0; i < kG / 2; ++i) h[i] = hmul2(h[i], down);
-    const uint32_t field = ex >> 26;
-    const uint32_t eb[2] = {__float_as_uint(__uint_as_float(0x4b000000u | field) - 8388624.f), (143u - field) << 23};
+    const uint32_t at = m ? (ex >> 26) + kValue : kNoValue;
+    const uint32_t eb[2] = {__float_as_uint(value_e(at)), __float_as_uint(value_back(at))};
     sts(prep + K::kExp + key * 8, eb);
     // Pairs of keys, in the order of the products' key axis (1 0 in the second and
     // third pair of eight): the even key's lane takes the first half of the groups.
@@ -921,7 +928,7 @@ template <int D, int N> __device__ __forceinline__ void mid_values(uint32_t o, u
 }
 
 // A key's scales (f16 pairs) times 2^(26 - field), each twice; returns the exponent
-// field of the largest (1 to 30).
+// field of the largest (1 to 30), or 0 where all are 0.
 template <int D> __device__ __forceinline__ uint32_t mid_scales(const uint32_t (&h)[D / 64], uint32_t (&sc)[D / 32]) {
     uint32_t m = h[0];
 #pragma unroll
@@ -938,7 +945,7 @@ template <int D> __device__ __forceinline__ uint32_t mid_scales(const uint32_t (
         sc[2 * i] = __byte_perm(x, x, 0x1010);
         sc[2 * i + 1] = __byte_perm(x, x, 0x3232);
     }
-    return ex >> 26;
+    return m ? ex >> 26 : 0;
 }
 // Half of a key's codes into its row of a tile.  Lanes are keys; which 16 bytes each
 // takes first depends on its key, so that neither loads nor stores meet in a bank.
@@ -1098,7 +1105,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem, smem = smem_u32(dsmem);
-    // Exponent fields of K's and V's largest scales, the tile's parts that are there.
+    // Exponent field of K's largest scale, V's e, the tile's parts that are there.
     uint32_t* const keys = reinterpret_cast<uint32_t*>(dsmem + K::kKeys);
     Walk walk;
     walk.start(a, t, hdr, blockIdx.x);
@@ -1176,10 +1183,9 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 tc_fence_after();
                 uint32_t r[kC];
                 tmem_ld<kC>(lanes + (tile & 1) * N, r);
-                // K's scale is 2^(field - 26) times what it was expanded with, V's e is field - 16.
+                // K's scale is 2^(field - 26) times what it was expanded with.
                 const uint32_t info = keys[(tile & 3) * 128 + key], here = info >> 16;
-                const float ek = __uint_as_float((101u + (info & 255u)) << 23), ev = __uint_as_float(0x4b000000u | (info >> 8 & 255u)) - 8388624.f,
-                            back = __uint_as_float((143u - (info >> 8 & 255u)) << 23);
+                const float ek = __uint_as_float((101u + (info & 255u)) << 23), ev = value_e(info >> 8 & 255u), back = value_back(info >> 8 & 255u);
                 float z[kC], most = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < kC; i += 2)
@@ -1337,7 +1343,7 @@ __global__ void __launch_bounds__(896, 1) kv4_mid_kernel(const KvArgs a) {
                 // The tile before the last is done with its rows.
                 if (tile >= 2 && !(ok = wait2(sh.s_full, tile - 2))) break;
                 tc_fence_after();
-                if (!half) keys[(tile & 3) * 128 + key] = fk | fv << 8 | here << 16;
+                if (!half) keys[(tile & 3) * 128 + key] = fk | (fv ? fv + kValue : kNoValue) << 8 | here << 16;
                 mid_expand_lane<D>(raw, tmem + ((uint32_t)(warp & 3) << 21) + K::kColK + (tile & 1) * (D / 2), key, half, sc);
                 tc_fence_before();
                 __syncwarp();

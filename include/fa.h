@@ -567,9 +567,10 @@ int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages
  * without a prefix (rows, tables, lengths, causal limit, absent pages, rows that
  * see no key and rows outside every request as there), keys and values read from
  * 4-bit pages.  Scores, sums and the output's accumulator are 32 bits wide, the
- * weights fp16 relative to the largest weight times value scale (one below 2^-30 of
- * it counts for nothing in O), the queries fp16 relative to a row's largest element
- * (exact down to 2^-31 of it).
+ * weights fp16 relative to the largest weight times value scale (a key's largest; one
+ * below 2^-30 of it counts for nothing in O, below 2^-27 where that scale is under
+ * 2^-14; a key whose value scales are all 0 counts there as one of 2^-62), the queries
+ * fp16 relative to a row's largest element (exact down to 2^-31 of it).
  * Up to d rows of a request and key/value head (max_seqlen * Hq / Hkv) are computed
  * from the codes; above that, and while 4 * B * table_width * page_size
  * * Hkv * d is up to 2^32, the call expands the requests' pages into the
