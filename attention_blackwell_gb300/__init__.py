@@ -548,8 +548,8 @@ def _tokens(t, name):
     return T, H, d, between if T > 1 else H * d
 
 
-def _rope_tables(cos, sin, positions, T, d, q_weight, k_weight):
-    """Checks; returns (max_pos, rot, 1 for bf16 weights)."""
+def _rope_tables(cos, sin, positions, T, N, d, q_weight, k_weight):
+    """Checks, for T tokens in sequences of N; returns (max_pos, rot, 1 for bf16 weights)."""
     f32 = torch.float32
     if cos.dtype is not f32 or sin.dtype is not f32 or not cos.is_contiguous() or not sin.is_contiguous():
         _need(cos, "cos", f32)
@@ -557,7 +557,10 @@ def _rope_tables(cos, sin, positions, T, d, q_weight, k_weight):
     shape = cos.shape
     if len(shape) != 2 or shape != sin.shape:
         raise ValueError("cos and sin must be [max_pos, rot / 2]")
-    if positions is not None:
+    if positions is None:
+        if T and N > shape[0]:
+            raise ValueError("cos and sin must have a row for every token of a sequence")
+    else:
         if positions.dtype is not torch.int32 or not positions.is_contiguous():
             _need(positions, "positions", torch.int32)
         if positions.numel() != T:
@@ -584,8 +587,8 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
 
     q [.., Hq, d], k [.., Hkv, d] bf16 with leading [B, N] or [T] (tokens may be
     strided), cos / sin float32 [max_pos, rot / 2], positions int32, one a token
-    (None: a token's index in its sequence, or in [T]; outside the tables: the
-    token is left alone), weights [d] float32 or bf16.  Pairs are (i, i + rot / 2),
+    (None: a token's index in its sequence, or in [T], which the tables must have;
+    a position outside the tables: the token is left alone), weights [d] float32 or bf16.  Pairs are (i, i + rot / 2),
     or (2 i, 2 i + 1) when interleaved.  The outputs may be q and k themselves.
     """
     dev = q.get_device()
@@ -596,7 +599,7 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
     Tk, Hkv, dk, ks = _tokens(k, "k")
     if T != Tk or d != dk or q.shape[:-2] != k.shape[:-2]:
         raise ValueError("q and k must have the same tokens and head dim")
-    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, q.shape[-3], d, q_weight, k_weight)
     if q_out is None:
         q_out, qo = torch.empty_like(q), Hq * d     # dense: q's tokens are
     else:
@@ -648,7 +651,7 @@ def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k
     Tk, Hkv, d2, gks = _tokens(dk_out, "dk_out")
     if dq_out.shape[:-2] != dk_out.shape[:-2] or d != d2:
         raise ValueError("dq_out and dk_out must have the same tokens and head dim")
-    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, dq_out.shape[-3], d, q_weight, k_weight)
     qs = ks = 0
     if q_weight is not None:
         if q is None or q.shape != dq_out.shape:
@@ -740,7 +743,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
         _need(slots, "slots", torch.int32)
     if positions is None or slots.numel() != T:
         raise ValueError("positions and slots must have one element a token")
-    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, d, q_weight, k_weight)
+    max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, T, d, q_weight, k_weight)
     Hq = qs = qo = 0
     if q is None:
         q_out = None

@@ -752,11 +752,12 @@ bool meet(const Rows& a, const Rows& b, long long T) { return rows_meet(a.p, a.b
 bool same(const Rows& a, const Rows& b, long long T) { return a.p == b.p && a.bytes == b.bytes && (a.stride == b.stride || T == 1); }
 bool meet(const Span& s, const Rows& a, long long T) { return a.bytes && T > 0 && overlap_rows(s, a.p, T, a.bytes, a.stride); }
 
-// What the rotation's own arguments have to be.
-int check_rope(const float* cos, const float* sin, int max_pos, int rot, int d, const int* positions, int seq_len, const void* wq,
+// What the rotation's own arguments have to be.  Without positions the tables have a row
+// for every index that the T tokens take.
+int check_rope(const float* cos, const float* sin, int max_pos, int rot, int d, int T, const int* positions, int seq_len, const void* wq,
                const void* wk, float eps) {
     if (!cos || !sin || max_pos < 1 || rot < 1 || rot > d) return FA_ERR_INVALID;
-    if (!positions && seq_len < 1) return FA_ERR_INVALID;
+    if (!positions && (seq_len < 1 || (seq_len < T ? seq_len : T) > max_pos)) return FA_ERR_INVALID;
     if ((wq || wk) && !(eps >= 0.f && isfinite(eps))) return FA_ERR_INVALID;
     if (rot % 16) return FA_ERR_UNSUPPORTED;
     if (misaligned(cos, 15) || misaligned(sin, 15) || misaligned(positions, 3) || misaligned(wq, 15) || misaligned(wk, 15)) return FA_ERR_ALIGN;
@@ -813,7 +814,7 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
     int rc = check_heads(T, Hq, Hkv, d);
     if (rc != FA_OK) return rc;
     if (T > 0 && ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)))) return FA_ERR_INVALID;
-    rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
+    rc = check_rope(cos, sin, max_pos, rot, d, T, positions, seq_len, q_weight, k_weight, eps);
     if (rc != FA_OK) return rc;
     const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
     if (Hq == 0) q = q_out = nullptr, q_stride = q_out_stride = 0;
@@ -866,7 +867,7 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     if (rc != FA_OK) return rc;
     if (T > 0 && ((Hq > 0 && (!dq_out || !dq || (q_weight && !q))) || (Hkv > 0 && (!dk_out || !dk || (k_weight && !k))))) return FA_ERR_INVALID;
     if ((q_weight != nullptr) != (dq_weight != nullptr) || (k_weight != nullptr) != (dk_weight != nullptr)) return FA_ERR_INVALID;
-    rc = check_rope(cos, sin, max_pos, rot, d, positions, seq_len, q_weight, k_weight, eps);
+    rc = check_rope(cos, sin, max_pos, rot, d, T, positions, seq_len, q_weight, k_weight, eps);
     if (rc != FA_OK) return rc;
     const long long nq = (long long)Hq * d, nk = (long long)Hkv * d;
     if (Hq == 0) dq_out = q = dq = nullptr, dq_out_stride = q_stride = 0;
@@ -934,7 +935,7 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
     if (rc != FA_OK) return rc;
     if (!k || !v || !slots || !positions || !k_pages || !v_pages || Hkv < 1 || num_pages < 1) return FA_ERR_INVALID;
     if ((Hq > 0 && (!q || !q_out)) || (k_scales != nullptr) != (v_scales != nullptr)) return FA_ERR_INVALID;
-    rc = check_rope(cos, sin, max_pos, rot, d, positions, 1, q_weight, k_weight, eps);
+    rc = check_rope(cos, sin, max_pos, rot, d, T, positions, 1, q_weight, k_weight, eps);
     if (rc != FA_OK) return rc;
     const int lg = page_log2(page_size);
     if (lg < 0 || (long long)num_pages * page_size > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;

@@ -459,8 +459,9 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  * - cos, sin: float32 [max_pos, rot / 2], 16-byte aligned.  rot is a multiple of
  *   16 up to d.
  * - positions: device int32 [T]; NULL (not in fa_rope_store): token t is at t %
- *   seq_len.  A token whose position is not in [0, max_pos) is left alone:
- *   nothing of its rows is written, and it adds nothing to a weight's gradient.
+ *   seq_len, for which the tables must have a row (min(seq_len, T) <= max_pos).  A
+ *   token whose own position is not in [0, max_pos) is left alone: nothing of its
+ *   rows is written, and it adds nothing to a weight's gradient.
  * - Weights: [d], float32 or (weights_bf16 = 1) bf16, each may be NULL.
  * - *_stride: elements between tokens (at least heads * d, a multiple of 8), so
  *   operands may be cut from one projection's output.  Tensors are 16-byte
@@ -475,7 +476,7 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  * q [T, Hq, d], k [T, Hkv, d] -> q_out, k_out, normed and rotated.  One launch, no
  * workspace.  T == 0 is a no-op.
  * Errors: FA_ERR_INVALID (null pointer, T or heads < 0, no heads, max_pos, rot
- * or (without positions) seq_len < 1, rot > d, a stride below heads * d, eps
+ * or (without positions) seq_len < 1, tables too short for it, rot > d, a stride below heads * d, eps
  * negative or not finite, arrays that overlap), FA_ERR_UNSUPPORTED (d not 64,
  * 128 or 256, rot not a multiple of 16, heads * d above 2^30 - 1, T times the
  * kilobytes of a token's rows of q and of k twice, each rounded up, above 2^30 - 1),
