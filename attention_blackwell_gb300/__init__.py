@@ -576,6 +576,9 @@ def _rope_tables(cos, sin, positions, T, N, d, q_weight, k_weight):
     return shape[0], 2 * shape[1], 0 if kind is f32 else 1
 
 
+_CLEAR_Q, _CLEAR_K = 256, 512      # FA_ROPE_CLEAR_Q, FA_ROPE_CLEAR_K: for outputs that a call allocates
+
+
 def _at(t):
     return t.data_ptr() if t is not None else None
 
@@ -588,7 +591,8 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
     q [.., Hq, d], k [.., Hkv, d] bf16 with leading [B, N] or [T] (tokens may be
     strided), cos / sin float32 [max_pos, rot / 2], positions int32, one a token
     (None: a token's index in its sequence, or in [T], which the tables must have;
-    a position outside the tables: the token is left alone), weights [d] float32 or bf16.  Pairs are (i, i + rot / 2),
+    a position outside the tables: the token is left alone, in an output that the call
+    allocates its rows are 0), weights [d] float32 or bf16.  Pairs are (i, i + rot / 2),
     or (2 i, 2 i + 1) when interleaved.  The outputs may be q and k themselves.
     """
     dev = q.get_device()
@@ -600,14 +604,17 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
     if T != Tk or d != dk or q.shape[:-2] != k.shape[:-2]:
         raise ValueError("q and k must have the same tokens and head dim")
     max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, q.shape[-3], d, q_weight, k_weight)
+    flags = 1 if interleaved else 0
     if q_out is None:
         q_out, qo = torch.empty_like(q), Hq * d     # dense: q's tokens are
+        flags |= _CLEAR_Q
     else:
         qo = _tokens(q_out, "q_out")[3]
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
     if k_out is None:
         k_out, ko = torch.empty_like(k), Hkv * d
+        flags |= _CLEAR_K
     else:
         ko = _tokens(k_out, "k_out")[3]
         if k_out.shape != k.shape:
@@ -616,7 +623,7 @@ def qk_rope(q, k, cos, sin, positions=None, q_weight=None, k_weight=None, eps=1e
     if T == 0:
         return q_out, k_out
     rc = (_lib or lib()).fa_qk_rope(q.data_ptr(), k.data_ptr(), qs, ks, q_out.data_ptr(), k_out.data_ptr(), qo, ko, T, Hq, Hkv, d,
-                                    cos.data_ptr(), sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, _at(positions),
+                                    cos.data_ptr(), sin.data_ptr(), max_pos, rot, flags, _at(positions),
                                     q.shape[-3], _at(q_weight), _at(k_weight), bf16, eps, _current_raw_stream(dev))
     if rc:
         _check(rc, "fa_qk_rope")
@@ -640,7 +647,8 @@ def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k
 
     dq_out, dk_out: gradients of qk_rope's outputs; q, k and the rest as it took
     them (q and k may be None without their weight).  dq and dk are contiguous and
-    may be dq_out and dk_out themselves.
+    may be dq_out and dk_out themselves; a token outside the tables is left alone
+    there, in one that the call allocates its rows are 0.
     """
     dev = dq_out.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
@@ -661,10 +669,13 @@ def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k
         if k is None or k.shape != dk_out.shape:
             raise ValueError("k must have dk_out's shape")
         ks = _tokens(k, "k")[3]
+    flags = 1 if interleaved else 0
     if dq is None:
         dq = torch.empty(dq_out.shape, dtype=torch.bfloat16, device=dq_out.device)
+        flags |= _CLEAR_Q
     if dk is None:
         dk = torch.empty(dk_out.shape, dtype=torch.bfloat16, device=dq_out.device)
+        flags |= _CLEAR_K
     _need(dq, "dq", torch.bfloat16)
     _need(dk, "dk", torch.bfloat16)
     if dq.shape != dq_out.shape or dk.shape != dk_out.shape:
@@ -689,7 +700,7 @@ def qk_rope_bwd(dq_out, dk_out, q, k, cos, sin, positions=None, q_weight=None, k
                       workspace))
     rc = (_lib or lib()).fa_qk_rope_bwd(dq_out.data_ptr(), dk_out.data_ptr(), gqs, gks, _at(q) if qs else None, _at(k) if ks else None, qs, ks,
                                         dq.data_ptr(), dk.data_ptr(), _at(dq_weight), _at(dk_weight), T, Hq, Hkv, d, cos.data_ptr(),
-                                        sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, _at(positions), max(dq_out.shape[-3], 1),
+                                        sin.data_ptr(), max_pos, rot, flags, _at(positions), max(dq_out.shape[-3], 1),
                                         _at(q_weight), _at(k_weight), bf16, eps, _at(workspace),
                                         workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                         _current_raw_stream(dev))
@@ -721,7 +732,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
 
     q [T, Hq, d] (or None), k, v [T, Hkv, d] bf16 (tokens may be strided),
     positions and slots int32 [T] (a position outside the tables: the token is left
-    alone; a slot outside the cache: its key and value are not stored).  Pages are
+    alone, in a q_out that the call allocates its rows are 0; a slot outside the cache: its key and value are not stored).  Pages are
     bf16 [num_pages, Hkv, page_size, d], or with scales uint8 [.., d / 2] and
     [.., d / 32] in 4 bits; cos, sin, weights and pairs as in qk_rope.  q_out may
     be q itself.
@@ -745,6 +756,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
         raise ValueError("positions and slots must have one element a token")
     max_pos, rot, bf16 = _rope_tables(cos, sin, positions, T, T, d, q_weight, k_weight)
     Hq = qs = qo = 0
+    flags = 1 if interleaved else 0
     if q is None:
         q_out = None
     else:
@@ -754,6 +766,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
             raise ValueError("q must be [T, Hq, d] with k's T and d")
         if q_out is None:
             q_out, qo = torch.empty_like(q), Hq * d
+            flags |= _CLEAR_Q
         else:
             qo = _rows(q_out, "q_out")
             if q_out.shape != q.shape:
@@ -762,7 +775,7 @@ def rope_store(q, k, v, cos, sin, positions, slots, k_pages, v_pages, k_scales=N
     if T == 0:
         return q_out
     rc = (_lib or lib()).fa_rope_store(_at(q), k.data_ptr(), v.data_ptr(), qs, ks, vs, _at(q_out), qo, T, Hq, Hkv, d, cos.data_ptr(),
-                                       sin.data_ptr(), max_pos, rot, 1 if interleaved else 0, positions.data_ptr(), _at(q_weight),
+                                       sin.data_ptr(), max_pos, rot, flags, positions.data_ptr(), _at(q_weight),
                                        _at(k_weight), bf16, eps, slots.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                        _at(k_scales), _at(v_scales), P, page, _current_raw_stream(dev))
     if rc:

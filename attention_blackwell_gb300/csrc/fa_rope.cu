@@ -46,6 +46,7 @@ struct RopeArgs {
     float eps;
     int chunk, per_q, per_k, per;    // rows a unit; units of a token's q rows, of its k (and v) rows, of all
     int units;
+    int clear;                   // bits 0 and 1: q's, k's outputs of tokens off the tables become 0
     DevStatus* status;
 };
 
@@ -212,9 +213,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 // Calls work(unit, rows, tables) for this warp's units.  rows(t, j, array, bytes) is
-// where a unit's rows are and how many bytes of them.
-template <int D, int kBytes, int kArrays, int kRing, int kWarps, class Rows, class Work>
-__device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t* full, const int* slots, const Rows& rows, const Work& work) {
+// where a unit's rows are and how many bytes of them; off(t, j) is called for those of
+// tokens off the tables, which are passed over, where something becomes of them.
+template <int D, int kBytes, int kArrays, int kRing, int kWarps, class Rows, class Off, class Work>
+__device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t* full, const int* slots, const Rows& rows, const Off& off, const Work& work) {
     using F = Feed<D, kBytes, kArrays, kRing>;
     const int lane = threadIdx.x & 31;
     // A range of the units, so that every warp gets q, k and v in the same proportion.
@@ -237,7 +239,7 @@ __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t*
     uint32_t filled = 0, issued = 0;
     auto copy = [&]() {
         Unit u;
-        do {                                         // tokens off the tables are passed over
+        for (;;) {
             if (k >= n) return;
             if (k && (k & 31) == 0) {
                 now = next;
@@ -249,7 +251,9 @@ __device__ __forceinline__ void feed(const RopeArgs& r, uint8_t* ring, uint64_t*
             u.j = __shfl_sync(0xffffffffu, now.j, i);
             u.slot = __shfl_sync(0xffffffffu, now.slot, i);
             ++k;
-        } while (u.pos < 0);
+            if (u.pos >= 0) break;
+            if (r.clear) off(u.t, u.j);
+        }
         uint8_t* to = ring + filled * F::kSlot;
         uint64_t* bar = &full[filled];
         uint32_t bytes = r.rot * 2, total = 2 * bytes;
@@ -308,6 +312,13 @@ __device__ __forceinline__ Chunk chunk_of(const RopeArgs& r, int j) {
     c.h0 = (c.what == 0 ? j : c.what == 1 ? j - r.per_q : j - r.per_q - r.per_k) * r.chunk;
     c.n = min(r.chunk, (c.what == 0 ? r.Hq : r.Hkv) - c.h0);
     return c;
+}
+
+// A unit's rows of an output as 0, if it is one that the call clears.
+template <int D> __device__ __forceinline__ void clear_rows(const RopeArgs& r, const Chunk& c, __nv_bfloat16* token) {
+    if (!(r.clear >> (c.what != 0) & 1)) return;
+    uint4* to = reinterpret_cast<uint4*>(token + c.h0 * D);
+    for (int i = threadIdx.x & 31; i < c.n * (D / 8); i += 32) to[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Bytes of rows a unit at most, of each array: four passes of 32 lanes.  What a unit
@@ -378,10 +389,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) qk_rope_kernel(const RopeArgs 
         bytes = c.n * D * 2;
         return reinterpret_cast<const uint8_t*>((c.what ? a.k + t * a.k_stride : a.q + t * a.q_stride) + c.h0 * D);
     };
-    feed<D, kBytes, 1, kRing, kWarps>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], nullptr, rows,
+    auto out = [&](int t, const Chunk& c) { return c.what ? a.k_out + t * a.k_out_stride : a.q_out + t * a.q_out_stride; };
+    auto off = [&](int t, int j) {
+        const Chunk c = chunk_of(r, j);
+        clear_rows<D>(r, c, out(t, c));
+    };
+    feed<D, kBytes, 1, kRing, kWarps>(r, dsmem + warp * Feed<D, kBytes, 1, kRing>::kWarp, full[warp], nullptr, rows, off,
                               [&](const Unit& u, const uint8_t* in, const float* table) {
         const Chunk c = chunk_of(r, u.j);
-        __nv_bfloat16* to = c.what ? a.k_out + u.t * a.k_out_stride : a.q_out + u.t * a.q_out_stride;
+        __nv_bfloat16* to = out(u.t, c);
         turn_rows<D, false>(r, me, c, in, table, s_w, [&](int h) { return to + h * D; });
     });
 }
@@ -449,11 +465,16 @@ __global__ void __launch_bounds__(32 * kWarpsGrad, 1) qk_rope_bwd_kernel(const R
         const __nv_bfloat16* p = c.what ? (array ? a.k + t * a.k_stride : a.gk + t * a.gk_stride) : array ? a.q + t * a.q_stride : a.gq + t * a.gq_stride;
         return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
     };
-    feed<D, kBytesGrad, 2, kRingGrad, kWarpsGrad>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRingGrad>::kWarp, full[warp], nullptr, rows,
+    auto token = [&](int t, const Chunk& c) { return c.what ? a.dk + (long long)t * r.Hkv * D : a.dq + (long long)t * r.Hq * D; };
+    auto off = [&](int t, int j) {
+        const Chunk c = chunk_of(r, j);
+        clear_rows<D>(r, c, token(t, c));
+    };
+    feed<D, kBytesGrad, 2, kRingGrad, kWarpsGrad>(r, dsmem + warp * Feed<D, kBytesGrad, 2, kRingGrad>::kWarp, full[warp], nullptr, rows, off,
                                   [&](const Unit& u, const uint8_t* in, const float* table) {
         const Chunk c = chunk_of(r, u.j);
         me.template angles<false>(r, table, lane, -1.f);
-        __nv_bfloat16* out = c.what ? a.dk + ((long long)u.t * r.Hkv + c.h0) * D : a.dq + ((long long)u.t * r.Hq + c.h0) * D;
+        __nv_bfloat16* out = token(u.t, c) + c.h0 * D;
         const uint8_t* g = in + sub * D * 2;
         auto passes = [&](const float* w, F2 (&dw)[8]) {
             for (int p = 0; p < c.n; p += Me::kRows)
@@ -703,7 +724,11 @@ __global__ void __launch_bounds__(32 * kWarpsPut, 1) rope_store_kernel(const Rop
         const __nv_bfloat16* p = c.what == 0 ? a.q + t * a.q_stride : c.what == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
         return reinterpret_cast<const uint8_t*>(p + c.h0 * D);
     };
-    feed<D, kBytes, 1, kRingPut, kWarpsPut>(r, dsmem + warp * Feed<D, kBytes, 1, kRingPut>::kWarp, full[warp], a.slots, rows,
+    auto off = [&](int t, int j) {
+        const Chunk c = chunk_of(r, j);
+        if (c.what == 0) clear_rows<D>(r, c, a.q_out + t * a.q_out_stride);
+    };
+    feed<D, kBytes, 1, kRingPut, kWarpsPut>(r, dsmem + warp * Feed<D, kBytes, 1, kRingPut>::kWarp, full[warp], a.slots, rows, off,
                               [&](const Unit& u, const uint8_t* in, const float* table) {
         const Chunk c = chunk_of(r, u.j);
         if (c.what == 0) {
@@ -778,7 +803,7 @@ int grid_for(int units, int sms, int warps) { return units < warps * sms ? (unit
 // The rotation's arguments, with `arrays` of Hkv rows.  Rows a unit: as many as fill
 // a slot, but no more than leave every warp a unit (whole passes).
 RopeArgs rope_args(const float* cos, const float* sin, const int* positions, const void* wq, const void* wk, int T, int Hq, int Hkv, int max_pos, int rot,
-                   int inter, int seq_len, int w_bf16, float eps, int pass, int most, int arrays, int workers, DevStatus* status) {
+                   int flags, int seq_len, int w_bf16, float eps, int pass, int most, int arrays, int workers, DevStatus* status) {
     int chunk = most, per_q, per_k;
     for (;; chunk /= 2) {
         per_q = (Hq + chunk - 1) / chunk;
@@ -786,7 +811,8 @@ RopeArgs rope_args(const float* cos, const float* sin, const int* positions, con
         if (chunk == pass || (long long)T * (per_q + arrays * per_k) >= workers) break;
     }
     const int per = per_q + arrays * per_k;
-    return {cos, sin, positions, wq, wk, T, Hq, Hkv, max_pos, rot, inter != 0, seq_len, w_bf16 != 0, eps, chunk, per_q, per_k, per, T * per, status};
+    return {cos, sin, positions, wq, wk, T, Hq, Hkv, max_pos, rot, (flags & 0xff) != 0, seq_len, w_bf16 != 0, eps, chunk, per_q, per_k, per, T * per,
+            (flags & FA_ROPE_CLEAR_Q ? 1 : 0) | (flags & FA_ROPE_CLEAR_K ? 2 : 0), status};
 }
 // Launches with `smem` bytes of dynamic shared memory, which a kernel is allowed once a device.
 template <typename A>
@@ -809,7 +835,7 @@ extern "C" {
 
 int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, void* q_out, void* k_out, int64_t q_out_stride,
                int64_t k_out_stride, int T, int Hq, int Hkv, int d, const float* cos, const float* sin, int max_pos, int rot,
-               int interleaved, const int* positions, int seq_len, const void* q_weight, const void* k_weight, int weights_bf16,
+               int flags, const int* positions, int seq_len, const void* q_weight, const void* k_weight, int weights_bf16,
                float eps, cudaStream_t stream) {
     int rc = check_heads(T, Hq, Hkv, d);
     if (rc != FA_OK) return rc;
@@ -844,7 +870,7 @@ int fa_qk_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride,
     auto launch = [&](auto dim) {
         constexpr int D = decltype(dim)::value;
         static std::atomic<uint64_t> prepared{0};
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kPass<D>, kChunk<D>, 1, kWarps * sms, status);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, flags, seq_len, weights_bf16, eps, kPass<D>, kChunk<D>, 1, kWarps * sms, status);
         return launch_rope(qk_rope_kernel<D>, prepared, grid_for(r.units, sms, kWarps), 32 * kWarps, kSmem<D>, stream, r, a);
     };
     if (d == 64) return launch(std::integral_constant<int, 64>{});
@@ -860,7 +886,7 @@ size_t fa_qk_rope_bwd_workspace_size(int d) {
 
 int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride, int64_t dk_out_stride, const void* q, const void* k,
                    int64_t q_stride, int64_t k_stride, void* dq, void* dk, float* dq_weight, float* dk_weight, int T, int Hq, int Hkv,
-                   int d, const float* cos, const float* sin, int max_pos, int rot, int interleaved, const int* positions, int seq_len,
+                   int d, const float* cos, const float* sin, int max_pos, int rot, int flags, const int* positions, int seq_len,
                    const void* q_weight, const void* k_weight, int weights_bf16, float eps, void* workspace, size_t workspace_bytes,
                    cudaStream_t stream) {
     int rc = check_heads(T, Hq, Hkv, d);
@@ -917,7 +943,7 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
     auto launch = [&](auto dim) -> int {
         constexpr int D = decltype(dim)::value;
         static std::atomic<uint64_t> prepared{0};
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, seq_len, weights_bf16, eps, kPass<D>, kChunkGrad<D>, 1, kWarpsGrad * sms, status);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, flags, seq_len, weights_bf16, eps, kPass<D>, kChunkGrad<D>, 1, kWarpsGrad * sms, status);
         grid = grid_for(r.units, sms, kWarpsGrad);
         return grid < 1 ? FA_OK : launch_rope(qk_rope_bwd_kernel<D>, prepared, grid, 32 * kWarpsGrad, kSmemGrad<D>, stream, r, a);
     };
@@ -928,7 +954,7 @@ int fa_qk_rope_bwd(const void* dq_out, const void* dk_out, int64_t dq_out_stride
 
 int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride, void* q_out,
                   int64_t q_out_stride, int T, int Hq, int Hkv, int d, const float* cos, const float* sin, int max_pos, int rot,
-                  int interleaved, const int* positions, const void* q_weight, const void* k_weight, int weights_bf16, float eps,
+                  int flags, const int* positions, const void* q_weight, const void* k_weight, int weights_bf16, float eps,
                   const int* slots, void* k_pages, void* v_pages, void* k_scales, void* v_scales, int num_pages, int page_size,
                   cudaStream_t stream) {
     int rc = check_heads(T, Hq, Hkv, d);
@@ -978,8 +1004,8 @@ int fa_rope_store(const void* q, const void* k, const void* v, int64_t q_stride,
         constexpr int D = decltype(dim)::value;
         constexpr bool kFour = decltype(bits4)::value;
         static std::atomic<uint64_t> prepared[2];
-        const bool whole = rot == D && !interleaved;
-        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, interleaved, 1, weights_bf16, eps, kPass<D>, kChunk<D>, 2, kWarpsPut * sms, status);
+        const bool whole = rot == D && !(flags & 0xff);
+        const RopeArgs r = rope_args(cos, sin, positions, q_weight, k_weight, T, Hq, Hkv, max_pos, rot, flags, 1, weights_bf16, eps, kPass<D>, kChunk<D>, 2, kWarpsPut * sms, status);
         return launch_rope(whole ? rope_store_kernel<D, kFour, true> : rope_store_kernel<D, kFour, false>, prepared[whole], grid_for(r.units, sms, kWarpsPut), 32 * kWarpsPut, kSmemPut<D>, stream, r, a);
     };
     auto pick = [&](auto bits4) {

@@ -452,7 +452,7 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  *   n(x) = x r w,  r = (mean x^2 + eps)^(-1/2)  over a head's d elements (no
  *          weights: n(x) = x),
  *   y = R n(x):  pairs (i, i + rot / 2) of the first rot elements, or (2 i, 2 i +
- *          1) when interleaved = 1, become (a c - b s, b c + a s) with c, s = cos,
+ *          1) with FA_ROPE_INTERLEAVED, become (a c - b s, b c + a s) with c, s = cos,
  *          sin [position][i]; elements from rot on stay.
  *
  * - All sums and products are 32 bits wide; a result is rounded to bf16 once.
@@ -462,6 +462,8 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  *   seq_len, for which the tables must have a row (min(seq_len, T) <= max_pos).  A
  *   token whose own position is not in [0, max_pos) is left alone: nothing of its
  *   rows is written, and it adds nothing to a weight's gradient.
+ * - flags: 0, or FA_ROPE_INTERLEAVED, and with FA_ROPE_CLEAR_Q (_K) added the rows of
+ *   q_out or dq (k_out or dk) of a token off the tables become 0.
  * - Weights: [d], float32 or (weights_bf16 = 1) bf16, each may be NULL.
  * - *_stride: elements between tokens (at least heads * d, a multiple of 8), so
  *   operands may be cut from one projection's output.  Tensors are 16-byte
@@ -471,6 +473,10 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  * - Heads of one of the two may be 0: its pointers and strides are then not looked
  *   at.
  */
+
+#define FA_ROPE_INTERLEAVED 1
+#define FA_ROPE_CLEAR_Q 256
+#define FA_ROPE_CLEAR_K 512
 
 /*
  * q [T, Hq, d], k [T, Hkv, d] -> q_out, k_out, normed and rotated.  One launch, no
@@ -485,7 +491,7 @@ size_t fa_prefix_workspace_size(int T, int B, int Hq, int Hkv, int d, int max_se
  */
 int fa_qk_rope(const void *q, const void *k, int64_t q_stride, int64_t k_stride, void *q_out, void *k_out,
                int64_t q_out_stride, int64_t k_out_stride, int T, int Hq, int Hkv, int d, const float *cos,
-               const float *sin, int max_pos, int rot, int interleaved, const int *positions, int seq_len,
+               const float *sin, int max_pos, int rot, int flags, const int *positions, int seq_len,
                const void *q_weight, const void *k_weight, int weights_bf16, float eps, cudaStream_t stream);
 
 /*
@@ -507,7 +513,7 @@ int fa_qk_rope(const void *q, const void *k, int64_t q_stride, int64_t k_stride,
 int fa_qk_rope_bwd(const void *dq_out, const void *dk_out, int64_t dq_out_stride, int64_t dk_out_stride,
                    const void *q, const void *k, int64_t q_stride, int64_t k_stride, void *dq, void *dk,
                    float *dq_weight, float *dk_weight, int T, int Hq, int Hkv, int d, const float *cos,
-                   const float *sin, int max_pos, int rot, int interleaved, const int *positions, int seq_len,
+                   const float *sin, int max_pos, int rot, int flags, const int *positions, int seq_len,
                    const void *q_weight, const void *k_weight, int weights_bf16, float eps, void *workspace,
                    size_t workspace_bytes, cudaStream_t stream);
 
@@ -528,7 +534,7 @@ size_t fa_qk_rope_bwd_workspace_size(int d);
  */
 int fa_rope_store(const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                   void *q_out, int64_t q_out_stride, int T, int Hq, int Hkv, int d, const float *cos,
-                  const float *sin, int max_pos, int rot, int interleaved, const int *positions,
+                  const float *sin, int max_pos, int rot, int flags, const int *positions,
                   const void *q_weight, const void *k_weight, int weights_bf16, float eps, const int *slots,
                   void *k_pages, void *v_pages, void *k_scales, void *v_scales, int num_pages, int page_size,
                   cudaStream_t stream);
