@@ -71,3 +71,20 @@ def test_allocated_rows_of_tokens_off_the_tables_are_zero(fa, d, hq, hkv, norm):
         assert (q[gone] == 0).all()
         assert (store(q_out=given(c.q))[gone] == 5).all()
         assert all((x.transpose(1, 2).flatten(0, 1)[:200][gone] == 0).all() for x in cache)      # no key or value of theirs
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_store_turns_queries_where_they_are(fa, d):
+    """q_out may be q, here a projection's rows: keys and values beside them are read only."""
+    c = Case(150, 6, 3, d, d, bad=((0, -1), (99, 200)))
+    x = torch.cat([c.q, c.k, c.v], 1)
+    before, gone = x.clone(), ~torch.tensor(c.real, device="cuda")
+    cache, want = fa.kv4_pages(10, 3, 16, d), fa.kv4_pages(10, 3, 16, d)
+    slots = torch.arange(150, dtype=torch.int32, device="cuda")
+    kw = dict(q_weight=c.wq, k_weight=c.wk, eps=c.eps)
+    fa.rope_store(None, c.k, c.v, c.cos, c.sin, c.pos, slots, want[0], want[2], want[1], want[3], **kw)
+    q = fa.rope_store(x[:, :6], x[:, 6:9], x[:, 9:], c.cos, c.sin, c.pos, slots, cache[0], cache[2], cache[1], cache[3], q_out=x[:, :6], **kw)
+    assert q.data_ptr() == x.data_ptr() and torch.equal(x[:, 6:], before[:, 6:])
+    c.check(x[:, :6], c.q, c.wq, before[:, :6])
+    assert torch.equal(x[:, :6][gone], before[:, :6][gone])
+    assert all(torch.equal(a, b) for a, b in zip(cache, want))
