@@ -793,7 +793,8 @@ def kv4_pages(num_pages, Hkv, page_size, d=HEAD_DIM, device=None):
 def kv4_expand(k_pages, k_scales, v_pages, v_scales, pages=None, k_out=None, v_out=None, stream=None):
     """4-bit pages as bf16 pages, exactly.  Returns (k_out, v_out), bf16 [n, Hkv,
     page_size, d]: page i is page pages[i] of the cache (int32 [n], None: all
-    pages in order; left as it was where there is no such page)."""
+    pages in order; left as it was where there is no such page, which in an output
+    that the call allocates is anything)."""
     dev = k_pages.get_device()
     if stream is not None or dev < 0 or dev != _current_device():
         return _elsewhere(stream, (k_pages, k_scales, v_pages, v_scales, pages, k_out, v_out),
@@ -840,8 +841,12 @@ def kv4_fwd(q, k_pages, k_scales, v_pages, v_scales, block_table, kv_lens, cu_se
     q [T, Hq, d] bf16 (tokens may be strided), pages and scales as kv4_pages makes
     them, block_table int32 [B, W], kv_lens int32 [B] (new tokens included) -> o
     [T, Hq, d] bf16, lse float32 [Hq, T].  Without cu_seqlens (int32 [B+1]) every
-    request has one row; with it max_seqlen bounds a request's rows.  out, lse and
-    the workspace must not overlap q, the pages or the tables.
+    request has one row; with it max_seqlen bounds a request's rows.  Rows outside
+    every request are not written (in an out or lse that the call allocates they hold
+    anything).  out, lse and the workspace must not overlap q, the pages or the tables.
+    Prompts (more than d rows a key/value head) want a call of their own and tables no
+    wider than they need: their pages are expanded, with all others of the call, in a
+    workspace of up to 4 GB and more, which the call allocates where none is given.
     """
     dev, i32 = q.get_device(), torch.int32
     if stream is not None or dev < 0 or dev != _current_device():

@@ -4,9 +4,10 @@
 // Key j has codes c and, for group g of 32 elements, a scale s_jg (fa_kv4.cuh):
 //   x_j = alpha q . k_j = alpha sum_g s_jg (q_g . c_jg),
 //   O = sum_j w_j v_j / sum_j w_j,  v_jg = t_jg c'_jg,  w_j = e^(x_j - M).
-// Nothing is unpacked into memory: codes become fp16 in registers by the hardware's
-// conversion (exact) and go to the tensor core as they are.  A key's scales
-// multiply the sums of its groups' products, a value's scales its weight.
+// Codes become fp16 by the hardware's conversion (exact).  Where rows are few they go
+// from registers to the tensor core as they are: a key's scales multiply the sums of its
+// groups' products, a value's scales its weight.  More rows share codes that are expanded
+// and scaled in tensor and shared memory, prompts pages expanded to bf16 in the workspace.
 //
 // fp16 weights.  A weight times a scale spans more than fp16 does, so weights are
 // kept relative to what matters for O: with key j's largest value scale in [2, 4) 2^e_j
@@ -50,7 +51,7 @@
 //   instructions for 1088 bytes, the same start.
 //   32 rows of 256 over up to 16384 keys (234 MB): 89 us (134 when four warps shared an
 //   item's 32 rows with m16n8k16); see "more rows".
-//   one token over 1017 keys: 13 us, 12 as a graph.
+//   one token over 1017 keys: 12 to 13 us, 12 as a graph.
 //   prompts, six of up to 2048 tokens over up to 10000 keys (563 GFLOP): 520 us, 25 of
 //   them the expansion (164 MB), the rest fa_prefix_fwd's.
 #include <limits.h>
@@ -79,10 +80,21 @@ __device__ __forceinline__ float value_back(uint32_t x) { return __uint_as_float
 constexpr int kMaxKeys = 1 << 29;       // of a request
 constexpr int kExtraMost = 12;          // units that an item costs besides its keys', at most
 constexpr int kPrefetchMost = 1 << 20;  // bytes of block tables that are brought to L2
-// Rows of a request and key/value head above which pages are expanded.  8 requests of
-// 8000 keys and 8 heads of 128, from the codes and expanded: 64 rows 73 and 133 us, 128
-// rows 130 and 142, 192 rows 199 and 149; of 64, 16 heads: 64 rows 117 and 152, 128 rows
-// 242 and 171; of 256, one head: 256 rows 57 and 61, 512 rows 97 and 72.
+// Rows of a request and key/value head above which pages are expanded, for all of a call's
+// requests.  From the codes and expanded (us):
+//   requests x keys, heads      d/2 rows    d rows     2 d rows   4 d rows
+//   128: 8 x 8000, 8              72 133    128 142    239 159    462 202
+//        8 x 500, 8               21  28     29  32     48  43     80  31
+//        64 x 2000, 8            168 251    318 270    586 282   1162 401
+//        64 x 500, 2              29  35     48  39     80  33    150  73
+//        2 x 30000, 8             66 130    116 134    216 138    415 181
+//        1 x 1000, 1              15  20     15  21     16  22     16  23
+//    64: 8 x 8000, 8              41  71     67  89    116  97    216 115
+//        64 x 2000, 8             79 130    145 170    271 189    524 186
+//   256: 8 x 8000, 2              58  78     98  89    181 122    344 186
+//        64 x 2000, 2            143 149    264 194    521 264    932 397
+// d is nearest to where the two cross; with many requests of 128 and 256 that is about
+// d/2 (at d they take up to 1.4 times as long as expanded), with one short one past 4 d.
 constexpr int many_rows(int d) { return d; }
 constexpr size_t kExpandMost = 4ull << 30;   // bytes of expanded pages a call takes
 
@@ -880,8 +892,10 @@ __global__ void __launch_bounds__(Kv<D, NT>::kThreads, 1) kv4_kernel(const KvArg
 // sixteen warps for the softmax and half as many that expand (32 rows of 128 250, of 64
 // 210).
 template <int D, int N> struct Mid {
-    // An item's start and end take as long as 12 units (100 requests of up to 16384 keys, 32 rows of 256: with 3, 6,
-    // 8, 12 and 16 100, 96, 94, 91 and 91 us).
+    // An item's start and end take as long as 8 to 12 units.  With 4, 8, 12, 16 and 24 (us), 32 rows: 100 requests of up
+    // to 16384 keys, one head: of 256 91.0 86.0 86.3 88.5 90.7, of 128 61.7 59.6 60.3 62.5 64.7, of 64 56.2 54.3 55.1 56.5
+    // 58.9; 300 requests of up to 1500, two heads: of 256 115 104 101 106 109, of 128 74.0 66.4 65.6 67.7 70.2, of 64 65.2
+    // 57.6 58.0 58.7 61.8; 64 requests of 8192: within 3 % of each other up to 12.
     static constexpr int kRows = N, kExtra = 12, kThreads = 896, kWorkers = 1, kHalves = D == 256 ? 2 : 1;
     static constexpr int kRing = D == 256 ? 2 : 4;       // slots of K (codes, both scales) and of V (codes)
     static constexpr uint32_t kCodes = 8 * D, kScales = D / 2, kSlotK = 8 * (kCodes + 2 * kScales), kSlotV = 8 * kCodes;
@@ -1690,7 +1704,7 @@ struct ManyLayout {
 ManyLayout many_layout(int T, int B, int Hq, int Hkv, int d, int max_seqlen, int W, int page) {
     ManyLayout w = {};
     const size_t one = (size_t)B * W * page * Hkv * d * 2;
-    if (max_seqlen * (long long)(Hq / Hkv) <= many_rows(d) || one > kExpandMost / 2 || (long long)B * W * page * Hkv > 0x7fffffffLL) return w;
+    if (max_seqlen * (long long)(Hq / Hkv) <= many_rows(d) || one > kExpandMost / 2) return w;
     w.v = align256(one);
     w.table = w.v + align256(one);
     w.prefix = align256(w.table + 4 * (size_t)B * W);

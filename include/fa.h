@@ -585,6 +585,14 @@ int fa_kv4_expand(const void *k_pages, const void *k_scales, const void *v_pages
  * not for a call with max_seqlen 1, makes the rows be computed from the codes: right,
  * and for long prompts several times slower.  Equal calls with equal workspace
  * sizes give equal results, bit for bit.
+ * max_seqlen and table_width decide for all requests of a call, whatever they hold:
+ * - prompts and single tokens are faster in a call each.  60 single tokens and 4
+ *   prompts of 512 (32 / 8 heads of 128, up to 8191 keys) take 567 us together, 67 and
+ *   198 apart; 63 single tokens and a prompt of 33 531 together, 175 with the workspace
+ *   of single tokens, 83 and 32 apart;
+ * - so are tables no wider than the longest request.  8 prompts of 512 over 2000 keys
+ *   take 173 us with tables for 8256 keys, 293 (and 4.2 GB of workspace) with tables for
+ *   131072; 16 of them 297 and, past the limit above, from the codes, 1103.
  * What the cache holds behind the lengths does not matter.  A NaN in a query or
  * in a key that a row sees gives NaN in its O and LSE; one in a value (a scale of
  * 0xFC) may also reach the O of other rows of its request.
